@@ -14,6 +14,7 @@ STATUS = {0: "S5_OK", 1: "S5_ERR_INVALID_ARGUMENT", 2: "S5_ERR_UNSUPPORTED", 3: 
 
 # Every exported entry point of include/s5.h: name -> (restype, argtypes)
 _vp, _i, _sz, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+_f = ctypes.c_float
 SIGNATURES = {
     "s5_discretize": (_i, [_vp, _vp, _vp, _i, _i, _vp, _vp, _vp]),
     "s5_forward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp,
@@ -42,6 +43,23 @@ SIGNATURES = {
     "s5_ssm_backward": (_i, [_vp] * 16 + [_i] * 4 + [_vp] * 7 + [_sz, _vp]),
     "s5_gemm_bf16": (_i, [_i, _i, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp]),
     "s5_gemm_fault": (_i, []),
+    # gated delta rule
+    "s5_delta_saved_size": (_sz, [_i] * 5),
+    "s5_delta_workspace_size": (_sz, [_i] * 6),
+    "s5_delta_forward": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _vp, _vp, _vp, _f] + [_i] * 6
+                         + [_vp, _ll, _vp, _vp, _sz, _vp, _sz, _vp]),
+    "s5_delta_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _vp, _vp, _vp, _f] + [_i] * 6
+                          + [_vp, _ll, _vp, _vp, _sz, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp,
+                             _vp, _sz, _vp]),
+    "s5_delta_step": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _f] + [_i] * 5 + [_vp, _vp, _vp]),
+    # position rotation and norms of queries and keys
+    "s5_rotary": (_i, [_vp, _ll, _i, _vp, _vp, _i, _i, _f, _i, _ll, _i, _i, _vp, _ll, _vp]),
+    "s5_qk_norm_rotary": (_i, [_vp, _ll, _vp, _ll, _i, _vp, _vp, _i, _f, _vp, _vp, _i, _i, _f, _ll,
+                               _i, _i, _i, _vp, _ll, _vp, _ll, _vp]),
+    "s5_qk_norm_rotary_workspace_size": (_sz, [_i]),
+    "s5_qk_norm_rotary_backward": (_i, [_vp, _ll, _vp, _ll, _i, _vp, _vp, _i, _f, _vp, _vp, _i, _i,
+                                        _f, _ll, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll,
+                                        _vp, _vp, _vp, _sz, _vp]),
 }
 
 _lock = threading.Lock()

@@ -1,13 +1,15 @@
 """Thin torch binding of libs5.so: the same entry points as include/s5.h.
 
 Argument marshalling only.  Every tensor must already be on the GPU with the
-documented dtype, contiguous and 16-byte aligned; nothing is converted or
-copied here, and every numeric step runs in the library's kernels.  Complex
+documented dtype, contiguous (where a call does not take a pitch between
+tokens) and 16-byte aligned; nothing is converted or copied here, and every numeric step runs in the library's kernels.  Complex
 arrays are torch.complex64 tensors (interleaved re/im float32, as the C ABI
 expects).  Work is queued on the current torch CUDA stream unless ``stream``
 is given.
 """
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -222,7 +224,221 @@ def s5_sync_status(workspace, stream=None) -> int:
                                             _stream(stream)))
 
 
+# ---------------------------------------------------------------------------
+# Gated delta rule, position rotation, norms of queries and keys.  Here q, k,
+# v, o and their gradients may be views with a pitch between tokens (slices of
+# a fused projection); a head's values and a token's heads are contiguous.
+# ---------------------------------------------------------------------------
+def _rows(t, name, dtype=None, shape=None):
+    """(address, elements between two tokens) of a [..., H, D] array."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[-1] * t.shape[-2]
+    H, D = t.shape[-2:]
+    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+        raise ValueError("%s: a token's heads must be contiguous" % name)
+    pitch = step = None        # of the innermost token axis, and of the next one out
+    for n, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n == 1:
+            continue
+        if pitch is None:
+            pitch = st
+        elif st != step:
+            raise ValueError("%s: tokens must be evenly spaced" % name)
+        step = n * st
+    return t.data_ptr(), H * D if pitch is None else pitch
+
+
+def _on(stream, *made):
+    """The stream's handle; tensors made here outlive their use on it."""
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+        return stream.cuda_stream
+    other = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    for t in made:
+        if t is not None:
+            t.record_stream(other)
+    return int(stream)
+
+
+def _delta_sizes(q, k, v, lead):
+    if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor) or q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError("q, k and v must have %d axes" % (lead + 2))
+    if q.dtype not in _DT:
+        raise ValueError("q, k and v must be float32 or bfloat16")
+    if q.shape[:lead] != v.shape[:lead]:
+        raise ValueError("q and v have different tokens")
+    return (*q.shape, *v.shape[lead:])
+
+
+def s5_delta_saved_size(B: int, L: int, Hv: int, Dk: int, Dv: int) -> int:
+    return int(_native.lib().s5_delta_saved_size(B, L, Hv, Dk, Dv))
+
+
+def s5_delta_workspace_size(B: int, L: int, Hv: int, Dk: int, Dv: int, backward: bool = False) -> int:
+    return int(_native.lib().s5_delta_workspace_size(B, L, Hv, Dk, Dv, int(backward)))
+
+
+def _buffer(n, what, device):
+    if n == 0:
+        raise S5Error(what, 2, "head sizes are multiples of 4 up to 256")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def new_delta_saved(q, v) -> torch.Tensor:
+    """The buffer that s5_delta_forward fills for s5_delta_backward."""
+    B, L, _, Dk, Hv, Dv = _delta_sizes(q, q, v, 2)
+    return _buffer(s5_delta_saved_size(B, L, Hv, Dk, Dv), "new_delta_saved", q.device)
+
+
+def s5_delta_forward(q, k, v, g, beta, scale=None, s0=None, s_last=None, o=None, saved=None, workspace=None,
+                     stream=None):
+    """Gated delta rule over whole sequences: q, k [B,L,Hk,Dk], v [B,L,Hv,Dv], g, beta [B,L,Hv] float32,
+    from the state s0 [B,Hv,Dk,Dv] float32 (None: zero).  scale defaults to Dk^-0.5.  Returns o, or
+    (o, s_last) when s_last is a tensor (it may be s0) or True; with `saved` (new_delta_saved) also what
+    s5_delta_backward needs."""
+    B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
+    f32, dev, dt = torch.float32, q.device, q.dtype
+    if o is None:
+        o = torch.empty(B, L, Hv, Dv, dtype=dt, device=dev)
+    if s_last is True:
+        s_last = torch.empty(B, Hv, Dk, Dv, dtype=f32, device=dev)
+    lib = _native.lib()
+    if workspace is None:
+        workspace = _buffer(lib.s5_delta_workspace_size(B, L, Hv, Dk, Dv, 0), "s5_delta_forward", dev)
+    code = lib.s5_delta_forward(
+        *_rows(q, "q"), *_rows(k, "k", dt, q.shape), *_rows(v, "v", dt), _DT[dt],
+        _ptr(g, "g", f32, (B, L, Hv)), _ptr(beta, "beta", f32, (B, L, Hv)), _ptr(s0, "s0", f32, (B, Hv, Dk, Dv), True),
+        Dk ** -0.5 if scale is None else float(scale), B, L, Hk, Hv, Dk, Dv, *_rows(o, "o", dt, v.shape),
+        _ptr(s_last, "s_last", f32, (B, Hv, Dk, Dv), True), _ptr(saved, "saved", torch.uint8, None, True),
+        0 if saved is None else saved.numel(), _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
+        _on(stream, o, s_last, workspace))
+    check("s5_delta_forward", code)
+    return o if s_last is None else (o, s_last)
+
+
+def s5_delta_backward(q, k, v, g, beta, do, saved, scale=None, s0=None, ds_last=None, workspace=None, stream=None):
+    """Gradients of sum(do * o) + sum(ds_last * s_last) after s5_delta_forward with the same inputs and `saved`.
+    Returns a dict: dq, dk, dv of q's type, dg, dbeta float32, ds0 float32 (None without s0)."""
+    B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
+    f32, dev, dt = torch.float32, q.device, q.dtype
+    e = lambda shape, t: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
+    out = dict(dq=e(q.shape, dt), dk=e(q.shape, dt), dv=e(v.shape, dt), dg=e((B, L, Hv), f32), dbeta=e((B, L, Hv), f32),
+               ds0=None if s0 is None else e((B, Hv, Dk, Dv), f32))
+    lib = _native.lib()
+    if workspace is None:
+        workspace = _buffer(lib.s5_delta_workspace_size(B, L, Hv, Dk, Dv, 1), "s5_delta_backward", dev)
+    code = lib.s5_delta_backward(
+        *_rows(q, "q"), *_rows(k, "k", dt, q.shape), *_rows(v, "v", dt), _DT[dt],
+        _ptr(g, "g", f32, (B, L, Hv)), _ptr(beta, "beta", f32, (B, L, Hv)), _ptr(s0, "s0", f32, (B, Hv, Dk, Dv), True),
+        Dk ** -0.5 if scale is None else float(scale), B, L, Hk, Hv, Dk, Dv, *_rows(do, "do", dt, v.shape),
+        _ptr(ds_last, "ds_last", f32, (B, Hv, Dk, Dv), True), _ptr(saved, "saved", torch.uint8), saved.numel(),
+        out["dq"].data_ptr(), Hk * Dk, out["dk"].data_ptr(), Hk * Dk, out["dv"].data_ptr(), Hv * Dv,
+        out["dg"].data_ptr(), out["dbeta"].data_ptr(), None if s0 is None else out["ds0"].data_ptr(),
+        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _on(stream, workspace, *out.values()))
+    check("s5_delta_backward", code)
+    return out
+
+
+def s5_delta_step(q, k, v, g, beta, state, scale=None, o=None, stream=None):
+    """One token per sequence: q, k [B,Hk,Dk], v [B,Hv,Dv], g, beta [B,Hv] float32; state [B,Hv,Dk,Dv] float32 is
+    updated in place.  Returns o [B,Hv,Dv]."""
+    B, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 1)
+    f32, dt = torch.float32, q.dtype
+    if o is None:
+        o = torch.empty(B, Hv, Dv, dtype=dt, device=q.device)
+    code = _native.lib().s5_delta_step(
+        _ptr(q, "q"), _ptr(k, "k", dt, q.shape), _ptr(v, "v", dt), _DT[dt], _ptr(g, "g", f32, (B, Hv)),
+        _ptr(beta, "beta", f32, (B, Hv)), Dk ** -0.5 if scale is None else float(scale), B, Hk, Hv, Dk, Dv,
+        _ptr(state, "state", f32, (B, Hv, Dk, Dv)), _ptr(o, "o", dt, v.shape), _on(stream, o))
+    check("s5_delta_step", code)
+    return o
+
+
+_LAYOUT = {"half": 0, "interleaved": 1}
+_NORM = {None: 0, "none": 0, "rms": 1, "l2": 2}
+
+
+def _rot_args(x, name, positions, freq):
+    if not isinstance(x, torch.Tensor) or x.dim() < 3 or x.dtype not in _DT:
+        raise ValueError("%s must be a float32 or bfloat16 array [..., H, D]" % name)
+    T = math.prod(x.shape[:-2])
+    if freq is None:
+        return T, None, None, 0
+    return (T, _ptr(positions, "positions", torch.int64, x.shape[:-2]), _ptr(freq, "freq", torch.float64),
+            2 * freq.numel())
+
+
+def s5_rotary(x, positions, freq, layout="half", amplitude=1.0, inverse=False, out=None, stream=None):
+    """Rotates the first 2 * len(freq) values of each head of x [..., H, D] by the angles positions [...] (int64) *
+    freq (float64, init.rotary_frequencies) and scales them by amplitude; inverse: the transpose (its backward
+    pass).  out may be x."""
+    T, pos, fr, rot = _rot_args(x, "x", positions, freq)
+    H, D = x.shape[-2:]
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    code = _native.lib().s5_rotary(*_rows(x, "x"), _DT[x.dtype], pos, fr, rot, _LAYOUT[layout], float(amplitude),
+                                   int(inverse), T, H, D, *_rows(out, "out", x.dtype, x.shape), _on(stream, out))
+    check("s5_rotary", code)
+    return out
+
+
+def s5_qk_norm_rotary(q, k, positions, freq, norm="rms", eps=1e-6, q_weight=None, k_weight=None, layout="half",
+                      amplitude=1.0, q_out=None, k_out=None, stream=None):
+    """Norm of each head ("rms", "l2" or None), its weight [D] float32 (None: ones) and the rotation of s5_rotary, of
+    q [..., Hq, D] and k [..., Hk, D] in one launch.  freq None: no rotation.  q_out may be q, k_out may be k."""
+    T, pos, fr, rot = _rot_args(q, "q", positions, freq)
+    (Hq, D), Hk, dt, f32 = q.shape[-2:], k.shape[-2], q.dtype, torch.float32
+    kshape = (*q.shape[:-2], Hk, D)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(kshape, dtype=dt, device=q.device)
+    code = _native.lib().s5_qk_norm_rotary(
+        *_rows(q, "q"), *_rows(k, "k", dt, kshape), _DT[dt], _ptr(q_weight, "q_weight", f32, (D,), True),
+        _ptr(k_weight, "k_weight", f32, (D,), True), _NORM[norm], float(eps), pos, fr, rot, _LAYOUT[layout],
+        float(amplitude), T, Hq, Hk, D, *_rows(q_out, "q_out", dt, q.shape), *_rows(k_out, "k_out", dt, kshape),
+        _on(stream, q_out, k_out))
+    check("s5_qk_norm_rotary", code)
+    return q_out, k_out
+
+
+def s5_qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, norm="rms", eps=1e-6, q_weight=None,
+                               k_weight=None, layout="half", amplitude=1.0, workspace=None, stream=None):
+    """Gradients of s5_qk_norm_rotary from those of its outputs.  Returns a dict: dq, dk, and dwq, dwk [D] float32
+    (None without the weight)."""
+    T, pos, fr, rot = _rot_args(q, "q", positions, freq)
+    (Hq, D), Hk, dt, f32, dev = q.shape[-2:], k.shape[-2], q.dtype, torch.float32, q.device
+    kshape = (*q.shape[:-2], Hk, D)
+    lib = _native.lib()
+    out = dict(dq=torch.empty(q.shape, dtype=dt, device=dev), dk=torch.empty(kshape, dtype=dt, device=dev),
+               dwq=None if q_weight is None else torch.empty(D, dtype=f32, device=dev),
+               dwk=None if k_weight is None else torch.empty(D, dtype=f32, device=dev))
+    if workspace is None and (q_weight is not None or k_weight is not None):
+        workspace = _buffer(lib.s5_qk_norm_rotary_workspace_size(D), "s5_qk_norm_rotary_backward", dev)
+    code = lib.s5_qk_norm_rotary_backward(
+        *_rows(q, "q"), *_rows(k, "k", dt, kshape), _DT[dt], _ptr(q_weight, "q_weight", f32, (D,), True),
+        _ptr(k_weight, "k_weight", f32, (D,), True), _NORM[norm], float(eps), pos, fr, rot, _LAYOUT[layout],
+        float(amplitude), T, Hq, Hk, D, *_rows(dq_out, "dq_out", dt, q.shape), *_rows(dk_out, "dk_out", dt, kshape),
+        out["dq"].data_ptr(), Hq * D, out["dk"].data_ptr(), Hk * D, _ptr(out["dwq"], "dwq", None, None, True),
+        _ptr(out["dwk"], "dwk", None, None, True), _ptr(workspace, "workspace", torch.uint8, None, True),
+        0 if workspace is None else workspace.numel(), _on(stream, workspace, *out.values()))
+    check("s5_qk_norm_rotary_backward", code)
+    return out
+
+
 __all__ = ["s5_discretize", "s5_discretize_ex", "s5_forward", "s5_forward_varying_dt",
            "s5_forward_bidirectional", "s5_step", "s5_forward_noalloc", "s5_workspace_size",
-           "s5_bidirectional_workspace_size", "s5_sync_status", "new_workspace", "S5Error", "S5_F32",
-           "S5_BF16"]
+           "s5_bidirectional_workspace_size", "s5_sync_status", "new_workspace",
+           "s5_delta_forward", "s5_delta_backward", "s5_delta_step", "s5_delta_saved_size",
+           "s5_delta_workspace_size", "new_delta_saved", "s5_rotary", "s5_qk_norm_rotary",
+           "s5_qk_norm_rotary_backward", "S5Error", "S5_F32", "S5_BF16"]

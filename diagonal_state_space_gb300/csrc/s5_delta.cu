@@ -1,0 +1,615 @@
+// s5_delta.cu -- the gated delta rule: a linear recurrence whose state is a
+// matrix S [Dk][Dv] per sequence and value head, with a = exp(g):
+//   e_t = v_t - a_t S_{t-1}^T k_t,  u_t = beta_t e_t,
+//   S_t = a_t S_{t-1} + k_t u_t^T,  o_t = scale S_t^T q_t.
+// This file has the entry points, the single-token step and the CUDA-core
+// sweeps that serve every type and head size; bf16 heads of 64 or 128 run on
+// the tensor cores in chunks of 64 tokens (s5_delta_tc.cu).
+//
+// Sweeps.  Every column of S (a value index) is a recurrence of its own given
+// the keys, and every row (a key index) is one given the u_t.  So the forward
+// sweep and the adjoint sweep of Z_t = dL/dS_t,
+//   Z_t = scale q_t do_t^T + a_{t+1} (Z_{t+1} - k_{t+1} dv_{t+1}^T),
+//   X_t = Z_t^T k_t,  dv_t = beta_t X_t,  dbeta_t = X_t . e_t,
+// run with columns spread over the grid and no exchange between blocks, and
+//   dq_t = scale S_t do_t,   dk_t = Z_t u_t - a_t S_{t-1} dv_t
+// come from a second pair of sweeps with rows spread over the grid: four
+// sweeps, all sums inside 16 lanes, no atomics, one order of addition.
+//
+// The decay's gradient dg_t = <a_t S_{t-1}, Z_t - k_t dv_t^T> needs no sweep:
+//   dg_t - dg_{t+1} = o_t . do_t - v_t . dv_t,
+// (insert the recurrences), anchored at every 64th token by <S_c, Z_c> of the
+// kept states, so that at most 64 terms are added in a row.
+//
+// Bound: the chain of a token (product, sum over 16 lanes, update), about 300
+// cycles; the state stays in registers.
+#include "s5_delta.cuh"
+
+namespace s5 {
+namespace delta {
+namespace {
+
+constexpr int TB = 16;        // tokens staged in shared memory
+constexpr int OWN = 32;       // columns (or rows) of a block
+constexpr int SWT = 128;      // threads of a sweep: 16 lanes x 8 groups of 4
+
+// Sums of four values over 16 lanes; lane l gets the sum of value l / 4 % 4.
+__device__ __forceinline__ float sum4_16(const float (&v)[4], int lane) {
+    const bool up = lane & 8, up2 = lane & 4;
+    float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
+    a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 8);
+    b += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 8);
+    float c = up2 ? b : a;
+    c += __shfl_xor_sync(0xffffffffu, up2 ? a : b, 4);
+    c += __shfl_xor_sync(0xffffffffu, c, 2);
+    c += __shfl_xor_sync(0xffffffffu, c, 1);
+    return c;
+}
+
+template <typename T> __device__ __forceinline__ float elem(const void *p, long long i) {
+    return load_elem<T>(static_cast<const T *>(p) + i);
+}
+
+// Columns over the grid.  REV false: the forward recurrence, writing o (and
+// what the backward pass needs); REV true: the adjoint, writing X.
+template <typename T, int RPT, bool REV>
+__global__ void __launch_bounds__(SWT) column_sweep_kernel(const Args a) {
+    __shared__ float sq[TB][16 * RPT], sk[TB][16 * RPT], sv[TB][OWN], sa[TB], sb[TB];
+    __shared__ float red[SWT / 32];
+    const int lane = threadIdx.x % 16, grp = threadIdx.x / 16;
+    const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
+    const int col = blockIdx.x * OWN + grp * 4;
+    const int mine = lane / 4;                       // the column whose sums this lane gets
+    const bool on = col < a.Dv;                      // Dv is a multiple of 4
+    const int N = chunks(a.L);
+    const long long bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
+    const float *init = REV ? a.ds_last : a.s0;
+    float S[RPT][4];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = lane + 16 * i;
+        const float4 t = (init && on && r < a.Dk) ? *reinterpret_cast<const float4 *>(init + bh * mat + (long long)r * a.Dv + col)
+                                                  : make_float4(0, 0, 0, 0);
+        S[i][0] = t.x, S[i][1] = t.y, S[i][2] = t.z, S[i][3] = t.w;
+    }
+    // <S_c, Z_c> of this block's columns
+    auto inner = [&](int c) {
+        const float *s = a.states + (bh * (N + 1) + c) * mat;
+        float w = 0.0f;
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const int r = lane + 16 * i;
+            if (on && r < a.Dk) {
+                const float4 t = *reinterpret_cast<const float4 *>(s + (long long)r * a.Dv + col);
+                w += t.x * S[i][0] + t.y * S[i][1] + t.z * S[i][2] + t.w * S[i][3];
+            }
+        }
+        for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
+        if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = w;
+        __syncthreads();
+        if (threadIdx.x == 0) a.inner[(bh * (N + 1) + c) * a.parts + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
+        __syncthreads();
+    };
+    auto keep = [&](float *to) {
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const int r = lane + 16 * i;
+            if (on && r < a.Dk)
+                *reinterpret_cast<float4 *>(to + (long long)r * a.Dv + col) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+        }
+    };
+    if (REV) inner(N);
+    const int stages = (a.L + TB - 1) / TB;
+    for (int st = 0; st < stages; ++st) {
+        const int t0 = (REV ? stages - 1 - st : st) * TB, nt = min(TB, a.L - t0);
+        const long long row0 = (long long)b * a.L + t0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < nt * 16 * RPT; i += SWT) {
+            const int t = i / (16 * RPT), r = i % (16 * RPT);
+            const bool in = r < a.Dk;
+            sq[t][r] = in ? a.scale * elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
+            sk[t][r] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
+        }
+        for (int i = threadIdx.x; i < nt * OWN; i += SWT) {
+            const int t = i / OWN, c = blockIdx.x * OWN + i % OWN;
+            sv[t][i % OWN] = c >= a.Dv ? 0.0f
+                             : REV     ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + c)
+                                       : elem<T>(a.v, (row0 + t) * a.ldv + (long long)h * a.Dv + c);
+        }
+        if (threadIdx.x < nt) {
+            sa[threadIdx.x] = expf(clamp_g(a.g[(row0 + threadIdx.x) * a.Hv + h]));
+            sb[threadIdx.x] = a.beta[(row0 + threadIdx.x) * a.Hv + h];
+        }
+        __syncthreads();
+        for (int j = 0; j < nt; ++j) {
+            const int t = REV ? nt - 1 - j : j, tok = t0 + t;
+            const long long out = ((row0 + t) * a.Hv + h) * a.Dv + col + mine;
+            float p[4] = {0, 0, 0, 0}, u[4];
+            const float al = sa[t];
+            if (!REV) {
+                if (a.states && tok % CHUNK == 0) keep(a.states + (bh * (N + 1) + tok / CHUNK) * mat);
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                    const float kk = sk[t][lane + 16 * i];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        S[i][c] *= al;
+                        p[c] = fmaf(S[i][c], kk, p[c]);
+                    }
+                }
+                const float e = sv[t][grp * 4 + mine] - sum4_16(p, lane);
+                if (a.e && on && lane % 4 == 0) a.e[out] = e;
+                const float um = sb[t] * e;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, um, (threadIdx.x & 16) + 4 * c), p[c] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                    const float kk = sk[t][lane + 16 * i], qq = sq[t][lane + 16 * i];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        S[i][c] = fmaf(kk, u[c], S[i][c]);
+                        p[c] = fmaf(S[i][c], qq, p[c]);
+                    }
+                }
+                const float o = sum4_16(p, lane);
+                if (on && lane % 4 == 0) {
+                    store_elem<T>(static_cast<T *>(a.o) + (row0 + t) * a.ldo + (long long)h * a.Dv + col + mine, o);
+                    if (a.o32) a.o32[out] = o;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                    const float kk = sk[t][lane + 16 * i], qq = sq[t][lane + 16 * i];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        S[i][c] = fmaf(qq, sv[t][grp * 4 + c], S[i][c]);
+                        p[c] = fmaf(S[i][c], kk, p[c]);
+                    }
+                }
+                const float x = sum4_16(p, lane);
+                if (on && lane % 4 == 0) a.x[out] = x;
+                const float um = sb[t] * x;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, um, (threadIdx.x & 16) + 4 * c);
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                    const float kk = sk[t][lane + 16 * i];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) S[i][c] = al * fmaf(-kk, u[c], S[i][c]);
+                }
+                if (tok % CHUNK == 0) inner(tok / CHUNK);
+            }
+        }
+    }
+    float *last = REV ? a.ds0 : a.s_last;
+    if (last) keep(last + bh * mat);
+    if (!REV && a.states) keep(a.states + (bh * (N + 1) + N) * mat);
+}
+
+// Rows over the grid, with u_t = beta_t e_t and dv_t = beta_t X_t known.  REV
+// false: dq_t and -a_t S_{t-1} dv_t; REV true: adds Z_t u_t to the latter.
+template <typename T, int RPT, bool REV>
+__global__ void __launch_bounds__(SWT) row_sweep_kernel(const Args a) {
+    __shared__ float se[TB][16 * RPT], sx[TB][16 * RPT], sd[TB][16 * RPT], sq[TB][OWN], sk[TB][OWN], sa[TB];
+    const int lane = threadIdx.x % 16, grp = threadIdx.x / 16;
+    const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
+    const int row = blockIdx.x * OWN + grp * 4, mine = lane / 4;
+    const bool on = row < a.Dk;
+    const long long bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
+    const float *init = REV ? a.ds_last : a.s0;
+    float S[RPT][4];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            S[i][r] = (init && on && lane + 16 * i < a.Dv) ? init[bh * mat + (long long)(row + r) * a.Dv + lane + 16 * i] : 0.0f;
+    const int stages = (a.L + TB - 1) / TB;
+    for (int st = 0; st < stages; ++st) {
+        const int t0 = (REV ? stages - 1 - st : st) * TB, nt = min(TB, a.L - t0);
+        const long long row0 = (long long)b * a.L + t0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < nt * 16 * RPT; i += SWT) {
+            const int t = i / (16 * RPT), c = i % (16 * RPT);
+            const bool in = c < a.Dv;
+            const long long hv = (row0 + t) * a.Hv + h;
+            const float be = a.beta[hv];
+            se[t][c] = in ? be * a.e[hv * a.Dv + c] : 0.0f;
+            sx[t][c] = in ? be * a.x[hv * a.Dv + c] : 0.0f;
+            sd[t][c] = in ? a.scale * elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + c) : 0.0f;
+        }
+        for (int i = threadIdx.x; i < nt * OWN; i += SWT) {
+            const int t = i / OWN, r = blockIdx.x * OWN + i % OWN;
+            sq[t][i % OWN] = r < a.Dk ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
+            sk[t][i % OWN] = r < a.Dk ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
+        }
+        if (threadIdx.x < nt) sa[threadIdx.x] = expf(clamp_g(a.g[(row0 + threadIdx.x) * a.Hv + h]));
+        __syncthreads();
+        for (int j = 0; j < nt; ++j) {
+            const int t = REV ? nt - 1 - j : j;
+            const long long out = ((row0 + t) * a.Hv + h) * a.Dk + row + mine;
+            const float al = sa[t];
+            float p[4] = {0, 0, 0, 0}, w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                const float e = se[t][lane + 16 * i], x = sx[t][lane + 16 * i], d = sd[t][lane + 16 * i];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if (!REV) {
+                        S[i][r] *= al;
+                        p[r] = fmaf(S[i][r], x, p[r]);
+                        S[i][r] = fmaf(sk[t][grp * 4 + r], e, S[i][r]);
+                        w[r] = fmaf(S[i][r], d, w[r]);
+                    } else {
+                        S[i][r] = fmaf(sq[t][grp * 4 + r], d, S[i][r]);
+                        p[r] = fmaf(S[i][r], e, p[r]);
+                        S[i][r] = al * fmaf(-sk[t][grp * 4 + r], x, S[i][r]);
+                    }
+                }
+            }
+            const float v = sum4_16(p, lane);
+            if (!REV) {
+                const float dq = sum4_16(w, lane);
+                if (on && lane % 4 == 0) a.dqh[out] = dq, a.dkh[out] = -v;
+            } else if (on && lane % 4 == 0)
+                a.dkh[out] += v;
+        }
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
+// One warp per token and value head: dv = beta X, dbeta = X . e, o . do - v . dv.
+template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(const Args a) {
+    const long long hv = (long long)blockIdx.x * 8 + threadIdx.x / 32, rows = (long long)a.B * a.L * a.Hv;
+    const int lane = threadIdx.x % 32;
+    if (hv >= rows) return;
+    const long long row = hv / a.Hv;
+    const int h = (int)(hv % a.Hv);
+    const float be = a.beta[hv];
+    float db = 0.0f, w = 0.0f;
+    for (int c = lane; c < a.Dv; c += 32) {
+        const float x = a.x[hv * a.Dv + c], dv = be * x;
+        const float v = elem<T>(a.v, row * a.ldv + (long long)h * a.Dv + c);
+        const float d = elem<T>(a.dout, row * a.lddo + (long long)h * a.Dv + c);
+        db = fmaf(x, a.e[hv * a.Dv + c], db);
+        w = fmaf(a.o32[hv * a.Dv + c], d, fmaf(-v, dv, w));
+        store_elem<T>(static_cast<T *>(a.dv) + row * a.lddv + (long long)h * a.Dv + c, dv);
+    }
+    db = warp_sum(db), w = warp_sum(w);
+    if (lane == 0) a.dbeta[hv] = db, a.dots[hv] = w;
+}
+
+// One warp per chunk and value head: dg by adding the chunk's terms from its
+// end on top of <S, Z> there.  A token whose decay is zero has no gradient.
+__global__ void __launch_bounds__(256) decay_grads_kernel(const Args a) {
+    const int N = chunks(a.L), lane = threadIdx.x % 32;
+    const long long id = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+    if (id >= (long long)a.B * a.Hv * N) return;
+    const int c = (int)(id % N);
+    const long long bh = id / N;
+    const int h = (int)(bh % a.Hv);
+    const long long b = bh / a.Hv;
+    float s = 0.0f;
+    for (int p = 0; p < a.parts; ++p) s += a.inner[(bh * (N + 1) + c + 1) * a.parts + p];
+    // two tokens per lane, later tokens in lower lanes
+    for (int half = 0; half < 2; ++half) {
+        const int t = c * CHUNK + CHUNK - 1 - 32 * half - lane;
+        const long long hv = (b * a.L + t) * a.Hv + h;
+        float w = t < a.L ? a.dots[hv] : 0.0f;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const float up = __shfl_up_sync(0xffffffffu, w, m);
+            if (lane >= m) w += up;
+        }
+        if (t < a.L) a.dg[hv] = expf(clamp_g(a.g[hv])) == 0.0f ? 0.0f : s + w;
+        s += __shfl_sync(0xffffffffu, w, 31);
+    }
+}
+
+// dq and dk of a key head: the sum over its value heads, rounded once.
+template <typename T> __global__ void __launch_bounds__(256) group_sum_kernel(const Args a) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, n = (long long)a.B * a.L * a.Hk * a.Dk;
+    if (i >= n) return;
+    const int d = (int)(i % a.Dk), hk = (int)(i / a.Dk % a.Hk), group = a.Hv / a.Hk;
+    const long long row = i / ((long long)a.Dk * a.Hk);
+    float q = 0.0f, k = 0.0f;
+    for (int j = 0; j < group; ++j) {
+        const long long at = (row * a.Hv + hk * group + j) * a.Dk + d;
+        q += a.dqh[at], k += a.dkh[at];
+    }
+    store_elem<T>(static_cast<T *>(a.dq) + row * a.lddq + (long long)hk * a.Dk + d, q);
+    store_elem<T>(static_cast<T *>(a.dk) + row * a.lddk + (long long)hk * a.Dk + d, k);
+}
+
+// ---------------------------------------------------------------------------
+// One token.  The state is read and written once (the bound: its bytes), held
+// in registers in between: a block takes 32 columns of one head, 8 lanes of
+// four columns by 32 rows at a time.  Both sums over the rows, S^T k and
+// S^T q, are taken of the old state, so that one exchange between the warps
+// serves them:  o = scale (a S^T q + (q . k) u).
+// ---------------------------------------------------------------------------
+template <typename T, int RPT>
+__global__ void __launch_bounds__(256) delta_step_kernel(const void *q, const void *k, const void *v, const float *g,
+                                                         const float *beta, float scale, int Hk, int Hv, int Dk,
+                                                         int Dv, float *state, void *o) {
+    __shared__ float4 rk[8][8], rq[8][8];
+    __shared__ float rd[8];
+    const int cv = threadIdx.x % 8, rg = threadIdx.x / 8, warp = threadIdx.x / 32;
+    const int col = blockIdx.x * 32 + cv * 4, h = blockIdx.y, b = blockIdx.z, hk = h / (Hv / Hk);
+    const long long bh = (long long)b * Hv + h;
+    const bool on = col < Dv;
+    float *s = state + bh * (long long)Dk * Dv + col;
+    const long long kb = ((long long)b * Hk + hk) * Dk;
+    griddep_wait();
+    griddep_launch_dependents();
+    float4 S[RPT];
+    float kk[RPT], qk = 0.0f;
+    float4 pk = make_float4(0, 0, 0, 0), pq = pk;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = rg + 32 * i;
+        S[i] = (on && r < Dk) ? *reinterpret_cast<const float4 *>(s + (long long)r * Dv) : make_float4(0, 0, 0, 0);
+    }
+    const float al = expf(clamp_g(g[bh])), be = beta[bh];
+    float vv[4] = {0, 0, 0, 0};
+    if (on)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) vv[c] = elem<T>(v, bh * Dv + col + c);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = rg + 32 * i;
+        kk[i] = r < Dk ? elem<T>(k, kb + r) : 0.0f;
+        const float qq = r < Dk ? elem<T>(q, kb + r) : 0.0f;
+        qk = fmaf(qq, kk[i], qk);
+        pk.x = fmaf(S[i].x, kk[i], pk.x), pk.y = fmaf(S[i].y, kk[i], pk.y);
+        pk.z = fmaf(S[i].z, kk[i], pk.z), pk.w = fmaf(S[i].w, kk[i], pk.w);
+        pq.x = fmaf(S[i].x, qq, pq.x), pq.y = fmaf(S[i].y, qq, pq.y);
+        pq.z = fmaf(S[i].z, qq, pq.z), pq.w = fmaf(S[i].w, qq, pq.w);
+    }
+#pragma unroll
+    for (int m = 8; m < 32; m <<= 1) {
+        pk.x += __shfl_xor_sync(0xffffffffu, pk.x, m), pk.y += __shfl_xor_sync(0xffffffffu, pk.y, m);
+        pk.z += __shfl_xor_sync(0xffffffffu, pk.z, m), pk.w += __shfl_xor_sync(0xffffffffu, pk.w, m);
+        pq.x += __shfl_xor_sync(0xffffffffu, pq.x, m), pq.y += __shfl_xor_sync(0xffffffffu, pq.y, m);
+        pq.z += __shfl_xor_sync(0xffffffffu, pq.z, m), pq.w += __shfl_xor_sync(0xffffffffu, pq.w, m);
+        qk += __shfl_xor_sync(0xffffffffu, qk, m);
+    }
+    if (threadIdx.x % 32 < 8) rk[warp][cv] = pk, rq[warp][cv] = pq;
+    if (threadIdx.x % 32 == 0) rd[warp] = qk;
+    __syncthreads();
+    pk = pq = make_float4(0, 0, 0, 0), qk = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const float4 x = rk[w][cv], y = rq[w][cv];
+        pk.x += x.x, pk.y += x.y, pk.z += x.z, pk.w += x.w;
+        pq.x += y.x, pq.y += y.y, pq.z += y.z, pq.w += y.w;
+        qk += rd[w];
+    }
+    const float ux = be * (vv[0] - al * pk.x), uy = be * (vv[1] - al * pk.y), uz = be * (vv[2] - al * pk.z),
+                uw = be * (vv[3] - al * pk.w);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = rg + 32 * i;
+        if (on && r < Dk)
+            *reinterpret_cast<float4 *>(s + (long long)r * Dv) =
+                make_float4(fmaf(kk[i], ux, al * S[i].x), fmaf(kk[i], uy, al * S[i].y), fmaf(kk[i], uz, al * S[i].z),
+                            fmaf(kk[i], uw, al * S[i].w));
+    }
+    if (on && rg == 0) {
+        T *out = static_cast<T *>(o) + bh * Dv + col;
+        store_elem<T>(out, scale * fmaf(al, pq.x, qk * ux));
+        store_elem<T>(out + 1, scale * fmaf(al, pq.y, qk * uy));
+        store_elem<T>(out + 2, scale * fmaf(al, pq.z, qk * uz));
+        store_elem<T>(out + 3, scale * fmaf(al, pq.w, qk * uw));
+    }
+}
+
+template <typename T, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
+    const dim3 grid((a.Dv + OWN - 1) / OWN, a.Hv, a.B);
+    if (a.Dk <= 64)
+        column_sweep_kernel<T, 4, REV><<<grid, SWT, 0, st>>>(a);
+    else if (a.Dk <= 128)
+        column_sweep_kernel<T, 8, REV><<<grid, SWT, 0, st>>>(a);
+    else
+        column_sweep_kernel<T, 16, REV><<<grid, SWT, 0, st>>>(a);
+    return cudaGetLastError();
+}
+template <typename T, bool REV> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
+    const dim3 grid((a.Dk + OWN - 1) / OWN, a.Hv, a.B);
+    if (a.Dv <= 64)
+        row_sweep_kernel<T, 4, REV><<<grid, SWT, 0, st>>>(a);
+    else if (a.Dv <= 128)
+        row_sweep_kernel<T, 8, REV><<<grid, SWT, 0, st>>>(a);
+    else
+        row_sweep_kernel<T, 16, REV><<<grid, SWT, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
+    cudaError_t e = column_sweep<T, true>(a, st);
+    if (e != cudaSuccess || a.L == 0) return e;
+    if ((e = row_sweep<T, false>(a, st)) != cudaSuccess || (e = row_sweep<T, true>(a, st)) != cudaSuccess) return e;
+    const long long rows = (long long)a.B * a.L * a.Hv;
+    token_grads_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
+    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a);
+    const long long n = (long long)a.B * a.L * a.Hk * a.Dk;
+    group_sum_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool floats(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }   // read one by one
+bool aligned16_or_null(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Sizes that every entry point takes; offsets are 64-bit, launches 32-bit.
+s5_status check_sizes(long long B, long long L, long long Hk, long long Hv, long long Dk, long long Dv, s5_dtype dtype) {
+    if (dtype != S5_F32 && dtype != S5_BF16) return S5_ERR_INVALID_ARGUMENT;
+    if (B < 0 || L < 0 || Hk < 1 || Hv < 1 || Dk < 1 || Dv < 1 || Hv % Hk) return S5_ERR_INVALID_ARGUMENT;
+    if (Dk % 4 || Dv % 4 || Dk > 256 || Dv > 256 || B > 65535 || Hv > 65535) return S5_ERR_UNSUPPORTED;
+    if (B * Hv > (1ll << 24) || L > (1ll << 30) || B * L * Hv > (1ll << 30)) return S5_ERR_UNSUPPORTED;
+    return S5_OK;
+}
+
+struct Sizes {
+    size_t e, states, images;
+};
+Sizes sizes(int B, int L, int Hv, int Dk, int Dv) {
+    Sizes s;
+    s.e = align256(sizeof(float) * (size_t)B * L * Hv * Dv);
+    s.states = align256(sizeof(float) * (size_t)B * Hv * (chunks(L) + 1) * Dk * Dv);
+    s.images = align256(tc_image_bytes(B, L, Hv));
+    return s;
+}
+
+}  // namespace
+}  // namespace delta
+}  // namespace s5
+
+using namespace s5;
+using namespace s5::delta;
+
+extern "C" size_t s5_delta_saved_size(int B, int L, int Hv, int Dk, int Dv) {
+    if (check_sizes(B, L, Hv, Hv, Dk, Dv, S5_F32) != S5_OK) return 0;
+    const Sizes s = sizes(B, L, Hv, Dk, Dv);
+    return 2 * s.e + s.states + 256;
+}
+
+extern "C" size_t s5_delta_workspace_size(int B, int L, int Hv, int Dk, int Dv, int backward) {
+    if (check_sizes(B, L, Hv, Hv, Dk, Dv, S5_F32) != S5_OK) return 0;
+    const Sizes s = sizes(B, L, Hv, Dk, Dv);
+    size_t n = 256 + s.images;
+    if (backward)
+        n += s.e + 2 * align256(sizeof(float) * (size_t)B * L * Hv * Dk) +
+             align256(sizeof(float) * (size_t)B * Hv * (chunks(L) + 1) * ((Dv + OWN - 1) / OWN)) +
+             align256(sizeof(float) * (size_t)B * L * Hv);
+    return n;
+}
+
+extern "C" s5_status s5_delta_forward(const void *q, long long ldq, const void *k, long long ldk, const void *v,
+                                      long long ldv, s5_dtype dtype, const float *g, const float *beta,
+                                      const float *s0, float scale, int B, int L, int Hk, int Hv, int Dk, int Dv,
+                                      void *o, long long ldo, float *s_last, void *saved, size_t saved_bytes,
+                                      void *workspace, size_t workspace_bytes, s5_stream_t stream) {
+    const s5_status c = check_sizes(B, L, Hk, Hv, Dk, Dv, dtype);
+    if (c != S5_OK) return c;
+    if (!(scale == scale) || !aligned16_or_null(s0) || !aligned16_or_null(s_last) || !aligned16_or_null(saved))
+        return S5_ERR_INVALID_ARGUMENT;
+    if (saved && saved_bytes < s5_delta_saved_size(B, L, Hv, Dk, Dv)) return S5_ERR_INVALID_ARGUMENT;
+    if (B == 0) return S5_OK;
+    if (L > 0) {
+        if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !floats(g) || !floats(beta) || !aligned16(o))
+            return S5_ERR_INVALID_ARGUMENT;
+        if (ldq < (long long)Hk * Dk || ldk < (long long)Hk * Dk || ldv < (long long)Hv * Dv || ldo < (long long)Hv * Dv)
+            return S5_ERR_INVALID_ARGUMENT;
+        if (!aligned16(workspace) || workspace_bytes < s5_delta_workspace_size(B, L, Hv, Dk, Dv, 0))
+            return S5_ERR_INVALID_ARGUMENT;
+    }
+    Args a = {};
+    a.q = q, a.k = k, a.v = v, a.ldq = ldq, a.ldk = ldk, a.ldv = ldv, a.g = g, a.beta = beta, a.s0 = s0;
+    a.scale = scale, a.B = B, a.L = L, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv;
+    a.o = o, a.ldo = ldo, a.s_last = s_last;
+    const Sizes s = sizes(B, L, Hv, Dk, Dv);
+    if (saved) {
+        char *p = static_cast<char *>(saved);
+        a.e = reinterpret_cast<float *>(p);
+        a.o32 = reinterpret_cast<float *>(p + s.e);
+        a.states = reinterpret_cast<float *>(p + 2 * s.e);
+    }
+    a.images = reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    if (tc_supported(a, dtype, false))
+        e = tc_forward(a, st);
+    else
+        e = dtype == S5_BF16 ? column_sweep<__nv_bfloat16, false>(a, st) : column_sweep<float, false>(a, st);
+    return e == cudaSuccess ? S5_OK : cuda_failure(e);
+}
+
+extern "C" s5_status s5_delta_backward(const void *q, long long ldq, const void *k, long long ldk, const void *v,
+                                       long long ldv, s5_dtype dtype, const float *g, const float *beta,
+                                       const float *s0, float scale, int B, int L, int Hk, int Hv, int Dk, int Dv,
+                                       const void *dout, long long lddo, const float *ds_last, const void *saved,
+                                       size_t saved_bytes, void *dq, long long lddq, void *dk, long long lddk,
+                                       void *dv, long long lddv, float *dg, float *dbeta, float *ds0, void *workspace,
+                                       size_t workspace_bytes, s5_stream_t stream) {
+    const s5_status c = check_sizes(B, L, Hk, Hv, Dk, Dv, dtype);
+    if (c != S5_OK) return c;
+    if (!(scale == scale) || !aligned16_or_null(s0) || !aligned16_or_null(ds_last) || !aligned16_or_null(ds0))
+        return S5_ERR_INVALID_ARGUMENT;
+    if (B == 0) return S5_OK;
+    if (!aligned16(saved) || saved_bytes < s5_delta_saved_size(B, L, Hv, Dk, Dv) || !aligned16(workspace) ||
+        workspace_bytes < s5_delta_workspace_size(B, L, Hv, Dk, Dv, 1))
+        return S5_ERR_INVALID_ARGUMENT;
+    if (L > 0) {
+        const void *all[] = {q, k, v, dout, dq, dk, dv, dg, dbeta};
+        for (const void *p : all)
+            if (!aligned16(p)) return S5_ERR_INVALID_ARGUMENT;
+        if (!floats(g) || !floats(beta)) return S5_ERR_INVALID_ARGUMENT;
+        const long long nk = (long long)Hk * Dk, nv = (long long)Hv * Dv;
+        if (ldq < nk || ldk < nk || ldv < nv || lddo < nv || lddq < nk || lddk < nk || lddv < nv)
+            return S5_ERR_INVALID_ARGUMENT;
+    }
+    Args a = {};
+    a.q = q, a.k = k, a.v = v, a.ldq = ldq, a.ldk = ldk, a.ldv = ldv, a.g = g, a.beta = beta, a.s0 = s0;
+    a.scale = scale, a.B = B, a.L = L, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv;
+    const Sizes s = sizes(B, L, Hv, Dk, Dv);
+    char *p = static_cast<char *>(const_cast<void *>(saved));   // read only here
+    a.e = reinterpret_cast<float *>(p);
+    a.o32 = reinterpret_cast<float *>(p + s.e);
+    a.states = reinterpret_cast<float *>(p + 2 * s.e);
+    a.dout = dout, a.lddo = lddo, a.ds_last = ds_last;
+    a.dq = dq, a.dk = dk, a.dv = dv, a.lddq = lddq, a.lddk = lddk, a.lddv = lddv;
+    a.dg = dg, a.dbeta = dbeta, a.ds0 = ds0;
+    char *w = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
+    a.images = w;
+    w += s.images;
+    a.x = reinterpret_cast<float *>(w);
+    w += s.e;
+    const size_t heads = align256(sizeof(float) * (size_t)B * L * Hv * Dk);
+    a.dqh = reinterpret_cast<float *>(w);
+    w += heads;
+    a.dkh = reinterpret_cast<float *>(w);
+    w += heads;
+    a.parts = (Dv + OWN - 1) / OWN;
+    a.inner = reinterpret_cast<float *>(w);
+    w += align256(sizeof(float) * (size_t)B * Hv * (chunks(L) + 1) * a.parts);
+    a.dots = reinterpret_cast<float *>(w);
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = dtype == S5_BF16 ? backward<__nv_bfloat16>(a, st) : backward<float>(a, st);
+    return e == cudaSuccess ? S5_OK : cuda_failure(e);
+}
+
+extern "C" s5_status s5_delta_step(const void *q, const void *k, const void *v, s5_dtype dtype, const float *g,
+                                   const float *beta, float scale, int B, int Hk, int Hv, int Dk, int Dv,
+                                   float *state, void *o, s5_stream_t stream) {
+    const s5_status c = check_sizes(B, 1, Hk, Hv, Dk, Dv, dtype);
+    if (c != S5_OK) return c;
+    if (!(scale == scale)) return S5_ERR_INVALID_ARGUMENT;
+    if (B == 0) return S5_OK;
+    const uintptr_t four = dtype == S5_BF16 ? 7 : 15;   // a slice of any head size starts at four values
+    const void *rows[] = {q, k, v, o};
+    for (const void *p : rows)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & four)) return S5_ERR_INVALID_ARGUMENT;
+    if (!floats(g) || !floats(beta) || !aligned16(state)) return S5_ERR_INVALID_ARGUMENT;
+    cudaLaunchAttribute attr;
+    set_programmatic(attr);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((Dv + 31) / 32, Hv, B);
+    cfg.blockDim = dim3(256);
+    cfg.stream = (cudaStream_t)stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const bool wide = Dk > 128;
+    cudaError_t e;
+    if (dtype == S5_BF16)
+        e = wide ? cudaLaunchKernelEx(&cfg, delta_step_kernel<__nv_bfloat16, 8>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o)
+                 : cudaLaunchKernelEx(&cfg, delta_step_kernel<__nv_bfloat16, 4>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o);
+    else
+        e = wide ? cudaLaunchKernelEx(&cfg, delta_step_kernel<float, 8>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o)
+                 : cudaLaunchKernelEx(&cfg, delta_step_kernel<float, 4>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o);
+    return e == cudaSuccess ? S5_OK : cuda_failure(e);
+}

@@ -1,0 +1,57 @@
+// s5_delta.cuh -- what the kernels of the gated delta rule share
+// (s5_delta.cu: entry points, streaming step, CUDA-core sweeps;
+// s5_delta_tc.cu: tensor-core chunks).
+#pragma once
+#include "s5_internal.cuh"
+
+namespace s5 {
+namespace delta {
+
+constexpr int CHUNK = 64;   // tokens between two kept states
+
+// Arrays as in include/s5.h.  Row of token t of sequence b: b * L + t.
+struct Args {
+    const void *q, *k, *v;
+    long long ldq, ldk, ldv;          // elements between two tokens
+    const float *g, *beta;            // [B][L][Hv]
+    const float *s0;                  // [B][Hv][Dk][Dv] or null
+    float scale;
+    int B, L, Hk, Hv, Dk, Dv;
+    void *o;
+    long long ldo;
+    float *s_last;                    // or null
+    // kept for the backward pass (null: nothing is kept)
+    float *e;                         // [B][L][Hv][Dv]   v_t - a_t S_{t-1}^T k_t
+    float *o32;                       // [B][L][Hv][Dv]   o before its rounding
+    float *states;                    // [B][Hv][N + 1][Dk][Dv]   S entering chunk c; [N] is the last state
+    // backward
+    const void *dout;                 // dL/do
+    long long lddo;
+    const float *ds_last;             // or null
+    void *dq, *dk, *dv;
+    long long lddq, lddk, lddv;
+    float *dg, *dbeta, *ds0;          // ds0 may be null
+    // backward workspace
+    float *x;                         // [B][L][Hv][Dv]   dL/du_t
+    float *dqh, *dkh;                 // [B][L][Hv][Dk]   per value head
+    float *inner;                     // [B][Hv][N + 1][parts]   parts of <S_c, dL/dS_c>
+    float *dots;                      // [B][L][Hv]       o.do - v.dv
+    int parts;
+    void *images;                     // operand images of the tensor-core path
+};
+
+__host__ __device__ inline int chunks(int L) { return (L + CHUNK - 1) / CHUNK; }
+
+// A decay factor: exp(g) is zero in 32 bits below -104, so that g = -inf and
+// the type's lowest value (a reset of the state) act as -128, which sums of
+// 64 can hold; NaN stays NaN.
+__device__ __forceinline__ float clamp_g(float g) { return g < -128.0f ? -128.0f : g; }
+
+// Whether the tensor-core path takes these arguments.
+bool tc_supported(const Args &a, s5_dtype dtype, bool backward);
+size_t tc_image_bytes(int B, int L, int Hv);
+cudaError_t tc_forward(const Args &a, cudaStream_t st);
+cudaError_t tc_backward_scan(const Args &a, cudaStream_t st);
+
+}  // namespace delta
+}  // namespace s5

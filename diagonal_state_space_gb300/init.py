@@ -81,4 +81,32 @@ def init_s5(P: int, H: int, blocks: int = 1, dt_min: float = 1e-3, dt_max: float
             c_tilde.astype(np.complex64), d.astype(np.float32))
 
 
-__all__ = ["hippo_normal", "hippo_normal_eig", "init_s5"]
+def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       trained: int | None = None, low: float = 1.0, high: float = 32.0):
+    """(freq [rot/2] float64, amplitude) of the position rotation: pair i turns by base^(-2i/rot) a position.
+
+    scaling stretches a context `factor` times the trained one:
+      "linear"    positions divided by factor, f / factor
+      "ntk"       base times factor^(rot / (rot - 2)): the fastest pair as trained, the slowest divided by factor
+      "by_parts"  pairs that make at least `high` turns over the `trained` positions stay, those that make at most
+                  `low` are divided by factor, linear in the turns between; amplitude 0.1 ln(factor) + 1
+    """
+    if rot < 2 or rot % 2 or base <= 0 or factor < 1:
+        raise ValueError("rot must be even and positive, base positive, factor at least 1")
+    i = np.arange(rot // 2, dtype=np.float64)
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    freq = float(base) ** (-2.0 * i / rot)
+    if scaling in ("none", "ntk"):
+        return freq, 1.0
+    if scaling == "linear":
+        return freq / factor, 1.0
+    if scaling == "by_parts":
+        if trained is None or trained < 1 or not low < high:
+            raise ValueError("by_parts needs the trained length and low < high")
+        keep = np.clip((trained * freq / (2 * np.pi) - low) / (high - low), 0.0, 1.0)
+        return freq * keep + freq / factor * (1.0 - keep), 0.1 * float(np.log(factor)) + 1.0
+    raise ValueError("scaling must be none, linear, ntk or by_parts")
+
+
+__all__ = ["rotary_frequencies", "hippo_normal", "hippo_normal_eig", "init_s5"]

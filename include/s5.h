@@ -352,6 +352,125 @@ s5_status s5_ssm_backward(const float *lambda, const float *log_dt, const float 
                           float *dlambda, float *dlog_dt, float *db_tilde, float *dc_tilde,
                           float *dd, void *workspace, size_t workspace_bytes, s5_stream_t stream);
 
+/* ========================================================================
+ * Gated delta rule: a linear recurrence with a matrix state and data-dependent
+ * transitions, for layers whose queries, keys and values are projections of
+ * the tokens.  Per sequence and value head h, with key head h / (Hv / Hk),
+ * a_t = exp(g_t) and state S [Dk][Dv] (float32):
+ *   e_t = v_t - a_t S_{t-1}^T k_t        what the state does not yet answer for k_t
+ *   S_t = a_t S_{t-1} + beta_t k_t e_t^T
+ *   o_t = scale S_t^T q_t
+ * Keys of unit norm and 0 <= beta <= 1 keep the transition a contraction; the
+ * calls do not normalise (s5_qk_norm_rotary below does).  g <= 0 decays; g of
+ * -inf (or any g below -128) resets the state before its token.
+ *
+ * Arrays: q, k [B][L][Hk][Dk], v, o [B][L][Hv][Dv] of `dtype`, each with its
+ * own pitch in elements between two tokens (ld >= heads * head size; a batch
+ * is L pitches), so that slices of a fused projection need no copy.  g, beta
+ * [B][L][Hv], states [B][Hv][Dk][Dv] float32 contiguous.  Bases 16-byte
+ * aligned (g, beta: 4-byte, so that one token's slice can be passed).  Dk and Dv: multiples of 4 up to 256 (S5_ERR_UNSUPPORTED
+ * otherwise); Hv a multiple of Hk; B L Hv <= 2^30.  L = 0 leaves the state as
+ * it is; B = 0 is a no-op.  Inputs must be finite but for g.
+ *
+ * Arithmetic: states, sums and decays in 32 bits.  On the tensor cores (bf16
+ * q, k, v with heads of 128, pitches that are multiples of 8) an operand that
+ * is not itself bf16 is carried as a sum of three bf16 values.
+ * ======================================================================== */
+
+/* Bytes of the `saved` buffer that s5_delta_forward fills for
+ * s5_delta_backward (e_t, o_t in 32 bits, the state every 64 tokens), and of
+ * the workspaces of the two calls (scratch, no initialisation).  0 for
+ * arguments that the calls reject. */
+size_t s5_delta_saved_size(int B, int L, int Hv, int Dk, int Dv);
+size_t s5_delta_workspace_size(int B, int L, int Hv, int Dk, int Dv, int backward);
+
+/* The recurrence over whole sequences, from s0 (NULL: zero).  s_last (may be
+ * NULL, may be s0) gets the state after token L.  saved NULL: nothing is
+ * kept.  Asynchronous; errors S5_ERR_INVALID_ARGUMENT, S5_ERR_UNSUPPORTED,
+ * S5_ERR_CUDA. */
+s5_status s5_delta_forward(const void *q, long long ldq, const void *k, long long ldk, const void *v,
+                           long long ldv, s5_dtype dtype, const float *g, const float *beta,
+                           const float *s0, float scale, int B, int L, int Hk, int Hv, int Dk, int Dv,
+                           void *o, long long ldo, float *s_last, void *saved, size_t saved_bytes,
+                           void *workspace, size_t workspace_bytes, s5_stream_t stream);
+
+/* Gradients of sum(dout * o) + sum(ds_last * s_last) (ds_last NULL: zero),
+ * with the forward's inputs and its `saved` buffer:
+ *   Z_t = scale q_t dout_t^T + a_{t+1} (Z_{t+1} - k_{t+1} dv_{t+1}^T)   (dL/dS_t)
+ *   dv_t = beta_t Z_t^T k_t,  dbeta_t = (Z_t^T k_t) . e_t,  dq_t = scale S_t dout_t,
+ *   dk_t = beta_t Z_t e_t - a_t S_{t-1} dv_t,  dg_t = <a_t S_{t-1}, Z_t - k_t dv_t^T>,
+ *   ds0 = a_1 (Z_1 - k_1 dv_1^T).
+ * dq, dk (summed over the value heads of a key head), dv of `dtype` with their
+ * pitches; dg, dbeta [B][L][Hv] and ds0 (NULL: not wanted) float32.  No
+ * atomics: equal inputs give equal bits. */
+s5_status s5_delta_backward(const void *q, long long ldq, const void *k, long long ldk, const void *v,
+                            long long ldv, s5_dtype dtype, const float *g, const float *beta,
+                            const float *s0, float scale, int B, int L, int Hk, int Hv, int Dk, int Dv,
+                            const void *dout, long long lddo, const float *ds_last, const void *saved,
+                            size_t saved_bytes, void *dq, long long lddq, void *dk, long long lddk, void *dv,
+                            long long lddv, float *dg, float *dbeta, float *ds0, void *workspace,
+                            size_t workspace_bytes, s5_stream_t stream);
+
+/* One token per sequence: q, k [B][Hk][Dk], v, o [B][Hv][Dv] of `dtype`, g,
+ * beta [B][Hv]; state [B][Hv][Dk][Dv] is updated in place.  All contiguous;
+ * q, k, v, o need start at a multiple of four values only.
+ * Launched with programmatic stream serialisation, as s5_step. */
+s5_status s5_delta_step(const void *q, const void *k, const void *v, s5_dtype dtype, const float *g,
+                        const float *beta, float scale, int B, int Hk, int Hv, int Dk, int Dv, float *state,
+                        void *o, s5_stream_t stream);
+
+/* ========================================================================
+ * Position rotation, alone or with the norm of each head in the same pass.
+ * A row x is one head's D values of one token at position p.  The first rot
+ * values form rot/2 pairs, (x_i, x_{i + rot/2}) in the half layout,
+ * (x_2i, x_2i+1) in the interleaved one; pair i turns by the angle
+ * p freq[i] and is scaled by `amplitude`; values past rot stay as they are:
+ *   y_a = A (cos z_a - sin z_b),  y_b = A (sin z_a + cos z_b),  z = x r w,
+ *   r = 1, 1/sqrt(mean x^2 + eps) or 1/sqrt(sum x^2 + eps) by `norm`,
+ *   w [D] float32, or ones (NULL).
+ * Angles are taken modulo whole turns in 64-bit fixed point, so that any
+ * position below 2^63 keeps its phase as far as freq (float64) defines it.
+ * Rows: [T][H][D] of `dtype` with a pitch in elements between two tokens; an
+ * output may be its input (same pitch).  positions [T], freq [rot/2] on the
+ * device; rot = 0 needs neither.  D even, up to 256 (S5_ERR_UNSUPPORTED
+ * otherwise), rot even, 0 <= rot <= D; amplitude > 0; T H <= 2^31.  Sums in 32
+ * bits, one rounding at the end.  Asynchronous, launched with programmatic
+ * stream serialisation.
+ * ======================================================================== */
+typedef enum { S5_ROTARY_HALF = 0, S5_ROTARY_INTERLEAVED = 1 } s5_rotary_layout;
+typedef enum { S5_NORM_NONE = 0, S5_NORM_RMS = 1, S5_NORM_L2 = 2 } s5_norm;
+
+/* The rotation of one array.  inverse != 0 turns back by the same angles with
+ * the same amplitude: the transpose, which is the rotation's backward pass. */
+s5_status s5_rotary(const void *x, long long ldx, s5_dtype dtype, const long long *positions,
+                    const double *freq, int rot, s5_rotary_layout layout, float amplitude, int inverse,
+                    long long T, int H, int D, void *y, long long ldy, s5_stream_t stream);
+
+/* Norm and rotation of queries [T][Hq][D] and keys [T][Hk][D] in one launch. */
+s5_status s5_qk_norm_rotary(const void *q, long long ldq, const void *k, long long ldk, s5_dtype dtype,
+                            const float *q_weight, const float *k_weight, s5_norm norm, float eps,
+                            const long long *positions, const double *freq, int rot,
+                            s5_rotary_layout layout, float amplitude, long long T, int Hq, int Hk, int D,
+                            void *q_out, long long ldqo, void *k_out, long long ldko, s5_stream_t stream);
+
+/* Workspace of the backward pass, needed where a weight's gradient is wanted. */
+size_t s5_qk_norm_rotary_workspace_size(int D);
+
+/* Its backward pass from the outputs' gradients dq_out, dk_out:
+ *   dz = A R^T dy,  dw = sum over rows of dz x r,  dx = r w dz - x r^3 sum(w dz x) / count
+ * with count = D (S5_NORM_RMS) or 1 (S5_NORM_L2).  dq_weight, dk_weight [D]
+ * float32 or NULL.  dq may be q or dq_out, dk likewise (same pitch).  No
+ * atomics: equal inputs give equal bits. */
+s5_status s5_qk_norm_rotary_backward(const void *q, long long ldq, const void *k, long long ldk,
+                                     s5_dtype dtype, const float *q_weight, const float *k_weight,
+                                     s5_norm norm, float eps, const long long *positions,
+                                     const double *freq, int rot, s5_rotary_layout layout,
+                                     float amplitude, long long T, int Hq, int Hk, int D,
+                                     const void *dq_out, long long lddqo, const void *dk_out,
+                                     long long lddko, void *dq, long long lddq, void *dk, long long lddk,
+                                     float *dq_weight, float *dk_weight, void *workspace,
+                                     size_t workspace_bytes, s5_stream_t stream);
+
 /* Waits for `stream`, returns the first device-side condition latched in
  * `workspace` since the last call (S5_OK if none) and clears it. */
 s5_status s5_sync_status(void *workspace, s5_stream_t stream);
