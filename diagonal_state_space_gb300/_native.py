@@ -52,6 +52,7 @@ SIGNATURES = {
                           + [_vp, _ll, _vp, _vp, _sz, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp,
                              _vp, _sz, _vp]),
     "s5_delta_step": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _f] + [_i] * 5 + [_vp, _vp, _vp]),
+    "s5_delta_fault": (_i, []),
     # position rotation and norms of queries and keys
     "s5_rotary": (_i, [_vp, _ll, _i, _vp, _vp, _i, _i, _f, _i, _ll, _i, _i, _vp, _ll, _vp]),
     "s5_qk_norm_rotary": (_i, [_vp, _ll, _vp, _ll, _i, _vp, _vp, _i, _f, _vp, _vp, _i, _i, _f, _ll,

@@ -1,8 +1,697 @@
+// s5_delta_tc.cu -- the gated delta rule on the 5th-generation tensor cores:
+// bf16 queries, keys and values, heads of 64 or 128.
+//
+// A chunk of 64 tokens that starts from the state S0, with G_i the sum of the
+// chunk's log decays up to token i and D_ij = exp(G_i - G_j):
+//   E = (I + strict lower(D_ij k_i.k_j beta_j))^-1,   P_ij = scale D_ij q_i.k_j (j <= i)
+//   R = V - e^G K S0
+//   e = E R,  o = scale e^G Q S0 + (P beta E) R
+//   S = e^{G_64} S0 + K^T (e^{G_64 - G} beta e)
+// Everything without S0 is done for all chunks at once by delta_prep_kernel:
+// it leaves the 128 x 64 matrix [E; P beta E] of each chunk.  The recurrence
+// over chunks then is three matrix products in a row, one CTA per sequence,
+// head and 64 value columns:
+//   D1 = [K; Q] S0      (128 x 64, depth Dk)
+//   D2 = [E; P beta E] R  (128 x 64, depth 64)
+//   D3 = K^T U          (Dk x 64, depth 64)
+// all of M = 128: the rows 64..127 of the first two give the outputs beside
+// the rows that the recurrence needs.
+//
+// Precision.  Keys, queries and values are bf16 and enter the products as they
+// are.  S0, R, U and [E; P beta E] are 32-bit values, carried as sums of three
+// bf16 values (8 + 8 + 8 significant bits): three products against a bf16
+// operand, six against another split one (the three smallest, below 2^-24, are
+// left out).  One rounding to bf16 instead would leave 2^-9 in the state.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "s5_delta.cuh"
+#include "s5_sm100.cuh"
+
 namespace s5 {
 namespace delta {
-bool tc_supported(const Args &, s5_dtype, bool) { return false; }
-size_t tc_image_bytes(int, int, int) { return 0; }
-cudaError_t tc_forward(const Args &, cudaStream_t) { return cudaErrorNotSupported; }
+using namespace sm100;
+
+namespace {
+
+constexpr int C = CHUNK;
+constexpr uint32_t M2_BYTES = 128 * 128;              // one split of a 128 x 64 matrix
+constexpr uint32_t META_BYTES = 1024;                 // up, down, beta [64], total decay
+constexpr uint32_t IMG_BYTES = 3 * M2_BYTES + META_BYTES;
+constexpr unsigned long long WAIT_NS = 2000000000ull;
+
+__device__ int g_delta_fault = 0;   // a bounded wait ran out
+
+struct Meta {            // of one chunk and value head
+    float up[C];         // e^{G_i}
+    float down[C];       // e^{G_64 - G_i}
+    float beta[C];
+    float last;          // e^{G_64}
+};
+static_assert(sizeof(Meta) <= META_BYTES, "meta block");
+
+// ---------------------------------------------------------------------------
+// Splits.  x = h + m + l with bf16 h, m, l; two values at a time.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void split3(float a, float b, uint32_t &h, uint32_t &m, uint32_t &l) {
+    h = pack2(a, b);
+    a -= __uint_as_float(h << 16), b -= __uint_as_float(h & 0xffff0000u);
+    m = pack2(a, b);
+    a -= __uint_as_float(m << 16), b -= __uint_as_float(m & 0xffff0000u);
+    l = pack2(a, b);
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Writes 32 values of row `row` (columns c0 .. c0 + 31 of 64) as three images
+// `stride` bytes apart, 128 bytes a row in the 128-byte swizzle.
+__device__ __forceinline__ void store_split32(uint32_t img, uint32_t stride, int row, int c0, const float (&v)[32]) {
+    const uint32_t at = img + (uint32_t)row * 128u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t h[4], m[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split3(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], h[i], m[i], l[i]);
+        const uint32_t to = at + (uint32_t)(((c0 / 8 + j) ^ (row & 7)) << 4);
+        sts128(to, h[0], h[1], h[2], h[3]);
+        sts128(to + stride, m[0], m[1], m[2], m[3]);
+        sts128(to + 2 * stride, l[0], l[1], l[2], l[3]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Preparation: one CTA per chunk and key head; the products k.k and q.k are
+// shared by the key head's value heads.
+//
+// The inverse goes by blocks: the four 16 x 16 blocks on the diagonal by
+// substitution (one column per lane), then
+//   [[A, 0], [B, D]]^-1 = [[A^-1, 0], [-D^-1 B A^-1, D^-1]]
+// to 32 and to 64 rows.  All of it in 32 bits on the CUDA cores: the inverse
+// is what the states' precision hangs on, and its 0.1 MFMA per chunk and head
+// are less than the conversions that a split product would take.
+//
+// TRANS: (I + strict lower(beta_i D_ij k_i.k_j))^-1 = T and [T; P T] instead,
+// which the backward pass uses.
+// ---------------------------------------------------------------------------
+constexpr int PT = 128;             // threads
+constexpr int LD = 68;              // pitch of 64-wide fp32 tiles (16-byte rows, no conflicts on columns of 4)
+
+struct PrepSmem {
+    float kk[C][LD], qk[C][LD];     // products of the key head
+    float a[C][LD];                 // triangular system, then scratch of the blocks
+    float t[C][LD];                 // its inverse
+    float p[C][LD];                 // P (times beta)
+    float hi[C], lo[C], beta[C];    // cumulated log decay as a pair of floats
+};
+
+// mma.sync m16n8k16: D += A B^T, rows of A and B in shared memory.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int DK, bool TRANS> __global__ void __launch_bounds__(PT) delta_prep_kernel(const Args a) {
+    extern __shared__ __align__(16) unsigned char psm[];
+    PrepSmem &s = *reinterpret_cast<PrepSmem *>(psm);
+    constexpr int KP = DK + 8;      // bf16 pitch: 4 banks a row, conflict-free fragments
+    __nv_bfloat16 *sk = reinterpret_cast<__nv_bfloat16 *>(&s.t[0][0]);   // [64][KP] until the products are done
+    __nv_bfloat16 *sq = sk + C * KP;
+    static_assert(2 * C * KP * 2 <= 2 * sizeof(s.t), "tiles fit the inverse's and P's space");
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, group = a.Hv / a.Hk;
+    const int t0 = c * C, nt = min(C, a.L - t0), N = chunks(a.L);
+    const long long row0 = (long long)b * a.L + t0;
+    for (int i = tid; i < C * (DK / 8); i += PT) {
+        const int t = i / (DK / 8), d = i % (DK / 8) * 8;
+        uint4 xk = make_uint4(0, 0, 0, 0), xq = xk;
+        if (t < nt) {
+            xk = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + d);
+            xq = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + d);
+        }
+        *reinterpret_cast<uint4 *>(sk + t * KP + d) = xk;
+        *reinterpret_cast<uint4 *>(sq + t * KP + d) = xq;
+    }
+    __syncthreads();
+    {   // warp w: rows 16 w .. 16 w + 15 of both products, columns up to its own
+        float kk[8][4] = {}, qk[8][4] = {};
+        const int g = lane / 4, q2 = lane % 4 * 2;
+#pragma unroll 2
+        for (int k0 = 0; k0 < DK; k0 += 16) {
+            uint32_t fk[4], fq[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = (16 * warp + g + (i & 1) * 8) * KP + k0 + q2 + (i >> 1) * 8;
+                fk[i] = *reinterpret_cast<const uint32_t *>(sk + at);
+                fq[i] = *reinterpret_cast<const uint32_t *>(sq + at);
+            }
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                if (n > 2 * warp + 1) continue;
+                const int at = (8 * n + g) * KP + k0 + q2;
+                const uint32_t b0 = *reinterpret_cast<const uint32_t *>(sk + at);
+                const uint32_t b1 = *reinterpret_cast<const uint32_t *>(sk + at + 8);
+                mma16816(kk[n], fk, b0, b1);
+                mma16816(qk[n], fq, b0, b1);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 16 * warp + g + 8 * i, col = 8 * n + q2;
+                *reinterpret_cast<float2 *>(&s.kk[r][col]) = make_float2(kk[n][2 * i], kk[n][2 * i + 1]);
+                *reinterpret_cast<float2 *>(&s.qk[r][col]) = make_float2(qk[n][2 * i], qk[n][2 * i + 1]);
+            }
+    }
+    for (int j = 0; j < group; ++j) {
+        const int h = hk * group + j;
+        unsigned char *img = static_cast<unsigned char *>(a.images) + (((long long)b * a.Hv + h) * N + c) * IMG_BYTES;
+        __syncthreads();
+        if (warp == 0) {
+            // G in float64 (64 terms of up to 128), kept as two floats, so that
+            // a small difference of large sums keeps 24 bits
+            double x0 = 2 * lane < nt ? (double)clamp_g(a.g[(row0 + 2 * lane) * a.Hv + h]) : 0.0;
+            double x1 = 2 * lane + 1 < nt ? (double)clamp_g(a.g[(row0 + 2 * lane + 1) * a.Hv + h]) : 0.0;
+            double w = x0 + x1;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const double up = __shfl_up_sync(0xffffffffu, w, m);
+                if (lane >= m) w += up;
+            }
+            const double tot = __shfl_sync(0xffffffffu, w, 31);
+            Meta *meta = reinterpret_cast<Meta *>(img + 3 * M2_BYTES);
+            const double G[2] = {w - x1, w};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                const float be = t < nt ? a.beta[(row0 + t) * a.Hv + h] : 0.0f;
+                s.hi[t] = (float)G[i];
+                s.lo[t] = (float)(G[i] - (double)s.hi[t]);
+                s.beta[t] = be;
+                meta->up[t] = expf((float)G[i]);
+                meta->down[t] = expf((float)(tot - G[i]));
+                meta->beta[t] = be;
+            }
+            if (lane == 0) meta->last = expf((float)tot);
+        }
+        __syncthreads();
+        for (int i = tid; i < C * C; i += PT) {
+            const int r = i / C, col = i % C;
+            const float d = col <= r ? expf((s.hi[r] - s.hi[col]) + (s.lo[r] - s.lo[col])) : 0.0f;
+            s.a[r][col] = col < r ? d * s.kk[r][col] * (TRANS ? s.beta[r] : s.beta[col]) : 0.0f;
+            s.p[r][col] = col <= r ? a.scale * d * s.qk[r][col] * (TRANS ? 1.0f : s.beta[col]) : 0.0f;
+            s.t[r][col] = 0.0f;
+        }
+        __syncthreads();
+        if (lane < 16) {   // warp w: block w of the diagonal, lane: column of its inverse
+            const int o = 16 * warp;
+            float x[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float v = r == lane ? 1.0f : 0.0f;
+#pragma unroll
+                for (int m = 0; m < r; ++m) v = fmaf(-s.a[o + r][o + m], x[m], v);
+                x[r] = v;
+                s.t[o + r][o + lane] = v;
+            }
+        }
+        __syncthreads();
+        // 32-row blocks: -D^-1 (B A^-1), both pairs at once, four values per thread
+        {
+            const int o = 32 * (tid / 64), r = tid % 64 / 4, c4 = tid % 4 * 4;
+            float v[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < 16; ++m) {
+                const float x = s.a[o + 16 + r][o + m];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fmaf(x, s.t[o + m][o + c4 + i], v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s.a[o + r][o + 16 + c4 + i] = v[i];   // the system's unused upper part
+            __syncthreads();
+            float w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < 16; ++m) {
+                const float x = s.t[o + 16 + r][o + 16 + m];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = fmaf(-x, s.a[o + m][o + 16 + c4 + i], w[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s.t[o + 16 + r][o + c4 + i] = w[i];
+        }
+        __syncthreads();
+        // 64 rows: eight values per thread
+        {
+            const int r = tid / 4, c8 = tid % 4 * 8;
+            float v[8] = {};
+#pragma unroll 8
+            for (int m = 0; m < 32; ++m) {
+                const float x = s.a[32 + r][m];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = fmaf(x, s.t[m][c8 + i], v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s.a[r][32 + c8 + i] = v[i];
+            __syncthreads();
+            float w[8] = {};
+#pragma unroll 8
+            for (int m = 0; m < 32; ++m) {
+                const float x = s.t[32 + r][32 + m];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = fmaf(-x, s.a[m][32 + c8 + i], w[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s.t[32 + r][c8 + i] = w[i];
+        }
+        __syncthreads();
+        // P E: rows r, r + 16, r + 32, r + 48 and eight columns per thread, into
+        // a; both factors are triangular, so that columns m < c8 add nothing
+        {
+            const int r = tid / 8, c8 = tid % 8 * 8;
+            float v[4][8] = {};
+            for (int m = c8; m < C; ++m) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = s.t[m][c8 + i];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x = s.p[r + 16 * k][m];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] = fmaf(x, y[i], v[k][i]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s.a[r + 16 * k][c8 + i] = v[k][i];
+        }
+        __syncthreads();
+        for (int i = tid; i < 128 * 8; i += PT) {
+            const int r = i / 8, ch = i % 8;
+            const float *x = r < C ? &s.t[r][8 * ch] : &s.a[r - C][8 * ch];
+            uint32_t hh[4], mm[4], ll[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) split3(x[2 * k], x[2 * k + 1], hh[k], mm[k], ll[k]);
+            unsigned char *to = img + r * 128 + ((ch ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4 *>(to) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+            *reinterpret_cast<uint4 *>(to + M2_BYTES) = make_uint4(mm[0], mm[1], mm[2], mm[3]);
+            *reinterpret_cast<uint4 *>(to + 2 * M2_BYTES) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Recurrence over chunks.
+// ---------------------------------------------------------------------------
+constexpr int NV = 64;                       // value columns of a CTA
+constexpr int SCAN_THREADS = 320;            // 8 compute warps, MMA issue, copies
+constexpr uint32_t KQ_BOX = 128 * 128;       // 128 rows (64 keys, 64 queries) of 64 values
+constexpr uint32_t RU_IMG = 64 * 128;        // one split of a 64 x 64 operand
+
+template <int DK> struct ScanSmem {
+    static constexpr uint32_t KQ = KQ_BOX * (DK / 64);
+    static constexpr uint32_t S_IMG = DK * 128;
+    static constexpr uint32_t kq = 0;                      // two stages
+    static constexpr uint32_t img = kq + 2 * KQ;           // [E; P beta E] and meta
+    static constexpr uint32_t s = img + IMG_BYTES;
+    static constexpr uint32_t ru = s + 3 * S_IMG;
+    static constexpr uint32_t bars = ru + 3 * RU_IMG;
+    static constexpr uint32_t total = bars + 256 + 1024;   // + alignment slack
+};
+
+struct ScanBars {
+    uint64_t kq_full[2], kq_empty[2], img_full, img_empty, d1, d2, d3, s_ready, r_ready, u_ready, drain;
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+// K-major: 128-byte rows of 64 K values; step k of 16.  MN-major: 128-byte
+// rows of 64 M or N values, one row per K value; the next 64 are `far` on.
+__device__ __forceinline__ uint64_t desc_k(uint32_t base, int k) { return desc128(base + 32u * k, 16u, 1024u); }
+__device__ __forceinline__ uint64_t desc_mn(uint32_t base, int k, uint32_t far) {
+    return desc128(base + 2048u * k, far, 1024u);
+}
+constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;
+
+__device__ __forceinline__ bool scan_wait(uint64_t *bar, uint32_t parity, ScanBars *sb) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    for (;;) {
+        if (mbar_try_wait_sleep(bar, parity, 100000)) return true;
+        if (*reinterpret_cast<volatile int *>(&sb->abort)) return false;
+        if (global_ns() - t0 > WAIT_NS) {
+            *reinterpret_cast<volatile int *>(&sb->abort) = 1;
+            atomicExch(&g_delta_fault, 1);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int c0, int c1, int c2, int c3, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// The 32 values of one token row from column c0 on.
+__device__ __forceinline__ void load_bf16_32(const __nv_bfloat16 *p, bool on, uint4 (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = on ? *reinterpret_cast<const uint4 *>(p + 8 * j) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ float bf_at(const uint4 (&v)[4], int i) {
+    const uint32_t w = i % 8 / 2 == 0 ? v[i / 8].x : i % 8 / 2 == 1 ? v[i / 8].y : i % 8 / 2 == 2 ? v[i / 8].z : v[i / 8].w;
+    return __uint_as_float(i % 2 ? (w & 0xffff0000u) : (w << 16));
+}
+__device__ __forceinline__ void store_f32_32(float *p, const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4 *>(p + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+__device__ __forceinline__ void store_bf16_32(__nv_bfloat16 *p, const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4 *>(p + 8 * j) =
+            make_uint4(pack2(v[8 * j], v[8 * j + 1]), pack2(v[8 * j + 2], v[8 * j + 3]), pack2(v[8 * j + 4], v[8 * j + 5]),
+                       pack2(v[8 * j + 6], v[8 * j + 7]));
+}
+__device__ __forceinline__ void load_acc(uint32_t addr, float (&v)[32]) {
+    uint32_t r[32];
+    tmem_ld32(addr, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// What the compute warps wrote to shared memory and read from TMEM is done
+// before the MMA warp goes on.
+__device__ __forceinline__ void hand_over(uint64_t *bar, int lane) {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+template <int DK>
+__global__ void __launch_bounds__(SCAN_THREADS, 1)
+delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_q, const Args a) {
+    using L = ScanSmem<DK>;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    ScanBars *sb = reinterpret_cast<ScanBars *>(smem + L::bars);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int n0 = blockIdx.x * NV, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
+    const int N = chunks(a.L);
+    const long long bh = (long long)b * a.Hv + h;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) mbar_init(&sb->kq_full[i], 1), mbar_init(&sb->kq_empty[i], 1);
+        mbar_init(&sb->img_full, 1), mbar_init(&sb->img_empty, 8);
+        mbar_init(&sb->d1, 1), mbar_init(&sb->d2, 1), mbar_init(&sb->d3, 1);
+        mbar_init(&sb->s_ready, 8), mbar_init(&sb->r_ready, 4), mbar_init(&sb->u_ready, 4);
+        mbar_init(&sb->drain, 1);
+        sb->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&sb->tmem, 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sb->tmem, D1 = tmem, D2 = tmem + 64, D3 = tmem + 128;
+
+    if (warp == 9) {
+        // ---------------------------------------------------------- copies
+        bool ok = true;
+        int c = 0;
+        for (; ok && c < N; ++c) {
+            const int st = c & 1;
+            if (c >= 2) ok = __shfl_sync(0xffffffffu, (int)scan_wait(&sb->kq_empty[st], ((c >> 1) - 1) & 1, sb), 0);
+            if (!ok) break;
+            if (elect_one()) {
+                unsigned char *to = smem + L::kq + st * L::KQ;
+                mbar_arrive_tx(&sb->kq_full[st], L::KQ);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x) {
+                    tma_load_4d(to + x * KQ_BOX, &tmap_k, 64 * x, hk, c * C, b, &sb->kq_full[st]);
+                    tma_load_4d(to + x * KQ_BOX + KQ_BOX / 2, &tmap_q, 64 * x, hk, c * C, b, &sb->kq_full[st]);
+                }
+            }
+            __syncwarp();
+            if (c >= 1) ok = __shfl_sync(0xffffffffu, (int)scan_wait(&sb->img_empty, (c - 1) & 1, sb), 0);
+            if (!ok) {
+                ++c;
+                break;
+            }
+            if (elect_one()) {
+                mbar_arrive_tx(&sb->img_full, IMG_BYTES);
+                bulk_load(smem + L::img, static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES, IMG_BYTES,
+                          &sb->img_full);
+            }
+            __syncwarp();
+        }
+        // after a wait that gave up: copies in flight land before the CTA ends
+        if (!ok) {
+            const unsigned long long t0 = global_ns();
+            for (int j = max(0, c - 2); j < c; ++j)
+                while (!mbar_try_wait_sleep(&sb->kq_full[j & 1], (j >> 1) & 1, 100000))
+                    if (global_ns() - t0 > 200000000ull) break;
+            while (global_ns() - t0 < 1000000ull) {}
+        }
+    } else if (warp == 8) {
+        // ---------------------------------------------------------- products
+        const uint32_t id1 = idesc_bf16_f32(128, NV) | B_MN, id3 = id1 | A_MN;
+        const uint32_t img = smem_addr(smem + L::img), sS = smem_addr(smem + L::s), sR = smem_addr(smem + L::ru);
+        bool ok = true;
+        for (int c = 0; ok && c < N; ++c) {
+            const int st = c & 1;
+            const uint32_t kq = smem_addr(smem + L::kq + st * L::KQ);
+            ok = scan_wait(&sb->kq_full[st], (c >> 1) & 1, sb) && scan_wait(&sb->s_ready, c & 1, sb);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int p = 2; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k)
+                        mma_bf16(D1, desc_k(kq + (k / 4) * KQ_BOX, k % 4), desc_mn(sS + p * L::S_IMG, k, 16), id1, !(p == 2 && k == 0));
+                mma_commit(&sb->d1);
+            }
+            __syncwarp();
+            ok = scan_wait(&sb->img_full, c & 1, sb) && scan_wait(&sb->r_ready, c & 1, sb);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)     // the small products first
+#pragma unroll
+                    for (int p = 0; p <= sum; ++p)
+#pragma unroll
+                        for (int k = 0; k < C / 16; ++k)
+                            mma_bf16(D2, desc_k(img + p * M2_BYTES, k), desc_mn(sR + (sum - p) * RU_IMG, k, 16), id1,
+                                     !(sum == 2 && p == 0 && k == 0));
+                mma_commit(&sb->d2);
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, scan_wait(&sb->u_ready, c & 1, sb));
+            if (!ok) break;
+            tc_fence_after();
+            // M is 128 for heads of 64 too: their lanes 64..127 of D3 come from
+            // whatever follows the keys in shared memory, and are not read
+            if (elect_one()) {
+#pragma unroll
+                for (int p = 2; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        mma_bf16(D3, desc_mn(kq, k, KQ_BOX), desc_mn(sR + p * RU_IMG, k, 16), id3, !(p == 2 && k == 0));
+                mma_commit(&sb->d3);
+                mma_commit(&sb->kq_empty[st]);
+            }
+            __syncwarp();
+        }
+        // every MMA has completed before TMEM is freed
+        if (elect_one()) mma_commit(&sb->drain);
+        __syncwarp();
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait_sleep(&sb->drain, 0, 100000))
+            if (global_ns() - t0 > 200000000ull) break;
+    } else {
+        // ---------------------------------------------------------- compute
+        // warp w: TMEM lanes 32 (w % 4) on, columns 32 (w / 4) on.  Lanes 0..63
+        // are tokens of R, e and U, lanes 64..127 tokens of o; in D3 and in
+        // the state a lane is a key index.
+        const int q = warp & 3, c0 = warp / 4 * 32, row = 32 * q + lane;
+        __syncwarp();
+        const bool keys = q < 2;                 // R, U rows; else o rows
+        const int tk = row & 63;                 // token in the chunk
+        const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+        const uint32_t d1 = D1 + lane_base + c0, d2 = D2 + lane_base + c0, d3 = D3 + lane_base + c0;
+        const uint32_t sS = smem_addr(smem + L::s), sR = smem_addr(smem + L::ru);
+        const Meta *meta = reinterpret_cast<const Meta *>(smem + L::img + 3 * M2_BYTES);
+        const bool state = row < DK;
+        const long long mat = (long long)DK * a.Dv;
+        float S[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 t = (a.s0 && state) ? *reinterpret_cast<const float4 *>(a.s0 + bh * mat + (long long)row * a.Dv + n0 + c0 + 4 * j)
+                                             : make_float4(0, 0, 0, 0);
+            S[4 * j] = t.x, S[4 * j + 1] = t.y, S[4 * j + 2] = t.z, S[4 * j + 3] = t.w;
+        }
+        if (state) store_split32(sS, L::S_IMG, row, c0, S);
+        hand_over(&sb->s_ready, lane);
+        bool ok = true;
+        for (int c = 0; c < N; ++c) {
+            const int t = c * C + tk;
+            const bool on = t < a.L;
+            const long long tok = (long long)b * a.L + t;
+            const long long out = (tok * a.Hv + h) * a.Dv + n0 + c0;
+            uint4 v[4];
+            if (keys)
+                load_bf16_32(static_cast<const __nv_bfloat16 *>(a.v) + tok * a.ldv + (long long)h * a.Dv + n0 + c0, on, v);
+            if (a.states && state) store_f32_32(a.states + (bh * (N + 1) + c) * mat + (long long)row * a.Dv + n0 + c0, S);
+            float x[32], y[32];
+            ok = scan_wait(&sb->img_full, c & 1, sb) && scan_wait(&sb->d1, c & 1, sb);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            load_acc(d1, x);
+            const float up = meta->up[tk], down = meta->down[tk], be = meta->beta[tk], last = meta->last;
+            if (keys) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = fmaf(-up, x[i], bf_at(v, i));
+                store_split32(sR, RU_IMG, tk, c0, x);
+                hand_over(&sb->r_ready, lane);
+            }
+            ok = scan_wait(&sb->d2, c & 1, sb);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            if (lane == 0) mbar_arrive(&sb->img_empty);   // D2 is done with the matrix, this warp with its factors
+            load_acc(d2, y);
+            if (keys) {
+                if (a.e && on) store_f32_32(a.e + out, y);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] *= be * down;
+                store_split32(sR, RU_IMG, tk, c0, y);
+                hand_over(&sb->u_ready, lane);
+            } else if (on) {
+                const float w = a.scale * up;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = fmaf(w, x[i], y[i]);
+                store_bf16_32(static_cast<__nv_bfloat16 *>(a.o) + tok * a.ldo + (long long)h * a.Dv + n0 + c0, y);
+                if (a.o32) store_f32_32(a.o32 + out, y);
+            }
+            ok = scan_wait(&sb->d3, c & 1, sb);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            if (state) {
+                load_acc(d3, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) S[i] = fmaf(last, S[i], x[i]);
+                if (c + 1 < N) store_split32(sS, L::S_IMG, row, c0, S);
+            }
+            if (c + 1 < N) hand_over(&sb->s_ready, lane);
+        }
+        if (state) {
+            if (a.s_last) store_f32_32(a.s_last + bh * mat + (long long)row * a.Dv + n0 + c0, S);
+            if (a.states) store_f32_32(a.states + (bh * (N + 1) + N) * mat + (long long)row * a.Dv + n0 + c0, S);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 256);
+}
+
+// Rows [B][L][H][D] of bf16 as boxes of 64 tokens x 64 values of one head;
+// tokens past L read as zeros.
+cudaError_t encode_rows(CUtensorMap *m, const void *p, long long ld, int B, int Ltok, int H, int D) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return cudaErrorNotSupported;
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)Ltok, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * Ltok};
+    const cuuint32_t box[4] = {64, 1, 64, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+template <typename K> cudaError_t big_smem(K *kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int DK, bool TRANS> cudaError_t launch_prep(const Args &a, cudaStream_t st) {
+    const cudaError_t e = big_smem(delta_prep_kernel<DK, TRANS>, sizeof(PrepSmem));
+    if (e != cudaSuccess) return e;
+    delta_prep_kernel<DK, TRANS><<<dim3(chunks(a.L), a.Hk, a.B), PT, sizeof(PrepSmem), st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
+    CUtensorMap mk, mq;
+    cudaError_t e = encode_rows(&mk, a.k, a.ldk, a.B, a.L, a.Hk, DK);
+    if (e == cudaSuccess) e = encode_rows(&mq, a.q, a.ldq, a.B, a.L, a.Hk, DK);
+    if (e == cudaSuccess) e = launch_prep<DK, false>(a, st);
+    if (e == cudaSuccess) e = big_smem(delta_scan_kernel<DK>, ScanSmem<DK>::total);
+    if (e != cudaSuccess) return e;
+    delta_scan_kernel<DK><<<dim3(a.Dv / NV, a.Hv, a.B), SCAN_THREADS, ScanSmem<DK>::total, st>>>(mk, mq, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// bf16 with heads of 64 or 128; pitches that the copies can address (multiples
+// of 16 bytes).  From how many tokens on, both sides measured: see tc_forward.
+bool tc_supported(const Args &a, s5_dtype dtype, bool backward) {
+    if (dtype != S5_BF16 || a.L < 1) return false;
+    if ((a.Dk != 64 && a.Dk != 128) || (a.Dv != 64 && a.Dv != 128)) return false;
+    if (a.ldq % 8 || a.ldk % 8 || a.ldv % 8) return false;
+    return backward ? false : a.ldo % 8 == 0;
+}
+
+size_t tc_image_bytes(int B, int L, int Hv) { return (size_t)B * Hv * chunks(L) * IMG_BYTES; }
+
+cudaError_t tc_forward(const Args &a, cudaStream_t st) {
+    return a.Dk == 128 ? forward<128>(a, st) : forward<64>(a, st);
+}
+
+int fault_take() {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_delta_fault, sizeof(int)) != cudaSuccess) return -1;
+    if (v && cudaMemcpyToSymbol(g_delta_fault, &zero, sizeof(int)) != cudaSuccess) return -1;
+    return v;
+}
+
 }  // namespace delta
 }  // namespace s5
+
+extern "C" int s5_delta_fault(void) { return s5::delta::fault_take(); }

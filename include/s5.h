@@ -411,6 +411,11 @@ s5_status s5_delta_backward(const void *q, long long ldq, const void *k, long lo
                             long long lddv, float *dg, float *dbeta, float *ds0, void *workspace,
                             size_t workspace_bytes, s5_stream_t stream);
 
+/* 1 if a wait inside the tensor-core kernels of the two calls above ran out
+ * since the last call (their results are then not valid), 0 if none; the flag
+ * is cleared.  Synchronises the device. */
+int s5_delta_fault(void);
+
 /* One token per sequence: q, k [B][Hk][Dk], v, o [B][Hv][Dv] of `dtype`, g,
  * beta [B][Hv]; state [B][Hv][Dk][Dv] is updated in place.  All contiguous;
  * q, k, v, o need start at a multiple of four values only.
