@@ -285,7 +285,8 @@ template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(
 
 // One warp per chunk and value head: dg by adding the chunk's terms from its
 // end on top of <S, Z> there.  A token whose decay is zero has no gradient.
-__global__ void __launch_bounds__(256) decay_grads_kernel(const Args a) {
+// tok > 0: the tokens' terms (and dbeta's) come in that many parts.
+__global__ void __launch_bounds__(256) decay_grads_kernel(const Args a, int tok) {
     const int N = chunks(a.L), lane = threadIdx.x % 32;
     const long long id = (long long)blockIdx.x * 8 + threadIdx.x / 32;
     if (id >= (long long)a.B * a.Hv * N) return;
@@ -299,7 +300,20 @@ __global__ void __launch_bounds__(256) decay_grads_kernel(const Args a) {
     for (int half = 0; half < 2; ++half) {
         const int t = c * CHUNK + CHUNK - 1 - 32 * half - lane;
         const long long hv = (b * a.L + t) * a.Hv + h;
-        float w = t < a.L ? a.dots[hv] : 0.0f;
+        float w = 0.0f;
+        if (t < a.L) {
+            if (tok == 0)
+                w = a.dots[hv];
+            else {
+                const long long n = (long long)a.B * a.L * a.Hv * tok;
+                float db = 0.0f;
+                for (int p = 0; p < tok; ++p) {
+                    db += a.dots[hv * tok + p];
+                    w += a.dots[2 * n + hv * tok + p] - a.dots[n + hv * tok + p];
+                }
+                a.dbeta[hv] = db;
+            }
+        }
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const float up = __shfl_up_sync(0xffffffffu, w, m);
@@ -435,9 +449,17 @@ template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
     if ((e = row_sweep<T, false>(a, st)) != cudaSuccess || (e = row_sweep<T, true>(a, st)) != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.L * a.Hv;
     token_grads_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
-    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a);
+    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a, 0);
     const long long n = (long long)a.B * a.L * a.Hk * a.Dk;
     group_sum_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+// The tensor-core path's launches, and the gates' gradients from its parts.
+cudaError_t backward_tc(const Args &a, cudaStream_t st) {
+    const cudaError_t e = tc_backward(a, st);
+    if (e != cudaSuccess) return e;
+    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a, a.Dv / 32);
     return cudaGetLastError();
 }
 
@@ -454,16 +476,24 @@ s5_status check_sizes(long long B, long long L, long long Hk, long long Hv, long
     return S5_OK;
 }
 
+// Regions of the two buffers.  The backward workspace holds what either path
+// needs: dq and dk per value head or the chunks' Z; parts of <S, Z> and of the
+// tokens' sums (16 and 3 Dv / 32 at most).
 struct Sizes {
-    size_t e, states, images;
+    size_t e, states, images, heads, inner, dots;
 };
 Sizes sizes(int B, int L, int Hv, int Dk, int Dv) {
     Sizes s;
-    s.e = align256(sizeof(float) * (size_t)B * L * Hv * Dv);
-    s.states = align256(sizeof(float) * (size_t)B * Hv * (chunks(L) + 1) * Dk * Dv);
-    s.images = align256(tc_image_bytes(B, L, Hv));
+    const size_t rows = (size_t)B * L * Hv, N = chunks(L);
+    s.e = align256(sizeof(float) * rows * Dv);
+    s.states = align256(sizeof(float) * (size_t)B * Hv * (N + 1) * Dk * Dv);
+    s.images = align256(tc_image_bytes(B, L, Hv, Dk, Dv));
+    s.heads = align256(sizeof(float) * rows * Dk);
+    s.inner = align256(sizeof(float) * (size_t)B * Hv * (N + 1) * 16);
+    s.dots = align256(sizeof(float) * rows * 3 * ((Dv + 31) / 32));
     return s;
 }
+size_t z_or_heads(const Sizes &s) { return s.images ? (s.states > 2 * s.heads ? s.states : 2 * s.heads) : 2 * s.heads; }
 
 }  // namespace
 }  // namespace delta
@@ -482,10 +512,7 @@ extern "C" size_t s5_delta_workspace_size(int B, int L, int Hv, int Dk, int Dv, 
     if (check_sizes(B, L, Hv, Hv, Dk, Dv, S5_F32) != S5_OK) return 0;
     const Sizes s = sizes(B, L, Hv, Dk, Dv);
     size_t n = 256 + s.images;
-    if (backward)
-        n += s.e + 2 * align256(sizeof(float) * (size_t)B * L * Hv * Dk) +
-             align256(sizeof(float) * (size_t)B * Hv * (chunks(L) + 1) * ((Dv + OWN - 1) / OWN)) +
-             align256(sizeof(float) * (size_t)B * L * Hv);
+    if (backward) n += s.e + z_or_heads(s) + s.inner + s.dots;
     return n;
 }
 
@@ -569,17 +596,21 @@ extern "C" s5_status s5_delta_backward(const void *q, long long ldq, const void 
     w += s.images;
     a.x = reinterpret_cast<float *>(w);
     w += s.e;
-    const size_t heads = align256(sizeof(float) * (size_t)B * L * Hv * Dk);
     a.dqh = reinterpret_cast<float *>(w);
-    w += heads;
-    a.dkh = reinterpret_cast<float *>(w);
-    w += heads;
+    a.dkh = reinterpret_cast<float *>(w + s.heads);
+    a.z = reinterpret_cast<float *>(w);
+    w += z_or_heads(s);
     a.parts = (Dv + OWN - 1) / OWN;
     a.inner = reinterpret_cast<float *>(w);
-    w += align256(sizeof(float) * (size_t)B * Hv * (chunks(L) + 1) * a.parts);
+    w += s.inner;
     a.dots = reinterpret_cast<float *>(w);
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = dtype == S5_BF16 ? backward<__nv_bfloat16>(a, st) : backward<float>(a, st);
+    cudaError_t e;
+    if (tc_supported(a, dtype, true)) {
+        a.parts = tc_inner_parts(Dk, Dv);
+        e = backward_tc(a, st);
+    } else
+        e = dtype == S5_BF16 ? backward<__nv_bfloat16>(a, st) : backward<float>(a, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
 

@@ -35,8 +35,9 @@ struct Args {
     float *x;                         // [B][L][Hv][Dv]   dL/du_t
     float *dqh, *dkh;                 // [B][L][Hv][Dk]   per value head
     float *inner;                     // [B][Hv][N + 1][parts]   parts of <S_c, dL/dS_c>
-    float *dots;                      // [B][L][Hv]       o.do - v.dv
+    float *dots;                      // [B][L][Hv] o.do - v.dv; tensor cores: [3][B][L][Hv][Dv / 32] parts of X.e, v.dv, o.do
     int parts;
+    float *z;                         // [B][Hv][N][Dk][Dv]   dL/dS at the end of chunk c (tensor cores)
     void *images;                     // operand images of the tensor-core path
 };
 
@@ -49,9 +50,12 @@ __device__ __forceinline__ float clamp_g(float g) { return g < -128.0f ? -128.0f
 
 // Whether the tensor-core path takes these arguments.
 bool tc_supported(const Args &a, s5_dtype dtype, bool backward);
-size_t tc_image_bytes(int B, int L, int Hv);
+// Workspace of the tensor-core path; 0 for head sizes that it does not take.
+size_t tc_image_bytes(int B, int L, int Hv, int Dk, int Dv);
 cudaError_t tc_forward(const Args &a, cudaStream_t st);
-cudaError_t tc_backward_scan(const Args &a, cudaStream_t st);
+// All gradients but dg and dbeta, and their parts (inner, dots).
+cudaError_t tc_backward(const Args &a, cudaStream_t st);
+int tc_inner_parts(int Dk, int Dv);
 
 }  // namespace delta
 }  // namespace s5

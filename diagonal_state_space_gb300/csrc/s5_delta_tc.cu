@@ -36,7 +36,7 @@ namespace {
 
 constexpr int C = CHUNK;
 constexpr uint32_t M2_BYTES = 128 * 128;              // one split of a 128 x 64 matrix
-constexpr uint32_t META_BYTES = 1024;                 // up, down, beta [64], total decay
+constexpr uint32_t META_BYTES = 2048;                 // the chunk's factors (Meta)
 constexpr uint32_t IMG_BYTES = 3 * M2_BYTES + META_BYTES;
 constexpr unsigned long long WAIT_NS = 2000000000ull;
 
@@ -46,6 +46,7 @@ struct Meta {            // of one chunk and value head
     float up[C];         // e^{G_i}
     float down[C];       // e^{G_64 - G_i}
     float beta[C];
+    float hi[C], lo[C];  // G_i as a pair of floats
     float last;          // e^{G_64}
 };
 static_assert(sizeof(Meta) <= META_BYTES, "meta block");
@@ -201,6 +202,7 @@ template <int DK, bool TRANS> __global__ void __launch_bounds__(PT) delta_prep_k
                 meta->up[t] = expf((float)G[i]);
                 meta->down[t] = expf((float)(tot - G[i]));
                 meta->beta[t] = be;
+                meta->hi[t] = s.hi[t], meta->lo[t] = s.lo[t];
             }
             if (lane == 0) meta->last = expf((float)tot);
         }
@@ -411,6 +413,59 @@ __device__ __forceinline__ void hand_over(uint64_t *bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
+// The copy warp of both recurrences: each chunk's keys and queries (two
+// stages) and its matrix with the factors (one), in the order of the chunks
+// or, REV, from the last one.
+template <int DK, bool REV>
+__device__ __forceinline__ void copy_chunks(unsigned char *kq, unsigned char *img, const CUtensorMap *tmap_k,
+                                            const CUtensorMap *tmap_q, const Args &a, ScanBars *sb, int hk, int b,
+                                            long long bh, int N) {
+    constexpr uint32_t KQ = KQ_BOX * (DK / 64);
+    bool ok = true;
+    int it = 0;
+    for (; it < N; ++it) {
+        const int st = it & 1, c = REV ? N - 1 - it : it;
+        if (it >= 2) ok = __all_sync(0xffffffffu, scan_wait(&sb->kq_empty[st], ((it >> 1) - 1) & 1, sb));
+        if (!ok) break;
+        if (elect_one()) {
+            unsigned char *to = kq + st * KQ;
+            mbar_arrive_tx(&sb->kq_full[st], KQ);
+#pragma unroll
+            for (int x = 0; x < DK / 64; ++x) {
+                tma_load_4d(to + x * KQ_BOX, tmap_k, 64 * x, hk, c * C, b, &sb->kq_full[st]);
+                tma_load_4d(to + x * KQ_BOX + KQ_BOX / 2, tmap_q, 64 * x, hk, c * C, b, &sb->kq_full[st]);
+            }
+        }
+        __syncwarp();
+        if (it >= 1) ok = __all_sync(0xffffffffu, scan_wait(&sb->img_empty, (it - 1) & 1, sb));
+        if (!ok) {
+            ++it;
+            break;
+        }
+        if (elect_one()) {
+            mbar_arrive_tx(&sb->img_full, IMG_BYTES);
+            bulk_load(img, static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES, IMG_BYTES, &sb->img_full);
+        }
+        __syncwarp();
+    }
+    if (!ok) {   // a wait gave up: copies in flight land before the CTA ends
+        const unsigned long long t0 = global_ns();
+        for (int j = max(0, it - 2); j < it; ++j)
+            while (!mbar_try_wait_sleep(&sb->kq_full[j & 1], (j >> 1) & 1, 100000))
+                if (global_ns() - t0 > 200000000ull) break;
+        while (global_ns() - t0 < 1000000ull) {}
+    }
+}
+
+// Every MMA issued has completed before TMEM is freed (whole warp).
+__device__ __forceinline__ void drain_products(ScanBars *sb) {
+    if (elect_one()) mma_commit(&sb->drain);
+    __syncwarp();
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait_sleep(&sb->drain, 0, 100000))
+        if (global_ns() - t0 > 200000000ull) break;
+}
+
 template <int DK>
 __global__ void __launch_bounds__(SCAN_THREADS, 1)
 delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_q, const Args a) {
@@ -441,43 +496,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     const uint32_t tmem = sb->tmem, D1 = tmem, D2 = tmem + 64, D3 = tmem + 128;
 
     if (warp == 9) {
-        // ---------------------------------------------------------- copies
-        bool ok = true;
-        int c = 0;
-        for (; ok && c < N; ++c) {
-            const int st = c & 1;
-            if (c >= 2) ok = __shfl_sync(0xffffffffu, (int)scan_wait(&sb->kq_empty[st], ((c >> 1) - 1) & 1, sb), 0);
-            if (!ok) break;
-            if (elect_one()) {
-                unsigned char *to = smem + L::kq + st * L::KQ;
-                mbar_arrive_tx(&sb->kq_full[st], L::KQ);
-#pragma unroll
-                for (int x = 0; x < DK / 64; ++x) {
-                    tma_load_4d(to + x * KQ_BOX, &tmap_k, 64 * x, hk, c * C, b, &sb->kq_full[st]);
-                    tma_load_4d(to + x * KQ_BOX + KQ_BOX / 2, &tmap_q, 64 * x, hk, c * C, b, &sb->kq_full[st]);
-                }
-            }
-            __syncwarp();
-            if (c >= 1) ok = __shfl_sync(0xffffffffu, (int)scan_wait(&sb->img_empty, (c - 1) & 1, sb), 0);
-            if (!ok) {
-                ++c;
-                break;
-            }
-            if (elect_one()) {
-                mbar_arrive_tx(&sb->img_full, IMG_BYTES);
-                bulk_load(smem + L::img, static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES, IMG_BYTES,
-                          &sb->img_full);
-            }
-            __syncwarp();
-        }
-        // after a wait that gave up: copies in flight land before the CTA ends
-        if (!ok) {
-            const unsigned long long t0 = global_ns();
-            for (int j = max(0, c - 2); j < c; ++j)
-                while (!mbar_try_wait_sleep(&sb->kq_full[j & 1], (j >> 1) & 1, 100000))
-                    if (global_ns() - t0 > 200000000ull) break;
-            while (global_ns() - t0 < 1000000ull) {}
-        }
+        copy_chunks<DK, false>(smem + L::kq, smem + L::img, &tmap_k, &tmap_q, a, sb, hk, b, bh, N);
     } else if (warp == 8) {
         // ---------------------------------------------------------- products
         const uint32_t id1 = idesc_bf16_f32(128, NV) | B_MN, id3 = id1 | A_MN;
@@ -531,12 +550,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             }
             __syncwarp();
         }
-        // every MMA has completed before TMEM is freed
-        if (elect_one()) mma_commit(&sb->drain);
-        __syncwarp();
-        const unsigned long long t0 = global_ns();
-        while (!mbar_try_wait_sleep(&sb->drain, 0, 100000))
-            if (global_ns() - t0 > 200000000ull) break;
+        drain_products(sb);
     } else {
         // ---------------------------------------------------------- compute
         // warp w: TMEM lanes 32 (w % 4) on, columns 32 (w / 4) on.  Lanes 0..63
@@ -623,6 +637,504 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     if (warp == 8) tmem_dealloc(tmem, 256);
 }
 
+// ---------------------------------------------------------------------------
+// The adjoint over chunks, last chunk first, with Z = dL/dS at the chunk's end
+// and [T; P T] from the preparation (T = (I + strict lower(beta_i D_ij k_i.k_j))^-1):
+//   X = T^T (e^{G_64 - G} K Z) + (P T)^T dO          X_t = dL/du_t
+//   dv = beta X
+//   Z_start = e^{G_64} Z + K^T (-e^G dv) + Q^T (scale e^G dO)
+// the forward's three products transposed, on the same tiles: D1 = [K; Q] Z,
+// D2 = [T; P T]^T [e^{..} K Z; dO] (depth 128), D3 = [K; Q]^T [..; ..] (depth
+// 128).  Each token's parts of X . e, v . dv and o . dO (32 columns a thread)
+// and each chunk's <S, Z> go to the workspace for the gates' gradients.
+// ---------------------------------------------------------------------------
+template <int DK> struct AdjSmem {
+    static constexpr uint32_t KQ = KQ_BOX * (DK / 64);
+    static constexpr uint32_t S_IMG = DK * 128;
+    static constexpr uint32_t kq = 0;                      // two stages
+    static constexpr uint32_t img = kq + 2 * KQ;
+    static constexpr uint32_t s = img + IMG_BYTES;         // Z, three images
+    static constexpr uint32_t ru = s + 3 * S_IMG;          // e^{..} K Z, then -e^G dv: three images
+    static constexpr uint32_t yq = ru + 3 * RU_IMG;        // scale e^G dO: three images
+    static constexpr uint32_t go = yq + 3 * RU_IMG;        // dO
+    static constexpr uint32_t bars = go + RU_IMG;
+    static constexpr uint32_t total = bars + 256 + 1024;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(SCAN_THREADS, 1)
+delta_adjoint_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_q, const Args a) {
+    using L = AdjSmem<DK>;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    ScanBars *sb = reinterpret_cast<ScanBars *>(smem + L::bars);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int n0 = blockIdx.x * NV, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
+    const int N = chunks(a.L);
+    const long long bh = (long long)b * a.Hv + h;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) mbar_init(&sb->kq_full[i], 1), mbar_init(&sb->kq_empty[i], 1);
+        mbar_init(&sb->img_full, 1), mbar_init(&sb->img_empty, 8);
+        mbar_init(&sb->d1, 1), mbar_init(&sb->d2, 1), mbar_init(&sb->d3, 1);
+        mbar_init(&sb->s_ready, 8), mbar_init(&sb->r_ready, 8), mbar_init(&sb->u_ready, 4);
+        mbar_init(&sb->drain, 1);
+        sb->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&sb->tmem, 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sb->tmem, D1 = tmem, D2 = tmem + 64, D3 = tmem + 128;
+
+    if (warp == 9) {
+        copy_chunks<DK, true>(smem + L::kq, smem + L::img, &tmap_k, &tmap_q, a, sb, hk, b, bh, N);
+    } else if (warp == 8) {
+        const uint32_t id1 = idesc_bf16_f32(128, NV) | B_MN, id2 = id1 | A_MN;
+        const uint32_t img = smem_addr(smem + L::img), sS = smem_addr(smem + L::s), sR = smem_addr(smem + L::ru),
+                       sY = smem_addr(smem + L::yq), sG = smem_addr(smem + L::go);
+        bool ok = true;
+        for (int it = 0; ok && it < N; ++it) {
+            const int st = it & 1;
+            const uint32_t kq = smem_addr(smem + L::kq + st * L::KQ);
+            ok = scan_wait(&sb->kq_full[st], (it >> 1) & 1, sb) && scan_wait(&sb->s_ready, it & 1, sb);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int p = 2; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k)
+                        mma_bf16(D1, desc_k(kq + (k / 4) * KQ_BOX, k % 4), desc_mn(sS + p * L::S_IMG, k, 16), id1, !(p == 2 && k == 0));
+                mma_commit(&sb->d1);
+            }
+            __syncwarp();
+            ok = scan_wait(&sb->img_full, it & 1, sb) && scan_wait(&sb->r_ready, it & 1, sb);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            // the matrix transposed has 64 rows: lanes 64..127 of D2 come from
+            // what follows it in shared memory, and are not read
+            if (elect_one()) {
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                    for (int p = 0; p <= sum; ++p)
+#pragma unroll
+                        for (int k = 0; k < C / 16; ++k)
+                            mma_bf16(D2, desc_mn(img + p * M2_BYTES, k, M2_BYTES), desc_mn(sR + (sum - p) * RU_IMG, k, 16), id2,
+                                     !(sum == 2 && p == 0 && k == 0));
+#pragma unroll
+                for (int p = 2; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        mma_bf16(D2, desc_mn(img + p * M2_BYTES + M2_BYTES / 2, k, M2_BYTES), desc_mn(sG, k, 16), id2, 1);
+                mma_commit(&sb->d2);
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, scan_wait(&sb->u_ready, it & 1, sb));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int p = 2; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < 2 * C / 16; ++k)
+                        mma_bf16(D3, desc_mn(kq, k, KQ_BOX), desc_mn((k < 4 ? sR : sY) + p * RU_IMG, k % 4, 16), id2,
+                                 !(p == 2 && k == 0));
+                mma_commit(&sb->d3);
+                mma_commit(&sb->kq_empty[st]);
+            }
+            __syncwarp();
+        }
+        drain_products(sb);
+    } else {
+        const int q = warp & 3, c0 = warp / 4 * 32, row = 32 * q + lane;
+        const bool keys = q < 2;
+        const int tk = row & 63;
+        const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+        const uint32_t d1 = D1 + lane_base + c0, d2 = D2 + lane_base + c0, d3 = D3 + lane_base + c0;
+        const uint32_t sS = smem_addr(smem + L::s), sR = smem_addr(smem + L::ru), sY = smem_addr(smem + L::yq),
+                       sG = smem_addr(smem + L::go);
+        const Meta *meta = reinterpret_cast<const Meta *>(smem + L::img + 3 * M2_BYTES);
+        const bool state = row < DK;
+        const long long mat = (long long)DK * a.Dv;
+        const int parts = a.Dv / 32, part = (n0 + c0) / 32;
+        const long long nrows = (long long)a.B * a.L * a.Hv;
+        float *pb = a.dots, *pk = a.dots + nrows * parts, *pq = pk + nrows * parts;
+        float S[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 t = (a.ds_last && state)
+                                 ? *reinterpret_cast<const float4 *>(a.ds_last + bh * mat + (long long)row * a.Dv + n0 + c0 + 4 * j)
+                                 : make_float4(0, 0, 0, 0);
+            S[4 * j] = t.x, S[4 * j + 1] = t.y, S[4 * j + 2] = t.z, S[4 * j + 3] = t.w;
+        }
+        if (state) store_split32(sS, L::S_IMG, row, c0, S);
+        hand_over(&sb->s_ready, lane);
+        for (int it = 0; it < N; ++it) {
+            const int c = N - 1 - it, t = c * C + tk;
+            const bool on = t < a.L;
+            const long long tok = (long long)b * a.L + t, hv = tok * a.Hv + h;
+            const long long out = hv * a.Dv + n0 + c0;
+            uint4 v[4];
+            load_bf16_32(keys ? static_cast<const __nv_bfloat16 *>(a.v) + tok * a.ldv + (long long)h * a.Dv + n0 + c0
+                              : static_cast<const __nv_bfloat16 *>(a.dout) + tok * a.lddo + (long long)h * a.Dv + n0 + c0,
+                         on, v);
+            float x[32];
+            bool ok = scan_wait(&sb->img_full, it & 1, sb);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const float up = meta->up[tk], down = meta->down[tk], be = meta->beta[tk], last = meta->last;
+            if (!keys) {   // dO as it is for D2, scaled for D3
+                const uint32_t at = sG + (uint32_t)tk * 128u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sts128(at + (uint32_t)(((c0 / 8 + j) ^ (tk & 7)) << 4), v[j].x, v[j].y, v[j].z, v[j].w);
+                const float w = a.scale * up;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = w * bf_at(v, i);
+                store_split32(sY, RU_IMG, tk, c0, x);
+                hand_over(&sb->r_ready, lane);
+            }
+            // Z for the chunk's local gradients, <S, Z> at its end
+            if (state) {
+                store_f32_32(a.z + (bh * N + c) * mat + (long long)row * a.Dv + n0 + c0, S);
+                const float *s = a.states + (bh * (N + 1) + c + 1) * mat + (long long)row * a.Dv + n0 + c0;
+                float w = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 f = *reinterpret_cast<const float4 *>(s + 4 * j);
+                    w += f.x * S[4 * j] + f.y * S[4 * j + 1] + f.z * S[4 * j + 2] + f.w * S[4 * j + 3];
+                }
+                for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
+                if (lane == 0) a.inner[(bh * (N + 1) + c + 1) * a.parts + blockIdx.x * (DK / 16) + q * 2 + warp / 4] = w;
+            }
+            if (!keys && on) {
+                float w = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 f = *reinterpret_cast<const float4 *>(a.o32 + out + 4 * j);
+                    w += f.x * bf_at(v, 4 * j) + f.y * bf_at(v, 4 * j + 1) + f.z * bf_at(v, 4 * j + 2) + f.w * bf_at(v, 4 * j + 3);
+                }
+                pq[hv * parts + part] = w;
+            }
+            ok = scan_wait(&sb->d1, it & 1, sb);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            if (keys) {
+                load_acc(d1, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] *= down;
+                store_split32(sR, RU_IMG, tk, c0, x);
+                hand_over(&sb->r_ready, lane);
+            }
+            ok = scan_wait(&sb->d2, it & 1, sb);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            if (lane == 0) mbar_arrive(&sb->img_empty);
+            if (keys) {
+                load_acc(d2, x);
+                float y[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = -up * (be * x[i]);
+                store_split32(sR, RU_IMG, tk, c0, y);
+                hand_over(&sb->u_ready, lane);
+                if (on) {
+                    float w = 0.0f, r = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 f = *reinterpret_cast<const float4 *>(a.e + out + 4 * j);
+                        w += f.x * x[4 * j] + f.y * x[4 * j + 1] + f.z * x[4 * j + 2] + f.w * x[4 * j + 3];
+                    }
+                    store_f32_32(a.x + out, x);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        x[i] *= be;
+                        r = fmaf(x[i], bf_at(v, i), r);
+                    }
+                    store_bf16_32(static_cast<__nv_bfloat16 *>(a.dv) + tok * a.lddv + (long long)h * a.Dv + n0 + c0, x);
+                    pb[hv * parts + part] = w, pk[hv * parts + part] = r;
+                }
+            }
+            ok = scan_wait(&sb->d3, it & 1, sb);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            if (state) {
+                load_acc(d3, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) S[i] = fmaf(last, S[i], x[i]);
+                if (c > 0) store_split32(sS, L::S_IMG, row, c0, S);
+            }
+            if (c > 0) hand_over(&sb->s_ready, lane);
+        }
+        if (state && a.ds0) store_f32_32(a.ds0 + bh * mat + (long long)row * a.Dv + n0 + c0, S);
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 256);
+}
+
+// ---------------------------------------------------------------------------
+// dq and dk, all chunks at once: one CTA per chunk and key head, summing over
+// its value heads.  With S0 and Z the state at the chunk's start and the
+// adjoint at its end, U = beta e, and N_ij = scale D_ij dO_i.U_j (j <= i),
+// W_ij = -D_ij dv_i.U_j (j < i):
+//   dq = scale e^G dO S0^T + N K
+//   dk = e^{G_64 - G} U Z^T - e^G dv S0^T + W K + W^T K + N^T Q
+// as tcgen05 products of M = 128 with the rows of [dv; dO] stacked, so that
+// dk lies in TMEM lanes 0..63 and dq in 64..127:
+//   D1 = [dv; dO] S0^T,  D3 = [dv; dO] U^T,  D2 = [U; -] Z^T,
+//   D4 = [W; N] K,  D5 = [W; N]^T [K; Q].
+// dq and dk are rounded to bf16, so that 32-bit operands are carried as two
+// bf16 values here (2^-17), three products against another pair, two against
+// a bf16 operand.
+// Bound: the states and adjoints it reads (128 KB per chunk and head).
+// ---------------------------------------------------------------------------
+constexpr int LT = 512;
+
+template <int DK, int DV> struct LocalSmem {
+    static constexpr uint32_t KQ = KQ_BOX * (DK / 64);
+    static constexpr uint32_t A_IMG = 128 * 128 * (DV / 64);   // [dv; dO]
+    static constexpr uint32_t U_IMG = 64 * 128 * (DV / 64);
+    static constexpr uint32_t S_IMG = DK * 128 * (DV / 64);
+    static constexpr uint32_t kq = 0;
+    static constexpr uint32_t a = kq + KQ;                     // two images; [W; N], two images, later
+    static constexpr uint32_t u = a + (2 * A_IMG > 2 * M2_BYTES ? 2 * A_IMG : 2 * M2_BYTES);
+    static constexpr uint32_t s = u + 2 * U_IMG;               // S0, then Z: two images
+    static constexpr uint32_t meta = s + 2 * S_IMG;
+    static constexpr uint32_t bars = meta + META_BYTES;
+    static constexpr uint32_t total = bars + 64 + 1024;
+    // M = 128 over 64 rows of U reads 8 KB past the last box
+    static_assert(2 * S_IMG >= 8192, "rows past U are in shared memory");
+};
+
+struct LocalBars {
+    uint64_t first, second;
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ void split2(float a, float b, uint32_t &h, uint32_t &m) {
+    h = pack2(a, b);
+    m = pack2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+}
+// Eight fp32 values times w as a 16-byte piece of two images.
+__device__ __forceinline__ void put_split8(unsigned char *img, uint32_t stride, uint32_t box, int row, int d,
+                                           const float4 &x, const float4 &y, float w) {
+    uint32_t h[4], m[4];
+    split2(x.x * w, x.y * w, h[0], m[0]);
+    split2(x.z * w, x.w * w, h[1], m[1]);
+    split2(y.x * w, y.y * w, h[2], m[2]);
+    split2(y.z * w, y.w * w, h[3], m[3]);
+    unsigned char *to = img + d / 64 * box + row * 128 + (((d % 64 / 8) ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(to + stride) = make_uint4(m[0], m[1], m[2], m[3]);
+}
+__device__ __forceinline__ bool local_wait(uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 100000))
+        if (global_ns() - t0 > WAIT_NS) {
+            atomicExch(&g_delta_fault, 1);
+            return false;
+        }
+    return true;
+}
+
+template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_kernel(const Args a) {
+    using L = LocalSmem<DK, DV>;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    LocalBars *lb = reinterpret_cast<LocalBars *>(smem + L::bars);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, group = a.Hv / a.Hk;
+    const int t0 = c * C, nt = min(C, a.L - t0), N = chunks(a.L);
+    const long long row0 = (long long)b * a.L + t0, mat = (long long)DK * DV;
+    if (tid == 0) {
+        mbar_init(&lb->first, 1);
+        mbar_init(&lb->second, 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&lb->tmem, 512);
+        tmem_relinquish();
+    }
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < 128 * (DK / 8); i += LT) {
+        const int r = i / (DK / 8), d = i % (DK / 8) * 8, t = r & 63;
+        const __nv_bfloat16 *p = r < C ? static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + d
+                                       : static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + d;
+        *reinterpret_cast<uint4 *>(smem + L::kq + d / 64 * KQ_BOX + r * 128 + (((d % 64 / 8) ^ (r & 7)) << 4)) =
+            t < nt ? *reinterpret_cast<const uint4 *>(p) : none;
+    }
+    for (int i = tid; i < C * (DV / 8); i += LT) {   // dO is bf16: the rows of its second image are zero
+        const int r = C + i / (DV / 8), d = i % (DV / 8) * 8;
+        *reinterpret_cast<uint4 *>(smem + L::a + L::A_IMG + d / 64 * M2_BYTES + r * 128 + (((d % 64 / 8) ^ (r & 7)) << 4)) = none;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lb->tmem, D1 = tmem, D2 = tmem + 128, D4 = tmem + 256, D3 = tmem + 384, D5 = tmem + 384;
+    const uint32_t kq = smem_addr(smem + L::kq), sA = smem_addr(smem + L::a), sU = smem_addr(smem + L::u),
+                   sS = smem_addr(smem + L::s);
+    Meta *meta = reinterpret_cast<Meta *>(smem + L::meta);
+    // warp w: TMEM lanes 32 (w % 4) on, columns 32 (w / 4) on
+    const int row = 32 * (warp & 3) + lane, c0 = warp / 4 * 32, tk = row & 63;
+    const bool keys = row < C;
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    float acc[32] = {};
+    bool ok = true;
+    for (int j = 0; j < group; ++j) {
+        const int h = hk * group + j;
+        const long long bh = (long long)b * a.Hv + h;
+        const unsigned char *img = static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES;
+        for (int i = tid; i < (int)(sizeof(Meta) / 4); i += LT)
+            reinterpret_cast<float *>(meta)[i] = reinterpret_cast<const float *>(img + 3 * M2_BYTES)[i];
+        for (int i = tid; i < C * (DV / 8); i += LT) {
+            const int t = i / (DV / 8), d = i % (DV / 8) * 8;
+            const long long hv = (row0 + t) * a.Hv + h;
+            float4 x0 = make_float4(0, 0, 0, 0), x1 = x0, e0 = x0, e1 = x0;
+            uint4 g = none;
+            float be = 0.0f;
+            if (t < nt) {
+                x0 = *reinterpret_cast<const float4 *>(a.x + hv * DV + d), x1 = *reinterpret_cast<const float4 *>(a.x + hv * DV + d + 4);
+                e0 = *reinterpret_cast<const float4 *>(a.e + hv * DV + d), e1 = *reinterpret_cast<const float4 *>(a.e + hv * DV + d + 4);
+                g = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dout) + (row0 + t) * a.lddo +
+                                                     (long long)h * DV + d);
+                be = a.beta[hv];
+            }
+            put_split8(smem + L::a, L::A_IMG, M2_BYTES, t, d, x0, x1, be);
+            put_split8(smem + L::u, L::U_IMG, RU_IMG, t, d, e0, e1, be);
+            const int r = C + t;
+            *reinterpret_cast<uint4 *>(smem + L::a + d / 64 * M2_BYTES + r * 128 + (((d % 64 / 8) ^ (r & 7)) << 4)) = g;
+        }
+        const float *s0 = a.states + (bh * (N + 1) + c) * mat, *z = a.z + (bh * N + c) * mat;
+        for (int i = tid; i < DK * (DV / 8); i += LT) {
+            const int r = i / (DV / 8), d = i % (DV / 8) * 8;
+            put_split8(smem + L::s, L::S_IMG, DK * 128, r, d, *reinterpret_cast<const float4 *>(s0 + r * DV + d),
+                       *reinterpret_cast<const float4 *>(s0 + r * DV + d + 4), 1.0f);
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (warp == 0) {
+            const uint32_t id = idesc_bf16_f32(128, DK), idU = idesc_bf16_f32(128, 64);
+            if (elect_one()) {
+#pragma unroll
+                for (int sum = 1; sum >= 0; --sum)
+#pragma unroll
+                    for (int p = 0; p <= sum; ++p)
+#pragma unroll
+                        for (int k = 0; k < DV / 16; ++k) {
+                            const uint64_t da = desc_k(sA + p * L::A_IMG + (k / 4) * M2_BYTES, k % 4);
+                            const bool add = !(sum == 1 && p == 0 && k == 0);
+                            mma_bf16(D1, da, desc_k(sS + (sum - p) * L::S_IMG + (k / 4) * (DK * 128), k % 4), id, add);
+                            mma_bf16(D3, da, desc_k(sU + (sum - p) * L::U_IMG + (k / 4) * RU_IMG, k % 4), idU, add);
+                        }
+                mma_commit(&lb->first);
+            }
+            __syncwarp();
+        }
+        float4 zr[(DK * DV / 4 + LT - 1) / LT];
+#pragma unroll
+        for (int n = 0; n < DK * DV / 8 / LT; ++n) {
+            const int i = tid + n * LT;
+            zr[2 * n] = *reinterpret_cast<const float4 *>(z + i * 8);
+            zr[2 * n + 1] = *reinterpret_cast<const float4 *>(z + i * 8 + 4);
+        }
+        ok = local_wait(&lb->first, j & 1) && ok;
+        tc_fence_after();
+#pragma unroll
+        for (int n = 0; n < DK * DV / 8 / LT; ++n) {
+            const int i = tid + n * LT;
+            put_split8(smem + L::s, L::S_IMG, DK * 128, i / (DV / 8), i % (DV / 8) * 8, zr[2 * n], zr[2 * n + 1], 1.0f);
+        }
+        if (c0 < 64) {   // [W; N] into the first images' place
+            float x[32];
+            load_acc(D3 + lane_base + c0, x);
+            const float gh = meta->hi[tk], gl = meta->lo[tk];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int col = c0 + i;
+                const bool in = keys ? col < tk : col <= tk;
+                const float w = in ? expf((gh - meta->hi[col]) + (gl - meta->lo[col])) : 0.0f;
+                x[i] = in ? (keys ? -w : a.scale * w) * x[i] : 0.0f;
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                put_split8(smem + L::a, M2_BYTES, 0, row, c0 + 8 * n, make_float4(x[8 * n], x[8 * n + 1], x[8 * n + 2], x[8 * n + 3]),
+                           make_float4(x[8 * n + 4], x[8 * n + 5], x[8 * n + 6], x[8 * n + 7]), 1.0f);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 0) {
+            const uint32_t id = idesc_bf16_f32(128, DK), idB = id | B_MN, idAB = idB | A_MN;
+            if (elect_one()) {
+#pragma unroll
+                for (int sum = 1; sum >= 0; --sum)
+#pragma unroll
+                    for (int p = 0; p <= sum; ++p)
+#pragma unroll
+                        for (int k = 0; k < DV / 16; ++k)
+                            mma_bf16(D2, desc_k(sU + p * L::U_IMG + (k / 4) * RU_IMG, k % 4),
+                                     desc_k(sS + (sum - p) * L::S_IMG + (k / 4) * (DK * 128), k % 4), id,
+                                     !(sum == 1 && p == 0 && k == 0));
+#pragma unroll
+                for (int p = 1; p >= 0; --p) {
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        mma_bf16(D4, desc_k(sA + p * M2_BYTES, k), desc_mn(kq, k, KQ_BOX), idB, !(p == 1 && k == 0));
+#pragma unroll
+                    for (int k = 0; k < 2 * C / 16; ++k)
+                        mma_bf16(D5, desc_mn(sA + p * M2_BYTES, k, M2_BYTES), desc_mn(kq, k, KQ_BOX), idAB, !(p == 1 && k == 0));
+                }
+                mma_commit(&lb->second);
+            }
+            __syncwarp();
+        }
+        ok = local_wait(&lb->second, j & 1) && ok;
+        tc_fence_after();
+        if (c0 < DK) {
+            float x[32];
+            const float up = meta->up[tk], down = meta->down[tk], w = keys ? -up : a.scale * up;
+            load_acc(D1 + lane_base + c0, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] = fmaf(w, x[i], acc[i]);
+            load_acc(D4 + lane_base + c0, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] += x[i];
+            if (keys) {
+                load_acc(D2 + lane_base + c0, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[i] = fmaf(down, x[i], acc[i]);
+                load_acc(D5 + lane_base + c0, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[i] += x[i];
+            }
+        }
+        if (j + 1 < group && ok)   // the second images' zero rows were [W; N]'s place only where DV is 64
+            if (DV == 64)
+                for (int i = tid; i < C * (DV / 8); i += LT) {
+                    const int r = C + i / (DV / 8), d = i % (DV / 8) * 8;
+                    *reinterpret_cast<uint4 *>(smem + L::a + L::A_IMG + r * 128 + (((d / 8) ^ (r & 7)) << 4)) = none;
+                }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
+    if (c0 < DK && tk < nt) {
+        __nv_bfloat16 *p = keys ? static_cast<__nv_bfloat16 *>(a.dk) + (row0 + tk) * a.lddk + hk * DK + c0
+                                : static_cast<__nv_bfloat16 *>(a.dq) + (row0 + tk) * a.lddq + hk * DK + c0;
+        store_bf16_32(p, acc);
+    }
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
 // Rows [B][L][H][D] of bf16 as boxes of 64 tokens x 64 values of one head;
 // tokens past L read as zeros.
 cudaError_t encode_rows(CUtensorMap *m, const void *p, long long ld, int B, int Ltok, int H, int D) {
@@ -667,6 +1179,26 @@ template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <int DK, int DV> cudaError_t launch_local(const Args &a, cudaStream_t st) {
+    const cudaError_t e = big_smem(delta_local_kernel<DK, DV>, LocalSmem<DK, DV>::total);
+    if (e != cudaSuccess) return e;
+    delta_local_kernel<DK, DV><<<dim3(chunks(a.L), a.Hk, a.B), LT, LocalSmem<DK, DV>::total, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int DK> cudaError_t backward(const Args &a, cudaStream_t st) {
+    CUtensorMap mk, mq;
+    cudaError_t e = encode_rows(&mk, a.k, a.ldk, a.B, a.L, a.Hk, DK);
+    if (e == cudaSuccess) e = encode_rows(&mq, a.q, a.ldq, a.B, a.L, a.Hk, DK);
+    if (e == cudaSuccess) e = launch_prep<DK, true>(a, st);
+    if (e == cudaSuccess) e = big_smem(delta_adjoint_kernel<DK>, AdjSmem<DK>::total);
+    if (e != cudaSuccess) return e;
+    delta_adjoint_kernel<DK><<<dim3(a.Dv / NV, a.Hv, a.B), SCAN_THREADS, AdjSmem<DK>::total, st>>>(mk, mq, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return a.Dv == 128 ? launch_local<DK, 128>(a, st) : launch_local<DK, 64>(a, st);
+}
+
 }  // namespace
 
 // bf16 with heads of 64 or 128; pitches that the copies can address (multiples
@@ -675,14 +1207,23 @@ bool tc_supported(const Args &a, s5_dtype dtype, bool backward) {
     if (dtype != S5_BF16 || a.L < 1) return false;
     if ((a.Dk != 64 && a.Dk != 128) || (a.Dv != 64 && a.Dv != 128)) return false;
     if (a.ldq % 8 || a.ldk % 8 || a.ldv % 8) return false;
-    return backward ? false : a.ldo % 8 == 0;
+    return backward ? a.lddo % 8 == 0 && a.lddq % 8 == 0 && a.lddk % 8 == 0 && a.lddv % 8 == 0 : a.ldo % 8 == 0;
 }
 
-size_t tc_image_bytes(int B, int L, int Hv) { return (size_t)B * Hv * chunks(L) * IMG_BYTES; }
+size_t tc_image_bytes(int B, int L, int Hv, int Dk, int Dv) {
+    if ((Dk != 64 && Dk != 128) || (Dv != 64 && Dv != 128)) return 0;
+    return (size_t)B * Hv * chunks(L) * IMG_BYTES;
+}
 
 cudaError_t tc_forward(const Args &a, cudaStream_t st) {
     return a.Dk == 128 ? forward<128>(a, st) : forward<64>(a, st);
 }
+
+cudaError_t tc_backward(const Args &a, cudaStream_t st) {
+    return a.Dk == 128 ? backward<128>(a, st) : backward<64>(a, st);
+}
+
+int tc_inner_parts(int Dk, int Dv) { return Dv / NV * (Dk / 16); }
 
 int fault_take() {
     int v = 0, zero = 0;
