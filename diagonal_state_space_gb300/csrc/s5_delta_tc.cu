@@ -71,6 +71,11 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+                 : "memory");
+}
+
 // Writes 32 values of row `row` (columns c0 .. c0 + 31 of 64) as three images
 // `stride` bytes apart, 128 bytes a row in the 128-byte swizzle.
 __device__ __forceinline__ void store_split32(uint32_t img, uint32_t stride, int row, int c0, const float (&v)[32]) {
@@ -89,30 +94,37 @@ __device__ __forceinline__ void store_split32(uint32_t img, uint32_t stride, int
 
 // ---------------------------------------------------------------------------
 // Preparation: one CTA per chunk and key head; the products k.k and q.k are
-// shared by the key head's value heads.
+// taken once (mma.sync, exact bf16 operands) and stay in registers for the
+// key head's value heads.
 //
-// The inverse goes by blocks: the four 16 x 16 blocks on the diagonal by
-// substitution (one column per lane), then
+// Decay factors D_ij of two different blocks of 16 tokens are products
+// e^{G_i - G_b} e^{G_b - G_j} at the end b of j's block (both at most 1 where
+// g <= 0); inside a block each is an exponential of its own.
+//
+// The inverse goes by blocks, in place and in 32 bits: the four 16 x 16 blocks
+// on the diagonal by substitution (one column per lane), then
 //   [[A, 0], [B, D]]^-1 = [[A^-1, 0], [-D^-1 B A^-1, D^-1]]
-// to 32 and to 64 rows.  All of it in 32 bits on the CUDA cores: the inverse
-// is what the states' precision hangs on, and its 0.1 MFMA per chunk and head
-// are less than the conversions that a split product would take.
+// to 32 and to 64 rows.  P E is a product of two triangular 64 x 64 matrices
+// in three bf16 parts each (mma.sync, the 20 of 64 block products that are not
+// zero).  The whole image is built in shared memory in the layout that the
+// recurrences' products read, and leaves by one bulk copy.
 //
 // TRANS: (I + strict lower(beta_i D_ij k_i.k_j))^-1 = T and [T; P T] instead,
 // which the backward pass uses.
 // ---------------------------------------------------------------------------
-constexpr int PT = 128;             // threads
-constexpr int LD = 68;              // pitch of 64-wide fp32 tiles (16-byte rows, no conflicts on columns of 4)
+constexpr int PT = 256;             // threads
+constexpr int LD = 68;              // pitch of the fp32 tile: 16-byte rows, no conflicts on 8 rows of 4
 
-struct PrepSmem {
-    float kk[C][LD], qk[C][LD];     // products of the key head
-    float a[C][LD];                 // triangular system, then scratch of the blocks
-    float t[C][LD];                 // its inverse
-    float p[C][LD];                 // P (times beta)
-    float hi[C], lo[C], beta[C];    // cumulated log decay as a pair of floats
+template <int DK> struct PrepSmem {
+    static constexpr int KP = DK + 8;                    // bf16 pitch of the tiles: conflict-free fragments
+    static constexpr uint32_t tiles = 2 * C * KP * 2;    // keys and queries, before the image
+    static constexpr uint32_t a = IMG_BYTES;             // [64][LD] fp32, after the image (and the tiles)
+    static constexpr uint32_t near = a + C * LD * 4;     // e^{G_b - G_j}
+    static constexpr uint32_t total = near + C * 4;
+    static_assert(tiles <= IMG_BYTES, "the tiles lie in the image's place");
 };
 
-// mma.sync m16n8k16: D += A B^T, rows of A and B in shared memory.
+// mma.sync m16n8k16: D += A B.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
@@ -120,63 +132,80 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 
-template <int DK, bool TRANS> __global__ void __launch_bounds__(PT) delta_prep_kernel(const Args a) {
-    extern __shared__ __align__(16) unsigned char psm[];
-    PrepSmem &s = *reinterpret_cast<PrepSmem *>(psm);
-    constexpr int KP = DK + 8;      // bf16 pitch: 4 banks a row, conflict-free fragments
-    __nv_bfloat16 *sk = reinterpret_cast<__nv_bfloat16 *>(&s.t[0][0]);   // [64][KP] until the products are done
-    __nv_bfloat16 *sq = sk + C * KP;
-    static_assert(2 * C * KP * 2 <= 2 * sizeof(s.t), "tiles fit the inverse's and P's space");
+template <int DK, bool TRANS> __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const Args a) {
+    using L = PrepSmem<DK>;
+    extern __shared__ __align__(128) unsigned char psm[];
+    unsigned char *img = psm;
+    float(*A)[LD] = reinterpret_cast<float(*)[LD]>(psm + L::a);
+    float *near = reinterpret_cast<float *>(psm + L::near);
+    Meta *meta = reinterpret_cast<Meta *>(psm + 3 * M2_BYTES);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, group = a.Hv / a.Hk;
     const int t0 = c * C, nt = min(C, a.L - t0), N = chunks(a.L);
     const long long row0 = (long long)b * a.L + t0;
-    for (int i = tid; i < C * (DK / 8); i += PT) {
-        const int t = i / (DK / 8), d = i % (DK / 8) * 8;
-        uint4 xk = make_uint4(0, 0, 0, 0), xq = xk;
-        if (t < nt) {
-            xk = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + d);
-            xq = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + d);
+    const int rb = warp & 3, g = lane / 4, q2 = lane % 4 * 2;   // block of 16 rows; fragment row and column
+    const bool isq = warp >= 4;                                 // warps 0..3: k.k, 4..7: q.k
+    float acc[8][4] = {};
+    {
+        constexpr int KP = L::KP;
+        __nv_bfloat16 *sk = reinterpret_cast<__nv_bfloat16 *>(psm), *sq = sk + C * KP;
+        for (int i = tid; i < C * (DK / 8); i += PT) {
+            const int t = i / (DK / 8), d = i % (DK / 8) * 8;
+            uint4 xk = make_uint4(0, 0, 0, 0), xq = xk;
+            if (t < nt) {
+                xk = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + d);
+                xq = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + d);
+            }
+            *reinterpret_cast<uint4 *>(sk + t * KP + d) = xk;
+            *reinterpret_cast<uint4 *>(sq + t * KP + d) = xq;
         }
-        *reinterpret_cast<uint4 *>(sk + t * KP + d) = xk;
-        *reinterpret_cast<uint4 *>(sq + t * KP + d) = xq;
-    }
-    __syncthreads();
-    {   // warp w: rows 16 w .. 16 w + 15 of both products, columns up to its own
-        float kk[8][4] = {}, qk[8][4] = {};
-        const int g = lane / 4, q2 = lane % 4 * 2;
+        __syncthreads();
+        const __nv_bfloat16 *rows = isq ? sq : sk;
 #pragma unroll 2
         for (int k0 = 0; k0 < DK; k0 += 16) {
-            uint32_t fk[4], fq[4];
+            uint32_t f[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = (16 * warp + g + (i & 1) * 8) * KP + k0 + q2 + (i >> 1) * 8;
-                fk[i] = *reinterpret_cast<const uint32_t *>(sk + at);
-                fq[i] = *reinterpret_cast<const uint32_t *>(sq + at);
-            }
+            for (int i = 0; i < 4; ++i)
+                f[i] = *reinterpret_cast<const uint32_t *>(rows + (16 * rb + g + (i & 1) * 8) * KP + k0 + q2 + (i >> 1) * 8);
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-                if (n > 2 * warp + 1) continue;
+                if (n > 2 * rb + 1) continue;
                 const int at = (8 * n + g) * KP + k0 + q2;
-                const uint32_t b0 = *reinterpret_cast<const uint32_t *>(sk + at);
-                const uint32_t b1 = *reinterpret_cast<const uint32_t *>(sk + at + 8);
-                mma16816(kk[n], fk, b0, b1);
-                mma16816(qk[n], fq, b0, b1);
+                mma16816(acc[n], f, *reinterpret_cast<const uint32_t *>(sk + at), *reinterpret_cast<const uint32_t *>(sk + at + 8));
             }
         }
+        if (isq)
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+            for (int n = 0; n < 8; ++n)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 16 * warp + g + 8 * i, col = 8 * n + q2;
-                *reinterpret_cast<float2 *>(&s.kk[r][col]) = make_float2(kk[n][2 * i], kk[n][2 * i + 1]);
-                *reinterpret_cast<float2 *>(&s.qk[r][col]) = make_float2(qk[n][2 * i], qk[n][2 * i + 1]);
-            }
+                for (int i = 0; i < 4; ++i) acc[n][i] *= a.scale;
     }
+    // rows 64..127 of the image: three parts of two neighbouring values
+    auto put2 = [&](int r, int n, float x, float y) {
+        uint32_t h, m, l;
+        split3(x, y, h, m, l);
+        unsigned char *to = img + (C + r) * 128 + ((n ^ (r & 7)) << 4) + q2 * 2;
+        *reinterpret_cast<uint32_t *>(to) = h;
+        *reinterpret_cast<uint32_t *>(to + M2_BYTES) = m;
+        *reinterpret_cast<uint32_t *>(to + 2 * M2_BYTES) = l;
+    };
+    const uint32_t simg = smem_addr(img);
     for (int j = 0; j < group; ++j) {
         const int h = hk * group + j;
-        unsigned char *img = static_cast<unsigned char *>(a.images) + (((long long)b * a.Hv + h) * N + c) * IMG_BYTES;
+        if (j > 0 && tid == 0) bulk_wait_read_all();   // the last image has left
         __syncthreads();
         if (warp == 0) {
             // G in float64 (64 terms of up to 128), kept as two floats, so that
@@ -189,127 +218,169 @@ template <int DK, bool TRANS> __global__ void __launch_bounds__(PT) delta_prep_k
                 const double up = __shfl_up_sync(0xffffffffu, w, m);
                 if (lane >= m) w += up;
             }
-            const double tot = __shfl_sync(0xffffffffu, w, 31);
-            Meta *meta = reinterpret_cast<Meta *>(img + 3 * M2_BYTES);
+            const double tot = __shfl_sync(0xffffffffu, w, 31), edge = __shfl_sync(0xffffffffu, w, lane | 7);
             const double G[2] = {w - x1, w};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
-                const float be = t < nt ? a.beta[(row0 + t) * a.Hv + h] : 0.0f;
-                s.hi[t] = (float)G[i];
-                s.lo[t] = (float)(G[i] - (double)s.hi[t]);
-                s.beta[t] = be;
-                meta->up[t] = expf((float)G[i]);
+                const float hi = (float)G[i];
+                meta->hi[t] = hi;
+                meta->lo[t] = (float)(G[i] - (double)hi);
+                meta->beta[t] = t < nt ? a.beta[(row0 + t) * a.Hv + h] : 0.0f;
+                meta->up[t] = expf(hi);
                 meta->down[t] = expf((float)(tot - G[i]));
-                meta->beta[t] = be;
-                meta->hi[t] = s.hi[t], meta->lo[t] = s.lo[t];
+                near[t] = expf((float)(edge - G[i]));
             }
             if (lane == 0) meta->last = expf((float)tot);
         }
         __syncthreads();
-        for (int i = tid; i < C * C; i += PT) {
-            const int r = i / C, col = i % C;
-            const float d = col <= r ? expf((s.hi[r] - s.hi[col]) + (s.lo[r] - s.lo[col])) : 0.0f;
-            s.a[r][col] = col < r ? d * s.kk[r][col] * (TRANS ? s.beta[r] : s.beta[col]) : 0.0f;
-            s.p[r][col] = col <= r ? a.scale * d * s.qk[r][col] * (TRANS ? 1.0f : s.beta[col]) : 0.0f;
-            s.t[r][col] = 0.0f;
-        }
-        __syncthreads();
-        if (lane < 16) {   // warp w: block w of the diagonal, lane: column of its inverse
-            const int o = 16 * warp;
-            float x[16];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float v = r == lane ? 1.0f : 0.0f;
+        for (int i = 0; i < 2; ++i) {      // rows g and g + 8 of the warp's block
+            const int r = 16 * rb + g + 8 * i;
+            const float gh = meta->hi[r], gl = meta->lo[r], br = meta->beta[r];
 #pragma unroll
-                for (int m = 0; m < r; ++m) v = fmaf(-s.a[o + r][o + m], x[m], v);
-                x[r] = v;
-                s.t[o + r][o + lane] = v;
-            }
-        }
-        __syncthreads();
-        // 32-row blocks: -D^-1 (B A^-1), both pairs at once, four values per thread
-        {
-            const int o = 32 * (tid / 64), r = tid % 64 / 4, c4 = tid % 4 * 4;
-            float v[4] = {0, 0, 0, 0};
+            for (int nb = 0; nb < 4; ++nb) {
+                float w[4] = {0, 0, 0, 0};
+                if (nb <= rb) {
+                    const float far = nb < rb ? expf((gh - meta->hi[16 * nb + 15]) + (gl - meta->lo[16 * nb + 15])) : 0.0f;
 #pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const float x = s.a[o + 16 + r][o + m];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = fmaf(x, s.t[o + m][o + c4 + i], v[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s.a[o + r][o + 16 + c4 + i] = v[i];   // the system's unused upper part
-            __syncthreads();
-            float w[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const float x = s.t[o + 16 + r][o + 16 + m];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = fmaf(-x, s.a[o + m][o + 16 + c4 + i], w[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s.t[o + 16 + r][o + c4 + i] = w[i];
-        }
-        __syncthreads();
-        // 64 rows: eight values per thread
-        {
-            const int r = tid / 4, c8 = tid % 4 * 8;
-            float v[8] = {};
-#pragma unroll 8
-            for (int m = 0; m < 32; ++m) {
-                const float x = s.a[32 + r][m];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = fmaf(x, s.t[m][c8 + i], v[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s.a[r][32 + c8 + i] = v[i];
-            __syncthreads();
-            float w[8] = {};
-#pragma unroll 8
-            for (int m = 0; m < 32; ++m) {
-                const float x = s.t[32 + r][32 + m];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = fmaf(-x, s.a[m][32 + c8 + i], w[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s.t[32 + r][c8 + i] = w[i];
-        }
-        __syncthreads();
-        // P E: rows r, r + 16, r + 32, r + 48 and eight columns per thread, into
-        // a; both factors are triangular, so that columns m < c8 add nothing
-        {
-            const int r = tid / 8, c8 = tid % 8 * 8;
-            float v[4][8] = {};
-            for (int m = c8; m < C; ++m) {
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = s.t[m][c8 + i];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = s.p[r + 16 * k][m];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[k][i] = fmaf(x, y[i], v[k][i]);
+                    for (int x = 0; x < 4; ++x) {
+                        const int n = 2 * nb + x / 2, col = 8 * n + q2 + x % 2;
+                        const float p = acc[n][2 * i + x % 2];
+                        const float d = nb < rb ? far * near[col] : expf((gh - meta->hi[col]) + (gl - meta->lo[col]));
+                        const bool in = isq ? col <= r : col < r;
+                        const float by = isq ? (TRANS ? 1.0f : meta->beta[col]) : (TRANS ? br : meta->beta[col]);
+                        w[x] = in ? p * (d * by) : 0.0f;
+                    }
+                }
+                if (isq) {
+                    put2(r, 2 * nb, w[0], w[1]);
+                    put2(r, 2 * nb + 1, w[2], w[3]);
+                } else {
+                    *reinterpret_cast<float2 *>(&A[r][16 * nb + q2]) = make_float2(w[0], w[1]);
+                    *reinterpret_cast<float2 *>(&A[r][16 * nb + 8 + q2]) = make_float2(w[2], w[3]);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s.a[r + 16 * k][c8 + i] = v[k][i];
         }
         __syncthreads();
-        for (int i = tid; i < 128 * 8; i += PT) {
-            const int r = i / 8, ch = i % 8;
-            const float *x = r < C ? &s.t[r][8 * ch] : &s.a[r - C][8 * ch];
-            uint32_t hh[4], mm[4], ll[4];
+        if (warp < 2) {   // two blocks of the diagonal per warp; lane: a column of the inverse
+            const int o = 32 * warp + (lane & 16), col = lane & 15;
+            float x[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) split3(x[2 * k], x[2 * k + 1], hh[k], mm[k], ll[k]);
+            for (int r = 0; r < 16; ++r) x[r] = r == col ? 1.0f : 0.0f;
+#pragma unroll
+            for (int r = 1; r < 16; ++r)
+#pragma unroll
+                for (int m = 0; m < r; m += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&A[o + r][o + m]);
+                    x[r] = fmaf(-f.x, x[m], x[r]);
+                    if (m + 1 < r) x[r] = fmaf(-f.y, x[m + 1], x[r]);
+                    if (m + 2 < r) x[r] = fmaf(-f.z, x[m + 2], x[r]);
+                    if (m + 3 < r) x[r] = fmaf(-f.w, x[m + 3], x[r]);
+                }
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < 16; ++r) A[o + r][o + col] = x[r];
+        }
+        __syncthreads();
+        {   // 32-row blocks, both pairs at once: B A^-1 into the unused upper part, then -D^-1 of it
+            const int o = 32 * (tid / 128), r = tid % 128 / 8, c2 = tid % 8 * 2;
+            float v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+            for (int m = 0; m < 16; ++m) {
+                const float x = A[o + 16 + r][o + m];
+                const float2 y = *reinterpret_cast<const float2 *>(&A[o + m][o + c2]);
+                v0 = fmaf(x, y.x, v0), v1 = fmaf(x, y.y, v1);
+            }
+            *reinterpret_cast<float2 *>(&A[o + r][o + 16 + c2]) = make_float2(v0, v1);
+            __syncthreads();
+            v0 = v1 = 0.0f;
+#pragma unroll
+            for (int m = 0; m < 16; ++m) {
+                const float x = A[o + 16 + r][o + 16 + m];
+                const float2 y = *reinterpret_cast<const float2 *>(&A[o + m][o + 16 + c2]);
+                v0 = fmaf(-x, y.x, v0), v1 = fmaf(-x, y.y, v1);
+            }
+            *reinterpret_cast<float2 *>(&A[o + 16 + r][o + c2]) = make_float2(v0, v1);
+            __syncthreads();
+            *reinterpret_cast<float2 *>(&A[o + r][o + 16 + c2]) = make_float2(0.0f, 0.0f);
+        }
+        __syncthreads();
+        {   // 64 rows
+            const int r = tid / 8, c4 = tid % 8 * 4;
+            float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+            for (int m = 0; m < 32; ++m) {
+                const float x = A[32 + r][m];
+                const float4 y = *reinterpret_cast<const float4 *>(&A[m][c4]);
+                v.x = fmaf(x, y.x, v.x), v.y = fmaf(x, y.y, v.y), v.z = fmaf(x, y.z, v.z), v.w = fmaf(x, y.w, v.w);
+            }
+            *reinterpret_cast<float4 *>(&A[r][32 + c4]) = v;
+            __syncthreads();
+            v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+            for (int m = 0; m < 32; ++m) {
+                const float x = A[32 + r][32 + m];
+                const float4 y = *reinterpret_cast<const float4 *>(&A[m][32 + c4]);
+                v.x = fmaf(-x, y.x, v.x), v.y = fmaf(-x, y.y, v.y), v.z = fmaf(-x, y.z, v.z), v.w = fmaf(-x, y.w, v.w);
+            }
+            *reinterpret_cast<float4 *>(&A[32 + r][c4]) = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < C * 8 / PT; ++k) {   // E's three parts
+            const int i = tid + k * PT, r = i / 8, ch = i % 8;
+            float4 x = make_float4(0, 0, 0, 0), y = x;
+            if (!(r < 32 && ch >= 4)) {          // that quarter holds the intermediate product
+                x = *reinterpret_cast<const float4 *>(&A[r][8 * ch]);
+                y = *reinterpret_cast<const float4 *>(&A[r][8 * ch + 4]);
+            }
+            uint32_t hh[4], mm[4], ll[4];
+            split3(x.x, x.y, hh[0], mm[0], ll[0]);
+            split3(x.z, x.w, hh[1], mm[1], ll[1]);
+            split3(y.x, y.y, hh[2], mm[2], ll[2]);
+            split3(y.z, y.w, hh[3], mm[3], ll[3]);
             unsigned char *to = img + r * 128 + ((ch ^ (r & 7)) << 4);
             *reinterpret_cast<uint4 *>(to) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
             *reinterpret_cast<uint4 *>(to + M2_BYTES) = make_uint4(mm[0], mm[1], mm[2], mm[3]);
             *reinterpret_cast<uint4 *>(to + 2 * M2_BYTES) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
         }
+        __syncthreads();
+        // P E: warp w takes the rows of block w % 4 and the columns 32 (w / 4) on
+        float pe[4][4] = {};
+#pragma unroll
+        for (int jb = 0; jb < 2; ++jb) {
+            const int cb = 2 * (warp >> 2) + jb;       // block of 16 columns
+            for (int kb = cb; kb <= rb; ++kb) {
+                uint32_t fa[3][4], fb[3][4];
+                const int r = C + 16 * rb + (lane & 15), m = 16 * kb + (lane & 15);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    ldmatrix4(simg + p * M2_BYTES + r * 128 + (((2 * kb + (lane >> 4)) ^ (r & 7)) << 4), fa[p]);
+                    ldmatrix4t(simg + p * M2_BYTES + m * 128 + (((2 * cb + (lane >> 4)) ^ (m & 7)) << 4), fb[p]);
+                }
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                    for (int p = 0; p <= sum; ++p) {
+                        mma16816(pe[2 * jb], fa[p], fb[sum - p][0], fb[sum - p][1]);
+                        mma16816(pe[2 * jb + 1], fa[p], fb[sum - p][2], fb[sum - p][3]);
+                    }
+            }
+        }
+        __syncthreads();   // P has been read
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) put2(16 * rb + g + 8 * i, 4 * (warp >> 2) + n, pe[n][2 * i], pe[n][2 * i + 1]);
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            bulk_store(static_cast<unsigned char *>(a.images) + (((long long)b * a.Hv + h) * N + c) * IMG_BYTES, img, IMG_BYTES);
+            bulk_commit();
+        }
     }
+    if (tid == 0) bulk_wait_all();
 }
 
 // ---------------------------------------------------------------------------
@@ -332,7 +403,7 @@ template <int DK> struct ScanSmem {
 };
 
 struct ScanBars {
-    uint64_t kq_full[2], kq_empty[2], img_full, img_empty, d1, d2, d3, s_ready, r_ready, u_ready, drain;
+    uint64_t kq_full[2], kq_empty[2], img_full, img_empty, d1, d2, d3, s_ready, r_ready, u_ready, g_ready, drain;
     uint32_t tmem;
     int abort;
 };
@@ -346,12 +417,15 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo, uint32_
     d |= (uint64_t)2u << 61;
     return d;
 }
-// K-major: 128-byte rows of 64 K values; step k of 16.  MN-major: 128-byte
-// rows of 64 M or N values, one row per K value; the next 64 are `far` on.
-__device__ __forceinline__ uint64_t desc_k(uint32_t base, int k) { return desc128(base + 32u * k, 16u, 1024u); }
-__device__ __forceinline__ uint64_t desc_mn(uint32_t base, int k, uint32_t far) {
-    return desc128(base + 2048u * k, far, 1024u);
-}
+// K-major: 128-byte rows of 64 K values; a step of 16 is 32 bytes on.
+// MN-major: 128-byte rows of 64 M or N values, one row per K value; a step of
+// 16 is 2048 bytes on, the next 64 values of M or N are `far` on.
+__device__ __forceinline__ uint64_t desc_k(uint32_t base) { return desc128(base, 16u, 1024u); }
+__device__ __forceinline__ uint64_t desc_mn(uint32_t base, uint32_t far) { return desc128(base, far, 1024u); }
+// The same operand `bytes` on (the address field cannot carry: shared memory
+// ends below its 256 KB).
+__device__ __forceinline__ uint64_t on(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+constexpr uint32_t K_STEP = 32, MN_STEP = 2048;
 constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;
 
 __device__ __forceinline__ bool scan_wait(uint64_t *bar, uint32_t parity, ScanBars *sb) {
@@ -403,6 +477,21 @@ __device__ __forceinline__ void load_acc(uint32_t addr, float (&v)[32]) {
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// The sum of P column blocks, 64 apart: an accumulator for each part of the
+// split operand, so that one product covers all parts.
+template <int P> __device__ __forceinline__ void load_parts(uint32_t addr, float (&v)[32]) {
+    uint32_t r[P][32];
+#pragma unroll
+    for (int p = 0; p < P; ++p) tmem_ld32(addr + p * NV, r[p]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        float t = __uint_as_float(r[P - 1][i]);
+#pragma unroll
+        for (int p = P - 2; p >= 0; --p) t += __uint_as_float(r[p][i]);
+        v[i] = t;
+    }
 }
 // What the compute warps wrote to shared memory and read from TMEM is done
 // before the MMA warp goes on.
@@ -487,34 +576,35 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         fence_mbar_init();
     }
     if (warp == 8) {
-        tmem_alloc(&sb->tmem, 256);
+        tmem_alloc(&sb->tmem, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sb->tmem, D1 = tmem, D2 = tmem + 64, D3 = tmem + 128;
+    const uint32_t tmem = sb->tmem, D1 = tmem, D2 = tmem + 3 * NV, D3 = tmem + 5 * NV;
 
     if (warp == 9) {
         copy_chunks<DK, false>(smem + L::kq, smem + L::img, &tmap_k, &tmap_q, a, sb, hk, b, bh, N);
     } else if (warp == 8) {
         // ---------------------------------------------------------- products
-        const uint32_t id1 = idesc_bf16_f32(128, NV) | B_MN, id3 = id1 | A_MN;
-        const uint32_t img = smem_addr(smem + L::img), sS = smem_addr(smem + L::s), sR = smem_addr(smem + L::ru);
+        const uint32_t w1 = idesc_bf16_f32(128, NV) | B_MN, w2 = idesc_bf16_f32(128, 2 * NV) | B_MN,
+                       w3 = idesc_bf16_f32(128, 3 * NV) | B_MN;
+        const uint64_t mat = desc_k(smem_addr(smem + L::img)), S = desc_mn(smem_addr(smem + L::s), L::S_IMG),
+                       R = desc_mn(smem_addr(smem + L::ru), RU_IMG);
         bool ok = true;
         for (int c = 0; ok && c < N; ++c) {
             const int st = c & 1;
             const uint32_t kq = smem_addr(smem + L::kq + st * L::KQ);
+            const uint64_t rows = desc_k(kq), cols = desc_mn(kq, KQ_BOX);
             ok = scan_wait(&sb->kq_full[st], (c >> 1) & 1, sb) && scan_wait(&sb->s_ready, c & 1, sb);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int p = 2; p >= 0; --p)
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        mma_bf16(D1, desc_k(kq + (k / 4) * KQ_BOX, k % 4), desc_mn(sS + p * L::S_IMG, k, 16), id1, !(p == 2 && k == 0));
+                for (int k = 0; k < DK / 16; ++k)
+                    mma_bf16(D1, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), on(S, k * MN_STEP), w3, k > 0);
                 mma_commit(&sb->d1);
             }
             __syncwarp();
@@ -524,13 +614,12 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int sum = 2; sum >= 0; --sum)     // the small products first
-#pragma unroll
-                    for (int p = 0; p <= sum; ++p)
-#pragma unroll
-                        for (int k = 0; k < C / 16; ++k)
-                            mma_bf16(D2, desc_k(img + p * M2_BYTES, k), desc_mn(sR + (sum - p) * RU_IMG, k, 16), id1,
-                                     !(sum == 2 && p == 0 && k == 0));
+                for (int k = 0; k < C / 16; ++k) {
+                    mma_bf16(D2, on(mat, M2_BYTES + k * K_STEP), on(R, k * MN_STEP), w2, k > 0);
+                    mma_bf16(D2, on(mat, 2 * M2_BYTES + k * K_STEP), on(R, k * MN_STEP), w1, 1);
+                    mma_bf16(D2, on(mat, k * K_STEP), on(R, 2 * RU_IMG + k * MN_STEP), w1, 1);
+                    mma_bf16(D2, on(mat, k * K_STEP), on(R, k * MN_STEP), w2, 1);
+                }
                 mma_commit(&sb->d2);
             }
             __syncwarp();
@@ -541,10 +630,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             // whatever follows the keys in shared memory, and are not read
             if (elect_one()) {
 #pragma unroll
-                for (int p = 2; p >= 0; --p)
-#pragma unroll
-                    for (int k = 0; k < C / 16; ++k)
-                        mma_bf16(D3, desc_mn(kq, k, KQ_BOX), desc_mn(sR + p * RU_IMG, k, 16), id3, !(p == 2 && k == 0));
+                for (int k = 0; k < C / 16; ++k) mma_bf16(D3, on(cols, k * MN_STEP), on(R, k * MN_STEP), w3 | A_MN, k > 0);
                 mma_commit(&sb->d3);
                 mma_commit(&sb->kq_empty[st]);
             }
@@ -589,7 +675,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             ok = scan_wait(&sb->img_full, c & 1, sb) && scan_wait(&sb->d1, c & 1, sb);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            load_acc(d1, x);
+            load_parts<3>(d1, x);
             const float up = meta->up[tk], down = meta->down[tk], be = meta->beta[tk], last = meta->last;
             if (keys) {
 #pragma unroll
@@ -601,7 +687,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             if (lane == 0) mbar_arrive(&sb->img_empty);   // D2 is done with the matrix, this warp with its factors
-            load_acc(d2, y);
+            load_parts<2>(d2, y);
             if (keys) {
                 if (a.e && on) store_f32_32(a.e + out, y);
 #pragma unroll
@@ -619,7 +705,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             if (state) {
-                load_acc(d3, x);
+                load_parts<3>(d3, x);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) S[i] = fmaf(last, S[i], x[i]);
                 if (c + 1 < N) store_split32(sS, L::S_IMG, row, c0, S);
@@ -634,7 +720,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 256);
+    if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -676,44 +762,47 @@ delta_adjoint_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         for (int i = 0; i < 2; ++i) mbar_init(&sb->kq_full[i], 1), mbar_init(&sb->kq_empty[i], 1);
         mbar_init(&sb->img_full, 1), mbar_init(&sb->img_empty, 8);
         mbar_init(&sb->d1, 1), mbar_init(&sb->d2, 1), mbar_init(&sb->d3, 1);
-        mbar_init(&sb->s_ready, 8), mbar_init(&sb->r_ready, 8), mbar_init(&sb->u_ready, 4);
+        mbar_init(&sb->s_ready, 8), mbar_init(&sb->r_ready, 4), mbar_init(&sb->u_ready, 4), mbar_init(&sb->g_ready, 4);
         mbar_init(&sb->drain, 1);
         sb->abort = 0;
         fence_mbar_init();
     }
     if (warp == 8) {
-        tmem_alloc(&sb->tmem, 256);
+        tmem_alloc(&sb->tmem, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sb->tmem, D1 = tmem, D2 = tmem + 64, D3 = tmem + 128;
+    // D3 takes D1's place: the warps that read D1 hand over after it
+    const uint32_t tmem = sb->tmem, D1 = tmem, D2 = tmem + 3 * NV, D3 = tmem;
 
     if (warp == 9) {
         copy_chunks<DK, true>(smem + L::kq, smem + L::img, &tmap_k, &tmap_q, a, sb, hk, b, bh, N);
     } else if (warp == 8) {
-        const uint32_t id1 = idesc_bf16_f32(128, NV) | B_MN, id2 = id1 | A_MN;
-        const uint32_t img = smem_addr(smem + L::img), sS = smem_addr(smem + L::s), sR = smem_addr(smem + L::ru),
-                       sY = smem_addr(smem + L::yq), sG = smem_addr(smem + L::go);
+        const uint32_t w1 = idesc_bf16_f32(128, NV) | B_MN, w2 = idesc_bf16_f32(128, 2 * NV) | B_MN,
+                       w3 = idesc_bf16_f32(128, 3 * NV) | B_MN;
+        const uint64_t mat = desc_mn(smem_addr(smem + L::img), M2_BYTES), S = desc_mn(smem_addr(smem + L::s), L::S_IMG),
+                       R = desc_mn(smem_addr(smem + L::ru), RU_IMG), Y = desc_mn(smem_addr(smem + L::yq), RU_IMG),
+                       G = desc_mn(smem_addr(smem + L::go), RU_IMG);
         bool ok = true;
         for (int it = 0; ok && it < N; ++it) {
             const int st = it & 1;
             const uint32_t kq = smem_addr(smem + L::kq + st * L::KQ);
+            const uint64_t rows = desc_k(kq), cols = desc_mn(kq, KQ_BOX);
             ok = scan_wait(&sb->kq_full[st], (it >> 1) & 1, sb) && scan_wait(&sb->s_ready, it & 1, sb);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int p = 2; p >= 0; --p)
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        mma_bf16(D1, desc_k(kq + (k / 4) * KQ_BOX, k % 4), desc_mn(sS + p * L::S_IMG, k, 16), id1, !(p == 2 && k == 0));
+                for (int k = 0; k < DK / 16; ++k)
+                    mma_bf16(D1, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), on(S, k * MN_STEP), w3, k > 0);
                 mma_commit(&sb->d1);
             }
             __syncwarp();
-            ok = scan_wait(&sb->img_full, it & 1, sb) && scan_wait(&sb->r_ready, it & 1, sb);
+            // (P T)^T dO waits for nothing but its operands
+            ok = scan_wait(&sb->img_full, it & 1, sb) && scan_wait(&sb->g_ready, it & 1, sb);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -721,18 +810,24 @@ delta_adjoint_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             // what follows it in shared memory, and are not read
             if (elect_one()) {
 #pragma unroll
-                for (int sum = 2; sum >= 0; --sum)
+                for (int k = 0; k < C / 16; ++k)
 #pragma unroll
-                    for (int p = 0; p <= sum; ++p)
+                    for (int p = 2; p >= 0; --p)
+                        mma_bf16(D2, on(mat, p * M2_BYTES + M2_BYTES / 2 + k * MN_STEP), on(G, k * MN_STEP), w1 | A_MN,
+                                 k > 0 || p < 2);
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, scan_wait(&sb->r_ready, it & 1, sb));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < C / 16; ++k)
-                            mma_bf16(D2, desc_mn(img + p * M2_BYTES, k, M2_BYTES), desc_mn(sR + (sum - p) * RU_IMG, k, 16), id2,
-                                     !(sum == 2 && p == 0 && k == 0));
-#pragma unroll
-                for (int p = 2; p >= 0; --p)
-#pragma unroll
-                    for (int k = 0; k < C / 16; ++k)
-                        mma_bf16(D2, desc_mn(img + p * M2_BYTES + M2_BYTES / 2, k, M2_BYTES), desc_mn(sG, k, 16), id2, 1);
+                for (int k = 0; k < C / 16; ++k) {
+                    mma_bf16(D2 + NV, on(mat, M2_BYTES + k * MN_STEP), on(R, k * MN_STEP), w2 | A_MN, k > 0);
+                    mma_bf16(D2, on(mat, 2 * M2_BYTES + k * MN_STEP), on(R, k * MN_STEP), w1 | A_MN, 1);
+                    mma_bf16(D2, on(mat, k * MN_STEP), on(R, 2 * RU_IMG + k * MN_STEP), w1 | A_MN, 1);
+                    mma_bf16(D2 + NV, on(mat, k * MN_STEP), on(R, k * MN_STEP), w2 | A_MN, 1);
+                }
                 mma_commit(&sb->d2);
             }
             __syncwarp();
@@ -741,11 +836,8 @@ delta_adjoint_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int p = 2; p >= 0; --p)
-#pragma unroll
-                    for (int k = 0; k < 2 * C / 16; ++k)
-                        mma_bf16(D3, desc_mn(kq, k, KQ_BOX), desc_mn((k < 4 ? sR : sY) + p * RU_IMG, k % 4, 16), id2,
-                                 !(p == 2 && k == 0));
+                for (int k = 0; k < 2 * C / 16; ++k)
+                    mma_bf16(D3, on(cols, k * MN_STEP), on(k < 4 ? R : Y, k % 4 * MN_STEP), w3 | A_MN, k > 0);
                 mma_commit(&sb->d3);
                 mma_commit(&sb->kq_empty[st]);
             }
@@ -798,7 +890,7 @@ delta_adjoint_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = w * bf_at(v, i);
                 store_split32(sY, RU_IMG, tk, c0, x);
-                hand_over(&sb->r_ready, lane);
+                hand_over(&sb->g_ready, lane);
             }
             // Z for the chunk's local gradients, <S, Z> at its end
             if (state) {
@@ -826,7 +918,7 @@ delta_adjoint_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             if (keys) {
-                load_acc(d1, x);
+                load_parts<3>(d1, x);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] *= down;
                 store_split32(sR, RU_IMG, tk, c0, x);
@@ -837,7 +929,7 @@ delta_adjoint_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             tc_fence_after();
             if (lane == 0) mbar_arrive(&sb->img_empty);
             if (keys) {
-                load_acc(d2, x);
+                load_parts<3>(d2, x);
                 float y[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) y[i] = -up * (be * x[i]);
@@ -864,7 +956,7 @@ delta_adjoint_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             if (state) {
-                load_acc(d3, x);
+                load_parts<3>(d3, x);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) S[i] = fmaf(last, S[i], x[i]);
                 if (c > 0) store_split32(sS, L::S_IMG, row, c0, S);
@@ -876,7 +968,7 @@ delta_adjoint_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 256);
+    if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -979,8 +1071,9 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = lb->tmem, D1 = tmem, D2 = tmem + 128, D4 = tmem + 256, D3 = tmem + 384, D5 = tmem + 384;
-    const uint32_t kq = smem_addr(smem + L::kq), sA = smem_addr(smem + L::a), sU = smem_addr(smem + L::u),
-                   sS = smem_addr(smem + L::s);
+    const uint64_t A0 = desc_k(smem_addr(smem + L::a)), AT = desc_mn(smem_addr(smem + L::a), M2_BYTES),
+                   U0 = desc_k(smem_addr(smem + L::u)), S0 = desc_k(smem_addr(smem + L::s)),
+                   cols = desc_mn(smem_addr(smem + L::kq), KQ_BOX);
     Meta *meta = reinterpret_cast<Meta *>(smem + L::meta);
     // warp w: TMEM lanes 32 (w % 4) on, columns 32 (w / 4) on
     const int row = 32 * (warp & 3) + lane, c0 = warp / 4 * 32, tk = row & 63;
@@ -1029,10 +1122,10 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                     for (int p = 0; p <= sum; ++p)
 #pragma unroll
                         for (int k = 0; k < DV / 16; ++k) {
-                            const uint64_t da = desc_k(sA + p * L::A_IMG + (k / 4) * M2_BYTES, k % 4);
+                            const uint64_t da = on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP);
                             const bool add = !(sum == 1 && p == 0 && k == 0);
-                            mma_bf16(D1, da, desc_k(sS + (sum - p) * L::S_IMG + (k / 4) * (DK * 128), k % 4), id, add);
-                            mma_bf16(D3, da, desc_k(sU + (sum - p) * L::U_IMG + (k / 4) * RU_IMG, k % 4), idU, add);
+                            mma_bf16(D1, da, on(S0, (sum - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id, add);
+                            mma_bf16(D3, da, on(U0, (sum - p) * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP), idU, add);
                         }
                 mma_commit(&lb->first);
             }
@@ -1081,17 +1174,17 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                     for (int p = 0; p <= sum; ++p)
 #pragma unroll
                         for (int k = 0; k < DV / 16; ++k)
-                            mma_bf16(D2, desc_k(sU + p * L::U_IMG + (k / 4) * RU_IMG, k % 4),
-                                     desc_k(sS + (sum - p) * L::S_IMG + (k / 4) * (DK * 128), k % 4), id,
+                            mma_bf16(D2, on(U0, p * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP),
+                                     on(S0, (sum - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id,
                                      !(sum == 1 && p == 0 && k == 0));
 #pragma unroll
                 for (int p = 1; p >= 0; --p) {
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
-                        mma_bf16(D4, desc_k(sA + p * M2_BYTES, k), desc_mn(kq, k, KQ_BOX), idB, !(p == 1 && k == 0));
+                        mma_bf16(D4, on(A0, p * M2_BYTES + k * K_STEP), on(cols, k * MN_STEP), idB, !(p == 1 && k == 0));
 #pragma unroll
                     for (int k = 0; k < 2 * C / 16; ++k)
-                        mma_bf16(D5, desc_mn(sA + p * M2_BYTES, k, M2_BYTES), desc_mn(kq, k, KQ_BOX), idAB, !(p == 1 && k == 0));
+                        mma_bf16(D5, on(AT, p * M2_BYTES + k * MN_STEP), on(cols, k * MN_STEP), idAB, !(p == 1 && k == 0));
                 }
                 mma_commit(&lb->second);
             }
@@ -1162,9 +1255,9 @@ template <typename K> cudaError_t big_smem(K *kernel, size_t bytes) {
 }
 
 template <int DK, bool TRANS> cudaError_t launch_prep(const Args &a, cudaStream_t st) {
-    const cudaError_t e = big_smem(delta_prep_kernel<DK, TRANS>, sizeof(PrepSmem));
+    const cudaError_t e = big_smem(delta_prep_kernel<DK, TRANS>, PrepSmem<DK>::total);
     if (e != cudaSuccess) return e;
-    delta_prep_kernel<DK, TRANS><<<dim3(chunks(a.L), a.Hk, a.B), PT, sizeof(PrepSmem), st>>>(a);
+    delta_prep_kernel<DK, TRANS><<<dim3(chunks(a.L), a.Hk, a.B), PT, PrepSmem<DK>::total, st>>>(a);
     return cudaGetLastError();
 }
 
