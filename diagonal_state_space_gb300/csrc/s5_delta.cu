@@ -4,7 +4,8 @@
 //   S_t = a_t S_{t-1} + k_t u_t^T,  o_t = scale S_t^T q_t.
 // This file has the entry points, the single-token step and the CUDA-core
 // sweeps that serve every type and head size; bf16 heads of 64 or 128 run on
-// the tensor cores in chunks of 64 tokens (s5_delta_tc.cu).
+// the tensor cores in chunks of 64 tokens (s5_delta_prep.cu, s5_delta_scan.cu,
+// s5_delta_adjoint.cu).
 //
 // Sweeps.  Every column of S (a value index) is a recurrence of its own given
 // the keys, and every row (a key index) is one given the u_t.  So the forward
@@ -285,8 +286,7 @@ template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(
 
 // One warp per chunk and value head: dg by adding the chunk's terms from its
 // end on top of <S, Z> there.  A token whose decay is zero has no gradient.
-// tok > 0: the tokens' terms (and dbeta's) come in that many parts.
-__global__ void __launch_bounds__(256) decay_grads_kernel(const Args a, int tok) {
+__global__ void __launch_bounds__(256) decay_grads_kernel(const Args a) {
     const int N = chunks(a.L), lane = threadIdx.x % 32;
     const long long id = (long long)blockIdx.x * 8 + threadIdx.x / 32;
     if (id >= (long long)a.B * a.Hv * N) return;
@@ -300,20 +300,7 @@ __global__ void __launch_bounds__(256) decay_grads_kernel(const Args a, int tok)
     for (int half = 0; half < 2; ++half) {
         const int t = c * CHUNK + CHUNK - 1 - 32 * half - lane;
         const long long hv = (b * a.L + t) * a.Hv + h;
-        float w = 0.0f;
-        if (t < a.L) {
-            if (tok == 0)
-                w = a.dots[hv];
-            else {
-                const long long n = (long long)a.B * a.L * a.Hv * tok;
-                float db = 0.0f;
-                for (int p = 0; p < tok; ++p) {
-                    db += a.dots[hv * tok + p];
-                    w += a.dots[2 * n + hv * tok + p] - a.dots[n + hv * tok + p];
-                }
-                a.dbeta[hv] = db;
-            }
-        }
+        float w = t < a.L ? a.dots[hv] : 0.0f;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const float up = __shfl_up_sync(0xffffffffu, w, m);
@@ -449,17 +436,17 @@ template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
     if ((e = row_sweep<T, false>(a, st)) != cudaSuccess || (e = row_sweep<T, true>(a, st)) != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.L * a.Hv;
     token_grads_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
-    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a, 0);
+    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a);
     const long long n = (long long)a.B * a.L * a.Hk * a.Dk;
     group_sum_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
-// The tensor-core path's launches, and the gates' gradients from its parts.
+// The tensor-core path's launches, and the decays' gradients.
 cudaError_t backward_tc(const Args &a, cudaStream_t st) {
     const cudaError_t e = tc_backward(a, st);
     if (e != cudaSuccess) return e;
-    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a, a.Dv / 32);
+    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -477,8 +464,8 @@ s5_status check_sizes(long long B, long long L, long long Hk, long long Hv, long
 }
 
 // Regions of the two buffers.  The backward workspace holds what either path
-// needs: dq and dk per value head or the chunks' Z; parts of <S, Z> and of the
-// tokens' sums (16 and 3 Dv / 32 at most).
+// needs: dq and dk per value head or the chunks' Z; parts of <S, Z> (16 at
+// most) and the tokens' sums.
 struct Sizes {
     size_t e, states, images, heads, inner, dots;
 };
@@ -490,7 +477,7 @@ Sizes sizes(int B, int L, int Hv, int Dk, int Dv) {
     s.images = align256(tc_image_bytes(B, L, Hv, Dk, Dv));
     s.heads = align256(sizeof(float) * rows * Dk);
     s.inner = align256(sizeof(float) * (size_t)B * Hv * (N + 1) * 16);
-    s.dots = align256(sizeof(float) * rows * 3 * ((Dv + 31) / 32));
+    s.dots = align256(sizeof(float) * rows);
     return s;
 }
 size_t z_or_heads(const Sizes &s) { return s.images ? (s.states > 2 * s.heads ? s.states : 2 * s.heads) : 2 * s.heads; }
@@ -598,7 +585,7 @@ extern "C" s5_status s5_delta_backward(const void *q, long long ldq, const void 
     w += s.e;
     a.dqh = reinterpret_cast<float *>(w);
     a.dkh = reinterpret_cast<float *>(w + s.heads);
-    a.z = reinterpret_cast<float *>(w);
+    a.z = w;
     w += z_or_heads(s);
     a.parts = (Dv + OWN - 1) / OWN;
     a.inner = reinterpret_cast<float *>(w);

@@ -1,6 +1,6 @@
 // s5_delta.cuh -- what the kernels of the gated delta rule share
 // (s5_delta.cu: entry points, streaming step, CUDA-core sweeps;
-// s5_delta_tc.cu: tensor-core chunks).
+// s5_delta_prep.cu, s5_delta_scan.cu, s5_delta_adjoint.cu: tensor-core chunks).
 #pragma once
 #include "s5_internal.cuh"
 
@@ -35,9 +35,9 @@ struct Args {
     float *x;                         // [B][L][Hv][Dv]   dL/du_t
     float *dqh, *dkh;                 // [B][L][Hv][Dk]   per value head
     float *inner;                     // [B][Hv][N + 1][parts]   parts of <S_c, dL/dS_c>
-    float *dots;                      // [B][L][Hv] o.do - v.dv; tensor cores: [3][B][L][Hv][Dv / 32] parts of X.e, v.dv, o.do
+    float *dots;                      // [B][L][Hv] o.do - v.dv
     int parts;
-    float *z;                         // [B][Hv][N][Dk][Dv]   dL/dS at the end of chunk c (tensor cores)
+    void *z;                          // [B][Hv][N][Dv / 64][2][Dk][64] bf16: dL/dS at the end of chunk c, two parts (tensor cores)
     void *images;                     // operand images of the tensor-core path
 };
 
@@ -53,7 +53,7 @@ bool tc_supported(const Args &a, s5_dtype dtype, bool backward);
 // Workspace of the tensor-core path; 0 for head sizes that it does not take.
 size_t tc_image_bytes(int B, int L, int Hv, int Dk, int Dv);
 cudaError_t tc_forward(const Args &a, cudaStream_t st);
-// All gradients but dg and dbeta, and their parts (inner, dots).
+// All gradients but dg, and its terms (inner, dots).
 cudaError_t tc_backward(const Args &a, cudaStream_t st);
 int tc_inner_parts(int Dk, int Dv);
 

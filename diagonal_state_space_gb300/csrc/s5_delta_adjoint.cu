@@ -1,0 +1,640 @@
+// s5_delta_adjoint.cu -- the gated delta rule's backward pass on the tensor
+// cores; notation and precision as in s5_delta_scan.cu.
+//
+// The adjoint over chunks, last chunk first, with Z = dL/dS at the chunk's end
+// and T = (I + strict lower(beta_i D_ij k_i.k_j))^-1:
+//   X = T^T (e^{G_64 - G} K Z) + (P T)^T dO          X_t = dL/du_t
+//   dv = beta X
+//   Z_start = e^{G_64} Z + K^T (-e^G dv) + Q^T (scale e^G dO)
+// the forward's three products transposed, on the same tiles: D1 = [K; Q] Z,
+// D2 = [T; P T]^T [e^{..} K Z; dO] (depth 128), D3 = [K; Q]^T [..; ..] (depth
+// 128).  Z leaves chunk by chunk as the two upper parts of its operand, in the
+// layout that the local products below read.  <S, Z> at each chunk's end, the
+// anchor of the decays' gradients, is taken in 32 bits on the way.
+//
+// All else is local to a chunk (delta_local_kernel).
+#include "s5_delta_mma.cuh"
+
+namespace s5 {
+namespace delta {
+namespace {
+
+struct AdjMaps {
+    CUtensorMap k, q, g, x, s;   // keys, queries, dO, X, states
+};
+
+template <int DK> struct AdjSmem {
+    static constexpr uint32_t KQ = KQ_BOX * (DK / 64);
+    static constexpr uint32_t S_IMG = DK * 128;
+    static constexpr uint32_t kq = 0;                      // two stages
+    static constexpr uint32_t mat = kq + 2 * KQ;
+    // Z's parts until D1 is done; then e^{..} K Z's, later -e^G dv's, and
+    // behind them scale e^G dO's
+    static constexpr uint32_t ops = mat + MAT_BYTES;
+    static constexpr uint32_t go = ops + 6 * RU_IMG;       // dO
+    static constexpr uint32_t xs = go + RU_IMG;            // X, to be stored
+    static constexpr uint32_t sin = xs + 2 * RU_IMG;       // the state at the chunk's end
+    static constexpr uint32_t meta = sin + DK * 256;
+    static constexpr uint32_t bars = meta + META_BYTES;
+    static constexpr uint32_t total = bars + 256 + 1024;
+    static_assert(total <= 232448, "shared memory of a CTA");
+    static_assert(3 * S_IMG <= 6 * RU_IMG, "Z fits");
+};
+
+struct AdjBars {
+    uint64_t kq_full[2], kq_empty[2], img_full, img_empty, go_full, go_empty, sin_full, sin_empty;
+    uint64_t d1, d2, d3, z_ready, r_ready, y_ready, z_left, x_ready, x_left, drain;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(AdjBars) <= 256, "barriers");
+
+constexpr int ADJ_THREADS = 320;   // 8 compute warps, products, copies
+
+template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoint_kernel(const __grid_constant__ AdjMaps maps, const Args a) {
+    using L = AdjSmem<DK>;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    AdjBars *sb = reinterpret_cast<AdjBars *>(smem + L::bars);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int n0 = blockIdx.x * NV, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
+    const int N = chunks(a.L);
+    const long long bh = (long long)b * a.Hv + h;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) mbar_init(&sb->kq_full[i], 1), mbar_init(&sb->kq_empty[i], 1);
+        mbar_init(&sb->img_full, 1), mbar_init(&sb->img_empty, 8);
+        mbar_init(&sb->go_full, 1), mbar_init(&sb->go_empty, 4);
+        mbar_init(&sb->sin_full, 1), mbar_init(&sb->sin_empty, 8);
+        mbar_init(&sb->d1, 1), mbar_init(&sb->d2, 1), mbar_init(&sb->d3, 1);
+        mbar_init(&sb->z_ready, 8), mbar_init(&sb->r_ready, 4), mbar_init(&sb->y_ready, 8);
+        mbar_init(&sb->z_left, 1), mbar_init(&sb->x_ready, 4), mbar_init(&sb->x_left, 1);
+        mbar_init(&sb->drain, 1);
+        sb->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&sb->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // D3 takes D1's place: every warp that reads D1 has done so before it hands
+    // the operands of D3 over
+    const uint32_t tmem = sb->tmem, D1 = tmem, D2 = tmem + 3 * NV, D3 = tmem;
+    auto wait = [&](uint64_t *bar, int parity) { return bounded_wait(bar, (uint32_t)parity, &sb->abort); };
+
+    if (warp == 9) {
+        if (lane == 0) {
+            // ------------------------------------------------------ copies
+            auto load_kq = [&](int it) {
+                const int c = N - 1 - it;
+                unsigned char *to = smem + L::kq + (it & 1) * L::KQ;
+                uint64_t *bar = &sb->kq_full[it & 1];
+                mbar_arrive_tx(bar, L::KQ);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x) {
+                    tma_load_4d(to + x * KQ_BOX, &maps.k, 64 * x, hk, c * C, b, bar);
+                    tma_load_4d(to + x * KQ_BOX + KQ_BOX / 2, &maps.q, 64 * x, hk, c * C, b, bar);
+                }
+            };
+            auto load_img = [&](int it) {
+                const unsigned char *from = static_cast<const unsigned char *>(a.images) + (bh * N + N - 1 - it) * IMG_BYTES;
+                mbar_arrive_tx(&sb->img_full, IMG_BYTES);
+                bulk_load(smem + L::mat, from, MAT_BYTES, &sb->img_full);
+                bulk_load(smem + L::meta, from + MAT_BYTES, META_BYTES, &sb->img_full);
+            };
+            auto load_go = [&](int it) {
+                mbar_arrive_tx(&sb->go_full, RU_IMG);
+                tma_load_4d(smem + L::go, &maps.g, n0, h, (N - 1 - it) * C, b, &sb->go_full);
+            };
+            auto load_state = [&](int it) {
+                mbar_arrive_tx(&sb->sin_full, DK * 256);
+                for (int x = 0; x < 2; ++x)
+                    tma_load_3d(smem + L::sin + x * DK * 128, &maps.s, n0 + 32 * x, 0, (int)(bh * (N + 1) + N - it), &sb->sin_full);
+            };
+            load_kq(0);
+            load_state(0);
+            load_img(0);
+            load_go(0);
+            if (N > 1) load_kq(1);
+            bool ok = true;
+            for (int it = 0; it < N; ++it) {
+                const int c = N - 1 - it;
+                if (!(ok = wait(&sb->z_ready, it & 1))) break;
+                bulk_store(static_cast<unsigned char *>(a.z) + ((bh * N + c) * (a.Dv / NV) + blockIdx.x) * (2 * L::S_IMG),
+                           smem + L::ops, 2 * L::S_IMG);
+                bulk_commit();
+                bulk_wait_read_all();
+                mbar_arrive(&sb->z_left);
+                if (it + 1 < N) {
+                    if (!(ok = wait(&sb->sin_empty, it & 1))) break;
+                    load_state(it + 1);
+                    if (!(ok = wait(&sb->img_empty, it & 1) && wait(&sb->go_empty, it & 1))) break;
+                    load_img(it + 1);
+                    load_go(it + 1);
+                }
+                if (!(ok = wait(&sb->x_ready, it & 1))) break;
+                for (int x = 0; x < 2; ++x) tma_store_4d(&maps.x, smem + L::xs + x * RU_IMG, n0 + 32 * x, h, c * C, b);
+                bulk_commit();
+                bulk_wait_read_all();
+                mbar_arrive(&sb->x_left);
+                if (it + 2 < N) {
+                    if (!(ok = wait(&sb->kq_empty[it & 1], (it >> 1) & 1))) break;
+                    load_kq(it + 2);
+                }
+            }
+            bulk_wait_all();
+            if (!ok) settle_copies();
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        if (lane == 0) {
+            // ------------------------------------------------------ products
+            const uint32_t w1 = idesc_bf16_f32(128, NV) | B_MN, w2 = idesc_bf16_f32(128, 2 * NV) | B_MN,
+                           w3 = idesc_bf16_f32(128, 3 * NV) | B_MN;
+            const uint64_t mat = desc_mn(smem_addr(smem + L::mat), M2_BYTES), Z = desc_mn(smem_addr(smem + L::ops), L::S_IMG),
+                           R = desc_mn(smem_addr(smem + L::ops), RU_IMG), Y = desc_mn(smem_addr(smem + L::ops + 3 * RU_IMG), RU_IMG),
+                           G = desc_mn(smem_addr(smem + L::go), RU_IMG);
+            bool ok = true;
+            for (int it = 0; ok && it < N; ++it) {
+                const uint32_t kq = smem_addr(smem + L::kq + (it & 1) * L::KQ);
+                const uint64_t rows = desc_k(kq), cols = desc_mn(kq, KQ_BOX);
+                if (!(ok = wait(&sb->kq_full[it & 1], (it >> 1) & 1) && wait(&sb->z_ready, it & 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k)
+                    mma_bf16(D1, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), on(Z, k * MN_STEP), w3, k > 0);
+                mma_commit(&sb->d1);
+                // (P T)^T dO waits for nothing else.  The matrix transposed has
+                // 64 rows: lanes 64..127 of D2 come from what follows it in
+                // shared memory, and are not read
+                if (!(ok = wait(&sb->img_full, it & 1) && wait(&sb->go_full, it & 1))) break;
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k)
+#pragma unroll
+                    for (int p = 2; p >= 0; --p)
+                        mma_bf16(D2, on(mat, p * M2_BYTES + M2_BYTES / 2 + k * MN_STEP), on(G, k * MN_STEP), w1 | A_MN, k > 0 || p < 2);
+                if (!(ok = wait(&sb->r_ready, it & 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k) {
+                    mma_bf16(D2 + NV, on(mat, M2_BYTES + k * MN_STEP), on(R, k * MN_STEP), w2 | A_MN, k > 0);
+                    mma_bf16(D2, on(mat, 2 * M2_BYTES + k * MN_STEP), on(R, k * MN_STEP), w1 | A_MN, 1);
+                    mma_bf16(D2, on(mat, k * MN_STEP), on(R, 2 * RU_IMG + k * MN_STEP), w1 | A_MN, 1);
+                    mma_bf16(D2 + NV, on(mat, k * MN_STEP), on(R, k * MN_STEP), w2 | A_MN, 1);
+                }
+                mma_commit(&sb->d2);
+                if (!(ok = wait(&sb->y_ready, it & 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 2 * C / 16; ++k)
+                    mma_bf16(D3, on(cols, k * MN_STEP), on(k < 4 ? R : Y, k % 4 * MN_STEP), w3 | A_MN, k > 0);
+                mma_commit(&sb->d3);
+                mma_commit(&sb->kq_empty[it & 1]);
+            }
+            drain_products(&sb->drain);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- compute
+        const int q = warp & 3, c0 = warp / 4 * 32, row = 32 * q + lane;
+        const bool keys = q < 2;
+        const int tk = row & 63;
+        const uint32_t lanes = ((uint32_t)(32 * q) << 16) + c0;
+        const uint32_t ops = smem_addr(smem + L::ops), go = smem_addr(smem + L::go), xs = smem_addr(smem + L::xs),
+                       sin = smem_addr(smem + L::sin);
+        const Meta *meta = reinterpret_cast<const Meta *>(smem + L::meta);
+        const bool state = row < DK;
+        const long long place = bh * DK * a.Dv + (long long)row * a.Dv + n0 + c0;   // this row in ds_last, ds0
+        f2 Z[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 t = (a.ds_last && state) ? *reinterpret_cast<const float4 *>(a.ds_last + place + 4 * j) : make_float4(0, 0, 0, 0);
+            Z[2 * j] = make2(t.x, t.y), Z[2 * j + 1] = make2(t.z, t.w);
+        }
+        if (state) put3<32>(ops, L::S_IMG, row, c0, Z);
+        hand_over(&sb->z_ready, lane);
+        for (int it = 0; it < N; ++it) {
+            const int c = N - 1 - it;
+            // <S, Z> at the chunk's end
+            bool ok = wait(&sb->sin_full, it & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (state) {
+                f2 w = both(0.0f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint4 t = lds128(piece(sin + c0 / 32 * (DK * 128), row, j));
+                    w = fma2(make2(t.x, t.y), Z[2 * j], w);
+                    w = fma2(make2(t.z, t.w), Z[2 * j + 1], w);
+                }
+                float s = lof(w) + hif(w);
+                for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                if (lane == 0) a.inner[(bh * (N + 1) + c + 1) * a.parts + blockIdx.x * (DK / 16) + q * 2 + warp / 4] = s;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sb->sin_empty);
+            ok = wait(&sb->img_full, it & 1) && wait(&sb->d1, it & 1) && wait(&sb->z_left, it & 1) && (keys || wait(&sb->go_full, it & 1));
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            f2 x[16];
+            const f2 last = both(meta->last);
+            const float up = meta->up[tk], be = meta->beta[tk];
+            if (keys) {
+                const f2 down = both(meta->down[tk]);
+                load_parts<3, 32>(D1 + lanes, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = mul2(down, x[i]);
+                put3<32>(ops, RU_IMG, tk, c0, x);
+                hand_over(&sb->r_ready, lane);
+            } else {
+                const f2 w = both(a.scale * up);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 v = lds128(piece(go, tk, c0 / 8 + j));
+                    x[4 * j] = mul2(w, widen(v.x)), x[4 * j + 1] = mul2(w, widen(v.y));
+                    x[4 * j + 2] = mul2(w, widen(v.z)), x[4 * j + 3] = mul2(w, widen(v.w));
+                }
+                put3<32>(ops + 3 * RU_IMG, RU_IMG, tk, c0, x);
+                hand_over(&sb->y_ready, lane);
+            }
+            ok = wait(&sb->d2, it & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mbar_arrive(&sb->img_empty);
+                if (!keys) mbar_arrive(&sb->go_empty);
+            }
+            if (keys) {
+                load_parts<3, 32>(D2 + lanes, x);
+                const f2 w = both(-up * be);
+                f2 y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = mul2(w, x[i]);
+                put3<32>(ops, RU_IMG, tk, c0, y);
+                hand_over(&sb->y_ready, lane);
+                ok = it == 0 || wait(&sb->x_left, (it - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                put_row(xs + c0 / 32 * RU_IMG, tk, x);
+                hand_over(&sb->x_ready, lane);
+            }
+            ok = wait(&sb->d3, it & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            if (state) {
+                load_parts<3, 32>(D3 + lanes, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) Z[i] = fma2(last, Z[i], x[i]);
+                if (c > 0) put3<32>(ops, L::S_IMG, row, c0, Z);
+            }
+            if (c > 0) hand_over(&sb->z_ready, lane);
+        }
+        if (state && a.ds0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4 *>(a.ds0 + place + 4 * j) =
+                    make_float4(lof(Z[2 * j]), hif(Z[2 * j]), lof(Z[2 * j + 1]), hif(Z[2 * j + 1]));
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// What is local to a chunk, all chunks at once: one CTA per chunk and key head,
+// over its value heads.  Per token dv = beta X, dbeta = X . e and
+// o . dO - v . dv (for the decays, s5_delta.cu).  With S0 and Z the state at
+// the chunk's start and the adjoint at its end, U = beta e, and
+// N_ij = scale D_ij dO_i.U_j (j <= i), W_ij = -D_ij dv_i.U_j (j < i):
+//   dq = scale e^G dO S0^T + N K
+//   dk = e^{G_64 - G} U Z^T - e^G dv S0^T + W K + W^T K + N^T Q
+// as products of M = 128 with the rows of [dv; dO] stacked, so that dk lies in
+// TMEM lanes 0..63 and dq in 64..127:
+//   D2 = [U; -] Z^T,  D3 = [dv; dO] U^T,
+//   D1 = [dv; dO] S0^T,  D4 = [W; N] K,  D5 = [W; N]^T [K; Q].
+// dq and dk are rounded to bf16, so that 32-bit operands are carried as two
+// bf16 values here (17 bits), three products against another pair, two against
+// a bf16 operand.
+// Bound: what it reads (the state, the adjoint and 64 tokens' X, e, o, dO, v:
+// 240 KB per chunk and head of 128 x 128).
+// ---------------------------------------------------------------------------
+constexpr int LT = 512;
+
+template <int DK, int DV> struct LocalSmem {
+    static constexpr uint32_t KQ = KQ_BOX * (DK / 64);
+    static constexpr uint32_t A_IMG = 128 * 128 * (DV / 64);   // [dv; dO]
+    static constexpr uint32_t U_IMG = 64 * 128 * (DV / 64);
+    static constexpr uint32_t S_IMG = DK * 128 * (DV / 64);
+    static constexpr uint32_t kq = 0;
+    static constexpr uint32_t a = kq + KQ;                     // two parts; [W; N], two parts, later
+    static constexpr uint32_t u = a + 2 * A_IMG;
+    static constexpr uint32_t s = u + 2 * U_IMG;               // Z, then S0: two parts
+    static constexpr uint32_t meta = s + 2 * S_IMG;
+    static constexpr uint32_t bars = meta + META_BYTES;
+    static constexpr uint32_t total = bars + 64 + 1024;
+    static_assert(total <= 232448, "shared memory of a CTA");
+    static_assert(A_IMG >= M2_BYTES, "[W; N] fits");
+    static_assert(2 * S_IMG >= 8192, "M = 128 over the 64 rows of U reads 8 KB on");
+};
+
+struct LocalBars {
+    uint64_t z_full, first, second;
+    uint32_t tmem;
+    int abort;
+};
+
+// Eight values (pairs v) as a 16-byte piece of two images.
+__device__ __forceinline__ void put2(uint32_t img, uint32_t stride, int row, int j, const f2 (&v)[4]) {
+    uint32_t h[4], m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2(v[i], h[i], m[i]);
+    const uint32_t to = piece(img, row, j);
+    sts128(to, h[0], h[1], h[2], h[3]);
+    sts128(to + stride, m[0], m[1], m[2], m[3]);
+}
+__device__ __forceinline__ void load8(const float *p, f2 (&v)[4]) {
+    const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = make2(x.x, x.y), v[1] = make2(x.z, x.w), v[2] = make2(y.x, y.y), v[3] = make2(y.z, y.w);
+}
+
+template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_kernel(const Args a) {
+    using L = LocalSmem<DK, DV>;
+    constexpr int PR = DV / 8;     // lanes of a token's row, 8 values each
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    LocalBars *lb = reinterpret_cast<LocalBars *>(smem + L::bars);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, group = a.Hv / a.Hk;
+    const int t0 = c * C, nt = min(C, a.L - t0), N = chunks(a.L);
+    const long long row0 = (long long)b * a.L + t0, mat = (long long)DK * DV;
+    if (tid == 0) {
+        mbar_init(&lb->z_full, 1);
+        mbar_init(&lb->first, 1);
+        mbar_init(&lb->second, 1);
+        lb->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&lb->tmem, 512);
+        tmem_relinquish();
+    }
+    const uint32_t kq = smem_addr(smem + L::kq), sA = smem_addr(smem + L::a), sU = smem_addr(smem + L::u),
+                   sS = smem_addr(smem + L::s);
+    for (int i = tid; i < 128 * (DK / 8); i += LT) {
+        const int r = i / (DK / 8), d = i % (DK / 8) * 8, t = r & 63;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (t < nt)
+            v = r < C ? *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + d)
+                      : *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + d);
+        sts128(piece(kq + d / 64 * KQ_BOX, r, d % 64 / 8), v.x, v.y, v.z, v.w);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lb->tmem, D1 = tmem, D2 = tmem + 128, D4 = tmem + 256, D3 = tmem + 384, D5 = tmem + 384;
+    const uint64_t A0 = desc_k(sA), AT = desc_mn(sA, M2_BYTES), U0 = desc_k(sU), S0 = desc_k(sS), cols = desc_mn(kq, KQ_BOX);
+    Meta *meta = reinterpret_cast<Meta *>(smem + L::meta);
+    auto wait = [&](uint64_t *bar, int parity) { return bounded_wait(bar, (uint32_t)parity, &lb->abort); };
+    // warp w: TMEM lanes 32 (w % 4) on, columns 32 (w / 4) on
+    const int row = 32 * (warp & 3) + lane, c0 = warp / 4 * 32, tk = row & 63;
+    const bool keys = row < C;
+    const uint32_t lanes = ((uint32_t)(32 * (warp & 3)) << 16) + c0;
+    f2 sum[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[i] = both(0.0f);
+    bool ok = true;
+    for (int j = 0; j < group; ++j) {
+        const int h = hk * group + j;
+        const long long bh = (long long)b * a.Hv + h;
+        if (tid == 0) {
+            mbar_arrive_tx(&lb->z_full, 2 * L::S_IMG + META_BYTES);
+            const unsigned char *z = reinterpret_cast<const unsigned char *>(a.z) + (bh * N + c) * (2 * L::S_IMG);
+            for (int x = 0; x < DV / 64; ++x)
+                for (int p = 0; p < 2; ++p)
+                    bulk_load(smem + L::s + p * L::S_IMG + x * (DK * 128), z + (2 * x + p) * (DK * 128), DK * 128, &lb->z_full);
+            bulk_load(meta, static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES + MAT_BYTES, META_BYTES, &lb->z_full);
+        }
+#pragma unroll
+        for (int n = 0; n < C * PR / LT; ++n) {
+            const int i = tid + n * LT, t = i / PR, d = i % PR * 8;
+            const long long hv = (row0 + t) * a.Hv + h;
+            f2 x[4], e[4], o[4], w = both(0.0f), db = w;
+            uint4 g = make_uint4(0, 0, 0, 0), v = g;
+            float be = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = e[k] = o[k] = w;
+            if (t < nt) {
+                load8(a.x + hv * DV + d, x);
+                load8(a.e + hv * DV + d, e);
+                load8(a.o32 + hv * DV + d, o);
+                g = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dout) + (row0 + t) * a.lddo + (long long)h * DV + d);
+                v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) + (row0 + t) * a.ldv + (long long)h * DV + d);
+                be = a.beta[hv];
+            }
+            const f2 b2 = both(be), minus = both(-1.0f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                db = fma2(x[k], e[k], db);
+                x[k] = mul2(b2, x[k]), e[k] = mul2(b2, e[k]);
+                const uint32_t gk = k == 0 ? g.x : k == 1 ? g.y : k == 2 ? g.z : g.w, vk = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+                w = fma2(o[k], widen(gk), w);
+                w = fma2(mul2(minus, widen(vk)), x[k], w);
+            }
+            const int box = d / 64, at = d % 64 / 8;
+            put2(sA + box * M2_BYTES, L::A_IMG, t, at, x);
+            put2(sU + box * RU_IMG, L::U_IMG, t, at, e);
+            sts128(piece(sA + box * M2_BYTES, C + t, at), g.x, g.y, g.z, g.w);
+            sts128(piece(sA + L::A_IMG + box * M2_BYTES, C + t, at), 0, 0, 0, 0);   // dO is bf16: no second part
+            float s1 = lof(db) + hif(db), s2 = lof(w) + hif(w);
+#pragma unroll
+            for (int m = PR / 2; m > 0; m >>= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, m), s2 += __shfl_xor_sync(0xffffffffu, s2, m);
+            if (t < nt) {
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dv) + (row0 + t) * a.lddv + (long long)h * DV + d) =
+                    make_uint4(pack2(lof(x[0]), hif(x[0])), pack2(lof(x[1]), hif(x[1])), pack2(lof(x[2]), hif(x[2])),
+                               pack2(lof(x[3]), hif(x[3])));
+                if (d == 0) a.dbeta[hv] = s1, a.dots[hv] = s2;
+            }
+        }
+        // S0 is on its way while the first products run
+        const float *s0 = a.states + (bh * (N + 1) + c) * mat;
+        constexpr int SN = DK * DV / 8 / LT;
+        float4 sr[2 * SN];
+#pragma unroll
+        for (int n = 0; n < SN; ++n) {
+            sr[2 * n] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8);
+            sr[2 * n + 1] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8 + 4);
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            const uint32_t id = idesc_bf16_f32(128, DK), idU = idesc_bf16_f32(128, 64);
+#pragma unroll
+            for (int ps = 1; ps >= 0; --ps)
+#pragma unroll
+                for (int p = 0; p <= ps; ++p)
+#pragma unroll
+                    for (int k = 0; k < DV / 16; ++k)
+                        mma_bf16(D3, on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP),
+                                 on(U0, (ps - p) * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP), idU, !(ps == 1 && p == 0 && k == 0));
+            if (wait(&lb->z_full, j & 1)) {
+#pragma unroll
+                for (int ps = 1; ps >= 0; --ps)
+#pragma unroll
+                    for (int p = 0; p <= ps; ++p)
+#pragma unroll
+                        for (int k = 0; k < DV / 16; ++k)
+                            mma_bf16(D2, on(U0, p * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP),
+                                     on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id,
+                                     !(ps == 1 && p == 0 && k == 0));
+            }
+            mma_commit(&lb->first);
+        }
+        __syncwarp();
+        ok = wait(&lb->first, j & 1) && wait(&lb->z_full, j & 1) && ok;
+        tc_fence_after();
+        f2 x[16];
+        if (c0 < 64) load_parts<1, 32>(D3 + lanes, x);
+#pragma unroll
+        for (int n = 0; n < SN; ++n) {
+            const int i = tid + n * LT, r = i / PR, d = i % PR * 8;
+            f2 v[4] = {make2(sr[2 * n].x, sr[2 * n].y), make2(sr[2 * n].z, sr[2 * n].w), make2(sr[2 * n + 1].x, sr[2 * n + 1].y),
+                       make2(sr[2 * n + 1].z, sr[2 * n + 1].w)};
+            put2(sS + d / 64 * (DK * 128), L::S_IMG, r, d % 64 / 8, v);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        const uint32_t id = idesc_bf16_f32(128, DK), idB = id | B_MN, idAB = idB | A_MN;
+        if (tid == 0) {
+#pragma unroll
+            for (int ps = 1; ps >= 0; --ps)
+#pragma unroll
+                for (int p = 0; p <= ps; ++p)
+#pragma unroll
+                    for (int k = 0; k < DV / 16; ++k)
+                        mma_bf16(D1, on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP),
+                                 on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id, !(ps == 1 && p == 0 && k == 0));
+            mma_commit(&lb->second);
+        }
+        __syncwarp();
+        if (c0 < 64) {   // [W; N]
+            const float gh = meta->hi[tk], gl = meta->lo[tk];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float w[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int col = c0 + 2 * i + k;
+                    const bool in = keys ? col < tk : col <= tk;
+                    w[k] = in ? (keys ? -1.0f : a.scale) * expf((gh - meta->hi[col]) + (gl - meta->lo[col])) : 0.0f;
+                }
+                x[i] = mul2(make2(w[0], w[1]), x[i]);
+                // a masked product may be infinite or NaN where its factor is 0
+                if (keys ? c0 + 2 * i >= tk : c0 + 2 * i > tk) x[i] = both(0.0f);
+                else if (keys ? c0 + 2 * i + 1 >= tk : c0 + 2 * i + 1 > tk) x[i] = make2(lo32(x[i]), 0u);
+            }
+        }
+        ok = wait(&lb->second, 0) && ok;   // [dv; dO] has been read
+        tc_fence_after();
+        if (c0 < 64)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const f2 v[4] = {x[4 * n], x[4 * n + 1], x[4 * n + 2], x[4 * n + 3]};
+                put2(sA, M2_BYTES, row, c0 / 8 + n, v);
+            }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (tid == 0) {
+#pragma unroll
+            for (int p = 1; p >= 0; --p) {
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k)
+                    mma_bf16(D4, on(A0, p * M2_BYTES + k * K_STEP), on(cols, k * MN_STEP), idB, !(p == 1 && k == 0));
+#pragma unroll
+                for (int k = 0; k < 2 * C / 16; ++k)
+                    mma_bf16(D5, on(AT, p * M2_BYTES + k * MN_STEP), on(cols, k * MN_STEP), idAB, !(p == 1 && k == 0));
+            }
+            mma_commit(&lb->second);
+        }
+        __syncwarp();
+        if (c0 < DK) {   // meanwhile what the earlier products give
+            const float up = meta->up[tk];
+            const f2 w = both(keys ? -up : a.scale * up), down = both(meta->down[tk]);
+            load_parts<1, 32>(D1 + lanes, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[i] = fma2(w, x[i], sum[i]);
+            if (keys) {
+                load_parts<1, 32>(D2 + lanes, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[i] = fma2(down, x[i], sum[i]);
+            }
+        }
+        ok = wait(&lb->second, 1) && ok;
+        tc_fence_after();
+        if (c0 < DK) {
+            load_parts<1, 32>(D4 + lanes, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[i] = add2(x[i], sum[i]);
+            if (keys) {
+                load_parts<1, 32>(D5 + lanes, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[i] = add2(x[i], sum[i]);
+            }
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
+    if (c0 < DK && tk < nt) {
+        __nv_bfloat16 *p = keys ? static_cast<__nv_bfloat16 *>(a.dk) + (row0 + tk) * a.lddk + hk * DK + c0
+                                : static_cast<__nv_bfloat16 *>(a.dq) + (row0 + tk) * a.lddq + hk * DK + c0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(p + 8 * j) =
+                make_uint4(pack2(lof(sum[4 * j]), hif(sum[4 * j])), pack2(lof(sum[4 * j + 1]), hif(sum[4 * j + 1])),
+                           pack2(lof(sum[4 * j + 2]), hif(sum[4 * j + 2])), pack2(lof(sum[4 * j + 3]), hif(sum[4 * j + 3])));
+    }
+    if (!ok) settle_copies();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <int DK, int DV> cudaError_t launch_local(const Args &a, cudaStream_t st) {
+    const cudaError_t e = big_smem(delta_local_kernel<DK, DV>, LocalSmem<DK, DV>::total);
+    if (e != cudaSuccess) return e;
+    delta_local_kernel<DK, DV><<<dim3(chunks(a.L), a.Hk, a.B), LT, LocalSmem<DK, DV>::total, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int DK> cudaError_t backward(const Args &a, cudaStream_t st) {
+    AdjMaps m = {};
+    cudaError_t e = encode_rows(&m.k, false, a.k, a.ldk, a.B, a.L, a.Hk, DK);
+    if (e == cudaSuccess) e = encode_rows(&m.q, false, a.q, a.ldq, a.B, a.L, a.Hk, DK);
+    if (e == cudaSuccess) e = encode_rows(&m.g, false, a.dout, a.lddo, a.B, a.L, a.Hv, a.Dv);
+    if (e == cudaSuccess) e = encode_rows(&m.x, true, a.x, (long long)a.Hv * a.Dv, a.B, a.L, a.Hv, a.Dv);
+    if (e == cudaSuccess) e = encode_states(&m.s, a.states, (long long)a.B * a.Hv * (chunks(a.L) + 1), DK, a.Dv);
+    if (e == cudaSuccess) e = tc_prepare(a, true, st);
+    if (e == cudaSuccess) e = big_smem(delta_adjoint_kernel<DK>, AdjSmem<DK>::total);
+    if (e != cudaSuccess) return e;
+    delta_adjoint_kernel<DK><<<dim3(a.Dv / NV, a.Hv, a.B), ADJ_THREADS, AdjSmem<DK>::total, st>>>(m, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return a.Dv == 128 ? launch_local<DK, 128>(a, st) : launch_local<DK, 64>(a, st);
+}
+
+}  // namespace
+
+cudaError_t tc_backward(const Args &a, cudaStream_t st) {
+    return a.Dk == 128 ? backward<128>(a, st) : backward<64>(a, st);
+}
+
+int tc_inner_parts(int Dk, int Dv) { return Dv / NV * (Dk / 16); }
+
+int adjoint_fault_take() { return fault_take(); }
+
+}  // namespace delta
+}  // namespace s5
