@@ -63,11 +63,11 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) mbar_init(&sb->kq_full[i], 1), mbar_init(&sb->kq_empty[i], 1);
         mbar_init(&sb->img_full, 1), mbar_init(&sb->img_empty, 8);
-        mbar_init(&sb->go_full, 1), mbar_init(&sb->go_empty, 4);
+        mbar_init(&sb->go_full, 1), mbar_init(&sb->go_empty, 8);
         mbar_init(&sb->sin_full, 1), mbar_init(&sb->sin_empty, 8);
         mbar_init(&sb->d1, 1), mbar_init(&sb->d2, 1), mbar_init(&sb->d3, 1);
-        mbar_init(&sb->z_ready, 8), mbar_init(&sb->r_ready, 4), mbar_init(&sb->y_ready, 8);
-        mbar_init(&sb->z_left, 1), mbar_init(&sb->x_ready, 4), mbar_init(&sb->x_left, 1);
+        mbar_init(&sb->z_ready, 8), mbar_init(&sb->r_ready, 8), mbar_init(&sb->y_ready, 8);
+        mbar_init(&sb->z_left, 1), mbar_init(&sb->x_ready, 8), mbar_init(&sb->x_left, 1);
         mbar_init(&sb->drain, 1);
         sb->abort = 0;
         fence_mbar_init();
@@ -88,15 +88,7 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
         if (lane == 0) {
             // ------------------------------------------------------ copies
             auto load_kq = [&](int it) {
-                const int c = N - 1 - it;
-                unsigned char *to = smem + L::kq + (it & 1) * L::KQ;
-                uint64_t *bar = &sb->kq_full[it & 1];
-                mbar_arrive_tx(bar, L::KQ);
-#pragma unroll
-                for (int x = 0; x < DK / 64; ++x) {
-                    tma_load_4d(to + x * KQ_BOX, &maps.k, 64 * x, hk, c * C, b, bar);
-                    tma_load_4d(to + x * KQ_BOX + KQ_BOX / 2, &maps.q, 64 * x, hk, c * C, b, bar);
-                }
+                load_chunk_rows<DK>(smem + L::kq + (it & 1) * L::KQ, &maps.k, &maps.q, hk, (N - 1 - it) * C, b, &sb->kq_full[it & 1]);
             };
             auto load_img = [&](int it) {
                 const unsigned char *from = static_cast<const unsigned char *>(a.images) + (bh * N + N - 1 - it) * IMG_BYTES;
@@ -151,7 +143,9 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
     } else if (warp == 8) {
         if (lane == 0) {
             // ------------------------------------------------------ products
-            const uint32_t w1 = idesc_bf16_f32(128, NV) | B_MN, w2 = idesc_bf16_f32(128, 2 * NV) | B_MN,
+            // D2 has 64 rows (the matrix transposed): M = 64 spreads them over
+            // 16 of each 32 lanes
+            const uint32_t w1 = idesc_bf16_f32(64, NV) | A_MN | B_MN, w2 = idesc_bf16_f32(64, 2 * NV) | A_MN | B_MN,
                            w3 = idesc_bf16_f32(128, 3 * NV) | B_MN;
             const uint64_t mat = desc_mn(smem_addr(smem + L::mat), M2_BYTES), Z = desc_mn(smem_addr(smem + L::ops), L::S_IMG),
                            R = desc_mn(smem_addr(smem + L::ops), RU_IMG), Y = desc_mn(smem_addr(smem + L::ops + 3 * RU_IMG), RU_IMG),
@@ -166,30 +160,29 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
                 for (int k = 0; k < DK / 16; ++k)
                     mma_bf16(D1, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), on(Z, k * MN_STEP), w3, k > 0);
                 mma_commit(&sb->d1);
-                // (P T)^T dO waits for nothing else.  The matrix transposed has
-                // 64 rows: lanes 64..127 of D2 come from what follows it in
-                // shared memory, and are not read
+                // (P T)^T dO waits for nothing else
                 if (!(ok = wait(&sb->img_full, it & 1) && wait(&sb->go_full, it & 1))) break;
 #pragma unroll
                 for (int k = 0; k < C / 16; ++k)
 #pragma unroll
                     for (int p = 2; p >= 0; --p)
-                        mma_bf16(D2, on(mat, p * M2_BYTES + M2_BYTES / 2 + k * MN_STEP), on(G, k * MN_STEP), w1 | A_MN, k > 0 || p < 2);
+                        mma_bf16(D2, on(mat, p * M2_BYTES + (2 * k + 1) * KQ_GROUP), on(G, k * MN_STEP), w1, k > 0 || p < 2);
                 if (!(ok = wait(&sb->r_ready, it & 1))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < C / 16; ++k) {
-                    mma_bf16(D2 + NV, on(mat, M2_BYTES + k * MN_STEP), on(R, k * MN_STEP), w2 | A_MN, k > 0);
-                    mma_bf16(D2, on(mat, 2 * M2_BYTES + k * MN_STEP), on(R, k * MN_STEP), w1 | A_MN, 1);
-                    mma_bf16(D2, on(mat, k * MN_STEP), on(R, 2 * RU_IMG + k * MN_STEP), w1 | A_MN, 1);
-                    mma_bf16(D2 + NV, on(mat, k * MN_STEP), on(R, k * MN_STEP), w2 | A_MN, 1);
+                    const uint64_t T = on(mat, 2 * k * KQ_GROUP);
+                    mma_bf16(D2 + NV, on(T, M2_BYTES), on(R, k * MN_STEP), w2, k > 0);
+                    mma_bf16(D2, on(T, 2 * M2_BYTES), on(R, k * MN_STEP), w1, 1);
+                    mma_bf16(D2, T, on(R, 2 * RU_IMG + k * MN_STEP), w1, 1);
+                    mma_bf16(D2 + NV, T, on(R, k * MN_STEP), w2, 1);
                 }
                 mma_commit(&sb->d2);
                 if (!(ok = wait(&sb->y_ready, it & 1))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 2 * C / 16; ++k)
-                    mma_bf16(D3, on(cols, k * MN_STEP), on(k < 4 ? R : Y, k % 4 * MN_STEP), w3 | A_MN, k > 0);
+                for (int k = 0; k < 2 * C / 16; ++k)   // keys and queries in turn
+                    mma_bf16(D3, on(cols, k * KQ_GROUP), on(k % 2 ? Y : R, k / 2 * MN_STEP), w3 | A_MN, k > 0);
                 mma_commit(&sb->d3);
                 mma_commit(&sb->kq_empty[it & 1]);
             }
@@ -199,19 +192,18 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
     } else {
         // ---------------------------------------------------------- compute
         const int q = warp & 3, c0 = warp / 4 * 32, row = 32 * q + lane;
-        const bool keys = q < 2;
-        const int tk = row & 63;
+        const int t16 = 16 * q, ta = t16 + lane / 4, tb = ta + 8;   // tokens of a fragment's rows
         const uint32_t lanes = ((uint32_t)(32 * q) << 16) + c0;
         const uint32_t ops = smem_addr(smem + L::ops), go = smem_addr(smem + L::go), xs = smem_addr(smem + L::xs),
                        sin = smem_addr(smem + L::sin);
         const Meta *meta = reinterpret_cast<const Meta *>(smem + L::meta);
         const bool state = row < DK;
         const long long place = bh * DK * a.Dv + (long long)row * a.Dv + n0 + c0;   // this row in ds_last, ds0
-        f2 Z[16];
+        float Z[32];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float4 t = (a.ds_last && state) ? *reinterpret_cast<const float4 *>(a.ds_last + place + 4 * j) : make_float4(0, 0, 0, 0);
-            Z[2 * j] = make2(t.x, t.y), Z[2 * j + 1] = make2(t.z, t.w);
+            Z[4 * j] = t.x, Z[4 * j + 1] = t.y, Z[4 * j + 2] = t.z, Z[4 * j + 3] = t.w;
         }
         if (state) put3<32>(ops, L::S_IMG, row, c0, Z);
         hand_over(&sb->z_ready, lane);
@@ -221,70 +213,54 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
             bool ok = wait(&sb->sin_full, it & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (state) {
-                f2 w = both(0.0f);
+                float w = 0.0f, v = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const uint4 t = lds128(piece(sin + c0 / 32 * (DK * 128), row, j));
-                    w = fma2(make2(t.x, t.y), Z[2 * j], w);
-                    w = fma2(make2(t.z, t.w), Z[2 * j + 1], w);
+                    w = fmaf(__uint_as_float(t.x), Z[4 * j], w), v = fmaf(__uint_as_float(t.y), Z[4 * j + 1], v);
+                    w = fmaf(__uint_as_float(t.z), Z[4 * j + 2], w), v = fmaf(__uint_as_float(t.w), Z[4 * j + 3], v);
                 }
-                float s = lof(w) + hif(w);
-                for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-                if (lane == 0) a.inner[(bh * (N + 1) + c + 1) * a.parts + blockIdx.x * (DK / 16) + q * 2 + warp / 4] = s;
+                w += v;
+                for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
+                if (lane == 0) a.inner[(bh * (N + 1) + c + 1) * a.parts + blockIdx.x * (DK / 16) + q * 2 + warp / 4] = w;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb->sin_empty);
-            ok = wait(&sb->img_full, it & 1) && wait(&sb->d1, it & 1) && wait(&sb->z_left, it & 1) && (keys || wait(&sb->go_full, it & 1));
+            ok = wait(&sb->img_full, it & 1) && wait(&sb->go_full, it & 1) && wait(&sb->z_left, it & 1) && wait(&sb->d1, it & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            f2 x[16];
-            const f2 last = both(meta->last);
-            const float up = meta->up[tk], be = meta->beta[tk];
-            if (keys) {
-                const f2 down = both(meta->down[tk]);
-                load_parts<3, 32>(D1 + lanes, x);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = mul2(down, x[i]);
-                put3<32>(ops, RU_IMG, tk, c0, x);
-                hand_over(&sb->r_ready, lane);
-            } else {
-                const f2 w = both(a.scale * up);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 v = lds128(piece(go, tk, c0 / 8 + j));
-                    x[4 * j] = mul2(w, widen(v.x)), x[4 * j + 1] = mul2(w, widen(v.y));
-                    x[4 * j + 2] = mul2(w, widen(v.z)), x[4 * j + 3] = mul2(w, widen(v.w));
-                }
-                put3<32>(ops + 3 * RU_IMG, RU_IMG, tk, c0, x);
-                hand_over(&sb->y_ready, lane);
-            }
+            float f[16];
+            frag_load<3>(D1 + lanes, f);
+            frag_scale(f, meta->down[ta], meta->down[tb]);
+            frag_put3(ops, RU_IMG, t16, c0, lane, f);
+            hand_over(&sb->r_ready, lane);
+            const float last = meta->last, ua = meta->up[ta], ub = meta->up[tb];
+            const float ya = -ua * meta->beta[ta], yb = -ub * meta->beta[tb];
+            frag_get(go, t16, c0, lane, f);
+            frag_scale(f, a.scale * ua, a.scale * ub);
+            frag_put3(ops + 3 * RU_IMG, RU_IMG, t16, c0, lane, f);
             ok = wait(&sb->d2, it & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            if (lane == 0) {
-                mbar_arrive(&sb->img_empty);
-                if (!keys) mbar_arrive(&sb->go_empty);
-            }
-            if (keys) {
-                load_parts<3, 32>(D2 + lanes, x);
-                const f2 w = both(-up * be);
-                f2 y[16];
+            if (lane == 0) mbar_arrive(&sb->img_empty), mbar_arrive(&sb->go_empty);
+            frag_load<3>(D2 + lanes, f);
+            float y[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = mul2(w, x[i]);
-                put3<32>(ops, RU_IMG, tk, c0, y);
-                hand_over(&sb->y_ready, lane);
-                ok = it == 0 || wait(&sb->x_left, (it - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                put_row(xs + c0 / 32 * RU_IMG, tk, x);
-                hand_over(&sb->x_ready, lane);
-            }
+            for (int i = 0; i < 16; ++i) y[i] = f[i] * ((i & 2) ? yb : ya);
+            frag_put3(ops, RU_IMG, t16, c0, lane, y);
+            hand_over(&sb->y_ready, lane);
+            ok = it == 0 || wait(&sb->x_left, (it - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            frag_put_rows(xs + c0 / 32 * RU_IMG, t16, lane, f);
+            hand_over(&sb->x_ready, lane);
             ok = wait(&sb->d3, it & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             if (state) {
+                float x[32];
                 load_parts<3, 32>(D3 + lanes, x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) Z[i] = fma2(last, Z[i], x[i]);
+                for (int i = 0; i < 32; ++i) Z[i] = fmaf(last, Z[i], x[i]);
                 if (c > 0) put3<32>(ops, L::S_IMG, row, c0, Z);
             }
             if (c > 0) hand_over(&sb->z_ready, lane);
@@ -292,8 +268,7 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
         if (state && a.ds0)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<float4 *>(a.ds0 + place + 4 * j) =
-                    make_float4(lof(Z[2 * j]), hif(Z[2 * j]), lof(Z[2 * j + 1]), hif(Z[2 * j + 1]));
+                *reinterpret_cast<float4 *>(a.ds0 + place + 4 * j) = make_float4(Z[4 * j], Z[4 * j + 1], Z[4 * j + 2], Z[4 * j + 3]);
         tc_fence_before();
     }
     __syncthreads();
@@ -326,7 +301,7 @@ template <int DK, int DV> struct LocalSmem {
     static constexpr uint32_t A_IMG = 128 * 128 * (DV / 64);   // [dv; dO]
     static constexpr uint32_t U_IMG = 64 * 128 * (DV / 64);
     static constexpr uint32_t S_IMG = DK * 128 * (DV / 64);
-    static constexpr uint32_t kq = 0;
+    static constexpr uint32_t kq = 0;                          // 64 keys, then 64 queries
     static constexpr uint32_t a = kq + KQ;                     // two parts; [W; N], two parts, later
     static constexpr uint32_t u = a + 2 * A_IMG;
     static constexpr uint32_t s = u + 2 * U_IMG;               // Z, then S0: two parts
@@ -344,18 +319,18 @@ struct LocalBars {
     int abort;
 };
 
-// Eight values (pairs v) as a 16-byte piece of two images.
-__device__ __forceinline__ void put2(uint32_t img, uint32_t stride, int row, int j, const f2 (&v)[4]) {
+// Eight values as a 16-byte piece of two images.
+__device__ __forceinline__ void put2(uint32_t img, uint32_t stride, int row, int j, const float (&v)[8]) {
     uint32_t h[4], m[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split2(v[i], h[i], m[i]);
+    for (int i = 0; i < 4; ++i) split2(v[2 * i], v[2 * i + 1], h[i], m[i]);
     const uint32_t to = piece(img, row, j);
     sts128(to, h[0], h[1], h[2], h[3]);
     sts128(to + stride, m[0], m[1], m[2], m[3]);
 }
-__device__ __forceinline__ void load8(const float *p, f2 (&v)[4]) {
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
     const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = make2(x.x, x.y), v[1] = make2(x.z, x.w), v[2] = make2(y.x, y.y), v[3] = make2(y.z, y.w);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
 }
 
 template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_kernel(const Args a) {
@@ -400,9 +375,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
     const int row = 32 * (warp & 3) + lane, c0 = warp / 4 * 32, tk = row & 63;
     const bool keys = row < C;
     const uint32_t lanes = ((uint32_t)(32 * (warp & 3)) << 16) + c0;
-    f2 sum[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) sum[i] = both(0.0f);
+    float sum[32] = {};
     bool ok = true;
     for (int j = 0; j < group; ++j) {
         const int h = hk * group + j;
@@ -419,11 +392,8 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         for (int n = 0; n < C * PR / LT; ++n) {
             const int i = tid + n * LT, t = i / PR, d = i % PR * 8;
             const long long hv = (row0 + t) * a.Hv + h;
-            f2 x[4], e[4], o[4], w = both(0.0f), db = w;
+            float x[8] = {}, e[8] = {}, o[8] = {}, s1 = 0.0f, s2 = 0.0f, be = 0.0f;
             uint4 g = make_uint4(0, 0, 0, 0), v = g;
-            float be = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = e[k] = o[k] = w;
             if (t < nt) {
                 load8(a.x + hv * DV + d, x);
                 load8(a.e + hv * DV + d, e);
@@ -432,27 +402,24 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                 v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) + (row0 + t) * a.ldv + (long long)h * DV + d);
                 be = a.beta[hv];
             }
-            const f2 b2 = both(be), minus = both(-1.0f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                db = fma2(x[k], e[k], db);
-                x[k] = mul2(b2, x[k]), e[k] = mul2(b2, e[k]);
-                const uint32_t gk = k == 0 ? g.x : k == 1 ? g.y : k == 2 ? g.z : g.w, vk = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
-                w = fma2(o[k], widen(gk), w);
-                w = fma2(mul2(minus, widen(vk)), x[k], w);
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t gk = k < 2 ? g.x : k < 4 ? g.y : k < 6 ? g.z : g.w, vk = k < 2 ? v.x : k < 4 ? v.y : k < 6 ? v.z : v.w;
+                s1 = fmaf(x[k], e[k], s1);
+                x[k] *= be, e[k] *= be;
+                s2 = fmaf(o[k], k % 2 ? hi16(gk) : lo16(gk), s2);
+                s2 = fmaf(-(k % 2 ? hi16(vk) : lo16(vk)), x[k], s2);
             }
             const int box = d / 64, at = d % 64 / 8;
             put2(sA + box * M2_BYTES, L::A_IMG, t, at, x);
             put2(sU + box * RU_IMG, L::U_IMG, t, at, e);
             sts128(piece(sA + box * M2_BYTES, C + t, at), g.x, g.y, g.z, g.w);
             sts128(piece(sA + L::A_IMG + box * M2_BYTES, C + t, at), 0, 0, 0, 0);   // dO is bf16: no second part
-            float s1 = lof(db) + hif(db), s2 = lof(w) + hif(w);
 #pragma unroll
             for (int m = PR / 2; m > 0; m >>= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, m), s2 += __shfl_xor_sync(0xffffffffu, s2, m);
             if (t < nt) {
                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dv) + (row0 + t) * a.lddv + (long long)h * DV + d) =
-                    make_uint4(pack2(lof(x[0]), hif(x[0])), pack2(lof(x[1]), hif(x[1])), pack2(lof(x[2]), hif(x[2])),
-                               pack2(lof(x[3]), hif(x[3])));
+                    make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
                 if (d == 0) a.dbeta[hv] = s1, a.dots[hv] = s2;
             }
         }
@@ -493,13 +460,13 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         __syncwarp();
         ok = wait(&lb->first, j & 1) && wait(&lb->z_full, j & 1) && ok;
         tc_fence_after();
-        f2 x[16];
+        float x[32];
         if (c0 < 64) load_parts<1, 32>(D3 + lanes, x);
 #pragma unroll
         for (int n = 0; n < SN; ++n) {
             const int i = tid + n * LT, r = i / PR, d = i % PR * 8;
-            f2 v[4] = {make2(sr[2 * n].x, sr[2 * n].y), make2(sr[2 * n].z, sr[2 * n].w), make2(sr[2 * n + 1].x, sr[2 * n + 1].y),
-                       make2(sr[2 * n + 1].z, sr[2 * n + 1].w)};
+            const float v[8] = {sr[2 * n].x,     sr[2 * n].y,     sr[2 * n].z,     sr[2 * n].w,
+                                sr[2 * n + 1].x, sr[2 * n + 1].y, sr[2 * n + 1].z, sr[2 * n + 1].w};
             put2(sS + d / 64 * (DK * 128), L::S_IMG, r, d % 64 / 8, v);
         }
         fence_proxy_async_smem();
@@ -522,18 +489,10 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         if (c0 < 64) {   // [W; N]
             const float gh = meta->hi[tk], gl = meta->lo[tk];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float w[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int col = c0 + 2 * i + k;
-                    const bool in = keys ? col < tk : col <= tk;
-                    w[k] = in ? (keys ? -1.0f : a.scale) * expf((gh - meta->hi[col]) + (gl - meta->lo[col])) : 0.0f;
-                }
-                x[i] = mul2(make2(w[0], w[1]), x[i]);
-                // a masked product may be infinite or NaN where its factor is 0
-                if (keys ? c0 + 2 * i >= tk : c0 + 2 * i > tk) x[i] = both(0.0f);
-                else if (keys ? c0 + 2 * i + 1 >= tk : c0 + 2 * i + 1 > tk) x[i] = make2(lo32(x[i]), 0u);
+            for (int i = 0; i < 32; ++i) {
+                const int col = c0 + i;
+                const bool in = keys ? col < tk : col <= tk;   // a masked product may be infinite: it is not multiplied by 0
+                x[i] = in ? (keys ? -1.0f : a.scale) * expf((gh - meta->hi[col]) + (gl - meta->lo[col])) * x[i] : 0.0f;
             }
         }
         ok = wait(&lb->second, 0) && ok;   // [dv; dO] has been read
@@ -541,7 +500,8 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         if (c0 < 64)
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const f2 v[4] = {x[4 * n], x[4 * n + 1], x[4 * n + 2], x[4 * n + 3]};
+                const float v[8] = {x[8 * n],     x[8 * n + 1], x[8 * n + 2], x[8 * n + 3],
+                                    x[8 * n + 4], x[8 * n + 5], x[8 * n + 6], x[8 * n + 7]};
                 put2(sA, M2_BYTES, row, c0 / 8 + n, v);
             }
         fence_proxy_async_smem();
@@ -563,14 +523,14 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         __syncwarp();
         if (c0 < DK) {   // meanwhile what the earlier products give
             const float up = meta->up[tk];
-            const f2 w = both(keys ? -up : a.scale * up), down = both(meta->down[tk]);
+            const float w = keys ? -up : a.scale * up, down = meta->down[tk];
             load_parts<1, 32>(D1 + lanes, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[i] = fma2(w, x[i], sum[i]);
+            for (int i = 0; i < 32; ++i) sum[i] = fmaf(w, x[i], sum[i]);
             if (keys) {
                 load_parts<1, 32>(D2 + lanes, x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sum[i] = fma2(down, x[i], sum[i]);
+                for (int i = 0; i < 32; ++i) sum[i] = fmaf(down, x[i], sum[i]);
             }
         }
         ok = wait(&lb->second, 1) && ok;
@@ -578,11 +538,11 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         if (c0 < DK) {
             load_parts<1, 32>(D4 + lanes, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[i] = add2(x[i], sum[i]);
+            for (int i = 0; i < 32; ++i) sum[i] += x[i];
             if (keys) {
                 load_parts<1, 32>(D5 + lanes, x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sum[i] = add2(x[i], sum[i]);
+                for (int i = 0; i < 32; ++i) sum[i] += x[i];
             }
         }
         tc_fence_before();
@@ -595,8 +555,8 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4 *>(p + 8 * j) =
-                make_uint4(pack2(lof(sum[4 * j]), hif(sum[4 * j])), pack2(lof(sum[4 * j + 1]), hif(sum[4 * j + 1])),
-                           pack2(lof(sum[4 * j + 2]), hif(sum[4 * j + 2])), pack2(lof(sum[4 * j + 3]), hif(sum[4 * j + 3])));
+                make_uint4(pack2(sum[8 * j], sum[8 * j + 1]), pack2(sum[8 * j + 2], sum[8 * j + 3]),
+                           pack2(sum[8 * j + 4], sum[8 * j + 5]), pack2(sum[8 * j + 6], sum[8 * j + 7]));
     }
     if (!ok) settle_copies();
     __syncthreads();
@@ -612,8 +572,8 @@ template <int DK, int DV> cudaError_t launch_local(const Args &a, cudaStream_t s
 
 template <int DK> cudaError_t backward(const Args &a, cudaStream_t st) {
     AdjMaps m = {};
-    cudaError_t e = encode_rows(&m.k, false, a.k, a.ldk, a.B, a.L, a.Hk, DK);
-    if (e == cudaSuccess) e = encode_rows(&m.q, false, a.q, a.ldq, a.B, a.L, a.Hk, DK);
+    cudaError_t e = encode_rows(&m.k, false, a.k, a.ldk, a.B, a.L, a.Hk, DK, 16);
+    if (e == cudaSuccess) e = encode_rows(&m.q, false, a.q, a.ldq, a.B, a.L, a.Hk, DK, 16);
     if (e == cudaSuccess) e = encode_rows(&m.g, false, a.dout, a.lddo, a.B, a.L, a.Hv, a.Dv);
     if (e == cudaSuccess) e = encode_rows(&m.x, true, a.x, (long long)a.Hv * a.Dv, a.B, a.L, a.Hv, a.Dv);
     if (e == cudaSuccess) e = encode_states(&m.s, a.states, (long long)a.B * a.Hv * (chunks(a.L) + 1), DK, a.Dv);

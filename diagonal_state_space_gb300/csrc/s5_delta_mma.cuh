@@ -47,59 +47,33 @@ inline int fault_take() {
 }
 
 // ---------------------------------------------------------------------------
-// Pairs of 32-bit values in one 64-bit register (the low half is the first).
+// bf16 pairs and parts.
 // ---------------------------------------------------------------------------
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 make2(uint32_t lo, uint32_t hi) { return (f2)hi << 32 | lo; }
-__device__ __forceinline__ f2 make2(float lo, float hi) { return make2(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ f2 both(float x) { return make2(x, x); }
-__device__ __forceinline__ uint32_t lo32(f2 x) { return (uint32_t)x; }
-__device__ __forceinline__ uint32_t hi32(f2 x) { return (uint32_t)(x >> 32); }
-__device__ __forceinline__ float lof(f2 x) { return __uint_as_float(lo32(x)); }
-__device__ __forceinline__ float hif(f2 x) { return __uint_as_float(hi32(x)); }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-// Two bf16 values as two floats.
-__device__ __forceinline__ f2 widen(uint32_t v) { return make2(v << 16, v & 0xffff0000u); }
+__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 // Two floats rounded to bf16.
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-
 // Parts.  x = h + m + l with bf16 h, m, l: 8 significant bits each, cut off and
 // not rounded, so that three parts hold all 24 bits of a normal x and the
-// differences are exact.
-__device__ __forceinline__ uint32_t tops(f2 x) { return __byte_perm(lo32(x), hi32(x), 0x7632); }
-__device__ __forceinline__ f2 minus_tops(f2 x) {   // -(the tops' values), to be added
-    return make2((lo32(x) & 0xffff0000u) ^ 0x80000000u, (hi32(x) & 0xffff0000u) ^ 0x80000000u);
-}
-__device__ __forceinline__ void split3(f2 x, uint32_t &h, uint32_t &m, uint32_t &l) {
-    h = tops(x);
-    x = add2(x, minus_tops(x));
-    m = tops(x);
-    x = add2(x, minus_tops(x));
-    l = tops(x);
+// differences are exact.  Eleven instructions a pair, the least of the forms
+// measured (seven of them integer, at half rate: 15 cycles a pair and warp;
+// packed f32x2 differences need 24).
+__device__ __forceinline__ uint32_t tops(float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); }
+__device__ __forceinline__ float rest(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
+__device__ __forceinline__ void split3(float a, float b, uint32_t &h, uint32_t &m, uint32_t &l) {
+    h = tops(a, b);
+    a = rest(a), b = rest(b);
+    m = tops(a, b);
+    l = tops(rest(a), rest(b));
 }
 // Two parts, the second rounded: 17 bits.
-__device__ __forceinline__ void split2(f2 x, uint32_t &h, uint32_t &m) {
-    h = tops(x);
-    x = add2(x, minus_tops(x));
-    m = pack2(lof(x), hif(x));
+__device__ __forceinline__ void split2(float a, float b, uint32_t &h, uint32_t &m) {
+    h = tops(a, b);
+    m = pack2(rest(a), rest(b));
 }
 
 // ---------------------------------------------------------------------------
@@ -117,14 +91,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
-// W values (pairs v) of a row from column c0 on, as three images `stride`
-// bytes apart.
-template <int W> __device__ __forceinline__ void put3(uint32_t img, uint32_t stride, int row, int c0, const f2 *v) {
+// W values of a row from column c0 on, as three images `stride` bytes apart.
+template <int W> __device__ __forceinline__ void put3(uint32_t img, uint32_t stride, int row, int c0, const float *v) {
 #pragma unroll
     for (int j = 0; j < W / 8; ++j) {
         uint32_t h[4], m[4], l[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split3(v[4 * j + i], h[i], m[i], l[i]);
+        for (int i = 0; i < 4; ++i) split3(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], h[i], m[i], l[i]);
         const uint32_t to = piece(img, row, c0 / 8 + j);
         sts128(to, h[0], h[1], h[2], h[3]);
         sts128(to + stride, m[0], m[1], m[2], m[3]);
@@ -132,10 +105,76 @@ template <int W> __device__ __forceinline__ void put3(uint32_t img, uint32_t str
     }
 }
 // 32 floats as the 128-byte row of a staged tile.
-__device__ __forceinline__ void put_row(uint32_t tile, int row, const f2 *v) {
+__device__ __forceinline__ void put_row(uint32_t tile, int row, const float *v) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        sts128(piece(tile, row, j), lo32(v[2 * j]), hi32(v[2 * j]), lo32(v[2 * j + 1]), hi32(v[2 * j + 1]));
+        sts128(piece(tile, row, j), __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+               __float_as_uint(v[4 * j + 3]));
+}
+
+// ---------------------------------------------------------------------------
+// Fragments: 16 rows x 32 columns over a warp, f[4 j + 2 i + k] = row
+// lane / 4 + 8 i, column 8 j + 2 (lane % 4) + k: what the 16-lane TMEM loads
+// give and the 8 x 8 matrix stores and loads take.  The tokens of a chunk lie
+// 16 to a warp's 32 TMEM lanes, so that all warps share their conversion.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t frag_addr(uint32_t img, int row0, int c0, int j, int lane) {
+    return piece(img, row0 + (lane & 15), c0 / 8 + j + (lane >> 4));
+}
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// Rows row0 .. row0 + 15, columns c0 .. c0 + 31 as three images.
+__device__ __forceinline__ void frag_put3(uint32_t img, uint32_t stride, int row0, int c0, int lane, const float (&f)[16]) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        uint32_t h[4], m[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split3(f[4 * j + 2 * i], f[4 * j + 2 * i + 1], h[i], m[i], l[i]);
+        const uint32_t to = frag_addr(img, row0, c0, j, lane);
+        stmatrix4(to, h[0], h[1], h[2], h[3]);
+        stmatrix4(to + stride, m[0], m[1], m[2], m[3]);
+        stmatrix4(to + 2 * stride, l[0], l[1], l[2], l[3]);
+    }
+}
+// The same rows and columns of a bf16 tile, as floats; and rounded to one.
+__device__ __forceinline__ void frag_get(uint32_t tile, int row0, int c0, int lane, float (&f)[16]) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        uint32_t r[4];
+        ldmatrix4(frag_addr(tile, row0, c0, j, lane), r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[4 * j + 2 * i] = lo16(r[i]), f[4 * j + 2 * i + 1] = hi16(r[i]);
+    }
+}
+__device__ __forceinline__ void frag_round(uint32_t tile, int row0, int c0, int lane, const float (&f)[16]) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2)
+        stmatrix4(frag_addr(tile, row0, c0, j, lane), pack2(f[4 * j], f[4 * j + 1]), pack2(f[4 * j + 2], f[4 * j + 3]),
+                  pack2(f[4 * j + 4], f[4 * j + 5]), pack2(f[4 * j + 6], f[4 * j + 7]));
+}
+// In 32 bits: 32 columns are the tile's whole row.
+__device__ __forceinline__ void frag_put_rows(uint32_t tile, int row0, int lane, const float (&f)[16]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(piece(tile, row0 + lane / 4 + 8 * i, 2 * j + lane % 4 / 2) +
+                                                                 (lane & 1) * 8u),
+                         "f"(f[4 * j + 2 * i]), "f"(f[4 * j + 2 * i + 1])
+                         : "memory");
+}
+// f's rows times a (lane / 4) and b (lane / 4 + 8).
+__device__ __forceinline__ void frag_scale(float (&f)[16], float a, float b) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] *= (i & 2) ? b : a;
 }
 
 // ---------------------------------------------------------------------------
@@ -143,23 +182,44 @@ __device__ __forceinline__ void put_row(uint32_t tile, int row, const f2 *v) {
 // ---------------------------------------------------------------------------
 constexpr int NV = 64;                       // value columns of a slice
 
-__device__ __forceinline__ void tmem_ldw(uint32_t addr, uint32_t (&r)[8]) { tmem_ld8(addr, r); }
 __device__ __forceinline__ void tmem_ldw(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
 __device__ __forceinline__ void tmem_ldw(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
-// W columns as W / 2 pairs: the sum of P column blocks, 64 apart, one for each
-// part of a split operand.
-template <int P, int W> __device__ __forceinline__ void load_parts(uint32_t addr, f2 *v) {
+// W columns of this thread's lane: the sum of P column blocks, 64 apart, one
+// for each part of a split operand.
+template <int P, int W> __device__ __forceinline__ void load_parts(uint32_t addr, float *v) {
     uint32_t r[P][W];
 #pragma unroll
     for (int p = 0; p < P; ++p) tmem_ldw(addr + p * NV, r[p]);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-        v[i] = make2(r[P - 1][2 * i], r[P - 1][2 * i + 1]);
+    for (int i = 0; i < W; ++i) {
+        v[i] = __uint_as_float(r[P - 1][i]);
 #pragma unroll
-        for (int p = P - 2; p >= 0; --p) v[i] = add2(v[i], make2(r[p][2 * i], r[p][2 * i + 1]));
+        for (int p = P - 2; p >= 0; --p) v[i] += __uint_as_float(r[p][i]);
     }
 }
+// 16 lanes x 32 columns as a fragment.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+template <int P> __device__ __forceinline__ void frag_load(uint32_t addr, float (&f)[16]) {
+    uint32_t r[P][16];
+#pragma unroll
+    for (int p = 0; p < P; ++p) tmem_ld_frag(addr + p * NV, r[p]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        f[i] = __uint_as_float(r[P - 1][i]);
+#pragma unroll
+        for (int p = P - 2; p >= 0; --p) f[i] += __uint_as_float(r[p][i]);
+    }
+}
+constexpr uint32_t QUERY_LANES = 16u << 16;   // the query rows' lanes, past the key rows'
 
 // ---------------------------------------------------------------------------
 // Operand descriptors.
@@ -183,7 +243,10 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t base, uint32_t far) { retur
 __device__ __forceinline__ uint64_t on(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 constexpr uint32_t K_STEP = 32, MN_STEP = 2048;
 constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;
-constexpr uint32_t KQ_BOX = 128 * 128;       // 128 rows (64 keys, 64 queries) of 64 values
+// 128 rows of 64 values: 16 keys, 16 queries, 16 keys, ...; a chunk's matrix
+// [E; P beta E] has its rows in the same order.
+constexpr uint32_t KQ_BOX = 128 * 128;
+constexpr uint32_t KQ_GROUP = 16 * 128;      // 16 of those rows
 constexpr uint32_t RU_IMG = 64 * 128;        // one part of a 64 x 64 operand
 
 // ---------------------------------------------------------------------------
@@ -205,6 +268,19 @@ __device__ __forceinline__ void tma_store_4d(const void *tmap, const void *src, 
                      reinterpret_cast<uint64_t>(tmap)),
                  "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(src))
                  : "memory");
+}
+// The keys and queries of a chunk, as DK / 64 boxes of interleaved rows.
+template <int DK>
+__device__ __forceinline__ void load_chunk_rows(unsigned char *to, const void *k, const void *q, int hk, int t0, int b,
+                                                uint64_t *bar) {
+    mbar_arrive_tx(bar, DK / 64 * KQ_BOX);
+#pragma unroll 1
+    for (int x = 0; x < DK / 64; ++x)
+#pragma unroll 1
+        for (int i = 0; i < C / 16; ++i) {
+            tma_load_4d(to + x * KQ_BOX + 2 * i * KQ_GROUP, k, 64 * x, hk, t0 + 16 * i, b, bar);
+            tma_load_4d(to + x * KQ_BOX + (2 * i + 1) * KQ_GROUP, q, 64 * x, hk, t0 + 16 * i, b, bar);
+        }
 }
 // True once the phase is over; false once a wait of the block has run out
 // (2 s): the block then ends without waiting further, and the host is told.
@@ -245,7 +321,7 @@ __device__ __forceinline__ void hand_over(uint64_t *bar, int lane) {
 
 // ---------------------------------------------------------------------------
 // Tensor maps.  Rows [B][L][H][D] with a pitch between tokens, in boxes of 64
-// tokens x 128 bytes of one head; tokens past L read as zeros and are not
+// (or fewer) tokens x 128 bytes of one head; tokens past L read as zeros and are not
 // written.
 // ---------------------------------------------------------------------------
 inline cudaError_t encode(CUtensorMap *m, bool f32, int rank, const void *p, const cuuint64_t *dims, const cuuint64_t *strides,
@@ -266,11 +342,12 @@ inline cudaError_t encode(CUtensorMap *m, bool f32, int rank, const void *p, con
                ? cudaSuccess
                : cudaErrorInvalidValue;
 }
-inline cudaError_t encode_rows(CUtensorMap *m, bool f32, const void *p, long long ld, int B, int L, int H, int D) {
+inline cudaError_t encode_rows(CUtensorMap *m, bool f32, const void *p, long long ld, int B, int L, int H, int D,
+                               int tokens = C) {
     const cuuint64_t e = f32 ? 4 : 2;
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)L, (cuuint64_t)B};
     const cuuint64_t strides[3] = {(cuuint64_t)D * e, (cuuint64_t)ld * e, (cuuint64_t)ld * e * L};
-    const cuuint32_t box[4] = {f32 ? 32u : 64u, 1, 64, 1};
+    const cuuint32_t box[4] = {f32 ? 32u : 64u, 1, (cuuint32_t)tokens, 1};
     return encode(m, f32, 4, p, dims, strides, box);
 }
 // Matrices [n][Dk][Dv] of floats in boxes of Dk rows x 32 columns.

@@ -20,7 +20,7 @@ namespace {
 //   [[A, 0], [B, D]]^-1 = [[A^-1, 0], [-D^-1 B A^-1, D^-1]]
 // to 32 and to 64 rows.  P E is a product of two triangular 64 x 64 matrices
 // in three bf16 parts each (mma.sync, the 20 of 64 block products that are not
-// zero).  The whole image is built in shared memory in the layout that the
+// zero).  In the image 16 rows of E and 16 of P E take turns.  The whole image is built in shared memory in the layout that the
 // recurrences' products read, and leaves by one bulk copy.
 //
 // TRANS: (I + strict lower(beta_i D_ij k_i.k_j))^-1 = T and [T; P T] instead,
@@ -45,12 +45,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         "%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
 }
 __device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -107,11 +101,11 @@ template <int DK, bool TRANS> __global__ void __launch_bounds__(PT, 3) delta_pre
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[n][i] *= a.scale;
     }
-    // rows 64..127 of the image: three parts of two neighbouring values
+    // row r of the image's lower matrix: three parts of two neighbouring values
     auto put2 = [&](int r, int n, float x, float y) {
         uint32_t h, m, l;
-        split3(make2(x, y), h, m, l);
-        unsigned char *to = img + (C + r) * 128 + ((n ^ (r & 7)) << 4) + q2 * 2;
+        split3(x, y, h, m, l);
+        unsigned char *to = img + (2 * r - (r & 15) + 16) * 128 + ((n ^ (r & 7)) << 4) + q2 * 2;
         *reinterpret_cast<uint32_t *>(to) = h;
         *reinterpret_cast<uint32_t *>(to + M2_BYTES) = m;
         *reinterpret_cast<uint32_t *>(to + 2 * M2_BYTES) = l;
@@ -250,11 +244,11 @@ template <int DK, bool TRANS> __global__ void __launch_bounds__(PT, 3) delta_pre
                 y = *reinterpret_cast<const float4 *>(&A[r][8 * ch + 4]);
             }
             uint32_t hh[4], mm[4], ll[4];
-            split3(make2(x.x, x.y), hh[0], mm[0], ll[0]);
-            split3(make2(x.z, x.w), hh[1], mm[1], ll[1]);
-            split3(make2(y.x, y.y), hh[2], mm[2], ll[2]);
-            split3(make2(y.z, y.w), hh[3], mm[3], ll[3]);
-            unsigned char *to = img + r * 128 + ((ch ^ (r & 7)) << 4);
+            split3(x.x, x.y, hh[0], mm[0], ll[0]);
+            split3(x.z, x.w, hh[1], mm[1], ll[1]);
+            split3(y.x, y.y, hh[2], mm[2], ll[2]);
+            split3(y.z, y.w, hh[3], mm[3], ll[3]);
+            unsigned char *to = img + (2 * r - (r & 15)) * 128 + ((ch ^ (r & 7)) << 4);
             *reinterpret_cast<uint4 *>(to) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
             *reinterpret_cast<uint4 *>(to + M2_BYTES) = make_uint4(mm[0], mm[1], mm[2], mm[3]);
             *reinterpret_cast<uint4 *>(to + 2 * M2_BYTES) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
@@ -267,7 +261,7 @@ template <int DK, bool TRANS> __global__ void __launch_bounds__(PT, 3) delta_pre
             const int cb = 2 * (warp >> 2) + jb;       // block of 16 columns
             for (int kb = cb; kb <= rb; ++kb) {
                 uint32_t fa[3][4], fb[3][4];
-                const int r = C + 16 * rb + (lane & 15), m = 16 * kb + (lane & 15);
+                const int r = 32 * rb + 16 + (lane & 15), m = 32 * kb + (lane & 15);
 #pragma unroll
                 for (int p = 0; p < 3; ++p) {
                     ldmatrix4(simg + p * M2_BYTES + r * 128 + (((2 * kb + (lane >> 4)) ^ (r & 7)) << 4), fa[p]);

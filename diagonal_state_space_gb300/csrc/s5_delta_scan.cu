@@ -14,8 +14,9 @@
 //   D1 = [K; Q] S0        (128 x 64, depth Dk)
 //   D2 = [E; P beta E] R  (128 x 64, depth 64)
 //   D3 = K^T U            (Dk x 64, depth 64)
-// all of M = 128: the rows 64..127 of the first two give the outputs beside
-// the rows that the recurrence needs.
+// all of M = 128: half the rows of the first two give the outputs beside the
+// rows that the recurrence needs, 16 of each in turn, so that every warp's 32
+// accumulator lanes hold 16 tokens of either.
 //
 // Precision.  Keys, queries and values are bf16 and enter the products as they
 // are.  S0, R, U and [E; P beta E] are 32-bit values, carried as sums of three
@@ -88,8 +89,8 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sb->kq_full[i], 1), mbar_init(&sb->kq_empty[i], 1);
             mbar_init(&sb->d1[i], 1), mbar_init(&sb->d2[i], 1), mbar_init(&sb->d3[i], 1);
-            mbar_init(&sb->s_ready[i], 8), mbar_init(&sb->r_ready[i], 4), mbar_init(&sb->u_ready[i], 8);
-            mbar_init(&sb->v_full[i], 1), mbar_init(&sb->o_ready[i], 4);
+            mbar_init(&sb->s_ready[i], 8), mbar_init(&sb->r_ready[i], 8), mbar_init(&sb->u_ready[i], 8);
+            mbar_init(&sb->v_full[i], 1), mbar_init(&sb->o_ready[i], 8);
         }
         mbar_init(&sb->img_full, 1), mbar_init(&sb->img_empty, 8 * SL);
         mbar_init(&sb->state_staged, 8), mbar_init(&sb->rows_staged, 8), mbar_init(&sb->stage_free, 1);
@@ -115,14 +116,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
         if (warp == COPY_WARP && lane == 0) {
             // ------------------------------------------------------ copies
             auto load_kq = [&](int c) {
-                unsigned char *to = smem + L::kq + (c & 1) * L::KQ;
-                uint64_t *bar = &sb->kq_full[c & 1];
-                mbar_arrive_tx(bar, L::KQ);
-#pragma unroll
-                for (int x = 0; x < DK / 64; ++x) {
-                    tma_load_4d(to + x * KQ_BOX, &maps.k, 64 * x, hk, c * C, b, bar);
-                    tma_load_4d(to + x * KQ_BOX + KQ_BOX / 2, &maps.q, 64 * x, hk, c * C, b, bar);
-                }
+                load_chunk_rows<DK>(smem + L::kq + (c & 1) * L::KQ, &maps.k, &maps.q, hk, c * C, b, &sb->kq_full[c & 1]);
             };
             auto load_img = [&](int c) {
                 const unsigned char *from = static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES;
@@ -240,10 +234,10 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k) {
                         if constexpr (P1 == 3) {
-                            mma_bf16(d, on(cols, k * MN_STEP), on(U, k * MN_STEP), w3 | A_MN, k > 0);
+                            mma_bf16(d, on(cols, 2 * k * KQ_GROUP), on(U, k * MN_STEP), w3 | A_MN, k > 0);
                         } else {
-                            mma_bf16(d, on(cols, k * MN_STEP), on(U, k * MN_STEP), w2 | A_MN, k > 0);
-                            mma_bf16(d, on(cols, k * MN_STEP), on(U, 2 * RU_IMG + k * MN_STEP), w1 | A_MN, 1);
+                            mma_bf16(d, on(cols, 2 * k * KQ_GROUP), on(U, k * MN_STEP), w2 | A_MN, k > 0);
+                            mma_bf16(d, on(cols, 2 * k * KQ_GROUP), on(U, 2 * RU_IMG + k * MN_STEP), w1 | A_MN, 1);
                         }
                     }
                     mma_commit(&sb->d3[s]);
@@ -256,22 +250,22 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
     } else {
         // ---------------------------------------------------------- compute
         // Eight warps a slice; warp w: TMEM lanes 32 (w % 4) on, columns
-        // 32 (w / 4) on.  Lanes 0..63 are tokens of R, e and U, lanes 64..127
-        // tokens of o; in D3 and in the state a lane is a key index.
+        // 32 (w / 4) on.  In D1 and D2 its first 16 lanes are tokens of R and
+        // e, the others tokens of o; in D3 and in the state a lane is a key
+        // index.
         const int s = warp / 8, q = warp & 3, c0 = warp % 8 / 4 * 32, row = 32 * q + lane;
-        const bool keys = q < 2;                 // R, U rows; else o rows
-        const int tk = row & 63;                 // token in the chunk
+        const int t16 = 16 * q, ta = t16 + lane / 4, tb = ta + 8;   // tokens of a fragment's rows
         const uint32_t acc = tmem + s * SLICE + ((uint32_t)(32 * q) << 16) + c0;
         const uint32_t ops = smem_addr(smem + L::ops + s * L::OPS), vo = smem_addr(smem + L::vo + s * RU_IMG);
         const uint32_t stage = smem_addr(smem + L::stage);
         const Meta *meta = reinterpret_cast<const Meta *>(smem + L::meta);
         const bool state = row < DK;
         const long long place = bh * DK * a.Dv + (long long)row * a.Dv + n0 + s * NV + c0;   // this row in s0, s_last
-        f2 S[16];
+        float S[32];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float4 t = (a.s0 && state) ? *reinterpret_cast<const float4 *>(a.s0 + place + 4 * j) : make_float4(0, 0, 0, 0);
-            S[2 * j] = make2(t.x, t.y), S[2 * j + 1] = make2(t.z, t.w);
+            S[4 * j] = t.x, S[4 * j + 1] = t.y, S[4 * j + 2] = t.z, S[4 * j + 3] = t.w;
         }
         if (state) put3<32>(ops, L::S_IMG, row, c0, S);
         hand_over(&sb->s_ready[s], lane);
@@ -280,69 +274,44 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
             hand_over(&sb->state_staged, lane);
         }
         for (int c = 0; c < N; ++c) {
-            bool ok = wait(&sb->img_full, c & 1) && wait(&sb->d1[s], c & 1) && (!keys || wait(&sb->v_full[s], c & 1));
+            bool ok = wait(&sb->img_full, c & 1) && wait(&sb->v_full[s], c & 1) && wait(&sb->d1[s], c & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            f2 x[16];
-            if (keys) {
-                const f2 up = both(-meta->up[tk]);
+            float f[16], o[16];
+            const float ua = meta->up[ta], ub = meta->up[tb];
+            {   // R
+                frag_get(vo, t16, c0, lane, o);
+                frag_load<P1>(acc + D1, f);
 #pragma unroll
-                for (int w = 0; w < 32; w += W) {
-                    load_parts<P1, W>(acc + D1 + w, x);
-#pragma unroll
-                    for (int j = 0; j < W / 8; ++j) {
-                        const uint4 v = lds128(piece(vo, tk, (c0 + w) / 8 + j));
-                        x[4 * j] = fma2(up, x[4 * j], widen(v.x)), x[4 * j + 1] = fma2(up, x[4 * j + 1], widen(v.y));
-                        x[4 * j + 2] = fma2(up, x[4 * j + 2], widen(v.z)), x[4 * j + 3] = fma2(up, x[4 * j + 3], widen(v.w));
-                    }
-                    put3<W>(ops, RU_IMG, tk, c0 + w, x);
-                }
+                for (int i = 0; i < 16; ++i) f[i] = fmaf(-((i & 2) ? ub : ua), f[i], o[i]);
+                frag_put3(ops, RU_IMG, t16, c0, lane, f);
                 hand_over(&sb->r_ready[s], lane);
-            } else {
-                const f2 up = both(a.scale * meta->up[tk]);
-#pragma unroll
-                for (int w = 0; w < 32; w += W) {
-                    load_parts<P1, W>(acc + D1 + w, x + w / 2);
-#pragma unroll
-                    for (int i = 0; i < W / 2; ++i) x[w / 2 + i] = mul2(up, x[w / 2 + i]);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sb->u_ready[s]);   // D1 has been read
             }
-            const f2 ud = both(meta->beta[tk] * meta->down[tk]), last = both(meta->last);
+            const float da = meta->beta[ta] * meta->down[ta], db = meta->beta[tb] * meta->down[tb], last = meta->last;
+            frag_load<P1>(acc + D1 + QUERY_LANES, o);
+            frag_scale(o, a.scale * ua, a.scale * ub);
             ok = wait(&sb->d2[s], c & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             if (lane == 0) mbar_arrive(&sb->img_empty);   // D2 is done with the matrix, this warp with its factors
-            if (keys) {
-                f2 u[W / 2];
+            {   // e, U
+                frag_load<2>(acc + D2, f);
+                float u[16];
 #pragma unroll
-                for (int w = 0; w < 32; w += W) {
-                    load_parts<2, W>(acc + D2 + w, x);
-#pragma unroll
-                    for (int i = 0; i < W / 2; ++i) u[i] = mul2(ud, x[i]);
-                    put3<W>(ops, RU_IMG, tk, c0 + w, u);
-                }
+                for (int i = 0; i < 16; ++i) u[i] = f[i] * ((i & 2) ? db : da);
+                frag_put3(ops, RU_IMG, t16, c0, lane, u);
                 hand_over(&sb->u_ready[s], lane);
-            } else {
+                frag_load<2>(acc + D2 + QUERY_LANES, u);
 #pragma unroll
-                for (int w = 0; w < 32; w += W) {
-                    f2 y[W / 2];
-                    load_parts<2, W>(acc + D2 + w, y);
-#pragma unroll
-                    for (int i = 0; i < W / 2; ++i) x[w / 2 + i] = add2(x[w / 2 + i], y[i]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sts128(piece(vo, tk, c0 / 8 + j), pack2(lof(x[4 * j]), hif(x[4 * j])), pack2(lof(x[4 * j + 1]), hif(x[4 * j + 1])),
-                           pack2(lof(x[4 * j + 2]), hif(x[4 * j + 2])), pack2(lof(x[4 * j + 3]), hif(x[4 * j + 3])));
+                for (int i = 0; i < 16; ++i) o[i] += u[i];
+                frag_round(vo, t16, c0, lane, o);
                 hand_over(&sb->o_ready[s], lane);
             }
-            if constexpr (KEEP) {   // e from the key rows, o from the query rows
+            if constexpr (KEEP) {
                 ok = wait(&sb->stage_free, 0);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                put_row(stage + (keys ? 0 : 2 * RU_IMG) + c0 / 32 * RU_IMG, tk, x);
+                frag_put_rows(stage + c0 / 32 * RU_IMG, t16, lane, f);
+                frag_put_rows(stage + (2 + c0 / 32) * RU_IMG, t16, lane, o);
                 hand_over(&sb->rows_staged, lane);
             }
             ok = wait(&sb->d3[s], c & 1);
@@ -351,11 +320,11 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
             if (state) {
 #pragma unroll
                 for (int w = 0; w < 32; w += W) {
-                    f2 y[W / 2];
+                    float y[W];
                     load_parts<P1, W>(acc + D3 + w, y);
 #pragma unroll
-                    for (int i = 0; i < W / 2; ++i) S[w / 2 + i] = fma2(last, S[w / 2 + i], y[i]);
-                    if (c + 1 < N) put3<W>(ops, L::S_IMG, row, c0 + w, S + w / 2);
+                    for (int i = 0; i < W; ++i) S[w + i] = fmaf(last, S[w + i], y[i]);
+                    if (c + 1 < N) put3<W>(ops, L::S_IMG, row, c0 + w, S + w);
                 }
             }
             if (c + 1 < N) hand_over(&sb->s_ready[s], lane);
@@ -369,8 +338,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
         if (state && a.s_last)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<float4 *>(a.s_last + place + 4 * j) =
-                    make_float4(lof(S[2 * j]), hif(S[2 * j]), lof(S[2 * j + 1]), hif(S[2 * j + 1]));
+                *reinterpret_cast<float4 *>(a.s_last + place + 4 * j) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
         tc_fence_before();
     }
     __syncthreads();
@@ -388,8 +356,8 @@ template <int DK, int SL, bool KEEP> cudaError_t launch(const ScanMaps &m, const
 
 template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
     ScanMaps m = {};
-    cudaError_t e = encode_rows(&m.k, false, a.k, a.ldk, a.B, a.L, a.Hk, DK);
-    if (e == cudaSuccess) e = encode_rows(&m.q, false, a.q, a.ldq, a.B, a.L, a.Hk, DK);
+    cudaError_t e = encode_rows(&m.k, false, a.k, a.ldk, a.B, a.L, a.Hk, DK, 16);
+    if (e == cudaSuccess) e = encode_rows(&m.q, false, a.q, a.ldq, a.B, a.L, a.Hk, DK, 16);
     if (e == cudaSuccess) e = encode_rows(&m.v, false, a.v, a.ldv, a.B, a.L, a.Hv, a.Dv);
     if (e == cudaSuccess) e = encode_rows(&m.o, false, a.o, a.ldo, a.B, a.L, a.Hv, a.Dv);
     if (a.states) {
