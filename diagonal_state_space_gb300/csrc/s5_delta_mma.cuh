@@ -12,6 +12,7 @@ namespace s5 {
 namespace delta {
 
 cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st);   // s5_delta_prep.cu
+int prep_fault_take();
 int scan_fault_take();                                                     // s5_delta_scan.cu
 int adjoint_fault_take();                                                  // s5_delta_adjoint.cu
 

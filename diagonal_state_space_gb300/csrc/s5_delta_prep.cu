@@ -1,239 +1,286 @@
 // s5_delta_prep.cu -- what a chunk of the gated delta rule needs besides its
-// state, for all chunks at once (s5_delta_scan.cu has the mathematics).
+// state, for all chunks at once (s5_delta_scan.cu has the mathematics): one
+// CTA per chunk and key head, over the key head's value heads.
+//
+// k_i.k_j and q_i.k_j are one tcgen05 product [K; Q] K^T, taken once and kept
+// in registers.  Decay factors D_ij of two different blocks of 16 tokens are
+// products e^{G_i - G_b} e^{G_b - G_j} at the end b of j's block (both at most
+// 1 where g <= 0); inside a block each is an exponential of its own.
+//
+// The inverse goes by blocks, in place and in 32 bits on the CUDA cores (a
+// split product would cost more in conversions): the four 16 x 16 blocks on
+// the diagonal by substitution, one column per lane, then
+//   [[A, 0], [B, D]]^-1 = [[A^-1, 0], [-D^-1 B A^-1, D^-1]]
+// to 32 and to 64 rows.  P E is a tcgen05 product of the image's own parts:
+// [E; P] E, of which the rows of P E are kept.  In a forward image that only
+// makes o (bf16) 17 bits (without the third parts) do; all 24 are taken where o is kept
+// in 32 bits or X hangs on it.
+// In the image 16 rows of E and 16 of P E take turns; it is built in shared
+// memory in the layout that the recurrences' products read and leaves by one
+// bulk copy.
+//
+// TRANS: T = (I + strict lower(beta_i D_ij k_i.k_j))^-1 and [T; P T] instead,
+// which the backward pass uses.
+//
+// Bound: the 50 KB image written per chunk and value head, and the latency of
+// the block steps, which three CTAs an SM cover for one another.
 #include "s5_delta_mma.cuh"
 
 namespace s5 {
 namespace delta {
 namespace {
 
-// ---------------------------------------------------------------------------
-// One CTA per chunk and key head; the products k.k and q.k are
-// taken once (mma.sync, exact bf16 operands) and stay in registers for the
-// key head's value heads.
-//
-// Decay factors D_ij of two different blocks of 16 tokens are products
-// e^{G_i - G_b} e^{G_b - G_j} at the end b of j's block (both at most 1 where
-// g <= 0); inside a block each is an exponential of its own.
-//
-// The inverse goes by blocks, in place and in 32 bits: the four 16 x 16 blocks
-// on the diagonal by substitution (one column per lane), then
-//   [[A, 0], [B, D]]^-1 = [[A^-1, 0], [-D^-1 B A^-1, D^-1]]
-// to 32 and to 64 rows.  P E is a product of two triangular 64 x 64 matrices
-// in three bf16 parts each (mma.sync, the 20 of 64 block products that are not
-// zero).  In the image 16 rows of E and 16 of P E take turns.  The whole image is built in shared memory in the layout that the
-// recurrences' products read, and leaves by one bulk copy.
-//
-// TRANS: (I + strict lower(beta_i D_ij k_i.k_j))^-1 = T and [T; P T] instead,
-// which the backward pass uses.
-// ---------------------------------------------------------------------------
-constexpr int PT = 256;             // threads
-constexpr int LD = 68;              // pitch of the fp32 tile: 16-byte rows, no conflicts on 8 rows of 4
+constexpr int PT = 256;   // threads
+constexpr int LD = 68;    // pitch of the fp32 tile: 16-byte rows, conflict-free on 8 rows of 4 values
+constexpr int TD = 20;    // pitch of a transposed diagonal block
 
-template <int DK> struct PrepSmem {
-    static constexpr int KP = DK + 8;                    // bf16 pitch of the tiles: conflict-free fragments
-    static constexpr uint32_t tiles = 2 * C * KP * 2;    // keys and queries, before the image
-    static constexpr uint32_t a = IMG_BYTES;             // [64][LD] fp32, after the image (and the tiles)
-    static constexpr uint32_t near = a + C * LD * 4;     // e^{G_b - G_j}
-    static constexpr uint32_t total = near + C * 4;
-    static_assert(tiles <= IMG_BYTES, "the tiles lie in the image's place");
+struct PrepMaps {
+    CUtensorMap k16, q16, k64;   // boxes of 16 and of 64 tokens
 };
 
-// mma.sync m16n8k16: D += A B.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+template <int DK> struct PrepSmem {
+    static constexpr uint32_t KQ = KQ_BOX * (DK / 64), K = 64 * 128 * (DK / 64);
+    // the image, and before it the tiles: [K; Q] in turns, then K
+    static constexpr uint32_t a = MAT_BYTES;                 // [64][LD]: the system, its inverse in its place
+    static constexpr uint32_t td = a + C * LD * 4;           // diagonal blocks, transposed
+    static constexpr uint32_t meta = td + 4 * 16 * TD * 4;   // this head's and the next one's factors
+    static constexpr uint32_t near = meta + 2 * META_BYTES;  // e^{G_b - G_j}, twice
+    static constexpr uint32_t bars = near + 2 * C * 4;
+    static constexpr uint32_t total = bars + 64 + 1024;
+    static_assert(KQ + K <= MAT_BYTES, "the tiles lie in the image's place");
+};
+
+struct PrepBars {
+    uint64_t tiles, done;
+    uint32_t tmem;
+    int abort;
+};
+
+// (hi, lo) += (bh, bl): sums of floats with 46 bits.
+__device__ __forceinline__ void add_pair(float &hi, float &lo, float bh, float bl) {
+    const float s = hi + bh, t = s - hi, e = (hi - (s - t)) + (bh - t);
+    const float l = lo + bl + e;
+    hi = s + l;
+    lo = l - (hi - s);
 }
 
-template <int DK, bool TRANS> __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const Args a) {
+// One warp: the factors of a chunk and value head.  G_i is summed in pairs of
+// floats, so that a small difference of large sums keeps 24 bits.
+__device__ __forceinline__ void chunk_factors(const Args &a, long long row0, int nt, int h, Meta *meta, float *near, int lane) {
+    const int t = 2 * lane;
+    const float x0 = t < nt ? clamp_g(a.g[(row0 + t) * a.Hv + h]) : 0.0f;
+    const float x1 = t + 1 < nt ? clamp_g(a.g[(row0 + t + 1) * a.Hv + h]) : 0.0f;
+    const float b0 = t < nt ? a.beta[(row0 + t) * a.Hv + h] : 0.0f;
+    const float b1 = t + 1 < nt ? a.beta[(row0 + t + 1) * a.Hv + h] : 0.0f;
+    float hi = x0, lo = 0.0f;
+    add_pair(hi, lo, x1, 0.0f);
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float uh = __shfl_up_sync(0xffffffffu, hi, m), ul = __shfl_up_sync(0xffffffffu, lo, m);
+        if (lane >= m) add_pair(hi, lo, uh, ul);
+    }
+    const float th = __shfl_sync(0xffffffffu, hi, 31), tl = __shfl_sync(0xffffffffu, lo, 31);
+    const float eh = __shfl_sync(0xffffffffu, hi, lane | 7), el = __shfl_sync(0xffffffffu, lo, lane | 7);
+    float h0 = hi, l0 = lo;
+    add_pair(h0, l0, -x1, 0.0f);
+    const float G[2] = {h0, hi}, g[2] = {l0, lo}, be[2] = {b0, b1};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        meta->hi[t + i] = G[i];
+        meta->lo[t + i] = g[i];
+        meta->beta[t + i] = be[i];
+        meta->up[t + i] = expf(G[i]);
+        meta->down[t + i] = expf((th - G[i]) + (tl - g[i]));
+        near[t + i] = expf((eh - G[i]) + (el - g[i]));
+    }
+    if (lane == 0) meta->last = expf(th);
+}
+
+template <int DK, bool TRANS>
+__global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant__ PrepMaps maps, const Args a) {
     using L = PrepSmem<DK>;
-    extern __shared__ __align__(128) unsigned char psm[];
-    unsigned char *img = psm;
-    float(*A)[LD] = reinterpret_cast<float(*)[LD]>(psm + L::a);
-    float *near = reinterpret_cast<float *>(psm + L::near);
-    Meta *meta = reinterpret_cast<Meta *>(psm + 3 * M2_BYTES);
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    float(*A)[LD] = reinterpret_cast<float(*)[LD]>(smem + L::a);
+    float(*T)[16][TD] = reinterpret_cast<float(*)[16][TD]>(smem + L::td);
+    PrepBars *pb = reinterpret_cast<PrepBars *>(smem + L::bars);
+    const uint32_t img = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, group = a.Hv / a.Hk;
     const int t0 = c * C, nt = min(C, a.L - t0), N = chunks(a.L);
     const long long row0 = (long long)b * a.L + t0;
-    const int rb = warp & 3, g = lane / 4, q2 = lane % 4 * 2;   // block of 16 rows; fragment row and column
-    const bool isq = warp >= 4;                                 // warps 0..3: k.k, 4..7: q.k
-    float acc[8][4] = {};
-    {
-        constexpr int KP = L::KP;
-        __nv_bfloat16 *sk = reinterpret_cast<__nv_bfloat16 *>(psm), *sq = sk + C * KP;
-        for (int i = tid; i < C * (DK / 8); i += PT) {
-            const int t = i / (DK / 8), d = i % (DK / 8) * 8;
-            uint4 xk = make_uint4(0, 0, 0, 0), xq = xk;
-            if (t < nt) {
-                xk = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + d);
-                xq = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + d);
+    const int q = warp & 3, c0 = warp / 4 * 32;   // the warp's fragment: tokens 16 q on, columns c0 on
+    auto meta_of = [&](int j) { return reinterpret_cast<Meta *>(smem + L::meta + (j & 1) * META_BYTES); };
+    auto near_of = [&](int j) { return reinterpret_cast<float *>(smem + L::near) + (j & 1) * C; };
+    auto wait = [&](uint64_t *bar, int parity) { return bounded_wait(bar, (uint32_t)parity, &pb->abort); };
+    if (tid == 0) {
+        mbar_init(&pb->tiles, 1);
+        mbar_init(&pb->done, 1);
+        pb->abort = 0;
+        fence_mbar_init();
+        mbar_arrive_tx(&pb->tiles, L::KQ + L::K);
+#pragma unroll 1
+        for (int x = 0; x < DK / 64; ++x) {
+#pragma unroll 1
+            for (int i = 0; i < C / 16; ++i) {
+                tma_load_4d(smem + x * KQ_BOX + 2 * i * KQ_GROUP, &maps.k16, 64 * x, hk, t0 + 16 * i, b, &pb->tiles);
+                tma_load_4d(smem + x * KQ_BOX + (2 * i + 1) * KQ_GROUP, &maps.q16, 64 * x, hk, t0 + 16 * i, b, &pb->tiles);
             }
-            *reinterpret_cast<uint4 *>(sk + t * KP + d) = xk;
-            *reinterpret_cast<uint4 *>(sq + t * KP + d) = xq;
+            tma_load_4d(smem + L::KQ + x * 8192, &maps.k64, 64 * x, hk, t0, b, &pb->tiles);
         }
-        __syncthreads();
-        const __nv_bfloat16 *rows = isq ? sq : sk;
-#pragma unroll 2
-        for (int k0 = 0; k0 < DK; k0 += 16) {
-            uint32_t f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[i] = *reinterpret_cast<const uint32_t *>(rows + (16 * rb + g + (i & 1) * 8) * KP + k0 + q2 + (i >> 1) * 8);
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                if (n > 2 * rb + 1) continue;
-                const int at = (8 * n + g) * KP + k0 + q2;
-                mma16816(acc[n], f, *reinterpret_cast<const uint32_t *>(sk + at), *reinterpret_cast<const uint32_t *>(sk + at + 8));
-            }
-        }
-        if (isq)
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] *= a.scale;
     }
-    // row r of the image's lower matrix: three parts of two neighbouring values
-    auto put2 = [&](int r, int n, float x, float y) {
-        uint32_t h, m, l;
-        split3(x, y, h, m, l);
-        unsigned char *to = img + (2 * r - (r & 15) + 16) * 128 + ((n ^ (r & 7)) << 4) + q2 * 2;
-        *reinterpret_cast<uint32_t *>(to) = h;
-        *reinterpret_cast<uint32_t *>(to + M2_BYTES) = m;
-        *reinterpret_cast<uint32_t *>(to + 2 * M2_BYTES) = l;
-    };
-    const uint32_t simg = smem_addr(img);
+    if (warp == 0) {
+        __syncwarp();
+        tmem_alloc(&pb->tmem, 128);
+        tmem_relinquish();
+    }
+    if (warp == 7) chunk_factors(a, row0, nt, hk * group, meta_of(0), near_of(0), lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = pb->tmem, frag = tmem + ((uint32_t)(32 * q) << 16) + c0;
+    const uint64_t rows = desc_k(img), cols = desc_mn(img, M2_BYTES);
+    const uint32_t n1 = idesc_bf16_f32(128, 64), n2 = idesc_bf16_f32(128, 128);
+    const bool whole = TRANS || a.states;   // P E in 24 bits
+    bool ok = true;
+    if (tid == 0) {
+        if (wait(&pb->tiles, 0)) {
+            const uint64_t K = desc_k(img + L::KQ);
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k)
+                mma_bf16(tmem, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), on(K, k / 4 * 8192 + k % 4 * K_STEP), n1, k > 0);
+        }
+        mma_commit(&pb->done);
+    }
+    __syncwarp();
+    ok = wait(&pb->done, 0) && ok;
+    tc_fence_after();
+    float kk[16], qk[16];
+    frag_load<1>(frag, kk);
+    frag_load<1>(frag + QUERY_LANES, qk);
+    frag_scale(qk, a.scale, a.scale);
     for (int j = 0; j < group; ++j) {
         const int h = hk * group + j;
+        Meta *meta = meta_of(j);
+        const float *near = near_of(j);
+        unsigned char *out = static_cast<unsigned char *>(a.images) + (((long long)b * a.Hv + h) * N + c) * IMG_BYTES;
         if (j > 0 && tid == 0) bulk_wait_read_all();   // the last image has left
+        tc_fence_before();
         __syncthreads();
-        if (warp == 0) {
-            // G in float64 (64 terms of up to 128), kept as two floats, so that
-            // a small difference of large sums keeps 24 bits
-            double x0 = 2 * lane < nt ? (double)clamp_g(a.g[(row0 + 2 * lane) * a.Hv + h]) : 0.0;
-            double x1 = 2 * lane + 1 < nt ? (double)clamp_g(a.g[(row0 + 2 * lane + 1) * a.Hv + h]) : 0.0;
-            double w = x0 + x1;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double up = __shfl_up_sync(0xffffffffu, w, m);
-                if (lane >= m) w += up;
-            }
-            const double tot = __shfl_sync(0xffffffffu, w, 31), edge = __shfl_sync(0xffffffffu, w, lane | 7);
-            const double G[2] = {w - x1, w};
+        tc_fence_after();
+        {
+            float p[16];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                const float hi = (float)G[i];
-                meta->hi[t] = hi;
-                meta->lo[t] = (float)(G[i] - (double)hi);
-                meta->beta[t] = t < nt ? a.beta[(row0 + t) * a.Hv + h] : 0.0f;
-                meta->up[t] = expf(hi);
-                meta->down[t] = expf((float)(tot - G[i]));
-                near[t] = expf((float)(edge - G[i]));
-            }
-            if (lane == 0) meta->last = expf((float)tot);
-        }
-        __syncthreads();
+                const int r = 16 * q + lane / 4 + 8 * i;
+                const float gh = meta->hi[r], gl = meta->lo[r], br = meta->beta[r];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {      // rows g and g + 8 of the warp's block
-            const int r = 16 * rb + g + 8 * i;
-            const float gh = meta->hi[r], gl = meta->lo[r], br = meta->beta[r];
+                for (int jb = 0; jb < 2; ++jb) {
+                    const int nb = c0 / 16 + jb;
+                    float far = 1.0f;
+                    if (nb < q) far = expf((gh - meta->hi[16 * nb + 15]) + (gl - meta->lo[16 * nb + 15]));
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-                float w[4] = {0, 0, 0, 0};
-                if (nb <= rb) {
-                    const float far = nb < rb ? expf((gh - meta->hi[16 * nb + 15]) + (gl - meta->lo[16 * nb + 15])) : 0.0f;
+                    for (int jj = 2 * jb; jj < 2 * jb + 2; ++jj) {
+                        float s[2];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int n = 2 * nb + x / 2, col = 8 * n + q2 + x % 2;
-                        const float p = acc[n][2 * i + x % 2];
-                        const float d = nb < rb ? far * near[col] : expf((gh - meta->hi[col]) + (gl - meta->lo[col]));
-                        const bool in = isq ? col <= r : col < r;
-                        const float by = isq ? (TRANS ? 1.0f : meta->beta[col]) : (TRANS ? br : meta->beta[col]);
-                        w[x] = in ? p * (d * by) : 0.0f;
+                        for (int k = 0; k < 2; ++k) {
+                            const int col = c0 + 8 * jj + 2 * (lane & 3) + k, at = 4 * jj + 2 * i + k;
+                            s[k] = p[at] = 0.0f;
+                            if (nb <= q) {
+                                const float d = nb < q ? far * near[col] : expf((gh - meta->hi[col]) + (gl - meta->lo[col]));
+                                const float bc = meta->beta[col];
+                                if (col < r) s[k] = kk[at] * (d * (TRANS ? br : bc));
+                                if (col <= r) p[at] = qk[at] * (TRANS ? d : d * bc);
+                            }
+                            if (nb == q) T[nb][col & 15][r & 15] = s[k];
+                        }
+                        *reinterpret_cast<float2 *>(&A[r][c0 + 8 * jj + 2 * (lane & 3)]) = make_float2(s[0], s[1]);
                     }
                 }
-                if (isq) {
-                    put2(r, 2 * nb, w[0], w[1]);
-                    put2(r, 2 * nb + 1, w[2], w[3]);
-                } else {
-                    *reinterpret_cast<float2 *>(&A[r][16 * nb + q2]) = make_float2(w[0], w[1]);
-                    *reinterpret_cast<float2 *>(&A[r][16 * nb + 8 + q2]) = make_float2(w[2], w[3]);
-                }
             }
+            frag_put3(img, M2_BYTES, 32 * q + 16, c0, lane, p);
         }
         __syncthreads();
         if (warp < 2) {   // two blocks of the diagonal per warp; lane: a column of the inverse
-            const int o = 32 * warp + (lane & 16), col = lane & 15;
+            const int blk = 2 * warp + (lane >> 4), o = 16 * blk, col = lane & 15;
             float x[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[r] = r == col ? 1.0f : 0.0f;
 #pragma unroll
-            for (int r = 1; r < 16; ++r)
+            for (int m = 0; m < 15; ++m)
 #pragma unroll
-                for (int m = 0; m < r; m += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(&A[o + r][o + m]);
-                    x[r] = fmaf(-f.x, x[m], x[r]);
-                    if (m + 1 < r) x[r] = fmaf(-f.y, x[m + 1], x[r]);
-                    if (m + 2 < r) x[r] = fmaf(-f.z, x[m + 2], x[r]);
-                    if (m + 3 < r) x[r] = fmaf(-f.w, x[m + 3], x[r]);
+                for (int r4 = (m + 1) / 4 * 4; r4 < 16; r4 += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&T[blk][m][r4]);
+                    if (r4 > m) x[r4] = fmaf(-f.x, x[m], x[r4]);
+                    if (r4 + 1 > m) x[r4 + 1] = fmaf(-f.y, x[m], x[r4 + 1]);
+                    if (r4 + 2 > m) x[r4 + 2] = fmaf(-f.z, x[m], x[r4 + 2]);
+                    if (r4 + 3 > m) x[r4 + 3] = fmaf(-f.w, x[m], x[r4 + 3]);
                 }
-            __syncwarp();
 #pragma unroll
             for (int r = 0; r < 16; ++r) A[o + r][o + col] = x[r];
+        } else if (warp == 7 && j + 1 < group) {
+            chunk_factors(a, row0, nt, h + 1, meta_of(j + 1), near_of(j + 1), lane);
         }
         __syncthreads();
         {   // 32-row blocks, both pairs at once: B A^-1 into the unused upper part, then -D^-1 of it
             const int o = 32 * (tid / 128), r = tid % 128 / 8, c2 = tid % 8 * 2;
             float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const float x = A[o + 16 + r][o + m];
-                const float2 y = *reinterpret_cast<const float2 *>(&A[o + m][o + c2]);
-                v0 = fmaf(x, y.x, v0), v1 = fmaf(x, y.y, v1);
+            for (int m = 0; m < 16; m += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(&A[o + 16 + r][o + m]);
+                const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 y = *reinterpret_cast<const float2 *>(&A[o + m + k][o + c2]);
+                    v0 = fmaf(xs[k], y.x, v0), v1 = fmaf(xs[k], y.y, v1);
+                }
             }
             *reinterpret_cast<float2 *>(&A[o + r][o + 16 + c2]) = make_float2(v0, v1);
             __syncthreads();
             v0 = v1 = 0.0f;
 #pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const float x = A[o + 16 + r][o + 16 + m];
-                const float2 y = *reinterpret_cast<const float2 *>(&A[o + m][o + 16 + c2]);
-                v0 = fmaf(-x, y.x, v0), v1 = fmaf(-x, y.y, v1);
+            for (int m = 0; m < 16; m += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(&A[o + 16 + r][o + 16 + m]);
+                const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 y = *reinterpret_cast<const float2 *>(&A[o + m + k][o + 16 + c2]);
+                    v0 = fmaf(-xs[k], y.x, v0), v1 = fmaf(-xs[k], y.y, v1);
+                }
             }
             *reinterpret_cast<float2 *>(&A[o + 16 + r][o + c2]) = make_float2(v0, v1);
             __syncthreads();
             *reinterpret_cast<float2 *>(&A[o + r][o + 16 + c2]) = make_float2(0.0f, 0.0f);
         }
         __syncthreads();
-        {   // 64 rows
-            const int r = tid / 8, c4 = tid % 8 * 4;
-            float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-            for (int m = 0; m < 32; ++m) {
-                const float x = A[32 + r][m];
-                const float4 y = *reinterpret_cast<const float4 *>(&A[m][c4]);
-                v.x = fmaf(x, y.x, v.x), v.y = fmaf(x, y.y, v.y), v.z = fmaf(x, y.z, v.z), v.w = fmaf(x, y.w, v.w);
+        // 64 rows: two rows x four columns a thread, so that eight products
+        // share six reads of 16 bytes over four steps
+        auto block64 = [&](int xr, int xc, int yr, int yc, int zr, int zc, float sign) {
+            const int r = tid / 8 * 2, c4 = tid % 8 * 4;
+            float v[2][4] = {};
+#pragma unroll
+            for (int m = 0; m < 32; m += 4) {
+                const float4 x0 = *reinterpret_cast<const float4 *>(&A[xr + r][xc + m]);
+                const float4 x1 = *reinterpret_cast<const float4 *>(&A[xr + r + 1][xc + m]);
+                const float xs[2][4] = {{x0.x, x0.y, x0.z, x0.w}, {x1.x, x1.y, x1.z, x1.w}};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 y = *reinterpret_cast<const float4 *>(&A[yr + m + k][yc + c4]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        v[i][0] = fmaf(xs[i][k], y.x, v[i][0]), v[i][1] = fmaf(xs[i][k], y.y, v[i][1]);
+                        v[i][2] = fmaf(xs[i][k], y.z, v[i][2]), v[i][3] = fmaf(xs[i][k], y.w, v[i][3]);
+                    }
+                }
             }
-            *reinterpret_cast<float4 *>(&A[r][32 + c4]) = v;
-            __syncthreads();
-            v = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-            for (int m = 0; m < 32; ++m) {
-                const float x = A[32 + r][32 + m];
-                const float4 y = *reinterpret_cast<const float4 *>(&A[m][32 + c4]);
-                v.x = fmaf(-x, y.x, v.x), v.y = fmaf(-x, y.y, v.y), v.z = fmaf(-x, y.z, v.z), v.w = fmaf(-x, y.w, v.w);
-            }
-            *reinterpret_cast<float4 *>(&A[32 + r][c4]) = v;
-        }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<float4 *>(&A[zr + r + i][zc + c4]) =
+                    make_float4(sign * v[i][0], sign * v[i][1], sign * v[i][2], sign * v[i][3]);
+        };
+        if (tid < 128) block64(32, 0, 0, 0, 0, 32, 1.0f);
+        __syncthreads();
+        if (tid < 128) block64(32, 32, 0, 32, 32, 0, -1.0f);
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < C * 8 / PT; ++k) {   // E's three parts
@@ -248,53 +295,58 @@ template <int DK, bool TRANS> __global__ void __launch_bounds__(PT, 3) delta_pre
             split3(x.z, x.w, hh[1], mm[1], ll[1]);
             split3(y.x, y.y, hh[2], mm[2], ll[2]);
             split3(y.z, y.w, hh[3], mm[3], ll[3]);
-            unsigned char *to = img + (2 * r - (r & 15)) * 128 + ((ch ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4 *>(to) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
-            *reinterpret_cast<uint4 *>(to + M2_BYTES) = make_uint4(mm[0], mm[1], mm[2], mm[3]);
-            *reinterpret_cast<uint4 *>(to + 2 * M2_BYTES) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
+            const uint32_t to = piece(img, 2 * r - (r & 15), ch);
+            sts128(to, hh[0], hh[1], hh[2], hh[3]);
+            sts128(to + M2_BYTES, mm[0], mm[1], mm[2], mm[3]);
+            sts128(to + 2 * M2_BYTES, ll[0], ll[1], ll[2], ll[3]);
         }
+        fence_proxy_async_smem();
         __syncthreads();
-        // P E: warp w takes the rows of block w % 4 and the columns 32 (w / 4) on
-        float pe[4][4] = {};
+        if (tid == 0) {   // [E; P] E: the second operand's rows are every second 16
 #pragma unroll
-        for (int jb = 0; jb < 2; ++jb) {
-            const int cb = 2 * (warp >> 2) + jb;       // block of 16 columns
-            for (int kb = cb; kb <= rb; ++kb) {
-                uint32_t fa[3][4], fb[3][4];
-                const int r = 32 * rb + 16 + (lane & 15), m = 32 * kb + (lane & 15);
-#pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                    ldmatrix4(simg + p * M2_BYTES + r * 128 + (((2 * kb + (lane >> 4)) ^ (r & 7)) << 4), fa[p]);
-                    ldmatrix4t(simg + p * M2_BYTES + m * 128 + (((2 * cb + (lane >> 4)) ^ (m & 7)) << 4), fb[p]);
+            for (int k = 0; k < C / 16; ++k) {
+                const uint64_t P = on(rows, k * K_STEP), E = on(cols, 2 * k * KQ_GROUP);
+                mma_bf16(tmem, on(P, M2_BYTES), E, n2 | B_MN, k > 0);
+                mma_bf16(tmem, P, E, n2 | B_MN, 1);
+                if (whole) {
+                    mma_bf16(tmem, on(P, 2 * M2_BYTES), E, n1 | B_MN, 1);
+                    mma_bf16(tmem, P, on(E, 2 * M2_BYTES), n1 | B_MN, 1);
                 }
-#pragma unroll
-                for (int sum = 2; sum >= 0; --sum)
-#pragma unroll
-                    for (int p = 0; p <= sum; ++p) {
-                        mma16816(pe[2 * jb], fa[p], fb[sum - p][0], fb[sum - p][1]);
-                        mma16816(pe[2 * jb + 1], fa[p], fb[sum - p][2], fb[sum - p][3]);
-                    }
             }
+            mma_commit(&pb->done);
         }
-        __syncthreads();   // P has been read
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) put2(16 * rb + g + 8 * i, 4 * (warp >> 2) + n, pe[n][2 * i], pe[n][2 * i + 1]);
+        __syncwarp();
+        ok = wait(&pb->done, (j + 1) & 1) && ok;
+        tc_fence_after();
+        {
+            float p[16];
+            frag_load<2>(frag + QUERY_LANES, p);
+            frag_put3(img, M2_BYTES, 32 * q + 16, c0, lane, p);
+        }
         fence_proxy_async_smem();
         __syncthreads();
         if (tid == 0) {
-            bulk_store(static_cast<unsigned char *>(a.images) + (((long long)b * a.Hv + h) * N + c) * IMG_BYTES, img, IMG_BYTES);
+            bulk_store(out, smem, MAT_BYTES);
+            bulk_store(out + MAT_BYTES, meta, META_BYTES);
             bulk_commit();
         }
     }
     if (tid == 0) bulk_wait_all();
+    if (!ok) settle_copies();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 128);
 }
 
 template <int DK, bool TRANS> cudaError_t launch(const Args &a, cudaStream_t st) {
-    const cudaError_t e = big_smem(delta_prep_kernel<DK, TRANS>, PrepSmem<DK>::total);
+    PrepMaps m = {};
+    cudaError_t e = encode_rows(&m.k16, false, a.k, a.ldk, a.B, a.L, a.Hk, DK, 16);
+    if (e == cudaSuccess) e = encode_rows(&m.q16, false, a.q, a.ldq, a.B, a.L, a.Hk, DK, 16);
+    if (e == cudaSuccess) e = encode_rows(&m.k64, false, a.k, a.ldk, a.B, a.L, a.Hk, DK);
+    if (e == cudaSuccess) e = big_smem(delta_prep_kernel<DK, TRANS>, PrepSmem<DK>::total);
     if (e != cudaSuccess) return e;
-    delta_prep_kernel<DK, TRANS><<<dim3(chunks(a.L), a.Hk, a.B), PT, PrepSmem<DK>::total, st>>>(a);
+    delta_prep_kernel<DK, TRANS><<<dim3(chunks(a.L), a.Hk, a.B), PT, PrepSmem<DK>::total, st>>>(m, a);
     return cudaGetLastError();
 }
 
@@ -304,6 +356,8 @@ cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st) {
     if (a.Dk == 128) return transposed ? launch<128, true>(a, st) : launch<128, false>(a, st);
     return transposed ? launch<64, true>(a, st) : launch<64, false>(a, st);
 }
+
+int prep_fault_take() { return fault_take(); }
 
 }  // namespace delta
 }  // namespace s5
