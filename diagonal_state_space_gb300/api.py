@@ -229,6 +229,18 @@ def s5_sync_status(workspace, stream=None) -> int:
 # v, o and their gradients may be views with a pitch between tokens (slices of
 # a fused projection); a head's values and a token's heads are contiguous.
 # ---------------------------------------------------------------------------
+def _arr(t, name, dtype, shape):
+    """_ptr of a contiguous array that has to be there: one expression where all is well."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, name, dtype, shape)
+
+
+def _new(t):
+    """A contiguous array of t's shape, type and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _rows(t, name, dtype=None, shape=None):
     """(address, elements between two tokens) of a [..., H, D] array."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -254,10 +266,13 @@ def _rows(t, name, dtype=None, shape=None):
     return t.data_ptr(), H * D if pitch is None else pitch
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream    # current_stream() builds an object: 8 us of a call
+
+
 def _on(stream, *made):
     """The stream's handle; tensors made here outlive their use on it."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(made[0].device.index)
     if isinstance(stream, torch.cuda.Stream):
         for t in made:
             if t is not None:
@@ -309,7 +324,7 @@ def s5_delta_forward(q, k, v, g, beta, scale=None, s0=None, s_last=None, o=None,
     B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
     f32, dev, dt = torch.float32, q.device, q.dtype
     if o is None:
-        o = torch.empty(B, L, Hv, Dv, dtype=dt, device=dev)
+        o = _new(v)
     if s_last is True:
         s_last = torch.empty(B, Hv, Dk, Dv, dtype=f32, device=dev)
     lib = _native.lib()
@@ -344,7 +359,7 @@ def s5_delta_backward(q, k, v, g, beta, do, saved, scale=None, s0=None, ds_last=
         _ptr(ds_last, "ds_last", f32, (B, Hv, Dk, Dv), True), _ptr(saved, "saved", torch.uint8), saved.numel(),
         out["dq"].data_ptr(), Hk * Dk, out["dk"].data_ptr(), Hk * Dk, out["dv"].data_ptr(), Hv * Dv,
         out["dg"].data_ptr(), out["dbeta"].data_ptr(), None if s0 is None else out["ds0"].data_ptr(),
-        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _on(stream, workspace, *out.values()))
+        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _on(stream, out["dq"], workspace, *out.values()))
     check("s5_delta_backward", code)
     return out
 
@@ -355,11 +370,11 @@ def s5_delta_step(q, k, v, g, beta, state, scale=None, o=None, stream=None):
     B, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 1)
     f32, dt = torch.float32, q.dtype
     if o is None:
-        o = torch.empty(B, Hv, Dv, dtype=dt, device=q.device)
+        o = _new(v)
     code = _native.lib().s5_delta_step(
-        _ptr(q, "q"), _ptr(k, "k", dt, q.shape), _ptr(v, "v", dt), _DT[dt], _ptr(g, "g", f32, (B, Hv)),
-        _ptr(beta, "beta", f32, (B, Hv)), Dk ** -0.5 if scale is None else float(scale), B, Hk, Hv, Dk, Dv,
-        _ptr(state, "state", f32, (B, Hv, Dk, Dv)), _ptr(o, "o", dt, v.shape), _on(stream, o))
+        _arr(q, "q", dt, q.shape), _arr(k, "k", dt, q.shape), _arr(v, "v", dt, v.shape), _DT[dt],
+        _arr(g, "g", f32, (B, Hv)), _arr(beta, "beta", f32, (B, Hv)), Dk ** -0.5 if scale is None else float(scale),
+        B, Hk, Hv, Dk, Dv, _arr(state, "state", f32, (B, Hv, Dk, Dv)), _arr(o, "o", dt, v.shape), _on(stream, o))
     check("s5_delta_step", code)
     return o
 
@@ -374,8 +389,7 @@ def _rot_args(x, name, positions, freq):
     T = math.prod(x.shape[:-2])
     if freq is None:
         return T, None, None, 0
-    return (T, _ptr(positions, "positions", torch.int64, x.shape[:-2]), _ptr(freq, "freq", torch.float64),
-            2 * freq.numel())
+    return T, _arr(positions, "positions", torch.int64, x.shape[:-2]), _ptr(freq, "freq", torch.float64), 2 * freq.numel()
 
 
 def s5_rotary(x, positions, freq, layout="half", amplitude=1.0, inverse=False, out=None, stream=None):
@@ -385,7 +399,7 @@ def s5_rotary(x, positions, freq, layout="half", amplitude=1.0, inverse=False, o
     T, pos, fr, rot = _rot_args(x, "x", positions, freq)
     H, D = x.shape[-2:]
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x)
     code = _native.lib().s5_rotary(*_rows(x, "x"), _DT[x.dtype], pos, fr, rot, _LAYOUT[layout], float(amplitude),
                                    int(inverse), T, H, D, *_rows(out, "out", x.dtype, x.shape), _on(stream, out))
     check("s5_rotary", code)
@@ -400,7 +414,7 @@ def s5_qk_norm_rotary(q, k, positions, freq, norm="rms", eps=1e-6, q_weight=None
     (Hq, D), Hk, dt, f32 = q.shape[-2:], k.shape[-2], q.dtype, torch.float32
     kshape = (*q.shape[:-2], Hk, D)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+        q_out = _new(q)
     if k_out is None:
         k_out = torch.empty(kshape, dtype=dt, device=q.device)
     code = _native.lib().s5_qk_norm_rotary(
@@ -431,7 +445,7 @@ def s5_qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, norm="rms"
         float(amplitude), T, Hq, Hk, D, *_rows(dq_out, "dq_out", dt, q.shape), *_rows(dk_out, "dk_out", dt, kshape),
         out["dq"].data_ptr(), Hq * D, out["dk"].data_ptr(), Hk * D, _ptr(out["dwq"], "dwq", None, None, True),
         _ptr(out["dwk"], "dwk", None, None, True), _ptr(workspace, "workspace", torch.uint8, None, True),
-        0 if workspace is None else workspace.numel(), _on(stream, workspace, *out.values()))
+        0 if workspace is None else workspace.numel(), _on(stream, out["dq"], workspace, *out.values()))
     check("s5_qk_norm_rotary_backward", code)
     return out
 

@@ -17,19 +17,36 @@
 // here); p times it wraps exactly at whole turns, and the top 32 bits give
 // sincospif an argument good to 2^-25 half turns at any p.
 //
-// Bound: memory.  A row is read and written once.  A group of lanes holds one
-// row (two vectors of V values per lane: both halves of a pair are in the
-// same lane in either layout) and keeps its token's cosines and sines in
-// registers over all heads that it takes, so that they cost a few percent of
-// the pass; four rows are in flight per group.
+// Bound: memory.  A row is read and written once.  Two forms:
+//  - Streaming, for rows that 16-byte copies can address: every warp runs a
+//    ring of its own, three items of up to 4 KB (some heads of one token) that
+//    bulk copies bring into shared memory, that it turns in place and that
+//    bulk copies take away; no warp waits for another.  192 KB an SM in
+//    flight.  A lane keeps one slot (four pairs) of its token's cosines and
+//    sines over the item's rows.
+//  - Direct, for small calls and odd pitches: a group of lanes loads four rows
+//    of one token at once; their angles are worked out while they are on
+//    their way.
+// In both a lane holds both halves of its pairs, in either layout.
 #include "s5_internal.cuh"
+#include "s5_sm100.cuh"
 
 namespace s5 {
 namespace {
+using namespace sm100;
 
 constexpr int RT = 128;             // threads per block
-constexpr int ROWS = 4;             // rows in flight per group
-constexpr int BWD_BLOCKS = 152 * 6; // blocks of the backward pass: one wave, one partial of dw each
+constexpr int SWARPS = 8;           // warps of a streaming block, two blocks an SM
+// Bytes of rows from which on the streaming form runs.  40 heads of 128 in
+// bf16, streaming against direct: forward 11.9 / 11.2 us at 21 MB, 15.3 / 15.6
+// at 31 MB, 68 / 83 at 168 MB; backward 6.2 / 8.4 us at 1.3 MB, 6.0 / 5.5 at
+// 0.7 MB, 58 / 104 at 84 MB.
+constexpr long long STREAM_FWD = 32 << 20, STREAM_BWD = 1 << 20;
+constexpr int STAGES = 3;           // items of a warp in shared memory
+constexpr int FWD_ITEM = 4096;      // bytes of rows an item holds at most
+constexpr int BWD_ITEM = 2048;      // of x, and as many of dy
+constexpr int ROWS = 4;             // rows of a group, all in flight
+constexpr int BWD_BLOCKS = 152 * 4; // blocks of the backward pass: one wave, one partial of dw each
 
 struct RotArgs {
     const void *x[2], *dy[2];   // queries, keys (dy: backward only)
@@ -41,71 +58,48 @@ struct RotArgs {
     const double *freq;
     float *partial;             // [2][blocks][D] of dw (backward)
     long long T;
-    int D, rot, count;          // count: divisor of the sum of squares, 0 = no norm
+    int D, rot;
+    float inv;                  // factor on the sum of squares (1 / D, 1), 0 = no norm
     float eps, amp;             // amp carries the sign of the sines in `turn`
     float turn;                 // +1 forward, -1 transposed
     int per;                    // heads per group
     int segs[2];                // groups per token for queries and keys
     int want_dw[2];
+    bool stream;                // which form runs
 };
 
-template <typename T, int V> struct Vec;
-template <int V> struct Vec<float, V> {
-    __device__ static void load(const float *p, float (&r)[V]) {
-        if constexpr (V >= 4) {
+// V values as they lie in memory, and as floats.
+template <int BYTES> struct Raw;
+template <> struct Raw<16> { using type = uint4; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<4> { using type = unsigned; };
+template <> struct Raw<2> { using type = unsigned short; };
+
+template <typename T, int V> struct Vec {
+    using raw = typename Raw<sizeof(T) * V>::type;
+    __device__ static raw load(const T *p) { return *reinterpret_cast<const raw *>(p); }
+    __device__ static void widen(const raw &t, float (&r)[V]) {
+        const T *e = reinterpret_cast<const T *>(&t);
 #pragma unroll
-            for (int i = 0; i < V; i += 4) {
-                const float4 t = *reinterpret_cast<const float4 *>(p + i);
-                r[i] = t.x, r[i + 1] = t.y, r[i + 2] = t.z, r[i + 3] = t.w;
-            }
-        } else if constexpr (V == 2) {
-            const float2 t = *reinterpret_cast<const float2 *>(p);
-            r[0] = t.x, r[1] = t.y;
-        } else
-            r[0] = *p;
+        for (int i = 0; i < V; ++i) r[i] = (float)e[i];
     }
-    __device__ static void store(float *p, const float (&r)[V]) {
-        if constexpr (V == 4)
-            *reinterpret_cast<float4 *>(p) = make_float4(r[0], r[1], r[2], r[3]);
-        else if constexpr (V == 2)
-            *reinterpret_cast<float2 *>(p) = make_float2(r[0], r[1]);
-        else
-            *p = r[0];
+    __device__ static void store(T *p, const float (&r)[V]) {
+        raw t;
+        T *e = reinterpret_cast<T *>(&t);
+        if constexpr (sizeof(T) == 2 && V > 1) {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) *reinterpret_cast<__nv_bfloat162 *>(e + i) = __floats2bfloat162_rn(r[i], r[i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[i] = (T)r[i];
+        }
+        *reinterpret_cast<raw *>(p) = t;
     }
 };
-__device__ __forceinline__ float bf_lo(unsigned v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf_hi(unsigned v) { return __uint_as_float(v & 0xffff0000u); }
-__device__ __forceinline__ unsigned bf_pack(float lo, float hi) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const unsigned *>(&t);
+// V floats of a weight.
+template <int V> __device__ __forceinline__ void load_weight(const float *p, float (&r)[V]) {
+    Vec<float, V>::widen(Vec<float, V>::load(p), r);
 }
-template <int V> struct Vec<__nv_bfloat16, V> {
-    __device__ static void load(const __nv_bfloat16 *p, float (&r)[V]) {
-        if constexpr (V == 8) {
-            const uint4 t = *reinterpret_cast<const uint4 *>(p);
-            r[0] = bf_lo(t.x), r[1] = bf_hi(t.x), r[2] = bf_lo(t.y), r[3] = bf_hi(t.y);
-            r[4] = bf_lo(t.z), r[5] = bf_hi(t.z), r[6] = bf_lo(t.w), r[7] = bf_hi(t.w);
-        } else if constexpr (V == 4) {
-            const uint2 t = *reinterpret_cast<const uint2 *>(p);
-            r[0] = bf_lo(t.x), r[1] = bf_hi(t.x), r[2] = bf_lo(t.y), r[3] = bf_hi(t.y);
-        } else if constexpr (V == 2) {
-            const unsigned t = *reinterpret_cast<const unsigned *>(p);
-            r[0] = bf_lo(t), r[1] = bf_hi(t);
-        } else
-            r[0] = __bfloat162float(*p);
-    }
-    __device__ static void store(__nv_bfloat16 *p, const float (&r)[V]) {
-        if constexpr (V == 8)
-            *reinterpret_cast<uint4 *>(p) =
-                make_uint4(bf_pack(r[0], r[1]), bf_pack(r[2], r[3]), bf_pack(r[4], r[5]), bf_pack(r[6], r[7]));
-        else if constexpr (V == 4)
-            *reinterpret_cast<uint2 *>(p) = make_uint2(bf_pack(r[0], r[1]), bf_pack(r[2], r[3]));
-        else if constexpr (V == 2)
-            *reinterpret_cast<unsigned *>(p) = bf_pack(r[0], r[1]);
-        else
-            *p = __float2bfloat16_rn(r[0]);
-    }
-};
 
 // f / 2 pi as a 64-bit fraction of a turn: the 53-bit significand times
 // 2^66 / 2 pi, shifted by the exponent.  Whole turns fall off the top.
@@ -192,13 +186,13 @@ template <int G> __device__ __forceinline__ float group_sum(float v) {
 template <typename T, int V, int G, bool INTER>
 __global__ void __launch_bounds__(RT) rotary_fwd_kernel(const RotArgs a) {
     constexpr int S = SLOTS<V>;
+    using X = Vec<T, V>;
     const int lane = threadIdx.x % G;
     const int n = a.rot / 2, nslots = a.D / (2 * V);
-    const long long groups = a.T * (a.segs[0] + a.segs[1]);
+    const int segs = a.segs[0] + a.segs[1];
+    const long long groups = a.T * segs;
     const long long gid = (long long)blockIdx.x * (RT / G) + threadIdx.x / G;
     griddep_launch_dependents();
-    unsigned long long f[S][V];
-    bool rotated[S];
     int lo[S], hi[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
@@ -206,79 +200,71 @@ __global__ void __launch_bounds__(RT) rotary_fwd_kernel(const RotArgs a) {
         slot_place<V, INTER>(slot, n, lo[j], hi[j]);
         if (slot >= nslots) lo[j] = -1;
     }
-    griddep_wait();
-#pragma unroll
-    for (int j = 0; j < S; ++j)
-        if (lo[j] >= 0)
-            slot_freq<V, INTER>(a, lane + j * G, f[j], rotated[j]);
-        else
-            rotated[j] = false;
-    // every lane of a warp makes the same number of passes: the sums over a
-    // group use full-warp shuffles
+    // every lane of a warp makes the same passes: the sums over a group use
+    // full-warp shuffles
     const bool live = gid < groups;
-    const long long token = live ? gid / (a.segs[0] + a.segs[1]) : 0;
-    const int seg = live ? (int)(gid % (a.segs[0] + a.segs[1])) : 0;
+    const long long token = live ? gid / segs : 0;
+    const int seg = live ? (int)(gid - token * segs) : 0;
     const int part = seg >= a.segs[0];
     const int h0 = (part ? seg - a.segs[0] : seg) * a.per;
-    const int h1 = live ? min(h0 + a.per, a.heads[part]) : h0;
+    const int rows = live ? min(a.per, (part ? a.heads[1] : a.heads[0]) - h0) : 0;
+    const T *x = static_cast<const T *>(part ? a.x[1] : a.x[0]) + token * (part ? a.ldx[1] : a.ldx[0]) + (long long)h0 * a.D;
+    T *y = static_cast<T *>(part ? a.y[1] : a.y[0]) + token * (part ? a.ldy[1] : a.ldy[0]) + (long long)h0 * a.D;
+    const float *w = part ? a.w[1] : a.w[0];
+    griddep_wait();
+    // all rows are on their way before the angles are worked out
+    typename X::raw u[ROWS][S], t[ROWS][S];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int j = 0; j < S; ++j)
+            if (r < rows && lo[j] >= 0) {
+                u[r][j] = X::load(x + r * a.D + lo[j]);
+                t[r][j] = X::load(x + r * a.D + hi[j]);
+            } else
+                u[r][j] = t[r][j] = typename X::raw{};
     const long long pos = (live && n) ? a.pos[token] : 0;
     float c[S][V], s[S][V];
+    bool rotated[S];
 #pragma unroll
-    for (int j = 0; j < S; ++j) slot_angles<V>(a, f[j], rotated[j], pos, c[j], s[j]);
-    const T *x = static_cast<const T *>(part ? a.x[1] : a.x[0]) + token * (part ? a.ldx[1] : a.ldx[0]);
-    T *y = static_cast<T *>(part ? a.y[1] : a.y[0]) + token * (part ? a.ldy[1] : a.ldy[0]);
-    const float *w = part ? a.w[1] : a.w[0];
-    for (int base = 0; base < a.per; base += ROWS) {
-        float u[ROWS][S][V], t[ROWS][S][V];
+    for (int j = 0; j < S; ++j) {
+        unsigned long long f[V];
+        rotated[j] = false;
+        if (lo[j] >= 0) slot_freq<V, INTER>(a, lane + j * G, f, rotated[j]);
+        slot_angles<V>(a, f, rotated[j], pos, c[j], s[j]);
+    }
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r)
+    for (int r = 0; r < ROWS; ++r) {
+        if (r >= a.per) break;
+        float p[S][V], q[S][V];
 #pragma unroll
-            for (int j = 0; j < S; ++j) {
-                if (h0 + base + r < h1 && lo[j] >= 0) {
-                    const T *row = x + (long long)(h0 + base + r) * a.D;
-                    Vec<T, V>::load(row + lo[j], u[r][j]);
-                    Vec<T, V>::load(row + hi[j], t[r][j]);
-                } else {
+        for (int j = 0; j < S; ++j) X::widen(u[r][j], p[j]), X::widen(t[r][j], q[j]);
+        if (a.inv != 0.0f) {
+            float ss = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) u[r][j][i] = t[r][j][i] = 0.0f;
-                }
-            }
+            for (int j = 0; j < S; ++j)
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            if (a.count) {
-                float ss = 0.0f;
+                for (int i = 0; i < V; ++i) ss = fmaf(p[j][i], p[j][i], fmaf(q[j][i], q[j][i], ss));
+            const float rs = rsqrtf(group_sum<G>(ss) * a.inv + a.eps);
 #pragma unroll
-                for (int j = 0; j < S; ++j)
+            for (int j = 0; j < S; ++j)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) ss = fmaf(u[r][j][i], u[r][j][i], fmaf(t[r][j][i], t[r][j][i], ss));
-                const float rs = rsqrtf(group_sum<G>(ss) / (float)a.count + a.eps);
-#pragma unroll
-                for (int j = 0; j < S; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) u[r][j][i] *= rs, t[r][j][i] *= rs;
-            }
-            if (w) {
-#pragma unroll
-                for (int j = 0; j < S; ++j)
-                    if (lo[j] >= 0) {
-                        float wl[V], wh[V];
-                        Vec<float, V>::load(w + lo[j], wl);
-                        Vec<float, V>::load(w + hi[j], wh);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) u[r][j][i] *= wl[i], t[r][j][i] *= wh[i];
-                    }
-            }
-            if (h0 + base + r < h1) {
-                T *row = y + (long long)(h0 + base + r) * a.D;
-#pragma unroll
-                for (int j = 0; j < S; ++j)
-                    if (lo[j] >= 0) {
-                        if (rotated[j]) rotate<V, INTER>(u[r][j], t[r][j], c[j], s[j]);
-                        Vec<T, V>::store(row + lo[j], u[r][j]);
-                        Vec<T, V>::store(row + hi[j], t[r][j]);
-                    }
-            }
+                for (int i = 0; i < V; ++i) p[j][i] *= rs, q[j][i] *= rs;
         }
+#pragma unroll
+        for (int j = 0; j < S; ++j)
+            if (r < rows && lo[j] >= 0) {
+                if (w) {
+                    float wl[V], wh[V];
+                    load_weight<V>(w + lo[j], wl);
+                    load_weight<V>(w + hi[j], wh);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) p[j][i] *= wl[i], q[j][i] *= wh[i];
+                }
+                if (rotated[j]) rotate<V, INTER>(p[j], q[j], c[j], s[j]);
+                X::store(y + r * a.D + lo[j], p[j]);
+                X::store(y + r * a.D + hi[j], q[j]);
+            }
     }
 }
 
@@ -301,6 +287,7 @@ __global__ void __launch_bounds__(RT) rotary_bwd_kernel(const RotArgs a, int qbl
     const T *xb = static_cast<const T *>(part ? a.x[1] : a.x[0]);
     const T *gb = static_cast<const T *>(part ? a.dy[1] : a.dy[0]);
     T *yb = static_cast<T *>(part ? a.y[1] : a.y[0]);
+    using X = Vec<T, V>;
     unsigned long long f[S][V];
     bool rotated[S];
     int lo[S], hi[S];
@@ -322,69 +309,84 @@ __global__ void __launch_bounds__(RT) rotary_bwd_kernel(const RotArgs a, int qbl
             dl[j][i] = dh[j][i] = 0.0f;
         }
     }
-    const long long items = a.T * segs, stride = (long long)nblk * NG;
-    // the trip count is the block's, not the group's: shuffles use full warps
-    for (long long it0 = (long long)blk * NG; it0 < items; it0 += stride) {
-        const long long it = it0 + grp;
-        const bool live = it < items;
-        const long long token = live ? it / segs : 0;
-        const int h0 = live ? (int)(it % segs) * a.per : 0, h1 = live ? min(h0 + a.per, heads) : 0;
-        const long long pos = (live && n) ? a.pos[token] : 0;
-        float c[S][V], s[S][V];
+    // Two rows at a time, the next two on their way.  The trip count is the
+    // block's, not the group's: shuffles use full warps.
+    const long long items = a.T * segs, stride = (long long)nblk * NG, it0 = (long long)blk * NG;
+    const int steps = (a.per + 1) / 2;
+    const long long trips = items > it0 ? (items - it0 + stride - 1) / stride * steps : 0;
+    typename X::raw nu[2][S], nt[2][S], np[2][S], nq[2][S];
+    long long token = 0;
+    int h0 = 0;
+    auto fetch = [&](long long trip, long long &tk, int &head) {
+        const long long it = it0 + trip / steps * stride + grp;
+        const bool live = trip < trips && it < items;
+        tk = live ? it / segs : 0;
+        const int first = live ? (int)(it - tk * segs) * a.per : heads;
+        head = first + (int)(trip % steps) * 2;
+        const int end = min(first + a.per, heads);
 #pragma unroll
-        for (int j = 0; j < S; ++j) slot_angles<V>(a, f[j], rotated[j], pos, c[j], s[j]);
-        for (int base = 0; base < a.per; base += 2) {
-            float u[2][S][V], t[2][S][V], p[2][S][V], q[2][S][V];
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int j = 0; j < S; ++j)
+                if (head + r < end && lo[j] >= 0) {
+                    const long long o = (long long)(head + r) * a.D;
+                    nu[r][j] = X::load(xb + tk * ldx + o + lo[j]);
+                    nt[r][j] = X::load(xb + tk * ldx + o + hi[j]);
+                    np[r][j] = X::load(gb + tk * lddy + o + lo[j]);
+                    nq[r][j] = X::load(gb + tk * lddy + o + hi[j]);
+                } else
+                    nu[r][j] = nt[r][j] = np[r][j] = nq[r][j] = typename X::raw{};
+        return end;
+    };
+    float c[S][V], s[S][V];
+    int end = fetch(0, token, h0);
+    for (long long trip = 0; trip < trips; ++trip) {
+        typename X::raw cu[2][S], ct[2][S], cp[2][S], cq[2][S];
 #pragma unroll
-                for (int j = 0; j < S; ++j) {
-                    if (h0 + base + r < h1 && lo[j] >= 0) {
-                        const long long o = (long long)(h0 + base + r) * a.D;
-                        Vec<T, V>::load(xb + token * ldx + o + lo[j], u[r][j]);
-                        Vec<T, V>::load(xb + token * ldx + o + hi[j], t[r][j]);
-                        Vec<T, V>::load(gb + token * lddy + o + lo[j], p[r][j]);
-                        Vec<T, V>::load(gb + token * lddy + o + hi[j], q[r][j]);
-                    } else {
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-                        for (int i = 0; i < V; ++i) u[r][j][i] = t[r][j][i] = p[r][j][i] = q[r][j][i] = 0.0f;
-                    }
+            for (int j = 0; j < S; ++j) cu[r][j] = nu[r][j], ct[r][j] = nt[r][j], cp[r][j] = np[r][j], cq[r][j] = nq[r][j];
+        const long long tok = token;
+        const int head = h0, last = end;
+        if (trip % steps == 0) {
+            const long long pos = n ? a.pos[tok] : 0;
+#pragma unroll
+            for (int j = 0; j < S; ++j) slot_angles<V>(a, f[j], rotated[j], pos, c[j], s[j]);
+        }
+        end = fetch(trip + 1, token, h0);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float u[S][V], t[S][V], p[S][V], q[S][V], ss = 0.0f, sx = 0.0f;
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                X::widen(cu[r][j], u[j]), X::widen(ct[r][j], t[j]), X::widen(cp[r][j], p[j]), X::widen(cq[r][j], q[j]);
+                if (rotated[j]) rotate<V, INTER>(p[j], q[j], c[j], s[j]);   // dz
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    ss = fmaf(u[j][i], u[j][i], fmaf(t[j][i], t[j][i], ss));
+                    sx = fmaf(p[j][i] * wl[j][i], u[j][i], fmaf(q[j][i] * wh[j][i], t[j][i], sx));
                 }
+            }
+            float rs = 1.0f, k = 0.0f;
+            if (a.inv != 0.0f) {
+                rs = rsqrtf(group_sum<G>(ss) * a.inv + a.eps);
+                k = rs * rs * rs * (group_sum<G>(sx) * a.inv);
+            }
+            if (head + r >= last) continue;   // a dead row would add 0 * rsqrt(eps): NaN where eps is 0
+            T *row = yb + tok * ldy + (long long)(head + r) * a.D;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float ss = 0.0f, sx = 0.0f;
+            for (int j = 0; j < S; ++j) {
+                float xl[V], xh[V];
 #pragma unroll
-                for (int j = 0; j < S; ++j) {
-                    if (rotated[j]) rotate<V, INTER>(p[r][j], q[r][j], c[j], s[j]);   // dz
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        ss = fmaf(u[r][j][i], u[r][j][i], fmaf(t[r][j][i], t[r][j][i], ss));
-                        sx = fmaf(p[r][j][i] * wl[j][i], u[r][j][i], fmaf(q[r][j][i] * wh[j][i], t[r][j][i], sx));
-                    }
+                for (int i = 0; i < V; ++i) {
+                    dl[j][i] = fmaf(p[j][i], u[j][i] * rs, dl[j][i]);
+                    dh[j][i] = fmaf(q[j][i], t[j][i] * rs, dh[j][i]);
+                    xl[i] = rs * wl[j][i] * p[j][i] - u[j][i] * k;
+                    xh[i] = rs * wh[j][i] * q[j][i] - t[j][i] * k;
                 }
-                float rs = 1.0f, k = 0.0f;
-                if (a.count) {
-                    rs = rsqrtf(group_sum<G>(ss) / (float)a.count + a.eps);
-                    k = rs * rs * rs * (group_sum<G>(sx) / (float)a.count);
-                }
-                const bool on = h0 + base + r < h1;
-                T *row = yb + token * ldy + (long long)(h0 + base + r) * a.D;
-#pragma unroll
-                for (int j = 0; j < S; ++j) {
-                    float xl[V], xh[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        if (on) {   // a dead row would add 0 * rsqrt(eps): NaN where eps is 0
-                            dl[j][i] = fmaf(p[r][j][i], u[r][j][i] * rs, dl[j][i]);
-                            dh[j][i] = fmaf(q[r][j][i], t[r][j][i] * rs, dh[j][i]);
-                        }
-                        xl[i] = rs * wl[j][i] * p[r][j][i] - u[r][j][i] * k;
-                        xh[i] = rs * wh[j][i] * q[r][j][i] - t[r][j][i] * k;
-                    }
-                    if (on && lo[j] >= 0) {
-                        Vec<T, V>::store(row + lo[j], xl);
-                        Vec<T, V>::store(row + hi[j], xh);
-                    }
+                if (lo[j] >= 0) {
+                    X::store(row + lo[j], xl);
+                    X::store(row + hi[j], xh);
                 }
             }
         }
@@ -402,6 +404,295 @@ __global__ void __launch_bounds__(RT) rotary_bwd_kernel(const RotArgs a, int qbl
     for (int d = threadIdx.x; d < a.D; d += RT) {
         float v = 0.0f;
         for (int g = 0; g < NG; ++g) v += red[g * a.D + d];
+        a.partial[(long long)blockIdx.x * a.D + d] = v;
+    }
+}
+
+
+// ---------------------------------------------------------------------------
+// Streaming form: V = 4, one slot a lane.  Items are (token, segment of heads),
+// item i of a warp being i strides on; segments of queries come first.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void bulk_out(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read_but_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ int g_rotary_fault = 0;
+// A copy that has not come after two seconds: the item is given up, the kernel
+// ends and the host is told.
+__device__ __forceinline__ void copy_wait(uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return;
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 100000))
+        if (global_ns() - t0 > 2000000000ull) {
+            atomicExch(&g_rotary_fault, 1);
+            return;
+        }
+}
+
+// Item i of warp w of W.  With enough tokens a warp takes all segments of one,
+// and works its angles out once; else the segments are dealt out one by one.
+struct Item {
+    long long token;
+    int part, h0, rows;
+};
+struct Deal {
+    int seg0, segs;
+    bool by_token;
+    long long first, step, count;   // of tokens, or of segments
+    __device__ Deal(const RotArgs &a, int s0, int n, int w, long long W) : seg0(s0), segs(n), first(w), step(W) {
+        by_token = a.T >= 2 * W;
+        const long long units = by_token ? a.T : a.T * n;
+        count = units > first ? (units - first + step - 1) / step * (by_token ? n : 1) : 0;
+    }
+    __device__ Item item(const RotArgs &a, long long i) const {
+        Item m;
+        int seg;
+        if (by_token) {
+            const long long t = i / segs;
+            seg = (int)(i - t * segs);
+            m.token = first + t * step;
+        } else {
+            const long long it = first + i * step;
+            m.token = it / segs;
+            seg = (int)(it - m.token * segs);
+        }
+        seg += seg0;
+        m.part = seg >= a.segs[0];
+        if (m.part) seg -= a.segs[0];
+        m.h0 = seg * a.per;
+        m.rows = min(a.per, (m.part ? a.heads[1] : a.heads[0]) - m.h0);
+        return m;
+    }
+};
+
+// A pair's two values in a slot.
+template <int V, bool INTER> __device__ __forceinline__ float &pair_a(float (&lo)[V], float (&hi)[V], int i) {
+    return INTER ? (i < V / 2 ? lo[2 * i] : hi[2 * i - V]) : lo[i];
+}
+template <int V, bool INTER> __device__ __forceinline__ float &pair_b(float (&lo)[V], float (&hi)[V], int i) {
+    return INTER ? (i < V / 2 ? lo[2 * i + 1] : hi[2 * i + 1 - V]) : hi[i];
+}
+
+template <typename T, int G, bool INTER>
+__global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_fwd_kernel(const RotArgs a) {
+    constexpr int V = 4, RP = 32 / G;
+    using X = Vec<T, V>;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ uint64_t full[SWARPS][STAGES];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, slot = lane % G;
+    T *buf = reinterpret_cast<T *>(ring + warp * STAGES * FWD_ITEM);
+    constexpr int STRIDE = FWD_ITEM / sizeof(T);
+    if (lane == 0) {
+        for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    const int n = a.rot / 2, segs = a.segs[0] + a.segs[1];
+    int lo, hi;
+    slot_place<V, INTER>(slot, n, lo, hi);
+    const bool in = slot < a.D / (2 * V);
+    griddep_launch_dependents();
+    griddep_wait();
+    unsigned long long f[V];
+    bool rotated = false;
+    if (in) slot_freq<V, INTER>(a, slot, f, rotated);
+    const Deal deal(a, 0, segs, blockIdx.x * SWARPS + warp, (long long)gridDim.x * SWARPS);
+    long long mypos = 0;   // lane i: the position of the item in stage i
+    auto fetch = [&](long long i, int st) {
+        if (i >= deal.count) return;
+        const Item m = deal.item(a, i);
+        if (n && lane == st) mypos = a.pos[m.token];
+        if (lane == 0) {
+            const T *x = static_cast<const T *>(m.part ? a.x[1] : a.x[0]) + m.token * (m.part ? a.ldx[1] : a.ldx[0]) + m.h0 * a.D;
+            const uint32_t bytes = (uint32_t)(m.rows * a.D * sizeof(T));
+            mbar_arrive_tx(&full[warp][st], bytes);
+            bulk_load(buf + st * STRIDE, x, bytes, &full[warp][st]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) fetch(i, i);
+    int st = 0, phase = 0;
+    long long token = -1;
+    int part = -1;
+    float c[V], s[V], ca[V], sa[V], cb[V], sb[V];   // a pair's cosine and sine, times its values' weights
+    for (long long it = 0; it < deal.count; ++it) {
+        const Item m = deal.item(a, it);
+        const long long pos = __shfl_sync(0xffffffffu, mypos, st);
+        if (m.token != token || m.part != part) {
+            if (m.token != token) slot_angles<V>(a, f, rotated, pos, c, s);
+            const float *w = m.part ? a.w[1] : a.w[0];
+            float wl[V], wh[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) wl[i] = wh[i] = 1.0f;
+            if (w && in) load_weight<V>(w + lo, wl), load_weight<V>(w + hi, wh);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float wa = pair_a<V, INTER>(wl, wh, i), wb = pair_b<V, INTER>(wl, wh, i);
+                ca[i] = c[i] * wa, sa[i] = s[i] * wa, cb[i] = c[i] * wb, sb[i] = s[i] * wb;
+            }
+            token = m.token, part = m.part;
+        }
+        copy_wait(&full[warp][st], phase);
+        T *x = buf + st * STRIDE;
+#pragma unroll 4
+        for (int r0 = 0; r0 < m.rows; r0 += RP) {
+            const int r = r0 + lane / G;
+            const bool on = in && r < m.rows;
+            float p[V] = {}, q[V] = {}, rs = 1.0f;
+            if (on) X::widen(X::load(x + r * a.D + lo), p), X::widen(X::load(x + r * a.D + hi), q);
+            if (a.inv != 0.0f) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) ss = fmaf(p[i], p[i], fmaf(q[i], q[i], ss));
+                rs = rsqrtf(group_sum<G>(ss) * a.inv + a.eps);
+            }
+            if (on) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float &va = pair_a<V, INTER>(p, q, i), &vb = pair_b<V, INTER>(p, q, i);
+                    const float xa = va * rs, xb = vb * rs;
+                    va = ca[i] * xa, vb = cb[i] * xb;
+                    if (rotated) va = fmaf(-sb[i], xb, va), vb = fmaf(sa[i], xa, vb);
+                }
+                X::store(x + r * a.D + lo, p);
+                X::store(x + r * a.D + hi, q);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            T *y = static_cast<T *>(m.part ? a.y[1] : a.y[0]) + m.token * (m.part ? a.ldy[1] : a.ldy[0]) + m.h0 * a.D;
+            bulk_out(y, x, (uint32_t)(m.rows * a.D * sizeof(T)));
+            bulk_commit();
+            if (it > 0) bulk_wait_read_but_1();   // the item before has left its stage
+        }
+        __syncwarp();
+        if (it > 0) fetch(it + STAGES - 1, st == 0 ? STAGES - 1 : st - 1);
+        if (++st == STAGES) st = 0, phase ^= 1;
+    }
+    if (lane == 0) bulk_wait_all();
+}
+
+template <typename T, int G, bool INTER>
+__global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_bwd_kernel(const RotArgs a, int qblocks) {
+    constexpr int V = 4, RP = 32 / G;
+    using X = Vec<T, V>;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ uint64_t full[SWARPS][STAGES];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, slot = lane % G;
+    T *buf = reinterpret_cast<T *>(ring + warp * STAGES * 2 * BWD_ITEM);
+    constexpr int STRIDE = 2 * BWD_ITEM / sizeof(T), DY = BWD_ITEM / sizeof(T);
+    if (lane == 0) {
+        for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    const int part = (int)blockIdx.x >= qblocks;
+    const int blk = part ? blockIdx.x - qblocks : blockIdx.x, nblk = part ? gridDim.x - qblocks : qblocks;
+    const int n = a.rot / 2, segs = part ? a.segs[1] : a.segs[0], seg0 = part ? a.segs[0] : 0;
+    const long long ldx = part ? a.ldx[1] : a.ldx[0], ldy = part ? a.ldy[1] : a.ldy[0], lddy = part ? a.lddy[1] : a.lddy[0];
+    const T *xb = static_cast<const T *>(part ? a.x[1] : a.x[0]);
+    const T *gb = static_cast<const T *>(part ? a.dy[1] : a.dy[0]);
+    T *yb = static_cast<T *>(part ? a.y[1] : a.y[0]);
+    const float *w = part ? a.w[1] : a.w[0];
+    int lo, hi;
+    slot_place<V, INTER>(slot, n, lo, hi);
+    const bool in = slot < a.D / (2 * V);
+    griddep_wait();
+    unsigned long long f[V];
+    bool rotated = false;
+    if (in) slot_freq<V, INTER>(a, slot, f, rotated);
+    float wl[V], wh[V], dl[V] = {}, dh[V] = {};
+#pragma unroll
+    for (int i = 0; i < V; ++i) wl[i] = wh[i] = 1.0f;
+    if (w && in) load_weight<V>(w + lo, wl), load_weight<V>(w + hi, wh);
+    const Deal deal(a, seg0, segs, blk * SWARPS + warp, (long long)nblk * SWARPS);
+    long long mypos = 0;
+    auto fetch = [&](long long i, int st) {
+        if (i >= deal.count) return;
+        const Item m = deal.item(a, i);
+        if (n && lane == st) mypos = a.pos[m.token];
+        if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(m.rows * a.D * sizeof(T));
+            mbar_arrive_tx(&full[warp][st], 2 * bytes);
+            bulk_load(buf + st * STRIDE, xb + m.token * ldx + m.h0 * a.D, bytes, &full[warp][st]);
+            bulk_load(buf + st * STRIDE + DY, gb + m.token * lddy + m.h0 * a.D, bytes, &full[warp][st]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) fetch(i, i);
+    int st = 0, phase = 0;
+    long long token = -1;
+    float c[V], s[V];
+    for (long long it = 0; it < deal.count; ++it) {
+        const Item m = deal.item(a, it);
+        const long long pos = __shfl_sync(0xffffffffu, mypos, st);
+        if (m.token != token) slot_angles<V>(a, f, rotated, pos, c, s);
+        token = m.token;
+        copy_wait(&full[warp][st], phase);
+        T *x = buf + st * STRIDE, *g = x + DY;
+#pragma unroll 2
+        for (int r0 = 0; r0 < m.rows; r0 += RP) {
+            const int r = r0 + lane / G;
+            const bool on = in && r < m.rows;
+            float u[V] = {}, t[V] = {}, p[V] = {}, q[V] = {}, ss = 0.0f, sx = 0.0f;
+            if (on) {
+                X::widen(X::load(x + r * a.D + lo), u), X::widen(X::load(x + r * a.D + hi), t);
+                X::widen(X::load(g + r * a.D + lo), p), X::widen(X::load(g + r * a.D + hi), q);
+            }
+            if (rotated) rotate<V, INTER>(p, q, c, s);   // dz
+            float rs = 1.0f, k = 0.0f, pw[V], qw[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) pw[i] = p[i] * wl[i], qw[i] = q[i] * wh[i];
+            if (a.inv != 0.0f) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    ss = fmaf(u[i], u[i], fmaf(t[i], t[i], ss));
+                    sx = fmaf(pw[i], u[i], fmaf(qw[i], t[i], sx));
+                }
+                rs = rsqrtf(group_sum<G>(ss) * a.inv + a.eps);
+                k = rs * rs * (group_sum<G>(sx) * a.inv);
+            }
+            if (on) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float xa = u[i] * rs, xb = t[i] * rs;
+                    dl[i] = fmaf(p[i], xa, dl[i]);
+                    dh[i] = fmaf(q[i], xb, dh[i]);
+                    u[i] = fmaf(-k, xa, rs * pw[i]);
+                    t[i] = fmaf(-k, xb, rs * qw[i]);
+                }
+                X::store(x + r * a.D + lo, u);
+                X::store(x + r * a.D + hi, t);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            bulk_out(yb + m.token * ldy + m.h0 * a.D, x, (uint32_t)(m.rows * a.D * sizeof(T)));
+            bulk_commit();
+            if (it > 0) bulk_wait_read_but_1();
+        }
+        __syncwarp();
+        if (it > 0) fetch(it + STAGES - 1, st == 0 ? STAGES - 1 : st - 1);
+        if (++st == STAGES) st = 0, phase ^= 1;
+    }
+    if (lane == 0) bulk_wait_all();
+    if (!(part ? a.want_dw[1] : a.want_dw[0])) return;
+    __syncthreads();                                   // every warp's ring is at rest
+    float *red = reinterpret_cast<float *>(ring);      // [SWARPS * RP][D]
+    if (in)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            red[(warp * RP + lane / G) * a.D + lo + i] = dl[i];
+            red[(warp * RP + lane / G) * a.D + hi + i] = dh[i];
+        }
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.D; d += SWARPS * 32) {
+        float v = 0.0f;
+        for (int g = 0; g < SWARPS * RP; ++g) v += red[g * a.D + d];
         a.partial[(long long)blockIdx.x * a.D + d] = v;
     }
 }
@@ -445,8 +736,8 @@ cudaError_t launch_pdl(void (*k)(Ks...), dim3 grid, int threads, size_t smem, cu
 
 // Values per vector: the widest (16 bytes at most) that divides the pair
 // offset, the unrotated rest and every pitch.
-int vec_width(int elem, int D, int rot, bool inter, const long long *lds, int nld) {
-    for (int V = elem == 2 ? 8 : 4; V > 1; V /= 2) {
+int vec_width(int D, int rot, bool inter, const long long *lds, int nld) {
+    for (int V = 4; V > 1; V /= 2) {
         bool ok = D % (2 * V) == 0 && (inter ? rot % (2 * V) == 0 : (rot / 2) % V == 0);
         for (int i = 0; i < nld; ++i) ok = ok && lds[i] % V == 0;
         if (ok) return V;
@@ -454,63 +745,105 @@ int vec_width(int elem, int D, int rot, bool inter, const long long *lds, int nl
     return 1;
 }
 
+// Heads of an item: as many as fill it, their bytes a multiple of 16.
+int item_heads(int limit, int row_bytes) {
+    int unit = 1;
+    while (unit * row_bytes % 16) unit *= 2;
+    return limit / row_bytes / unit * unit;
+}
+
+// Blocks of queries and of keys in the proportion of their work.
+void share_blocks(long long wq, long long wk, long long most, long long &qb, long long &kb) {
+    qb = wq, kb = wk;
+    if (wq + wk <= most) return;
+    qb = wq ? most * wq / (wq + wk) : 0;
+    if (wq && qb < 1) qb = 1;
+    if (wk && qb > most - 1) qb = most - 1;
+    kb = wk ? most - qb : 0;
+}
+
+cudaError_t launch_dw(const RotArgs &a, long long qb, long long kb, float *dwq, float *dwk, cudaStream_t st) {
+    return launch_pdl(rotary_dw_kernel, dim3((a.D + 7) / 8, 2), 256, 0, st, (const float *)a.partial, (int)qb, (int)(qb + kb), a.D,
+                      dwq, dwk);
+}
+
+template <typename T, int G, bool INTER>
+cudaError_t run_stream(RotArgs &a, bool backward, float *dwq, float *dwk, cudaStream_t st) {
+    for (int p = 0; p < 2; ++p) a.segs[p] = (a.heads[p] + a.per - 1) / a.per;
+    const size_t smem = (size_t)SWARPS * STAGES * (backward ? 2 * BWD_ITEM : FWD_ITEM);
+    cudaError_t e;
+    if (!backward) {
+        e = cudaFuncSetAttribute(rotary_stream_fwd_kernel<T, G, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        const long long blocks = (a.T * (a.segs[0] + a.segs[1]) + SWARPS - 1) / SWARPS;
+        return launch_pdl(rotary_stream_fwd_kernel<T, G, INTER>, dim3((unsigned)(blocks < 304 ? blocks : 304)), SWARPS * 32, smem,
+                          st, a);
+    }
+    e = cudaFuncSetAttribute(rotary_stream_bwd_kernel<T, G, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    long long qb, kb;
+    share_blocks((a.T * a.segs[0] + SWARPS - 1) / SWARPS, (a.T * a.segs[1] + SWARPS - 1) / SWARPS, 304, qb, kb);
+    e = launch_pdl(rotary_stream_bwd_kernel<T, G, INTER>, dim3((unsigned)(qb + kb)), SWARPS * 32, smem, st, a, (int)qb);
+    return e == cudaSuccess && (dwq || dwk) ? launch_dw(a, qb, kb, dwq, dwk, st) : e;
+}
+
 template <typename T, int V, int G, bool INTER>
 cudaError_t run_group(RotArgs &a, bool backward, float *dwq, float *dwk, cudaStream_t st) {
     constexpr int NG = RT / G;
+    if constexpr (V == 4)
+        if (a.stream) return run_stream<T, G, INTER>(a, backward, dwq, dwk, st);
+    // heads per group: four, all in flight; fewer where the call is too small
+    // to fill the SMs (152 x 1024 lanes), down to one
+    a.per = ROWS;
+    while (a.per > 1 && a.T * ((a.heads[0] + a.heads[1]) / a.per) * G < 152 * 1024) a.per /= 2;
+    for (int p = 0; p < 2; ++p) a.segs[p] = (a.heads[p] + a.per - 1) / a.per;
     if (!backward) {
         const long long groups = a.T * (a.segs[0] + a.segs[1]);
         return launch_pdl(rotary_fwd_kernel<T, V, G, INTER>, dim3((unsigned)((groups + NG - 1) / NG)), RT, 0, st, a);
     }
-    const long long wq = (a.T * a.segs[0] + NG - 1) / NG, wk = (a.T * a.segs[1] + NG - 1) / NG;
-    // blocks in the proportion of the work, one wave at most
-    long long qb = wq, kb = wk;
-    if (wq + wk > BWD_BLOCKS) {
-        qb = wq ? BWD_BLOCKS * wq / (wq + wk) : 0;
-        if (wq && qb < 1) qb = 1;
-        if (wk && qb > BWD_BLOCKS - 1) qb = BWD_BLOCKS - 1;
-        kb = wk ? BWD_BLOCKS - qb : 0;
-    }
-    a.want_dw[0] = dwq != nullptr;
-    a.want_dw[1] = dwk != nullptr;
-    cudaError_t e = launch_pdl(rotary_bwd_kernel<T, V, G, INTER>, dim3((unsigned)(qb + kb)), RT,
-                               sizeof(float) * NG * a.D, st, a, (int)qb);
-    if (e == cudaSuccess && (dwq || dwk))
-        e = launch_pdl(rotary_dw_kernel, dim3((a.D + 7) / 8, 2), 256, 0, st, (const float *)a.partial, (int)qb,
-                       (int)(qb + kb), a.D, dwq, dwk);
-    return e;
+    long long qb, kb;
+    share_blocks((a.T * a.segs[0] + NG - 1) / NG, (a.T * a.segs[1] + NG - 1) / NG, BWD_BLOCKS, qb, kb);
+    const cudaError_t e =
+        launch_pdl(rotary_bwd_kernel<T, V, G, INTER>, dim3((unsigned)(qb + kb)), RT, sizeof(float) * NG * a.D, st, a, (int)qb);
+    return e == cudaSuccess && (dwq || dwk) ? launch_dw(a, qb, kb, dwq, dwk, st) : e;
 }
 
 template <typename T, int V, bool INTER>
 cudaError_t run_vec(RotArgs &a, bool backward, float *dwq, float *dwk, cudaStream_t st) {
     const int lanes = (a.D / (2 * V) + SLOTS<V> - 1) / SLOTS<V>;
     // odd sizes (V of 1 or 2) take whole warps; else the least power of two
-    if constexpr (V == 8)
-        if (lanes <= 4) return run_group<T, V, 4, INTER>(a, backward, dwq, dwk, st);
-    if constexpr (V >= 4) {
+    if constexpr (V == 4) {
         if (lanes <= 8) return run_group<T, V, 8, INTER>(a, backward, dwq, dwk, st);
         if (lanes <= 16) return run_group<T, V, 16, INTER>(a, backward, dwq, dwk, st);
     }
-    if constexpr (V < 8) return run_group<T, V, 32, INTER>(a, backward, dwq, dwk, st);
-    return cudaErrorInvalidValue;   // V = 8: at most 16 lanes
+    return run_group<T, V, 32, INTER>(a, backward, dwq, dwk, st);
 }
 
 template <typename T>
-cudaError_t run_type(RotArgs &a, int V, bool inter, bool backward, float *dwq, float *dwk, cudaStream_t st) {
-    // heads per group: eight, so that a token's angles are paid once for
-    // eight rows; fewer where the call is too small to fill the SMs
-    // (152 x 2048 lanes), down to one
-    const int lanes = a.D / (2 * V) < 32 ? a.D / (2 * V) : 32;
-    a.per = 8;
-    while (a.per > 1 && a.T * ((a.heads[0] + a.heads[1]) / a.per) * lanes < 152 * 2048) a.per /= 2;
-    for (int p = 0; p < 2; ++p) a.segs[p] = (a.heads[p] + a.per - 1) / a.per;
+cudaError_t run_type(RotArgs &a, bool inter, const long long *lds, int nld, bool backward, float *dwq, float *dwk, cudaStream_t st) {
+    const int V = vec_width(a.D, a.rot, inter, lds, nld);
+    // Streaming needs 16-byte pitches and head groups, and enough rows to run
+    // the rings
+    a.want_dw[0] = dwq != nullptr;
+    a.want_dw[1] = dwk != nullptr;
+    const int row = a.D * (int)sizeof(T);
+    bool ok = V == 4 && a.T * (a.heads[0] + a.heads[1]) * row >= (backward ? STREAM_BWD : STREAM_FWD);
+    for (int i = 0; i < nld; ++i) ok = ok && lds[i] * (long long)sizeof(T) % 16 == 0;
+    for (int p = 0; p < 2; ++p) ok = ok && a.heads[p] * row % 16 == 0;
+    a.stream = ok;
+    if (ok) a.per = item_heads(backward ? BWD_ITEM : FWD_ITEM, row);
 #define S5_ROT(VV) \
     return inter ? run_vec<T, VV, true>(a, backward, dwq, dwk, st) : run_vec<T, VV, false>(a, backward, dwq, dwk, st)
-    if constexpr (sizeof(T) == 2)
-        if (V == 8) S5_ROT(8);
     if (V == 4) S5_ROT(4);
     if (V == 2) S5_ROT(2);
     S5_ROT(1);
 #undef S5_ROT
+}
+
+cudaError_t run(RotArgs &a, s5_dtype dtype, bool inter, const long long *lds, int nld, bool backward, float *dwq, float *dwk,
+                cudaStream_t st) {
+    return dtype == S5_BF16 ? run_type<__nv_bfloat16>(a, inter, lds, nld, backward, dwq, dwk, st)
+                            : run_type<float>(a, inter, lds, nld, backward, dwq, dwk, st);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -552,10 +885,9 @@ extern "C" s5_status s5_rotary(const void *x, long long ldx, s5_dtype dtype, con
     a.amp = amplitude, a.turn = inverse ? -1.0f : 1.0f;
     const long long lds[2] = {ldx, ldy};
     const bool inter = layout == S5_ROTARY_INTERLEAVED;
-    const int V = vec_width(dtype == S5_BF16 ? 2 : 4, D, rot, inter, lds, 2);
+    const int nld = 2;
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = dtype == S5_BF16 ? run_type<__nv_bfloat16>(a, V, inter, false, nullptr, nullptr, st)
-                                           : run_type<float>(a, V, inter, false, nullptr, nullptr, st);
+    const cudaError_t e = run(a, dtype, inter, lds, nld, false, nullptr, nullptr, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
 
@@ -581,14 +913,13 @@ extern "C" s5_status s5_qk_norm_rotary(const void *q, long long ldq, const void 
     a.ldx[0] = ldq, a.ldx[1] = ldk, a.ldy[0] = ldqo, a.ldy[1] = ldko;
     a.heads[0] = Hq, a.heads[1] = Hk;
     a.pos = positions, a.freq = freq, a.T = T, a.D = D, a.rot = rot;
-    a.count = norm == S5_NORM_RMS ? D : norm == S5_NORM_L2 ? 1 : 0;
+    a.inv = norm == S5_NORM_RMS ? 1.0f / D : norm == S5_NORM_L2 ? 1.0f : 0.0f;
     a.eps = eps, a.amp = amplitude, a.turn = 1.0f;
     const long long lds[4] = {Hq ? ldq : 0, Hk ? ldk : 0, Hq ? ldqo : 0, Hk ? ldko : 0};
     const bool inter = layout == S5_ROTARY_INTERLEAVED;
-    const int V = vec_width(dtype == S5_BF16 ? 2 : 4, D, rot, inter, lds, 4);
+    const int nld = 4;
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = dtype == S5_BF16 ? run_type<__nv_bfloat16>(a, V, inter, false, nullptr, nullptr, st)
-                                           : run_type<float>(a, V, inter, false, nullptr, nullptr, st);
+    const cudaError_t e = run(a, dtype, inter, lds, nld, false, nullptr, nullptr, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
 
@@ -632,14 +963,20 @@ extern "C" s5_status s5_qk_norm_rotary_backward(
     a.ldx[0] = ldq, a.ldx[1] = ldk, a.ldy[0] = lddq, a.ldy[1] = lddk, a.lddy[0] = lddqo, a.lddy[1] = lddko;
     a.heads[0] = Hq, a.heads[1] = Hk;
     a.pos = positions, a.freq = freq, a.T = T, a.D = D, a.rot = rot;
-    a.count = norm == S5_NORM_RMS ? D : norm == S5_NORM_L2 ? 1 : 0;
+    a.inv = norm == S5_NORM_RMS ? 1.0f / D : norm == S5_NORM_L2 ? 1.0f : 0.0f;
     a.eps = eps, a.amp = amplitude, a.turn = -1.0f;
     a.partial = static_cast<float *>(workspace);
     const long long lds[6] = {Hq ? ldq : 0,  Hk ? ldk : 0,  Hq ? lddqo : 0,
                               Hk ? lddko : 0, Hq ? lddq : 0, Hk ? lddk : 0};
     const bool inter = layout == S5_ROTARY_INTERLEAVED;
-    const int V = vec_width(dtype == S5_BF16 ? 2 : 4, D, rot, inter, lds, 6);
-    const cudaError_t e = dtype == S5_BF16 ? run_type<__nv_bfloat16>(a, V, inter, true, dq_weight, dk_weight, st)
-                                           : run_type<float>(a, V, inter, true, dq_weight, dk_weight, st);
+    const int nld = 6;
+    const cudaError_t e = run(a, dtype, inter, lds, nld, true, dq_weight, dk_weight, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
+}
+
+extern "C" int s5_rotary_fault(void) {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_rotary_fault, sizeof(int)) != cudaSuccess) return -1;
+    if (v && cudaMemcpyToSymbol(g_rotary_fault, &zero, sizeof(int)) != cudaSuccess) return -1;
+    return v;
 }

@@ -458,6 +458,11 @@ s5_status s5_qk_norm_rotary(const void *q, long long ldq, const void *k, long lo
                             s5_rotary_layout layout, float amplitude, long long T, int Hq, int Hk, int D,
                             void *q_out, long long ldqo, void *k_out, long long ldko, s5_stream_t stream);
 
+/* 1 if a wait for a copy inside the rotation kernels ran out since the last
+ * call (their results are then not valid), 0 if none; the flag is cleared.
+ * Synchronises the device. */
+int s5_rotary_fault(void);
+
 /* Workspace of the backward pass, needed where a weight's gradient is wanted. */
 size_t s5_qk_norm_rotary_workspace_size(int D);
 

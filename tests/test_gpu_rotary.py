@@ -2,8 +2,8 @@
 
 Tolerances (rel-L2).  An fp32 result passes at most 16 roundings of 2^-24 (sum
 of squares over a group of lanes, root, weight, angle of 2^-25 half turns =
-2^-23.3 radians, products); a weight's gradient sums up to 1000 rows in parts:
-64.  bf16 outputs get one rounding of 2^-8 besides.
+2^-23.3 radians, products); a weight's gradient sums the rows in parts, up to
+100 in a row in each: 64.  bf16 outputs get one rounding of 2^-8 besides.
 """
 import numpy as np
 import pytest
@@ -119,6 +119,38 @@ def test_qk_norm_rotary_and_backward(case, layout, weighted, dt):
             check(host(g["dw" + n]), dw, DW, "dw" + n)
         else:
             assert g["dw" + n] is None
+
+
+# Sizes from which on the rows stream through shared memory: several segments a
+# token, a last one that is not full, items that do not divide among the warps
+BIG = [(2, 4501, 12, 3, 128, 128, "rms", "half"), (1, 8100, 33, 1, 64, 32, "l2", "interleaved"),
+       (3, 500, 40, 8, 256, 256, "rms", "interleaved"), (1, 14099, 9, 7, 80, 48, "l2", "half"),
+       (1, 37000, 0, 5, 96, 96, "rms", "half"), (1, 19001, 7, 0, 128, 64, None, "interleaved")]
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("case", BIG)
+def test_large_qk_norm_rotary_and_backward(case, dt):
+    test_qk_norm_rotary_and_backward(case[:-1], case[-1], True, dt)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_large_rotary_from_and_into_views(dt):
+    """Pitches of a fused projection, a larger output, and in place."""
+    B, L, H, D = 1, 16007, 9, 128
+    fused = torch.full((B, L, 2 * H * D + 64), float("nan"), device="cuda", dtype=dt)
+    x = fused[:, :, 64:64 + H * D].unflatten(-1, (H, D))
+    x.copy_(torch.randn(B, L, H, D, device="cuda"))
+    vx, pos = host(x), torch.arange(L, device="cuda")[None] * 7
+    freq = init.rotary_frequencies(128)[0]
+    want = ref.turn(vx, pos.cpu().numpy(), freq, "half", 1.0)
+    y = api.s5_rotary(x, pos, torch.from_numpy(freq).cuda())
+    check(host(y), want, tol(dt), "y")
+    wide = torch.zeros(B, L, H * D + 8, device="cuda", dtype=dt)
+    api.s5_rotary(x, pos, torch.from_numpy(freq).cuda(), out=wide[:, :, :H * D].unflatten(-1, (H, D)))
+    assert torch.equal(wide[:, :, :H * D], y.flatten(-2)) and torch.count_nonzero(wide[:, :, H * D:]) == 0
+    api.s5_rotary(x, pos, torch.from_numpy(freq).cuda(), out=x)
+    assert torch.equal(x, y) and torch.isnan(fused[:, :, :64]).all() and torch.isnan(fused[:, :, 64 + H * D:]).all()
 
 
 def test_zero_rows_and_infinities_stay_in_their_rows():
