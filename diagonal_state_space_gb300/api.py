@@ -243,6 +243,8 @@ def _new(t):
 
 def _rows(t, name, dtype=None, shape=None):
     """(address, elements between two tokens) of a [..., H, D] array."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr(), shape[-1] * shape[-2]
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if dtype is not None and t.dtype != dtype:
@@ -386,10 +388,12 @@ _NORM = {None: 0, "none": 0, "rms": 1, "l2": 2}
 def _rot_args(x, name, positions, freq):
     if not isinstance(x, torch.Tensor) or x.dim() < 3 or x.dtype not in _DT:
         raise ValueError("%s must be a float32 or bfloat16 array [..., H, D]" % name)
-    T = math.prod(x.shape[:-2])
+    lead = x.shape[:-2]
+    T = math.prod(lead)
     if freq is None:
         return T, None, None, 0
-    return T, _arr(positions, "positions", torch.int64, x.shape[:-2]), _ptr(freq, "freq", torch.float64), 2 * freq.numel()
+    n = freq.shape[0] if isinstance(freq, torch.Tensor) and freq.dim() == 1 else -1
+    return T, _arr(positions, "positions", torch.int64, lead), _arr(freq, "freq", torch.float64, (n,)), 2 * n
 
 
 def s5_rotary(x, positions, freq, layout="half", amplitude=1.0, inverse=False, out=None, stream=None):
@@ -400,7 +404,7 @@ def s5_rotary(x, positions, freq, layout="half", amplitude=1.0, inverse=False, o
     H, D = x.shape[-2:]
     if out is None:
         out = _new(x)
-    code = _native.lib().s5_rotary(*_rows(x, "x"), _DT[x.dtype], pos, fr, rot, _LAYOUT[layout], float(amplitude),
+    code = _native.lib().s5_rotary(*_rows(x, "x", x.dtype, x.shape), _DT[x.dtype], pos, fr, rot, _LAYOUT[layout], float(amplitude),
                                    int(inverse), T, H, D, *_rows(out, "out", x.dtype, x.shape), _on(stream, out))
     check("s5_rotary", code)
     return out
@@ -412,15 +416,16 @@ def s5_qk_norm_rotary(q, k, positions, freq, norm="rms", eps=1e-6, q_weight=None
     q [..., Hq, D] and k [..., Hk, D] in one launch.  freq None: no rotation.  q_out may be q, k_out may be k."""
     T, pos, fr, rot = _rot_args(q, "q", positions, freq)
     (Hq, D), Hk, dt, f32 = q.shape[-2:], k.shape[-2], q.dtype, torch.float32
-    kshape = (*q.shape[:-2], Hk, D)
+    kshape = torch.Size((*q.shape[:-2], Hk, D))
     if q_out is None:
         q_out = _new(q)
     if k_out is None:
-        k_out = torch.empty(kshape, dtype=dt, device=q.device)
+        k_out = _new(k)
     code = _native.lib().s5_qk_norm_rotary(
-        *_rows(q, "q"), *_rows(k, "k", dt, kshape), _DT[dt], _ptr(q_weight, "q_weight", f32, (D,), True),
-        _ptr(k_weight, "k_weight", f32, (D,), True), _NORM[norm], float(eps), pos, fr, rot, _LAYOUT[layout],
-        float(amplitude), T, Hq, Hk, D, *_rows(q_out, "q_out", dt, q.shape), *_rows(k_out, "k_out", dt, kshape),
+        *_rows(q, "q", dt, q.shape), *_rows(k, "k", dt, kshape), _DT[dt],
+        None if q_weight is None else _arr(q_weight, "q_weight", f32, (D,)),
+        None if k_weight is None else _arr(k_weight, "k_weight", f32, (D,)), _NORM[norm], float(eps), pos, fr, rot,
+        _LAYOUT[layout], float(amplitude), T, Hq, Hk, D, *_rows(q_out, "q_out", dt, q.shape), *_rows(k_out, "k_out", dt, kshape),
         _on(stream, q_out, k_out))
     check("s5_qk_norm_rotary", code)
     return q_out, k_out
