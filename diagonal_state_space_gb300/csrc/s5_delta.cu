@@ -33,6 +33,10 @@ namespace {
 constexpr int TB = 16;        // tokens staged in shared memory
 constexpr int OWN = 32;       // columns (or rows) of a block
 constexpr int SWT = 128;      // threads of a sweep: 16 lanes x 8 groups of 4
+// Heads (B Hv) from which on a step takes a block for each, against a block for
+// 32 columns: 3.8 / 4.5 us at 96 heads of 128 x 128, 3.7 / 3.2 at 64, 63 / 77 at
+// 3072 (6.4 TB/s).
+constexpr int HEAD_BLOCKS = 80;
 
 // Sums of four values over 16 lanes; lane l gets the sum of value l / 4 % 4.
 __device__ __forceinline__ float sum4_16(const float (&v)[4], int lane) {
@@ -409,6 +413,114 @@ __global__ void __launch_bounds__(256) delta_step_kernel(const void *q, const vo
     }
 }
 
+// The same for a whole head a block (heads up to 128 x 128): 256 threads hold
+// the 64 KB of its state, LR lanes of four columns by 256 / LR rows at a time,
+// read and written with streaming hints; 128 KB an SM in flight.  For few
+// heads the blocks above spread the state over more SMs (launch rule).
+template <typename T, int LR>
+__global__ void __launch_bounds__(256, 2) delta_step_head_kernel(const void *q, const void *k, const void *v, const float *g,
+                                                                 const float *beta, float scale, int Hk, int Hv, int Dk,
+                                                                 int Dv, float *state, void *o) {
+    constexpr int RG = 256 / LR, RPT = 128 / RG;
+    __shared__ float4 rk[8][LR], rq[8][LR];
+    __shared__ float rd[8];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, cv = lane % LR, rg = threadIdx.x / LR;
+    const int col = cv * 4, h = blockIdx.x % Hv, b = blockIdx.x / Hv, hk = h / (Hv / Hk);
+    const long long bh = blockIdx.x;
+    const bool on = col < Dv;
+    float *s = state + bh * (long long)Dk * Dv + col;
+    const long long kb = ((long long)b * Hk + hk) * Dk;
+    griddep_wait();
+    griddep_launch_dependents();
+    float4 S[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = rg + RG * i;
+        S[i] = (on && r < Dk) ? __ldcs(reinterpret_cast<const float4 *>(s + (long long)r * Dv)) : make_float4(0, 0, 0, 0);
+    }
+    const float al = expf(clamp_g(g[bh])), be = beta[bh];
+    float vv[4] = {0, 0, 0, 0};
+    if (on)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) vv[c] = elem<T>(v, bh * Dv + col + c);
+    // lane c of a row group holds k and q of the group's row c (c < RPT)
+    const int mine = rg + RG * cv;
+    float kl = 0.0f, ql = 0.0f;
+    if (cv < RPT && mine < Dk) kl = elem<T>(k, kb + mine), ql = elem<T>(q, kb + mine);
+    float qk = kl * ql;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, m);
+    float4 pk = make_float4(0, 0, 0, 0), pq = pk;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const float kk = __shfl_sync(0xffffffffu, kl, i, LR), qq = __shfl_sync(0xffffffffu, ql, i, LR);
+        pk.x = fmaf(S[i].x, kk, pk.x), pk.y = fmaf(S[i].y, kk, pk.y);
+        pk.z = fmaf(S[i].z, kk, pk.z), pk.w = fmaf(S[i].w, kk, pk.w);
+        pq.x = fmaf(S[i].x, qq, pq.x), pq.y = fmaf(S[i].y, qq, pq.y);
+        pq.z = fmaf(S[i].z, qq, pq.z), pq.w = fmaf(S[i].w, qq, pq.w);
+    }
+    if (LR == 16) {
+        pk.x += __shfl_xor_sync(0xffffffffu, pk.x, 16), pk.y += __shfl_xor_sync(0xffffffffu, pk.y, 16);
+        pk.z += __shfl_xor_sync(0xffffffffu, pk.z, 16), pk.w += __shfl_xor_sync(0xffffffffu, pk.w, 16);
+        pq.x += __shfl_xor_sync(0xffffffffu, pq.x, 16), pq.y += __shfl_xor_sync(0xffffffffu, pq.y, 16);
+        pq.z += __shfl_xor_sync(0xffffffffu, pq.z, 16), pq.w += __shfl_xor_sync(0xffffffffu, pq.w, 16);
+    }
+    if (lane < LR) rk[warp][cv] = pk, rq[warp][cv] = pq;
+    if (lane == 0) rd[warp] = qk;
+    __syncthreads();
+    pk = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const float4 x = rk[w][cv];
+        pk.x += x.x, pk.y += x.y, pk.z += x.z, pk.w += x.w;
+    }
+    const float ux = be * (vv[0] - al * pk.x), uy = be * (vv[1] - al * pk.y), uz = be * (vv[2] - al * pk.z),
+                uw = be * (vv[3] - al * pk.w);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = rg + RG * i;
+        const float kk = __shfl_sync(0xffffffffu, kl, i, LR);
+        if (on && r < Dk)
+            __stcs(reinterpret_cast<float4 *>(s + (long long)r * Dv),
+                   make_float4(fmaf(kk, ux, al * S[i].x), fmaf(kk, uy, al * S[i].y), fmaf(kk, uz, al * S[i].z),
+                               fmaf(kk, uw, al * S[i].w)));
+    }
+    if (on && threadIdx.x < LR) {
+        pq = make_float4(0, 0, 0, 0), qk = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const float4 y = rq[w][cv];
+            pq.x += y.x, pq.y += y.y, pq.z += y.z, pq.w += y.w;
+            qk += rd[w];
+        }
+        T *out = static_cast<T *>(o) + bh * Dv + col;
+        store_elem<T>(out, scale * fmaf(al, pq.x, qk * ux));
+        store_elem<T>(out + 1, scale * fmaf(al, pq.y, qk * uy));
+        store_elem<T>(out + 2, scale * fmaf(al, pq.z, qk * uz));
+        store_elem<T>(out + 3, scale * fmaf(al, pq.w, qk * uw));
+    }
+}
+
+template <typename T>
+cudaError_t step(const void *q, const void *k, const void *v, const float *g, const float *beta, float scale, int B, int Hk,
+                 int Hv, int Dk, int Dv, float *state, void *o, cudaStream_t st) {
+    cudaLaunchAttribute attr;
+    set_programmatic(attr);
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (Dk <= 128 && Dv <= 128 && (long long)B * Hv >= HEAD_BLOCKS) {
+        cfg.gridDim = dim3(B * Hv);
+        return Dv > 64 ? cudaLaunchKernelEx(&cfg, delta_step_head_kernel<T, 32>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o)
+                       : cudaLaunchKernelEx(&cfg, delta_step_head_kernel<T, 16>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o);
+    }
+    cfg.gridDim = dim3((Dv + 31) / 32, Hv, B);
+    return Dk > 128 ? cudaLaunchKernelEx(&cfg, delta_step_kernel<T, 8>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o)
+                    : cudaLaunchKernelEx(&cfg, delta_step_kernel<T, 4>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o);
+}
+
 template <typename T, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
     const dim3 grid((a.Dv + OWN - 1) / OWN, a.Hv, a.B);
     if (a.Dk <= 64)
@@ -613,21 +725,8 @@ extern "C" s5_status s5_delta_step(const void *q, const void *k, const void *v, 
     for (const void *p : rows)
         if (!p || (reinterpret_cast<uintptr_t>(p) & four)) return S5_ERR_INVALID_ARGUMENT;
     if (!floats(g) || !floats(beta) || !aligned16(state)) return S5_ERR_INVALID_ARGUMENT;
-    cudaLaunchAttribute attr;
-    set_programmatic(attr);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((Dv + 31) / 32, Hv, B);
-    cfg.blockDim = dim3(256);
-    cfg.stream = (cudaStream_t)stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const bool wide = Dk > 128;
-    cudaError_t e;
-    if (dtype == S5_BF16)
-        e = wide ? cudaLaunchKernelEx(&cfg, delta_step_kernel<__nv_bfloat16, 8>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o)
-                 : cudaLaunchKernelEx(&cfg, delta_step_kernel<__nv_bfloat16, 4>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o);
-    else
-        e = wide ? cudaLaunchKernelEx(&cfg, delta_step_kernel<float, 8>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o)
-                 : cudaLaunchKernelEx(&cfg, delta_step_kernel<float, 4>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o);
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = dtype == S5_BF16 ? step<__nv_bfloat16>(q, k, v, g, beta, scale, B, Hk, Hv, Dk, Dv, state, o, st)
+                                           : step<float>(q, k, v, g, beta, scale, B, Hk, Hv, Dk, Dv, state, o, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }

@@ -191,7 +191,9 @@ def test_two_calls_equal_one_and_states_may_be_in_place(dt):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("shape", [(1, 1, 1, 4, 4), (3, 2, 6, 48, 80), (2, 2, 4, 128, 128), (1, 1, 2, 256, 132), (9, 1, 3, 64, 36)])
+@pytest.mark.parametrize("shape", [(1, 1, 1, 4, 4), (3, 2, 6, 48, 80), (2, 2, 4, 128, 128), (1, 1, 2, 256, 132), (9, 1, 3, 64, 36),
+                                   (17, 2, 4, 128, 128), (33, 1, 2, 48, 80), (11, 3, 6, 64, 64), (70, 1, 1, 20, 12),
+                                   (64, 1, 1, 128, 68)])
 def test_step(shape, dt):
     B, Hk, Hv, Dk, Dv = shape
     d, v = make(B, 6, Hk, Hv, Dk, Dv, dt=dt, seed=31, gates="resets")
