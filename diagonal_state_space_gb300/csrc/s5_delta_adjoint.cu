@@ -277,8 +277,8 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
 }
 
 // ---------------------------------------------------------------------------
-// What is local to a chunk, all chunks at once: one CTA per chunk and key head,
-// over its value heads.  Per token dv = beta X, dbeta = X . e and
+// What is local to a chunk: persistent CTAs over chunks and key heads, each
+// over its value heads, the next head's tiles on their way to L2.  Per token dv = beta X, dbeta = X . e and
 // o . dO - v . dv (for the decays, s5_delta.cu).  With S0 and Z the state at
 // the chunk's start and the adjoint at its end, U = beta e, and
 // N_ij = scale D_ij dO_i.U_j (j <= i), W_ij = -D_ij dv_i.U_j (j < i):
@@ -302,22 +302,55 @@ template <int DK, int DV> struct LocalSmem {
     static constexpr uint32_t U_IMG = 64 * 128 * (DV / 64);
     static constexpr uint32_t S_IMG = DK * 128 * (DV / 64);
     static constexpr uint32_t kq = 0;                          // 64 keys, then 64 queries
-    static constexpr uint32_t a = kq + KQ;                     // two parts; [W; N], two parts, later
-    static constexpr uint32_t u = a + 2 * A_IMG;
-    static constexpr uint32_t s = u + 2 * U_IMG;               // Z, then S0: two parts
+    static constexpr uint32_t a = kq + KQ;                     // two parts
+    static constexpr uint32_t u = a + 2 * A_IMG;               // two parts; where they fit, those of [W; N] later
+    static constexpr bool APART = U_IMG < M2_BYTES;            // [W; N] gets a place of its own
+    static constexpr uint32_t wn = APART ? u + 2 * U_IMG : u;
+    static constexpr uint32_t s = wn + 2 * (APART ? M2_BYTES : U_IMG);   // Z, then S0: two parts
     static constexpr uint32_t meta = s + 2 * S_IMG;
     static constexpr uint32_t bars = meta + META_BYTES;
     static constexpr uint32_t total = bars + 64 + 1024;
     static_assert(total <= 232448, "shared memory of a CTA");
-    static_assert(A_IMG >= M2_BYTES, "[W; N] fits");
-    static_assert(2 * S_IMG >= 8192, "M = 128 over the 64 rows of U reads 8 KB on");
+    // products of M = 128 over 64 rows or columns read on into what follows:
+    // 8 KB past U, 16 KB past [W; N]
+    static_assert(2 * S_IMG >= M2_BYTES, "what the products read on is the CTA's own memory");
 };
 
 struct LocalBars {
-    uint64_t z_full, first, second;
+    uint64_t z_full, first, second, third;
     uint32_t tmem;
     int abort;
 };
+
+__device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// The tiles of a chunk and value head, line by line over the block's threads
+// (a bulk prefetch for each row costs the SM 25 cycles a row).
+template <int DK, int DV>
+__device__ __forceinline__ void prefetch_head(const Args &a, int c, int b, int h, bool rows_too, int N, int tid) {
+    const int nt = min(C, a.L - c * C), hk = h / (a.Hv / a.Hk);
+    const long long row0 = (long long)b * a.L + c * C, bh = (long long)b * a.Hv + h;
+    constexpr int RL = DV / 32, HL = DV / 64, KL = DK / 64;   // lines of a row of floats, of bf16
+    for (int i = tid; i < C * 8; i += LT) {      // eight threads a token
+        const int t = i / 8, k = i % 8;
+        if (t >= nt) continue;
+        const long long at = ((row0 + t) * a.Hv + h) * DV;
+        if (k < RL) prefetch_line(a.x + at + k * 32), prefetch_line(a.e + at + k * 32), prefetch_line(a.o32 + at + k * 32);
+        if (k < HL) {
+            prefetch_line(static_cast<const __nv_bfloat16 *>(a.dout) + (row0 + t) * a.lddo + (long long)h * DV + k * 64);
+            prefetch_line(static_cast<const __nv_bfloat16 *>(a.v) + (row0 + t) * a.ldv + (long long)h * DV + k * 64);
+        }
+        if (rows_too && k >= 4 && k < 4 + KL) {
+            prefetch_line(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + (k - 4) * 64);
+            prefetch_line(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + (k - 4) * 64);
+        }
+    }
+    const char *s = reinterpret_cast<const char *>(a.states + (bh * (N + 1) + c) * DK * DV);
+    const char *z = static_cast<const char *>(a.z) + (bh * N + c) * DK * DV * 4;
+#pragma unroll
+    for (int i = 0; i < DK * DV / 32 / LT + (DK * DV / 32 % LT != 0); ++i)
+        if (tid + i * LT < DK * DV / 32) prefetch_line(s + (tid + i * LT) * 128), prefetch_line(z + (tid + i * LT) * 128);
+}
 
 // Eight values as a 16-byte piece of two images.
 __device__ __forceinline__ void put2(uint32_t img, uint32_t stride, int row, int j, const float (&v)[8]) {
@@ -339,224 +372,250 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     LocalBars *lb = reinterpret_cast<LocalBars *>(smem + L::bars);
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, group = a.Hv / a.Hk;
-    const int t0 = c * C, nt = min(C, a.L - t0), N = chunks(a.L);
-    const long long row0 = (long long)b * a.L + t0, mat = (long long)DK * DV;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
+    const int N = chunks(a.L), group = a.Hv / a.Hk;
+    const long long mat = (long long)DK * DV;
+    const int items = N * a.Hk * a.B;   // below 2^30: a token and value head each at least
     if (tid == 0) {
         mbar_init(&lb->z_full, 1);
         mbar_init(&lb->first, 1);
         mbar_init(&lb->second, 1);
+        mbar_init(&lb->third, 1);
         lb->abort = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
+        __syncwarp();
         tmem_alloc(&lb->tmem, 512);
         tmem_relinquish();
-    }
-    const uint32_t kq = smem_addr(smem + L::kq), sA = smem_addr(smem + L::a), sU = smem_addr(smem + L::u),
-                   sS = smem_addr(smem + L::s);
-    for (int i = tid; i < 128 * (DK / 8); i += LT) {
-        const int r = i / (DK / 8), d = i % (DK / 8) * 8, t = r & 63;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (t < nt)
-            v = r < C ? *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + d)
-                      : *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + d);
-        sts128(piece(kq + d / 64 * KQ_BOX, r, d % 64 / 8), v.x, v.y, v.z, v.w);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const uint32_t kq = smem_addr(smem + L::kq), sA = smem_addr(smem + L::a), sU = smem_addr(smem + L::u),
+                   sS = smem_addr(smem + L::s), sW = smem_addr(smem + L::wn);
     const uint32_t tmem = lb->tmem, D1 = tmem, D2 = tmem + 128, D4 = tmem + 256, D3 = tmem + 384, D5 = tmem + 384;
-    const uint64_t A0 = desc_k(sA), AT = desc_mn(sA, M2_BYTES), U0 = desc_k(sU), S0 = desc_k(sS), cols = desc_mn(kq, KQ_BOX);
+    const uint64_t A0 = desc_k(sA), W0 = desc_k(sW), WT = desc_mn(sW, M2_BYTES), U0 = desc_k(sU), S0 = desc_k(sS),
+                   cols = desc_mn(kq, KQ_BOX);
     Meta *meta = reinterpret_cast<Meta *>(smem + L::meta);
     auto wait = [&](uint64_t *bar, int parity) { return bounded_wait(bar, (uint32_t)parity, &lb->abort); };
-    // warp w: TMEM lanes 32 (w % 4) on, columns 32 (w / 4) on
+    // warp w: TMEM lanes 32 (w % 4) on, columns 32 (w / 4) on; of D3 and [W; N]
+    // columns 16 (w / 4) on
     const int row = 32 * (warp & 3) + lane, c0 = warp / 4 * 32, tk = row & 63;
     const bool keys = row < C;
-    const uint32_t lanes = ((uint32_t)(32 * (warp & 3)) << 16) + c0;
-    float sum[32] = {};
+    const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
     bool ok = true;
-    for (int j = 0; j < group; ++j) {
-        const int h = hk * group + j;
-        const long long bh = (long long)b * a.Hv + h;
-        if (tid == 0) {
-            mbar_arrive_tx(&lb->z_full, 2 * L::S_IMG + META_BYTES);
-            const unsigned char *z = reinterpret_cast<const unsigned char *>(a.z) + (bh * N + c) * (2 * L::S_IMG);
-            for (int x = 0; x < DV / 64; ++x)
-                for (int p = 0; p < 2; ++p)
-                    bulk_load(smem + L::s + p * L::S_IMG + x * (DK * 128), z + (2 * x + p) * (DK * 128), DK * 128, &lb->z_full);
-            bulk_load(meta, static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES + MAT_BYTES, META_BYTES, &lb->z_full);
+    int phase = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int c = item % N, hk = item / N % a.Hk, b = item / N / a.Hk;
+        const int t0 = c * C, nt = min(C, a.L - t0);
+        const long long row0 = (long long)b * a.L + t0;
+        for (int i = tid; i < 128 * (DK / 8); i += LT) {
+            const int r = i / (DK / 8), d = i % (DK / 8) * 8, t = r & 63;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (t < nt)
+                v = r < C ? *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + d)
+                          : *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + d);
+            sts128(piece(kq + d / 64 * KQ_BOX, r, d % 64 / 8), v.x, v.y, v.z, v.w);
         }
-#pragma unroll
-        for (int n = 0; n < C * PR / LT; ++n) {
-            const int i = tid + n * LT, t = i / PR, d = i % PR * 8;
-            const long long hv = (row0 + t) * a.Hv + h;
-            float x[8] = {}, e[8] = {}, o[8] = {}, s1 = 0.0f, s2 = 0.0f, be = 0.0f;
-            uint4 g = make_uint4(0, 0, 0, 0), v = g;
-            if (t < nt) {
-                load8(a.x + hv * DV + d, x);
-                load8(a.e + hv * DV + d, e);
-                load8(a.o32 + hv * DV + d, o);
-                g = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dout) + (row0 + t) * a.lddo + (long long)h * DV + d);
-                v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) + (row0 + t) * a.ldv + (long long)h * DV + d);
-                be = a.beta[hv];
+        float sum[32] = {};
+        for (int j = 0; j < group; ++j, phase ^= 1) {
+            const int h = hk * group + j;
+            const long long bh = (long long)b * a.Hv + h;
+            if (tid == 0) {
+                mbar_arrive_tx(&lb->z_full, 2 * L::S_IMG + META_BYTES);
+                const unsigned char *z = static_cast<const unsigned char *>(a.z) + (bh * N + c) * (2 * L::S_IMG);
+                for (int x = 0; x < DV / 64; ++x)
+                    for (int p = 0; p < 2; ++p)
+                        bulk_load(smem + L::s + p * L::S_IMG + x * (DK * 128), z + (2 * x + p) * (DK * 128), DK * 128, &lb->z_full);
+                bulk_load(meta, static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES + MAT_BYTES, META_BYTES, &lb->z_full);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t gk = k < 2 ? g.x : k < 4 ? g.y : k < 6 ? g.z : g.w, vk = k < 2 ? v.x : k < 4 ? v.y : k < 6 ? v.z : v.w;
-                s1 = fmaf(x[k], e[k], s1);
-                x[k] *= be, e[k] *= be;
-                s2 = fmaf(o[k], k % 2 ? hi16(gk) : lo16(gk), s2);
-                s2 = fmaf(-(k % 2 ? hi16(vk) : lo16(vk)), x[k], s2);
-            }
-            const int box = d / 64, at = d % 64 / 8;
-            put2(sA + box * M2_BYTES, L::A_IMG, t, at, x);
-            put2(sU + box * RU_IMG, L::U_IMG, t, at, e);
-            sts128(piece(sA + box * M2_BYTES, C + t, at), g.x, g.y, g.z, g.w);
-            sts128(piece(sA + L::A_IMG + box * M2_BYTES, C + t, at), 0, 0, 0, 0);   // dO is bf16: no second part
+            for (int n = 0; n < C * PR / LT; ++n) {
+                const int i = tid + n * LT, t = i / PR, d = i % PR * 8;
+                const long long hv = (row0 + t) * a.Hv + h;
+                float x[8] = {}, e[8] = {}, o[8] = {}, s1 = 0.0f, s2 = 0.0f, be = 0.0f;
+                uint4 g = make_uint4(0, 0, 0, 0), v = g;
+                if (t < nt) {
+                    load8(a.x + hv * DV + d, x);
+                    load8(a.e + hv * DV + d, e);
+                    load8(a.o32 + hv * DV + d, o);
+                    g = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dout) + (row0 + t) * a.lddo + (long long)h * DV + d);
+                    v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) + (row0 + t) * a.ldv + (long long)h * DV + d);
+                    be = a.beta[hv];
+                }
 #pragma unroll
-            for (int m = PR / 2; m > 0; m >>= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, m), s2 += __shfl_xor_sync(0xffffffffu, s2, m);
-            if (t < nt) {
-                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dv) + (row0 + t) * a.lddv + (long long)h * DV + d) =
-                    make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-                if (d == 0) a.dbeta[hv] = s1, a.dots[hv] = s2;
-            }
-        }
-        // S0 is on its way while the first products run
-        const float *s0 = a.states + (bh * (N + 1) + c) * mat;
-        constexpr int SN = DK * DV / 8 / LT;
-        float4 sr[2 * SN];
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t gk = k < 2 ? g.x : k < 4 ? g.y : k < 6 ? g.z : g.w, vk = k < 2 ? v.x : k < 4 ? v.y : k < 6 ? v.z : v.w;
+                    s1 = fmaf(x[k], e[k], s1);
+                    x[k] *= be, e[k] *= be;
+                    s2 = fmaf(o[k], k % 2 ? hi16(gk) : lo16(gk), s2);
+                    s2 = fmaf(-(k % 2 ? hi16(vk) : lo16(vk)), x[k], s2);
+                }
+                const int box = d / 64, at = d % 64 / 8;
+                put2(sA + box * M2_BYTES, L::A_IMG, t, at, x);
+                put2(sU + box * RU_IMG, L::U_IMG, t, at, e);
+                sts128(piece(sA + box * M2_BYTES, C + t, at), g.x, g.y, g.z, g.w);
+                sts128(piece(sA + L::A_IMG + box * M2_BYTES, C + t, at), 0, 0, 0, 0);   // dO is bf16: no second part
 #pragma unroll
-        for (int n = 0; n < SN; ++n) {
-            sr[2 * n] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8);
-            sr[2 * n + 1] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8 + 4);
-        }
-        fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
+                for (int m = PR / 2; m > 0; m >>= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, m), s2 += __shfl_xor_sync(0xffffffffu, s2, m);
+                if (t < nt) {
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dv) + (row0 + t) * a.lddv + (long long)h * DV + d) =
+                        make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+                    if (d == 0) a.dbeta[hv] = s1, a.dots[hv] = s2;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncthreads();
             const uint32_t id = idesc_bf16_f32(128, DK), idU = idesc_bf16_f32(128, 64);
-#pragma unroll
-            for (int ps = 1; ps >= 0; --ps)
-#pragma unroll
-                for (int p = 0; p <= ps; ++p)
-#pragma unroll
-                    for (int k = 0; k < DV / 16; ++k)
-                        mma_bf16(D3, on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP),
-                                 on(U0, (ps - p) * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP), idU, !(ps == 1 && p == 0 && k == 0));
-            if (wait(&lb->z_full, j & 1)) {
+            if (warp == 0) {
+                const bool z = wait(&lb->z_full, phase);
+                if (elect_one()) {
 #pragma unroll
                 for (int ps = 1; ps >= 0; --ps)
 #pragma unroll
                     for (int p = 0; p <= ps; ++p)
 #pragma unroll
                         for (int k = 0; k < DV / 16; ++k)
-                            mma_bf16(D2, on(U0, p * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP),
-                                     on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id,
-                                     !(ps == 1 && p == 0 && k == 0));
+                            mma_bf16(D3, on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP),
+                                     on(U0, (ps - p) * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP), idU, !(ps == 1 && p == 0 && k == 0));
+                mma_commit(&lb->first);
+                if (z) {
+#pragma unroll
+                    for (int ps = 1; ps >= 0; --ps)
+#pragma unroll
+                        for (int p = 0; p <= ps; ++p)
+#pragma unroll
+                            for (int k = 0; k < DV / 16; ++k)
+                                mma_bf16(D2, on(U0, p * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP),
+                                         on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id,
+                                         !(ps == 1 && p == 0 && k == 0));
+                }
+                mma_commit(&lb->second);
+                }
+                __syncwarp();
             }
-            mma_commit(&lb->first);
-        }
-        __syncwarp();
-        ok = wait(&lb->first, j & 1) && wait(&lb->z_full, j & 1) && ok;
-        tc_fence_after();
-        float x[32];
-        if (c0 < 64) load_parts<1, 32>(D3 + lanes, x);
+            // S0 is on its way while the first products run
+            const float *s0 = a.states + (bh * (N + 1) + c) * mat;
+            constexpr int SN = DK * DV / 8 / LT;
+            float4 sr[2 * SN];
 #pragma unroll
-        for (int n = 0; n < SN; ++n) {
-            const int i = tid + n * LT, r = i / PR, d = i % PR * 8;
-            const float v[8] = {sr[2 * n].x,     sr[2 * n].y,     sr[2 * n].z,     sr[2 * n].w,
-                                sr[2 * n + 1].x, sr[2 * n + 1].y, sr[2 * n + 1].z, sr[2 * n + 1].w};
-            put2(sS + d / 64 * (DK * 128), L::S_IMG, r, d % 64 / 8, v);
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        const uint32_t id = idesc_bf16_f32(128, DK), idB = id | B_MN, idAB = idB | A_MN;
-        if (tid == 0) {
-#pragma unroll
-            for (int ps = 1; ps >= 0; --ps)
-#pragma unroll
-                for (int p = 0; p <= ps; ++p)
-#pragma unroll
-                    for (int k = 0; k < DV / 16; ++k)
-                        mma_bf16(D1, on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP),
-                                 on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id, !(ps == 1 && p == 0 && k == 0));
-            mma_commit(&lb->second);
-        }
-        __syncwarp();
-        if (c0 < 64) {   // [W; N]
-            const float gh = meta->hi[tk], gl = meta->lo[tk];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int col = c0 + i;
-                const bool in = keys ? col < tk : col <= tk;   // a masked product may be infinite: it is not multiplied by 0
-                x[i] = in ? (keys ? -1.0f : a.scale) * expf((gh - meta->hi[col]) + (gl - meta->lo[col])) * x[i] : 0.0f;
+            for (int n = 0; n < SN; ++n) {
+                sr[2 * n] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8);
+                sr[2 * n + 1] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8 + 4);
             }
-        }
-        ok = wait(&lb->second, 0) && ok;   // [dv; dO] has been read
-        tc_fence_after();
-        if (c0 < 64)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const float v[8] = {x[8 * n],     x[8 * n + 1], x[8 * n + 2], x[8 * n + 3],
-                                    x[8 * n + 4], x[8 * n + 5], x[8 * n + 6], x[8 * n + 7]};
-                put2(sA, M2_BYTES, row, c0 / 8 + n, v);
+            // the next head's tiles come to L2 meanwhile
+            if (j + 1 < group) {
+                prefetch_head<DK, DV>(a, c, b, h + 1, false, N, tid);
+            } else if (const int next = item + (int)gridDim.x; next < items) {
+                prefetch_head<DK, DV>(a, next % N, next / N / a.Hk, next / N % a.Hk * group, true, N, tid);
             }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (tid == 0) {
+            // [W; N]: a block of 16 columns a warp.  Decay factors of two blocks
+            // are products at the end of the columns' block, as in the preparation
+            ok = wait(&lb->z_full, phase) && wait(&lb->first, phase) && ok;
+            tc_fence_after();
+            float w[16];
+            {
+                const int nb = warp >> 2, cb = 16 * nb, rb = tk >> 4;
+                load_parts<1, 16>(D3 + quarter + cb, w);
+                const float gh = meta->hi[tk], gl = meta->lo[tk], eh = meta->hi[cb + 15], el = meta->lo[cb + 15];
+                const int mine = cb + (lane & 15);
+                const float near = expf((eh - meta->hi[mine]) + (el - meta->lo[mine]));
+                const float sign = keys ? -1.0f : a.scale, far = nb < rb ? sign * expf((gh - eh) + (gl - el)) : 0.0f;
+                const bool own = nb == rb, any = __any_sync(0xffffffffu, own);
 #pragma unroll
-            for (int p = 1; p >= 0; --p) {
-#pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-                    mma_bf16(D4, on(A0, p * M2_BYTES + k * K_STEP), on(cols, k * MN_STEP), idB, !(p == 1 && k == 0));
-#pragma unroll
-                for (int k = 0; k < 2 * C / 16; ++k)
-                    mma_bf16(D5, on(AT, p * M2_BYTES + k * MN_STEP), on(cols, k * MN_STEP), idAB, !(p == 1 && k == 0));
+                for (int i = 0; i < 16; ++i) {
+                    const int col = cb + i;
+                    float d = far * __shfl_sync(0xffffffffu, near, i);
+                    if (any)
+                        if (const float e = expf((gh - meta->hi[col]) + (gl - meta->lo[col])); own) d = sign * e;
+                    // a masked product may be infinite: it is not multiplied by 0
+                    w[i] = (keys ? col < tk : col <= tk) ? d * w[i] : 0.0f;
+                }
             }
-            mma_commit(&lb->second);
-        }
-        __syncwarp();
-        if (c0 < DK) {   // meanwhile what the earlier products give
-            const float up = meta->up[tk];
-            const float w = keys ? -up : a.scale * up, down = meta->down[tk];
-            load_parts<1, 32>(D1 + lanes, x);
+            ok = wait(&lb->second, phase) && ok;
+            tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[i] = fmaf(w, x[i], sum[i]);
-            if (keys) {
-                load_parts<1, 32>(D2 + lanes, x);
+            for (int n = 0; n < SN; ++n) {
+                const int i = tid + n * LT, r = i / PR, d = i % PR * 8;
+                const float v[8] = {sr[2 * n].x,     sr[2 * n].y,     sr[2 * n].z,     sr[2 * n].w,
+                                    sr[2 * n + 1].x, sr[2 * n + 1].y, sr[2 * n + 1].z, sr[2 * n + 1].w};
+                put2(sS + d / 64 * (DK * 128), L::S_IMG, r, d % 64 / 8, v);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float v[8] = {w[8 * n], w[8 * n + 1], w[8 * n + 2], w[8 * n + 3], w[8 * n + 4], w[8 * n + 5], w[8 * n + 6], w[8 * n + 7]};
+                put2(sW, M2_BYTES, row, 2 * (warp >> 2) + n, v);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            tc_fence_after();
+            if (warp == 0 && elect_one()) {
+                const uint32_t idB = id | B_MN, idAB = idB | A_MN;
+#pragma unroll
+                for (int p = 1; p >= 0; --p) {
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        mma_bf16(D4, on(W0, p * M2_BYTES + k * K_STEP), on(cols, k * MN_STEP), idB, !(p == 1 && k == 0));
+#pragma unroll
+                    for (int k = 0; k < 2 * C / 16; ++k)
+                        mma_bf16(D5, on(WT, p * M2_BYTES + k * MN_STEP), on(cols, k * MN_STEP), idAB, !(p == 1 && k == 0));
+                }
+#pragma unroll
+                for (int ps = 1; ps >= 0; --ps)
+#pragma unroll
+                    for (int p = 0; p <= ps; ++p)
+#pragma unroll
+                        for (int k = 0; k < DV / 16; ++k)
+                            mma_bf16(D1, on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP),
+                                     on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id, !(ps == 1 && p == 0 && k == 0));
+                mma_commit(&lb->third);
+            }
+            __syncwarp();
+            float x[32];
+            const float up = meta->up[tk], down = meta->down[tk];
+            if (c0 < DK && keys) {
+                load_parts<1, 32>(D2 + quarter + c0, x);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sum[i] = fmaf(down, x[i], sum[i]);
             }
-        }
-        ok = wait(&lb->second, 1) && ok;
-        tc_fence_after();
-        if (c0 < DK) {
-            load_parts<1, 32>(D4 + lanes, x);
+            ok = wait(&lb->third, phase) && ok;
+            tc_fence_after();
+            if (c0 < DK) {
+                const float wd = keys ? -up : a.scale * up;
+                load_parts<1, 32>(D1 + quarter + c0, x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[i] += x[i];
-            if (keys) {
-                load_parts<1, 32>(D5 + lanes, x);
+                for (int i = 0; i < 32; ++i) sum[i] = fmaf(wd, x[i], sum[i]);
+                load_parts<1, 32>(D4 + quarter + c0, x);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sum[i] += x[i];
-            }
-        }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-    }
-    if (c0 < DK && tk < nt) {
-        __nv_bfloat16 *p = keys ? static_cast<__nv_bfloat16 *>(a.dk) + (row0 + tk) * a.lddk + hk * DK + c0
-                                : static_cast<__nv_bfloat16 *>(a.dq) + (row0 + tk) * a.lddq + hk * DK + c0;
+                if (keys) {
+                    load_parts<1, 32>(D5 + quarter + c0, x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(p + 8 * j) =
-                make_uint4(pack2(sum[8 * j], sum[8 * j + 1]), pack2(sum[8 * j + 2], sum[8 * j + 3]),
-                           pack2(sum[8 * j + 4], sum[8 * j + 5]), pack2(sum[8 * j + 6], sum[8 * j + 7]));
+                    for (int i = 0; i < 32; ++i) sum[i] += x[i];
+                }
+            }
+            tc_fence_before();
+            __syncthreads();
+            tc_fence_after();
+        }
+        // out by way of shared memory (A's place), whole rows at a time
+        if (c0 < DK)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sts128(piece(sA + c0 / 64 * M2_BYTES, row, c0 % 64 / 8 + j), pack2(sum[8 * j], sum[8 * j + 1]),
+                       pack2(sum[8 * j + 2], sum[8 * j + 3]), pack2(sum[8 * j + 4], sum[8 * j + 5]), pack2(sum[8 * j + 6], sum[8 * j + 7]));
+        __syncthreads();
+        for (int i = tid; i < 128 * (DK / 8); i += LT) {
+            const int r = i / (DK / 8), d = i % (DK / 8) * 8, t = r & 63;
+            if (t >= nt) continue;
+            __nv_bfloat16 *p = r < C ? static_cast<__nv_bfloat16 *>(a.dk) + (row0 + t) * a.lddk + hk * DK + d
+                                     : static_cast<__nv_bfloat16 *>(a.dq) + (row0 + t) * a.lddq + hk * DK + d;
+            *reinterpret_cast<uint4 *>(p) = lds128(piece(sA + d / 64 * M2_BYTES, r, d % 64 / 8));
+        }
+        __syncthreads();
+        if (lb->abort) break;   // read behind a barrier: the same for all
     }
     if (!ok) settle_copies();
     __syncthreads();
@@ -566,7 +625,8 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
 template <int DK, int DV> cudaError_t launch_local(const Args &a, cudaStream_t st) {
     const cudaError_t e = big_smem(delta_local_kernel<DK, DV>, LocalSmem<DK, DV>::total);
     if (e != cudaSuccess) return e;
-    delta_local_kernel<DK, DV><<<dim3(chunks(a.L), a.Hk, a.B), LT, LocalSmem<DK, DV>::total, st>>>(a);
+    const long long items = (long long)chunks(a.L) * a.Hk * a.B;
+    delta_local_kernel<DK, DV><<<(unsigned)(items < 152 ? items : 152), LT, LocalSmem<DK, DV>::total, st>>>(a);
     return cudaGetLastError();
 }
 
