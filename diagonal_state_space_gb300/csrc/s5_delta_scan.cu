@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     ScanBars *sb = reinterpret_cast<ScanBars *>(smem + L::bars);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int n0 = blockIdx.x * SL * NV, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
     const int N = chunks(a.L);
     const long long bh = (long long)b * a.Hv + h;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
                 }
             bulk_wait_all();
             if (!ok) settle_copies();
-        } else if (warp == MMA_WARP && lane == 0) {
+        } else if (warp == MMA_WARP) {
             // ------------------------------------------------------ products
             const uint32_t w1 = idesc_bf16_f32(128, NV) | B_MN, w2 = idesc_bf16_f32(128, 2 * NV) | B_MN,
                            w3 = idesc_bf16_f32(128, 3 * NV) | B_MN;
@@ -193,35 +193,44 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
                 for (int s = 0; s < SL; ++s) {
                     const uint32_t d = tmem + s * SLICE + D1;
                     const uint64_t S = desc_mn(smem_addr(smem + L::ops + s * L::OPS), L::S_IMG);
-                    if (!ok || !(ok = wait(&sb->s_ready[s], c & 1))) break;
+                    ok = __all_sync(0xffffffffu, ok && wait(&sb->s_ready[s], c & 1));
+                    if (!ok) break;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < DK / 16; ++k) {
-                        const uint64_t A = on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP);
-                        if constexpr (P1 == 3) {
-                            mma_bf16(d, A, on(S, k * MN_STEP), w3, k > 0);
-                        } else {
-                            mma_bf16(d, A, on(S, k * MN_STEP), w2, k > 0);
-                            mma_bf16(d, A, on(S, 2 * L::S_IMG + k * MN_STEP), w1, 1);
+                        for (int k = 0; k < DK / 16; ++k) {
+                            const uint64_t A = on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP);
+                            if constexpr (P1 == 3) {
+                                mma_bf16(d, A, on(S, k * MN_STEP), w3, k > 0);
+                            } else {
+                                mma_bf16(d, A, on(S, k * MN_STEP), w2, k > 0);
+                                mma_bf16(d, A, on(S, 2 * L::S_IMG + k * MN_STEP), w1, 1);
+                            }
                         }
+                        mma_commit(&sb->d1[s]);
                     }
-                    mma_commit(&sb->d1[s]);
+                    __syncwarp();
                 }
-                if (!ok || !(ok = wait(&sb->img_full, c & 1))) break;
+                ok = __all_sync(0xffffffffu, ok && wait(&sb->img_full, c & 1));
+                if (!ok) break;
 #pragma unroll
                 for (int s = 0; s < SL; ++s) {
                     const uint32_t d = tmem + s * SLICE + D2;
                     const uint64_t R = desc_mn(smem_addr(smem + L::ops + s * L::OPS), RU_IMG);
-                    if (!ok || !(ok = wait(&sb->r_ready[s], c & 1))) break;
+                    ok = __all_sync(0xffffffffu, ok && wait(&sb->r_ready[s], c & 1));
+                    if (!ok) break;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < C / 16; ++k) {
-                        mma_bf16(d, on(mat, M2_BYTES + k * K_STEP), on(R, k * MN_STEP), w2, k > 0);
-                        mma_bf16(d, on(mat, 2 * M2_BYTES + k * K_STEP), on(R, k * MN_STEP), w1, 1);
-                        mma_bf16(d, on(mat, k * K_STEP), on(R, 2 * RU_IMG + k * MN_STEP), w1, 1);
-                        mma_bf16(d, on(mat, k * K_STEP), on(R, k * MN_STEP), w2, 1);
+                        for (int k = 0; k < C / 16; ++k) {
+                            mma_bf16(d, on(mat, M2_BYTES + k * K_STEP), on(R, k * MN_STEP), w2, k > 0);
+                            mma_bf16(d, on(mat, 2 * M2_BYTES + k * K_STEP), on(R, k * MN_STEP), w1, 1);
+                            mma_bf16(d, on(mat, k * K_STEP), on(R, 2 * RU_IMG + k * MN_STEP), w1, 1);
+                            mma_bf16(d, on(mat, k * K_STEP), on(R, k * MN_STEP), w2, 1);
+                        }
+                        mma_commit(&sb->d2[s]);
                     }
-                    mma_commit(&sb->d2[s]);
+                    __syncwarp();
                 }
                 // M is 128 for heads of 64 too: their lanes 64..127 of D3 come
                 // from whatever follows the keys in shared memory, and are not read
@@ -229,22 +238,27 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
                 for (int s = 0; s < SL; ++s) {
                     const uint32_t d = tmem + s * SLICE + D3;
                     const uint64_t U = desc_mn(smem_addr(smem + L::ops + s * L::OPS), RU_IMG);
-                    if (!ok || !(ok = wait(&sb->u_ready[s], c & 1))) break;
+                    ok = __all_sync(0xffffffffu, ok && wait(&sb->u_ready[s], c & 1));
+                    if (!ok) break;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < C / 16; ++k) {
-                        if constexpr (P1 == 3) {
-                            mma_bf16(d, on(cols, 2 * k * KQ_GROUP), on(U, k * MN_STEP), w3 | A_MN, k > 0);
-                        } else {
-                            mma_bf16(d, on(cols, 2 * k * KQ_GROUP), on(U, k * MN_STEP), w2 | A_MN, k > 0);
-                            mma_bf16(d, on(cols, 2 * k * KQ_GROUP), on(U, 2 * RU_IMG + k * MN_STEP), w1 | A_MN, 1);
+                        for (int k = 0; k < C / 16; ++k) {
+                            const uint64_t A = on(cols, 2 * k * KQ_GROUP);
+                            if constexpr (P1 == 3) {
+                                mma_bf16(d, A, on(U, k * MN_STEP), w3 | A_MN, k > 0);
+                            } else {
+                                mma_bf16(d, A, on(U, k * MN_STEP), w2 | A_MN, k > 0);
+                                mma_bf16(d, A, on(U, 2 * RU_IMG + k * MN_STEP), w1 | A_MN, 1);
+                            }
                         }
+                        mma_commit(&sb->d3[s]);
+                        if (s == SL - 1) mma_commit(&sb->kq_empty[c & 1]);
                     }
-                    mma_commit(&sb->d3[s]);
+                    __syncwarp();
                 }
-                if (ok) mma_commit(&sb->kq_empty[c & 1]);
             }
-            drain_products(&sb->drain);
+            if (elect_one()) drain_products(&sb->drain);
         }
         __syncwarp();
     } else {
