@@ -92,8 +92,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
-// W values of a row from column c0 on, as three images `stride` bytes apart.
-template <int W> __device__ __forceinline__ void put3(uint32_t img, uint32_t stride, int row, int c0, const float *v) {
+// W values of a row from column c0 on, as three parts.  An operand of 64
+// columns is an image for each part, `stride` bytes apart; of 32 columns
+// (NARROW) the first two parts share an image's rows.
+template <int W, bool NARROW = false>
+__device__ __forceinline__ void put3(uint32_t img, uint32_t stride, int row, int c0, const float *v) {
 #pragma unroll
     for (int j = 0; j < W / 8; ++j) {
         uint32_t h[4], m[4], l[4];
@@ -101,8 +104,8 @@ template <int W> __device__ __forceinline__ void put3(uint32_t img, uint32_t str
         for (int i = 0; i < 4; ++i) split3(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], h[i], m[i], l[i]);
         const uint32_t to = piece(img, row, c0 / 8 + j);
         sts128(to, h[0], h[1], h[2], h[3]);
-        sts128(to + stride, m[0], m[1], m[2], m[3]);
-        sts128(to + 2 * stride, l[0], l[1], l[2], l[3]);
+        sts128(NARROW ? piece(img, row, c0 / 8 + j + 4) : to + stride, m[0], m[1], m[2], m[3]);
+        sts128(to + (NARROW ? 1 : 2) * stride, l[0], l[1], l[2], l[3]);
     }
 }
 // 32 floats as the 128-byte row of a staged tile.
@@ -114,13 +117,19 @@ __device__ __forceinline__ void put_row(uint32_t tile, int row, const float *v) 
 }
 
 // ---------------------------------------------------------------------------
-// Fragments: 16 rows x 32 columns over a warp, f[4 j + 2 i + k] = row
-// lane / 4 + 8 i, column 8 j + 2 (lane % 4) + k: what the 16-lane TMEM loads
-// give and the 8 x 8 matrix stores and loads take.  The tokens of a chunk lie
-// 16 to a warp's 32 TMEM lanes, so that all warps share their conversion.
+// Fragments: 16 rows x 2 F columns over a warp (F values a thread, 16 or 8),
+// f[4 j + 2 i + k] = row lane / 4 + 8 i, column 8 j + 2 (lane % 4) + k: what
+// the 16-lane TMEM loads give and the 8 x 8 matrix stores and loads take.  The
+// tokens of a chunk lie 16 to a warp's 32 TMEM lanes, so that all warps share
+// their conversion.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t frag_addr(uint32_t img, int row0, int c0, int j, int lane) {
     return piece(img, row0 + (lane & 15), c0 / 8 + j + (lane >> 4));
+}
+// The same in a tile of 64-byte rows (64-byte swizzle).
+__device__ __forceinline__ uint32_t frag_addr64(uint32_t tile, int row0, int c0, int j, int lane) {
+    const int r = row0 + (lane & 15), k = c0 / 8 + j + (lane >> 4);
+    return tile + (uint32_t)r * 64u + (uint32_t)((k ^ ((r >> 1) & 3)) << 4);
 }
 __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
@@ -132,34 +141,35 @@ __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr)
                  : "memory");
 }
-// Rows row0 .. row0 + 15, columns c0 .. c0 + 31 as three images.
-__device__ __forceinline__ void frag_put3(uint32_t img, uint32_t stride, int row0, int c0, int lane, const float (&f)[16]) {
+// Rows row0 .. row0 + 15, columns c0 on as three parts (F = 8: NARROW).
+template <int F> __device__ __forceinline__ void frag_put3(uint32_t img, uint32_t stride, int row0, int c0, int lane, const float (&f)[F]) {
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
+    for (int j = 0; j < F / 4; j += 2) {
         uint32_t h[4], m[4], l[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) split3(f[4 * j + 2 * i], f[4 * j + 2 * i + 1], h[i], m[i], l[i]);
         const uint32_t to = frag_addr(img, row0, c0, j, lane);
         stmatrix4(to, h[0], h[1], h[2], h[3]);
-        stmatrix4(to + stride, m[0], m[1], m[2], m[3]);
-        stmatrix4(to + 2 * stride, l[0], l[1], l[2], l[3]);
+        stmatrix4(F == 8 ? frag_addr(img, row0, c0 + 32, j, lane) : to + stride, m[0], m[1], m[2], m[3]);
+        stmatrix4(to + (F == 8 ? 1 : 2) * stride, l[0], l[1], l[2], l[3]);
     }
 }
-// The same rows and columns of a bf16 tile, as floats; and rounded to one.
-__device__ __forceinline__ void frag_get(uint32_t tile, int row0, int c0, int lane, float (&f)[16]) {
+// The same rows and columns of a bf16 tile (4 F columns wide), as floats; and
+// rounded to one.
+template <int F> __device__ __forceinline__ void frag_get(uint32_t tile, int row0, int c0, int lane, float (&f)[F]) {
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
+    for (int j = 0; j < F / 4; j += 2) {
         uint32_t r[4];
-        ldmatrix4(frag_addr(tile, row0, c0, j, lane), r);
+        ldmatrix4(F == 8 ? frag_addr64(tile, row0, c0, j, lane) : frag_addr(tile, row0, c0, j, lane), r);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[4 * j + 2 * i] = lo16(r[i]), f[4 * j + 2 * i + 1] = hi16(r[i]);
     }
 }
-__device__ __forceinline__ void frag_round(uint32_t tile, int row0, int c0, int lane, const float (&f)[16]) {
+template <int F> __device__ __forceinline__ void frag_round(uint32_t tile, int row0, int c0, int lane, const float (&f)[F]) {
 #pragma unroll
-    for (int j = 0; j < 4; j += 2)
-        stmatrix4(frag_addr(tile, row0, c0, j, lane), pack2(f[4 * j], f[4 * j + 1]), pack2(f[4 * j + 2], f[4 * j + 3]),
-                  pack2(f[4 * j + 4], f[4 * j + 5]), pack2(f[4 * j + 6], f[4 * j + 7]));
+    for (int j = 0; j < F / 4; j += 2)
+        stmatrix4(F == 8 ? frag_addr64(tile, row0, c0, j, lane) : frag_addr(tile, row0, c0, j, lane), pack2(f[4 * j], f[4 * j + 1]),
+                  pack2(f[4 * j + 2], f[4 * j + 3]), pack2(f[4 * j + 4], f[4 * j + 5]), pack2(f[4 * j + 6], f[4 * j + 7]));
 }
 // In 32 bits: 32 columns are the tile's whole row.
 __device__ __forceinline__ void frag_put_rows(uint32_t tile, int row0, int lane, const float (&f)[16]) {
@@ -173,9 +183,9 @@ __device__ __forceinline__ void frag_put_rows(uint32_t tile, int row0, int lane,
                          : "memory");
 }
 // f's rows times a (lane / 4) and b (lane / 4 + 8).
-__device__ __forceinline__ void frag_scale(float (&f)[16], float a, float b) {
+template <int F> __device__ __forceinline__ void frag_scale(float (&f)[F], float a, float b) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] *= (i & 2) ? b : a;
+    for (int i = 0; i < F; ++i) f[i] *= (i & 2) ? b : a;
 }
 
 // ---------------------------------------------------------------------------
@@ -185,12 +195,12 @@ constexpr int NV = 64;                       // value columns of a slice
 
 __device__ __forceinline__ void tmem_ldw(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
 __device__ __forceinline__ void tmem_ldw(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
-// W columns of this thread's lane: the sum of P column blocks, 64 apart, one
-// for each part of a split operand.
-template <int P, int W> __device__ __forceinline__ void load_parts(uint32_t addr, float *v) {
+// W columns of this thread's lane: the sum of P column blocks, STRIDE apart,
+// one for each part of a split operand.
+template <int P, int W, int STRIDE = NV> __device__ __forceinline__ void load_parts(uint32_t addr, float *v) {
     uint32_t r[P][W];
 #pragma unroll
-    for (int p = 0; p < P; ++p) tmem_ldw(addr + p * NV, r[p]);
+    for (int p = 0; p < P; ++p) tmem_ldw(addr + p * STRIDE, r[p]);
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < W; ++i) {
@@ -199,7 +209,7 @@ template <int P, int W> __device__ __forceinline__ void load_parts(uint32_t addr
         for (int p = P - 2; p >= 0; --p) v[i] += __uint_as_float(r[p][i]);
     }
 }
-// 16 lanes x 32 columns as a fragment.
+// 16 lanes x 32 or 16 columns as a fragment.
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
@@ -208,13 +218,19 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) 
           "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-template <int P> __device__ __forceinline__ void frag_load(uint32_t addr, float (&f)[16]) {
-    uint32_t r[P][16];
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+// The sum of P column blocks, 4 F apart.
+template <int P, int F> __device__ __forceinline__ void frag_load(uint32_t addr, float (&f)[F]) {
+    uint32_t r[P][F];
 #pragma unroll
-    for (int p = 0; p < P; ++p) tmem_ld_frag(addr + p * NV, r[p]);
+    for (int p = 0; p < P; ++p) tmem_ld_frag(addr + p * 4 * F, r[p]);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < F; ++i) {
         f[i] = __uint_as_float(r[P - 1][i]);
 #pragma unroll
         for (int p = P - 2; p >= 0; --p) f[i] += __uint_as_float(r[p][i]);
@@ -322,11 +338,12 @@ __device__ __forceinline__ void hand_over(uint64_t *bar, int lane) {
 
 // ---------------------------------------------------------------------------
 // Tensor maps.  Rows [B][L][H][D] with a pitch between tokens, in boxes of 64
-// (or fewer) tokens x 128 bytes of one head; tokens past L read as zeros and are not
+// (or fewer) tokens x 128 (or 64) bytes of one head; tokens past L read as zeros and are not
 // written.
 // ---------------------------------------------------------------------------
 inline cudaError_t encode(CUtensorMap *m, bool f32, int rank, const void *p, const cuuint64_t *dims, const cuuint64_t *strides,
                           const cuuint32_t *box) {
+    const bool half = box[0] * (f32 ? 4 : 2) == 64;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     if (!fn) {
         void *f = nullptr;
@@ -338,17 +355,17 @@ inline cudaError_t encode(CUtensorMap *m, bool f32, int rank, const void *p, con
     }
     const cuuint32_t es[4] = {1, 1, 1, 1};
     return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(p), dims,
-              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
 }
 inline cudaError_t encode_rows(CUtensorMap *m, bool f32, const void *p, long long ld, int B, int L, int H, int D,
-                               int tokens = C) {
+                               int tokens = C, int values = 0) {
     const cuuint64_t e = f32 ? 4 : 2;
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)L, (cuuint64_t)B};
     const cuuint64_t strides[3] = {(cuuint64_t)D * e, (cuuint64_t)ld * e, (cuuint64_t)ld * e * L};
-    const cuuint32_t box[4] = {f32 ? 32u : 64u, 1, (cuuint32_t)tokens, 1};
+    const cuuint32_t box[4] = {values ? (cuuint32_t)values : f32 ? 32u : 64u, 1, (cuuint32_t)tokens, 1};
     return encode(m, f32, 4, p, dims, strides, box);
 }
 // Matrices [n][Dk][Dv] of floats in boxes of Dk rows x 32 columns.

@@ -27,10 +27,11 @@
 // covers them (an MMA of N = 64 costs 48 cycles here, of N = 192 96), and the
 // reading thread adds the column blocks.
 //
-// A CTA takes one or two slices of a head.  Bound: the chain product -> sums,
-// splits -> product, three times a chunk.  With two slices the products of one
-// run while the other converts; that pays once there are enough heads to fill
-// the SMs anyway (launch rule below).
+// A CTA takes one or two slices of a head, of 64 columns, or one of 32.  Bound:
+// the chain product -> sums, splits -> product, three times a chunk.  With two
+// slices the products of one run while the other converts; that pays once
+// there are enough heads to fill the SMs anyway.  With few heads slices of 32
+// columns shorten the chain (launch rule below).
 #include "s5_delta_mma.cuh"
 
 namespace s5 {
@@ -42,16 +43,17 @@ struct ScanMaps {
     CUtensorMap e, o32, s;   // KEEP
 };
 
-template <int DK, int SL, bool KEEP> struct ScanSmem {
+template <int DK, int SL, bool KEEP, int NC> struct ScanSmem {
     static constexpr uint32_t KQ = KQ_BOX * (DK / 64);
     static constexpr uint32_t S_IMG = DK * 128;
     // S0's parts until D1 is done, R's until D2 is done, U's until D3 is done
-    static constexpr uint32_t OPS = 3 * S_IMG;
+    static constexpr uint32_t IMAGES = NC == 64 ? 3 : 2, OPS = IMAGES * S_IMG;
+    static constexpr uint32_t VO = C * NC * 2;
     static constexpr uint32_t kq = 0;                      // two stages
     static constexpr uint32_t mat = kq + 2 * KQ;
     static constexpr uint32_t ops = mat + MAT_BYTES;
     static constexpr uint32_t vo = ops + SL * OPS;         // V, then o
-    static constexpr uint32_t stage = vo + SL * RU_IMG;    // KEEP: a state, or e and o in 32 bits
+    static constexpr uint32_t stage = vo + SL * VO;        // KEEP: a state, or e and o in 32 bits
     static constexpr uint32_t meta = stage + (KEEP ? 32768 : 0);
     static constexpr uint32_t bars = meta + META_BYTES;
     static constexpr uint32_t total = bars + 256 + 1024;   // + alignment slack
@@ -72,17 +74,22 @@ static_assert(sizeof(ScanBars) <= 256, "barriers");
 
 template <int SL> constexpr int SCAN_THREADS = SL == 1 ? 320 : 576;
 
-template <int DK, int SL, bool KEEP>
+// NC: value columns of a slice, 64 or 32.
+template <int DK, int SL, bool KEEP, int NC>
 __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const __grid_constant__ ScanMaps maps, const Args a) {
-    using L = ScanSmem<DK, SL, KEEP>;
+    using L = ScanSmem<DK, SL, KEEP, NC>;
     static_assert(!(KEEP && SL == 2), "the staged tiles take the second slice's place");
+    static_assert(NC == 64 || (SL == 1 && !KEEP), "slices of 32 columns: one a CTA, nothing kept");
+    constexpr bool NARROW = NC == 32;
+    constexpr uint32_t L_PART = NARROW ? 1 : 2;   // the image of the third parts
     constexpr int P1 = SL == 1 ? 3 : 2;     // column blocks of D1 and D3: TMEM has 256 columns for each of two slices
-    constexpr int W = SL == 1 ? 32 : 16;    // columns converted at a time: registers for each of 16 warps
+    constexpr int PW = NC / 2, F = NC / 4;  // a warp's columns, and a thread's values of a fragment
+    constexpr int W = SL == 1 ? PW : 16;    // columns converted at a time: registers for each of 16 warps
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     ScanBars *sb = reinterpret_cast<ScanBars *>(smem + L::bars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    const int n0 = blockIdx.x * SL * NV, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
+    const int n0 = blockIdx.x * SL * NC, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
     const int N = chunks(a.L);
     const long long bh = (long long)b * a.Hv + h;
     if (threadIdx.x == 0) {
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
     const uint32_t tmem = sb->tmem;
     // D3 takes D1's place where two slices share the columns: every warp has
     // read D1 before it hands U over
-    constexpr uint32_t SLICE = 256, D1 = 0, D2 = P1 * NV, D3 = SL == 1 ? 5 * NV : 0;
+    constexpr uint32_t SLICE = 256, D1 = 0, D2 = P1 * NC, D3 = SL == 1 ? 5 * NC : 0;
     auto wait = [&](uint64_t *bar, int parity) { return bounded_wait(bar, (uint32_t)parity, &sb->abort); };
 
     if (warp >= 8 * SL) {
@@ -125,8 +132,8 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
                 bulk_load(smem + L::meta, from + MAT_BYTES, META_BYTES, &sb->img_full);
             };
             auto load_v = [&](int c, int s) {
-                mbar_arrive_tx(&sb->v_full[s], RU_IMG);
-                tma_load_4d(smem + L::vo + s * RU_IMG, &maps.v, n0 + s * NV, h, c * C, b, &sb->v_full[s]);
+                mbar_arrive_tx(&sb->v_full[s], L::VO);
+                tma_load_4d(smem + L::vo + s * L::VO, &maps.v, n0 + s * NC, h, c * C, b, &sb->v_full[s]);
             };
             load_kq(0);
             load_img(0);
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
                 }
                 for (int s = 0; ok && s < SL; ++s) {
                     if (!(ok = wait(&sb->o_ready[s], c & 1))) break;
-                    tma_store_4d(&maps.o, smem + L::vo + s * RU_IMG, n0 + s * NV, h, c * C, b);
+                    tma_store_4d(&maps.o, smem + L::vo + s * L::VO, n0 + s * NC, h, c * C, b);
                     bulk_commit();
                     if (c + 1 < N) {
                         bulk_wait_read_all();
@@ -181,8 +188,8 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
             if (!ok) settle_copies();
         } else if (warp == MMA_WARP) {
             // ------------------------------------------------------ products
-            const uint32_t w1 = idesc_bf16_f32(128, NV) | B_MN, w2 = idesc_bf16_f32(128, 2 * NV) | B_MN,
-                           w3 = idesc_bf16_f32(128, 3 * NV) | B_MN;
+            const uint32_t w1 = idesc_bf16_f32(128, NC) | B_MN, w2 = idesc_bf16_f32(128, 2 * NC) | B_MN,
+                           w3 = idesc_bf16_f32(128, 3 * NC) | B_MN;
             const uint64_t mat = desc_k(smem_addr(smem + L::mat));
             bool ok = true;
             for (int c = 0; ok && c < N; ++c) {
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
                         for (int k = 0; k < C / 16; ++k) {
                             mma_bf16(d, on(mat, M2_BYTES + k * K_STEP), on(R, k * MN_STEP), w2, k > 0);
                             mma_bf16(d, on(mat, 2 * M2_BYTES + k * K_STEP), on(R, k * MN_STEP), w1, 1);
-                            mma_bf16(d, on(mat, k * K_STEP), on(R, 2 * RU_IMG + k * MN_STEP), w1, 1);
+                            mma_bf16(d, on(mat, k * K_STEP), on(R, L_PART * RU_IMG + k * MN_STEP), w1, 1);
                             mma_bf16(d, on(mat, k * K_STEP), on(R, k * MN_STEP), w2, 1);
                         }
                         mma_commit(&sb->d2[s]);
@@ -264,24 +271,24 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
     } else {
         // ---------------------------------------------------------- compute
         // Eight warps a slice; warp w: TMEM lanes 32 (w % 4) on, columns
-        // 32 (w / 4) on.  In D1 and D2 its first 16 lanes are tokens of R and
+        // PW (w / 4) on.  In D1 and D2 its first 16 lanes are tokens of R and
         // e, the others tokens of o; in D3 and in the state a lane is a key
         // index.
-        const int s = warp / 8, q = warp & 3, c0 = warp % 8 / 4 * 32, row = 32 * q + lane;
+        const int s = warp / 8, q = warp & 3, c0 = warp % 8 / 4 * PW, row = 32 * q + lane;
         const int t16 = 16 * q, ta = t16 + lane / 4, tb = ta + 8;   // tokens of a fragment's rows
         const uint32_t acc = tmem + s * SLICE + ((uint32_t)(32 * q) << 16) + c0;
-        const uint32_t ops = smem_addr(smem + L::ops + s * L::OPS), vo = smem_addr(smem + L::vo + s * RU_IMG);
+        const uint32_t ops = smem_addr(smem + L::ops + s * L::OPS), vo = smem_addr(smem + L::vo + s * L::VO);
         const uint32_t stage = smem_addr(smem + L::stage);
         const Meta *meta = reinterpret_cast<const Meta *>(smem + L::meta);
         const bool state = row < DK;
-        const long long place = bh * DK * a.Dv + (long long)row * a.Dv + n0 + s * NV + c0;   // this row in s0, s_last
-        float S[32];
+        const long long place = bh * DK * a.Dv + (long long)row * a.Dv + n0 + s * NC + c0;   // this row in s0, s_last
+        float S[PW];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < PW / 4; ++j) {
             const float4 t = (a.s0 && state) ? *reinterpret_cast<const float4 *>(a.s0 + place + 4 * j) : make_float4(0, 0, 0, 0);
             S[4 * j] = t.x, S[4 * j + 1] = t.y, S[4 * j + 2] = t.z, S[4 * j + 3] = t.w;
         }
-        if (state) put3<32>(ops, L::S_IMG, row, c0, S);
+        if (state) put3<PW, NARROW>(ops, L::S_IMG, row, c0, S);
         hand_over(&sb->s_ready[s], lane);
         if constexpr (KEEP) {
             if (state) put_row(stage + c0 / 32 * (DK * 128), row, S);
@@ -291,13 +298,13 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
             bool ok = wait(&sb->img_full, c & 1) && wait(&sb->v_full[s], c & 1) && wait(&sb->d1[s], c & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            float f[16], o[16];
+            float f[F], o[F];
             const float ua = meta->up[ta], ub = meta->up[tb];
             {   // R
                 frag_get(vo, t16, c0, lane, o);
                 frag_load<P1>(acc + D1, f);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = fmaf(-((i & 2) ? ub : ua), f[i], o[i]);
+                for (int i = 0; i < F; ++i) f[i] = fmaf(-((i & 2) ? ub : ua), f[i], o[i]);
                 frag_put3(ops, RU_IMG, t16, c0, lane, f);
                 hand_over(&sb->r_ready[s], lane);
             }
@@ -310,14 +317,14 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
             if (lane == 0) mbar_arrive(&sb->img_empty);   // D2 is done with the matrix, this warp with its factors
             {   // e, U
                 frag_load<2>(acc + D2, f);
-                float u[16];
+                float u[F];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) u[i] = f[i] * ((i & 2) ? db : da);
+                for (int i = 0; i < F; ++i) u[i] = f[i] * ((i & 2) ? db : da);
                 frag_put3(ops, RU_IMG, t16, c0, lane, u);
                 hand_over(&sb->u_ready[s], lane);
                 frag_load<2>(acc + D2 + QUERY_LANES, u);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] += u[i];
+                for (int i = 0; i < F; ++i) o[i] += u[i];
                 frag_round(vo, t16, c0, lane, o);
                 hand_over(&sb->o_ready[s], lane);
             }
@@ -333,12 +340,12 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
             tc_fence_after();
             if (state) {
 #pragma unroll
-                for (int w = 0; w < 32; w += W) {
+                for (int w = 0; w < PW; w += W) {
                     float y[W];
-                    load_parts<P1, W>(acc + D3 + w, y);
+                    load_parts<P1, W, NC>(acc + D3 + w, y);
 #pragma unroll
                     for (int i = 0; i < W; ++i) S[w + i] = fmaf(last, S[w + i], y[i]);
-                    if (c + 1 < N) put3<W>(ops, L::S_IMG, row, c0 + w, S + w);
+                    if (c + 1 < N) put3<W, NARROW>(ops, L::S_IMG, row, c0 + w, S + w);
                 }
             }
             if (c + 1 < N) hand_over(&sb->s_ready[s], lane);
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
         }
         if (state && a.s_last)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < PW / 4; ++j)
                 *reinterpret_cast<float4 *>(a.s_last + place + 4 * j) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
         tc_fence_before();
     }
@@ -360,20 +367,23 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
     if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
-template <int DK, int SL, bool KEEP> cudaError_t launch(const ScanMaps &m, const Args &a, cudaStream_t st) {
-    using L = ScanSmem<DK, SL, KEEP>;
-    const cudaError_t e = big_smem(delta_scan_kernel<DK, SL, KEEP>, L::total);
+template <int DK, int SL, bool KEEP, int NC> cudaError_t launch(const ScanMaps &m, const Args &a, cudaStream_t st) {
+    using L = ScanSmem<DK, SL, KEEP, NC>;
+    const cudaError_t e = big_smem(delta_scan_kernel<DK, SL, KEEP, NC>, L::total);
     if (e != cudaSuccess) return e;
-    delta_scan_kernel<DK, SL, KEEP><<<dim3(a.Dv / (SL * NV), a.Hv, a.B), SCAN_THREADS<SL>, L::total, st>>>(m, a);
+    delta_scan_kernel<DK, SL, KEEP, NC><<<dim3(a.Dv / (SL * NC), a.Hv, a.B), SCAN_THREADS<SL>, L::total, st>>>(m, a);
     return cudaGetLastError();
 }
 
 template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
     ScanMaps m = {};
+    // slices of 32 columns where one CTA each still fits the SMs at once
+    const long long heads = (long long)a.B * a.Hv;
+    const bool narrow = !a.states && heads * (a.Dv / 32) <= 152;
     cudaError_t e = encode_rows(&m.k, false, a.k, a.ldk, a.B, a.L, a.Hk, DK, 16);
     if (e == cudaSuccess) e = encode_rows(&m.q, false, a.q, a.ldq, a.B, a.L, a.Hk, DK, 16);
-    if (e == cudaSuccess) e = encode_rows(&m.v, false, a.v, a.ldv, a.B, a.L, a.Hv, a.Dv);
-    if (e == cudaSuccess) e = encode_rows(&m.o, false, a.o, a.ldo, a.B, a.L, a.Hv, a.Dv);
+    if (e == cudaSuccess) e = encode_rows(&m.v, false, a.v, a.ldv, a.B, a.L, a.Hv, a.Dv, C, narrow ? 32 : 64);
+    if (e == cudaSuccess) e = encode_rows(&m.o, false, a.o, a.ldo, a.B, a.L, a.Hv, a.Dv, C, narrow ? 32 : 64);
     if (a.states) {
         const long long ld = (long long)a.Hv * a.Dv;
         if (e == cudaSuccess) e = encode_rows(&m.e, true, a.e, ld, a.B, a.L, a.Hv, a.Dv);
@@ -382,10 +392,11 @@ template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
     }
     if (e == cudaSuccess) e = tc_prepare(a, false, st);
     if (e != cudaSuccess) return e;
-    if (a.states) return launch<DK, 1, true>(m, a, st);
+    if (a.states) return launch<DK, 1, true, 64>(m, a, st);
+    if (narrow) return launch<DK, 1, false, 32>(m, a, st);
     // two slices a CTA where one a CTA would not fit the SMs at once
-    if (a.Dv == 2 * NV && (long long)a.B * a.Hv * 2 > 152) return launch<DK, 2, false>(m, a, st);
-    return launch<DK, 1, false>(m, a, st);
+    if (a.Dv == 128 && heads * 2 > 152) return launch<DK, 2, false, 64>(m, a, st);
+    return launch<DK, 1, false, 64>(m, a, st);
 }
 
 }  // namespace

@@ -84,8 +84,13 @@ SHAPES = [
 ]
 
 
+# As many heads as take wider slices, and two slices a block
+MANY = [(3, 130, 8, 16, 128, 128), (5, 100, 8, 16, 128, 128), (11, 70, 4, 8, 64, 64), (10, 129, 4, 8, 64, 128),
+        (10, 70, 8, 8, 128, 64)]
+
+
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", SHAPES + MANY)
 def test_forward(shape, dt):
     d, v = make(*shape, dt=dt, seed=sum(shape))
     o, s = forward(d)
@@ -224,7 +229,7 @@ def close_grads(got, v, dt):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", SHAPES + MANY)
 def test_backward(shape, dt):
     d, v = make(*shape, dt=dt, seed=sum(shape) + 1)
     close_grads(grads(d), v, dt)
