@@ -141,13 +141,16 @@ __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr)
                  : "memory");
 }
-// Rows row0 .. row0 + 15, columns c0 on as three parts (F = 8: NARROW).
-template <int F> __device__ __forceinline__ void frag_put3(uint32_t img, uint32_t stride, int row0, int c0, int lane, const float (&f)[F]) {
+// Rows row0 .. row0 + 15, columns c0 on as three parts (F = 8: NARROW).  Blocks
+// of 16 columns past `last` are zeros.
+template <int F>
+__device__ __forceinline__ void frag_put3(uint32_t img, uint32_t stride, int row0, int c0, int lane, const float (&f)[F], int last = 3) {
 #pragma unroll
     for (int j = 0; j < F / 4; j += 2) {
-        uint32_t h[4], m[4], l[4];
+        uint32_t h[4] = {}, m[4] = {}, l[4] = {};
+        if (c0 / 16 + j / 2 <= last)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split3(f[4 * j + 2 * i], f[4 * j + 2 * i + 1], h[i], m[i], l[i]);
+            for (int i = 0; i < 4; ++i) split3(f[4 * j + 2 * i], f[4 * j + 2 * i + 1], h[i], m[i], l[i]);
         const uint32_t to = frag_addr(img, row0, c0, j, lane);
         stmatrix4(to, h[0], h[1], h[2], h[3]);
         stmatrix4(F == 8 ? frag_addr(img, row0, c0 + 32, j, lane) : to + stride, m[0], m[1], m[2], m[3]);

@@ -177,6 +177,14 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
 #pragma unroll
                 for (int jb = 0; jb < 2; ++jb) {
                     const int nb = c0 / 16 + jb;
+                    if (nb > q) {   // above the diagonal
+#pragma unroll
+                        for (int jj = 2 * jb; jj < 2 * jb + 2; ++jj) {
+                            p[4 * jj + 2 * i] = p[4 * jj + 2 * i + 1] = 0.0f;
+                            *reinterpret_cast<float2 *>(&A[r][c0 + 8 * jj + 2 * (lane & 3)]) = make_float2(0.0f, 0.0f);
+                        }
+                        continue;
+                    }
                     float far = 1.0f;
                     if (nb < q) far = expf((gh - meta->hi[16 * nb + 15]) + (gl - meta->lo[16 * nb + 15]));
 #pragma unroll
@@ -185,20 +193,17 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int col = c0 + 8 * jj + 2 * (lane & 3) + k, at = 4 * jj + 2 * i + k;
-                            s[k] = p[at] = 0.0f;
-                            if (nb <= q) {
-                                const float d = nb < q ? far * near[col] : expf((gh - meta->hi[col]) + (gl - meta->lo[col]));
-                                const float bc = meta->beta[col];
-                                if (col < r) s[k] = kk[at] * (d * (TRANS ? br : bc));
-                                if (col <= r) p[at] = qk[at] * (TRANS ? d : d * bc);
-                            }
+                            const float d = nb < q ? far * near[col] : expf((gh - meta->hi[col]) + (gl - meta->lo[col]));
+                            const float bc = meta->beta[col];
+                            s[k] = col < r ? kk[at] * (d * (TRANS ? br : bc)) : 0.0f;
+                            p[at] = col <= r ? qk[at] * (TRANS ? d : d * bc) : 0.0f;
                             if (nb == q) T[nb][col & 15][r & 15] = s[k];
                         }
                         *reinterpret_cast<float2 *>(&A[r][c0 + 8 * jj + 2 * (lane & 3)]) = make_float2(s[0], s[1]);
                     }
                 }
             }
-            frag_put3(img, M2_BYTES, 32 * q + 16, c0, lane, p);
+            frag_put3(img, M2_BYTES, 32 * q + 16, c0, lane, p, q);
         }
         __syncthreads();
         if (warp < 2) {   // two blocks of the diagonal per warp; lane: a column of the inverse
@@ -249,6 +254,7 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
                 }
             }
             *reinterpret_cast<float2 *>(&A[o + 16 + r][o + c2]) = make_float2(v0, v1);
+            // the products below read the upper part as zeros
             __syncthreads();
             *reinterpret_cast<float2 *>(&A[o + r][o + 16 + c2]) = make_float2(0.0f, 0.0f);
         }
@@ -284,17 +290,21 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < C * 8 / PT; ++k) {   // E's three parts
-            const int i = tid + k * PT, r = i / 8, ch = i % 8;
-            float4 x = make_float4(0, 0, 0, 0), y = x;
-            if (!(r < 32 && ch >= 4)) {          // that quarter holds the intermediate product
-                x = *reinterpret_cast<const float4 *>(&A[r][8 * ch]);
-                y = *reinterpret_cast<const float4 *>(&A[r][8 * ch + 4]);
+            // a warp's 32 pieces are one 8-wide column of 32 rows: whole blocks of
+            // zeros above the diagonal are not split
+            const int r = lane + 32 * (warp & 1), ch = warp / 2 + 4 * k;
+            uint32_t hh[4] = {}, mm[4] = {}, ll[4] = {};
+            if (ch / 2 <= 2 * (warp & 1) + 1) {
+                float4 x = make_float4(0, 0, 0, 0), y = x;
+                if (ch / 2 <= r / 16) {
+                    x = *reinterpret_cast<const float4 *>(&A[r][8 * ch]);
+                    y = *reinterpret_cast<const float4 *>(&A[r][8 * ch + 4]);
+                }
+                split3(x.x, x.y, hh[0], mm[0], ll[0]);
+                split3(x.z, x.w, hh[1], mm[1], ll[1]);
+                split3(y.x, y.y, hh[2], mm[2], ll[2]);
+                split3(y.z, y.w, hh[3], mm[3], ll[3]);
             }
-            uint32_t hh[4], mm[4], ll[4];
-            split3(x.x, x.y, hh[0], mm[0], ll[0]);
-            split3(x.z, x.w, hh[1], mm[1], ll[1]);
-            split3(y.x, y.y, hh[2], mm[2], ll[2]);
-            split3(y.z, y.w, hh[3], mm[3], ll[3]);
             const uint32_t to = piece(img, 2 * r - (r & 15), ch);
             sts128(to, hh[0], hh[1], hh[2], hh[3]);
             sts128(to + M2_BYTES, mm[0], mm[1], mm[2], mm[3]);
@@ -321,7 +331,7 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
         {
             float p[16];
             frag_load<2>(frag + QUERY_LANES, p);
-            frag_put3(img, M2_BYTES, 32 * q + 16, c0, lane, p);
+            frag_put3(img, M2_BYTES, 32 * q + 16, c0, lane, p, q);
         }
         fence_proxy_async_smem();
         __syncthreads();
