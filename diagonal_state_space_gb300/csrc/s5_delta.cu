@@ -14,30 +14,43 @@
 //   X_t = Z_t^T k_t,  dv_t = beta_t X_t,  dbeta_t = X_t . e_t,
 // run with columns spread over the grid and no exchange between blocks, and
 //   dq_t = scale S_t do_t,   dk_t = Z_t u_t - a_t S_{t-1} dv_t
-// come from a second pair of sweeps with rows spread over the grid: four
-// sweeps, all sums inside 16 lanes, no atomics, one order of addition.
+// come from sweeps with rows spread over the grid, all chunks of 64 tokens at
+// once from the kept states and adjoints.  All sums are inside 8 or 16 lanes, no
+// atomics, one order of addition.
 //
 // The decay's gradient dg_t = <a_t S_{t-1}, Z_t - k_t dv_t^T> needs no sweep:
 //   dg_t - dg_{t+1} = o_t . do_t - v_t . dv_t,
 // (insert the recurrences), anchored at every 64th token by <S_c, Z_c> of the
 // kept states, so that at most 64 terms are added in a row.
 //
-// Bound: the chain of a token (product, sum over 16 lanes, update), about 300
-// cycles; the state stays in registers.
+// Bound: the chain of a token in the column sweeps (product, sum over 8 lanes,
+// update); the state stays in registers, two warps of a block bring the next
+// tokens to shared memory while the other two run these.
 #include "s5_delta.cuh"
 
 namespace s5 {
 namespace delta {
 namespace {
 
-constexpr int TB = 16;        // tokens staged in shared memory
+constexpr int TB = 16;        // tokens staged in shared memory (8 for heads above 128)
 constexpr int OWN = 32;       // columns (or rows) of a block
-constexpr int SWT = 128;      // threads of a sweep: 16 lanes x 8 groups of 4
+constexpr int SWT = 128;      // threads of a sweep
 // Heads (B Hv) from which on a step takes a block for each, against a block for
 // 32 columns: 3.8 / 4.5 us at 96 heads of 128 x 128, 3.7 / 3.2 at 64, 63 / 77 at
 // 3072 (6.4 TB/s).
 constexpr int HEAD_BLOCKS = 80;
 
+// Sums of four values over 8 lanes; lane l gets the sum of value l / 2 % 4.
+__device__ __forceinline__ float sum4_8(const float (&v)[4], int lane) {
+    const bool up = lane & 4, up2 = lane & 2;
+    float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
+    a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 4);
+    b += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 4);
+    float c = up2 ? b : a;
+    c += __shfl_xor_sync(0xffffffffu, up2 ? a : b, 2);
+    c += __shfl_xor_sync(0xffffffffu, c, 1);
+    return c;
+}
 // Sums of four values over 16 lanes; lane l gets the sum of value l / 4 % 4.
 __device__ __forceinline__ float sum4_16(const float (&v)[4], int lane) {
     const bool up = lane & 8, up2 = lane & 4;
@@ -56,34 +69,46 @@ template <typename T> __device__ __forceinline__ float elem(const void *p, long 
 }
 
 // Columns over the grid.  REV false: the forward recurrence, writing o (and
-// what the backward pass needs); REV true: the adjoint, writing X.
+// what the backward pass needs); REV true: the adjoint, writing X and the
+// adjoint at each chunk's end.  Warps 0 and 1: 8 lanes by 8 groups of four
+// columns, rows lane + 8 i; warps 2 and 3 stage the next tokens.
 template <typename T, int RPT, bool REV>
 __global__ void __launch_bounds__(SWT) column_sweep_kernel(const Args a) {
-    __shared__ float sq[TB][16 * RPT], sk[TB][16 * RPT], sv[TB][OWN], sa[TB], sb[TB];
-    __shared__ float red[SWT / 32];
-    const int lane = threadIdx.x % 16, grp = threadIdx.x / 16;
+    constexpr int NT = RPT > 16 ? TB / 2 : TB, D = 8 * RPT;
+    __shared__ float sq[2][NT][D], sk[2][NT][D], sv[2][NT][OWN], sa[2][NT], sb[2][NT];
+    __shared__ float red[2];
+    const int lane = threadIdx.x % 8, grp = threadIdx.x / 8 % 8;
+    const bool loads = threadIdx.x >= 64;
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
     const int col = blockIdx.x * OWN + grp * 4;
-    const int mine = lane / 4;                       // the column whose sums this lane gets
-    const bool on = col < a.Dv;                      // Dv is a multiple of 4
+    const int mine = lane / 2;                       // the column whose sums this lane gets
+    const bool on = !loads && col < a.Dv;            // Dv is a multiple of 4
     const int N = chunks(a.L);
     const long long bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
     const float *init = REV ? a.ds_last : a.s0;
     float S[RPT][4];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-        const int r = lane + 16 * i;
+        const int r = lane + 8 * i;
         const float4 t = (init && on && r < a.Dk) ? *reinterpret_cast<const float4 *>(init + bh * mat + (long long)r * a.Dv + col)
                                                   : make_float4(0, 0, 0, 0);
         S[i][0] = t.x, S[i][1] = t.y, S[i][2] = t.z, S[i][3] = t.w;
     }
-    // <S_c, Z_c> of this block's columns
+    auto keep = [&](float *to) {
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const int r = lane + 8 * i;
+            if (on && r < a.Dk)
+                *reinterpret_cast<float4 *>(to + (long long)r * a.Dv + col) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+        }
+    };
+    // <S_c, Z_c> of this block's columns (the two compute warps)
     auto inner = [&](int c) {
         const float *s = a.states + (bh * (N + 1) + c) * mat;
         float w = 0.0f;
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            const int r = lane + 16 * i;
+            const int r = lane + 8 * i;
             if (on && r < a.Dk) {
                 const float4 t = *reinterpret_cast<const float4 *>(s + (long long)r * a.Dv + col);
                 w += t.x * S[i][0] + t.y * S[i][1] + t.z * S[i][2] + t.w * S[i][3];
@@ -91,147 +116,160 @@ __global__ void __launch_bounds__(SWT) column_sweep_kernel(const Args a) {
         }
         for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
         if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = w;
-        __syncthreads();
-        if (threadIdx.x == 0) a.inner[(bh * (N + 1) + c) * a.parts + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
-        __syncthreads();
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+        if (threadIdx.x == 0) a.inner[(bh * (N + 1) + c) * a.parts + blockIdx.x] = red[0] + red[1];
+        asm volatile("bar.sync 1, 64;" ::: "memory");
     };
-    auto keep = [&](float *to) {
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            const int r = lane + 16 * i;
-            if (on && r < a.Dk)
-                *reinterpret_cast<float4 *>(to + (long long)r * a.Dv + col) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
-        }
-    };
-    if (REV) inner(N);
-    const int stages = (a.L + TB - 1) / TB;
-    for (int st = 0; st < stages; ++st) {
-        const int t0 = (REV ? stages - 1 - st : st) * TB, nt = min(TB, a.L - t0);
+    const int stages = (a.L + NT - 1) / NT;
+    auto stage = [&](int st, int buf, int tid, int threads) {
+        const int t0 = (REV ? stages - 1 - st : st) * NT, nt = min(NT, a.L - t0);
         const long long row0 = (long long)b * a.L + t0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < nt * 16 * RPT; i += SWT) {
-            const int t = i / (16 * RPT), r = i % (16 * RPT);
+        for (int i = tid; i < nt * D; i += threads) {
+            const int t = i / D, r = i % D;
             const bool in = r < a.Dk;
-            sq[t][r] = in ? a.scale * elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
-            sk[t][r] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
+            sq[buf][t][r] = in ? a.scale * elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
+            sk[buf][t][r] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
         }
-        for (int i = threadIdx.x; i < nt * OWN; i += SWT) {
+        for (int i = tid; i < nt * OWN; i += threads) {
             const int t = i / OWN, c = blockIdx.x * OWN + i % OWN;
-            sv[t][i % OWN] = c >= a.Dv ? 0.0f
-                             : REV     ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + c)
-                                       : elem<T>(a.v, (row0 + t) * a.ldv + (long long)h * a.Dv + c);
+            sv[buf][t][i % OWN] = c >= a.Dv ? 0.0f
+                                  : REV     ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + c)
+                                            : elem<T>(a.v, (row0 + t) * a.ldv + (long long)h * a.Dv + c);
         }
-        if (threadIdx.x < nt) {
-            sa[threadIdx.x] = expf(clamp_g(a.g[(row0 + threadIdx.x) * a.Hv + h]));
-            sb[threadIdx.x] = a.beta[(row0 + threadIdx.x) * a.Hv + h];
+        if (tid < nt) {
+            sa[buf][tid] = expf(clamp_g(a.g[(row0 + tid) * a.Hv + h]));
+            sb[buf][tid] = a.beta[(row0 + tid) * a.Hv + h];
         }
-        __syncthreads();
+    };
+    if (REV && !loads) inner(N);
+    if (stages > 0) stage(0, 0, threadIdx.x, SWT);
+    __syncthreads();
+    for (int st = 0; st < stages; ++st) {
+        const int buf = st & 1;
+        if (loads) {
+            if (st + 1 < stages) stage(st + 1, buf ^ 1, threadIdx.x - 64, 64);
+            __syncthreads();
+            continue;
+        }
+        const int t0 = (REV ? stages - 1 - st : st) * NT, nt = min(NT, a.L - t0);
+        const long long row0 = (long long)b * a.L + t0;
         for (int j = 0; j < nt; ++j) {
             const int t = REV ? nt - 1 - j : j, tok = t0 + t;
             const long long out = ((row0 + t) * a.Hv + h) * a.Dv + col + mine;
+            const float *kt = sk[buf][t], *qt = sq[buf][t];
             float p[4] = {0, 0, 0, 0}, u[4];
-            const float al = sa[t];
+            const float al = sa[buf][t], be = sb[buf][t];
             if (!REV) {
                 if (a.states && tok % CHUNK == 0) keep(a.states + (bh * (N + 1) + tok / CHUNK) * mat);
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                    const float kk = sk[t][lane + 16 * i];
+                    const float kk = kt[lane + 8 * i];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         S[i][c] *= al;
                         p[c] = fmaf(S[i][c], kk, p[c]);
                     }
                 }
-                const float e = sv[t][grp * 4 + mine] - sum4_16(p, lane);
-                if (a.e && on && lane % 4 == 0) a.e[out] = e;
-                const float um = sb[t] * e;
+                const float e = sv[buf][t][grp * 4 + mine] - sum4_8(p, lane);
+                if (a.e && on && lane % 2 == 0) a.e[out] = e;
+                const float um = be * e;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, um, (threadIdx.x & 16) + 4 * c), p[c] = 0.0f;
+                for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, um, 2 * c, 8), p[c] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                    const float kk = sk[t][lane + 16 * i], qq = sq[t][lane + 16 * i];
+                    const float kk = kt[lane + 8 * i], qq = qt[lane + 8 * i];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         S[i][c] = fmaf(kk, u[c], S[i][c]);
                         p[c] = fmaf(S[i][c], qq, p[c]);
                     }
                 }
-                const float o = sum4_16(p, lane);
-                if (on && lane % 4 == 0) {
+                const float o = sum4_8(p, lane);
+                if (on && lane % 2 == 0) {
                     store_elem<T>(static_cast<T *>(a.o) + (row0 + t) * a.ldo + (long long)h * a.Dv + col + mine, o);
                     if (a.o32) a.o32[out] = o;
                 }
             } else {
+                if ((tok + 1) % CHUNK == 0 || tok == a.L - 1)
+                    keep(static_cast<float *>(a.z) + (bh * N + tok / CHUNK) * mat);
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                    const float kk = sk[t][lane + 16 * i], qq = sq[t][lane + 16 * i];
+                    const float kk = kt[lane + 8 * i], qq = qt[lane + 8 * i];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        S[i][c] = fmaf(qq, sv[t][grp * 4 + c], S[i][c]);
+                        S[i][c] = fmaf(qq, sv[buf][t][grp * 4 + c], S[i][c]);
                         p[c] = fmaf(S[i][c], kk, p[c]);
                     }
                 }
-                const float x = sum4_16(p, lane);
-                if (on && lane % 4 == 0) a.x[out] = x;
-                const float um = sb[t] * x;
+                const float x = sum4_8(p, lane);
+                if (on && lane % 2 == 0) a.x[out] = x;
+                const float um = be * x;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, um, (threadIdx.x & 16) + 4 * c);
+                for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, um, 2 * c, 8);
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                    const float kk = sk[t][lane + 16 * i];
+                    const float kk = kt[lane + 8 * i];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) S[i][c] = al * fmaf(-kk, u[c], S[i][c]);
                 }
                 if (tok % CHUNK == 0) inner(tok / CHUNK);
             }
         }
+        __syncthreads();
     }
+    if (loads) return;
     float *last = REV ? a.ds0 : a.s_last;
     if (last) keep(last + bh * mat);
     if (!REV && a.states) keep(a.states + (bh * (N + 1) + N) * mat);
 }
 
-// Rows over the grid, with u_t = beta_t e_t and dv_t = beta_t X_t known.  REV
-// false: dq_t and -a_t S_{t-1} dv_t; REV true: adds Z_t u_t to the latter.
-template <typename T, int RPT, bool REV>
+// Rows and chunks over the grid, with u_t = beta_t e_t and dv_t = beta_t X_t
+// known: forward from the chunk's kept state for dq_t and -a_t S_{t-1} dv_t,
+// then backward from its kept adjoint for Z_t u_t.
+template <typename T, int RPT>
 __global__ void __launch_bounds__(SWT) row_sweep_kernel(const Args a) {
-    __shared__ float se[TB][16 * RPT], sx[TB][16 * RPT], sd[TB][16 * RPT], sq[TB][OWN], sk[TB][OWN], sa[TB];
+    constexpr int NT = RPT > 8 ? TB / 2 : TB;
+    __shared__ float se[NT][16 * RPT], sx[NT][16 * RPT], sd[NT][16 * RPT], sq[NT][OWN], sk[NT][OWN], sa[NT], dk[CHUNK][OWN];
     const int lane = threadIdx.x % 16, grp = threadIdx.x / 16;
+    const int rows = (a.Dk + OWN - 1) / OWN, c = blockIdx.x / rows, r0 = blockIdx.x % rows * OWN;
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
-    const int row = blockIdx.x * OWN + grp * 4, mine = lane / 4;
+    const int row = r0 + grp * 4, mine = lane / 4;
     const bool on = row < a.Dk;
+    const int N = chunks(a.L), first = c * CHUNK, len = min(CHUNK, a.L - first), stages = (len + NT - 1) / NT;
     const long long bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
-    const float *init = REV ? a.ds_last : a.s0;
     float S[RPT][4];
+    auto load = [&](const float *from) {
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
+        for (int i = 0; i < RPT; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            S[i][r] = (init && on && lane + 16 * i < a.Dv) ? init[bh * mat + (long long)(row + r) * a.Dv + lane + 16 * i] : 0.0f;
-    const int stages = (a.L + TB - 1) / TB;
-    for (int st = 0; st < stages; ++st) {
-        const int t0 = (REV ? stages - 1 - st : st) * TB, nt = min(TB, a.L - t0);
+            for (int r = 0; r < 4; ++r)
+                S[i][r] = (on && lane + 16 * i < a.Dv) ? from[(long long)(row + r) * a.Dv + lane + 16 * i] : 0.0f;
+    };
+    auto stage = [&](int t0, int nt) {
         const long long row0 = (long long)b * a.L + t0;
         __syncthreads();
         for (int i = threadIdx.x; i < nt * 16 * RPT; i += SWT) {
-            const int t = i / (16 * RPT), c = i % (16 * RPT);
-            const bool in = c < a.Dv;
+            const int t = i / (16 * RPT), v = i % (16 * RPT);
+            const bool in = v < a.Dv;
             const long long hv = (row0 + t) * a.Hv + h;
             const float be = a.beta[hv];
-            se[t][c] = in ? be * a.e[hv * a.Dv + c] : 0.0f;
-            sx[t][c] = in ? be * a.x[hv * a.Dv + c] : 0.0f;
-            sd[t][c] = in ? a.scale * elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + c) : 0.0f;
+            se[t][v] = in ? be * a.e[hv * a.Dv + v] : 0.0f;
+            sx[t][v] = in ? be * a.x[hv * a.Dv + v] : 0.0f;
+            sd[t][v] = in ? a.scale * elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + v) : 0.0f;
         }
         for (int i = threadIdx.x; i < nt * OWN; i += SWT) {
-            const int t = i / OWN, r = blockIdx.x * OWN + i % OWN;
+            const int t = i / OWN, r = r0 + i % OWN;
             sq[t][i % OWN] = r < a.Dk ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
             sk[t][i % OWN] = r < a.Dk ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
         }
         if (threadIdx.x < nt) sa[threadIdx.x] = expf(clamp_g(a.g[(row0 + threadIdx.x) * a.Hv + h]));
         __syncthreads();
-        for (int j = 0; j < nt; ++j) {
-            const int t = REV ? nt - 1 - j : j;
-            const long long out = ((row0 + t) * a.Hv + h) * a.Dk + row + mine;
+    };
+    load(a.states + (bh * (N + 1) + c) * mat);
+    for (int st = 0; st < stages; ++st) {
+        const int t0 = first + st * NT, nt = min(NT, first + len - t0);
+        stage(t0, nt);
+        for (int t = 0; t < nt; ++t) {
             const float al = sa[t];
             float p[4] = {0, 0, 0, 0}, w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -239,24 +277,39 @@ __global__ void __launch_bounds__(SWT) row_sweep_kernel(const Args a) {
                 const float e = se[t][lane + 16 * i], x = sx[t][lane + 16 * i], d = sd[t][lane + 16 * i];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    if (!REV) {
-                        S[i][r] *= al;
-                        p[r] = fmaf(S[i][r], x, p[r]);
-                        S[i][r] = fmaf(sk[t][grp * 4 + r], e, S[i][r]);
-                        w[r] = fmaf(S[i][r], d, w[r]);
-                    } else {
-                        S[i][r] = fmaf(sq[t][grp * 4 + r], d, S[i][r]);
-                        p[r] = fmaf(S[i][r], e, p[r]);
-                        S[i][r] = al * fmaf(-sk[t][grp * 4 + r], x, S[i][r]);
-                    }
+                    S[i][r] *= al;
+                    p[r] = fmaf(S[i][r], x, p[r]);
+                    S[i][r] = fmaf(sk[t][grp * 4 + r], e, S[i][r]);
+                    w[r] = fmaf(S[i][r], d, w[r]);
+                }
+            }
+            const float v = sum4_16(p, lane), dq = sum4_16(w, lane);
+            if (lane % 4 == 0) {
+                dk[t0 - first + t][grp * 4 + mine] = v;
+                if (on) a.dqh[(((long long)b * a.L + t0 + t) * a.Hv + h) * a.Dk + row + mine] = dq;
+            }
+        }
+    }
+    load(static_cast<const float *>(a.z) + (bh * N + c) * mat);
+    for (int st = stages - 1; st >= 0; --st) {
+        const int t0 = first + st * NT, nt = min(NT, first + len - t0);
+        stage(t0, nt);
+        for (int t = nt - 1; t >= 0; --t) {
+            const float al = sa[t];
+            float p[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                const float e = se[t][lane + 16 * i], x = sx[t][lane + 16 * i], d = sd[t][lane + 16 * i];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    S[i][r] = fmaf(sq[t][grp * 4 + r], d, S[i][r]);
+                    p[r] = fmaf(S[i][r], e, p[r]);
+                    S[i][r] = al * fmaf(-sk[t][grp * 4 + r], x, S[i][r]);
                 }
             }
             const float v = sum4_16(p, lane);
-            if (!REV) {
-                const float dq = sum4_16(w, lane);
-                if (on && lane % 4 == 0) a.dqh[out] = dq, a.dkh[out] = -v;
-            } else if (on && lane % 4 == 0)
-                a.dkh[out] += v;
+            if (on && lane % 4 == 0)
+                a.dkh[(((long long)b * a.L + t0 + t) * a.Hv + h) * a.Dk + row + mine] = v - dk[t0 - first + t][grp * 4 + mine];
         }
     }
 }
@@ -524,28 +577,28 @@ cudaError_t step(const void *q, const void *k, const void *v, const float *g, co
 template <typename T, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
     const dim3 grid((a.Dv + OWN - 1) / OWN, a.Hv, a.B);
     if (a.Dk <= 64)
-        column_sweep_kernel<T, 4, REV><<<grid, SWT, 0, st>>>(a);
-    else if (a.Dk <= 128)
         column_sweep_kernel<T, 8, REV><<<grid, SWT, 0, st>>>(a);
-    else
+    else if (a.Dk <= 128)
         column_sweep_kernel<T, 16, REV><<<grid, SWT, 0, st>>>(a);
+    else
+        column_sweep_kernel<T, 32, REV><<<grid, SWT, 0, st>>>(a);
     return cudaGetLastError();
 }
-template <typename T, bool REV> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
-    const dim3 grid((a.Dk + OWN - 1) / OWN, a.Hv, a.B);
+template <typename T> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
+    const dim3 grid((a.Dk + OWN - 1) / OWN * chunks(a.L), a.Hv, a.B);
     if (a.Dv <= 64)
-        row_sweep_kernel<T, 4, REV><<<grid, SWT, 0, st>>>(a);
+        row_sweep_kernel<T, 4><<<grid, SWT, 0, st>>>(a);
     else if (a.Dv <= 128)
-        row_sweep_kernel<T, 8, REV><<<grid, SWT, 0, st>>>(a);
+        row_sweep_kernel<T, 8><<<grid, SWT, 0, st>>>(a);
     else
-        row_sweep_kernel<T, 16, REV><<<grid, SWT, 0, st>>>(a);
+        row_sweep_kernel<T, 16><<<grid, SWT, 0, st>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
     cudaError_t e = column_sweep<T, true>(a, st);
     if (e != cudaSuccess || a.L == 0) return e;
-    if ((e = row_sweep<T, false>(a, st)) != cudaSuccess || (e = row_sweep<T, true>(a, st)) != cudaSuccess) return e;
+    if ((e = row_sweep<T>(a, st)) != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.L * a.Hv;
     token_grads_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
     decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a);
@@ -576,8 +629,8 @@ s5_status check_sizes(long long B, long long L, long long Hk, long long Hv, long
 }
 
 // Regions of the two buffers.  The backward workspace holds what either path
-// needs: dq and dk per value head or the chunks' Z; parts of <S, Z> (16 at
-// most) and the tokens' sums.
+// needs: dq and dk per value head, the chunks' Z (as many bytes in either form,
+// one less than the states), parts of <S, Z> (16 at most), the tokens' sums.
 struct Sizes {
     size_t e, states, images, heads, inner, dots;
 };
@@ -592,8 +645,6 @@ Sizes sizes(int B, int L, int Hv, int Dk, int Dv) {
     s.dots = align256(sizeof(float) * rows);
     return s;
 }
-size_t z_or_heads(const Sizes &s) { return s.images ? (s.states > 2 * s.heads ? s.states : 2 * s.heads) : 2 * s.heads; }
-
 }  // namespace
 }  // namespace delta
 }  // namespace s5
@@ -611,7 +662,7 @@ extern "C" size_t s5_delta_workspace_size(int B, int L, int Hv, int Dk, int Dv, 
     if (check_sizes(B, L, Hv, Hv, Dk, Dv, S5_F32) != S5_OK) return 0;
     const Sizes s = sizes(B, L, Hv, Dk, Dv);
     size_t n = 256 + s.images;
-    if (backward) n += s.e + z_or_heads(s) + s.inner + s.dots;
+    if (backward) n += s.e + 2 * s.heads + s.states + s.inner + s.dots;
     return n;
 }
 
@@ -697,8 +748,9 @@ extern "C" s5_status s5_delta_backward(const void *q, long long ldq, const void 
     w += s.e;
     a.dqh = reinterpret_cast<float *>(w);
     a.dkh = reinterpret_cast<float *>(w + s.heads);
+    w += 2 * s.heads;
     a.z = w;
-    w += z_or_heads(s);
+    w += s.states;
     a.parts = (Dv + OWN - 1) / OWN;
     a.inner = reinterpret_cast<float *>(w);
     w += s.inner;

@@ -37,7 +37,8 @@ struct Args {
     float *inner;                     // [B][Hv][N + 1][parts]   parts of <S_c, dL/dS_c>
     float *dots;                      // [B][L][Hv] o.do - v.dv
     int parts;
-    void *z;                          // [B][Hv][N][Dv / 64][2][Dk][64] bf16: dL/dS at the end of chunk c, two parts (tensor cores)
+    void *z;                          // dL/dS at the end of chunk c: [B][Hv][N][Dk][Dv] float32, or, for the tensor
+                                      // cores, [B][Hv][N][Dv / 64][2][Dk][64] bf16 (two parts)
     void *images;                     // operand images of the tensor-core path
 };
 
