@@ -25,7 +25,7 @@
 //
 // Bound: the chain of a token in the column sweeps (product, sum over 8 lanes,
 // update); the state stays in registers, two warps of a block bring the next
-// tokens to shared memory while the other two run these.
+// tokens to shared memory while the others run these.
 #include "s5_delta.cuh"
 
 namespace s5 {
@@ -40,16 +40,12 @@ constexpr int SWT = 128;      // threads of a sweep
 // 3072 (6.4 TB/s).
 constexpr int HEAD_BLOCKS = 80;
 
-// Sums of four values over 8 lanes; lane l gets the sum of value l / 2 % 4.
-__device__ __forceinline__ float sum4_8(const float (&v)[4], int lane) {
-    const bool up = lane & 4, up2 = lane & 2;
-    float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
-    a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 4);
-    b += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 4);
-    float c = up2 ? b : a;
-    c += __shfl_xor_sync(0xffffffffu, up2 ? a : b, 2);
-    c += __shfl_xor_sync(0xffffffffu, c, 1);
-    return c;
+// The sum over the 8 lanes that hold one column (lane bits 2 to 4).
+__device__ __forceinline__ float column_sum(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    return v;
 }
 // Sums of four values over 16 lanes; lane l gets the sum of value l / 4 % 4.
 __device__ __forceinline__ float sum4_16(const float (&v)[4], int lane) {
@@ -70,147 +66,147 @@ template <typename T> __device__ __forceinline__ float elem(const void *p, long 
 
 // Columns over the grid.  REV false: the forward recurrence, writing o (and
 // what the backward pass needs); REV true: the adjoint, writing X and the
-// adjoint at each chunk's end.  Warps 0 and 1: 8 lanes by 8 groups of four
-// columns, rows lane + 8 i; warps 2 and 3 stage the next tokens.
+// adjoint at each chunk's end.  Eight warps hold 32 columns, a column in 8
+// lanes, rows 32 i + 4 lane + 0..3 (one 16-byte read of a key for four rows);
+// two more warps stage the next tokens.
+constexpr int COLT = 256;
 template <typename T, int RPT, bool REV>
-__global__ void __launch_bounds__(SWT) column_sweep_kernel(const Args a) {
+__global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
     constexpr int NT = RPT > 16 ? TB / 2 : TB, D = 8 * RPT;
-    __shared__ float sq[2][NT][D], sk[2][NT][D], sv[2][NT][OWN], sa[2][NT], sb[2][NT];
-    __shared__ float red[2];
-    const int lane = threadIdx.x % 8, grp = threadIdx.x / 8 % 8;
-    const bool loads = threadIdx.x >= 64;
+    __shared__ __align__(16) float sq[2][NT][D], sk[2][NT][D];
+    __shared__ float sv[2][NT][OWN], sa[2][NT], sb[2][NT], red[COLT / 32];
+    const int lane = threadIdx.x / 4 % 8, own = threadIdx.x / 32 * 4 + threadIdx.x % 4;   // row lane, column
+    const bool loads = threadIdx.x >= COLT;
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
-    const int col = blockIdx.x * OWN + grp * 4;
-    const int mine = lane / 2;                       // the column whose sums this lane gets
-    const bool on = !loads && col < a.Dv;            // Dv is a multiple of 4
+    const int col = blockIdx.x * OWN + own;
+    const bool on = !loads && col < a.Dv, first = on && lane == 0;
     const int N = chunks(a.L);
     const long long bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
     const float *init = REV ? a.ds_last : a.s0;
-    float S[RPT][4];
+    float S[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-        const int r = lane + 8 * i;
-        const float4 t = (init && on && r < a.Dk) ? *reinterpret_cast<const float4 *>(init + bh * mat + (long long)r * a.Dv + col)
-                                                  : make_float4(0, 0, 0, 0);
-        S[i][0] = t.x, S[i][1] = t.y, S[i][2] = t.z, S[i][3] = t.w;
+        const int r = 32 * (i / 4) + 4 * lane + i % 4;
+        S[i] = (init && on && r < a.Dk) ? init[bh * mat + (long long)r * a.Dv + col] : 0.0f;
     }
     auto keep = [&](float *to) {
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            const int r = lane + 8 * i;
-            if (on && r < a.Dk)
-                *reinterpret_cast<float4 *>(to + (long long)r * a.Dv + col) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+            const int r = 32 * (i / 4) + 4 * lane + i % 4;
+            if (on && r < a.Dk) to[(long long)r * a.Dv + col] = S[i];
         }
     };
-    // <S_c, Z_c> of this block's columns (the two compute warps)
+    // <S_c, Z_c> of this block's columns (the compute warps)
     auto inner = [&](int c) {
         const float *s = a.states + (bh * (N + 1) + c) * mat;
         float w = 0.0f;
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            const int r = lane + 8 * i;
-            if (on && r < a.Dk) {
-                const float4 t = *reinterpret_cast<const float4 *>(s + (long long)r * a.Dv + col);
-                w += t.x * S[i][0] + t.y * S[i][1] + t.z * S[i][2] + t.w * S[i][3];
-            }
+            const int r = 32 * (i / 4) + 4 * lane + i % 4;
+            if (on && r < a.Dk) w = fmaf(s[(long long)r * a.Dv + col], S[i], w);
         }
         for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
         if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = w;
-        asm volatile("bar.sync 1, 64;" ::: "memory");
-        if (threadIdx.x == 0) a.inner[(bh * (N + 1) + c) * a.parts + blockIdx.x] = red[0] + red[1];
-        asm volatile("bar.sync 1, 64;" ::: "memory");
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (threadIdx.x == 0) {
+            w = 0.0f;
+            for (int i = 0; i < COLT / 32; ++i) w += red[i];
+            a.inner[(bh * (N + 1) + c) * a.parts + blockIdx.x] = w;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
     };
     const int stages = (a.L + NT - 1) / NT;
-    auto stage = [&](int st, int buf, int tid, int threads) {
+    // 64 threads, a column of values each: all tokens' loads are in flight at once
+    auto stage = [&](int st, int buf, int tid) {
         const int t0 = (REV ? stages - 1 - st : st) * NT, nt = min(NT, a.L - t0);
         const long long row0 = (long long)b * a.L + t0;
-        for (int i = tid; i < nt * D; i += threads) {
-            const int t = i / D, r = i % D;
-            const bool in = r < a.Dk;
-            sq[buf][t][r] = in ? a.scale * elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
-            sk[buf][t][r] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
+#pragma unroll
+        for (int r = tid; r < D; r += 64) {
+            float x[NT], y[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const bool in = t < nt && r < a.Dk;
+                x[t] = in ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
+                y[t] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sq[buf][t][r] = a.scale * x[t], sk[buf][t][r] = y[t];
         }
-        for (int i = tid; i < nt * OWN; i += threads) {
-            const int t = i / OWN, c = blockIdx.x * OWN + i % OWN;
-            sv[buf][t][i % OWN] = c >= a.Dv ? 0.0f
-                                  : REV     ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + c)
-                                            : elem<T>(a.v, (row0 + t) * a.ldv + (long long)h * a.Dv + c);
+        const int c = tid % OWN, v = blockIdx.x * OWN + c;
+        float x[NT / 2], g = 0.0f, be = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) {
+            const int t = 2 * i + tid / OWN;
+            const bool in = t < nt && v < a.Dv;
+            x[i] = !in   ? 0.0f
+                   : REV ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + v)
+                         : elem<T>(a.v, (row0 + t) * a.ldv + (long long)h * a.Dv + v);
         }
-        if (tid < nt) {
-            sa[buf][tid] = expf(clamp_g(a.g[(row0 + tid) * a.Hv + h]));
-            sb[buf][tid] = a.beta[(row0 + tid) * a.Hv + h];
-        }
+        if (tid < nt) g = a.g[(row0 + tid) * a.Hv + h], be = a.beta[(row0 + tid) * a.Hv + h];
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) sv[buf][2 * i + tid / OWN][c] = x[i];
+        if (tid < nt) sa[buf][tid] = expf(clamp_g(g)), sb[buf][tid] = be;
     };
     if (REV && !loads) inner(N);
-    if (stages > 0) stage(0, 0, threadIdx.x, SWT);
+    if (loads && stages > 0) stage(0, 0, threadIdx.x - COLT);
     __syncthreads();
     for (int st = 0; st < stages; ++st) {
         const int buf = st & 1;
         if (loads) {
-            if (st + 1 < stages) stage(st + 1, buf ^ 1, threadIdx.x - 64, 64);
+            if (st + 1 < stages) stage(st + 1, buf ^ 1, threadIdx.x - COLT);
             __syncthreads();
             continue;
         }
         const int t0 = (REV ? stages - 1 - st : st) * NT, nt = min(NT, a.L - t0);
         const long long row0 = (long long)b * a.L + t0;
+#pragma unroll 2
         for (int j = 0; j < nt; ++j) {
             const int t = REV ? nt - 1 - j : j, tok = t0 + t;
-            const long long out = ((row0 + t) * a.Hv + h) * a.Dv + col + mine;
-            const float *kt = sk[buf][t], *qt = sq[buf][t];
-            float p[4] = {0, 0, 0, 0}, u[4];
-            const float al = sa[buf][t], be = sb[buf][t];
+            const long long out = ((row0 + t) * a.Hv + h) * a.Dv + col;
+            const float4 *kt = reinterpret_cast<const float4 *>(sk[buf][t]) + lane, *qt = reinterpret_cast<const float4 *>(sq[buf][t]) + lane;
+            const float al = sa[buf][t], be = sb[buf][t], x = sv[buf][t][own];
+            float p[4] = {0, 0, 0, 0};   // four sums: a short chain
             if (!REV) {
                 if (a.states && tok % CHUNK == 0) keep(a.states + (bh * (N + 1) + tok / CHUNK) * mat);
 #pragma unroll
-                for (int i = 0; i < RPT; ++i) {
-                    const float kk = kt[lane + 8 * i];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        S[i][c] *= al;
-                        p[c] = fmaf(S[i][c], kk, p[c]);
-                    }
+                for (int i = 0; i < RPT / 4; ++i) {
+                    const float4 k = kt[8 * i];
+                    p[0] = fmaf(S[4 * i], k.x, p[0]), p[1] = fmaf(S[4 * i + 1], k.y, p[1]);
+                    p[2] = fmaf(S[4 * i + 2], k.z, p[2]), p[3] = fmaf(S[4 * i + 3], k.w, p[3]);
                 }
-                const float e = sv[buf][t][grp * 4 + mine] - sum4_8(p, lane);
-                if (a.e && on && lane % 2 == 0) a.e[out] = e;
-                const float um = be * e;
+                const float e = fmaf(-al, column_sum((p[0] + p[1]) + (p[2] + p[3])), x), u = be * e;
+                p[0] = p[1] = p[2] = p[3] = 0.0f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, um, 2 * c, 8), p[c] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < RPT; ++i) {
-                    const float kk = kt[lane + 8 * i], qq = qt[lane + 8 * i];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        S[i][c] = fmaf(kk, u[c], S[i][c]);
-                        p[c] = fmaf(S[i][c], qq, p[c]);
-                    }
+                for (int i = 0; i < RPT / 4; ++i) {
+                    const float4 k = kt[8 * i], q = qt[8 * i];
+                    S[4 * i] = fmaf(k.x, u, al * S[4 * i]), S[4 * i + 1] = fmaf(k.y, u, al * S[4 * i + 1]);
+                    S[4 * i + 2] = fmaf(k.z, u, al * S[4 * i + 2]), S[4 * i + 3] = fmaf(k.w, u, al * S[4 * i + 3]);
+                    p[0] = fmaf(S[4 * i], q.x, p[0]), p[1] = fmaf(S[4 * i + 1], q.y, p[1]);
+                    p[2] = fmaf(S[4 * i + 2], q.z, p[2]), p[3] = fmaf(S[4 * i + 3], q.w, p[3]);
                 }
-                const float o = sum4_8(p, lane);
-                if (on && lane % 2 == 0) {
-                    store_elem<T>(static_cast<T *>(a.o) + (row0 + t) * a.ldo + (long long)h * a.Dv + col + mine, o);
-                    if (a.o32) a.o32[out] = o;
+                const float o = column_sum((p[0] + p[1]) + (p[2] + p[3]));
+                if (first) {
+                    store_elem<T>(static_cast<T *>(a.o) + (row0 + t) * a.ldo + (long long)h * a.Dv + col, o);
+                    if (a.e) a.e[out] = e, a.o32[out] = o;
                 }
             } else {
                 if ((tok + 1) % CHUNK == 0 || tok == a.L - 1)
                     keep(static_cast<float *>(a.z) + (bh * N + tok / CHUNK) * mat);
 #pragma unroll
-                for (int i = 0; i < RPT; ++i) {
-                    const float kk = kt[lane + 8 * i], qq = qt[lane + 8 * i];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        S[i][c] = fmaf(qq, sv[buf][t][grp * 4 + c], S[i][c]);
-                        p[c] = fmaf(S[i][c], kk, p[c]);
-                    }
+                for (int i = 0; i < RPT / 4; ++i) {
+                    const float4 k = kt[8 * i], q = qt[8 * i];
+                    S[4 * i] = fmaf(q.x, x, S[4 * i]), S[4 * i + 1] = fmaf(q.y, x, S[4 * i + 1]);
+                    S[4 * i + 2] = fmaf(q.z, x, S[4 * i + 2]), S[4 * i + 3] = fmaf(q.w, x, S[4 * i + 3]);
+                    p[0] = fmaf(S[4 * i], k.x, p[0]), p[1] = fmaf(S[4 * i + 1], k.y, p[1]);
+                    p[2] = fmaf(S[4 * i + 2], k.z, p[2]), p[3] = fmaf(S[4 * i + 3], k.w, p[3]);
                 }
-                const float x = sum4_8(p, lane);
-                if (on && lane % 2 == 0) a.x[out] = x;
-                const float um = be * x;
+                const float X = column_sum((p[0] + p[1]) + (p[2] + p[3])), u = be * X;
+                if (first) a.x[out] = X;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, um, 2 * c, 8);
-#pragma unroll
-                for (int i = 0; i < RPT; ++i) {
-                    const float kk = kt[lane + 8 * i];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) S[i][c] = al * fmaf(-kk, u[c], S[i][c]);
+                for (int i = 0; i < RPT / 4; ++i) {
+                    const float4 k = kt[8 * i];
+                    S[4 * i] = al * fmaf(-k.x, u, S[4 * i]), S[4 * i + 1] = al * fmaf(-k.y, u, S[4 * i + 1]);
+                    S[4 * i + 2] = al * fmaf(-k.z, u, S[4 * i + 2]), S[4 * i + 3] = al * fmaf(-k.w, u, S[4 * i + 3]);
                 }
                 if (tok % CHUNK == 0) inner(tok / CHUNK);
             }
@@ -248,19 +244,31 @@ __global__ void __launch_bounds__(SWT) row_sweep_kernel(const Args a) {
     auto stage = [&](int t0, int nt) {
         const long long row0 = (long long)b * a.L + t0;
         __syncthreads();
-        for (int i = threadIdx.x; i < nt * 16 * RPT; i += SWT) {
-            const int t = i / (16 * RPT), v = i % (16 * RPT);
-            const bool in = v < a.Dv;
-            const long long hv = (row0 + t) * a.Hv + h;
-            const float be = a.beta[hv];
-            se[t][v] = in ? be * a.e[hv * a.Dv + v] : 0.0f;
-            sx[t][v] = in ? be * a.x[hv * a.Dv + v] : 0.0f;
-            sd[t][v] = in ? a.scale * elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + v) : 0.0f;
+        constexpr int DV = 16 * RPT, PER = NT * DV / SWT;   // a thread's values of each array, all in flight
+        {
+            float x[PER], y[PER], d[PER], be[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int at = threadIdx.x + i * SWT, t = at / DV, v = at % DV;
+                const bool in = t < nt && v < a.Dv;
+                const long long hv = (row0 + t) * a.Hv + h;
+                be[i] = in ? a.beta[hv] : 0.0f;
+                x[i] = in ? a.e[hv * a.Dv + v] : 0.0f;
+                y[i] = in ? a.x[hv * a.Dv + v] : 0.0f;
+                d[i] = in ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + v) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int at = threadIdx.x + i * SWT, t = at / DV, v = at % DV;
+                se[t][v] = be[i] * x[i], sx[t][v] = be[i] * y[i], sd[t][v] = a.scale * d[i];
+            }
         }
-        for (int i = threadIdx.x; i < nt * OWN; i += SWT) {
-            const int t = i / OWN, r = r0 + i % OWN;
-            sq[t][i % OWN] = r < a.Dk ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
-            sk[t][i % OWN] = r < a.Dk ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NT * OWN / SWT; ++i) {
+            const int at = threadIdx.x + i * SWT, t = at / OWN, r = r0 + at % OWN;
+            const bool in = t < nt && r < a.Dk;
+            sq[t][at % OWN] = in ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
+            sk[t][at % OWN] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
         }
         if (threadIdx.x < nt) sa[threadIdx.x] = expf(clamp_g(a.g[(row0 + threadIdx.x) * a.Hv + h]));
         __syncthreads();
@@ -577,11 +585,11 @@ cudaError_t step(const void *q, const void *k, const void *v, const float *g, co
 template <typename T, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
     const dim3 grid((a.Dv + OWN - 1) / OWN, a.Hv, a.B);
     if (a.Dk <= 64)
-        column_sweep_kernel<T, 8, REV><<<grid, SWT, 0, st>>>(a);
+        column_sweep_kernel<T, 8, REV><<<grid, COLT + 64, 0, st>>>(a);
     else if (a.Dk <= 128)
-        column_sweep_kernel<T, 16, REV><<<grid, SWT, 0, st>>>(a);
+        column_sweep_kernel<T, 16, REV><<<grid, COLT + 64, 0, st>>>(a);
     else
-        column_sweep_kernel<T, 32, REV><<<grid, SWT, 0, st>>>(a);
+        column_sweep_kernel<T, 32, REV><<<grid, COLT + 64, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename T> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
