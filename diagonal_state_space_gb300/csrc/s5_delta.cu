@@ -36,8 +36,8 @@ constexpr int TB = 16;        // tokens staged in shared memory (8 for heads abo
 constexpr int OWN = 32;       // columns (or rows) of a block
 constexpr int SWT = 128;      // threads of a sweep
 // Heads (B Hv) from which on a step takes a block for each, against a block for
-// 32 columns: 3.8 / 4.5 us at 96 heads of 128 x 128, 3.7 / 3.2 at 64, 63 / 77 at
-// 3072 (6.4 TB/s).
+// 32 columns: 3.8 / 4.5 us at 96 heads of 128 x 128, 3.7 / 3.2 at 64, 63 / 77 for
+// 96 sequences of 32 heads (6.4 TB/s).
 constexpr int HEAD_BLOCKS = 80;
 
 // The sum over the 8 lanes that hold one column (lane bits 2 to 4).
@@ -168,23 +168,33 @@ __global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
             float p[4] = {0, 0, 0, 0};   // four sums: a short chain
             if (!REV) {
                 if (a.states && tok % CHUNK == 0) keep(a.states + (bh * (N + 1) + tok / CHUNK) * mat);
-#pragma unroll
-                for (int i = 0; i < RPT / 4; ++i) {
-                    const float4 k = kt[8 * i];
-                    p[0] = fmaf(S[4 * i], k.x, p[0]), p[1] = fmaf(S[4 * i + 1], k.y, p[1]);
-                    p[2] = fmaf(S[4 * i + 2], k.z, p[2]), p[3] = fmaf(S[4 * i + 3], k.w, p[3]);
-                }
-                const float e = fmaf(-al, column_sum((p[0] + p[1]) + (p[2] + p[3])), x), u = be * e;
-                p[0] = p[1] = p[2] = p[3] = 0.0f;
+                float y[4] = {0, 0, 0, 0}, z[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < RPT / 4; ++i) {
                     const float4 k = kt[8 * i], q = qt[8 * i];
+                    p[0] = fmaf(S[4 * i], k.x, p[0]), p[1] = fmaf(S[4 * i + 1], k.y, p[1]);
+                    p[2] = fmaf(S[4 * i + 2], k.z, p[2]), p[3] = fmaf(S[4 * i + 3], k.w, p[3]);
+                    y[0] = fmaf(S[4 * i], q.x, y[0]), y[1] = fmaf(S[4 * i + 1], q.y, y[1]);
+                    y[2] = fmaf(S[4 * i + 2], q.z, y[2]), y[3] = fmaf(S[4 * i + 3], q.w, y[3]);
+                    z[0] = fmaf(k.x, q.x, z[0]), z[1] = fmaf(k.y, q.y, z[1]);
+                    z[2] = fmaf(k.z, q.z, z[2]), z[3] = fmaf(k.w, q.w, z[3]);
+                }
+                // o = a S^T q + u (k . q) from the state before: its sums run
+                // beside e's instead of after them
+                float sk = (p[0] + p[1]) + (p[2] + p[3]), sq = (y[0] + y[1]) + (y[2] + y[3]), kq = (z[0] + z[1]) + (z[2] + z[3]);
+#pragma unroll
+                for (int m = 16; m > 2; m >>= 1) {   // the column's 8 lanes
+                    const float x0 = __shfl_xor_sync(0xffffffffu, sk, m), x1 = __shfl_xor_sync(0xffffffffu, sq, m),
+                                x2 = __shfl_xor_sync(0xffffffffu, kq, m);
+                    sk += x0, sq += x1, kq += x2;
+                }
+                const float e = fmaf(-al, sk, x), u = be * e, o = fmaf(u, kq, al * sq);
+#pragma unroll
+                for (int i = 0; i < RPT / 4; ++i) {
+                    const float4 k = kt[8 * i];
                     S[4 * i] = fmaf(k.x, u, al * S[4 * i]), S[4 * i + 1] = fmaf(k.y, u, al * S[4 * i + 1]);
                     S[4 * i + 2] = fmaf(k.z, u, al * S[4 * i + 2]), S[4 * i + 3] = fmaf(k.w, u, al * S[4 * i + 3]);
-                    p[0] = fmaf(S[4 * i], q.x, p[0]), p[1] = fmaf(S[4 * i + 1], q.y, p[1]);
-                    p[2] = fmaf(S[4 * i + 2], q.z, p[2]), p[3] = fmaf(S[4 * i + 3], q.w, p[3]);
                 }
-                const float o = column_sum((p[0] + p[1]) + (p[2] + p[3]));
                 if (first) {
                     store_elem<T>(static_cast<T *>(a.o) + (row0 + t) * a.ldo + (long long)h * a.Dv + col, o);
                     if (a.e) a.e[out] = e, a.o32[out] = o;
