@@ -159,15 +159,17 @@ __global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
         }
         const int t0 = (REV ? stages - 1 - st : st) * NT, nt = min(NT, a.L - t0);
         const long long row0 = (long long)b * a.L + t0;
-#pragma unroll 2
+        // a stage lies within a chunk
+        if (!REV && a.states && t0 % CHUNK == 0) keep(a.states + (bh * (N + 1) + t0 / CHUNK) * mat);
+        if (REV && ((t0 + nt) % CHUNK == 0 || t0 + nt == a.L)) keep(static_cast<float *>(a.z) + (bh * N + t0 / CHUNK) * mat);
+#pragma unroll 4
         for (int j = 0; j < nt; ++j) {
-            const int t = REV ? nt - 1 - j : j, tok = t0 + t;
+            const int t = REV ? nt - 1 - j : j;
             const long long out = ((row0 + t) * a.Hv + h) * a.Dv + col;
             const float4 *kt = reinterpret_cast<const float4 *>(sk[buf][t]) + lane, *qt = reinterpret_cast<const float4 *>(sq[buf][t]) + lane;
             const float al = sa[buf][t], be = sb[buf][t], x = sv[buf][t][own];
             float p[4] = {0, 0, 0, 0};   // four sums: a short chain
             if (!REV) {
-                if (a.states && tok % CHUNK == 0) keep(a.states + (bh * (N + 1) + tok / CHUNK) * mat);
                 float y[4] = {0, 0, 0, 0}, z[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < RPT / 4; ++i) {
@@ -200,8 +202,6 @@ __global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
                     if (a.e) a.e[out] = e, a.o32[out] = o;
                 }
             } else {
-                if ((tok + 1) % CHUNK == 0 || tok == a.L - 1)
-                    keep(static_cast<float *>(a.z) + (bh * N + tok / CHUNK) * mat);
 #pragma unroll
                 for (int i = 0; i < RPT / 4; ++i) {
                     const float4 k = kt[8 * i], q = qt[8 * i];
@@ -218,9 +218,9 @@ __global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
                     S[4 * i] = al * fmaf(-k.x, u, S[4 * i]), S[4 * i + 1] = al * fmaf(-k.y, u, S[4 * i + 1]);
                     S[4 * i + 2] = al * fmaf(-k.z, u, S[4 * i + 2]), S[4 * i + 3] = al * fmaf(-k.w, u, S[4 * i + 3]);
                 }
-                if (tok % CHUNK == 0) inner(tok / CHUNK);
             }
         }
+        if (REV && t0 % CHUNK == 0) inner(t0 / CHUNK);
         __syncthreads();
     }
     if (loads) return;
