@@ -116,44 +116,55 @@ __global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
         asm volatile("bar.sync 1, 256;" ::: "memory");
     };
     const int stages = (a.L + NT - 1) / NT;
-    // 64 threads, a column of values each: all tokens' loads are in flight at once
-    auto stage = [&](int st, int buf, int tid) {
+    // Staging by 64 threads, a column of values each: `fetch` has all of a
+    // stage's loads in flight, `put` writes them a stage later.
+    const int tid = threadIdx.x - COLT, own_v = tid % OWN, half = tid / OWN;
+    constexpr int PER = D / 64;
+    float fq[PER][NT], fk[PER][NT], fv[NT / 2], fg = 0.0f, fb = 0.0f;
+    auto fetch = [&](int st) {
         const int t0 = (REV ? stages - 1 - st : st) * NT, nt = min(NT, a.L - t0);
         const long long row0 = (long long)b * a.L + t0;
 #pragma unroll
-        for (int r = tid; r < D; r += 64) {
-            float x[NT], y[NT];
+        for (int i = 0; i < PER; ++i) {
+            const int r = tid + 64 * i;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const bool in = t < nt && r < a.Dk;
-                x[t] = in ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
-                y[t] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
+                fq[i][t] = in ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
+                fk[i][t] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
             }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) sq[buf][t][r] = a.scale * x[t], sk[buf][t][r] = y[t];
         }
-        const int c = tid % OWN, v = blockIdx.x * OWN + c;
-        float x[NT / 2], g = 0.0f, be = 0.0f;
+        const int v = blockIdx.x * OWN + own_v;
 #pragma unroll
         for (int i = 0; i < NT / 2; ++i) {
-            const int t = 2 * i + tid / OWN;
+            const int t = 2 * i + half;
             const bool in = t < nt && v < a.Dv;
-            x[i] = !in   ? 0.0f
-                   : REV ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + v)
-                         : elem<T>(a.v, (row0 + t) * a.ldv + (long long)h * a.Dv + v);
+            fv[i] = !in   ? 0.0f
+                    : REV ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + v)
+                          : elem<T>(a.v, (row0 + t) * a.ldv + (long long)h * a.Dv + v);
         }
-        if (tid < nt) g = a.g[(row0 + tid) * a.Hv + h], be = a.beta[(row0 + tid) * a.Hv + h];
+        if (tid < nt) fg = a.g[(row0 + tid) * a.Hv + h], fb = a.beta[(row0 + tid) * a.Hv + h];
+    };
+    auto put = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i) sv[buf][2 * i + tid / OWN][c] = x[i];
-        if (tid < nt) sa[buf][tid] = expf(clamp_g(g)), sb[buf][tid] = be;
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sq[buf][t][tid + 64 * i] = a.scale * fq[i][t], sk[buf][t][tid + 64 * i] = fk[i][t];
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) sv[buf][2 * i + half][own_v] = fv[i];
+        if (tid < NT) sa[buf][tid] = expf(clamp_g(fg)), sb[buf][tid] = fb;
     };
     if (REV && !loads) inner(N);
-    if (loads && stages > 0) stage(0, 0, threadIdx.x - COLT);
+    if (loads && stages > 0) {
+        fetch(0), put(0);
+        if (stages > 1) fetch(1);
+    }
     __syncthreads();
     for (int st = 0; st < stages; ++st) {
         const int buf = st & 1;
         if (loads) {
-            if (st + 1 < stages) stage(st + 1, buf ^ 1, threadIdx.x - COLT);
+            if (st + 1 < stages) put(buf ^ 1);
+            if (st + 2 < stages) fetch(st + 2);
             __syncthreads();
             continue;
         }
