@@ -33,7 +33,13 @@ namespace delta {
 namespace {
 
 constexpr int TB = 16;        // tokens staged in shared memory (8 for heads above 128)
-constexpr int OWN = 32;       // columns (or rows) of a block
+constexpr int OWN = 32;       // rows of a block
+// Blocks of 8 columns up to which the column sweep uses them, against blocks of
+// 32 (one read of the keys for four times the columns, but a fourth of the SMs
+// when heads are few).  Forward, 400 tokens, 8 / 32 columns, us: 128 x 128 heads,
+// 83 / 131 at 64 blocks, 109 / 133 at 256, 211 / 132 at 512; 64 x 64, 73 / 89 at
+// 64, 89 / 89 at 256, 159 / 90 at 512.
+constexpr int NARROW_BLOCKS = 256;
 constexpr int SWT = 128;      // threads of a sweep
 // Heads (B Hv) from which on a step takes a block for each, against a block for
 // 32 columns: 3.8 / 4.5 us at 96 heads of 128 x 128, 3.7 / 3.2 at 64, 63 / 77 for
@@ -66,19 +72,21 @@ template <typename T> __device__ __forceinline__ float elem(const void *p, long 
 
 // Columns over the grid.  REV false: the forward recurrence, writing o (and
 // what the backward pass needs); REV true: the adjoint, writing X and the
-// adjoint at each chunk's end.  Eight warps hold 32 columns, a column in 8
-// lanes, rows 32 i + 4 lane + 0..3 (one 16-byte read of a key for four rows);
-// two more warps stage the next tokens.
-constexpr int COLT = 256;
-template <typename T, int RPT, bool REV>
-__global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
+// adjoint at each chunk's end.  A column is held by 8 lanes, rows 32 i + 4 lane +
+// 0..3 (one 16-byte read of a key for four rows), a block has C columns; two more
+// warps stage the tokens.  Bound by the chain from token to token (smem read,
+// products, three shuffles, update): 0.19 us a token forward, 0.13 back at heads of
+// 64 x 64, whatever their number while the blocks fit the SMs.
+template <typename T, int RPT, int C, bool REV>
+__global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) {
+    constexpr int COLT = 8 * C;
     constexpr int NT = RPT > 16 ? TB / 2 : TB, D = 8 * RPT;
     __shared__ __align__(16) float sq[2][NT][D], sk[2][NT][D];
-    __shared__ float sv[2][NT][OWN], sa[2][NT], sb[2][NT], red[COLT / 32];
+    __shared__ float sv[2][NT][C], sa[2][NT], sb[2][NT], red[COLT / 32];
     const int lane = threadIdx.x / 4 % 8, own = threadIdx.x / 32 * 4 + threadIdx.x % 4;   // row lane, column
     const bool loads = threadIdx.x >= COLT;
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
-    const int col = blockIdx.x * OWN + own;
+    const int col = blockIdx.x * C + own;
     const bool on = !loads && col < a.Dv, first = on && lane == 0;
     const int N = chunks(a.L);
     const long long bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
@@ -107,20 +115,20 @@ __global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
         }
         for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
         if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = w;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(COLT) : "memory");
         if (threadIdx.x == 0) {
             w = 0.0f;
             for (int i = 0; i < COLT / 32; ++i) w += red[i];
             a.inner[(bh * (N + 1) + c) * a.parts + blockIdx.x] = w;
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(COLT) : "memory");
     };
     const int stages = (a.L + NT - 1) / NT;
     // Staging by 64 threads, a column of values each: `fetch` has all of a
     // stage's loads in flight, `put` writes them a stage later.
-    const int tid = threadIdx.x - COLT, own_v = tid % OWN, half = tid / OWN;
-    constexpr int PER = D / 64;
-    float fq[PER][NT], fk[PER][NT], fv[NT / 2], fg = 0.0f, fb = 0.0f;
+    const int tid = threadIdx.x - COLT, own_v = tid % C, first_t = tid / C;
+    constexpr int PER = D / 64, TS = 64 / C;   // tokens a pass of values
+    float fq[PER][NT], fk[PER][NT], fv[NT / TS], fg = 0.0f, fb = 0.0f;
     auto fetch = [&](int st) {
         const int t0 = (REV ? stages - 1 - st : st) * NT, nt = min(NT, a.L - t0);
         const long long row0 = (long long)b * a.L + t0;
@@ -134,10 +142,10 @@ __global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
                 fk[i][t] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
             }
         }
-        const int v = blockIdx.x * OWN + own_v;
+        const int v = blockIdx.x * C + own_v;
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i) {
-            const int t = 2 * i + half;
+        for (int i = 0; i < NT / TS; ++i) {
+            const int t = TS * i + first_t;
             const bool in = t < nt && v < a.Dv;
             fv[i] = !in   ? 0.0f
                     : REV ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + v)
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(COLT + 64) column_sweep_kernel(const Args a) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) sq[buf][t][tid + 64 * i] = a.scale * fq[i][t], sk[buf][t][tid + 64 * i] = fk[i][t];
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i) sv[buf][2 * i + half][own_v] = fv[i];
+        for (int i = 0; i < NT / TS; ++i) sv[buf][TS * i + first_t][own_v] = fv[i];
         if (tid < NT) sa[buf][tid] = expf(clamp_g(fg)), sb[buf][tid] = fb;
     };
     if (REV && !loads) inner(N);
@@ -603,15 +611,21 @@ cudaError_t step(const void *q, const void *k, const void *v, const float *g, co
                     : cudaLaunchKernelEx(&cfg, delta_step_kernel<T, 4>, q, k, v, g, beta, scale, Hk, Hv, Dk, Dv, state, o);
 }
 
-template <typename T, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
-    const dim3 grid((a.Dv + OWN - 1) / OWN, a.Hv, a.B);
+// Columns of a block of the column sweep.
+int column_width(const Args &a) { return (long long)a.B * a.Hv * ((a.Dv + 7) / 8) <= NARROW_BLOCKS ? 8 : 32; }
+
+template <typename T, int C, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
+    const dim3 grid((a.Dv + C - 1) / C, a.Hv, a.B);
     if (a.Dk <= 64)
-        column_sweep_kernel<T, 8, REV><<<grid, COLT + 64, 0, st>>>(a);
+        column_sweep_kernel<T, 8, C, REV><<<grid, 8 * C + 64, 0, st>>>(a);
     else if (a.Dk <= 128)
-        column_sweep_kernel<T, 16, REV><<<grid, COLT + 64, 0, st>>>(a);
+        column_sweep_kernel<T, 16, C, REV><<<grid, 8 * C + 64, 0, st>>>(a);
     else
-        column_sweep_kernel<T, 32, REV><<<grid, COLT + 64, 0, st>>>(a);
+        column_sweep_kernel<T, 32, C, REV><<<grid, 8 * C + 64, 0, st>>>(a);
     return cudaGetLastError();
+}
+template <typename T, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
+    return column_width(a) == 8 ? column_sweep<T, 8, REV>(a, st) : column_sweep<T, 32, REV>(a, st);
 }
 template <typename T> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
     const dim3 grid((a.Dk + OWN - 1) / OWN * chunks(a.L), a.Hv, a.B);
@@ -670,7 +684,7 @@ Sizes sizes(int B, int L, int Hv, int Dk, int Dv) {
     s.states = align256(sizeof(float) * (size_t)B * Hv * (N + 1) * Dk * Dv);
     s.images = align256(tc_image_bytes(B, L, Hv, Dk, Dv));
     s.heads = align256(sizeof(float) * rows * Dk);
-    s.inner = align256(sizeof(float) * (size_t)B * Hv * (N + 1) * 16);
+    s.inner = align256(sizeof(float) * (size_t)B * Hv * (N + 1) * 32);
     s.dots = align256(sizeof(float) * rows);
     return s;
 }
@@ -780,7 +794,7 @@ extern "C" s5_status s5_delta_backward(const void *q, long long ldq, const void 
     w += 2 * s.heads;
     a.z = w;
     w += s.states;
-    a.parts = (Dv + OWN - 1) / OWN;
+    a.parts = (Dv + column_width(a) - 1) / column_width(a);
     a.inner = reinterpret_cast<float *>(w);
     w += s.inner;
     a.dots = reinterpret_cast<float *>(w);
