@@ -249,13 +249,28 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
 }
 
 // Rows and chunks over the grid, with u_t = beta_t e_t and dv_t = beta_t X_t
-// known: forward from the chunk's kept state for dq_t and -a_t S_{t-1} dv_t,
-// then backward from its kept adjoint for Z_t u_t.
+// known: half of a block runs forward from the chunk's kept state for dq_t and
+// a_t S_{t-1} dv_t, the other half back from its kept adjoint for Z_t u_t; their
+// difference is dk_t.  Bound by the chain of a token, 64 of them per half: 2 x 500
+// tokens of 4 heads of 64 x 64 in 25 us (38 with one half after the other).
+template <int RPT> struct RowSmem {
+    static constexpr int NT = RPT > 8 ? TB / 2 : TB;
+    float e[2][NT][16 * RPT], x[2][NT][16 * RPT], d[2][NT][16 * RPT], q[2][NT][OWN], k[2][NT][OWN], a[2][NT];
+    float dk[2][CHUNK][OWN];
+};
 template <typename T, int RPT>
-__global__ void __launch_bounds__(SWT) row_sweep_kernel(const Args a) {
-    constexpr int NT = RPT > 8 ? TB / 2 : TB;
-    __shared__ float se[NT][16 * RPT], sx[NT][16 * RPT], sd[NT][16 * RPT], sq[NT][OWN], sk[NT][OWN], sa[NT], dk[CHUNK][OWN];
-    const int lane = threadIdx.x % 16, grp = threadIdx.x / 16;
+__global__ void __launch_bounds__(2 * SWT) row_sweep_kernel(const Args a) {
+    constexpr int NT = RowSmem<RPT>::NT;
+    extern __shared__ __align__(16) unsigned char raw[];
+    RowSmem<RPT> &sm = *reinterpret_cast<RowSmem<RPT> *>(raw);
+    const bool back = threadIdx.x >= SWT;
+    const int tid = threadIdx.x % SWT;
+    auto &se = sm.e[back], &sx = sm.x[back], &sd = sm.d[back];
+    auto &sq = sm.q[back], &sk = sm.k[back];
+    auto &dk = sm.dk[back];
+    auto &sa = sm.a[back];
+    auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)back), "n"(SWT) : "memory"); };
+    const int lane = tid % 16, grp = tid / 16;
     const int rows = (a.Dk + OWN - 1) / OWN, c = blockIdx.x / rows, r0 = blockIdx.x % rows * OWN;
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
     const int row = r0 + grp * 4, mine = lane / 4;
@@ -272,13 +287,13 @@ __global__ void __launch_bounds__(SWT) row_sweep_kernel(const Args a) {
     };
     auto stage = [&](int t0, int nt) {
         const long long row0 = (long long)b * a.L + t0;
-        __syncthreads();
+        meet();
         constexpr int DV = 16 * RPT, PER = NT * DV / SWT;   // a thread's values of each array, all in flight
         {
             float x[PER], y[PER], d[PER], be[PER];
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int at = threadIdx.x + i * SWT, t = at / DV, v = at % DV;
+                const int at = tid + i * SWT, t = at / DV, v = at % DV;
                 const bool in = t < nt && v < a.Dv;
                 const long long hv = (row0 + t) * a.Hv + h;
                 be[i] = in ? a.beta[hv] : 0.0f;
@@ -288,66 +303,74 @@ __global__ void __launch_bounds__(SWT) row_sweep_kernel(const Args a) {
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int at = threadIdx.x + i * SWT, t = at / DV, v = at % DV;
+                const int at = tid + i * SWT, t = at / DV, v = at % DV;
                 se[t][v] = be[i] * x[i], sx[t][v] = be[i] * y[i], sd[t][v] = a.scale * d[i];
             }
         }
 #pragma unroll
         for (int i = 0; i < NT * OWN / SWT; ++i) {
-            const int at = threadIdx.x + i * SWT, t = at / OWN, r = r0 + at % OWN;
+            const int at = tid + i * SWT, t = at / OWN, r = r0 + at % OWN;
             const bool in = t < nt && r < a.Dk;
             sq[t][at % OWN] = in ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + r) : 0.0f;
             sk[t][at % OWN] = in ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + r) : 0.0f;
         }
-        if (threadIdx.x < nt) sa[threadIdx.x] = expf(clamp_g(a.g[(row0 + threadIdx.x) * a.Hv + h]));
-        __syncthreads();
+        if (tid < nt) sa[tid] = expf(clamp_g(a.g[(row0 + tid) * a.Hv + h]));
+        meet();
     };
-    load(a.states + (bh * (N + 1) + c) * mat);
-    for (int st = 0; st < stages; ++st) {
-        const int t0 = first + st * NT, nt = min(NT, first + len - t0);
-        stage(t0, nt);
-        for (int t = 0; t < nt; ++t) {
-            const float al = sa[t];
-            float p[4] = {0, 0, 0, 0}, w[4] = {0, 0, 0, 0};
+    if (!back) {
+        load(a.states + (bh * (N + 1) + c) * mat);
+        for (int st = 0; st < stages; ++st) {
+            const int t0 = first + st * NT, nt = min(NT, first + len - t0);
+            stage(t0, nt);
+            for (int t = 0; t < nt; ++t) {
+                const float al = sa[t];
+                float p[4] = {0, 0, 0, 0}, w[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-                const float e = se[t][lane + 16 * i], x = sx[t][lane + 16 * i], d = sd[t][lane + 16 * i];
+                for (int i = 0; i < RPT; ++i) {
+                    const float e = se[t][lane + 16 * i], x = sx[t][lane + 16 * i], d = sd[t][lane + 16 * i];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    S[i][r] *= al;
-                    p[r] = fmaf(S[i][r], x, p[r]);
-                    S[i][r] = fmaf(sk[t][grp * 4 + r], e, S[i][r]);
-                    w[r] = fmaf(S[i][r], d, w[r]);
+                    for (int r = 0; r < 4; ++r) {
+                        S[i][r] *= al;
+                        p[r] = fmaf(S[i][r], x, p[r]);
+                        S[i][r] = fmaf(sk[t][grp * 4 + r], e, S[i][r]);
+                        w[r] = fmaf(S[i][r], d, w[r]);
+                    }
+                }
+                const float v = sum4_16(p, lane), dq = sum4_16(w, lane);
+                if (lane % 4 == 0) {
+                    dk[t0 - first + t][grp * 4 + mine] = v;
+                    if (on) a.dqh[(((long long)b * a.L + t0 + t) * a.Hv + h) * a.Dk + row + mine] = dq;
                 }
             }
-            const float v = sum4_16(p, lane), dq = sum4_16(w, lane);
-            if (lane % 4 == 0) {
-                dk[t0 - first + t][grp * 4 + mine] = v;
-                if (on) a.dqh[(((long long)b * a.L + t0 + t) * a.Hv + h) * a.Dk + row + mine] = dq;
+        }
+    } else {
+        load(static_cast<const float *>(a.z) + (bh * N + c) * mat);
+        for (int st = stages - 1; st >= 0; --st) {
+            const int t0 = first + st * NT, nt = min(NT, first + len - t0);
+            stage(t0, nt);
+            for (int t = nt - 1; t >= 0; --t) {
+                const float al = sa[t];
+                float p[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                    const float e = se[t][lane + 16 * i], x = sx[t][lane + 16 * i], d = sd[t][lane + 16 * i];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        S[i][r] = fmaf(sq[t][grp * 4 + r], d, S[i][r]);
+                        p[r] = fmaf(S[i][r], e, p[r]);
+                        S[i][r] = al * fmaf(-sk[t][grp * 4 + r], x, S[i][r]);
+                    }
+                }
+                const float v = sum4_16(p, lane);
+                if (lane % 4 == 0) dk[t0 - first + t][grp * 4 + mine] = v;
             }
         }
     }
-    load(static_cast<const float *>(a.z) + (bh * N + c) * mat);
-    for (int st = stages - 1; st >= 0; --st) {
-        const int t0 = first + st * NT, nt = min(NT, first + len - t0);
-        stage(t0, nt);
-        for (int t = nt - 1; t >= 0; --t) {
-            const float al = sa[t];
-            float p[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-                const float e = se[t][lane + 16 * i], x = sx[t][lane + 16 * i], d = sd[t][lane + 16 * i];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    S[i][r] = fmaf(sq[t][grp * 4 + r], d, S[i][r]);
-                    p[r] = fmaf(S[i][r], e, p[r]);
-                    S[i][r] = al * fmaf(-sk[t][grp * 4 + r], x, S[i][r]);
-                }
-            }
-            const float v = sum4_16(p, lane);
-            if (on && lane % 4 == 0)
-                a.dkh[(((long long)b * a.L + t0 + t) * a.Hv + h) * a.Dk + row + mine] = v - dk[t0 - first + t][grp * 4 + mine];
-        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < len * OWN; i += 2 * SWT) {
+        const int t = i / OWN, r = i % OWN;
+        if (r0 + r < a.Dk)
+            a.dkh[(((long long)b * a.L + first + t) * a.Hv + h) * a.Dk + r0 + r] = sm.dk[1][t][r] - sm.dk[0][t][r];
     }
 }
 
@@ -627,15 +650,16 @@ template <typename T, int C, bool REV> cudaError_t column_sweep(const Args &a, c
 template <typename T, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
     return column_width(a) == 8 ? column_sweep<T, 8, REV>(a, st) : column_sweep<T, 32, REV>(a, st);
 }
-template <typename T> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
+template <typename T, int RPT> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
     const dim3 grid((a.Dk + OWN - 1) / OWN * chunks(a.L), a.Hv, a.B);
-    if (a.Dv <= 64)
-        row_sweep_kernel<T, 4><<<grid, SWT, 0, st>>>(a);
-    else if (a.Dv <= 128)
-        row_sweep_kernel<T, 8><<<grid, SWT, 0, st>>>(a);
-    else
-        row_sweep_kernel<T, 16><<<grid, SWT, 0, st>>>(a);
+    constexpr int bytes = sizeof(RowSmem<RPT>);
+    const cudaError_t e = cudaFuncSetAttribute(row_sweep_kernel<T, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    row_sweep_kernel<T, RPT><<<grid, 2 * SWT, bytes, st>>>(a);
     return cudaGetLastError();
+}
+template <typename T> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
+    return a.Dv <= 64 ? row_sweep<T, 4>(a, st) : a.Dv <= 128 ? row_sweep<T, 8>(a, st) : row_sweep<T, 16>(a, st);
 }
 
 template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
