@@ -39,7 +39,8 @@ struct Args {
     int parts;
     void *z;                          // dL/dS at the end of chunk c: [B][Hv][N][Dk][Dv] float32, or, for the tensor
                                       // cores, [B][Hv][N][Dv / 64][2][Dk][64] bf16 (two parts)
-    void *images;                     // operand images of the tensor-core path
+    void *images;                     // operand images of the tensor-core path; then a state between launches
+    int from, count;                  // tensor cores: the chunks of this launch
 };
 
 __host__ __device__ inline int chunks(int L) { return (L + CHUNK - 1) / CHUNK; }

@@ -637,7 +637,9 @@ template <int DK> cudaError_t backward(const Args &a, cudaStream_t st) {
     if (e == cudaSuccess) e = encode_rows(&m.g, false, a.dout, a.lddo, a.B, a.L, a.Hv, a.Dv);
     if (e == cudaSuccess) e = encode_rows(&m.x, true, a.x, (long long)a.Hv * a.Dv, a.B, a.L, a.Hv, a.Dv);
     if (e == cudaSuccess) e = encode_states(&m.s, a.states, (long long)a.B * a.Hv * (chunks(a.L) + 1), DK, a.Dv);
-    if (e == cudaSuccess) e = tc_prepare(a, true, st);
+    Args all = a;
+    all.count = chunks(a.L);
+    if (e == cudaSuccess) e = tc_prepare(all, true, st);
     if (e == cudaSuccess) e = big_smem(delta_adjoint_kernel<DK>, AdjSmem<DK>::total);
     if (e != cudaSuccess) return e;
     delta_adjoint_kernel<DK><<<dim3(a.Dv / NV, a.Hv, a.B), ADJ_THREADS, AdjSmem<DK>::total, st>>>(m, a);

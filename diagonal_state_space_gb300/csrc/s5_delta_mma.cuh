@@ -11,7 +11,9 @@
 namespace s5 {
 namespace delta {
 
-cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st);   // s5_delta_prep.cu
+// s5_delta_prep.cu.  beside: runs while the kernel before it on the stream does,
+// which it must not depend on, and ends after it.
+cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st, bool beside = false);
 int prep_fault_take();
 int scan_fault_take();                                                     // s5_delta_scan.cu
 int adjoint_fault_take();                                                  // s5_delta_adjoint.cu

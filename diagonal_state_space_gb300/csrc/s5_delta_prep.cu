@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
     PrepBars *pb = reinterpret_cast<PrepBars *>(smem + L::bars);
     const uint32_t img = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, group = a.Hv / a.Hk;
+    const int c = a.from + blockIdx.x, hk = blockIdx.y, b = blockIdx.z, group = a.Hv / a.Hk;
     const int t0 = c * C, nt = min(C, a.L - t0), N = chunks(a.L);
     const long long row0 = (long long)b * a.L + t0;
     const int q = warp & 3, c0 = warp / 4 * 32;   // the warp's fragment: tokens 16 q on, columns c0 on
@@ -347,24 +347,34 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 128);
+    // beside the scan of earlier chunks: this grid ends after that one
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) griddep_wait();
 }
 
-template <int DK, bool TRANS> cudaError_t launch(const Args &a, cudaStream_t st) {
+template <int DK, bool TRANS> cudaError_t launch(const Args &a, cudaStream_t st, bool beside) {
     PrepMaps m = {};
     cudaError_t e = encode_rows(&m.k16, false, a.k, a.ldk, a.B, a.L, a.Hk, DK, 16);
     if (e == cudaSuccess) e = encode_rows(&m.q16, false, a.q, a.ldq, a.B, a.L, a.Hk, DK, 16);
     if (e == cudaSuccess) e = encode_rows(&m.k64, false, a.k, a.ldk, a.B, a.L, a.Hk, DK);
     if (e == cudaSuccess) e = big_smem(delta_prep_kernel<DK, TRANS>, PrepSmem<DK>::total);
     if (e != cudaSuccess) return e;
-    delta_prep_kernel<DK, TRANS><<<dim3(chunks(a.L), a.Hk, a.B), PT, PrepSmem<DK>::total, st>>>(m, a);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    set_programmatic(attr);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.count, a.Hk, a.B);
+    cfg.blockDim = dim3(PT);
+    cfg.dynamicSmemBytes = PrepSmem<DK>::total;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = beside;
+    return cudaLaunchKernelEx(&cfg, delta_prep_kernel<DK, TRANS>, m, a);
 }
 
 }  // namespace
 
-cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st) {
-    if (a.Dk == 128) return transposed ? launch<128, true>(a, st) : launch<128, false>(a, st);
-    return transposed ? launch<64, true>(a, st) : launch<64, false>(a, st);
+cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st, bool beside) {
+    if (a.Dk == 128) return transposed ? launch<128, true>(a, st, beside) : launch<128, false>(a, st, beside);
+    return transposed ? launch<64, true>(a, st, beside) : launch<64, false>(a, st, beside);
 }
 
 int prep_fault_take() { return fault_take(); }

@@ -84,14 +84,18 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
     constexpr uint32_t L_PART = NARROW ? 1 : 2;   // the image of the third parts
     constexpr int P1 = SL == 1 ? 3 : 2;     // column blocks of D1 and D3: TMEM has 256 columns for each of two slices
     constexpr int PW = NC / 2, F = NC / 4;  // a warp's columns, and a thread's values of a fragment
+    // narrow slices leave columns to the preparation of later chunks (P1, 2, P1 blocks of 32)
+    constexpr int TMEM = NARROW ? 256 : 512;
     constexpr int W = SL == 1 ? PW : 16;    // columns converted at a time: registers for each of 16 warps
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     ScanBars *sb = reinterpret_cast<ScanBars *>(smem + L::bars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int n0 = blockIdx.x * SL * NC, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
-    const int N = chunks(a.L);
+    // this launch's chunks: N of them, from `from` on
+    const int N = a.count, from = a.from, all = chunks(a.L);
     const long long bh = (long long)b * a.Hv + h;
+    if (threadIdx.x == 0) griddep_launch_dependents();   // the rest's preparation needs nothing from here
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sb->kq_full[i], 1), mbar_init(&sb->kq_empty[i], 1);
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
     }
     constexpr int MMA_WARP = 8 * SL, COPY_WARP = MMA_WARP + 1;
     if (warp == MMA_WARP) {
-        tmem_alloc(&sb->tmem, 512);
+        tmem_alloc(&sb->tmem, TMEM);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -123,17 +127,17 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
         if (warp == COPY_WARP && lane == 0) {
             // ------------------------------------------------------ copies
             auto load_kq = [&](int c) {
-                load_chunk_rows<DK>(smem + L::kq + (c & 1) * L::KQ, &maps.k, &maps.q, hk, c * C, b, &sb->kq_full[c & 1]);
+                load_chunk_rows<DK>(smem + L::kq + (c & 1) * L::KQ, &maps.k, &maps.q, hk, (from + c) * C, b, &sb->kq_full[c & 1]);
             };
             auto load_img = [&](int c) {
-                const unsigned char *from = static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES;
+                const unsigned char *image = static_cast<const unsigned char *>(a.images) + (bh * all + from + c) * IMG_BYTES;
                 mbar_arrive_tx(&sb->img_full, IMG_BYTES);
-                bulk_load(smem + L::mat, from, MAT_BYTES, &sb->img_full);
-                bulk_load(smem + L::meta, from + MAT_BYTES, META_BYTES, &sb->img_full);
+                bulk_load(smem + L::mat, image, MAT_BYTES, &sb->img_full);
+                bulk_load(smem + L::meta, image + MAT_BYTES, META_BYTES, &sb->img_full);
             };
             auto load_v = [&](int c, int s) {
                 mbar_arrive_tx(&sb->v_full[s], L::VO);
-                tma_load_4d(smem + L::vo + s * L::VO, &maps.v, n0 + s * NC, h, c * C, b, &sb->v_full[s]);
+                tma_load_4d(smem + L::vo + s * L::VO, &maps.v, n0 + s * NC, h, (from + c) * C, b, &sb->v_full[s]);
             };
             load_kq(0);
             load_img(0);
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
                 }
                 for (int s = 0; ok && s < SL; ++s) {
                     if (!(ok = wait(&sb->o_ready[s], c & 1))) break;
-                    tma_store_4d(&maps.o, smem + L::vo + s * L::VO, n0 + s * NC, h, c * C, b);
+                    tma_store_4d(&maps.o, smem + L::vo + s * L::VO, n0 + s * NC, h, (from + c) * C, b);
                     bulk_commit();
                     if (c + 1 < N) {
                         bulk_wait_read_all();
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
+    if (warp == MMA_WARP) tmem_dealloc(tmem, TMEM);
 }
 
 template <int DK, int SL, bool KEEP, int NC> cudaError_t launch(const ScanMaps &m, const Args &a, cudaStream_t st) {
@@ -375,6 +379,7 @@ template <int DK, int SL, bool KEEP, int NC> cudaError_t launch(const ScanMaps &
     return cudaGetLastError();
 }
 
+constexpr int SPLIT_CHUNKS = 16, SPLIT = 4;
 template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
     ScanMaps m = {};
     // slices of 32 columns where one CTA each still fits the SMs at once
@@ -390,13 +395,26 @@ template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
         if (e == cudaSuccess) e = encode_rows(&m.o32, true, a.o32, ld, a.B, a.L, a.Hv, a.Dv);
         if (e == cudaSuccess) e = encode_states(&m.s, a.states, (long long)a.B * a.Hv * (chunks(a.L) + 1), DK, a.Dv);
     }
-    if (e == cudaSuccess) e = tc_prepare(a, false, st);
+    Args all = a;
+    all.count = chunks(a.L);
+    if (narrow && all.count >= SPLIT_CHUNKS) {
+        Args first = all, rest = all;
+        first.count = rest.from = all.count / SPLIT;
+        rest.count -= first.count;
+        float *carry = reinterpret_cast<float *>(static_cast<char *>(a.images) + heads * all.count * IMG_BYTES);
+        first.s_last = carry, rest.s0 = carry;
+        if (e == cudaSuccess) e = tc_prepare(first, false, st);
+        if (e == cudaSuccess) e = launch<DK, 1, false, 32>(m, first, st);
+        if (e == cudaSuccess) e = tc_prepare(rest, false, st, true);
+        return e == cudaSuccess ? launch<DK, 1, false, 32>(m, rest, st) : e;
+    }
+    if (e == cudaSuccess) e = tc_prepare(all, false, st);
     if (e != cudaSuccess) return e;
-    if (a.states) return launch<DK, 1, true, 64>(m, a, st);
-    if (narrow) return launch<DK, 1, false, 32>(m, a, st);
+    if (a.states) return launch<DK, 1, true, 64>(m, all, st);
+    if (narrow) return launch<DK, 1, false, 32>(m, all, st);
     // two slices a CTA where one a CTA would not fit the SMs at once
-    if (a.Dv == 128 && heads * 2 > 152) return launch<DK, 2, false, 64>(m, a, st);
-    return launch<DK, 1, false, 64>(m, a, st);
+    if (a.Dv == 128 && heads * 2 > 152) return launch<DK, 2, false, 64>(m, all, st);
+    return launch<DK, 1, false, 64>(m, all, st);
 }
 
 }  // namespace
@@ -412,7 +430,7 @@ bool tc_supported(const Args &a, s5_dtype dtype, bool backward) {
 
 size_t tc_image_bytes(int B, int L, int Hv, int Dk, int Dv) {
     if ((Dk != 64 && Dk != 128) || (Dv != 64 && Dv != 128)) return 0;
-    return (size_t)B * Hv * chunks(L) * IMG_BYTES;
+    return (size_t)B * Hv * (chunks(L) * (size_t)IMG_BYTES + sizeof(float) * Dk * Dv);   // and a state
 }
 
 cudaError_t tc_forward(const Args &a, cudaStream_t st) {

@@ -305,6 +305,28 @@ def test_other_stream_and_graph(dt):
         assert torch.equal(gg[n], wg[n]), n
 
 
+@pytest.mark.parametrize("shape", [(1, 1024, 1, 2, 128, 128), (2, 1100, 2, 4, 64, 128), (3, 1030, 4, 8, 128, 64)])
+def test_long_sequences_with_a_state(shape):
+    """The preparation of later chunks runs beside the scan of earlier ones: same results in a row, on one workspace
+    and in a captured graph."""
+    d, v = make(*shape, dt=torch.bfloat16, seed=shape[1])
+    wo, ws = expect(v)
+    B, L, _, Hv, Dk, Dv = *shape[:3], *shape[3:]
+    work = torch.empty(api.s5_delta_workspace_size(B, L, Hv, Dk, Dv), dtype=torch.uint8, device="cuda")
+    runs = [forward(d, workspace=work) for _ in range(3)]
+    close(runs[0][0], wo, FWD + BF16, "o")
+    close(runs[0][1], ws, FWD, "s_last")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        runs += [forward(d, workspace=work) for _ in range(2)]
+    for o, s in runs[3:]:
+        o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for o, s in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(s, runs[0][1])
+
+
 def test_nan_stays_in_its_sequence_and_head():
     d, v = make(2, 100, 1, 2, 128, 128, dt=torch.bfloat16, seed=71)
     clean = forward(d)
