@@ -379,7 +379,14 @@ template <int DK, int SL, bool KEEP, int NC> cudaError_t launch(const ScanMaps &
     return cudaGetLastError();
 }
 
-constexpr int SPLIT_CHUNKS = 16, SPLIT = 4;
+// Where the scan leaves half of the SMs free, the first quarter of the chunks is
+// prepared and scanned, and the rest prepared beside that scan, from this many
+// chunks of all heads on (below, two more launches cost more).  One piece / two,
+// heads of 128, us: 16 heads, 32 chunks 91 / 96, 64 chunks 177 / 165, 256 chunks
+// 646 / 605; 8 heads, 256 chunks 595 / 575; 32 heads (128 of 152 SMs scan), 64
+// chunks 206 / 211.  A half or a sixth first: 620, 608 at 16 heads, 256 chunks.
+constexpr int SPLIT_CHUNKS = 1024, SPLIT = 4;
+
 template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
     ScanMaps m = {};
     // slices of 32 columns where one CTA each still fits the SMs at once
@@ -397,7 +404,7 @@ template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
     }
     Args all = a;
     all.count = chunks(a.L);
-    if (narrow && all.count >= SPLIT_CHUNKS) {
+    if (narrow && heads * (a.Dv / 32) <= 76 && heads * all.count >= SPLIT_CHUNKS) {
         Args first = all, rest = all;
         first.count = rest.from = all.count / SPLIT;
         rest.count -= first.count;
