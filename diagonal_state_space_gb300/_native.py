@@ -1,4 +1,4 @@
-"""ctypes loader of libs5.so.  Loading fails loudly: there is no fallback."""
+"""Loader of libs5.so (ctypes) and of the binding's native half.  Loading fails loudly: there is no fallback."""
 from __future__ import annotations
 
 import ctypes
@@ -92,6 +92,23 @@ def lib() -> ctypes.CDLL:
                 f.argtypes = args
             _lib = h
     return _lib
+
+
+_marshal = None
+
+
+def marshal():
+    """The native half of the binding (csrc/marshal.cpp), built and loaded beside libs5.so."""
+    global _marshal
+    if _marshal is None:
+        lib()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError("the binding's native half is not built (%s); run __graft_entry__.build() or "
+                               "python diagonal_state_space_gb300/build.py" % e) from e
+        _marshal = m
+    return _marshal
 
 
 def check(fn: str, code: int) -> None:

@@ -1,6 +1,6 @@
 """Thin torch binding of libs5.so: the same entry points as include/s5.h.
 
-Argument marshalling only.  Every tensor must already be on the GPU with the
+Argument marshalling only (for some calls natively, csrc/marshal.cpp).  Every tensor must already be on the GPU with the
 documented dtype, contiguous (where a call does not take a pitch between
 tokens) and 16-byte aligned; nothing is converted or copied here, and every numeric step runs in the library's kernels.  Complex
 arrays are torch.complex64 tensors (interleaved re/im float32, as the C ABI
@@ -228,7 +228,16 @@ def s5_sync_status(workspace, stream=None) -> int:
 # Gated delta rule, position rotation, norms of queries and keys.  Here q, k,
 # v, o and their gradients may be views with a pitch between tokens (slices of
 # a fused projection); a head's values and a token's heads are contiguous.
+# Contiguous arrays on the current stream are marshalled natively
+# (csrc/marshal.cpp); what that returns None for is taken apart here.
 # ---------------------------------------------------------------------------
+def _taken(fn, out):
+    """Whether the native call did the work; raises its error."""
+    if out.__class__ is int:
+        check(fn, out)
+    return out is not None
+
+
 def _arr(t, name, dtype, shape):
     """_ptr of a contiguous array that has to be there: one expression where all is well."""
     if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
@@ -323,6 +332,10 @@ def s5_delta_forward(q, k, v, g, beta, scale=None, s0=None, s_last=None, o=None,
     from the state s0 [B,Hv,Dk,Dv] float32 (None: zero).  scale defaults to Dk^-0.5.  Returns o, or
     (o, s_last) when s_last is a tensor (it may be s0) or True; with `saved` (new_delta_saved) also what
     s5_delta_backward needs."""
+    if stream is None:
+        out = _native.marshal().delta_forward(q, k, v, g, beta, scale, s0, s_last, o, saved, workspace)
+        if _taken("s5_delta_forward", out):
+            return out
     B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
     f32, dev, dt = torch.float32, q.device, q.dtype
     if o is None:
@@ -346,6 +359,10 @@ def s5_delta_forward(q, k, v, g, beta, scale=None, s0=None, s_last=None, o=None,
 def s5_delta_backward(q, k, v, g, beta, do, saved, scale=None, s0=None, ds_last=None, workspace=None, stream=None):
     """Gradients of sum(do * o) + sum(ds_last * s_last) after s5_delta_forward with the same inputs and `saved`.
     Returns a dict: dq, dk, dv of q's type, dg, dbeta float32, ds0 float32 (None without s0)."""
+    if stream is None:
+        out = _native.marshal().delta_backward(q, k, v, g, beta, do, saved, scale, s0, ds_last, workspace)
+        if _taken("s5_delta_backward", out):
+            return out
     B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
     f32, dev, dt = torch.float32, q.device, q.dtype
     e = lambda shape, t: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
@@ -369,6 +386,10 @@ def s5_delta_backward(q, k, v, g, beta, do, saved, scale=None, s0=None, ds_last=
 def s5_delta_step(q, k, v, g, beta, state, scale=None, o=None, stream=None):
     """One token per sequence: q, k [B,Hk,Dk], v [B,Hv,Dv], g, beta [B,Hv] float32; state [B,Hv,Dk,Dv] float32 is
     updated in place.  Returns o [B,Hv,Dv]."""
+    if stream is None:
+        out = _native.marshal().delta_step(q, k, v, g, beta, state, scale, o)
+        if _taken("s5_delta_step", out):
+            return out
     B, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 1)
     f32, dt = torch.float32, q.dtype
     if o is None:
@@ -400,6 +421,10 @@ def s5_rotary(x, positions, freq, layout="half", amplitude=1.0, inverse=False, o
     """Rotates the first 2 * len(freq) values of each head of x [..., H, D] by the angles positions [...] (int64) *
     freq (float64, init.rotary_frequencies) and scales them by amplitude; inverse: the transpose (its backward
     pass).  out may be x."""
+    if stream is None:
+        done = _native.marshal().rotary(x, positions, freq, _LAYOUT[layout], amplitude, int(inverse), out)
+        if _taken("s5_rotary", done):
+            return done
     T, pos, fr, rot = _rot_args(x, "x", positions, freq)
     H, D = x.shape[-2:]
     if out is None:
@@ -414,6 +439,11 @@ def s5_qk_norm_rotary(q, k, positions, freq, norm="rms", eps=1e-6, q_weight=None
                       amplitude=1.0, q_out=None, k_out=None, stream=None):
     """Norm of each head ("rms", "l2" or None), its weight [D] float32 (None: ones) and the rotation of s5_rotary, of
     q [..., Hq, D] and k [..., Hk, D] in one launch.  freq None: no rotation.  q_out may be q, k_out may be k."""
+    if stream is None:
+        out = _native.marshal().qk_norm_rotary(q, k, positions, freq, _NORM[norm], eps, q_weight, k_weight, _LAYOUT[layout],
+                                               amplitude, q_out, k_out)
+        if _taken("s5_qk_norm_rotary", out):
+            return out
     T, pos, fr, rot = _rot_args(q, "q", positions, freq)
     (Hq, D), Hk, dt, f32 = q.shape[-2:], k.shape[-2], q.dtype, torch.float32
     kshape = torch.Size((*q.shape[:-2], Hk, D))
@@ -435,6 +465,11 @@ def s5_qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, norm="rms"
                                k_weight=None, layout="half", amplitude=1.0, workspace=None, stream=None):
     """Gradients of s5_qk_norm_rotary from those of its outputs.  Returns a dict: dq, dk, and dwq, dwk [D] float32
     (None without the weight)."""
+    if stream is None:
+        out = _native.marshal().qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, _NORM[norm], eps, q_weight,
+                                                        k_weight, _LAYOUT[layout], amplitude, workspace)
+        if _taken("s5_qk_norm_rotary_backward", out):
+            return out
     T, pos, fr, rot = _rot_args(q, "q", positions, freq)
     (Hq, D), Hk, dt, f32, dev = q.shape[-2:], k.shape[-2], q.dtype, torch.float32, q.device
     kshape = (*q.shape[:-2], Hk, D)

@@ -1,7 +1,8 @@
-"""Builds libs5.so in-tree with nvcc for sm_103a (one -gencode, no cmake).
+"""Builds libs5.so in-tree with nvcc for sm_103a (one -gencode, no cmake), and
+the binding's native half with g++ against the installed torch.
 
 Translation units compile in parallel into ``_build/`` at the repository root
-and link into ``diagonal_state_space_gb300/libs5.so``.
+and link into ``diagonal_state_space_gb300/libs5.so`` and ``_marshal.so``.
 """
 from __future__ import annotations
 
@@ -10,12 +11,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libs5.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -45,6 +48,33 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _run(cmd, what):
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("%s failed:\n%s%s" % (what, res.stdout, res.stderr))
+
+
+def _marshal_object(force: bool) -> str:
+    """csrc/marshal.cpp for the torch that is installed (its version is part of the object's name)."""
+    import torch
+    src = os.path.join(CSRC, "marshal.cpp")
+    obj = os.path.join(OBJ, "marshal-%s.o" % torch.__version__)
+    if force or _stale(obj, [src, os.path.join(ROOT, "include", "s5.h")]):
+        cuda = os.path.dirname(os.path.dirname(_nvcc()))
+        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include"),
+              "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(torch.__file__), "include"),
+              "-I", os.path.join(cuda, "include"), "-c", src, "-o", obj], "g++ for %s" % src)
+    return obj
+
+
+def _link_marshal(obj: str) -> None:
+    import torch
+    tmp = MARSHAL + ".tmp%d" % os.getpid()
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", PKG, "-ls5", "-Wl,-rpath,$ORIGIN"], "link of _marshal.so")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(OBJ, exist_ok=True)
@@ -67,7 +97,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        marshal = ex.submit(_marshal_object, force)
         list(ex.map(compile_one, zip(srcs, objs)))
+        marshal = marshal.result()
     if force or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-cudart", "static",
@@ -76,6 +108,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError("link failed:\n%s%s" % (res.stdout, res.stderr))
         os.replace(tmp, LIB)
+    if force or _stale(MARSHAL, [marshal]):
+        _link_marshal(marshal)
     return LIB
 
 

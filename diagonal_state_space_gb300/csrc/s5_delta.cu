@@ -697,7 +697,7 @@ s5_status check_sizes(long long B, long long L, long long Hk, long long Hv, long
 
 // Regions of the two buffers.  The backward workspace holds what either path
 // needs: dq and dk per value head, the chunks' Z (as many bytes in either form,
-// one less than the states), parts of <S, Z> (16 at most), the tokens' sums.
+// one less than the states), parts of <S, Z> (32 at most), the tokens' sums.
 struct Sizes {
     size_t e, states, images, heads, inner, dots;
 };

@@ -278,8 +278,8 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
 
 // ---------------------------------------------------------------------------
 // What is local to a chunk: persistent CTAs over chunks and key heads, each
-// over its value heads, the next head's tiles on their way to L2.  Per token dv = beta X, dbeta = X . e and
-// o . dO - v . dv (for the decays, s5_delta.cu).  With S0 and Z the state at
+// over its value heads, the next head's tiles on their way to L2.  Per token
+// dv = beta X, dbeta = X . e and o . dO - v . dv (for the decays, s5_delta.cu).  With S0 and Z the state at
 // the chunk's start and the adjoint at its end, U = beta e, and
 // N_ij = scale D_ij dO_i.U_j (j <= i), W_ij = -D_ij dv_i.U_j (j < i):
 //   dq = scale e^G dO S0^T + N K

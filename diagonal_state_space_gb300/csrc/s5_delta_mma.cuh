@@ -343,8 +343,8 @@ __device__ __forceinline__ void hand_over(uint64_t *bar, int lane) {
 
 // ---------------------------------------------------------------------------
 // Tensor maps.  Rows [B][L][H][D] with a pitch between tokens, in boxes of 64
-// (or fewer) tokens x 128 (or 64) bytes of one head; tokens past L read as zeros and are not
-// written.
+// (or fewer) tokens x 128 (or 64) bytes of one head; tokens past L read as
+// zeros and are not written.
 // ---------------------------------------------------------------------------
 inline cudaError_t encode(CUtensorMap *m, bool f32, int rank, const void *p, const cuuint64_t *dims, const cuuint64_t *strides,
                           const cuuint32_t *box) {

@@ -368,12 +368,13 @@ s5_status s5_ssm_backward(const float *lambda, const float *log_dt, const float 
  * own pitch in elements between two tokens (ld >= heads * head size; a batch
  * is L pitches), so that slices of a fused projection need no copy.  g, beta
  * [B][L][Hv], states [B][Hv][Dk][Dv] float32 contiguous.  Bases 16-byte
- * aligned (g, beta: 4-byte, so that one token's slice can be passed).  Dk and Dv: multiples of 4 up to 256 (S5_ERR_UNSUPPORTED
- * otherwise); Hv a multiple of Hk; B L Hv <= 2^30.  L = 0 leaves the state as
- * it is; B = 0 is a no-op.  Inputs must be finite but for g.
+ * aligned (g, beta: 4-byte, so that one token's slice can be passed).  Dk and
+ * Dv: multiples of 4 up to 256 (S5_ERR_UNSUPPORTED otherwise); Hv a multiple
+ * of Hk; B L Hv <= 2^30.  L = 0 leaves the state as it is; B = 0 is a no-op.
+ * Inputs must be finite but for g.
  *
  * Arithmetic: states, sums and decays in 32 bits.  On the tensor cores (bf16
- * q, k, v with heads of 128, pitches that are multiples of 8) an operand that
+ * q, k, v with heads of 64 or 128, pitches that are multiples of 8) an operand that
  * is not itself bf16 is carried as a sum of three bf16 values.
  * ======================================================================== */
 

@@ -11,7 +11,7 @@ import numpy as np
 import pytest
 import torch
 
-from diagonal_state_space_gb300 import api
+from diagonal_state_space_gb300 import _native, api
 
 import _mixer_ref as ref
 from _parity import check
@@ -335,3 +335,44 @@ def test_nan_stays_in_its_sequence_and_head():
     o, s = forward(d)
     assert torch.equal(o[0, :, 1], clean[0][0, :, 1]) and torch.equal(o[1, :, 0], clean[0][1, :, 0])
     assert torch.isnan(s[1, 1, :, 5]).any() and torch.isnan(s[0, 0]).all()
+
+
+def test_no_wait_ran_out():
+    d, _ = make(2, 300, 2, 4, 128, 128, dt=torch.bfloat16, seed=81)
+    forward(d)
+    grads(d)
+    assert _native.lib().s5_delta_fault() == 0
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_native_and_python_marshalling_agree(dt):
+    d, _ = make(2, 70, 1, 2, 64, 64, dt=dt, seed=91)
+    here = torch.cuda.current_stream()
+    a, b = forward(d), forward(d, stream=here)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    saved = api.new_delta_saved(d["q"], d["v"])
+    forward(d, saved=saved)
+    x = [d[n] for n in ("q", "k", "v", "g", "beta", "do")]
+    for kw in ({}, dict(s0=d["s0"], ds_last=d["ds_last"])):
+        a, b = api.s5_delta_backward(*x, saved, **kw), api.s5_delta_backward(*x, saved, stream=here, **kw)
+        assert list(a) == list(b)
+        for n in a:
+            assert a[n] is b[n] is None or (a[n].dtype is b[n].dtype and torch.equal(a[n], b[n])), n
+    tok = [d[n][:, 0].contiguous() for n in ("q", "k", "v", "g", "beta")]
+    s1, s2 = d["s0"].clone(), d["s0"].clone()
+    assert torch.equal(api.s5_delta_step(*tok, s1), api.s5_delta_step(*tok, s2, stream=here)) and torch.equal(s1, s2)
+
+
+def test_native_marshalling_refuses_as_python_does():
+    d, _ = make(1, 5, 1, 2, 64, 64, seed=92)
+    x = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    with pytest.raises(ValueError, match="g must have shape"):
+        api.s5_delta_forward(*x[:3], x[3][:, :3].contiguous(), x[4])
+    with pytest.raises(ValueError, match="beta must be"):
+        api.s5_delta_forward(*x[:4], x[4].double())
+    with pytest.raises(api.S5Error):                    # a saved buffer that is too small
+        api.s5_delta_forward(*x, saved=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(api.S5Error):
+        api.s5_delta_forward(*x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        api.s5_delta_step(*x, d["s0"])

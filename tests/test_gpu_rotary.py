@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from diagonal_state_space_gb300 import api, init
+from diagonal_state_space_gb300 import _native, api, init
 
 import _mixer_ref as ref
 from _parity import check
@@ -221,3 +221,10 @@ def test_refuses_wrong_arguments():
         api.s5_qk_norm_rotary(x, x[:1], pos, fr)
     with pytest.raises(KeyError):
         api.s5_rotary(x, pos, fr, layout="other")
+
+
+def test_no_copy_ran_out():
+    x = torch.randn(4, 4096, 16, 128, device="cuda", dtype=torch.bfloat16)
+    pos = torch.arange(4096, device="cuda").expand(4, 4096).contiguous()
+    api.s5_rotary(x, pos, torch.ones(64, dtype=torch.float64, device="cuda"))
+    assert _native.lib().s5_rotary_fault() == 0

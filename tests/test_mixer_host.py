@@ -192,3 +192,16 @@ def test_reference_norm_and_rotation_gradients_match_central_differences(kind, l
         d = np.zeros(8)
         d[i] = 1e-6
         assert abs((loss(x, w + d) - loss(x, w - d)) / 2e-6 - dw[i]) < 1e-7
+
+
+def test_native_half_leaves_the_rest_to_python(lib):
+    m = _native.marshal()
+    q, v, g = torch.zeros(2, 1, 8), torch.zeros(2, 2, 8), torch.zeros(2, 2)
+    state = torch.zeros(2, 2, 8, 8)
+    assert m.delta_step(q, q, v, g, g, state, None, None) is None           # not on a GPU
+    assert m.delta_step(None, q, v, g, g, state, None, None) is None
+    assert m.rotary(q, None, None, 0, 1.0, 0, None) is None
+    assert m.qk_norm_rotary(q, q, None, None, 1, 1e-6, None, None, 0, 1.0, None, None) is None
+    for fn in (m.delta_step, m.delta_forward, m.delta_backward, m.rotary, m.qk_norm_rotary, m.qk_norm_rotary_backward):
+        with pytest.raises(TypeError, match="arguments"):
+            fn(q)
