@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
     const bool on = !loads && col < a.Dv, first = on && lane == 0;
     const int N = chunks(a.L);
     const long long bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
+    griddep_wait();
     const float *init = REV ? a.ds_last : a.s0;
     float S[RPT];
 #pragma unroll
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(2 * SWT) row_sweep_kernel(const Args a) {
     const bool on = row < a.Dk;
     const int N = chunks(a.L), first = c * CHUNK, len = min(CHUNK, a.L - first), stages = (len + NT - 1) / NT;
     const long long bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
+    griddep_wait();
     float S[RPT][4];
     auto load = [&](const float *from) {
 #pragma unroll
@@ -382,6 +384,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // One warp per token and value head: dv = beta X, dbeta = X . e, o . do - v . dv.
 template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(const Args a) {
+    griddep_wait();
     const long long hv = (long long)blockIdx.x * 8 + threadIdx.x / 32, rows = (long long)a.B * a.L * a.Hv;
     const int lane = threadIdx.x % 32;
     if (hv >= rows) return;
@@ -404,6 +407,7 @@ template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(
 // One warp per chunk and value head: dg by adding the chunk's terms from its
 // end on top of <S, Z> there.  A token whose decay is zero has no gradient.
 __global__ void __launch_bounds__(256) decay_grads_kernel(const Args a) {
+    griddep_wait();
     const int N = chunks(a.L), lane = threadIdx.x % 32;
     const long long id = (long long)blockIdx.x * 8 + threadIdx.x / 32;
     if (id >= (long long)a.B * a.Hv * N) return;
@@ -430,6 +434,7 @@ __global__ void __launch_bounds__(256) decay_grads_kernel(const Args a) {
 
 // dq and dk of a key head: the sum over its value heads, rounded once.
 template <typename T> __global__ void __launch_bounds__(256) group_sum_kernel(const Args a) {
+    griddep_wait();
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x, n = (long long)a.B * a.L * a.Hk * a.Dk;
     if (i >= n) return;
     const int d = (int)(i % a.Dk), hk = (int)(i / a.Dk % a.Hk), group = a.Hv / a.Hk;
@@ -639,13 +644,9 @@ int column_width(const Args &a) { return (long long)a.B * a.Hv * ((a.Dv + 7) / 8
 
 template <typename T, int C, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
     const dim3 grid((a.Dv + C - 1) / C, a.Hv, a.B);
-    if (a.Dk <= 64)
-        column_sweep_kernel<T, 8, C, REV><<<grid, 8 * C + 64, 0, st>>>(a);
-    else if (a.Dk <= 128)
-        column_sweep_kernel<T, 16, C, REV><<<grid, 8 * C + 64, 0, st>>>(a);
-    else
-        column_sweep_kernel<T, 32, C, REV><<<grid, 8 * C + 64, 0, st>>>(a);
-    return cudaGetLastError();
+    auto *kernel = a.Dk <= 64 ? column_sweep_kernel<T, 8, C, REV>
+                   : a.Dk <= 128 ? column_sweep_kernel<T, 16, C, REV> : column_sweep_kernel<T, 32, C, REV>;
+    return launch_after(kernel, grid, 8 * C + 64, 0, st, a);
 }
 template <typename T, bool REV> cudaError_t column_sweep(const Args &a, cudaStream_t st) {
     return column_width(a) == 8 ? column_sweep<T, 8, REV>(a, st) : column_sweep<T, 32, REV>(a, st);
@@ -655,31 +656,29 @@ template <typename T, int RPT> cudaError_t row_sweep(const Args &a, cudaStream_t
     constexpr int bytes = sizeof(RowSmem<RPT>);
     const cudaError_t e = cudaFuncSetAttribute(row_sweep_kernel<T, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    row_sweep_kernel<T, RPT><<<grid, 2 * SWT, bytes, st>>>(a);
-    return cudaGetLastError();
+    return launch_after(row_sweep_kernel<T, RPT>, grid, 2 * SWT, bytes, st, a);
 }
 template <typename T> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
     return a.Dv <= 64 ? row_sweep<T, 4>(a, st) : a.Dv <= 128 ? row_sweep<T, 8>(a, st) : row_sweep<T, 16>(a, st);
 }
 
+cudaError_t decay_grads(const Args &a, cudaStream_t st) {
+    return launch_after(decay_grads_kernel, (unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st, a);
+}
 template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
     cudaError_t e = column_sweep<T, true>(a, st);
     if (e != cudaSuccess || a.L == 0) return e;
     if ((e = row_sweep<T>(a, st)) != cudaSuccess) return e;
-    const long long rows = (long long)a.B * a.L * a.Hv;
-    token_grads_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
-    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a);
-    const long long n = (long long)a.B * a.L * a.Hk * a.Dk;
-    group_sum_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    const long long rows = (long long)a.B * a.L * a.Hv, n = (long long)a.B * a.L * a.Hk * a.Dk;
+    if ((e = launch_after(token_grads_kernel<T>, (unsigned)((rows + 7) / 8), 256, 0, st, a)) != cudaSuccess) return e;
+    if ((e = decay_grads(a, st)) != cudaSuccess) return e;
+    return launch_after(group_sum_kernel<T>, (unsigned)((n + 255) / 256), 256, 0, st, a);
 }
 
 // The tensor-core path's launches, and the decays' gradients.
 cudaError_t backward_tc(const Args &a, cudaStream_t st) {
     const cudaError_t e = tc_backward(a, st);
-    if (e != cudaSuccess) return e;
-    decay_grads_kernel<<<(unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    return e == cudaSuccess ? decay_grads(a, st) : e;
 }
 
 bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

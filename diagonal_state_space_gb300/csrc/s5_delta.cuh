@@ -41,6 +41,9 @@ struct Args {
                                       // cores, [B][Hv][N][Dv / 64][2][Dk][64] bf16 (two parts)
     void *images;                     // operand images of the tensor-core path; then a state between launches
     int from, count;                  // tensor cores: the chunks of this launch
+    bool first;                       // more chunks follow, whose preparation may start
+    bool beside;                      // the preparation runs while the kernel before it on the stream does, on which
+                                      // it must not depend, and ends after that one
 };
 
 __host__ __device__ inline int chunks(int L) { return (L + CHUNK - 1) / CHUNK; }
@@ -50,6 +53,24 @@ __host__ __device__ inline int chunks(int L) { return (L + CHUNK - 1) / CHUNK; }
 // 64 can hold; NaN stays NaN.
 __device__ __forceinline__ float clamp_g(float g) { return g < -128.0f ? -128.0f : g; }
 
+// A launch whose blocks may be scheduled while the kernel before it drains: every
+// kernel of the delta rule waits for that one (griddep_wait in all threads)
+// before it touches global memory or TMEM, so that it also comes after all
+// earlier ones.  None lets the next one in early: blocks that wait crowd some SMs
+// (2 x 500 tokens of 4 heads of 64 x 64, forward and backward, 235 against 187 us).
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+    cudaLaunchAttribute attr;
+    set_programmatic(attr);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 // Whether the tensor-core path takes these arguments.
 bool tc_supported(const Args &a, s5_dtype dtype, bool backward);
 // Workspace of the tensor-core path; 0 for head sizes that it does not take.

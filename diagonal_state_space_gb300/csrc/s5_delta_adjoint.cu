@@ -72,6 +72,7 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
         sb->abort = 0;
         fence_mbar_init();
     }
+    griddep_wait();
     if (warp == 8) {
         tmem_alloc(&sb->tmem, 512);
         tmem_relinquish();
@@ -384,6 +385,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         lb->abort = 0;
         fence_mbar_init();
     }
+    griddep_wait();
     if (warp == 0) {
         __syncwarp();
         tmem_alloc(&lb->tmem, 512);
@@ -626,8 +628,7 @@ template <int DK, int DV> cudaError_t launch_local(const Args &a, cudaStream_t s
     const cudaError_t e = big_smem(delta_local_kernel<DK, DV>, LocalSmem<DK, DV>::total);
     if (e != cudaSuccess) return e;
     const long long items = (long long)chunks(a.L) * a.Hk * a.B;
-    delta_local_kernel<DK, DV><<<(unsigned)(items < 152 ? items : 152), LT, LocalSmem<DK, DV>::total, st>>>(a);
-    return cudaGetLastError();
+    return launch_after(delta_local_kernel<DK, DV>, (unsigned)(items < 152 ? items : 152), LT, LocalSmem<DK, DV>::total, st, a);
 }
 
 template <int DK> cudaError_t backward(const Args &a, cudaStream_t st) {
@@ -642,8 +643,7 @@ template <int DK> cudaError_t backward(const Args &a, cudaStream_t st) {
     if (e == cudaSuccess) e = tc_prepare(all, true, st);
     if (e == cudaSuccess) e = big_smem(delta_adjoint_kernel<DK>, AdjSmem<DK>::total);
     if (e != cudaSuccess) return e;
-    delta_adjoint_kernel<DK><<<dim3(a.Dv / NV, a.Hv, a.B), ADJ_THREADS, AdjSmem<DK>::total, st>>>(m, a);
-    e = cudaGetLastError();
+    e = launch_after(delta_adjoint_kernel<DK>, dim3(a.Dv / NV, a.Hv, a.B), ADJ_THREADS, AdjSmem<DK>::total, st, m, a);
     if (e != cudaSuccess) return e;
     return a.Dv == 128 ? launch_local<DK, 128>(a, st) : launch_local<DK, 64>(a, st);
 }

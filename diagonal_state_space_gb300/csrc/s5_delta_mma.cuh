@@ -11,9 +11,7 @@
 namespace s5 {
 namespace delta {
 
-// s5_delta_prep.cu.  beside: runs while the kernel before it on the stream does,
-// which it must not depend on, and ends after it.
-cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st, bool beside = false);
+cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st);   // s5_delta_prep.cu
 int prep_fault_take();
 int scan_fault_take();                                                     // s5_delta_scan.cu
 int adjoint_fault_take();                                                  // s5_delta_adjoint.cu

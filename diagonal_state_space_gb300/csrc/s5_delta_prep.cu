@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
     auto meta_of = [&](int j) { return reinterpret_cast<Meta *>(smem + L::meta + (j & 1) * META_BYTES); };
     auto near_of = [&](int j) { return reinterpret_cast<float *>(smem + L::near) + (j & 1) * C; };
     auto wait = [&](uint64_t *bar, int parity) { return bounded_wait(bar, (uint32_t)parity, &pb->abort); };
+    if (!a.beside) griddep_wait();
     if (tid == 0) {
         mbar_init(&pb->tiles, 1);
         mbar_init(&pb->done, 1);
@@ -348,33 +349,24 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 128);
     // beside the scan of earlier chunks: this grid ends after that one
-    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) griddep_wait();
+    if (a.beside && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) griddep_wait();
 }
 
-template <int DK, bool TRANS> cudaError_t launch(const Args &a, cudaStream_t st, bool beside) {
+template <int DK, bool TRANS> cudaError_t launch(const Args &a, cudaStream_t st) {
     PrepMaps m = {};
     cudaError_t e = encode_rows(&m.k16, false, a.k, a.ldk, a.B, a.L, a.Hk, DK, 16);
     if (e == cudaSuccess) e = encode_rows(&m.q16, false, a.q, a.ldq, a.B, a.L, a.Hk, DK, 16);
     if (e == cudaSuccess) e = encode_rows(&m.k64, false, a.k, a.ldk, a.B, a.L, a.Hk, DK);
     if (e == cudaSuccess) e = big_smem(delta_prep_kernel<DK, TRANS>, PrepSmem<DK>::total);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    set_programmatic(attr);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.count, a.Hk, a.B);
-    cfg.blockDim = dim3(PT);
-    cfg.dynamicSmemBytes = PrepSmem<DK>::total;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = beside;
-    return cudaLaunchKernelEx(&cfg, delta_prep_kernel<DK, TRANS>, m, a);
+    return launch_after(delta_prep_kernel<DK, TRANS>, dim3(a.count, a.Hk, a.B), PT, PrepSmem<DK>::total, st, m, a);
 }
 
 }  // namespace
 
-cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st, bool beside) {
-    if (a.Dk == 128) return transposed ? launch<128, true>(a, st, beside) : launch<128, false>(a, st, beside);
-    return transposed ? launch<64, true>(a, st, beside) : launch<64, false>(a, st, beside);
+cudaError_t tc_prepare(const Args &a, bool transposed, cudaStream_t st) {
+    if (a.Dk == 128) return transposed ? launch<128, true>(a, st) : launch<128, false>(a, st);
+    return transposed ? launch<64, true>(a, st) : launch<64, false>(a, st);
 }
 
 int prep_fault_take() { return fault_take(); }

@@ -95,7 +95,6 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
     // this launch's chunks: N of them, from `from` on
     const int N = a.count, from = a.from, all = chunks(a.L);
     const long long bh = (long long)b * a.Hv + h;
-    if (threadIdx.x == 0) griddep_launch_dependents();   // the rest's preparation needs nothing from here
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sb->kq_full[i], 1), mbar_init(&sb->kq_empty[i], 1);
@@ -110,6 +109,8 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
         fence_mbar_init();
     }
     constexpr int MMA_WARP = 8 * SL, COPY_WARP = MMA_WARP + 1;
+    griddep_wait();
+    if (a.first) griddep_launch_dependents();   // the rest's preparation needs nothing from here
     if (warp == MMA_WARP) {
         tmem_alloc(&sb->tmem, TMEM);
         tmem_relinquish();
@@ -375,8 +376,7 @@ template <int DK, int SL, bool KEEP, int NC> cudaError_t launch(const ScanMaps &
     using L = ScanSmem<DK, SL, KEEP, NC>;
     const cudaError_t e = big_smem(delta_scan_kernel<DK, SL, KEEP, NC>, L::total);
     if (e != cudaSuccess) return e;
-    delta_scan_kernel<DK, SL, KEEP, NC><<<dim3(a.Dv / (SL * NC), a.Hv, a.B), SCAN_THREADS<SL>, L::total, st>>>(m, a);
-    return cudaGetLastError();
+    return launch_after(delta_scan_kernel<DK, SL, KEEP, NC>, dim3(a.Dv / (SL * NC), a.Hv, a.B), SCAN_THREADS<SL>, L::total, st, m, a);
 }
 
 // Where the scan leaves half of the SMs free, the first quarter of the chunks is
@@ -409,10 +409,10 @@ template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
         first.count = rest.from = all.count / SPLIT;
         rest.count -= first.count;
         float *carry = reinterpret_cast<float *>(static_cast<char *>(a.images) + heads * all.count * IMG_BYTES);
-        first.s_last = carry, rest.s0 = carry;
+        first.s_last = carry, rest.s0 = carry, first.first = rest.beside = true;
         if (e == cudaSuccess) e = tc_prepare(first, false, st);
         if (e == cudaSuccess) e = launch<DK, 1, false, 32>(m, first, st);
-        if (e == cudaSuccess) e = tc_prepare(rest, false, st, true);
+        if (e == cudaSuccess) e = tc_prepare(rest, false, st);
         return e == cudaSuccess ? launch<DK, 1, false, 32>(m, rest, st) : e;
     }
     if (e == cudaSuccess) e = tc_prepare(all, false, st);
