@@ -12,6 +12,10 @@
 // layout that the local products below read.  <S, Z> at each chunk's end, the
 // anchor of the decays' gradients, is taken in 32 bits on the way.
 //
+// Bound: as the forward scan, the chain product -> sums, splits -> product three
+// times a chunk, 4.1 us with 64 columns a CTA and the tiles of X, Z and the state
+// beside it: 4 sequences of 2048 tokens, 16 heads of 128, 131 us.
+//
 // All else is local to a chunk (delta_local_kernel).
 #include "s5_delta_mma.cuh"
 
@@ -293,7 +297,9 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
 // bf16 values here (17 bits), three products against another pair, two against
 // a bf16 operand.
 // Bound: what it reads (the state, the adjoint and 64 tokens' X, e, o, dO, v:
-// 240 KB per chunk and head of 128 x 128).
+// 240 KB per chunk and head of 128 x 128), and the phases between its products in
+// a CTA alone on its SM: 2048 chunks and heads in 161 us, 3.1 TB/s.  One CTA a
+// chunk without the prefetch took 200 us.
 // ---------------------------------------------------------------------------
 constexpr int LT = 512;
 

@@ -1,6 +1,7 @@
 // s5_delta_prep.cu -- what a chunk of the gated delta rule needs besides its
 // state, for all chunks at once (s5_delta_scan.cu has the mathematics): one
-// CTA per chunk and key head, over the key head's value heads.
+// CTA per chunk and key head, over the key head's value heads (or, where there
+// are few, per value head).
 //
 // k_i.k_j and q_i.k_j are one tcgen05 product [K; Q] K^T, taken once and kept
 // in registers.  Decay factors D_ij of two different blocks of 16 tokens are
@@ -22,8 +23,10 @@
 // TRANS: T = (I + strict lower(beta_i D_ij k_i.k_j))^-1 and [T; P T] instead,
 // which the backward pass uses.
 //
-// Bound: the 50 KB image written per chunk and value head, and the latency of
-// the block steps, which three CTAs an SM cover for one another.
+// Bound: the latency of the block steps between barriers, which three CTAs an SM
+// cover for one another (issue slots 43 % busy): 8 sequences of 1999 tokens, 32
+// heads of 128 on 16 key heads, 177 us, 8192 images of 50 KB at 2.3 TB/s; 8.3 us
+// for a single chunk.
 #include "s5_delta_mma.cuh"
 
 namespace s5 {
@@ -106,7 +109,9 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
     PrepBars *pb = reinterpret_cast<PrepBars *>(smem + L::bars);
     const uint32_t img = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int c = a.from + blockIdx.x, hk = blockIdx.y, b = blockIdx.z, group = a.Hv / a.Hk;
+    // this block's value heads: `per` of them from h0 on, all of one key head
+    const int per = a.Hv / gridDim.y, h0 = blockIdx.y * per, hk = h0 / (a.Hv / a.Hk);
+    const int c = a.from + blockIdx.x, b = blockIdx.z;
     const int t0 = c * C, nt = min(C, a.L - t0), N = chunks(a.L);
     const long long row0 = (long long)b * a.L + t0;
     const int q = warp & 3, c0 = warp / 4 * 32;   // the warp's fragment: tokens 16 q on, columns c0 on
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
         tmem_alloc(&pb->tmem, 128);
         tmem_relinquish();
     }
-    if (warp == 7) chunk_factors(a, row0, nt, hk * group, meta_of(0), near_of(0), lane);
+    if (warp == 7) chunk_factors(a, row0, nt, h0, meta_of(0), near_of(0), lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -160,8 +165,8 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
     frag_load<1>(frag, kk);
     frag_load<1>(frag + QUERY_LANES, qk);
     frag_scale(qk, a.scale, a.scale);
-    for (int j = 0; j < group; ++j) {
-        const int h = hk * group + j;
+    for (int j = 0; j < per; ++j) {
+        const int h = h0 + j;
         Meta *meta = meta_of(j);
         const float *near = near_of(j);
         unsigned char *out = static_cast<unsigned char *>(a.images) + (((long long)b * a.Hv + h) * N + c) * IMG_BYTES;
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
                 }
 #pragma unroll
             for (int r = 0; r < 16; ++r) A[o + r][o + col] = x[r];
-        } else if (warp == 7 && j + 1 < group) {
+        } else if (warp == 7 && j + 1 < per) {
             chunk_factors(a, row0, nt, h + 1, meta_of(j + 1), near_of(j + 1), lane);
         }
         __syncthreads();
@@ -352,6 +357,13 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
     if (a.beside && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) griddep_wait();
 }
 
+// Blocks of a key head (chunk by chunk) up to which each is split into blocks of
+// one value head, which take its products again but not one after the other.
+// Heads of 128, a block a key head / a value head, us: 16 value heads on 8 key
+// heads, 8 chunks (64 blocks) 13.9 / 8.8, 24 chunks 17.7 / 14.2, 32 chunks (256)
+// 18.0 / 18.7; on 4 key heads, 32 chunks (128) 25.3 / 18.7.
+constexpr int SPLIT_BLOCKS = 228;
+
 template <int DK, bool TRANS> cudaError_t launch(const Args &a, cudaStream_t st) {
     PrepMaps m = {};
     cudaError_t e = encode_rows(&m.k16, false, a.k, a.ldk, a.B, a.L, a.Hk, DK, 16);
@@ -359,7 +371,8 @@ template <int DK, bool TRANS> cudaError_t launch(const Args &a, cudaStream_t st)
     if (e == cudaSuccess) e = encode_rows(&m.k64, false, a.k, a.ldk, a.B, a.L, a.Hk, DK);
     if (e == cudaSuccess) e = big_smem(delta_prep_kernel<DK, TRANS>, PrepSmem<DK>::total);
     if (e != cudaSuccess) return e;
-    return launch_after(delta_prep_kernel<DK, TRANS>, dim3(a.count, a.Hk, a.B), PT, PrepSmem<DK>::total, st, m, a);
+    const bool single = (long long)a.count * a.Hk * a.B <= SPLIT_BLOCKS;
+    return launch_after(delta_prep_kernel<DK, TRANS>, dim3(a.count, single ? a.Hv : a.Hk, a.B), PT, PrepSmem<DK>::total, st, m, a);
 }
 
 }  // namespace
