@@ -28,8 +28,8 @@
 //    of one token at once; their angles are worked out while they are on
 //    their way.
 // In both a lane holds both halves of its pairs, in either layout.  Norm and
-// rotation of 336 MB of bf16 (40 heads of 128): 66 us, 5.1 TB/s; with the backward
-// pass 537 MB in 145 us, 3.7 TB/s; rotation alone of 537 MB in 92 us, 5.9 TB/s.
+// rotation of 336 MB of bf16 (40 heads of 128): 59 us, 5.7 TB/s; with the backward
+// pass 537 MB in 127 us, 4.2 TB/s; rotation alone of 537 MB in 86 us, 6.3 TB/s.
 #include "s5_internal.cuh"
 #include "s5_sm100.cuh"
 
@@ -415,8 +415,24 @@ __global__ void __launch_bounds__(RT) rotary_bwd_kernel(const RotArgs a, int qbl
 // Streaming form: V = 4, one slot a lane.  Items are (token, segment of heads),
 // item i of a warp being i strides on; segments of queries come first.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void bulk_out(void *dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+__device__ __forceinline__ uint64_t l2_policy(bool first) {
+    uint64_t p;
+    if (first)
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    else
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void bulk_in(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_addr(dst)),
+        "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_out(void *dst, const void *src, uint32_t bytes, uint64_t policy) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;" ::"l"(dst),
+                 "r"(smem_addr(src)), "r"(bytes), "l"(policy)
                  : "memory");
 }
 __device__ __forceinline__ void bulk_wait_read_but_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
@@ -433,38 +449,44 @@ __device__ __forceinline__ void copy_wait(uint64_t *bar, uint32_t parity) {
         }
 }
 
-// Item i of warp w of W.  With enough tokens a warp takes all segments of one,
-// and works its angles out once; else the segments are dealt out one by one.
+// The items of warp w of W, one after the other.  With a norm and enough tokens a
+// warp takes consecutive tokens, all segments of each, and works a token's
+// angles and weights out once; the copies go first out of L2.  The rotation
+// alone waits for memory more than for its angles: there the segments are dealt
+// out one by one, so that all warps are at work on one stretch of memory.
+// Dealt / by token, us: norm and rotation of 336 MB 65 / 60, with its backward
+// pass 537 MB 134 / 128; rotation alone of 537 MB 86 / 97.
 struct Item {
     long long token;
     int part, h0, rows;
 };
 struct Deal {
-    int seg0, segs;
-    bool by_token;
-    long long first, step, count;   // of tokens, or of segments
-    __device__ Deal(const RotArgs &a, int s0, int n, int w, long long W) : seg0(s0), segs(n), first(w), step(W) {
-        by_token = a.T >= 2 * W;
-        const long long units = by_token ? a.T : a.T * n;
-        count = units > first ? (units - first + step - 1) / step * (by_token ? n : 1) : 0;
-    }
-    __device__ Item item(const RotArgs &a, long long i) const {
-        Item m;
-        int seg;
-        if (by_token) {
-            const long long t = i / segs;
-            seg = (int)(i - t * segs);
-            m.token = first + t * step;
+    int seg0, segs, seg = 0;
+    long long token, count;          // the next item, and how many there are
+    long long tokens_on;             // from one item to the next
+    int segs_on;
+    __device__ Deal(const RotArgs &a, int s0, int n, int w, long long W) : seg0(s0), segs(n) {
+        if (a.inv != 0.0f && a.T >= 2 * W) {
+            const long long per = (a.T + W - 1) / W;
+            token = w * per, tokens_on = 0, segs_on = 1;
+            count = a.T > token ? min(per, a.T - token) * n : 0;
         } else {
-            const long long it = first + i * step;
-            m.token = it / segs;
-            seg = (int)(it - m.token * segs);
+            const long long units = a.T * n;
+            count = units > w ? (units - w + W - 1) / W : 0;
+            token = w / n, seg = w % n;
+            tokens_on = W / n, segs_on = (int)(W % n);
         }
-        seg += seg0;
-        m.part = seg >= a.segs[0];
-        if (m.part) seg -= a.segs[0];
-        m.h0 = seg * a.per;
+    }
+    __device__ Item next(const RotArgs &a) {
+        Item m;
+        int at = seg + seg0;
+        m.token = token;
+        m.part = at >= a.segs[0];
+        if (m.part) at -= a.segs[0];
+        m.h0 = at * a.per;
         m.rows = min(a.per, (m.part ? a.heads[1] : a.heads[0]) - m.h0);
+        token += tokens_on, seg += segs_on;
+        if (seg >= segs) seg -= segs, ++token;
         return m;
     }
 };
@@ -500,17 +522,18 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_fwd_kernel(const
     unsigned long long f[V];
     bool rotated = false;
     if (in) slot_freq<V, INTER>(a, slot, f, rotated);
-    const Deal deal(a, 0, segs, blockIdx.x * SWARPS + warp, (long long)gridDim.x * SWARPS);
+    const uint64_t policy = l2_policy(a.inv != 0.0f);
+    Deal deal(a, 0, segs, blockIdx.x * SWARPS + warp, (long long)gridDim.x * SWARPS), ahead = deal;
     long long mypos = 0;   // lane i: the position of the item in stage i
     auto fetch = [&](long long i, int st) {
         if (i >= deal.count) return;
-        const Item m = deal.item(a, i);
+        const Item m = ahead.next(a);
         if (n && lane == st) mypos = a.pos[m.token];
         if (lane == 0) {
             const T *x = static_cast<const T *>(m.part ? a.x[1] : a.x[0]) + m.token * (m.part ? a.ldx[1] : a.ldx[0]) + m.h0 * a.D;
             const uint32_t bytes = (uint32_t)(m.rows * a.D * sizeof(T));
             mbar_arrive_tx(&full[warp][st], bytes);
-            bulk_load(buf + st * STRIDE, x, bytes, &full[warp][st]);
+            bulk_in(buf + st * STRIDE, x, bytes, &full[warp][st], policy);
         }
     };
 #pragma unroll
@@ -520,7 +543,7 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_fwd_kernel(const
     int part = -1;
     float c[V], s[V], ca[V], sa[V], cb[V], sb[V];   // a pair's cosine and sine, times its values' weights
     for (long long it = 0; it < deal.count; ++it) {
-        const Item m = deal.item(a, it);
+        const Item m = deal.next(a);
         const long long pos = __shfl_sync(0xffffffffu, mypos, st);
         if (m.token != token || m.part != part) {
             if (m.token != token) slot_angles<V>(a, f, rotated, pos, c, s);
@@ -566,7 +589,7 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_fwd_kernel(const
         __syncwarp();
         if (lane == 0) {
             T *y = static_cast<T *>(m.part ? a.y[1] : a.y[0]) + m.token * (m.part ? a.ldy[1] : a.ldy[0]) + m.h0 * a.D;
-            bulk_out(y, x, (uint32_t)(m.rows * a.D * sizeof(T)));
+            bulk_out(y, x, (uint32_t)(m.rows * a.D * sizeof(T)), policy);
             bulk_commit();
             if (it > 0) bulk_wait_read_but_1();   // the item before has left its stage
         }
@@ -610,17 +633,18 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_bwd_kernel(const
 #pragma unroll
     for (int i = 0; i < V; ++i) wl[i] = wh[i] = 1.0f;
     if (w && in) load_weight<V>(w + lo, wl), load_weight<V>(w + hi, wh);
-    const Deal deal(a, seg0, segs, blk * SWARPS + warp, (long long)nblk * SWARPS);
+    const uint64_t policy = l2_policy(a.inv != 0.0f);
+    Deal deal(a, seg0, segs, blk * SWARPS + warp, (long long)nblk * SWARPS), ahead = deal;
     long long mypos = 0;
     auto fetch = [&](long long i, int st) {
         if (i >= deal.count) return;
-        const Item m = deal.item(a, i);
+        const Item m = ahead.next(a);
         if (n && lane == st) mypos = a.pos[m.token];
         if (lane == 0) {
             const uint32_t bytes = (uint32_t)(m.rows * a.D * sizeof(T));
             mbar_arrive_tx(&full[warp][st], 2 * bytes);
-            bulk_load(buf + st * STRIDE, xb + m.token * ldx + m.h0 * a.D, bytes, &full[warp][st]);
-            bulk_load(buf + st * STRIDE + DY, gb + m.token * lddy + m.h0 * a.D, bytes, &full[warp][st]);
+            bulk_in(buf + st * STRIDE, xb + m.token * ldx + m.h0 * a.D, bytes, &full[warp][st], policy);
+            bulk_in(buf + st * STRIDE + DY, gb + m.token * lddy + m.h0 * a.D, bytes, &full[warp][st], policy);
         }
     };
 #pragma unroll
@@ -629,7 +653,7 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_bwd_kernel(const
     long long token = -1;
     float c[V], s[V];
     for (long long it = 0; it < deal.count; ++it) {
-        const Item m = deal.item(a, it);
+        const Item m = deal.next(a);
         const long long pos = __shfl_sync(0xffffffffu, mypos, st);
         if (m.token != token) slot_angles<V>(a, f, rotated, pos, c, s);
         token = m.token;
@@ -673,7 +697,7 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_bwd_kernel(const
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            bulk_out(yb + m.token * ldy + m.h0 * a.D, x, (uint32_t)(m.rows * a.D * sizeof(T)));
+            bulk_out(yb + m.token * ldy + m.h0 * a.D, x, (uint32_t)(m.rows * a.D * sizeof(T)), policy);
             bulk_commit();
             if (it > 0) bulk_wait_read_but_1();
         }
