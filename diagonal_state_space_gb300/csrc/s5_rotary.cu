@@ -39,11 +39,12 @@ using namespace sm100;
 
 constexpr int RT = 128;             // threads per block
 constexpr int SWARPS = 8;           // warps of a streaming block, two blocks an SM
-// Bytes of rows from which on the streaming form runs.  40 heads of 128 in
-// bf16, streaming against direct: forward 11.9 / 11.2 us at 21 MB, 15.3 / 15.6
-// at 31 MB, 68 / 83 at 168 MB; backward 6.2 / 8.4 us at 1.3 MB, 6.0 / 5.5 at
-// 0.7 MB, 58 / 104 at 84 MB.
-constexpr long long STREAM_FWD = 32 << 20, STREAM_BWD = 1 << 20;
+// Bytes of rows from which on the streaming form runs: with a norm, the rotation
+// alone, backward.  Heads of 128 in bf16, streaming / direct, us: with a norm 11.5
+// / 11.2 at 21 MB, 14.5 / 15.5 at 31 MB, 35.8 / 40.2 at 84 MB; the rotation alone
+// 4.3 / 4.0 at 1 MB, 4.5 / 4.8 at 2.1 MB, 5.3 / 7.0 at 8.4 MB, 26.5 / 28.8 at 67 MB;
+// backward 5.8 / 5.5 at 0.7 MB, 6.0 / 8.4 at 1.3 MB, 55 / 101 at 84 MB.
+constexpr long long STREAM_FWD = 24 << 20, STREAM_TURN = 2 << 20, STREAM_BWD = 1 << 20;
 constexpr int STAGES = 3;           // items of a warp in shared memory
 constexpr int FWD_ITEM = 4096;      // bytes of rows an item holds at most
 constexpr int BWD_ITEM = 2048;      // of x, and as many of dy
@@ -853,7 +854,7 @@ cudaError_t run_type(RotArgs &a, bool inter, const long long *lds, int nld, bool
     a.want_dw[0] = dwq != nullptr;
     a.want_dw[1] = dwk != nullptr;
     const int row = a.D * (int)sizeof(T);
-    bool ok = V == 4 && a.T * (a.heads[0] + a.heads[1]) * row >= (backward ? STREAM_BWD : STREAM_FWD);
+    bool ok = V == 4 && a.T * (a.heads[0] + a.heads[1]) * row >= (backward ? STREAM_BWD : a.inv != 0.0f ? STREAM_FWD : STREAM_TURN);
     for (int i = 0; i < nld; ++i) ok = ok && lds[i] * (long long)sizeof(T) % 16 == 0;
     for (int p = 0; p < 2; ++p) ok = ok && a.heads[p] * row % 16 == 0;
     a.stream = ok;
