@@ -3,7 +3,7 @@
 //
 // A call for one token of a sequence is a few microseconds of kernel; read in
 // Python, a dozen arguments take longer than that (a key's norm and rotation
-// for one token: 20 us in Python, 10 here).  Each function below takes the
+// of eight tokens: 26 us in Python, 6.5 to 9 here).  Each function below takes the
 // arguments of the api.py function of its name, and either does the whole call
 // (outputs made, launched on the device's current stream) or returns None,
 // having done nothing, where an argument is not a contiguous CUDA tensor of the
