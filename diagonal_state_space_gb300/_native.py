@@ -56,6 +56,7 @@ SIGNATURES = {
     # position rotation and norms of queries and keys
     "s5_rotary": (_i, [_vp, _ll, _i, _vp, _vp, _i, _i, _f, _i, _ll, _i, _i, _vp, _ll, _vp]),
     "s5_rotary_fault": (_i, []),
+    "s5_rotary_wait_limit": (ctypes.c_ulonglong, [ctypes.c_ulonglong]),
     "s5_qk_norm_rotary": (_i, [_vp, _ll, _vp, _ll, _i, _vp, _vp, _i, _f, _vp, _vp, _i, _i, _f, _ll,
                                _i, _i, _i, _vp, _ll, _vp, _ll, _vp]),
     "s5_qk_norm_rotary_workspace_size": (_sz, [_i]),

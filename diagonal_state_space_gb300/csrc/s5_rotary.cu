@@ -30,6 +30,8 @@
 // In both a lane holds both halves of its pairs, in either layout.  Norm and
 // rotation of 336 MB of bf16 (40 heads of 128): 59 us, 5.7 TB/s; with the backward
 // pass 537 MB in 127 us, 4.2 TB/s; rotation alone of 537 MB in 86 us, 6.3 TB/s.
+#include <atomic>
+
 #include "s5_internal.cuh"
 #include "s5_sm100.cuh"
 
@@ -69,6 +71,7 @@ struct RotArgs {
     int segs[2];                // groups per token for queries and keys
     int want_dw[2];
     bool stream;                // which form runs
+    unsigned long long limit;   // of a wait for a copy, ns (streaming)
 };
 
 // V values as they lie in memory, and as floats.
@@ -438,16 +441,29 @@ __device__ __forceinline__ void bulk_out(void *dst, const void *src, uint32_t by
 }
 __device__ __forceinline__ void bulk_wait_read_but_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ int g_rotary_fault = 0;
-// A copy that has not come after two seconds: the item is given up, the kernel
-// ends and the host is told.
-__device__ __forceinline__ void copy_wait(uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return;
-    const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait_sleep(bar, parity, 100000))
-        if (global_ns() - t0 > 2000000000ull) {
-            atomicExch(&g_rotary_fault, 1);
-            return;
+// The whole warp: whether the copy has come.  One that has not by the call's
+// limit ends the warp's work: it turns, stores and fetches nothing more
+// (copies_settle), and the host is told.
+__device__ __forceinline__ bool copy_wait(uint64_t *bar, uint32_t parity, unsigned long long limit) {
+    bool came = mbar_test_wait(bar, parity);
+    if (!came && limit) {
+        const unsigned long long t0 = global_ns();
+        while (!(came = mbar_try_wait_sleep(bar, parity, 100000)) && global_ns() - t0 < limit) {
         }
+    }
+    came = __all_sync(0xffffffffu, came);
+    if (!came) atomicExch(&g_rotary_fault, 1);
+    return came;
+}
+// After a wait that ran out: what the warp has armed, `count` stages from `st`
+// on, lands (or 0.2 s pass) before the block gives its memory back.
+__device__ __forceinline__ void copies_settle(uint64_t *full, int st, uint32_t parity, int count) {
+    const unsigned long long t0 = global_ns();
+    for (; count > 0; --count) {
+        while (!mbar_try_wait_sleep(full + st, parity, 100000) && global_ns() - t0 < 200000000ull) {
+        }
+        if (++st == STAGES) st = 0, parity ^= 1;
+    }
 }
 
 // The items of warp w of W, one after the other.  With a norm and enough tokens a
@@ -560,7 +576,10 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_fwd_kernel(const
             }
             token = m.token, part = m.part;
         }
-        copy_wait(&full[warp][st], phase);
+        if (!copy_wait(&full[warp][st], phase, a.limit)) {
+            copies_settle(full[warp], st, phase, (int)min(deal.count - it, it > 0 ? STAGES - 1ll : STAGES));
+            break;
+        }
         T *x = buf + st * STRIDE;
 #pragma unroll 4
         for (int r0 = 0; r0 < m.rows; r0 += RP) {
@@ -658,7 +677,10 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_bwd_kernel(const
         const long long pos = __shfl_sync(0xffffffffu, mypos, st);
         if (m.token != token) slot_angles<V>(a, f, rotated, pos, c, s);
         token = m.token;
-        copy_wait(&full[warp][st], phase);
+        if (!copy_wait(&full[warp][st], phase, a.limit)) {
+            copies_settle(full[warp], st, phase, (int)min(deal.count - it, it > 0 ? STAGES - 1ll : STAGES));
+            break;
+        }
         T *x = buf + st * STRIDE, *g = x + DY;
 #pragma unroll 2
         for (int r0 = 0; r0 < m.rows; r0 += RP) {
@@ -867,8 +889,11 @@ cudaError_t run_type(RotArgs &a, bool inter, const long long *lds, int nld, bool
 #undef S5_ROT
 }
 
+std::atomic<unsigned long long> wait_limit{2000000000ull};
+
 cudaError_t run(RotArgs &a, s5_dtype dtype, bool inter, const long long *lds, int nld, bool backward, float *dwq, float *dwk,
                 cudaStream_t st) {
+    a.limit = wait_limit.load(std::memory_order_relaxed);
     return dtype == S5_BF16 ? run_type<__nv_bfloat16>(a, inter, lds, nld, backward, dwq, dwk, st)
                             : run_type<float>(a, inter, lds, nld, backward, dwq, dwk, st);
 }
@@ -1000,6 +1025,8 @@ extern "C" s5_status s5_qk_norm_rotary_backward(
     const cudaError_t e = run(a, dtype, inter, lds, nld, true, dq_weight, dk_weight, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
+
+extern "C" unsigned long long s5_rotary_wait_limit(unsigned long long ns) { return wait_limit.exchange(ns); }
 
 extern "C" int s5_rotary_fault(void) {
     int v = 0, zero = 0;

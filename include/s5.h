@@ -460,9 +460,14 @@ s5_status s5_qk_norm_rotary(const void *q, long long ldq, const void *k, long lo
                             void *q_out, long long ldqo, void *k_out, long long ldko, s5_stream_t stream);
 
 /* 1 if a wait for a copy inside the rotation kernels ran out since the last
- * call (their results are then not valid), 0 if none; the flag is cleared.
- * Synchronises the device. */
+ * call (their results are then not valid: rows may be unwritten), 0 if none; the
+ * flag is cleared.  Synchronises the device. */
 int s5_rotary_fault(void);
+
+/* Sets the longest such wait of later calls, in ns, and returns the one before
+ * (2 s at first).  0 gives up every copy that is not there at the first look:
+ * what a caller does about s5_rotary_fault can be tried with it. */
+unsigned long long s5_rotary_wait_limit(unsigned long long ns);
 
 /* Workspace of the backward pass, needed where a weight's gradient is wanted. */
 size_t s5_qk_norm_rotary_workspace_size(int D);
