@@ -474,8 +474,8 @@ __device__ __forceinline__ void copies_settle(uint64_t *full, int st, uint32_t p
 // Dealt / by token, us: norm and rotation of 336 MB 65 / 60, with its backward
 // pass 537 MB 134 / 128; rotation alone of 537 MB 86 / 97.
 struct Item {
-    long long token;
-    int part, h0, rows;
+    long long token, place;   // place: of its first head in the token's row
+    int part, rows;
 };
 struct Deal {
     int seg0, segs, seg = 0;
@@ -500,8 +500,9 @@ struct Deal {
         m.token = token;
         m.part = at >= a.segs[0];
         if (m.part) at -= a.segs[0];
-        m.h0 = at * a.per;
-        m.rows = min(a.per, (m.part ? a.heads[1] : a.heads[0]) - m.h0);
+        const int h0 = at * a.per;
+        m.place = (long long)h0 * a.D;   // a single token may have more values than 32 bits count
+        m.rows = min(a.per, (m.part ? a.heads[1] : a.heads[0]) - h0);
         token += tokens_on, seg += segs_on;
         if (seg >= segs) seg -= segs, ++token;
         return m;
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_fwd_kernel(const
         const Item m = ahead.next(a);
         if (n && lane == st) mypos = a.pos[m.token];
         if (lane == 0) {
-            const T *x = static_cast<const T *>(m.part ? a.x[1] : a.x[0]) + m.token * (m.part ? a.ldx[1] : a.ldx[0]) + m.h0 * a.D;
+            const T *x = static_cast<const T *>(m.part ? a.x[1] : a.x[0]) + m.token * (m.part ? a.ldx[1] : a.ldx[0]) + m.place;
             const uint32_t bytes = (uint32_t)(m.rows * a.D * sizeof(T));
             mbar_arrive_tx(&full[warp][st], bytes);
             bulk_in(buf + st * STRIDE, x, bytes, &full[warp][st], policy);
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_fwd_kernel(const
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            T *y = static_cast<T *>(m.part ? a.y[1] : a.y[0]) + m.token * (m.part ? a.ldy[1] : a.ldy[0]) + m.h0 * a.D;
+            T *y = static_cast<T *>(m.part ? a.y[1] : a.y[0]) + m.token * (m.part ? a.ldy[1] : a.ldy[0]) + m.place;
             bulk_out(y, x, (uint32_t)(m.rows * a.D * sizeof(T)), policy);
             bulk_commit();
             if (it > 0) bulk_wait_read_but_1();   // the item before has left its stage
@@ -663,8 +664,8 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_bwd_kernel(const
         if (lane == 0) {
             const uint32_t bytes = (uint32_t)(m.rows * a.D * sizeof(T));
             mbar_arrive_tx(&full[warp][st], 2 * bytes);
-            bulk_in(buf + st * STRIDE, xb + m.token * ldx + m.h0 * a.D, bytes, &full[warp][st], policy);
-            bulk_in(buf + st * STRIDE + DY, gb + m.token * lddy + m.h0 * a.D, bytes, &full[warp][st], policy);
+            bulk_in(buf + st * STRIDE, xb + m.token * ldx + m.place, bytes, &full[warp][st], policy);
+            bulk_in(buf + st * STRIDE + DY, gb + m.token * lddy + m.place, bytes, &full[warp][st], policy);
         }
     };
 #pragma unroll
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_bwd_kernel(const
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            bulk_out(yb + m.token * ldy + m.h0 * a.D, x, (uint32_t)(m.rows * a.D * sizeof(T)), policy);
+            bulk_out(yb + m.token * ldy + m.place, x, (uint32_t)(m.rows * a.D * sizeof(T)), policy);
             bulk_commit();
             if (it > 0) bulk_wait_read_but_1();
         }
@@ -878,7 +879,7 @@ cudaError_t run_type(RotArgs &a, bool inter, const long long *lds, int nld, bool
     const int row = a.D * (int)sizeof(T);
     bool ok = V == 4 && a.T * (a.heads[0] + a.heads[1]) * row >= (backward ? STREAM_BWD : a.inv != 0.0f ? STREAM_FWD : STREAM_TURN);
     for (int i = 0; i < nld; ++i) ok = ok && lds[i] * (long long)sizeof(T) % 16 == 0;
-    for (int p = 0; p < 2; ++p) ok = ok && a.heads[p] * row % 16 == 0;
+    for (int p = 0; p < 2; ++p) ok = ok && (long long)a.heads[p] * row % 16 == 0;
     a.stream = ok;
     if (ok) a.per = item_heads(backward ? BWD_ITEM : FWD_ITEM, row);
 #define S5_ROT(VV) \
@@ -908,7 +909,7 @@ s5_status check_common(s5_dtype dtype, const long long *pos, const double *freq,
     if (T < 0 || H < 0 || D < 1 || rot < 0 || rot > D || rot % 2) return S5_ERR_INVALID_ARGUMENT;
     if (!(amp > 0.0f) || amp > 1e30f) return S5_ERR_INVALID_ARGUMENT;
     if (D % 2 || D > 256) return S5_ERR_UNSUPPORTED;
-    if (T > (1ll << 31) / (H > 0 ? H : 1)) return S5_ERR_UNSUPPORTED;
+    if (H > 1 << 30 || T > (1ll << 31) / (H > 0 ? H : 1)) return S5_ERR_UNSUPPORTED;
     if (T > 0 && rot > 0 && (!pos || !freq || !aligned16(freq) || (reinterpret_cast<uintptr_t>(pos) & 7u)))
         return S5_ERR_INVALID_ARGUMENT;
     return S5_OK;

@@ -439,7 +439,7 @@ s5_status s5_delta_step(const void *q, const void *k, const void *v, s5_dtype dt
  * Rows: [T][H][D] of `dtype` with a pitch in elements between two tokens; an
  * output may be its input (same pitch).  positions [T], freq [rot/2] on the
  * device; rot = 0 needs neither.  D even, up to 256 (S5_ERR_UNSUPPORTED
- * otherwise), rot even, 0 <= rot <= D; amplitude > 0; T H <= 2^31.  Sums in 32
+ * otherwise), rot even, 0 <= rot <= D; amplitude > 0; H <= 2^30, T H <= 2^31.  Sums in 32
  * bits, one rounding at the end.  Asynchronous, launched with programmatic
  * stream serialisation.
  * ======================================================================== */
