@@ -280,6 +280,37 @@ def _rows(t, name, dtype=None, shape=None):
 _raw_stream = torch._C._cuda_getCurrentRawStream    # current_stream() builds an object: 8 us of a call
 
 
+def _one_device(**arrays):
+    """The device that all of a call's arrays are on (None: no array is on a GPU; the checks that follow say so)."""
+    dev = first = None
+    for name, t in arrays.items():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            continue
+        if dev is None:
+            dev, first = t.device, name
+        elif t.device != dev:
+            raise ValueError("%s is on %s, %s on %s" % (name, t.device, first, dev))
+    return dev
+
+
+class _Launch:
+    """Makes the arrays' device the current one: the library launches on that, whatever the stream."""
+
+    def __init__(self, dev):
+        self.guard = None
+        if dev is not None and dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *error):
+        if self.guard is not None:
+            self.guard.__exit__(*error)
+
+
 def _on(stream, *made):
     """The stream's handle; tensors made here outlive their use on it."""
     if stream is None:
@@ -336,24 +367,25 @@ def s5_delta_forward(q, k, v, g, beta, scale=None, s0=None, s_last=None, o=None,
         out = _native.marshal().delta_forward(q, k, v, g, beta, scale, s0, s_last, o, saved, workspace)
         if _taken("s5_delta_forward", out):
             return out
-    B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
-    f32, dev, dt = torch.float32, q.device, q.dtype
-    if o is None:
-        o = _new(v)
-    if s_last is True:
-        s_last = torch.empty(B, Hv, Dk, Dv, dtype=f32, device=dev)
-    lib = _native.lib()
-    if workspace is None:
-        workspace = _buffer(lib.s5_delta_workspace_size(B, L, Hv, Dk, Dv, 0), "s5_delta_forward", dev)
-    code = lib.s5_delta_forward(
-        *_rows(q, "q"), *_rows(k, "k", dt, q.shape), *_rows(v, "v", dt), _DT[dt],
-        _ptr(g, "g", f32, (B, L, Hv)), _ptr(beta, "beta", f32, (B, L, Hv)), _ptr(s0, "s0", f32, (B, Hv, Dk, Dv), True),
-        Dk ** -0.5 if scale is None else float(scale), B, L, Hk, Hv, Dk, Dv, *_rows(o, "o", dt, v.shape),
-        _ptr(s_last, "s_last", f32, (B, Hv, Dk, Dv), True), _ptr(saved, "saved", torch.uint8, None, True),
-        0 if saved is None else saved.numel(), _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
-        _on(stream, o, s_last, workspace))
-    check("s5_delta_forward", code)
-    return o if s_last is None else (o, s_last)
+    with _Launch(_one_device(q=q, k=k, v=v, g=g, beta=beta, s0=s0, s_last=s_last, o=o, saved=saved, workspace=workspace)):
+        B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
+        f32, dev, dt = torch.float32, q.device, q.dtype
+        if o is None:
+            o = _new(v)
+        if s_last is True:
+            s_last = torch.empty(B, Hv, Dk, Dv, dtype=f32, device=dev)
+        lib = _native.lib()
+        if workspace is None:
+            workspace = _buffer(lib.s5_delta_workspace_size(B, L, Hv, Dk, Dv, 0), "s5_delta_forward", dev)
+        code = lib.s5_delta_forward(
+            *_rows(q, "q"), *_rows(k, "k", dt, q.shape), *_rows(v, "v", dt), _DT[dt],
+            _ptr(g, "g", f32, (B, L, Hv)), _ptr(beta, "beta", f32, (B, L, Hv)), _ptr(s0, "s0", f32, (B, Hv, Dk, Dv), True),
+            Dk ** -0.5 if scale is None else float(scale), B, L, Hk, Hv, Dk, Dv, *_rows(o, "o", dt, v.shape),
+            _ptr(s_last, "s_last", f32, (B, Hv, Dk, Dv), True), _ptr(saved, "saved", torch.uint8, None, True),
+            0 if saved is None else saved.numel(), _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
+            _on(stream, o, s_last, workspace))
+        check("s5_delta_forward", code)
+        return o if s_last is None else (o, s_last)
 
 
 def s5_delta_backward(q, k, v, g, beta, do, saved, scale=None, s0=None, ds_last=None, workspace=None, stream=None):
@@ -363,24 +395,25 @@ def s5_delta_backward(q, k, v, g, beta, do, saved, scale=None, s0=None, ds_last=
         out = _native.marshal().delta_backward(q, k, v, g, beta, do, saved, scale, s0, ds_last, workspace)
         if _taken("s5_delta_backward", out):
             return out
-    B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
-    f32, dev, dt = torch.float32, q.device, q.dtype
-    e = lambda shape, t: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
-    out = dict(dq=e(q.shape, dt), dk=e(q.shape, dt), dv=e(v.shape, dt), dg=e((B, L, Hv), f32), dbeta=e((B, L, Hv), f32),
-               ds0=None if s0 is None else e((B, Hv, Dk, Dv), f32))
-    lib = _native.lib()
-    if workspace is None:
-        workspace = _buffer(lib.s5_delta_workspace_size(B, L, Hv, Dk, Dv, 1), "s5_delta_backward", dev)
-    code = lib.s5_delta_backward(
-        *_rows(q, "q"), *_rows(k, "k", dt, q.shape), *_rows(v, "v", dt), _DT[dt],
-        _ptr(g, "g", f32, (B, L, Hv)), _ptr(beta, "beta", f32, (B, L, Hv)), _ptr(s0, "s0", f32, (B, Hv, Dk, Dv), True),
-        Dk ** -0.5 if scale is None else float(scale), B, L, Hk, Hv, Dk, Dv, *_rows(do, "do", dt, v.shape),
-        _ptr(ds_last, "ds_last", f32, (B, Hv, Dk, Dv), True), _ptr(saved, "saved", torch.uint8), saved.numel(),
-        out["dq"].data_ptr(), Hk * Dk, out["dk"].data_ptr(), Hk * Dk, out["dv"].data_ptr(), Hv * Dv,
-        out["dg"].data_ptr(), out["dbeta"].data_ptr(), None if s0 is None else out["ds0"].data_ptr(),
-        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _on(stream, out["dq"], workspace, *out.values()))
-    check("s5_delta_backward", code)
-    return out
+    with _Launch(_one_device(q=q, k=k, v=v, g=g, beta=beta, do=do, saved=saved, s0=s0, ds_last=ds_last, workspace=workspace)):
+        B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
+        f32, dev, dt = torch.float32, q.device, q.dtype
+        e = lambda shape, t: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
+        out = dict(dq=e(q.shape, dt), dk=e(q.shape, dt), dv=e(v.shape, dt), dg=e((B, L, Hv), f32), dbeta=e((B, L, Hv), f32),
+                   ds0=None if s0 is None else e((B, Hv, Dk, Dv), f32))
+        lib = _native.lib()
+        if workspace is None:
+            workspace = _buffer(lib.s5_delta_workspace_size(B, L, Hv, Dk, Dv, 1), "s5_delta_backward", dev)
+        code = lib.s5_delta_backward(
+            *_rows(q, "q"), *_rows(k, "k", dt, q.shape), *_rows(v, "v", dt), _DT[dt],
+            _ptr(g, "g", f32, (B, L, Hv)), _ptr(beta, "beta", f32, (B, L, Hv)), _ptr(s0, "s0", f32, (B, Hv, Dk, Dv), True),
+            Dk ** -0.5 if scale is None else float(scale), B, L, Hk, Hv, Dk, Dv, *_rows(do, "do", dt, v.shape),
+            _ptr(ds_last, "ds_last", f32, (B, Hv, Dk, Dv), True), _ptr(saved, "saved", torch.uint8), saved.numel(),
+            out["dq"].data_ptr(), Hk * Dk, out["dk"].data_ptr(), Hk * Dk, out["dv"].data_ptr(), Hv * Dv,
+            out["dg"].data_ptr(), out["dbeta"].data_ptr(), None if s0 is None else out["ds0"].data_ptr(),
+            _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _on(stream, out["dq"], workspace, *out.values()))
+        check("s5_delta_backward", code)
+        return out
 
 
 def s5_delta_step(q, k, v, g, beta, state, scale=None, o=None, stream=None):
@@ -390,16 +423,17 @@ def s5_delta_step(q, k, v, g, beta, state, scale=None, o=None, stream=None):
         out = _native.marshal().delta_step(q, k, v, g, beta, state, scale, o)
         if _taken("s5_delta_step", out):
             return out
-    B, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 1)
-    f32, dt = torch.float32, q.dtype
-    if o is None:
-        o = _new(v)
-    code = _native.lib().s5_delta_step(
-        _arr(q, "q", dt, q.shape), _arr(k, "k", dt, q.shape), _arr(v, "v", dt, v.shape), _DT[dt],
-        _arr(g, "g", f32, (B, Hv)), _arr(beta, "beta", f32, (B, Hv)), Dk ** -0.5 if scale is None else float(scale),
-        B, Hk, Hv, Dk, Dv, _arr(state, "state", f32, (B, Hv, Dk, Dv)), _arr(o, "o", dt, v.shape), _on(stream, o))
-    check("s5_delta_step", code)
-    return o
+    with _Launch(_one_device(q=q, k=k, v=v, g=g, beta=beta, state=state, o=o)):
+        B, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 1)
+        f32, dt = torch.float32, q.dtype
+        if o is None:
+            o = _new(v)
+        code = _native.lib().s5_delta_step(
+            _arr(q, "q", dt, q.shape), _arr(k, "k", dt, q.shape), _arr(v, "v", dt, v.shape), _DT[dt],
+            _arr(g, "g", f32, (B, Hv)), _arr(beta, "beta", f32, (B, Hv)), Dk ** -0.5 if scale is None else float(scale),
+            B, Hk, Hv, Dk, Dv, _arr(state, "state", f32, (B, Hv, Dk, Dv)), _arr(o, "o", dt, v.shape), _on(stream, o))
+        check("s5_delta_step", code)
+        return o
 
 
 _LAYOUT = {"half": 0, "interleaved": 1}
@@ -425,14 +459,15 @@ def s5_rotary(x, positions, freq, layout="half", amplitude=1.0, inverse=False, o
         done = _native.marshal().rotary(x, positions, freq, _LAYOUT[layout], amplitude, int(inverse), out)
         if _taken("s5_rotary", done):
             return done
-    T, pos, fr, rot = _rot_args(x, "x", positions, freq)
-    H, D = x.shape[-2:]
-    if out is None:
-        out = _new(x)
-    code = _native.lib().s5_rotary(*_rows(x, "x", x.dtype, x.shape), _DT[x.dtype], pos, fr, rot, _LAYOUT[layout], float(amplitude),
-                                   int(inverse), T, H, D, *_rows(out, "out", x.dtype, x.shape), _on(stream, out))
-    check("s5_rotary", code)
-    return out
+    with _Launch(_one_device(x=x, positions=positions, freq=freq, out=out)):
+        T, pos, fr, rot = _rot_args(x, "x", positions, freq)
+        H, D = x.shape[-2:]
+        if out is None:
+            out = _new(x)
+        code = _native.lib().s5_rotary(*_rows(x, "x", x.dtype, x.shape), _DT[x.dtype], pos, fr, rot, _LAYOUT[layout], float(amplitude),
+                                       int(inverse), T, H, D, *_rows(out, "out", x.dtype, x.shape), _on(stream, out))
+        check("s5_rotary", code)
+        return out
 
 
 def s5_qk_norm_rotary(q, k, positions, freq, norm="rms", eps=1e-6, q_weight=None, k_weight=None, layout="half",
@@ -444,21 +479,23 @@ def s5_qk_norm_rotary(q, k, positions, freq, norm="rms", eps=1e-6, q_weight=None
                                                amplitude, q_out, k_out)
         if _taken("s5_qk_norm_rotary", out):
             return out
-    T, pos, fr, rot = _rot_args(q, "q", positions, freq)
-    (Hq, D), Hk, dt, f32 = q.shape[-2:], k.shape[-2], q.dtype, torch.float32
-    kshape = torch.Size((*q.shape[:-2], Hk, D))
-    if q_out is None:
-        q_out = _new(q)
-    if k_out is None:
-        k_out = _new(k)
-    code = _native.lib().s5_qk_norm_rotary(
-        *_rows(q, "q", dt, q.shape), *_rows(k, "k", dt, kshape), _DT[dt],
-        None if q_weight is None else _arr(q_weight, "q_weight", f32, (D,)),
-        None if k_weight is None else _arr(k_weight, "k_weight", f32, (D,)), _NORM[norm], float(eps), pos, fr, rot,
-        _LAYOUT[layout], float(amplitude), T, Hq, Hk, D, *_rows(q_out, "q_out", dt, q.shape), *_rows(k_out, "k_out", dt, kshape),
-        _on(stream, q_out, k_out))
-    check("s5_qk_norm_rotary", code)
-    return q_out, k_out
+    with _Launch(_one_device(q=q, k=k, positions=positions, freq=freq, q_weight=q_weight, k_weight=k_weight,
+                             q_out=q_out, k_out=k_out)):
+        T, pos, fr, rot = _rot_args(q, "q", positions, freq)
+        (Hq, D), Hk, dt, f32 = q.shape[-2:], k.shape[-2], q.dtype, torch.float32
+        kshape = torch.Size((*q.shape[:-2], Hk, D))
+        if q_out is None:
+            q_out = _new(q)
+        if k_out is None:
+            k_out = _new(k)
+        code = _native.lib().s5_qk_norm_rotary(
+            *_rows(q, "q", dt, q.shape), *_rows(k, "k", dt, kshape), _DT[dt],
+            None if q_weight is None else _arr(q_weight, "q_weight", f32, (D,)),
+            None if k_weight is None else _arr(k_weight, "k_weight", f32, (D,)), _NORM[norm], float(eps), pos, fr, rot,
+            _LAYOUT[layout], float(amplitude), T, Hq, Hk, D, *_rows(q_out, "q_out", dt, q.shape), *_rows(k_out, "k_out", dt, kshape),
+            _on(stream, q_out, k_out))
+        check("s5_qk_norm_rotary", code)
+        return q_out, k_out
 
 
 def s5_qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, norm="rms", eps=1e-6, q_weight=None,
@@ -470,24 +507,26 @@ def s5_qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, norm="rms"
                                                         k_weight, _LAYOUT[layout], amplitude, workspace)
         if _taken("s5_qk_norm_rotary_backward", out):
             return out
-    T, pos, fr, rot = _rot_args(q, "q", positions, freq)
-    (Hq, D), Hk, dt, f32, dev = q.shape[-2:], k.shape[-2], q.dtype, torch.float32, q.device
-    kshape = (*q.shape[:-2], Hk, D)
-    lib = _native.lib()
-    out = dict(dq=torch.empty(q.shape, dtype=dt, device=dev), dk=torch.empty(kshape, dtype=dt, device=dev),
-               dwq=None if q_weight is None else torch.empty(D, dtype=f32, device=dev),
-               dwk=None if k_weight is None else torch.empty(D, dtype=f32, device=dev))
-    if workspace is None and (q_weight is not None or k_weight is not None):
-        workspace = _buffer(lib.s5_qk_norm_rotary_workspace_size(D), "s5_qk_norm_rotary_backward", dev)
-    code = lib.s5_qk_norm_rotary_backward(
-        *_rows(q, "q"), *_rows(k, "k", dt, kshape), _DT[dt], _ptr(q_weight, "q_weight", f32, (D,), True),
-        _ptr(k_weight, "k_weight", f32, (D,), True), _NORM[norm], float(eps), pos, fr, rot, _LAYOUT[layout],
-        float(amplitude), T, Hq, Hk, D, *_rows(dq_out, "dq_out", dt, q.shape), *_rows(dk_out, "dk_out", dt, kshape),
-        out["dq"].data_ptr(), Hq * D, out["dk"].data_ptr(), Hk * D, _ptr(out["dwq"], "dwq", None, None, True),
-        _ptr(out["dwk"], "dwk", None, None, True), _ptr(workspace, "workspace", torch.uint8, None, True),
-        0 if workspace is None else workspace.numel(), _on(stream, out["dq"], workspace, *out.values()))
-    check("s5_qk_norm_rotary_backward", code)
-    return out
+    with _Launch(_one_device(q=q, k=k, dq_out=dq_out, dk_out=dk_out, positions=positions, freq=freq,
+                             q_weight=q_weight, k_weight=k_weight, workspace=workspace)):
+        T, pos, fr, rot = _rot_args(q, "q", positions, freq)
+        (Hq, D), Hk, dt, f32, dev = q.shape[-2:], k.shape[-2], q.dtype, torch.float32, q.device
+        kshape = (*q.shape[:-2], Hk, D)
+        lib = _native.lib()
+        out = dict(dq=torch.empty(q.shape, dtype=dt, device=dev), dk=torch.empty(kshape, dtype=dt, device=dev),
+                   dwq=None if q_weight is None else torch.empty(D, dtype=f32, device=dev),
+                   dwk=None if k_weight is None else torch.empty(D, dtype=f32, device=dev))
+        if workspace is None and (q_weight is not None or k_weight is not None):
+            workspace = _buffer(lib.s5_qk_norm_rotary_workspace_size(D), "s5_qk_norm_rotary_backward", dev)
+        code = lib.s5_qk_norm_rotary_backward(
+            *_rows(q, "q"), *_rows(k, "k", dt, kshape), _DT[dt], _ptr(q_weight, "q_weight", f32, (D,), True),
+            _ptr(k_weight, "k_weight", f32, (D,), True), _NORM[norm], float(eps), pos, fr, rot, _LAYOUT[layout],
+            float(amplitude), T, Hq, Hk, D, *_rows(dq_out, "dq_out", dt, q.shape), *_rows(dk_out, "dk_out", dt, kshape),
+            out["dq"].data_ptr(), Hq * D, out["dk"].data_ptr(), Hk * D, _ptr(out["dwq"], "dwq", None, None, True),
+            _ptr(out["dwk"], "dwk", None, None, True), _ptr(workspace, "workspace", torch.uint8, None, True),
+            0 if workspace is None else workspace.numel(), _on(stream, out["dq"], workspace, *out.values()))
+        check("s5_qk_norm_rotary_backward", code)
+        return out
 
 
 __all__ = ["s5_discretize", "s5_discretize_ex", "s5_forward", "s5_forward_varying_dt",

@@ -6,13 +6,14 @@
 // of eight tokens: 26 us in Python, 6.5 to 9 here).  Each function below takes the
 // arguments of the api.py function of its name, and either does the whole call
 // (outputs made, launched on the device's current stream) or returns None,
-// having done nothing, where an argument is not a contiguous CUDA tensor of the
-// expected type and shape; api.py then takes it apart itself, pitches and
-// messages included.  An error of the call comes back as its status, an int.
+// having done nothing, where an argument is not a contiguous tensor on the current
+// CUDA device, of the expected type and shape; api.py then takes it apart itself,
+// pitches, other devices and messages included.  An error of the call comes back as its status, an int.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -37,7 +38,10 @@ struct Reader {
         if (!ok || !THPVariable_CheckExact(args[i])) return ok = false, nullptr;
         const Tensor &t = THPVariable_Unpack(args[i]);
         if (!t.is_cuda() || !t.is_contiguous() || t.numel() == 0) return ok = false, nullptr;
-        if (device < 0) device = t.get_device();
+        if (device < 0) {
+            device = t.get_device();
+            if (device != c10::cuda::current_device()) return ok = false, nullptr;   // launches go to that one
+        }
         if (t.get_device() != device) return ok = false, nullptr;
         return &t;
     }
