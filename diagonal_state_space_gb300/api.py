@@ -280,51 +280,55 @@ def _rows(t, name, dtype=None, shape=None):
 _raw_stream = torch._C._cuda_getCurrentRawStream    # current_stream() builds an object: 8 us of a call
 
 
-def _one_device(**arrays):
-    """The device that all of a call's arrays are on (None: no array is on a GPU; the checks that follow say so)."""
-    dev = first = None
-    for name, t in arrays.items():
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            continue
-        if dev is None:
-            dev, first = t.device, name
-        elif t.device != dev:
-            raise ValueError("%s is on %s, %s on %s" % (name, t.device, first, dev))
-    return dev
-
-
 class _Launch:
-    """Makes the arrays' device the current one: the library launches on that, whatever the stream."""
+    """The device and the stream of a call on the given arrays, both current inside it.  The library launches on the
+    current device, so that has to be the arrays'.  What is made inside belongs to the call's stream: no other stream's
+    work can still be using its memory.  Where that is not the caller's stream, memory that one of the two hands to
+    the other (the arrays, and what goes through made()) is not given away before both are done with it."""
 
-    def __init__(self, dev):
-        self.guard = None
-        if dev is not None and dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(dev)
+    def __init__(self, stream, **arrays):
+        self.stream, self.guards, self.home, self.handle = stream, [], None, 0
+        self.arrays = {n: t for n, t in arrays.items() if isinstance(t, torch.Tensor) and t.is_cuda}
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+        dev = first = None
+        for name, t in self.arrays.items():
+            if dev is None:
+                dev, first = t.device, name
+            elif t.device != dev:
+                raise ValueError("%s is on %s, %s on %s" % (name, t.device, first, dev))
+        if dev is None:                  # no array on a GPU: the checks inside say so
+            return self
+        side = self.stream
+        if side is not None and not isinstance(side, torch.cuda.Stream):
+            side = torch.cuda.ExternalStream(int(side), dev) if int(side) else torch.cuda.default_stream(dev)
+        if side is not None and side.device != dev:
+            raise ValueError("the stream is on %s, the arrays on %s" % (side.device, dev))
+        if dev.index != torch.cuda.current_device():
+            self._enter(torch.cuda.device(dev))
+        if side is None:
+            self.handle = _raw_stream(dev.index)
+            return self
+        self.handle, home = side.cuda_stream, torch.cuda.current_stream(dev)
+        if self.handle != home.cuda_stream:
+            self.home = home
+            for t in self.arrays.values():
+                t.record_stream(side)
+            self._enter(torch.cuda.stream(side))
         return self
 
+    def _enter(self, guard):
+        guard.__enter__()
+        self.guards.append(guard)
+
     def __exit__(self, *error):
-        if self.guard is not None:
-            self.guard.__exit__(*error)
+        while self.guards:
+            self.guards.pop().__exit__(*error)
 
-
-def _on(stream, *made):
-    """The stream's handle; tensors made here outlive their use on it."""
-    if stream is None:
-        return _raw_stream(made[0].device.index)
-    if isinstance(stream, torch.cuda.Stream):
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-        return stream.cuda_stream
-    other = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    for t in made:
-        if t is not None:
-            t.record_stream(other)
-    return int(stream)
+    def made(self, t):
+        if self.home is not None:
+            t.record_stream(self.home)
+        return t
 
 
 def _delta_sizes(q, k, v, lead):
@@ -367,13 +371,14 @@ def s5_delta_forward(q, k, v, g, beta, scale=None, s0=None, s_last=None, o=None,
         out = _native.marshal().delta_forward(q, k, v, g, beta, scale, s0, s_last, o, saved, workspace)
         if _taken("s5_delta_forward", out):
             return out
-    with _Launch(_one_device(q=q, k=k, v=v, g=g, beta=beta, s0=s0, s_last=s_last, o=o, saved=saved, workspace=workspace)):
+    with _Launch(stream, q=q, k=k, v=v, g=g, beta=beta, s0=s0, s_last=s_last, o=o, saved=saved,
+                 workspace=workspace) as on:
         B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
         f32, dev, dt = torch.float32, q.device, q.dtype
         if o is None:
-            o = _new(v)
+            o = on.made(_new(v))
         if s_last is True:
-            s_last = torch.empty(B, Hv, Dk, Dv, dtype=f32, device=dev)
+            s_last = on.made(torch.empty(B, Hv, Dk, Dv, dtype=f32, device=dev))
         lib = _native.lib()
         if workspace is None:
             workspace = _buffer(lib.s5_delta_workspace_size(B, L, Hv, Dk, Dv, 0), "s5_delta_forward", dev)
@@ -383,7 +388,7 @@ def s5_delta_forward(q, k, v, g, beta, scale=None, s0=None, s_last=None, o=None,
             Dk ** -0.5 if scale is None else float(scale), B, L, Hk, Hv, Dk, Dv, *_rows(o, "o", dt, v.shape),
             _ptr(s_last, "s_last", f32, (B, Hv, Dk, Dv), True), _ptr(saved, "saved", torch.uint8, None, True),
             0 if saved is None else saved.numel(), _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
-            _on(stream, o, s_last, workspace))
+            on.handle)
         check("s5_delta_forward", code)
         return o if s_last is None else (o, s_last)
 
@@ -395,10 +400,11 @@ def s5_delta_backward(q, k, v, g, beta, do, saved, scale=None, s0=None, ds_last=
         out = _native.marshal().delta_backward(q, k, v, g, beta, do, saved, scale, s0, ds_last, workspace)
         if _taken("s5_delta_backward", out):
             return out
-    with _Launch(_one_device(q=q, k=k, v=v, g=g, beta=beta, do=do, saved=saved, s0=s0, ds_last=ds_last, workspace=workspace)):
+    with _Launch(stream, q=q, k=k, v=v, g=g, beta=beta, do=do, saved=saved, s0=s0, ds_last=ds_last,
+                 workspace=workspace) as on:
         B, L, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 2)
         f32, dev, dt = torch.float32, q.device, q.dtype
-        e = lambda shape, t: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
+        e = lambda shape, t: on.made(torch.empty(shape, dtype=t, device=dev))  # noqa: E731
         out = dict(dq=e(q.shape, dt), dk=e(q.shape, dt), dv=e(v.shape, dt), dg=e((B, L, Hv), f32), dbeta=e((B, L, Hv), f32),
                    ds0=None if s0 is None else e((B, Hv, Dk, Dv), f32))
         lib = _native.lib()
@@ -411,7 +417,7 @@ def s5_delta_backward(q, k, v, g, beta, do, saved, scale=None, s0=None, ds_last=
             _ptr(ds_last, "ds_last", f32, (B, Hv, Dk, Dv), True), _ptr(saved, "saved", torch.uint8), saved.numel(),
             out["dq"].data_ptr(), Hk * Dk, out["dk"].data_ptr(), Hk * Dk, out["dv"].data_ptr(), Hv * Dv,
             out["dg"].data_ptr(), out["dbeta"].data_ptr(), None if s0 is None else out["ds0"].data_ptr(),
-            _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _on(stream, out["dq"], workspace, *out.values()))
+            _ptr(workspace, "workspace", torch.uint8), workspace.numel(), on.handle)
         check("s5_delta_backward", code)
         return out
 
@@ -423,15 +429,15 @@ def s5_delta_step(q, k, v, g, beta, state, scale=None, o=None, stream=None):
         out = _native.marshal().delta_step(q, k, v, g, beta, state, scale, o)
         if _taken("s5_delta_step", out):
             return out
-    with _Launch(_one_device(q=q, k=k, v=v, g=g, beta=beta, state=state, o=o)):
+    with _Launch(stream, q=q, k=k, v=v, g=g, beta=beta, state=state, o=o) as on:
         B, Hk, Dk, Hv, Dv = _delta_sizes(q, k, v, 1)
         f32, dt = torch.float32, q.dtype
         if o is None:
-            o = _new(v)
+            o = on.made(_new(v))
         code = _native.lib().s5_delta_step(
             _arr(q, "q", dt, q.shape), _arr(k, "k", dt, q.shape), _arr(v, "v", dt, v.shape), _DT[dt],
             _arr(g, "g", f32, (B, Hv)), _arr(beta, "beta", f32, (B, Hv)), Dk ** -0.5 if scale is None else float(scale),
-            B, Hk, Hv, Dk, Dv, _arr(state, "state", f32, (B, Hv, Dk, Dv)), _arr(o, "o", dt, v.shape), _on(stream, o))
+            B, Hk, Hv, Dk, Dv, _arr(state, "state", f32, (B, Hv, Dk, Dv)), _arr(o, "o", dt, v.shape), on.handle)
         check("s5_delta_step", code)
         return o
 
@@ -459,13 +465,13 @@ def s5_rotary(x, positions, freq, layout="half", amplitude=1.0, inverse=False, o
         done = _native.marshal().rotary(x, positions, freq, _LAYOUT[layout], amplitude, int(inverse), out)
         if _taken("s5_rotary", done):
             return done
-    with _Launch(_one_device(x=x, positions=positions, freq=freq, out=out)):
+    with _Launch(stream, x=x, positions=positions, freq=freq, out=out) as on:
         T, pos, fr, rot = _rot_args(x, "x", positions, freq)
         H, D = x.shape[-2:]
         if out is None:
-            out = _new(x)
+            out = on.made(_new(x))
         code = _native.lib().s5_rotary(*_rows(x, "x", x.dtype, x.shape), _DT[x.dtype], pos, fr, rot, _LAYOUT[layout], float(amplitude),
-                                       int(inverse), T, H, D, *_rows(out, "out", x.dtype, x.shape), _on(stream, out))
+                                       int(inverse), T, H, D, *_rows(out, "out", x.dtype, x.shape), on.handle)
         check("s5_rotary", code)
         return out
 
@@ -479,21 +485,21 @@ def s5_qk_norm_rotary(q, k, positions, freq, norm="rms", eps=1e-6, q_weight=None
                                                amplitude, q_out, k_out)
         if _taken("s5_qk_norm_rotary", out):
             return out
-    with _Launch(_one_device(q=q, k=k, positions=positions, freq=freq, q_weight=q_weight, k_weight=k_weight,
-                             q_out=q_out, k_out=k_out)):
+    with _Launch(stream, q=q, k=k, positions=positions, freq=freq, q_weight=q_weight, k_weight=k_weight,
+                 q_out=q_out, k_out=k_out) as on:
         T, pos, fr, rot = _rot_args(q, "q", positions, freq)
         (Hq, D), Hk, dt, f32 = q.shape[-2:], k.shape[-2], q.dtype, torch.float32
         kshape = torch.Size((*q.shape[:-2], Hk, D))
         if q_out is None:
-            q_out = _new(q)
+            q_out = on.made(_new(q))
         if k_out is None:
-            k_out = _new(k)
+            k_out = on.made(_new(k))
         code = _native.lib().s5_qk_norm_rotary(
             *_rows(q, "q", dt, q.shape), *_rows(k, "k", dt, kshape), _DT[dt],
             None if q_weight is None else _arr(q_weight, "q_weight", f32, (D,)),
             None if k_weight is None else _arr(k_weight, "k_weight", f32, (D,)), _NORM[norm], float(eps), pos, fr, rot,
             _LAYOUT[layout], float(amplitude), T, Hq, Hk, D, *_rows(q_out, "q_out", dt, q.shape), *_rows(k_out, "k_out", dt, kshape),
-            _on(stream, q_out, k_out))
+            on.handle)
         check("s5_qk_norm_rotary", code)
         return q_out, k_out
 
@@ -507,15 +513,15 @@ def s5_qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, norm="rms"
                                                         k_weight, _LAYOUT[layout], amplitude, workspace)
         if _taken("s5_qk_norm_rotary_backward", out):
             return out
-    with _Launch(_one_device(q=q, k=k, dq_out=dq_out, dk_out=dk_out, positions=positions, freq=freq,
-                             q_weight=q_weight, k_weight=k_weight, workspace=workspace)):
+    with _Launch(stream, q=q, k=k, dq_out=dq_out, dk_out=dk_out, positions=positions, freq=freq,
+                 q_weight=q_weight, k_weight=k_weight, workspace=workspace) as on:
         T, pos, fr, rot = _rot_args(q, "q", positions, freq)
         (Hq, D), Hk, dt, f32, dev = q.shape[-2:], k.shape[-2], q.dtype, torch.float32, q.device
         kshape = (*q.shape[:-2], Hk, D)
         lib = _native.lib()
-        out = dict(dq=torch.empty(q.shape, dtype=dt, device=dev), dk=torch.empty(kshape, dtype=dt, device=dev),
-                   dwq=None if q_weight is None else torch.empty(D, dtype=f32, device=dev),
-                   dwk=None if k_weight is None else torch.empty(D, dtype=f32, device=dev))
+        e = lambda shape, t: on.made(torch.empty(shape, dtype=t, device=dev))  # noqa: E731
+        out = dict(dq=e(q.shape, dt), dk=e(kshape, dt), dwq=None if q_weight is None else e((D,), f32),
+                   dwk=None if k_weight is None else e((D,), f32))
         if workspace is None and (q_weight is not None or k_weight is not None):
             workspace = _buffer(lib.s5_qk_norm_rotary_workspace_size(D), "s5_qk_norm_rotary_backward", dev)
         code = lib.s5_qk_norm_rotary_backward(
@@ -524,7 +530,7 @@ def s5_qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, norm="rms"
             float(amplitude), T, Hq, Hk, D, *_rows(dq_out, "dq_out", dt, q.shape), *_rows(dk_out, "dk_out", dt, kshape),
             out["dq"].data_ptr(), Hq * D, out["dk"].data_ptr(), Hk * D, _ptr(out["dwq"], "dwq", None, None, True),
             _ptr(out["dwk"], "dwk", None, None, True), _ptr(workspace, "workspace", torch.uint8, None, True),
-            0 if workspace is None else workspace.numel(), _on(stream, out["dq"], workspace, *out.values()))
+            0 if workspace is None else workspace.numel(), on.handle)
         check("s5_qk_norm_rotary_backward", code)
         return out
 

@@ -1,5 +1,6 @@
-"""Host checks of which device (and stream) the mixer's calls launch on, with stand-ins for tensors of several
-GPUs and for the library: the device that is current when the library is entered has to be the tensors'."""
+"""Host checks of which device and stream the mixer's calls launch on, with stand-ins for tensors of several
+GPUs, for streams and for the library: the device that is current when the library is entered has to be the
+tensors', and what a call makes has to belong to its stream."""
 import contextlib
 
 import pytest
@@ -14,8 +15,11 @@ class OnGpu(torch.Tensor):
     @staticmethod
     def __new__(cls, shape, index, dtype=torch.float32):
         t = torch.Tensor._make_subclass(cls, torch.zeros(shape, dtype=dtype))
-        t.index = index
+        t.index, t.made_on, t.users = index, None, []
         return t
+
+    def record_stream(self, stream):
+        self.users.append(stream)
 
     is_cuda = property(lambda self: True)
     device = property(lambda self: torch.device("cuda", self.index))
@@ -26,14 +30,21 @@ class OnGpu(torch.Tensor):
             return func(*args, **(kwargs or {}))
 
 
+class Stream:
+    def __init__(self, index, handle):
+        self.device, self.cuda_stream = torch.device("cuda", index), handle
+
+
 @pytest.fixture
 def world(monkeypatch):
-    """current: the device; calls: (entry point, device current at the call)."""
+    """current: the device; stream: the stream; calls: (entry point, device current at the call); made: what calls
+    made; handles: the streams that they launched on."""
     class World:
-        current, calls = 0, []
+        pass
 
     w = World()
-    w.calls = []
+    w.current, w.calls, w.made, w.handles = 0, [], [], []
+    w.home = w.stream = Stream(0, 11)
 
     @contextlib.contextmanager
     def device(d):
@@ -47,9 +58,26 @@ def world(monkeypatch):
         def __getattr__(self, name):
             if name.endswith("_size"):
                 return lambda *a: 256
-            return lambda *a: w.calls.append((name, w.current)) or 0
+            return lambda *a: w.calls.append((name, w.current)) or w.handles.append(a[-1]) or 0
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, w.stream = w.stream, s
+        try:
+            yield
+        finally:
+            w.stream = before
+
+    def new(shape, index, dtype):
+        t = OnGpu(tuple(shape), index, dtype)
+        t.made_on = w.stream
+        w.made.append(t)
+        return t
 
     real_empty = torch.empty
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: w.stream)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: w.current)
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(_native, "lib", lambda: Lib())
@@ -59,10 +87,10 @@ def world(monkeypatch):
         shape = shape[0] if len(shape) == 1 and not isinstance(shape[0], int) else shape
         if device is None or torch.device(device).type != "cuda":
             return real_empty(shape, dtype=dtype)
-        return OnGpu(tuple(shape), torch.device(device).index, dtype)
+        return new(shape, torch.device(device).index, dtype)
 
     monkeypatch.setattr(torch, "empty", empty)
-    monkeypatch.setattr(api, "_new", lambda t: OnGpu(tuple(t.shape), t.index, t.dtype))
+    monkeypatch.setattr(api, "_new", lambda t: new(t.shape, t.index, t.dtype))
     if _native._marshal is None:
         class Native:                        # leaves every call to Python
             def __getattr__(self, name):
@@ -122,3 +150,34 @@ def test_arrays_of_two_devices_are_refused(world, name, odd):
     with pytest.raises(ValueError, match="is on cuda:"):
         calls(x)[name]()
     assert world.calls == []
+
+
+def returned(out):
+    out = list(out.values()) if isinstance(out, dict) else list(out) if isinstance(out, tuple) else [out]
+    return [t for t in out if t is not None]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_what_a_call_makes_belongs_to_its_stream(world, name):
+    x = arrays(0)
+    side = Stream(0, 22)
+    out = returned(calls(x)[name](stream=side))
+    assert world.handles == [22] and world.stream is world.home
+    assert world.made and all(t.made_on is side for t in world.made)
+    for t in world.made:                    # the caller's stream is known for what it gets, and only for that
+        assert t.users == ([world.home] if any(t is u for u in out) else [])
+    used = [t for t in x.values() if side in t.users]
+    assert used and all(t.users == [side] * len(t.users) for t in used)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_the_callers_own_stream_needs_no_records(world, name):
+    x = arrays(0)
+    calls(x)[name](stream=Stream(0, 11))
+    assert world.handles == [11] and not any(t.users for t in [*x.values(), *world.made])
+
+
+def test_a_stream_of_another_device_is_refused(world):
+    with pytest.raises(ValueError, match="the stream is on cuda:1"):
+        calls(arrays(0))["s5_rotary"](stream=Stream(1, 22))
+    assert world.calls == [] and world.current == 0
