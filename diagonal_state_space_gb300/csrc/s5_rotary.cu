@@ -445,7 +445,7 @@ __device__ int g_rotary_fault = 0;
 // limit ends the warp's work: it turns, stores and fetches nothing more
 // (copies_settle), and the host is told.
 __device__ __forceinline__ bool copy_wait(uint64_t *bar, uint32_t parity, unsigned long long limit) {
-    bool came = mbar_test_wait(bar, parity);
+    bool came = limit && mbar_test_wait(bar, parity);   // a limit of 0 gives everything up
     if (!came && limit) {
         const unsigned long long t0 = global_ns();
         while (!(came = mbar_try_wait_sleep(bar, parity, 100000)) && global_ns() - t0 < limit) {

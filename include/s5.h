@@ -465,8 +465,8 @@ s5_status s5_qk_norm_rotary(const void *q, long long ldq, const void *k, long lo
 int s5_rotary_fault(void);
 
 /* Sets the longest such wait of later calls, in ns, and returns the one before
- * (2 s at first).  0 gives up every copy that is not there at the first look:
- * what a caller does about s5_rotary_fault can be tried with it. */
+ * (2 s at first).  0 gives up every copy, there or not: what a caller does about
+ * s5_rotary_fault can be tried with it. */
 unsigned long long s5_rotary_wait_limit(unsigned long long ns);
 
 /* Workspace of the backward pass, needed where a weight's gradient is wanted. */

@@ -1,6 +1,6 @@
 """GPU tests of waits that run out inside the streaming rotation: with a limit of
-0 ns a copy that is not there at the first look is given up.  The kernel ends,
-stores nothing of what did not come, and says so; the next call is whole."""
+0 ns every copy is given up, still in flight or not.  The kernel ends, stores
+nothing of what did not come, and says so; the next call is whole."""
 import time
 
 import pytest
