@@ -9,6 +9,7 @@ is given.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -442,6 +443,25 @@ def s5_delta_step(q, k, v, g, beta, state, scale=None, o=None, stream=None):
         return o
 
 
+def _fault(fn, device):
+    with contextlib.nullcontext() if device is None else torch.cuda.device(device):
+        code = getattr(_native.lib(), fn)()
+    if code < 0:
+        raise S5Error(fn, 3, "the flag could not be read")
+    return code != 0
+
+
+def s5_delta_fault(device=None) -> bool:
+    """Whether a wait inside s5_delta_forward or s5_delta_backward has run out on the device (the current one) since
+    this was last asked: what those calls gave is then not valid.  Waits for the device."""
+    return _fault("s5_delta_fault", device)
+
+
+def s5_rotary_fault(device=None) -> bool:
+    """The same for s5_rotary, s5_qk_norm_rotary and s5_qk_norm_rotary_backward."""
+    return _fault("s5_rotary_fault", device)
+
+
 _LAYOUT = {"half": 0, "interleaved": 1}
 _NORM = {None: 0, "none": 0, "rms": 1, "l2": 2}
 
@@ -539,5 +559,5 @@ __all__ = ["s5_discretize", "s5_discretize_ex", "s5_forward", "s5_forward_varyin
            "s5_forward_bidirectional", "s5_step", "s5_forward_noalloc", "s5_workspace_size",
            "s5_bidirectional_workspace_size", "s5_sync_status", "new_workspace",
            "s5_delta_forward", "s5_delta_backward", "s5_delta_step", "s5_delta_saved_size",
-           "s5_delta_workspace_size", "new_delta_saved", "s5_rotary", "s5_qk_norm_rotary",
-           "s5_qk_norm_rotary_backward", "S5Error", "S5_F32", "S5_BF16"]
+           "s5_delta_workspace_size", "s5_delta_fault", "new_delta_saved", "s5_rotary", "s5_qk_norm_rotary",
+           "s5_qk_norm_rotary_backward", "s5_rotary_fault", "S5Error", "S5_F32", "S5_BF16"]

@@ -80,6 +80,12 @@ class DeltaMixer:
         return dict(w_in=dp.flatten(0, 1).t() @ x.flatten(0, 1), w_out=dw_out, log_a=(d["dg"] * kept["g"]).sum((0, 1)))
 
 
+def finished():
+    """Raises if a wait inside the mixer's kernels ran out: their results are then not valid."""
+    if api.s5_delta_fault() or api.s5_rotary_fault():
+        raise RuntimeError("a wait inside a mixer kernel ran out")
+
+
 def prompt_and_stream(B=2, L=200, H=256, tokens=8, seed=1):
     """Largest difference of streamed outputs from those of one call over all
     tokens, over the outputs' size."""
@@ -89,6 +95,7 @@ def prompt_and_stream(B=2, L=200, H=256, tokens=8, seed=1):
     y, state = m.forward(x[:, :L])
     got = [m.step(x[:, L + i], state, L + i) for i in range(tokens)]
     got = torch.cat([y] + [u[:, None] for u in got], 1)
+    finished()
     return float((got - want).norm() / want.norm())
 
 
@@ -108,6 +115,7 @@ def train(steps=60, B=2, L=128, H=64, lag=1, rate=3e-3, seed=2):
             a.lerp_(grads[name], 0.1)
             b.lerp_(grads[name].square(), 0.01)
             p -= rate * (a / (1 - 0.9 ** i)) / ((b / (1 - 0.99 ** i)).sqrt() + 1e-8)
+    finished()
     return losses
 
 
