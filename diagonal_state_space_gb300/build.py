@@ -1,5 +1,6 @@
 """Builds libs5.so in-tree with nvcc for sm_103a (one -gencode, no cmake), and
-the binding's native half with g++ against the installed torch.
+the binding's native half with g++ against the installed torch (where there is
+one: the library needs nvcc alone).
 
 Translation units compile in parallel into ``_build/`` at the repository root
 and link into ``diagonal_state_space_gb300/libs5.so`` and ``_marshal.so``.
@@ -54,6 +55,15 @@ def _run(cmd, what):
         raise RuntimeError("%s failed:\n%s%s" % (what, res.stdout, res.stderr))
 
 
+def _has_torch() -> bool:
+    """Whether there is a torch with CUDA to build the binding for; the library itself is for C callers too."""
+    try:
+        import torch
+    except ImportError:
+        return False
+    return torch.version.cuda is not None
+
+
 def _marshal_object(force: bool) -> str:
     """csrc/marshal.cpp for the torch that is installed (its version is part of the object's name)."""
     import torch
@@ -97,9 +107,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        marshal = ex.submit(_marshal_object, force)
+        marshal = ex.submit(_marshal_object, force) if _has_torch() else None
         list(ex.map(compile_one, zip(srcs, objs)))
-        marshal = marshal.result()
+        _link_library(nvcc, objs, force)     # needs nothing of torch: it is there whatever becomes of the binding
+        marshal = marshal and marshal.result()
+    if marshal and (force or _stale(MARSHAL, [marshal])):
+        _link_marshal(marshal)
+    return LIB
+
+
+def _link_library(nvcc: str, objs: list[str], force: bool) -> None:
     if force or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-cudart", "static",
@@ -108,9 +125,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError("link failed:\n%s%s" % (res.stdout, res.stderr))
         os.replace(tmp, LIB)
-    if force or _stale(MARSHAL, [marshal]):
-        _link_marshal(marshal)
-    return LIB
 
 
 if __name__ == "__main__":
