@@ -64,17 +64,33 @@ def _has_torch() -> bool:
     return torch.version.cuda is not None
 
 
+def _binary_interface() -> str:
+    """What the binding's compiled half depends on: torch, Python and the C++ library's interface."""
+    import torch
+    return "%s-%s-abi%d" % (torch.__version__, sysconfig.get_config_var("SOABI"), torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
 def _marshal_object(force: bool) -> str:
-    """csrc/marshal.cpp for the torch that is installed (its version is part of the object's name)."""
+    """csrc/marshal.cpp for the torch and the Python that are installed (part of the object's name)."""
     import torch
     src = os.path.join(CSRC, "marshal.cpp")
-    obj = os.path.join(OBJ, "marshal-%s.o" % torch.__version__)
+    obj = os.path.join(OBJ, "marshal-%s.o" % _binary_interface())
     if force or _stale(obj, [src, os.path.join(ROOT, "include", "s5.h")]):
         cuda = os.path.dirname(os.path.dirname(_nvcc()))
-        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include"),
+        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC",
+              "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", os.path.join(ROOT, "include"),
               "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(torch.__file__), "include"),
               "-I", os.path.join(cuda, "include"), "-c", src, "-o", obj], "g++ for %s" % src)
     return obj
+
+
+def _linked_from(obj: str) -> bool:
+    """Whether _marshal.so comes from this object: a later object of another torch says nothing about it."""
+    try:
+        with open(os.path.join(OBJ, "marshal.linked")) as f:
+            return f.read() == os.path.basename(obj) and not _stale(MARSHAL, [obj])
+    except OSError:
+        return False
 
 
 def _link_marshal(obj: str) -> None:
@@ -83,6 +99,8 @@ def _link_marshal(obj: str) -> None:
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", PKG, "-ls5", "-Wl,-rpath,$ORIGIN"], "link of _marshal.so")
     os.replace(tmp, MARSHAL)
+    with open(os.path.join(OBJ, "marshal.linked"), "w") as f:
+        f.write(os.path.basename(obj))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -111,7 +129,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         list(ex.map(compile_one, zip(srcs, objs)))
         _link_library(nvcc, objs, force)     # needs nothing of torch: it is there whatever becomes of the binding
         marshal = marshal and marshal.result()
-    if marshal and (force or _stale(MARSHAL, [marshal])):
+    if marshal and (force or not _linked_from(marshal)):
         _link_marshal(marshal)
     return LIB
 

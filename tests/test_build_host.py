@@ -54,3 +54,25 @@ def test_a_torch_without_cuda_gets_no_binding(monkeypatch):
     assert not build._has_torch()
     monkeypatch.setitem(__import__("sys").modules, "torch", None)
     assert not build._has_torch()
+
+
+def links(tools):
+    return [out for tool, out in tools.runs if tool == "g++" and out.startswith("_marshal.so")]
+
+
+@pytest.mark.parametrize("what", ["torch", "python", "abi"])
+def test_the_binding_is_linked_again_when_what_it_was_made_for_comes_back(tools, monkeypatch, what):
+    def become(which):
+        if what == "torch":
+            monkeypatch.setattr(torch, "__version__", which)
+        elif what == "python":
+            monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: which)
+        else:
+            monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", which == "a")
+
+    for n, which in enumerate("aba", 1):
+        become(which)
+        build.build()
+        assert len(links(tools)) == n
+        build.build()
+        assert len(links(tools)) == n        # nothing has changed
