@@ -278,7 +278,8 @@ def _rows(t, name, dtype=None, shape=None):
     return t.data_ptr(), H * D if pitch is None else pitch
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream    # current_stream() builds an object: 8 us of a call
+# current_stream() builds an object: 8 us of a call.  A torch without CUDA lacks it, and has no tensor to need it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class _Launch:
