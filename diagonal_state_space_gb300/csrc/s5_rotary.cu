@@ -135,15 +135,21 @@ __device__ __forceinline__ void slot_place(int slot, int n, int &lo, int &hi) {
     }
 }
 
-// cos and sin of the slot's V pairs (identity past the rotated part).
+// The slot's frequencies.  rotated: 0 past the rotated part, else bit 0, and
+// bit 1 + i where pair i's frequency is not finite, whose values are NaN then.
 template <int V, bool INTER>
-__device__ __forceinline__ void slot_freq(const RotArgs &a, int slot, unsigned long long (&f)[V], bool &rotated) {
+__device__ __forceinline__ void slot_freq(const RotArgs &a, int slot, unsigned long long (&f)[V], unsigned &rotated) {
     rotated = slot * V < a.rot / 2;
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = rotated ? turns64(a.freq[slot * V + i]) : 0ull;
+    for (int i = 0; i < V; ++i) {
+        const double x = rotated ? a.freq[slot * V + i] : 0.0;
+        f[i] = turns64(x);
+        if (!isfinite(x)) rotated |= 2u << i;
+    }
 }
+// cos and sin of the slot's V pairs (identity past the rotated part).
 template <int V>
-__device__ __forceinline__ void slot_angles(const RotArgs &a, const unsigned long long (&f)[V], bool rotated,
+__device__ __forceinline__ void slot_angles(const RotArgs &a, const unsigned long long (&f)[V], unsigned rotated,
                                             long long pos, float (&c)[V], float (&s)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -157,6 +163,10 @@ __device__ __forceinline__ void slot_angles(const RotArgs &a, const unsigned lon
             s[i] = 0.0f;
         }
     }
+    if (rotated > 1u)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (rotated >> (i + 1) & 1u) c[i] = s[i] = __int_as_float(0x7fffffff);
 }
 
 // Pair i of the slot: (lo[i], hi[i]) in the half layout; neighbours in the
@@ -231,11 +241,11 @@ __global__ void __launch_bounds__(RT) rotary_fwd_kernel(const RotArgs a) {
                 u[r][j] = t[r][j] = typename X::raw{};
     const long long pos = (live && n) ? a.pos[token] : 0;
     float c[S][V], s[S][V];
-    bool rotated[S];
+    unsigned rotated[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
         unsigned long long f[V];
-        rotated[j] = false;
+        rotated[j] = 0;
         if (lo[j] >= 0) slot_freq<V, INTER>(a, lane + j * G, f, rotated[j]);
         slot_angles<V>(a, f, rotated[j], pos, c[j], s[j]);
     }
@@ -295,7 +305,7 @@ __global__ void __launch_bounds__(RT) rotary_bwd_kernel(const RotArgs a, int qbl
     T *yb = static_cast<T *>(part ? a.y[1] : a.y[0]);
     using X = Vec<T, V>;
     unsigned long long f[S][V];
-    bool rotated[S];
+    unsigned rotated[S];
     int lo[S], hi[S];
     float wl[S][V], wh[S][V], dl[S][V], dh[S][V];
     griddep_wait();
@@ -303,7 +313,7 @@ __global__ void __launch_bounds__(RT) rotary_bwd_kernel(const RotArgs a, int qbl
     for (int j = 0; j < S; ++j) {
         const int slot = lane + j * G;
         slot_place<V, INTER>(slot, n, lo[j], hi[j]);
-        rotated[j] = false;
+        rotated[j] = 0;
         if (slot >= nslots)
             lo[j] = -1;
         else
@@ -538,7 +548,7 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_fwd_kernel(const
     griddep_launch_dependents();
     griddep_wait();
     unsigned long long f[V];
-    bool rotated = false;
+    unsigned rotated = 0;
     if (in) slot_freq<V, INTER>(a, slot, f, rotated);
     const uint64_t policy = l2_policy(a.inv != 0.0f);
     Deal deal(a, 0, segs, blockIdx.x * SWARPS + warp, (long long)gridDim.x * SWARPS), ahead = deal;
@@ -648,7 +658,7 @@ __global__ void __launch_bounds__(SWARPS * 32, 2) rotary_stream_bwd_kernel(const
     const bool in = slot < a.D / (2 * V);
     griddep_wait();
     unsigned long long f[V];
-    bool rotated = false;
+    unsigned rotated = 0;
     if (in) slot_freq<V, INTER>(a, slot, f, rotated);
     float wl[V], wh[V], dl[V] = {}, dh[V] = {};
 #pragma unroll

@@ -1,0 +1,37 @@
+"""GPU test of broken frequency tables: what is not finite shows in its pair, and in no other."""
+import numpy as np
+import pytest
+import torch
+
+from diagonal_state_space_gb300 import api, init
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("L,D,rot", [(5, 128, 64), (5, 18, 6), (5, 20, 20), (12000, 128, 64)])
+def test_a_frequency_that_is_not_finite_makes_its_pair_nan(L, D, rot, layout):
+    n = rot // 2
+    freq = init.rotary_frequencies(rot)[0]
+    bad = freq.copy()
+    broken = [0, n - 1] if n < 4 else [1, 2, n - 1]
+    bad[broken] = [np.nan, -np.inf, np.inf][:len(broken)]
+    x = torch.randn(1, L, 3, D, device="cuda")
+    pos = torch.arange(L, device="cuda")[None]
+    good_t, bad_t = torch.from_numpy(freq).cuda(), torch.from_numpy(bad).cuda()
+    mask = torch.zeros(D, dtype=torch.bool, device="cuda")
+    for i in broken:
+        mask[[i, i + n] if layout == "half" else [2 * i, 2 * i + 1]] = True
+    for call in (lambda f: api.s5_rotary(x, pos, f, layout=layout), lambda f: api.s5_rotary(x, pos, f, layout=layout, inverse=True),
+                 lambda f: api.s5_qk_norm_rotary(x, x, pos, f, layout=layout)[1]):
+        want, got = call(good_t), call(bad_t)
+        assert torch.isnan(got[..., mask]).all()
+        assert torch.equal(got[..., ~mask], want[..., ~mask])
+    g = api.s5_qk_norm_rotary_backward(x, x, x, x, pos, bad_t, norm=None, layout=layout)["dq"]
+    assert torch.isnan(g[..., mask]).all() and torch.isfinite(g[..., ~mask]).all()
