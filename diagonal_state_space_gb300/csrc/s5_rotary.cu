@@ -15,7 +15,8 @@
 // frequency is turned once per thread into a 64-bit fraction of a turn,
 // f / 2 pi * 2^64, by integer arithmetic (FP64 runs at 1/64 of the FP32 rate
 // here); p times it wraps exactly at whole turns, and the top 32 bits give
-// sincospif an argument good to 2^-25 half turns at any p.
+// sincospif an argument good to 2^-25 half turns.  The fraction itself is off by up
+// to max(1, f) 2^-63 turns, p times that at position p.
 //
 // Bound: memory.  A row is read and written once.  Two forms:
 //  - Streaming, for rows that 16-byte copies can address: every warp runs a

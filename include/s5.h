@@ -434,9 +434,9 @@ s5_status s5_delta_step(const void *q, const void *k, const void *v, s5_dtype dt
  *   y_a = A (cos z_a - sin z_b),  y_b = A (sin z_a + cos z_b),  z = x r w,
  *   r = 1, 1/sqrt(mean x^2 + eps) or 1/sqrt(sum x^2 + eps) by `norm`,
  *   w [D] float32, or ones (NULL).
- * Angles are taken modulo whole turns in 64-bit fixed point, so that any
- * position below 2^63 keeps its phase as far as freq (float64) defines it.  A
- * pair whose frequency is NaN or infinite becomes NaN.
+ * Angles are taken modulo whole turns in 64-bit fixed point: at position p one is
+ * off by at most |p| max(1, |freq|) 2^-63 turns (2^-23 at 2^40) beside the 2^-26
+ * of its sine and cosine.  A pair whose frequency is NaN or infinite becomes NaN.
  * Rows: [T][H][D] of `dtype` with a pitch in elements between two tokens; an
  * output may be its input (same pitch).  positions [T], freq [rot/2] on the
  * device; rot = 0 needs neither.  D even, up to 256 (S5_ERR_UNSUPPORTED

@@ -35,3 +35,21 @@ def test_a_frequency_that_is_not_finite_makes_its_pair_nan(L, D, rot, layout):
         assert torch.equal(got[..., ~mask], want[..., ~mask])
     g = api.s5_qk_norm_rotary_backward(x, x, x, x, pos, bad_t, norm=None, layout=layout)["dq"]
     assert torch.isnan(g[..., mask]).all() and torch.isfinite(g[..., ~mask]).all()
+
+
+@pytest.mark.parametrize("start", [1 << 44, 1 << 50, (1 << 52) + 3])
+def test_phases_at_far_positions_are_as_good_as_stated(start):
+    """|p| max(1, |freq|) 2^-63 turns, and the 16 roundings of 2^-24 of test_gpu_rotary.py; the angles from exact
+    integer products.  A pair's values are off by at most its length times the angle's error."""
+    from fractions import Fraction
+    two_pi = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)
+    freq = np.array([1.0, 0.37, 1e-3, 3e-5, 7e-9, 30.0, -2.5, 1000.0])
+    n, pos = len(freq), torch.arange(6, device="cuda") + start
+    x = torch.randn(6, 2, 2 * n, device="cuda")
+    vx = x.double().cpu().numpy()
+    turns = np.array([[float((Fraction(int(p)) * Fraction(float(f)) / two_pi) % 1) for f in freq] for p in pos.tolist()])
+    c = (vx[..., :n] + 1j * vx[..., n:]) * np.exp(2j * np.pi * turns)[:, None, :]
+    y = api.s5_rotary(x, pos, torch.from_numpy(freq).cuda()).double().cpu().numpy()
+    off = np.abs(y[..., :n] + 1j * y[..., n:] - c) / np.abs(c)
+    bound = 2 * np.pi * (start + 6) * np.maximum(1, np.abs(freq)) * 2.0 ** -63 + 16 * 2.0 ** -24
+    assert (off <= bound).all(), off.max((0, 1)) / bound
