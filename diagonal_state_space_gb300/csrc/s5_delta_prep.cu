@@ -13,9 +13,8 @@
 // the diagonal by substitution, one column per lane, then
 //   [[A, 0], [B, D]]^-1 = [[A^-1, 0], [-D^-1 B A^-1, D^-1]]
 // to 32 and to 64 rows.  P E is a tcgen05 product of the image's own parts:
-// [E; P] E, of which the rows of P E are kept.  In a forward image that only
-// makes o (bf16) 17 bits (without the third parts) do; all 24 are taken where o is kept
-// in 32 bits or X hangs on it.
+// [E; P] E, of which the rows of P E are kept, in 24 bits: o is the same
+// whether the call keeps anything for a backward pass or not.
 // In the image 16 rows of E and 16 of P E take turns; it is built in shared
 // memory in the layout that the recurrences' products read and leaves by one
 // bulk copy.
@@ -147,7 +146,6 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
     const uint32_t tmem = pb->tmem, frag = tmem + ((uint32_t)(32 * q) << 16) + c0;
     const uint64_t rows = desc_k(img), cols = desc_mn(img, M2_BYTES);
     const uint32_t n1 = idesc_bf16_f32(128, 64), n2 = idesc_bf16_f32(128, 128);
-    const bool whole = TRANS || a.states;   // P E in 24 bits
     bool ok = true;
     if (tid == 0) {
         if (wait(&pb->tiles, 0)) {
@@ -324,10 +322,8 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
                 const uint64_t P = on(rows, k * K_STEP), E = on(cols, 2 * k * KQ_GROUP);
                 mma_bf16(tmem, on(P, M2_BYTES), E, n2 | B_MN, k > 0);
                 mma_bf16(tmem, P, E, n2 | B_MN, 1);
-                if (whole) {
-                    mma_bf16(tmem, on(P, 2 * M2_BYTES), E, n1 | B_MN, 1);
-                    mma_bf16(tmem, P, on(E, 2 * M2_BYTES), n1 | B_MN, 1);
-                }
+                mma_bf16(tmem, on(P, 2 * M2_BYTES), E, n1 | B_MN, 1);
+                mma_bf16(tmem, P, on(E, 2 * M2_BYTES), n1 | B_MN, 1);
             }
             mma_commit(&pb->done);
         }
