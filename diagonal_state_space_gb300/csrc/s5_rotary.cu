@@ -456,7 +456,7 @@ __device__ int g_rotary_fault = 0;
 // limit ends the warp's work: it turns, stores and fetches nothing more
 // (copies_settle), and the host is told.
 __device__ __forceinline__ bool copy_wait(uint64_t *bar, uint32_t parity, unsigned long long limit) {
-    bool came = limit && mbar_test_wait(bar, parity);   // a limit of 0 gives everything up
+    bool came = limit && mbar_try_wait(bar, parity);   // a limit of 0 gives everything up
     if (!came && limit) {
         const unsigned long long t0 = global_ns();
         while (!(came = mbar_try_wait_sleep(bar, parity, 100000)) && global_ns() - t0 < limit) {
@@ -468,7 +468,7 @@ __device__ __forceinline__ bool copy_wait(uint64_t *bar, uint32_t parity, unsign
 }
 // After a wait that ran out: what the warp has armed, `count` stages from `st`
 // on, lands (or 0.2 s pass) before the block gives its memory back.
-__device__ __forceinline__ void copies_settle(uint64_t *full, int st, uint32_t parity, int count) {
+__device__ __noinline__ void copies_settle(uint64_t *full, int st, uint32_t parity, int count) {
     const unsigned long long t0 = global_ns();
     for (; count > 0; --count) {
         while (!mbar_try_wait_sleep(full + st, parity, 100000) && global_ns() - t0 < 200000000ull) {
