@@ -18,10 +18,19 @@
 // once from the kept states and adjoints.  All sums are inside 8 or 16 lanes, no
 // atomics, one order of addition.
 //
-// The decay's gradient dg_t = <a_t S_{t-1}, Z_t - k_t dv_t^T> needs no sweep:
-//   dg_t - dg_{t+1} = o_t . do_t - v_t . dv_t,
-// (insert the recurrences), anchored at every 64th token by <S_c, Z_c> of the
-// kept states, so that at most 64 terms are added in a row.
+// The decay's gradient dg_t = <a_t S_{t-1}, Z_t - k_t dv_t^T> is the sum of all
+// that crosses token t, from writes before it (or the state S of the chunk's start)
+// to reads at or after it (or the adjoint Z of the chunk's end).  With G_i the sum
+// of the chunk's log decays up to i and D_ij = exp(G_i - G_j),
+//   dg_t = sum over j < t <= i of M_ij + sum over i >= t of a_i
+//          + sum over j < t of b_j + e^{G_64} <S, Z>,
+//   M_ij = D_ij (scale (q_i.k_j) (do_i.u_j) - (k_i.k_j) (dv_i.u_j)),
+//   a_i = e^{G_i} (scale (S^T q_i).do_i - (S^T k_i).dv_i),
+//   b_j = e^{G_64 - G_j} (Z^T k_j).u_j
+// (decay_grads_kernel).  Every term carries its own decay and nothing is
+// subtracted, so that the gradient of a gate that is all but shut keeps its digits;
+// dg_t - dg_{t+1} = o_t.do_t - v_t.dv_t, which costs nothing, would leave 2^-24 of
+// o.do in it.
 //
 // Bound: the chain of a token in the column sweeps (product, sum over 8 lanes,
 // update); the state stays in registers, two warps of a block bring the next
@@ -82,7 +91,7 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
     constexpr int COLT = 8 * C;
     constexpr int NT = RPT > 16 ? TB / 2 : TB, D = 8 * RPT;
     __shared__ __align__(16) float sq[2][NT][D], sk[2][NT][D];
-    __shared__ float sv[2][NT][C], sa[2][NT], sb[2][NT], red[COLT / 32];
+    __shared__ float sv[2][NT][C], sa[2][NT], sb[2][NT];
     const int lane = threadIdx.x / 4 % 8, own = threadIdx.x / 32 * 4 + threadIdx.x % 4;   // row lane, column
     const bool loads = threadIdx.x >= COLT;
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
@@ -104,25 +113,6 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
             const int r = 32 * (i / 4) + 4 * lane + i % 4;
             if (on && r < a.Dk) to[(long long)r * a.Dv + col] = S[i];
         }
-    };
-    // <S_c, Z_c> of this block's columns (the compute warps)
-    auto inner = [&](int c) {
-        const float *s = a.states + (bh * (N + 1) + c) * mat;
-        float w = 0.0f;
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            const int r = 32 * (i / 4) + 4 * lane + i % 4;
-            if (on && r < a.Dk) w = fmaf(s[(long long)r * a.Dv + col], S[i], w);
-        }
-        for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
-        if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = w;
-        asm volatile("bar.sync 1, %0;" ::"n"(COLT) : "memory");
-        if (threadIdx.x == 0) {
-            w = 0.0f;
-            for (int i = 0; i < COLT / 32; ++i) w += red[i];
-            a.inner[(bh * (N + 1) + c) * a.parts + blockIdx.x] = w;
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(COLT) : "memory");
     };
     const int stages = (a.L + NT - 1) / NT;
     // Staging by 64 threads, a column of values each: `fetch` has all of a
@@ -163,7 +153,6 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
         for (int i = 0; i < NT / TS; ++i) sv[buf][TS * i + first_t][own_v] = fv[i];
         if (tid < NT) sa[buf][tid] = expf(clamp_g(fg)), sb[buf][tid] = fb;
     };
-    if (REV && !loads) inner(N);
     if (loads && stages > 0) {
         fetch(0), put(0);
         if (stages > 1) fetch(1);
@@ -240,7 +229,6 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
                 }
             }
         }
-        if (REV && t0 % CHUNK == 0) inner(t0 / CHUNK);
         __syncthreads();
     }
     if (loads) return;
@@ -382,7 +370,7 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// One warp per token and value head: dv = beta X, dbeta = X . e, o . do - v . dv.
+// One warp per token and value head: dv = beta X, dbeta = X . e.
 template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(const Args a) {
     griddep_wait();
     const long long hv = (long long)blockIdx.x * 8 + threadIdx.x / 32, rows = (long long)a.B * a.L * a.Hv;
@@ -391,22 +379,19 @@ template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(
     const long long row = hv / a.Hv;
     const int h = (int)(hv % a.Hv);
     const float be = a.beta[hv];
-    float db = 0.0f, w = 0.0f;
+    float db = 0.0f;
     for (int c = lane; c < a.Dv; c += 32) {
-        const float x = a.x[hv * a.Dv + c], dv = be * x;
-        const float v = elem<T>(a.v, row * a.ldv + (long long)h * a.Dv + c);
-        const float d = elem<T>(a.dout, row * a.lddo + (long long)h * a.Dv + c);
+        const float x = a.x[hv * a.Dv + c];
         db = fmaf(x, a.e[hv * a.Dv + c], db);
-        w = fmaf(a.o32[hv * a.Dv + c], d, fmaf(-v, dv, w));
-        store_elem<T>(static_cast<T *>(a.dv) + row * a.lddv + (long long)h * a.Dv + c, dv);
+        store_elem<T>(static_cast<T *>(a.dv) + row * a.lddv + (long long)h * a.Dv + c, be * x);
     }
-    db = warp_sum(db), w = warp_sum(w);
-    if (lane == 0) a.dbeta[hv] = db, a.dots[hv] = w;
+    db = warp_sum(db);
+    if (lane == 0) a.dbeta[hv] = db;
 }
 
 // One warp per chunk and value head: dg by adding the chunk's terms from its
 // end on top of <S, Z> there.  A token whose decay is zero has no gradient.
-__global__ void __launch_bounds__(256) decay_grads_kernel(const Args a) {
+__global__ void __launch_bounds__(256) decay_chain_kernel(const Args a) {
     griddep_wait();
     const int N = chunks(a.L), lane = threadIdx.x % 32;
     const long long id = (long long)blockIdx.x * 8 + threadIdx.x / 32;
@@ -429,6 +414,193 @@ __global__ void __launch_bounds__(256) decay_grads_kernel(const Args a) {
         }
         if (t < a.L) a.dg[hv] = expf(clamp_g(a.g[hv])) == 0.0f ? 0.0f : s + w;
         s += __shfl_sync(0xffffffffu, w, 31);
+    }
+}
+
+// dg of a chunk and value head (the formula is at the top of this file).  Half of
+// a block forms M, the other half a, b and <S, Z>, both as products of 64 x 64 tiles
+// (four rows and columns a thread, slices of 16 of the depth staged in shared
+// memory, the next slice on its way); M's rows are then summed along j, its
+// columns along i, both from nothing, so that no term is taken away again.  Bound by
+// the products, in 32 bits on the CUDA cores as all of this path.
+constexpr int GT = 512, GS = 16, GP = 68;
+template <typename T> __global__ void __launch_bounds__(GT) decay_grads_kernel(const Args a) {
+    __shared__ __align__(16) float tiles[2][4][GS][GP];
+    __shared__ float hi[CHUNK], lo[CHUNK], av[CHUNK], bv[CHUNK], mv[GT / 64];
+    constexpr int MP = CHUNK + 1;
+    float *M = &tiles[0][0][0][0];   // [64][MP], in the place of the first half's tiles
+    static_assert(CHUNK * MP <= 4 * GS * GP, "M fits");
+    const int c = blockIdx.x, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
+    const int half = threadIdx.x / 256, tid = threadIdx.x % 256, ti = tid / 16 * 4, tj = tid % 16 * 4;
+    const int N = chunks(a.L), t0 = c * CHUNK, nt = min(CHUNK, a.L - t0);
+    const long long row0 = (long long)b * a.L + t0, bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
+    auto(&st)[4][GS][GP] = tiles[half];
+    auto meet = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + half) : "memory"); };
+    griddep_wait();
+    if (threadIdx.x < 32) {
+        float G[2], g[2];
+        decay_sums(a, row0, nt, h, threadIdx.x, G, g);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) hi[2 * threadIdx.x + i] = G[i], lo[2 * threadIdx.x + i] = g[i];
+    }
+    __syncthreads();
+    // values of token t: keys, queries; dL/do; u and dv
+    auto key = [&](int t, int d) { return t < nt && d < a.Dk ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + d) : 0.0f; };
+    auto query = [&](int t, int d) { return t < nt && d < a.Dk ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + d) : 0.0f; };
+    auto dout = [&](int t, int d) { return t < nt && d < a.Dv ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + d) : 0.0f; };
+    auto beta = [&](int t) { return t < nt ? a.beta[(row0 + t) * a.Hv + h] : 0.0f; };
+    auto write = [&](int t, int d) { return t < nt && d < a.Dv ? a.e[((row0 + t) * a.Hv + h) * a.Dv + d] : 0.0f; };
+    auto adjoint = [&](int t, int d) { return t < nt && d < a.Dv ? a.x[((row0 + t) * a.Hv + h) * a.Dv + d] : 0.0f; };
+    // a slice of 64 tokens x 16 values: thread's token of piece n, and its value
+    const int own_d = tid % GS;
+    auto own_t = [&](int n) { return tid / GS + 16 * n; };
+    auto row4 = [&](int j, int d, int at, float (&r)[4]) {
+        const float4 v = *reinterpret_cast<const float4 *>(&st[j][d][at]);
+        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    };
+    if (half == 0) {
+        float kk[4][4] = {}, qk[4][4] = {}, du[4][4] = {}, ou[4][4] = {};
+        float x[3][4];
+        // first all products along the keys, then all along the values
+        const int ks = (a.Dk + GS - 1) / GS, all = ks + (a.Dv + GS - 1) / GS;
+        auto fetch = [&](int s) {
+            const int d = (s < ks ? s : s - ks) * GS + own_d;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int t = own_t(n);
+                if (s < ks)
+                    x[0][n] = key(t, d), x[1][n] = query(t, d);
+                else
+                    x[0][n] = beta(t) * adjoint(t, d), x[1][n] = dout(t, d), x[2][n] = beta(t) * write(t, d);
+            }
+        };
+        fetch(0);
+        for (int s = 0; s < all; ++s) {
+            meet();
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                st[0][own_d][own_t(n)] = x[0][n], st[1][own_d][own_t(n)] = x[1][n];
+                st[2][own_d][own_t(n)] = s < ks ? x[0][n] : x[2][n];
+            }
+            meet();
+            if (s + 1 < all) fetch(s + 1);
+            auto add = [&](float (&p)[4][4], float (&r)[4][4]) {
+#pragma unroll 4
+                for (int d = 0; d < GS; ++d) {
+                    float u[4], v[4], w[4];
+                    row4(0, d, ti, u), row4(1, d, ti, v), row4(2, d, tj, w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) p[i][j] = fmaf(u[i], w[j], p[i][j]), r[i][j] = fmaf(v[i], w[j], r[i][j]);
+                }
+            };
+            if (s < ks)
+                add(kk, qk);
+            else
+                add(du, ou);
+        }
+        meet();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = ti + i, q = tj + j;
+                const float d = expf((hi[r] - hi[q]) + (lo[r] - lo[q]));
+                M[r * MP + q] = q < r ? d * (a.scale * qk[i][j] * ou[i][j] - kk[i][j] * du[i][j]) : 0.0f;
+            }
+        meet();
+        // M_it becomes the sum of M_ij over j < t, a row a thread
+        if (tid < CHUNK) {
+            float w = 0.0f;
+#pragma unroll 8
+            for (int j = 0; j < CHUNK; ++j) {
+                const float v = M[tid * MP + j];
+                M[tid * MP + j] = w;
+                w += v;
+            }
+        }
+    } else {
+        float x[4][4], m = 0.0f, aw[4] = {}, bw[4] = {};
+        const float *S = a.states + (bh * (N + 1) + c) * mat, *Z = static_cast<const float *>(a.z) + (bh * N + c) * mat;
+        const int ks = (a.Dk + GS - 1) / GS, vs = (a.Dv + 63) / 64;
+        // depth along the keys; columns 64 of the values at a time
+        auto fetch = [&](int s) {
+            const int d = s % ks * GS + own_d;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                x[0][n] = key(own_t(n), d), x[1][n] = query(own_t(n), d);
+                const int r = s % ks * GS + tid / 64 + 4 * n, v = s / ks * 64 + tid % 64;
+                const bool in = r < a.Dk && v < a.Dv;
+                x[2][n] = in ? S[(long long)r * a.Dv + v] : 0.0f, x[3][n] = in ? Z[(long long)r * a.Dv + v] : 0.0f;
+            }
+        };
+        float ks4[4][4], qs4[4][4], kz4[4][4];
+        fetch(0);
+        for (int s = 0; s < ks * vs; ++s) {
+            if (s % ks == 0)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ks4[i / 4][i % 4] = qs4[i / 4][i % 4] = kz4[i / 4][i % 4] = 0.0f;
+            meet();
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                st[0][own_d][own_t(n)] = x[0][n], st[1][own_d][own_t(n)] = x[1][n];
+                st[2][tid / 64 + 4 * n][tid % 64] = x[2][n], st[3][tid / 64 + 4 * n][tid % 64] = x[3][n];
+                m = fmaf(x[2][n], x[3][n], m);
+            }
+            meet();
+            if (s + 1 < ks * vs) fetch(s + 1);
+#pragma unroll 4
+            for (int d = 0; d < GS; ++d) {
+                float u[4], v[4], y[4], z[4];
+                row4(0, d, ti, u), row4(1, d, ti, v), row4(2, d, tj, y), row4(3, d, tj, z);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        ks4[i][j] = fmaf(u[i], y[j], ks4[i][j]), qs4[i][j] = fmaf(v[i], y[j], qs4[i][j]);
+                        kz4[i][j] = fmaf(u[i], z[j], kz4[i][j]);
+                    }
+            }
+            if (s % ks == ks - 1) {
+                const int v0 = s / ks * 64 + tj;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float be = beta(ti + i);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        aw[i] = fmaf(a.scale * qs4[i][j], dout(ti + i, v0 + j), aw[i]);
+                        aw[i] = fmaf(-ks4[i][j], be * adjoint(ti + i, v0 + j), aw[i]);
+                        bw[i] = fmaf(kz4[i][j], be * write(ti + i, v0 + j), bw[i]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int w = 1; w < 16; w <<= 1) {
+                aw[i] += __shfl_xor_sync(0xffffffffu, aw[i], w);
+                bw[i] += __shfl_xor_sync(0xffffffffu, bw[i], w);
+            }
+            if (tid % 16 == 0) {
+                const int r = ti + i;
+                av[r] = expf(hi[r]) * aw[i];
+                bv[r] = expf((hi[CHUNK - 1] - hi[r]) + (lo[CHUNK - 1] - lo[r])) * bw[i];
+            }
+        }
+        m = warp_sum(m);
+        if (tid % 32 == 0) mv[tid / 32] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x < nt) {
+        const int t = threadIdx.x;
+        float m = 0.0f, w = 0.0f, x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < GT / 64; ++i) m += mv[i];
+        for (int i = t; i < CHUNK; ++i) w += M[i * MP + t], x += av[i];
+        for (int j = 0; j < t; ++j) y += bv[j];
+        a.dg[(row0 + t) * a.Hv + h] = fmaf(expf(hi[CHUNK - 1]), m, (x + y) + w);
     }
 }
 
@@ -662,8 +834,8 @@ template <typename T> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
     return a.Dv <= 64 ? row_sweep<T, 4>(a, st) : a.Dv <= 128 ? row_sweep<T, 8>(a, st) : row_sweep<T, 16>(a, st);
 }
 
-cudaError_t decay_grads(const Args &a, cudaStream_t st) {
-    return launch_after(decay_grads_kernel, (unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st, a);
+cudaError_t decay_chain(const Args &a, cudaStream_t st) {
+    return launch_after(decay_chain_kernel, (unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st, a);
 }
 template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
     cudaError_t e = column_sweep<T, true>(a, st);
@@ -671,14 +843,14 @@ template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
     if ((e = row_sweep<T>(a, st)) != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.L * a.Hv, n = (long long)a.B * a.L * a.Hk * a.Dk;
     if ((e = launch_after(token_grads_kernel<T>, (unsigned)((rows + 7) / 8), 256, 0, st, a)) != cudaSuccess) return e;
-    if ((e = decay_grads(a, st)) != cudaSuccess) return e;
+    if ((e = launch_after(decay_grads_kernel<T>, dim3(chunks(a.L), a.Hv, a.B), GT, 0, st, a)) != cudaSuccess) return e;
     return launch_after(group_sum_kernel<T>, (unsigned)((n + 255) / 256), 256, 0, st, a);
 }
 
 // The tensor-core path's launches, and the decays' gradients.
 cudaError_t backward_tc(const Args &a, cudaStream_t st) {
     const cudaError_t e = tc_backward(a, st);
-    return e == cudaSuccess ? decay_grads(a, st) : e;
+    return e == cudaSuccess ? decay_chain(a, st) : e;
 }
 
 bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -53,6 +53,31 @@ __host__ __device__ inline int chunks(int L) { return (L + CHUNK - 1) / CHUNK; }
 // 64 can hold; NaN stays NaN.
 __device__ __forceinline__ float clamp_g(float g) { return g < -128.0f ? -128.0f : g; }
 
+// (hi, lo) += (bh, bl): sums of floats with 46 bits.
+__device__ __forceinline__ void add_pair(float &hi, float &lo, float bh, float bl) {
+    const float s = hi + bh, t = s - hi, e = (hi - (s - t)) + (bh - t);
+    const float l = lo + bl + e;
+    hi = s + l;
+    lo = l - (hi - s);
+}
+// One warp: G_i, the sums of a chunk's log decays, of tokens 2 lane and
+// 2 lane + 1, in pairs of floats, so that a small difference of large sums keeps
+// 24 bits.  Tokens past the end do not decay.
+__device__ __forceinline__ void decay_sums(const Args &a, long long row0, int nt, int h, int lane, float (&hi)[2], float (&lo)[2]) {
+    const int t = 2 * lane;
+    const float x0 = t < nt ? clamp_g(a.g[(row0 + t) * a.Hv + h]) : 0.0f;
+    const float x1 = t + 1 < nt ? clamp_g(a.g[(row0 + t + 1) * a.Hv + h]) : 0.0f;
+    hi[1] = x0, lo[1] = 0.0f;
+    add_pair(hi[1], lo[1], x1, 0.0f);
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float uh = __shfl_up_sync(0xffffffffu, hi[1], m), ul = __shfl_up_sync(0xffffffffu, lo[1], m);
+        if (lane >= m) add_pair(hi[1], lo[1], uh, ul);
+    }
+    hi[0] = hi[1], lo[0] = lo[1];
+    add_pair(hi[0], lo[0], -x1, 0.0f);
+}
+
 // A launch whose blocks may be scheduled while the kernel before it drains: every
 // kernel of the delta rule waits for that one (griddep_wait in all threads)
 // before it touches global memory or TMEM, so that it also comes after all

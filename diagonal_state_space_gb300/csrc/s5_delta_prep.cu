@@ -58,34 +58,16 @@ struct PrepBars {
     int abort;
 };
 
-// (hi, lo) += (bh, bl): sums of floats with 46 bits.
-__device__ __forceinline__ void add_pair(float &hi, float &lo, float bh, float bl) {
-    const float s = hi + bh, t = s - hi, e = (hi - (s - t)) + (bh - t);
-    const float l = lo + bl + e;
-    hi = s + l;
-    lo = l - (hi - s);
-}
-
-// One warp: the factors of a chunk and value head.  G_i is summed in pairs of
-// floats, so that a small difference of large sums keeps 24 bits.
+// One warp: the factors of a chunk and value head.
 __device__ __forceinline__ void chunk_factors(const Args &a, long long row0, int nt, int h, Meta *meta, float *near, int lane) {
     const int t = 2 * lane;
-    const float x0 = t < nt ? clamp_g(a.g[(row0 + t) * a.Hv + h]) : 0.0f;
-    const float x1 = t + 1 < nt ? clamp_g(a.g[(row0 + t + 1) * a.Hv + h]) : 0.0f;
     const float b0 = t < nt ? a.beta[(row0 + t) * a.Hv + h] : 0.0f;
     const float b1 = t + 1 < nt ? a.beta[(row0 + t + 1) * a.Hv + h] : 0.0f;
-    float hi = x0, lo = 0.0f;
-    add_pair(hi, lo, x1, 0.0f);
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const float uh = __shfl_up_sync(0xffffffffu, hi, m), ul = __shfl_up_sync(0xffffffffu, lo, m);
-        if (lane >= m) add_pair(hi, lo, uh, ul);
-    }
-    const float th = __shfl_sync(0xffffffffu, hi, 31), tl = __shfl_sync(0xffffffffu, lo, 31);
-    const float eh = __shfl_sync(0xffffffffu, hi, lane | 7), el = __shfl_sync(0xffffffffu, lo, lane | 7);
-    float h0 = hi, l0 = lo;
-    add_pair(h0, l0, -x1, 0.0f);
-    const float G[2] = {h0, hi}, g[2] = {l0, lo}, be[2] = {b0, b1};
+    float G[2], g[2];
+    decay_sums(a, row0, nt, h, lane, G, g);
+    const float th = __shfl_sync(0xffffffffu, G[1], 31), tl = __shfl_sync(0xffffffffu, g[1], 31);
+    const float eh = __shfl_sync(0xffffffffu, G[1], lane | 7), el = __shfl_sync(0xffffffffu, g[1], lane | 7);
+    const float be[2] = {b0, b1};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         meta->hi[t + i] = G[i];
