@@ -8,8 +8,8 @@
 //   Z_start = e^{G_64} Z + K^T (-e^G dv) + Q^T (scale e^G dO)
 // the forward's three products transposed, on the same tiles: D1 = [K; Q] Z,
 // D2 = [T; P T]^T [e^{..} K Z; dO] (depth 128), D3 = [K; Q]^T [..; ..] (depth
-// 128).  Z leaves chunk by chunk as the two upper parts of its operand, in the
-// layout that the local products below read.  <S, Z> at each chunk's end, the
+// 128).  Z leaves chunk by chunk as the two upper parts of its operand (rounded
+// ones), in the layout that the local products below read.  <S, Z> at each chunk's end, the
 // anchor of the decays' gradients, is taken in 32 bits on the way.
 //
 // Bound: as the forward scan, the chain product -> sums, splits -> product three
@@ -210,7 +210,7 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
             const float4 t = (a.ds_last && state) ? *reinterpret_cast<const float4 *>(a.ds_last + place + 4 * j) : make_float4(0, 0, 0, 0);
             Z[4 * j] = t.x, Z[4 * j + 1] = t.y, Z[4 * j + 2] = t.z, Z[4 * j + 3] = t.w;
         }
-        if (state) put3<32>(ops, L::S_IMG, row, c0, Z);
+        if (state) put3<32, false, true>(ops, L::S_IMG, row, c0, Z);
         hand_over(&sb->z_ready, lane);
         for (int it = 0; it < N; ++it) {
             const int c = N - 1 - it;
@@ -266,7 +266,7 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
                 load_parts<3, 32>(D3 + lanes, x);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) Z[i] = fmaf(last, Z[i], x[i]);
-                if (c > 0) put3<32>(ops, L::S_IMG, row, c0, Z);
+                if (c > 0) put3<32, false, true>(ops, L::S_IMG, row, c0, Z);
             }
             if (c > 0) hand_over(&sb->z_ready, lane);
         }
@@ -293,9 +293,9 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
 // TMEM lanes 0..63 and dq in 64..127:
 //   D2 = [U; -] Z^T,  D3 = [dv; dO] U^T,
 //   D1 = [dv; dO] S0^T,  D4 = [W; N] K,  D5 = [W; N]^T [K; Q].
-// dq and dk are rounded to bf16, so that 32-bit operands are carried as two
-// bf16 values here (17 bits), three products against another pair, two against
-// a bf16 operand.
+// dq and dk are rounded to bf16, off by up to 2^-9: 32-bit operands are carried as
+// two bf16 values here, off by up to 2^-17, three products against another pair, two
+// against a bf16 operand.
 // Bound: what it reads (the state, the adjoint and 64 tokens' X, e, o, dO, v:
 // 240 KB per chunk and head of 128 x 128), and the phases between its products in
 // a CTA alone on its SM: 2048 chunks and heads in 161 us, 3.1 TB/s.  One CTA a

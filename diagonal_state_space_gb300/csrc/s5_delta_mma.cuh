@@ -71,10 +71,20 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t &h, uint32_t &
     m = tops(a, b);
     l = tops(rest(a), rest(b));
 }
-// Two parts, the second rounded: 17 bits.
+// Two parts, both rounded: off by at most 2^-17 of the value, to either side.  Two
+// cut-off parts would be off by 2^-15 towards zero, and the product of two second
+// parts, which is left out, would have the values' sign: 7e-6 of them each.
 __device__ __forceinline__ void split2(float a, float b, uint32_t &h, uint32_t &m) {
-    h = tops(a, b);
-    m = pack2(rest(a), rest(b));
+    h = pack2(a, b);
+    m = pack2(a - lo16(h), b - hi16(h));
+}
+// Three parts whose first two are split2's: where they are used by themselves
+// too.  What the second leaves has 7 bits at most, so that all 24 are held.
+__device__ __forceinline__ void split3_rounded(float a, float b, uint32_t &h, uint32_t &m, uint32_t &l) {
+    h = pack2(a, b);
+    a -= lo16(h), b -= hi16(h);
+    m = pack2(a, b);
+    l = tops(a - lo16(m), b - hi16(m));
 }
 
 // ---------------------------------------------------------------------------
@@ -94,14 +104,18 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 }
 // W values of a row from column c0 on, as three parts.  An operand of 64
 // columns is an image for each part, `stride` bytes apart; of 32 columns
-// (NARROW) the first two parts share an image's rows.
-template <int W, bool NARROW = false>
+// (NARROW) the first two parts share an image's rows.  ROUNDED: split3_rounded.
+template <int W, bool NARROW = false, bool ROUNDED = false>
 __device__ __forceinline__ void put3(uint32_t img, uint32_t stride, int row, int c0, const float *v) {
 #pragma unroll
     for (int j = 0; j < W / 8; ++j) {
         uint32_t h[4], m[4], l[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split3(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], h[i], m[i], l[i]);
+        for (int i = 0; i < 4; ++i)
+            if constexpr (ROUNDED)
+                split3_rounded(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], h[i], m[i], l[i]);
+            else
+                split3(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], h[i], m[i], l[i]);
         const uint32_t to = piece(img, row, c0 / 8 + j);
         sts128(to, h[0], h[1], h[2], h[3]);
         sts128(NARROW ? piece(img, row, c0 / 8 + j + 4) : to + stride, m[0], m[1], m[2], m[3]);

@@ -375,7 +375,9 @@ s5_status s5_ssm_backward(const float *lambda, const float *log_dt, const float 
  *
  * Arithmetic: states, sums and decays in 32 bits.  On the tensor cores (bf16
  * q, k, v with heads of 64 or 128, pitches that are multiples of 8) an operand that
- * is not itself bf16 is carried as a sum of three bf16 values.
+ * is not itself bf16 is carried as a sum of three bf16 values, all its 24 bits; only
+ * in the last products of dq and dk, which are rounded to bf16 themselves, as a sum
+ * of two, off by at most 2^-17 of the operand to either side.
  * ======================================================================== */
 
 /* Bytes of the `saved` buffer that s5_delta_forward fills for
