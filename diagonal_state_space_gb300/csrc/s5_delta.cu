@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
                 }
                 if (first) {
                     store_elem<T>(static_cast<T *>(a.o) + (row0 + t) * a.ldo + (long long)h * a.Dv + col, o);
-                    if (a.e) a.e[out] = e, a.o32[out] = o;
+                    if (a.e) a.e[out] = e;
                 }
             } else {
 #pragma unroll
@@ -364,12 +364,6 @@ __global__ void __launch_bounds__(2 * SWT) row_sweep_kernel(const Args a) {
     }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    return v;
-}
-
 // One warp per token and value head: dv = beta X, dbeta = X . e.
 template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(const Args a) {
     griddep_wait();
@@ -387,34 +381,6 @@ template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(
     }
     db = warp_sum(db);
     if (lane == 0) a.dbeta[hv] = db;
-}
-
-// One warp per chunk and value head: dg by adding the chunk's terms from its
-// end on top of <S, Z> there.  A token whose decay is zero has no gradient.
-__global__ void __launch_bounds__(256) decay_chain_kernel(const Args a) {
-    griddep_wait();
-    const int N = chunks(a.L), lane = threadIdx.x % 32;
-    const long long id = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-    if (id >= (long long)a.B * a.Hv * N) return;
-    const int c = (int)(id % N);
-    const long long bh = id / N;
-    const int h = (int)(bh % a.Hv);
-    const long long b = bh / a.Hv;
-    float s = 0.0f;
-    for (int p = 0; p < a.parts; ++p) s += a.inner[(bh * (N + 1) + c + 1) * a.parts + p];
-    // two tokens per lane, later tokens in lower lanes
-    for (int half = 0; half < 2; ++half) {
-        const int t = c * CHUNK + CHUNK - 1 - 32 * half - lane;
-        const long long hv = (b * a.L + t) * a.Hv + h;
-        float w = t < a.L ? a.dots[hv] : 0.0f;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const float up = __shfl_up_sync(0xffffffffu, w, m);
-            if (lane >= m) w += up;
-        }
-        if (t < a.L) a.dg[hv] = expf(clamp_g(a.g[hv])) == 0.0f ? 0.0f : s + w;
-        s += __shfl_sync(0xffffffffu, w, 31);
-    }
 }
 
 // dg of a chunk and value head (the formula is at the top of this file).  Half of
@@ -834,9 +800,6 @@ template <typename T> cudaError_t row_sweep(const Args &a, cudaStream_t st) {
     return a.Dv <= 64 ? row_sweep<T, 4>(a, st) : a.Dv <= 128 ? row_sweep<T, 8>(a, st) : row_sweep<T, 16>(a, st);
 }
 
-cudaError_t decay_chain(const Args &a, cudaStream_t st) {
-    return launch_after(decay_chain_kernel, (unsigned)(((long long)a.B * a.Hv * chunks(a.L) + 7) / 8), 256, 0, st, a);
-}
 template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
     cudaError_t e = column_sweep<T, true>(a, st);
     if (e != cudaSuccess || a.L == 0) return e;
@@ -845,12 +808,6 @@ template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
     if ((e = launch_after(token_grads_kernel<T>, (unsigned)((rows + 7) / 8), 256, 0, st, a)) != cudaSuccess) return e;
     if ((e = launch_after(decay_grads_kernel<T>, dim3(chunks(a.L), a.Hv, a.B), GT, 0, st, a)) != cudaSuccess) return e;
     return launch_after(group_sum_kernel<T>, (unsigned)((n + 255) / 256), 256, 0, st, a);
-}
-
-// The tensor-core path's launches, and the decays' gradients.
-cudaError_t backward_tc(const Args &a, cudaStream_t st) {
-    const cudaError_t e = tc_backward(a, st);
-    return e == cudaSuccess ? decay_chain(a, st) : e;
 }
 
 bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -868,9 +825,9 @@ s5_status check_sizes(long long B, long long L, long long Hk, long long Hv, long
 
 // Regions of the two buffers.  The backward workspace holds what either path
 // needs: dq and dk per value head, the chunks' Z (as many bytes in either form,
-// one less than the states), parts of <S, Z> (32 at most), the tokens' sums.
+// one less than the states), parts of the decays' gradients.
 struct Sizes {
-    size_t e, states, images, heads, inner, dots;
+    size_t e, states, images, heads, inner, writes;
 };
 Sizes sizes(int B, int L, int Hv, int Dk, int Dv) {
     Sizes s;
@@ -879,8 +836,8 @@ Sizes sizes(int B, int L, int Hv, int Dk, int Dv) {
     s.states = align256(sizeof(float) * (size_t)B * Hv * (N + 1) * Dk * Dv);
     s.images = align256(tc_image_bytes(B, L, Hv, Dk, Dv));
     s.heads = align256(sizeof(float) * rows * Dk);
-    s.inner = align256(sizeof(float) * (size_t)B * Hv * (N + 1) * 32);
-    s.dots = align256(sizeof(float) * rows);
+    s.inner = s.images ? align256(sizeof(float) * (size_t)B * Hv * N * inner_parts(Dk, Dv)) : 0;
+    s.writes = s.images ? align256(sizeof(float) * (size_t)B * Hv * N * CHUNK * write_parts(Dv)) : 0;
     return s;
 }
 }  // namespace
@@ -900,7 +857,7 @@ extern "C" size_t s5_delta_workspace_size(int B, int L, int Hv, int Dk, int Dv, 
     if (check_sizes(B, L, Hv, Hv, Dk, Dv, S5_F32) != S5_OK) return 0;
     const Sizes s = sizes(B, L, Hv, Dk, Dv);
     size_t n = 256 + s.images;
-    if (backward) n += s.e + 2 * s.heads + s.states + s.inner + s.dots;
+    if (backward) n += s.e + 2 * s.heads + s.states + s.inner + s.writes;
     return n;
 }
 
@@ -931,7 +888,6 @@ extern "C" s5_status s5_delta_forward(const void *q, long long ldq, const void *
     if (saved) {
         char *p = static_cast<char *>(saved);
         a.e = reinterpret_cast<float *>(p);
-        a.o32 = reinterpret_cast<float *>(p + s.e);
         a.states = reinterpret_cast<float *>(p + 2 * s.e);
     }
     a.images = reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
@@ -974,7 +930,6 @@ extern "C" s5_status s5_delta_backward(const void *q, long long ldq, const void 
     const Sizes s = sizes(B, L, Hv, Dk, Dv);
     char *p = static_cast<char *>(const_cast<void *>(saved));   // read only here
     a.e = reinterpret_cast<float *>(p);
-    a.o32 = reinterpret_cast<float *>(p + s.e);
     a.states = reinterpret_cast<float *>(p + 2 * s.e);
     a.dout = dout, a.lddo = lddo, a.ds_last = ds_last;
     a.dq = dq, a.dk = dk, a.dv = dv, a.lddq = lddq, a.lddk = lddk, a.lddv = lddv;
@@ -989,16 +944,14 @@ extern "C" s5_status s5_delta_backward(const void *q, long long ldq, const void 
     w += 2 * s.heads;
     a.z = w;
     w += s.states;
-    a.parts = (Dv + column_width(a) - 1) / column_width(a);
     a.inner = reinterpret_cast<float *>(w);
     w += s.inner;
-    a.dots = reinterpret_cast<float *>(w);
+    a.writes = reinterpret_cast<float *>(w);
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
-    if (tc_supported(a, dtype, true)) {
-        a.parts = tc_inner_parts(Dk, Dv);
-        e = backward_tc(a, st);
-    } else
+    if (tc_supported(a, dtype, true))
+        e = tc_backward(a, st);
+    else
         e = dtype == S5_BF16 ? backward<__nv_bfloat16>(a, st) : backward<float>(a, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }

@@ -22,7 +22,6 @@ struct Args {
     float *s_last;                    // or null
     // kept for the backward pass (null: nothing is kept)
     float *e;                         // [B][L][Hv][Dv]   v_t - a_t S_{t-1}^T k_t
-    float *o32;                       // [B][L][Hv][Dv]   o before its rounding
     float *states;                    // [B][Hv][N + 1][Dk][Dv]   S entering chunk c; [N] is the last state
     // backward
     const void *dout;                 // dL/do
@@ -34,9 +33,9 @@ struct Args {
     // backward workspace
     float *x;                         // [B][L][Hv][Dv]   dL/du_t
     float *dqh, *dkh;                 // [B][L][Hv][Dk]   per value head
-    float *inner;                     // [B][Hv][N + 1][parts]   parts of <S_c, dL/dS_c>
-    float *dots;                      // [B][L][Hv] o.do - v.dv
-    int parts;
+    // tensor cores, of the decays' gradients: parts of <S, Z> and of b_j
+    float *inner;                     // [B][Hv][N][inner_parts]
+    float *writes;                    // [B][Hv][N][CHUNK][write_parts]
     void *z;                          // dL/dS at the end of chunk c: [B][Hv][N][Dk][Dv] float32, or, for the tensor
                                       // cores, [B][Hv][N][Dv / 64][2][Dk][64] bf16 (two parts)
     void *images;                     // operand images of the tensor-core path; then a state between launches
@@ -48,11 +47,20 @@ struct Args {
 
 __host__ __device__ inline int chunks(int L) { return (L + CHUNK - 1) / CHUNK; }
 
+// Parts of a chunk's <S, Z> and of a token's b_j: a warp of the adjoint each.
+__host__ __device__ constexpr int inner_parts(int Dk, int Dv) { return Dv / 64 * (Dk / 16); }
+__host__ __device__ constexpr int write_parts(int Dv) { return Dv / 64 * 2; }
+
 // A decay factor: exp(g) is zero in 32 bits below -104, so that g = -inf and
 // the type's lowest value (a reset of the state) act as -128, which sums of
 // 64 can hold; NaN stays NaN.
 __device__ __forceinline__ float clamp_g(float g) { return g < -128.0f ? -128.0f : g; }
 
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
 // (hi, lo) += (bh, bl): sums of floats with 46 bits.
 __device__ __forceinline__ void add_pair(float &hi, float &lo, float bh, float bl) {
     const float s = hi + bh, t = s - hi, e = (hi - (s - t)) + (bh - t);
@@ -101,9 +109,7 @@ bool tc_supported(const Args &a, s5_dtype dtype, bool backward);
 // Workspace of the tensor-core path; 0 for head sizes that it does not take.
 size_t tc_image_bytes(int B, int L, int Hv, int Dk, int Dv);
 cudaError_t tc_forward(const Args &a, cudaStream_t st);
-// All gradients but dg, and its terms (inner, dots).
 cudaError_t tc_backward(const Args &a, cudaStream_t st);
-int tc_inner_parts(int Dk, int Dv);
 
 }  // namespace delta
 }  // namespace s5

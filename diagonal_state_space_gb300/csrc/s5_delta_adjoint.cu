@@ -9,8 +9,8 @@
 // the forward's three products transposed, on the same tiles: D1 = [K; Q] Z,
 // D2 = [T; P T]^T [e^{..} K Z; dO] (depth 128), D3 = [K; Q]^T [..; ..] (depth
 // 128).  Z leaves chunk by chunk as the two upper parts of its operand (rounded
-// ones), in the layout that the local products below read.  <S, Z> at each chunk's end, the
-// anchor of the decays' gradients, is taken in 32 bits on the way.
+// ones), in the layout that the local products below read.  Of the decays' gradients
+// (formula in s5_delta.cu) <S, Z> and the b_j are taken in 32 bits on the way.
 //
 // Bound: as the forward scan, the chain product -> sums, splits -> product three
 // times a chunk, 4.1 us with 64 columns a CTA and the tiles of X, Z and the state
@@ -37,7 +37,7 @@ template <int DK> struct AdjSmem {
     static constexpr uint32_t ops = mat + MAT_BYTES;
     static constexpr uint32_t go = ops + 6 * RU_IMG;       // dO
     static constexpr uint32_t xs = go + RU_IMG;            // X, to be stored
-    static constexpr uint32_t sin = xs + 2 * RU_IMG;       // the state at the chunk's end
+    static constexpr uint32_t sin = xs + 2 * RU_IMG;       // the state at the chunk's start
     static constexpr uint32_t meta = sin + DK * 256;
     static constexpr uint32_t bars = meta + META_BYTES;
     static constexpr uint32_t total = bars + 256 + 1024;
@@ -108,7 +108,7 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
             auto load_state = [&](int it) {
                 mbar_arrive_tx(&sb->sin_full, DK * 256);
                 for (int x = 0; x < 2; ++x)
-                    tma_load_3d(smem + L::sin + x * DK * 128, &maps.s, n0 + 32 * x, 0, (int)(bh * (N + 1) + N - it), &sb->sin_full);
+                    tma_load_3d(smem + L::sin + x * DK * 128, &maps.s, n0 + 32 * x, 0, (int)(bh * (N + 1) + N - 1 - it), &sb->sin_full);
             };
             load_kq(0);
             load_state(0);
@@ -214,7 +214,7 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
         hand_over(&sb->z_ready, lane);
         for (int it = 0; it < N; ++it) {
             const int c = N - 1 - it;
-            // <S, Z> at the chunk's end
+            // <S, Z> of the chunk's start and end
             bool ok = wait(&sb->sin_full, it & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (state) {
@@ -227,10 +227,21 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
                 }
                 w += v;
                 for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
-                if (lane == 0) a.inner[(bh * (N + 1) + c + 1) * a.parts + blockIdx.x * (DK / 16) + q * 2 + warp / 4] = w;
+                if (lane == 0) a.inner[(bh * N + c) * inner_parts(DK, a.Dv) + blockIdx.x * (DK / 16) + q * 2 + warp / 4] = w;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb->sin_empty);
+            // e of this warp's fragment is on its way during D1
+            float2 e[8];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = c * C + ta + 8 * i;
+                    e[4 * i + j] = t < a.L ? *reinterpret_cast<const float2 *>(a.e + (((long long)b * a.L + t) * a.Hv + h) * a.Dv + n0 + c0 +
+                                                                               8 * j + 2 * (lane & 3))
+                                           : make_float2(0.0f, 0.0f);
+                }
             ok = wait(&sb->img_full, it & 1) && wait(&sb->go_full, it & 1) && wait(&sb->z_left, it & 1) && wait(&sb->d1, it & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -239,6 +250,21 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
             frag_scale(f, meta->down[ta], meta->down[tb]);
             frag_put3(ops, RU_IMG, t16, c0, lane, f);
             hand_over(&sb->r_ready, lane);
+            {   // this slice's share of b_j = e^{G_64 - G_j} (Z^T k_j).u_j, for the decays
+                float w[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[i] = fmaf(f[4 * j + 2 * i], e[4 * i + j].x, fmaf(f[4 * j + 2 * i + 1], e[4 * i + j].y, w[i]));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    w[i] += __shfl_xor_sync(0xffffffffu, w[i], 1);
+                    w[i] += __shfl_xor_sync(0xffffffffu, w[i], 2);
+                    if ((lane & 3) == 0)
+                        a.writes[((bh * N + c) * C + ta + 8 * i) * write_parts(a.Dv) + blockIdx.x * 2 + warp / 4] = meta->beta[ta + 8 * i] * w[i];
+                }
+            }
             const float last = meta->last, ua = meta->up[ta], ub = meta->up[tb];
             const float ya = -ua * meta->beta[ta], yb = -ub * meta->beta[tb];
             frag_get(go, t16, c0, lane, f);
@@ -284,8 +310,8 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
 // ---------------------------------------------------------------------------
 // What is local to a chunk: persistent CTAs over chunks and key heads, each
 // over its value heads, the next head's tiles on their way to L2.  Per token
-// dv = beta X, dbeta = X . e and o . dO - v . dv (for the decays, s5_delta.cu).  With S0 and Z the state at
-// the chunk's start and the adjoint at its end, U = beta e, and
+// dv = beta X, dbeta = X . e.  With S0 and Z the state at the chunk's start and the
+// adjoint at its end, U = beta e, and
 // N_ij = scale D_ij dO_i.U_j (j <= i), W_ij = -D_ij dv_i.U_j (j < i):
 //   dq = scale e^G dO S0^T + N K
 //   dk = e^{G_64 - G} U Z^T - e^G dv S0^T + W K + W^T K + N^T Q
@@ -294,12 +320,20 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
 //   D2 = [U; -] Z^T,  D3 = [dv; dO] U^T,
 //   D1 = [dv; dO] S0^T,  D4 = [W; N] K,  D5 = [W; N]^T [K; Q].
 // dq and dk are rounded to bf16, off by up to 2^-9: 32-bit operands are carried as
-// two bf16 values here, off by up to 2^-17, three products against another pair, two
+// two bf16 values there, off by up to 2^-17, three products against another pair, two
 // against a bf16 operand.
-// Bound: what it reads (the state, the adjoint and 64 tokens' X, e, o, dO, v:
-// 240 KB per chunk and head of 128 x 128), and the phases between its products in
-// a CTA alone on its SM: 2048 chunks and heads in 161 us, 3.1 TB/s.  One CTA a
-// chunk without the prefetch took 200 us.
+//
+// The decays' gradients (formula in s5_delta.cu) keep 32 bits.  With KK = [K; Q] K^T
+// and E1 = [K; Q] S0,
+//   M = W o KK above + N o KK below (row i of either half),
+//   a_i = scale e^{G_i} E1_{64+i}.dO_i - e^{G_i} E1_i.dv_i,
+// and D3 and E1 take third parts of dv, U and S0 besides.  A thread has a row's 16
+// columns of M: their running sums go to the tokens of its own columns' block, their
+// total to those of the later blocks.  The sums over rows are butterflies and scans
+// over lanes, while D1, D4, D5 and E1 run.
+// Bound: what it reads (the state, the adjoint and 64 tokens' X, e, dO: 208 KB per
+// chunk and head of 128 x 128), and the phases between its products in a CTA alone on
+// its SM.
 // ---------------------------------------------------------------------------
 constexpr int LT = 512;
 
@@ -314,13 +348,19 @@ template <int DK, int DV> struct LocalSmem {
     static constexpr bool APART = U_IMG < M2_BYTES;            // [W; N] gets a place of its own
     static constexpr uint32_t wn = APART ? u + 2 * U_IMG : u;
     static constexpr uint32_t s = wn + 2 * (APART ? M2_BYTES : U_IMG);   // Z, then S0: two parts
-    static constexpr uint32_t meta = s + 2 * S_IMG;
+    // third parts: of dv and behind them of U, later of S0
+    static constexpr uint32_t dv3 = s + 2 * S_IMG, u3 = dv3 + U_IMG, s3 = dv3;
+    static constexpr uint32_t meta = u3 + U_IMG;
     static constexpr uint32_t bars = meta + META_BYTES;
     static constexpr uint32_t total = bars + 64 + 1024;
     static_assert(total <= 232448, "shared memory of a CTA");
+    static_assert(S_IMG <= 2 * U_IMG, "S0's third part fits");
     // products of M = 128 over 64 rows or columns read on into what follows:
-    // 8 KB past U, 16 KB past [W; N]
-    static_assert(2 * S_IMG >= M2_BYTES, "what the products read on is the CTA's own memory");
+    // 8 KB past U and dv's third part, 16 KB past [W; N]
+    static_assert(2 * S_IMG >= M2_BYTES && U_IMG >= 64 * 128, "what the products read on is the CTA's own memory");
+    // sums on their way to the decays' gradients, in the state's place after its products
+    static constexpr uint32_t part = s, suffix = part + 16 * 16 * 4, rows = suffix + 16 * 32 * 4;
+    static_assert(rows + 128 * 4 * 4 <= s + 2 * S_IMG, "they fit");
 };
 
 struct LocalBars {
@@ -342,11 +382,8 @@ __device__ __forceinline__ void prefetch_head(const Args &a, int c, int b, int h
         const int t = i / 8, k = i % 8;
         if (t >= nt) continue;
         const long long at = ((row0 + t) * a.Hv + h) * DV;
-        if (k < RL) prefetch_line(a.x + at + k * 32), prefetch_line(a.e + at + k * 32), prefetch_line(a.o32 + at + k * 32);
-        if (k < HL) {
-            prefetch_line(static_cast<const __nv_bfloat16 *>(a.dout) + (row0 + t) * a.lddo + (long long)h * DV + k * 64);
-            prefetch_line(static_cast<const __nv_bfloat16 *>(a.v) + (row0 + t) * a.ldv + (long long)h * DV + k * 64);
-        }
+        if (k < RL) prefetch_line(a.x + at + k * 32), prefetch_line(a.e + at + k * 32);
+        if (k < HL) prefetch_line(static_cast<const __nv_bfloat16 *>(a.dout) + (row0 + t) * a.lddo + (long long)h * DV + k * 64);
         if (rows_too && k >= 4 && k < 4 + KL) {
             prefetch_line(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + (k - 4) * 64);
             prefetch_line(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + t) * a.ldq + hk * DK + (k - 4) * 64);
@@ -367,6 +404,58 @@ __device__ __forceinline__ void put2(uint32_t img, uint32_t stride, int row, int
     const uint32_t to = piece(img, row, j);
     sts128(to, h[0], h[1], h[2], h[3]);
     sts128(to + stride, m[0], m[1], m[2], m[3]);
+}
+// As a piece of three images, the third at `low`.
+__device__ __forceinline__ void put3(uint32_t img, uint32_t stride, uint32_t low, int row, int j, const float (&v)[8]) {
+    uint32_t h[4], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split3_rounded(v[2 * i], v[2 * i + 1], h[i], m[i], l[i]);
+    const uint32_t to = piece(img, row, j);
+    sts128(to, h[0], h[1], h[2], h[3]);
+    sts128(to + stride, m[0], m[1], m[2], m[3]);
+    sts128(piece(low, row, j), l[0], l[1], l[2], l[3]);
+}
+// Sums over the warp of 16 values a lane; lane l gets that of value l / 2.
+__device__ __forceinline__ float sum16(const float (&v)[16], int lane) {
+    float a[8], b[4], c[2], d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool up = lane & 16;
+        a[i] = (up ? v[i + 8] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 8], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 8;
+        b[i] = (up ? a[i + 4] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 4], 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 4;
+        c[i] = (up ? b[i + 2] : b[i]) + __shfl_xor_sync(0xffffffffu, up ? b[i] : b[i + 2], 4);
+    }
+    const bool up = lane & 2;
+    d = (up ? c[1] : c[0]) + __shfl_xor_sync(0xffffffffu, up ? c[0] : c[1], 2);
+    return d + __shfl_xor_sync(0xffffffffu, d, 1);
+}
+// The sum of this lane's and all later lanes' values.
+__device__ __forceinline__ float later_lanes(float v, int lane) {
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float x = __shfl_down_sync(0xffffffffu, v, m);
+        if (lane + m < 32) v += x;
+    }
+    return v;
+}
+// The sum of all earlier lanes' values.
+__device__ __forceinline__ float earlier_lanes(float v, int lane) {
+    float w = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float x = __shfl_up_sync(0xffffffffu, w, m);
+        if (lane >= m) w += x;
+    }
+    const float x = __shfl_up_sync(0xffffffffu, w, 1);
+    return lane ? x : 0.0f;
 }
 __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
     const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
@@ -401,11 +490,17 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
     __syncthreads();
     tc_fence_after();
     const uint32_t kq = smem_addr(smem + L::kq), sA = smem_addr(smem + L::a), sU = smem_addr(smem + L::u),
-                   sS = smem_addr(smem + L::s), sW = smem_addr(smem + L::wn);
-    const uint32_t tmem = lb->tmem, D1 = tmem, D2 = tmem + 128, D4 = tmem + 256, D3 = tmem + 384, D5 = tmem + 384;
+                   sS = smem_addr(smem + L::s), sW = smem_addr(smem + L::wn), dv3 = smem_addr(smem + L::dv3),
+                   u3 = smem_addr(smem + L::u3), s3 = smem_addr(smem + L::s3);
+    // KK lies where D1 will, E1 where D2 has been, D3 (and dv's third part by U, D3L) where D5 will
+    const uint32_t tmem = lb->tmem, D1 = tmem, D2 = tmem + 128, D4 = tmem + 256, D3 = tmem + 384, D3L = tmem + 448, D5 = tmem + 384,
+                   KK = tmem, E1 = tmem + 128;
     const uint64_t A0 = desc_k(sA), W0 = desc_k(sW), WT = desc_mn(sW, M2_BYTES), U0 = desc_k(sU), S0 = desc_k(sS),
-                   cols = desc_mn(kq, KQ_BOX);
+                   cols = desc_mn(kq, KQ_BOX), rows = desc_k(kq);
     Meta *meta = reinterpret_cast<Meta *>(smem + L::meta);
+    float(*part)[16] = reinterpret_cast<float(*)[16]>(smem + L::part);       // [warp][column]
+    float(*suffix)[32] = reinterpret_cast<float(*)[32]>(smem + L::suffix);   // [warp][row]
+    float(*reads)[4] = reinterpret_cast<float(*)[4]>(smem + L::rows);        // [row][32 columns]
     auto wait = [&](uint64_t *bar, int parity) { return bounded_wait(bar, (uint32_t)parity, &lb->abort); };
     // warp w: TMEM lanes 32 (w % 4) on, columns 32 (w / 4) on; of D3 and [W; N]
     // columns 16 (w / 4) on
@@ -442,90 +537,98 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
             for (int n = 0; n < C * PR / LT; ++n) {
                 const int i = tid + n * LT, t = i / PR, d = i % PR * 8;
                 const long long hv = (row0 + t) * a.Hv + h;
-                float x[8] = {}, e[8] = {}, o[8] = {}, s1 = 0.0f, s2 = 0.0f, be = 0.0f;
-                uint4 g = make_uint4(0, 0, 0, 0), v = g;
+                float x[8] = {}, e[8] = {}, s1 = 0.0f, be = 0.0f;
+                uint4 g = make_uint4(0, 0, 0, 0);
                 if (t < nt) {
                     load8(a.x + hv * DV + d, x);
                     load8(a.e + hv * DV + d, e);
-                    load8(a.o32 + hv * DV + d, o);
                     g = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dout) + (row0 + t) * a.lddo + (long long)h * DV + d);
-                    v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) + (row0 + t) * a.ldv + (long long)h * DV + d);
                     be = a.beta[hv];
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const uint32_t gk = k < 2 ? g.x : k < 4 ? g.y : k < 6 ? g.z : g.w, vk = k < 2 ? v.x : k < 4 ? v.y : k < 6 ? v.z : v.w;
                     s1 = fmaf(x[k], e[k], s1);
                     x[k] *= be, e[k] *= be;
-                    s2 = fmaf(o[k], k % 2 ? hi16(gk) : lo16(gk), s2);
-                    s2 = fmaf(-(k % 2 ? hi16(vk) : lo16(vk)), x[k], s2);
                 }
                 const int box = d / 64, at = d % 64 / 8;
-                put2(sA + box * M2_BYTES, L::A_IMG, t, at, x);
-                put2(sU + box * RU_IMG, L::U_IMG, t, at, e);
+                put3(sA + box * M2_BYTES, L::A_IMG, dv3 + box * RU_IMG, t, at, x);
+                put3(sU + box * RU_IMG, L::U_IMG, u3 + box * RU_IMG, t, at, e);
                 sts128(piece(sA + box * M2_BYTES, C + t, at), g.x, g.y, g.z, g.w);
                 sts128(piece(sA + L::A_IMG + box * M2_BYTES, C + t, at), 0, 0, 0, 0);   // dO is bf16: no second part
 #pragma unroll
-                for (int m = PR / 2; m > 0; m >>= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, m), s2 += __shfl_xor_sync(0xffffffffu, s2, m);
+                for (int m = PR / 2; m > 0; m >>= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, m);
                 if (t < nt) {
                     *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dv) + (row0 + t) * a.lddv + (long long)h * DV + d) =
                         make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-                    if (d == 0) a.dbeta[hv] = s1, a.dots[hv] = s2;
+                    if (d == 0) a.dbeta[hv] = s1;
                 }
             }
             fence_proxy_async_smem();
             __syncthreads();
             const uint32_t id = idesc_bf16_f32(128, DK), idU = idesc_bf16_f32(128, 64);
             if (warp == 0) {
-                const bool z = wait(&lb->z_full, phase);
                 if (elect_one()) {
-#pragma unroll
-                for (int ps = 1; ps >= 0; --ps)
-#pragma unroll
-                    for (int p = 0; p <= ps; ++p)
+                    // small products first
+                    auto dot = [&](uint32_t d, uint64_t x, uint64_t u, bool first) {
 #pragma unroll
                         for (int k = 0; k < DV / 16; ++k)
-                            mma_bf16(D3, on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP),
-                                     on(U0, (ps - p) * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP), idU, !(ps == 1 && p == 0 && k == 0));
-                mma_commit(&lb->first);
-                if (z) {
+                            mma_bf16(d, on(x, k / 4 * M2_BYTES + k % 4 * K_STEP), on(u, k / 4 * RU_IMG + k % 4 * K_STEP), idU, !(first && k == 0));
+                    };
+                    dot(D3, A0, desc_k(u3), true);
+                    dot(D3, on(A0, L::A_IMG), on(U0, L::U_IMG), false);
+                    dot(D3, A0, on(U0, L::U_IMG), false);
+                    dot(D3, on(A0, L::A_IMG), U0, false);
+                    dot(D3, A0, U0, false);
 #pragma unroll
-                    for (int ps = 1; ps >= 0; --ps)
+                    for (int k = 0; k < DV / 16; ++k)
+                        mma_bf16(D3L, on(desc_k(dv3), k / 4 * RU_IMG + k % 4 * K_STEP), on(U0, k / 4 * RU_IMG + k % 4 * K_STEP), idU, k > 0);
 #pragma unroll
-                        for (int p = 0; p <= ps; ++p)
-#pragma unroll
-                            for (int k = 0; k < DV / 16; ++k)
-                                mma_bf16(D2, on(U0, p * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP),
-                                         on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id,
-                                         !(ps == 1 && p == 0 && k == 0));
+                    for (int k = 0; k < DK / 16; ++k) {
+                        const uint64_t K = on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP);
+                        mma_bf16(KK, K, K, idU, k > 0);
+                    }
+                    mma_commit(&lb->first);
                 }
-                mma_commit(&lb->second);
+                __syncwarp();
+                const bool z = wait(&lb->z_full, phase);
+                if (elect_one()) {
+                    if (z) {
+#pragma unroll
+                        for (int ps = 1; ps >= 0; --ps)
+#pragma unroll
+                            for (int p = 0; p <= ps; ++p)
+#pragma unroll
+                                for (int k = 0; k < DV / 16; ++k)
+                                    mma_bf16(D2, on(U0, p * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP),
+                                             on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id,
+                                             !(ps == 1 && p == 0 && k == 0));
+                    }
+                    mma_commit(&lb->second);
                 }
                 __syncwarp();
             }
-            // S0 is on its way while the first products run
-            const float *s0 = a.states + (bh * (N + 1) + c) * mat;
-            constexpr int SN = DK * DV / 8 / LT;
-            float4 sr[2 * SN];
-#pragma unroll
-            for (int n = 0; n < SN; ++n) {
-                sr[2 * n] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8);
-                sr[2 * n + 1] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8 + 4);
-            }
-            // the next head's tiles come to L2 meanwhile
+            // the next head's tiles come to L2 while the first products run
             if (j + 1 < group) {
                 prefetch_head<DK, DV>(a, c, b, h + 1, false, N, tid);
             } else if (const int next = item + (int)gridDim.x; next < items) {
                 prefetch_head<DK, DV>(a, next % N, next / N / a.Hk, next / N % a.Hk * group, true, N, tid);
             }
-            // [W; N]: a block of 16 columns a warp.  Decay factors of two blocks
-            // are products at the end of the columns' block, as in the preparation
+            // [W; N], and M in mm: a block of 16 columns a warp.  Decay factors of
+            // two blocks are products at the end of the columns' block, as in the
+            // preparation
             ok = wait(&lb->z_full, phase) && wait(&lb->first, phase) && ok;
             tc_fence_after();
-            float w[16];
+            const int nb = warp >> 2, cb = 16 * nb;
+            float w[16], mm[16];
             {
-                const int nb = warp >> 2, cb = 16 * nb, rb = tk >> 4;
+                const int rb = tk >> 4;
                 load_parts<1, 16>(D3 + quarter + cb, w);
+                if (keys) {
+                    load_parts<1, 16>(D3L + quarter + cb, mm);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] += mm[i];
+                }
+                load_parts<1, 16>(KK + quarter + cb, mm);
                 const float gh = meta->hi[tk], gl = meta->lo[tk], eh = meta->hi[cb + 15], el = meta->lo[cb + 15];
                 const int mine = cb + (lane & 15);
                 const float near = expf((eh - meta->hi[mine]) + (el - meta->lo[mine]));
@@ -539,7 +642,17 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                         if (const float e = expf((gh - meta->hi[col]) + (gl - meta->lo[col])); own) d = sign * e;
                     // a masked product may be infinite: it is not multiplied by 0
                     w[i] = (keys ? col < tk : col <= tk) ? d * w[i] : 0.0f;
+                    mm[i] = col < tk ? w[i] * mm[i] : 0.0f;
                 }
+            }
+            // S0 is on its way while the second products run
+            const float *s0 = a.states + (bh * (N + 1) + c) * mat;
+            constexpr int SN = DK * DV / 8 / LT;
+            float4 sr[2 * SN];
+#pragma unroll
+            for (int n = 0; n < SN; ++n) {
+                sr[2 * n] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8);
+                sr[2 * n + 1] = *reinterpret_cast<const float4 *>(s0 + (tid + n * LT) * 8 + 4);
             }
             ok = wait(&lb->second, phase) && ok;
             tc_fence_after();
@@ -548,19 +661,33 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                 const int i = tid + n * LT, r = i / PR, d = i % PR * 8;
                 const float v[8] = {sr[2 * n].x,     sr[2 * n].y,     sr[2 * n].z,     sr[2 * n].w,
                                     sr[2 * n + 1].x, sr[2 * n + 1].y, sr[2 * n + 1].z, sr[2 * n + 1].w};
-                put2(sS + d / 64 * (DK * 128), L::S_IMG, r, d % 64 / 8, v);
+                put3(sS + d / 64 * (DK * 128), L::S_IMG, s3 + d / 64 * (DK * 128), r, d % 64 / 8, v);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const float v[8] = {w[8 * n], w[8 * n + 1], w[8 * n + 2], w[8 * n + 3], w[8 * n + 4], w[8 * n + 5], w[8 * n + 6], w[8 * n + 7]};
-                put2(sW, M2_BYTES, row, 2 * (warp >> 2) + n, v);
+                put2(sW, M2_BYTES, row, 2 * nb + n, v);
+            }
+            const float up = meta->up[tk], down = meta->down[tk];
+            if (c0 < DK && keys) {   // D2, before E1 takes its place
+                float x[32];
+                load_parts<1, 32>(D2 + quarter + c0, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[i] = fmaf(down, x[i], sum[i]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             __syncthreads();
             tc_fence_after();
             if (warp == 0 && elect_one()) {
-                const uint32_t idB = id | B_MN, idAB = idB | A_MN;
+                const uint32_t idB = id | B_MN, idAB = idB | A_MN, idE = idesc_bf16_f32(128, DV) | B_MN;
+                const uint64_t SE = desc_mn(sS, DK * 128), SL = desc_mn(s3, DK * 128);
+#pragma unroll
+                for (int p = 2; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k)
+                        mma_bf16(E1, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), p == 2 ? on(SL, k * MN_STEP) : on(SE, p * L::S_IMG + k * MN_STEP),
+                                 idE, !(p == 2 && k == 0));
 #pragma unroll
                 for (int p = 1; p >= 0; --p) {
 #pragma unroll
@@ -581,16 +708,48 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                 mma_commit(&lb->third);
             }
             __syncwarp();
-            float x[32];
-            const float up = meta->up[tk], down = meta->down[tk];
-            if (c0 < DK && keys) {
-                load_parts<1, 32>(D2 + quarter + c0, x);
+            // M's sums: mm[i] becomes the row's sum up to column cb + i - 1, for the
+            // token cb + i where it is at or before the row
+            float total = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) sum[i] = fmaf(down, x[i], sum[i]);
+            for (int i = 0; i < 16; ++i) {
+                const float v = mm[i];
+                mm[i] = tk >= cb + i ? total : 0.0f;
+                total += v;
             }
+            const float crossing = sum16(mm, lane), rest = later_lanes(total, lane);
+            // dv of this warp's fragments of E1 is on its way
+            float2 dx[2][8];
+            if (keys && c0 < DV)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int t = (row - lane) + 16 * f + lane / 4 + 8 * (i / 4);
+                        dx[f][i] = t < nt ? *reinterpret_cast<const float2 *>(a.x + ((row0 + t) * a.Hv + h) * DV + c0 + 8 * (i % 4) + 2 * (lane & 3))
+                                          : make_float2(0.0f, 0.0f);
+                    }
             ok = wait(&lb->third, phase) && ok;
             tc_fence_after();
+            float y[2][2] = {};   // E1's rows by dv or dO
+            if (c0 < DV)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    float x[16];
+                    frag_load<1>(E1 + quarter + c0 + (f ? QUERY_LANES : 0u), x);
+                    if (keys) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            y[f][i / 4] = fmaf(x[4 * (i % 4) + 2 * (i / 4)], dx[f][i].x, fmaf(x[4 * (i % 4) + 2 * (i / 4) + 1], dx[f][i].y, y[f][i / 4]));
+                    } else {
+                        float g[16];
+                        frag_get(sA + c0 / 64 * M2_BYTES, row - lane + 16 * f, c0 % 64, lane, g);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[f][(i >> 1) & 1] = fmaf(x[i], g[i], y[f][(i >> 1) & 1]);
+                    }
+                }
             if (c0 < DK) {
+                float x[32];
                 const float wd = keys ? -up : a.scale * up;
                 load_parts<1, 32>(D1 + quarter + c0, x);
 #pragma unroll
@@ -604,9 +763,50 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                     for (int i = 0; i < 32; ++i) sum[i] += x[i];
                 }
             }
+            // the products are done with the state: its place takes the sums
+            if ((lane & 1) == 0) part[warp][lane / 2] = crossing;
+            suffix[warp][lane] = rest;
+            if (c0 < DV)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = row - lane + 16 * f + lane / 4 + 8 * i, t = r & 63;
+                        float v = y[f][i];
+                        v += __shfl_xor_sync(0xffffffffu, v, 1);
+                        v += __shfl_xor_sync(0xffffffffu, v, 2);
+                        if ((lane & 3) == 0) reads[r][c0 / 32] = meta->up[t] * (keys ? -meta->beta[t] : a.scale) * v;
+                    }
+            fence_proxy_async_smem();   // the next adjoint is copied over these
             tc_fence_before();
             __syncthreads();
             tc_fence_after();
+            if (warp == 0) {   // tokens `lane` and `lane` + 32
+                float ai[2] = {}, bj[2] = {}, pairs[2] = {}, m = 0.0f;
+                constexpr int WP = write_parts(DV), IP = inner_parts(DK, DV);
+                if (lane < IP) m = a.inner[(bh * N + c) * IP + lane];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = lane + 32 * i;
+#pragma unroll
+                    for (int p = 0; p < WP; ++p) bj[i] += a.writes[((bh * N + c) * C + t) * WP + p];
+#pragma unroll
+                    for (int g = 0; g < DV / 32; ++g) ai[i] += reads[t][g] + reads[C + t][g];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) pairs[i] += part[t / 16 * 4 + q][t % 16];
+                    for (int n = 0; n < t / 16; ++n) {   // whole blocks before the token's
+                        pairs[i] += suffix[4 * n + i][lane] + suffix[4 * n + 2 + i][lane];
+                        if (i == 0) pairs[i] += suffix[4 * n + 1][0] + suffix[4 * n + 3][0];
+                    }
+                }
+                m = meta->last * warp_sum(m);
+                // a from the token on, b up to it
+                const float a1 = later_lanes(ai[1], lane), a0 = later_lanes(ai[0], lane) + __shfl_sync(0xffffffffu, a1, 0);
+                const float b0 = earlier_lanes(bj[0], lane), b1 = earlier_lanes(bj[1], lane) + warp_sum(bj[0]);
+                if (lane < nt) a.dg[(row0 + lane) * a.Hv + h] = (a0 + b0) + (m + pairs[0]);
+                if (lane + 32 < nt) a.dg[(row0 + lane + 32) * a.Hv + h] = (a1 + b1) + (m + pairs[1]);
+                __syncwarp();
+            }
         }
         // out by way of shared memory (A's place), whole rows at a time
         if (c0 < DK)
@@ -659,8 +859,6 @@ template <int DK> cudaError_t backward(const Args &a, cudaStream_t st) {
 cudaError_t tc_backward(const Args &a, cudaStream_t st) {
     return a.Dk == 128 ? backward<128>(a, st) : backward<64>(a, st);
 }
-
-int tc_inner_parts(int Dk, int Dv) { return Dv / NV * (Dk / 16); }
 
 int adjoint_fault_take() { return fault_take(); }
 

@@ -43,7 +43,7 @@ namespace {
 
 struct ScanMaps {
     CUtensorMap k, q, v, o;
-    CUtensorMap e, o32, s;   // KEEP
+    CUtensorMap e, s;   // KEEP
 };
 
 template <int DK, int SL, bool KEEP, int NC> struct ScanSmem {
@@ -56,7 +56,7 @@ template <int DK, int SL, bool KEEP, int NC> struct ScanSmem {
     static constexpr uint32_t mat = kq + 2 * KQ;
     static constexpr uint32_t ops = mat + MAT_BYTES;
     static constexpr uint32_t vo = ops + SL * OPS;         // V, then o
-    static constexpr uint32_t stage = vo + SL * VO;        // KEEP: a state, or e and o in 32 bits
+    static constexpr uint32_t stage = vo + SL * VO;        // KEEP: a state, or e in 32 bits
     static constexpr uint32_t meta = stage + (KEEP ? 32768 : 0);
     static constexpr uint32_t bars = meta + META_BYTES;
     static constexpr uint32_t total = bars + 256 + 1024;   // + alignment slack
@@ -173,10 +173,7 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
                 if (!ok) break;
                 if constexpr (KEEP) {
                     if (!(ok = wait(&sb->rows_staged, c & 1))) break;
-                    for (int x = 0; x < 2; ++x) {
-                        tma_store_4d(&maps.e, smem + L::stage + x * RU_IMG, n0 + 32 * x, h, c * C, b);
-                        tma_store_4d(&maps.o32, smem + L::stage + (2 + x) * RU_IMG, n0 + 32 * x, h, c * C, b);
-                    }
+                    for (int x = 0; x < 2; ++x) tma_store_4d(&maps.e, smem + L::stage + x * RU_IMG, n0 + 32 * x, h, c * C, b);
                     bulk_commit();
                     bulk_wait_read_all();
                     mbar_arrive(&sb->stage_free);
@@ -340,7 +337,6 @@ __global__ void __launch_bounds__(SCAN_THREADS<SL>, 1) delta_scan_kernel(const _
                 ok = wait(&sb->stage_free, 0);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 frag_put_rows(stage + c0 / 32 * RU_IMG, t16, lane, f);
-                frag_put_rows(stage + (2 + c0 / 32) * RU_IMG, t16, lane, o);
                 hand_over(&sb->rows_staged, lane);
             }
             ok = wait(&sb->d3[s], c & 1);
@@ -405,7 +401,6 @@ template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
     if (a.states) {
         const long long ld = (long long)a.Hv * a.Dv;
         if (e == cudaSuccess) e = encode_rows(&m.e, true, a.e, ld, a.B, a.L, a.Hv, a.Dv);
-        if (e == cudaSuccess) e = encode_rows(&m.o32, true, a.o32, ld, a.B, a.L, a.Hv, a.Dv);
         if (e == cudaSuccess) e = encode_states(&m.s, a.states, (long long)a.B * a.Hv * (chunks(a.L) + 1), DK, a.Dv);
     }
     Args all = a;

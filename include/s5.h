@@ -381,9 +381,9 @@ s5_status s5_ssm_backward(const float *lambda, const float *log_dt, const float 
  * ======================================================================== */
 
 /* Bytes of the `saved` buffer that s5_delta_forward fills for
- * s5_delta_backward (e_t, o_t in 32 bits, the state every 64 tokens), and of
- * the workspaces of the two calls (scratch, no initialisation).  0 for
- * arguments that the calls reject. */
+ * s5_delta_backward (e_t in 32 bits, room for as many values that is not used
+ * at present, the state every 64 tokens), and of the workspaces of the two
+ * calls (scratch, no initialisation).  0 for arguments that the calls reject. */
 size_t s5_delta_saved_size(int B, int L, int Hv, int Dk, int Dv);
 size_t s5_delta_workspace_size(int B, int L, int Hv, int Dk, int Dv, int backward);
 

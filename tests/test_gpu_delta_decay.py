@@ -34,7 +34,8 @@ def close_by_decay(got, exact, g):
         assert off <= DG, (x, off)
 
 
-SHAPES = [(1, 150, 1, 11, 48, 80, torch.bfloat16), (1, 150, 1, 11, 64, 64, torch.float32),
+SHAPES = [(1, 150, 1, 11, 128, 128, torch.bfloat16), (2, 100, 1, 11, 64, 128, torch.bfloat16), (1, 64, 11, 22, 128, 64, torch.bfloat16),
+          (1, 130, 1, 11, 64, 64, torch.bfloat16), (1, 150, 1, 11, 48, 80, torch.bfloat16), (1, 150, 1, 11, 64, 64, torch.float32),
           (1, 90, 1, 11, 132, 20, torch.float32), (1, 65, 1, 11, 36, 256, torch.float32)]
 
 
