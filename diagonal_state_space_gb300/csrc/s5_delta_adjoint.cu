@@ -336,6 +336,10 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
 // its SM.
 // ---------------------------------------------------------------------------
 constexpr int LT = 512;
+// Warps with an errand besides: one issues the products, one adds up the decays'
+// gradients and then copies the next adjoint over the sums it read.  Both have
+// query rows and a block of [W; N] off the diagonal, the least work otherwise.
+constexpr int ISSUE = 3, TAIL = 14;
 
 template <int DK, int DV> struct LocalSmem {
     static constexpr uint32_t KQ = KQ_BOX * (DK / 64);
@@ -364,7 +368,7 @@ template <int DK, int DV> struct LocalSmem {
 };
 
 struct LocalBars {
-    uint64_t z_full, first, second, third;
+    uint64_t z_full, first, second, third, fourth;
     uint32_t tmem;
     int abort;
 };
@@ -477,6 +481,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         mbar_init(&lb->first, 1);
         mbar_init(&lb->second, 1);
         mbar_init(&lb->third, 1);
+        mbar_init(&lb->fourth, 1);
         lb->abort = 0;
         fence_mbar_init();
     }
@@ -525,7 +530,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         for (int j = 0; j < group; ++j, phase ^= 1) {
             const int h = hk * group + j;
             const long long bh = (long long)b * a.Hv + h;
-            if (tid == 0) {
+            if (warp == TAIL && lane == 0) {
                 mbar_arrive_tx(&lb->z_full, 2 * L::S_IMG + META_BYTES);
                 const unsigned char *z = static_cast<const unsigned char *>(a.z) + (bh * N + c) * (2 * L::S_IMG);
                 for (int x = 0; x < DV / 64; ++x)
@@ -566,7 +571,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
             fence_proxy_async_smem();
             __syncthreads();
             const uint32_t id = idesc_bf16_f32(128, DK), idU = idesc_bf16_f32(128, 64);
-            if (warp == 0) {
+            if (warp == ISSUE) {
                 if (elect_one()) {
                     // small products first
                     auto dot = [&](uint32_t d, uint64_t x, uint64_t u, bool first) {
@@ -634,12 +639,14 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                 const float near = expf((eh - meta->hi[mine]) + (el - meta->lo[mine]));
                 const float sign = keys ? -1.0f : a.scale, far = nb < rb ? sign * expf((gh - eh) + (gl - el)) : 0.0f;
                 const bool own = nb == rb, any = __any_sync(0xffffffffu, own);
+                float e[8] = {};
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int col = cb + i;
-                    float d = far * __shfl_sync(0xffffffffu, near, i);
-                    if (any)
-                        if (const float e = expf((gh - meta->hi[col]) + (gl - meta->lo[col])); own) d = sign * e;
+                    if (any && i % 8 == 0)   // eight at a time in flight
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) e[k] = expf((gh - meta->hi[col + k]) + (gl - meta->lo[col + k]));
+                    const float f = far * __shfl_sync(0xffffffffu, near, i), d = own ? sign * e[i % 8] : f;
                     // a masked product may be infinite: it is not multiplied by 0
                     w[i] = (keys ? col < tk : col <= tk) ? d * w[i] : 0.0f;
                     mm[i] = col < tk ? w[i] * mm[i] : 0.0f;
@@ -679,15 +686,9 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
             tc_fence_before();
             __syncthreads();
             tc_fence_after();
-            if (warp == 0 && elect_one()) {
+            if (warp == ISSUE && elect_one()) {
                 const uint32_t idB = id | B_MN, idAB = idB | A_MN, idE = idesc_bf16_f32(128, DV) | B_MN;
                 const uint64_t SE = desc_mn(sS, DK * 128), SL = desc_mn(s3, DK * 128);
-#pragma unroll
-                for (int p = 2; p >= 0; --p)
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        mma_bf16(E1, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), p == 2 ? on(SL, k * MN_STEP) : on(SE, p * L::S_IMG + k * MN_STEP),
-                                 idE, !(p == 2 && k == 0));
 #pragma unroll
                 for (int p = 1; p >= 0; --p) {
 #pragma unroll
@@ -706,6 +707,13 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                             mma_bf16(D1, on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP),
                                      on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id, !(ps == 1 && p == 0 && k == 0));
                 mma_commit(&lb->third);
+#pragma unroll
+                for (int p = 2; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k)
+                        mma_bf16(E1, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), p == 2 ? on(SL, k * MN_STEP) : on(SE, p * L::S_IMG + k * MN_STEP),
+                                 idE, !(p == 2 && k == 0));
+                mma_commit(&lb->fourth);
             }
             __syncwarp();
             // M's sums: mm[i] becomes the row's sum up to column cb + i - 1, for the
@@ -718,6 +726,32 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                 total += v;
             }
             const float crossing = sum16(mm, lane), rest = later_lanes(total, lane);
+            float bj[2] = {}, inner = 0.0f;   // the tail's terms from the adjoint
+            if (warp == TAIL) {
+                constexpr int WP = write_parts(DV), IP = inner_parts(DK, DV);
+                if (lane < IP) inner = a.inner[(bh * N + c) * IP + lane];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int p = 0; p < WP; ++p) bj[i] += a.writes[((bh * N + c) * C + lane + 32 * i) * WP + p];
+            }
+            ok = wait(&lb->third, phase) && ok;
+            tc_fence_after();
+            if (c0 < DK) {
+                float x[32];
+                const float wd = keys ? -up : a.scale * up;
+                load_parts<1, 32>(D1 + quarter + c0, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[i] = fmaf(wd, x[i], sum[i]);
+                load_parts<1, 32>(D4 + quarter + c0, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[i] += x[i];
+                if (keys) {
+                    load_parts<1, 32>(D5 + quarter + c0, x);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[i] += x[i];
+                }
+            }
             // dv of this warp's fragments of E1 is on its way
             float2 dx[2][8];
             if (keys && c0 < DV)
@@ -729,7 +763,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                         dx[f][i] = t < nt ? *reinterpret_cast<const float2 *>(a.x + ((row0 + t) * a.Hv + h) * DV + c0 + 8 * (i % 4) + 2 * (lane & 3))
                                           : make_float2(0.0f, 0.0f);
                     }
-            ok = wait(&lb->third, phase) && ok;
+            ok = wait(&lb->fourth, phase) && ok;
             tc_fence_after();
             float y[2][2] = {};   // E1's rows by dv or dO
             if (c0 < DV)
@@ -748,21 +782,6 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                         for (int i = 0; i < 16; ++i) y[f][(i >> 1) & 1] = fmaf(x[i], g[i], y[f][(i >> 1) & 1]);
                     }
                 }
-            if (c0 < DK) {
-                float x[32];
-                const float wd = keys ? -up : a.scale * up;
-                load_parts<1, 32>(D1 + quarter + c0, x);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) sum[i] = fmaf(wd, x[i], sum[i]);
-                load_parts<1, 32>(D4 + quarter + c0, x);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) sum[i] += x[i];
-                if (keys) {
-                    load_parts<1, 32>(D5 + quarter + c0, x);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) sum[i] += x[i];
-                }
-            }
             // the products are done with the state: its place takes the sums
             if ((lane & 1) == 0) part[warp][lane / 2] = crossing;
             suffix[warp][lane] = rest;
@@ -781,31 +800,29 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
             tc_fence_before();
             __syncthreads();
             tc_fence_after();
-            if (warp == 0) {   // tokens `lane` and `lane` + 32
-                float ai[2] = {}, bj[2] = {}, pairs[2] = {}, m = 0.0f;
-                constexpr int WP = write_parts(DV), IP = inner_parts(DK, DV);
-                if (lane < IP) m = a.inner[(bh * N + c) * IP + lane];
+            if (warp == TAIL) {   // tokens `lane` and `lane` + 32
+                float ai[2] = {}, pairs[2] = {};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int t = lane + 32 * i;
 #pragma unroll
-                    for (int p = 0; p < WP; ++p) bj[i] += a.writes[((bh * N + c) * C + t) * WP + p];
-#pragma unroll
                     for (int g = 0; g < DV / 32; ++g) ai[i] += reads[t][g] + reads[C + t][g];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) pairs[i] += part[t / 16 * 4 + q][t % 16];
-                    for (int n = 0; n < t / 16; ++n) {   // whole blocks before the token's
-                        pairs[i] += suffix[4 * n + i][lane] + suffix[4 * n + 2 + i][lane];
-                        if (i == 0) pairs[i] += suffix[4 * n + 1][0] + suffix[4 * n + 3][0];
-                    }
+#pragma unroll
+                    for (int n = 0; n < 2 * i + 1; ++n)   // whole blocks before the token's
+                        if (n < t / 16) {
+                            pairs[i] += suffix[4 * n + i][lane] + suffix[4 * n + 2 + i][lane];
+                            if (i == 0) pairs[i] += suffix[4 * n + 1][0] + suffix[4 * n + 3][0];
+                        }
                 }
-                m = meta->last * warp_sum(m);
+                const float m = meta->last * warp_sum(inner);
                 // a from the token on, b up to it
                 const float a1 = later_lanes(ai[1], lane), a0 = later_lanes(ai[0], lane) + __shfl_sync(0xffffffffu, a1, 0);
                 const float b0 = earlier_lanes(bj[0], lane), b1 = earlier_lanes(bj[1], lane) + warp_sum(bj[0]);
                 if (lane < nt) a.dg[(row0 + lane) * a.Hv + h] = (a0 + b0) + (m + pairs[0]);
                 if (lane + 32 < nt) a.dg[(row0 + lane + 32) * a.Hv + h] = (a1 + b1) + (m + pairs[1]);
-                __syncwarp();
+                __syncwarp();   // then the next adjoint is copied over what was read here
             }
         }
         // out by way of shared memory (A's place), whole rows at a time
