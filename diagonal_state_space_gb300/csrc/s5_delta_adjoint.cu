@@ -250,23 +250,11 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
             frag_scale(f, meta->down[ta], meta->down[tb]);
             frag_put3(ops, RU_IMG, t16, c0, lane, f);
             hand_over(&sb->r_ready, lane);
-            {   // this slice's share of b_j = e^{G_64 - G_j} (Z^T k_j).u_j, for the decays
-                float w[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[i] = fmaf(f[4 * j + 2 * i], e[4 * i + j].x, fmaf(f[4 * j + 2 * i + 1], e[4 * i + j].y, w[i]));
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    w[i] += __shfl_xor_sync(0xffffffffu, w[i], 1);
-                    w[i] += __shfl_xor_sync(0xffffffffu, w[i], 2);
-                    if ((lane & 3) == 0)
-                        a.writes[((bh * N + c) * C + ta + 8 * i) * write_parts(a.Dv) + blockIdx.x * 2 + warp / 4] = meta->beta[ta + 8 * i] * w[i];
-                }
-            }
             const float last = meta->last, ua = meta->up[ta], ub = meta->up[tb];
-            const float ya = -ua * meta->beta[ta], yb = -ub * meta->beta[tb];
+            const float ba = meta->beta[ta], bb = meta->beta[tb], ya = -ua * ba, yb = -ub * bb;
+            float kz[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) kz[i] = f[i];
             frag_get(go, t16, c0, lane, f);
             frag_scale(f, a.scale * ua, a.scale * ub);
             frag_put3(ops + 3 * RU_IMG, RU_IMG, t16, c0, lane, f);
@@ -284,6 +272,22 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
             if (!__all_sync(0xffffffffu, ok)) break;
             frag_put_rows(xs + c0 / 32 * RU_IMG, t16, lane, f);
             hand_over(&sb->x_ready, lane);
+            {   // this slice's share of b_j = e^{G_64 - G_j} (Z^T k_j).u_j, for the decays,
+                // while D3 runs
+                float w[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[i] = fmaf(kz[4 * j + 2 * i], e[4 * i + j].x, fmaf(kz[4 * j + 2 * i + 1], e[4 * i + j].y, w[i]));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    w[i] += __shfl_xor_sync(0xffffffffu, w[i], 1);
+                    w[i] += __shfl_xor_sync(0xffffffffu, w[i], 2);
+                    if ((lane & 3) == 0)
+                        a.writes[((bh * N + c) * C + ta + 8 * i) * write_parts(a.Dv) + blockIdx.x * 2 + warp / 4] = (i ? bb : ba) * w[i];
+                }
+            }
             ok = wait(&sb->d3, it & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -348,20 +352,21 @@ template <int DK, int DV> struct LocalSmem {
     static constexpr uint32_t S_IMG = DK * 128 * (DV / 64);
     static constexpr uint32_t kq = 0;                          // 64 keys, then 64 queries
     static constexpr uint32_t a = kq + KQ;                     // two parts
-    static constexpr uint32_t u = a + 2 * A_IMG;               // two parts; where they fit, those of [W; N] later
-    static constexpr bool APART = U_IMG < M2_BYTES;            // [W; N] gets a place of its own
-    static constexpr uint32_t wn = APART ? u + 2 * U_IMG : u;
-    static constexpr uint32_t s = wn + 2 * (APART ? M2_BYTES : U_IMG);   // Z, then S0: two parts
-    // third parts: of dv and behind them of U, later of S0
-    static constexpr uint32_t dv3 = s + 2 * S_IMG, u3 = dv3 + U_IMG, s3 = dv3;
-    static constexpr uint32_t meta = u3 + U_IMG;
+    static constexpr uint32_t u = a + 2 * A_IMG;               // a box's three parts side by side
+    static constexpr uint32_t dv3 = u + 3 * U_IMG;             // dv's third part
+    // later: the two parts of [W; N] in the place of U, where they fit, and S0's third part behind them
+    static constexpr bool APART = U_IMG < M2_BYTES;
+    static constexpr uint32_t wn = APART ? dv3 + U_IMG : u;
+    static constexpr uint32_t s3 = u + 2 * U_IMG;
+    static constexpr uint32_t s = APART ? wn + 2 * M2_BYTES : dv3 + U_IMG;   // Z, then S0: a box's two parts side by side
+    static constexpr uint32_t meta = s + 2 * S_IMG;
     static constexpr uint32_t bars = meta + META_BYTES;
     static constexpr uint32_t total = bars + 64 + 1024;
     static_assert(total <= 232448, "shared memory of a CTA");
     static_assert(S_IMG <= 2 * U_IMG, "S0's third part fits");
     // products of M = 128 over 64 rows or columns read on into what follows:
     // 8 KB past U and dv's third part, 16 KB past [W; N]
-    static_assert(2 * S_IMG >= M2_BYTES && U_IMG >= 64 * 128, "what the products read on is the CTA's own memory");
+    static_assert(2 * S_IMG >= M2_BYTES, "what the products read on is the CTA's own memory");
     // sums on their way to the decays' gradients, in the state's place after its products
     static constexpr uint32_t part = s, suffix = part + 16 * 16 * 4, rows = suffix + 16 * 32 * 4;
     static_assert(rows + 128 * 4 * 4 <= s + 2 * S_IMG, "they fit");
@@ -496,9 +501,9 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
     tc_fence_after();
     const uint32_t kq = smem_addr(smem + L::kq), sA = smem_addr(smem + L::a), sU = smem_addr(smem + L::u),
                    sS = smem_addr(smem + L::s), sW = smem_addr(smem + L::wn), dv3 = smem_addr(smem + L::dv3),
-                   u3 = smem_addr(smem + L::u3), s3 = smem_addr(smem + L::s3);
-    // KK lies where D1 will, E1 where D2 has been, D3 (and dv's third part by U, D3L) where D5 will
-    const uint32_t tmem = lb->tmem, D1 = tmem, D2 = tmem + 128, D4 = tmem + 256, D3 = tmem + 384, D3L = tmem + 448, D5 = tmem + 384,
+                   s3 = smem_addr(smem + L::s3);
+    // KK lies where D1 will, E1 where D2 has been, D3 (and dv's third part by U, D3L) where D4 and D5 will
+    const uint32_t tmem = lb->tmem, D1 = tmem, D2 = tmem + 128, D4 = tmem + 256, D3 = tmem + 256, D3L = tmem + 448, D5 = tmem + 384,
                    KK = tmem, E1 = tmem + 128;
     const uint64_t A0 = desc_k(sA), W0 = desc_k(sW), WT = desc_mn(sW, M2_BYTES), U0 = desc_k(sU), S0 = desc_k(sS),
                    cols = desc_mn(kq, KQ_BOX), rows = desc_k(kq);
@@ -518,8 +523,9 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
         const int c = item % N, hk = item / N % a.Hk, b = item / N / a.Hk;
         const int t0 = c * C, nt = min(C, a.L - t0);
         const long long row0 = (long long)b * a.L + t0;
-        for (int i = tid; i < 128 * (DK / 8); i += LT) {
-            const int r = i / (DK / 8), d = i % (DK / 8) * 8, t = r & 63;
+#pragma unroll
+        for (int n = 0; n < 128 * (DK / 8) / LT; ++n) {
+            const int i = tid + n * LT, r = i / (DK / 8), d = i % (DK / 8) * 8, t = r & 63;
             uint4 v = make_uint4(0, 0, 0, 0);
             if (t < nt)
                 v = r < C ? *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k) + (row0 + t) * a.ldk + hk * DK + d)
@@ -535,7 +541,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                 const unsigned char *z = static_cast<const unsigned char *>(a.z) + (bh * N + c) * (2 * L::S_IMG);
                 for (int x = 0; x < DV / 64; ++x)
                     for (int p = 0; p < 2; ++p)
-                        bulk_load(smem + L::s + p * L::S_IMG + x * (DK * 128), z + (2 * x + p) * (DK * 128), DK * 128, &lb->z_full);
+                        bulk_load(smem + L::s + (2 * x + p) * (DK * 128), z + (2 * x + p) * (DK * 128), DK * 128, &lb->z_full);
                 bulk_load(meta, static_cast<const unsigned char *>(a.images) + (bh * N + c) * IMG_BYTES + MAT_BYTES, META_BYTES, &lb->z_full);
             }
 #pragma unroll
@@ -557,7 +563,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                 }
                 const int box = d / 64, at = d % 64 / 8;
                 put3(sA + box * M2_BYTES, L::A_IMG, dv3 + box * RU_IMG, t, at, x);
-                put3(sU + box * RU_IMG, L::U_IMG, u3 + box * RU_IMG, t, at, e);
+                put3(sU + box * 3 * RU_IMG, RU_IMG, sU + (box * 3 + 2) * RU_IMG, t, at, e);
                 sts128(piece(sA + box * M2_BYTES, C + t, at), g.x, g.y, g.z, g.w);
                 sts128(piece(sA + L::A_IMG + box * M2_BYTES, C + t, at), 0, 0, 0, 0);   // dO is bf16: no second part
 #pragma unroll
@@ -573,20 +579,17 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
             const uint32_t id = idesc_bf16_f32(128, DK), idU = idesc_bf16_f32(128, 64);
             if (warp == ISSUE) {
                 if (elect_one()) {
-                    // small products first
-                    auto dot = [&](uint32_t d, uint64_t x, uint64_t u, bool first) {
-#pragma unroll
-                        for (int k = 0; k < DV / 16; ++k)
-                            mma_bf16(d, on(x, k / 4 * M2_BYTES + k % 4 * K_STEP), on(u, k / 4 * RU_IMG + k % 4 * K_STEP), idU, !(first && k == 0));
-                    };
-                    dot(D3, A0, desc_k(u3), true);
-                    dot(D3, on(A0, L::A_IMG), on(U0, L::U_IMG), false);
-                    dot(D3, A0, on(U0, L::U_IMG), false);
-                    dot(D3, on(A0, L::A_IMG), U0, false);
-                    dot(D3, A0, U0, false);
+                    // U's parts are columns of one product each; D3's blocks are added when they are read
+                    const uint32_t id3 = idesc_bf16_f32(128, 192), id2 = idesc_bf16_f32(128, 128);
 #pragma unroll
                     for (int k = 0; k < DV / 16; ++k)
-                        mma_bf16(D3L, on(desc_k(dv3), k / 4 * RU_IMG + k % 4 * K_STEP), on(U0, k / 4 * RU_IMG + k % 4 * K_STEP), idU, k > 0);
+                        mma_bf16(D3, on(A0, k / 4 * M2_BYTES + k % 4 * K_STEP), on(U0, k / 4 * 3 * RU_IMG + k % 4 * K_STEP), id3, k > 0);
+#pragma unroll
+                    for (int k = 0; k < DV / 16; ++k)
+                        mma_bf16(D3, on(A0, L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP), on(U0, k / 4 * 3 * RU_IMG + k % 4 * K_STEP), id2, 1);
+#pragma unroll
+                    for (int k = 0; k < DV / 16; ++k)
+                        mma_bf16(D3L, on(desc_k(dv3), k / 4 * RU_IMG + k % 4 * K_STEP), on(U0, k / 4 * 3 * RU_IMG + k % 4 * K_STEP), idU, k > 0);
 #pragma unroll
                     for (int k = 0; k < DK / 16; ++k) {
                         const uint64_t K = on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP);
@@ -604,8 +607,8 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                             for (int p = 0; p <= ps; ++p)
 #pragma unroll
                                 for (int k = 0; k < DV / 16; ++k)
-                                    mma_bf16(D2, on(U0, p * L::U_IMG + k / 4 * RU_IMG + k % 4 * K_STEP),
-                                             on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id,
+                                    mma_bf16(D2, on(U0, p * RU_IMG + k / 4 * 3 * RU_IMG + k % 4 * K_STEP),
+                                             on(S0, (ps - p) * (DK * 128) + k / 4 * (2 * DK * 128) + k % 4 * K_STEP), id,
                                              !(ps == 1 && p == 0 && k == 0));
                     }
                     mma_commit(&lb->second);
@@ -627,7 +630,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
             float w[16], mm[16];
             {
                 const int rb = tk >> 4;
-                load_parts<1, 16>(D3 + quarter + cb, w);
+                load_parts<3, 16>(D3 + quarter + cb, w);
                 if (keys) {
                     load_parts<1, 16>(D3L + quarter + cb, mm);
 #pragma unroll
@@ -652,6 +655,16 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                     mm[i] = col < tk ? w[i] * mm[i] : 0.0f;
                 }
             }
+            // M's sums: mm[i] becomes the row's sum up to column cb + i - 1, for the
+            // token cb + i where it is at or before the row
+            float total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float v = mm[i];
+                mm[i] = tk >= cb + i ? total : 0.0f;
+                total += v;
+            }
+            const float crossing = sum16(mm, lane), rest = later_lanes(total, lane);
             // S0 is on its way while the second products run
             const float *s0 = a.states + (bh * (N + 1) + c) * mat;
             constexpr int SN = DK * DV / 8 / LT;
@@ -668,7 +681,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                 const int i = tid + n * LT, r = i / PR, d = i % PR * 8;
                 const float v[8] = {sr[2 * n].x,     sr[2 * n].y,     sr[2 * n].z,     sr[2 * n].w,
                                     sr[2 * n + 1].x, sr[2 * n + 1].y, sr[2 * n + 1].z, sr[2 * n + 1].w};
-                put3(sS + d / 64 * (DK * 128), L::S_IMG, s3 + d / 64 * (DK * 128), r, d % 64 / 8, v);
+                put3(sS + d / 64 * (2 * DK * 128), DK * 128, s3 + d / 64 * (DK * 128), r, d % 64 / 8, v);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
@@ -688,7 +701,7 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
             tc_fence_after();
             if (warp == ISSUE && elect_one()) {
                 const uint32_t idB = id | B_MN, idAB = idB | A_MN, idE = idesc_bf16_f32(128, DV) | B_MN;
-                const uint64_t SE = desc_mn(sS, DK * 128), SL = desc_mn(s3, DK * 128);
+                const uint64_t SE = desc_mn(sS, 2 * DK * 128), SL = desc_mn(s3, DK * 128);
 #pragma unroll
                 for (int p = 1; p >= 0; --p) {
 #pragma unroll
@@ -705,27 +718,17 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
 #pragma unroll
                         for (int k = 0; k < DV / 16; ++k)
                             mma_bf16(D1, on(A0, p * L::A_IMG + k / 4 * M2_BYTES + k % 4 * K_STEP),
-                                     on(S0, (ps - p) * L::S_IMG + k / 4 * (DK * 128) + k % 4 * K_STEP), id, !(ps == 1 && p == 0 && k == 0));
+                                     on(S0, (ps - p) * (DK * 128) + k / 4 * (2 * DK * 128) + k % 4 * K_STEP), id, !(ps == 1 && p == 0 && k == 0));
                 mma_commit(&lb->third);
 #pragma unroll
                 for (int p = 2; p >= 0; --p)
 #pragma unroll
                     for (int k = 0; k < DK / 16; ++k)
-                        mma_bf16(E1, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), p == 2 ? on(SL, k * MN_STEP) : on(SE, p * L::S_IMG + k * MN_STEP),
+                        mma_bf16(E1, on(rows, k / 4 * KQ_BOX + k % 4 * K_STEP), p == 2 ? on(SL, k * MN_STEP) : on(SE, p * (DK * 128) + k * MN_STEP),
                                  idE, !(p == 2 && k == 0));
                 mma_commit(&lb->fourth);
             }
             __syncwarp();
-            // M's sums: mm[i] becomes the row's sum up to column cb + i - 1, for the
-            // token cb + i where it is at or before the row
-            float total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float v = mm[i];
-                mm[i] = tk >= cb + i ? total : 0.0f;
-                total += v;
-            }
-            const float crossing = sum16(mm, lane), rest = later_lanes(total, lane);
             float bj[2] = {}, inner = 0.0f;   // the tail's terms from the adjoint
             if (warp == TAIL) {
                 constexpr int WP = write_parts(DV), IP = inner_parts(DK, DV);
@@ -752,17 +755,6 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                     for (int i = 0; i < 32; ++i) sum[i] += x[i];
                 }
             }
-            // dv of this warp's fragments of E1 is on its way
-            float2 dx[2][8];
-            if (keys && c0 < DV)
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int t = (row - lane) + 16 * f + lane / 4 + 8 * (i / 4);
-                        dx[f][i] = t < nt ? *reinterpret_cast<const float2 *>(a.x + ((row0 + t) * a.Hv + h) * DV + c0 + 8 * (i % 4) + 2 * (lane & 3))
-                                          : make_float2(0.0f, 0.0f);
-                    }
             ok = wait(&lb->fourth, phase) && ok;
             tc_fence_after();
             float y[2][2] = {};   // E1's rows by dv or dO
@@ -772,9 +764,16 @@ template <int DK, int DV> __global__ void __launch_bounds__(LT, 1) delta_local_k
                     float x[16];
                     frag_load<1>(E1 + quarter + c0 + (f ? QUERY_LANES : 0u), x);
                     if (keys) {
+                        float2 dx[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int t = (row - lane) + 16 * f + lane / 4 + 8 * (i / 4);
+                            dx[i] = t < nt ? *reinterpret_cast<const float2 *>(a.x + ((row0 + t) * a.Hv + h) * DV + c0 + 8 * (i % 4) + 2 * (lane & 3))
+                                           : make_float2(0.0f, 0.0f);
+                        }
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            y[f][i / 4] = fmaf(x[4 * (i % 4) + 2 * (i / 4)], dx[f][i].x, fmaf(x[4 * (i % 4) + 2 * (i / 4) + 1], dx[f][i].y, y[f][i / 4]));
+                            y[f][i / 4] = fmaf(x[4 * (i % 4) + 2 * (i / 4)], dx[i].x, fmaf(x[4 * (i % 4) + 2 * (i / 4) + 1], dx[i].y, y[f][i / 4]));
                     } else {
                         float g[16];
                         frag_get(sA + c0 / 64 * M2_BYTES, row - lane + 16 * f, c0 % 64, lane, g);
