@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
         }
         const int t0 = (REV ? stages - 1 - st : st) * NT, nt = min(NT, a.L - t0);
         const long long row0 = (long long)b * a.L + t0;
+        float *const ke = a.e ? a.e + (row0 * a.Hv + h) * a.Dv + col : nullptr;
         // a stage lies within a chunk
         if (!REV && a.states && t0 % CHUNK == 0) keep(a.states + (bh * (N + 1) + t0 / CHUNK) * mat);
         if (REV && ((t0 + nt) % CHUNK == 0 || t0 + nt == a.L)) keep(static_cast<float *>(a.z) + (bh * N + t0 / CHUNK) * mat);
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
                 }
                 if (first) {
                     store_elem<T>(static_cast<T *>(a.o) + (row0 + t) * a.ldo + (long long)h * a.Dv + col, o);
-                    if (a.e) a.e[out] = e;
+                    if (ke) ke[(long long)t * a.Hv * a.Dv] = e;
                 }
             } else {
 #pragma unroll
