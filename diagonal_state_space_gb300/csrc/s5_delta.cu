@@ -46,8 +46,8 @@ constexpr int OWN = 32;       // rows of a block
 // Blocks of 8 columns up to which the column sweep uses them, against blocks of
 // 32 (one read of the keys for four times the columns, but a fourth of the SMs
 // when heads are few).  Forward, 400 tokens, 8 / 32 columns, us: 128 x 128 heads,
-// 83 / 131 at 64 blocks, 109 / 133 at 256, 211 / 132 at 512; 64 x 64, 73 / 89 at
-// 64, 89 / 89 at 256, 159 / 90 at 512.
+// 77 / 119 at 64 blocks, 103 / 120 at 256, 204 / 120 at 512; 64 x 64, 66 / 82 at
+// 64, 81 / 83 at 256, 92 / 83 at 512.
 constexpr int NARROW_BLOCKS = 256;
 constexpr int SWT = 128;      // threads of a sweep
 // Heads (B Hv) from which on a step takes a block for each, against a block for
@@ -84,7 +84,7 @@ template <typename T> __device__ __forceinline__ float elem(const void *p, long 
 // adjoint at each chunk's end.  A column is held by 8 lanes, rows 32 i + 4 lane +
 // 0..3 (one 16-byte read of a key for four rows), a block has C columns; two more
 // warps stage the tokens.  Bound by the chain from token to token (smem read,
-// products, three shuffles, update): 0.19 us a token forward, 0.13 back at heads of
+// products, three shuffles, update): 0.17 us a token forward, 0.11 back at heads of
 // 64 x 64, whatever their number while the blocks fit the SMs.
 template <typename T, int RPT, int C, bool REV>
 __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) {
@@ -389,7 +389,9 @@ template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(
 // (four rows and columns a thread, slices of 16 of the depth staged in shared
 // memory, the next slice on its way); M's rows are then summed along j, its
 // columns along i, both from nothing, so that no term is taken away again.  Bound by
-// the products, in 32 bits on the CUDA cores as all of this path.
+// the products, in 32 bits on the CUDA cores as all of this path, and by the latency of
+// their slices where blocks are few: 2 x 500 tokens of 4 heads of 64 x 64 in 22 us
+// (the whole call with its forward pass 190; 187 when dg came of o.do - v.dv).
 constexpr int GT = 512, GS = 16, GP = 68;
 template <typename T> __global__ void __launch_bounds__(GT) decay_grads_kernel(const Args a) {
     __shared__ __align__(16) float tiles[2][4][GS][GP];

@@ -13,8 +13,9 @@
 // (formula in s5_delta.cu) <S, Z> and the b_j are taken in 32 bits on the way.
 //
 // Bound: as the forward scan, the chain product -> sums, splits -> product three
-// times a chunk, 4.1 us with 64 columns a CTA and the tiles of X, Z and the state
-// beside it: 4 sequences of 2048 tokens, 16 heads of 128, 131 us.
+// times a chunk, 4.2 us with 64 columns a CTA and the tiles of X, Z and the state
+// beside it: 4 sequences of 2048 tokens, 16 heads of 128, 134 us (131 without the
+// b_j, which are added up while D3 runs).
 //
 // All else is local to a chunk (delta_local_kernel).
 #include "s5_delta_mma.cuh"
@@ -337,7 +338,9 @@ template <int DK> __global__ void __launch_bounds__(ADJ_THREADS, 1) delta_adjoin
 // over lanes, while D1, D4, D5 and E1 run.
 // Bound: what it reads (the state, the adjoint and 64 tokens' X, e, dO: 208 KB per
 // chunk and head of 128 x 128), and the phases between its products in a CTA alone on
-// its SM.
+// its SM: 2048 chunks and heads in 197 us, 2.2 TB/s (161 us without the decays' sums;
+// 265 with D3 in products of 64 columns, the sums' registers spilled, and the same
+// warp issuing the products, finishing the decays and copying the adjoint).
 // ---------------------------------------------------------------------------
 constexpr int LT = 512;
 // Warps with an errand besides: one issues the products, one adds up the decays'

@@ -24,8 +24,7 @@
 //
 // Bound: the latency of the block steps between barriers, which three CTAs an SM
 // cover for one another (issue slots 43 % busy): 8 sequences of 1999 tokens, 32
-// heads of 128 on 16 key heads, 177 us, 8192 images of 50 KB at 2.3 TB/s; 8.3 us
-// for a single chunk.
+// heads of 128 on 16 key heads, 181 us, 8192 images of 50 KB at 2.3 TB/s.
 #include "s5_delta_mma.cuh"
 
 namespace s5 {
@@ -337,9 +336,9 @@ __global__ void __launch_bounds__(PT, 3) delta_prep_kernel(const __grid_constant
 
 // Blocks of a key head (chunk by chunk) up to which each is split into blocks of
 // one value head, which take its products again but not one after the other.
-// Heads of 128, a block a key head / a value head, us: 16 value heads on 8 key
-// heads, 8 chunks (64 blocks) 13.9 / 8.8, 24 chunks 17.7 / 14.2, 32 chunks (256)
-// 18.0 / 18.7; on 4 key heads, 32 chunks (128) 25.3 / 18.7.
+// Heads of 128, a block a key head / a value head, us of the whole forward call: 16
+// value heads on 8 key heads, 8 chunks (64 blocks) 32.8 / 28.0, 24 chunks 69.0 /
+// 65.0, 32 chunks (256) 86.1 / 87.3; on 4 key heads, 32 chunks (128) 92.9 / 85.8.
 constexpr int SPLIT_BLOCKS = 228;
 
 template <int DK, bool TRANS> cudaError_t launch(const Args &a, cudaStream_t st) {

@@ -33,7 +33,7 @@
 // there are enough heads to fill the SMs anyway.  With few heads slices of 32
 // columns shorten the chain (launch rule below): 2.1 us a chunk with heads of
 // 128, 2.8 in slices of 64, whatever the number of heads that fit at once.  In
-// two slices a CTA 8 sequences of 1999 tokens with 32 heads take 248 us, 277
+// two slices a CTA 8 sequences of 1999 tokens with 32 heads take 250 us, 275
 // TFLOP/s of the three products, each of which is three to six bf16 products.
 #include "s5_delta_mma.cuh"
 
@@ -380,18 +380,19 @@ template <int DK, int SL, bool KEEP, int NC> cudaError_t launch(const ScanMaps &
 
 // Where the scan leaves half of the SMs free, the first quarter of the chunks is
 // prepared and scanned, and the rest prepared beside that scan, from this many
-// chunks of all heads on (below, two more launches cost more).  One piece / two,
-// heads of 128, us: 16 heads, 32 chunks 91 / 96, 64 chunks 177 / 165, 256 chunks
-// 646 / 605; 8 heads, 256 chunks 595 / 575; 32 heads (128 of 152 SMs scan), 64
-// chunks 206 / 211.  A half or a sixth first: 620, 608 at 16 heads, 256 chunks.
+// chunks of all heads on (below, two more launches gain little or nothing).  One
+// piece / two, heads of 128, us: 16 heads, 32 chunks 86 / 83, 64 chunks 170 / 155,
+// 256 chunks 636 / 591; 8 heads, 256 chunks 586 / 562; 32 heads (128 of 152 SMs
+// scan), 64 chunks 199 / 203.  A half or a sixth first: 15 and 3 more at 16 heads, 256
+// chunks.
 constexpr int SPLIT_CHUNKS = 1024, SPLIT = 4;
 
 template <int DK> cudaError_t forward(const Args &a, cudaStream_t st) {
     ScanMaps m = {};
     // Slices of 32 columns where one CTA each still fits the SMs at once; two
     // slices a CTA where one would not.  10 chunks, heads of 128, one slice of 64
-    // / two / one of 32, us: 38 heads 31.8 / 40.3 / 23.6, 76 heads 32.3 / 40.9 /
-    // 47.5, 80 heads 62 / 41 / 68, 256 heads 133 / 88 / 176.
+    // / two / one of 32, us of the whole call: 38 heads 45 / 54 / 37, 76 heads 55 /
+    // 63 / 72, 80 heads 85 / 64 / 94, 256 heads 195 / 149 / 240.
     const long long heads = (long long)a.B * a.Hv;
     const bool narrow = !a.states && heads * (a.Dv / 32) <= 152;
     cudaError_t e = encode_rows(&m.k, false, a.k, a.ldk, a.B, a.L, a.Hk, DK, 16);

@@ -29,8 +29,10 @@
 //    of one token at once; their angles are worked out while they are on
 //    their way.
 // In both a lane holds both halves of its pairs, in either layout.  Norm and
-// rotation of 336 MB of bf16 (40 heads of 128): 59 us, 5.7 TB/s; with the backward
-// pass 537 MB in 127 us, 4.2 TB/s; rotation alone of 537 MB in 86 us, 6.3 TB/s.
+// rotation of 336 MB of bf16 (40 heads of 128): 60 us, 5.6 TB/s; with the backward
+// pass 537 MB in 131 us, 4.1 TB/s; rotation alone of 537 MB in 87 us, 6.2 TB/s.  (59,
+// 127 and 86 where a wait that ran out did not end the warp's work and frequencies
+// that are not finite were not looked for.)
 #include <atomic>
 
 #include "s5_internal.cuh"
