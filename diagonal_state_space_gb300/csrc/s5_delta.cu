@@ -365,111 +365,104 @@ __global__ void __launch_bounds__(2 * SWT) row_sweep_kernel(const Args a) {
     }
 }
 
-// One warp per token and value head: dv = beta X, dbeta = X . e.
-template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(const Args a) {
-    griddep_wait();
-    const long long hv = (long long)blockIdx.x * 8 + threadIdx.x / 32, rows = (long long)a.B * a.L * a.Hv;
-    const int lane = threadIdx.x % 32;
-    if (hv >= rows) return;
-    const long long row = hv / a.Hv;
-    const int h = (int)(hv % a.Hv);
-    const float be = a.beta[hv];
-    float db = 0.0f;
-    for (int c = lane; c < a.Dv; c += 32) {
-        const float x = a.x[hv * a.Dv + c];
-        db = fmaf(x, a.e[hv * a.Dv + c], db);
-        store_elem<T>(static_cast<T *>(a.dv) + row * a.lddv + (long long)h * a.Dv + c, be * x);
+// dg of a chunk and value head (the formula is at the top of this file), in
+// decay_parts parts that token_grads_kernel adds up: part 0 is M's, the others are
+// that of a, b and <S, Z> over 64 columns of the state each.  A part is a block of
+// its own: products of 64 x 64 tiles (four rows and columns a thread, slices of 16 of
+// the depth staged in shared memory, the next slice on its way).  M's rows are then
+// summed along j, its columns along i, both from nothing, so that no term is taken
+// away again.  Bound by the products, in 32 bits on the CUDA cores as all of this path.
+constexpr int GT = 256, GS = 16, GP = 68;
+int decay_parts(int Dv) { return 1 + (Dv + 63) / 64; }
+
+// Four consecutive values from p on; vec: p is aligned for one load.
+template <typename T> __device__ __forceinline__ float4 four(const T *p, bool vec) {
+    if constexpr (sizeof(T) == 4) {
+        if (vec) return *reinterpret_cast<const float4 *>(p);
+    } else if (vec) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xffff0000u));
     }
-    db = warp_sum(db);
-    if (lane == 0) a.dbeta[hv] = db;
+    return make_float4(load_elem<T>(p), load_elem<T>(p + 1), load_elem<T>(p + 2), load_elem<T>(p + 3));
 }
 
-// dg of a chunk and value head (the formula is at the top of this file).  Half of
-// a block forms M, the other half a, b and <S, Z>, both as products of 64 x 64 tiles
-// (four rows and columns a thread, slices of 16 of the depth staged in shared
-// memory, the next slice on its way); M's rows are then summed along j, its
-// columns along i, both from nothing, so that no term is taken away again.  Bound by
-// the products, in 32 bits on the CUDA cores as all of this path, and by the latency of
-// their slices where blocks are few: 2 x 500 tokens of 4 heads of 64 x 64 in 22 us
-// (the whole call with its forward pass 190; 187 when dg came of o.do - v.dv).
-constexpr int GT = 512, GS = 16, GP = 68;
-template <typename T> __global__ void __launch_bounds__(GT) decay_grads_kernel(const Args a) {
-    __shared__ __align__(16) float tiles[2][4][GS][GP];
-    __shared__ float hi[CHUNK], lo[CHUNK], av[CHUNK], bv[CHUNK], mv[GT / 64];
+template <typename T> __global__ void __launch_bounds__(GT, 2) decay_grads_kernel(const Args a, int parts) {
+    __shared__ __align__(16) float st[4][GS][GP];
+    __shared__ float hi[CHUNK], lo[CHUNK], av[CHUNK], bv[CHUNK], mv[GT / 32];
     constexpr int MP = CHUNK + 1;
-    float *M = &tiles[0][0][0][0];   // [64][MP], in the place of the first half's tiles
+    float *M = &st[0][0][0];   // [64][MP], in the place of the tiles
     static_assert(CHUNK * MP <= 4 * GS * GP, "M fits");
-    const int c = blockIdx.x, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
-    const int half = threadIdx.x / 256, tid = threadIdx.x % 256, ti = tid / 16 * 4, tj = tid % 16 * 4;
+    const int c = blockIdx.x / parts, part = blockIdx.x % parts, h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hv / a.Hk);
+    const int tid = threadIdx.x, ti = tid / 16 * 4, tj = tid % 16 * 4;
     const int N = chunks(a.L), t0 = c * CHUNK, nt = min(CHUNK, a.L - t0);
     const long long row0 = (long long)b * a.L + t0, bh = (long long)b * a.Hv + h, mat = (long long)a.Dk * a.Dv;
-    auto(&st)[4][GS][GP] = tiles[half];
-    auto meet = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + half) : "memory"); };
     griddep_wait();
-    if (threadIdx.x < 32) {
+    if (tid < 32) {
         float G[2], g[2];
-        decay_sums(a, row0, nt, h, threadIdx.x, G, g);
+        decay_sums(a, row0, nt, h, tid, G, g);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) hi[2 * threadIdx.x + i] = G[i], lo[2 * threadIdx.x + i] = g[i];
+        for (int i = 0; i < 2; ++i) hi[2 * tid + i] = G[i], lo[2 * tid + i] = g[i];
     }
-    __syncthreads();
-    // values of token t: keys, queries; dL/do; u and dv
-    auto key = [&](int t, int d) { return t < nt && d < a.Dk ? elem<T>(a.k, (row0 + t) * a.ldk + hk * a.Dk + d) : 0.0f; };
-    auto query = [&](int t, int d) { return t < nt && d < a.Dk ? elem<T>(a.q, (row0 + t) * a.ldq + hk * a.Dk + d) : 0.0f; };
-    auto dout = [&](int t, int d) { return t < nt && d < a.Dv ? elem<T>(a.dout, (row0 + t) * a.lddo + (long long)h * a.Dv + d) : 0.0f; };
-    auto beta = [&](int t) { return t < nt ? a.beta[(row0 + t) * a.Hv + h] : 0.0f; };
-    auto write = [&](int t, int d) { return t < nt && d < a.Dv ? a.e[((row0 + t) * a.Hv + h) * a.Dv + d] : 0.0f; };
-    auto adjoint = [&](int t, int d) { return t < nt && d < a.Dv ? a.x[((row0 + t) * a.Hv + h) * a.Dv + d] : 0.0f; };
-    // a slice of 64 tokens x 16 values: thread's token of piece n, and its value
-    const int own_d = tid % GS;
-    auto own_t = [&](int n) { return tid / GS + 16 * n; };
+    // a slice of 64 tokens x 16 values: this thread's token, and the first of its four values
+    const int mt = tid / 4, md = tid % 4 * 4;
+    const bool live = mt < nt;
+    const float4 zero = make_float4(0, 0, 0, 0);
+    const long long row = row0 + (live ? mt : 0), hv = row * a.Hv + h;
+    const T *k0 = static_cast<const T *>(a.k) + row * a.ldk + hk * a.Dk + md, *q0 = static_cast<const T *>(a.q) + row * a.ldq + hk * a.Dk + md;
+    const T *o0 = static_cast<const T *>(a.dout) + row * a.lddo + (long long)h * a.Dv + md;
+    const float *x0 = a.x + hv * a.Dv + md, *e0 = a.e + hv * a.Dv + md;
+    const bool vk = a.ldk % 4 == 0, vq = a.ldq % 4 == 0, vo = a.lddo % 4 == 0;
+    auto stage = [&](int j, float4 v) { st[j][md][mt] = v.x, st[j][md + 1][mt] = v.y, st[j][md + 2][mt] = v.z, st[j][md + 3][mt] = v.w; };
+    auto times = [](float4 v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); };
     auto row4 = [&](int j, int d, int at, float (&r)[4]) {
         const float4 v = *reinterpret_cast<const float4 *>(&st[j][d][at]);
         r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
     };
-    if (half == 0) {
+    float *out = a.writes + ((long long)part * a.B * a.L + row0) * a.Hv + h;   // [part][B][L][Hv]
+    const int ks = (a.Dk + GS - 1) / GS;
+    if (part == 0) {
         float kk[4][4] = {}, qk[4][4] = {}, du[4][4] = {}, ou[4][4] = {};
-        float x[3][4];
+        const float be = live ? a.beta[hv] : 0.0f;
+        float4 x[3];
         // first all products along the keys, then all along the values
-        const int ks = (a.Dk + GS - 1) / GS, all = ks + (a.Dv + GS - 1) / GS;
+        const int all = ks + (a.Dv + GS - 1) / GS;
         auto fetch = [&](int s) {
-            const int d = (s < ks ? s : s - ks) * GS + own_d;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int t = own_t(n);
-                if (s < ks)
-                    x[0][n] = key(t, d), x[1][n] = query(t, d);
-                else
-                    x[0][n] = beta(t) * adjoint(t, d), x[1][n] = dout(t, d), x[2][n] = beta(t) * write(t, d);
-            }
+            const int d = (s < ks ? s : s - ks) * GS;
+            const bool in = live && d + md < (s < ks ? a.Dk : a.Dv);
+            x[0] = x[1] = x[2] = zero;
+            if (!in) return;
+            if (s < ks)
+                x[0] = four<T>(k0 + d, vk), x[1] = four<T>(q0 + d, vq);
+            else
+                x[0] = four<float>(x0 + d, true), x[1] = four<T>(o0 + d, vo), x[2] = four<float>(e0 + d, true);
         };
         fetch(0);
         for (int s = 0; s < all; ++s) {
-            meet();
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                st[0][own_d][own_t(n)] = x[0][n], st[1][own_d][own_t(n)] = x[1][n];
-                st[2][own_d][own_t(n)] = s < ks ? x[0][n] : x[2][n];
-            }
-            meet();
+            __syncthreads();
+            if (s < ks)
+                stage(0, x[0]), stage(1, x[1]);
+            else
+                stage(0, times(x[0], be)), stage(1, x[1]), stage(2, times(x[2], be));
+            __syncthreads();
             if (s + 1 < all) fetch(s + 1);
-            auto add = [&](float (&p)[4][4], float (&r)[4][4]) {
+            auto add = [&](float (&p)[4][4], float (&r)[4][4], int w) {
 #pragma unroll 4
                 for (int d = 0; d < GS; ++d) {
-                    float u[4], v[4], w[4];
-                    row4(0, d, ti, u), row4(1, d, ti, v), row4(2, d, tj, w);
+                    float u[4], v[4], y[4];
+                    row4(0, d, ti, u), row4(1, d, ti, v), row4(w, d, tj, y);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) p[i][j] = fmaf(u[i], w[j], p[i][j]), r[i][j] = fmaf(v[i], w[j], r[i][j]);
+                        for (int j = 0; j < 4; ++j) p[i][j] = fmaf(u[i], y[j], p[i][j]), r[i][j] = fmaf(v[i], y[j], r[i][j]);
                 }
             };
             if (s < ks)
-                add(kk, qk);
+                add(kk, qk, 0);
             else
-                add(du, ou);
+                add(du, ou, 2);
         }
-        meet();
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -478,99 +471,122 @@ template <typename T> __global__ void __launch_bounds__(GT) decay_grads_kernel(c
                 const float d = expf((hi[r] - hi[q]) + (lo[r] - lo[q]));
                 M[r * MP + q] = q < r ? d * (a.scale * qk[i][j] * ou[i][j] - kk[i][j] * du[i][j]) : 0.0f;
             }
-        meet();
+        __syncthreads();
         // M_it becomes the sum of M_ij over j < t, a row a thread
         if (tid < CHUNK) {
             float w = 0.0f;
-#pragma unroll 8
+#pragma unroll 16
             for (int j = 0; j < CHUNK; ++j) {
                 const float v = M[tid * MP + j];
                 M[tid * MP + j] = w;
                 w += v;
             }
         }
-    } else {
-        float x[4][4], m = 0.0f, aw[4] = {}, bw[4] = {};
-        const float *S = a.states + (bh * (N + 1) + c) * mat, *Z = static_cast<const float *>(a.z) + (bh * N + c) * mat;
-        const int ks = (a.Dk + GS - 1) / GS, vs = (a.Dv + 63) / 64;
-        // depth along the keys; columns 64 of the values at a time
-        auto fetch = [&](int s) {
-            const int d = s % ks * GS + own_d;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                x[0][n] = key(own_t(n), d), x[1][n] = query(own_t(n), d);
-                const int r = s % ks * GS + tid / 64 + 4 * n, v = s / ks * 64 + tid % 64;
-                const bool in = r < a.Dk && v < a.Dv;
-                x[2][n] = in ? S[(long long)r * a.Dv + v] : 0.0f, x[3][n] = in ? Z[(long long)r * a.Dv + v] : 0.0f;
-            }
-        };
-        float ks4[4][4], qs4[4][4], kz4[4][4];
-        fetch(0);
-        for (int s = 0; s < ks * vs; ++s) {
-            if (s % ks == 0)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) ks4[i / 4][i % 4] = qs4[i / 4][i % 4] = kz4[i / 4][i % 4] = 0.0f;
-            meet();
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                st[0][own_d][own_t(n)] = x[0][n], st[1][own_d][own_t(n)] = x[1][n];
-                st[2][tid / 64 + 4 * n][tid % 64] = x[2][n], st[3][tid / 64 + 4 * n][tid % 64] = x[3][n];
-                m = fmaf(x[2][n], x[3][n], m);
-            }
-            meet();
-            if (s + 1 < ks * vs) fetch(s + 1);
+        __syncthreads();
+        if (tid < nt) {
+            float w = 0.0f;
+#pragma unroll 8
+            for (int i = 0; i < CHUNK; ++i) w += i >= tid ? M[i * MP + tid] : 0.0f;
+            out[(long long)tid * a.Hv] = w;
+        }
+        return;
+    }
+    const int v0 = (part - 1) * 64;
+    float m = 0.0f, ks4[4][4] = {}, qs4[4][4] = {}, kz4[4][4] = {};
+    float4 x[4];
+    // a slice of 16 x 64 of the state and its adjoint: this thread's row and first column
+    const int sr = tid / 16, sv = v0 + tid % 16 * 4;
+    const long long at = (long long)sr * a.Dv + sv;
+    const float *S = a.states + (bh * (N + 1) + c) * mat + at, *Z = static_cast<const float *>(a.z) + (bh * N + c) * mat + at;
+    auto fetch = [&](int s) {
+        const int d = s * GS;
+        x[0] = x[1] = x[2] = x[3] = zero;
+        if (live && d + md < a.Dk) x[0] = four<T>(k0 + d, vk), x[1] = four<T>(q0 + d, vq);
+        if (d + sr < a.Dk && sv < a.Dv) {
+            x[2] = four<float>(S + (long long)d * a.Dv, true);
+            x[3] = four<float>(Z + (long long)d * a.Dv, true);
+        }
+    };
+    fetch(0);
+    for (int s = 0; s < ks; ++s) {
+        __syncthreads();
+        stage(0, x[0]), stage(1, x[1]);
+        *reinterpret_cast<float4 *>(&st[2][sr][tid % 16 * 4]) = x[2];
+        *reinterpret_cast<float4 *>(&st[3][sr][tid % 16 * 4]) = x[3];
+        m = fmaf(x[2].x, x[3].x, fmaf(x[2].y, x[3].y, fmaf(x[2].z, x[3].z, fmaf(x[2].w, x[3].w, m))));
+        __syncthreads();
+        if (s + 1 < ks) fetch(s + 1);
 #pragma unroll 4
-            for (int d = 0; d < GS; ++d) {
-                float u[4], v[4], y[4], z[4];
-                row4(0, d, ti, u), row4(1, d, ti, v), row4(2, d, tj, y), row4(3, d, tj, z);
+        for (int d = 0; d < GS; ++d) {
+            float u[4], v[4], y[4], z[4];
+            row4(0, d, ti, u), row4(1, d, ti, v), row4(2, d, tj, y), row4(3, d, tj, z);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        ks4[i][j] = fmaf(u[i], y[j], ks4[i][j]), qs4[i][j] = fmaf(v[i], y[j], qs4[i][j]);
-                        kz4[i][j] = fmaf(u[i], z[j], kz4[i][j]);
-                    }
-            }
-            if (s % ks == ks - 1) {
-                const int v0 = s / ks * 64 + tj;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float be = beta(ti + i);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        aw[i] = fmaf(a.scale * qs4[i][j], dout(ti + i, v0 + j), aw[i]);
-                        aw[i] = fmaf(-ks4[i][j], be * adjoint(ti + i, v0 + j), aw[i]);
-                        bw[i] = fmaf(kz4[i][j], be * write(ti + i, v0 + j), bw[i]);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    ks4[i][j] = fmaf(u[i], y[j], ks4[i][j]), qs4[i][j] = fmaf(v[i], y[j], qs4[i][j]);
+                    kz4[i][j] = fmaf(u[i], z[j], kz4[i][j]);
                 }
-            }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int w = 1; w < 16; w <<= 1) {
-                aw[i] += __shfl_xor_sync(0xffffffffu, aw[i], w);
-                bw[i] += __shfl_xor_sync(0xffffffffu, bw[i], w);
-            }
-            if (tid % 16 == 0) {
-                const int r = ti + i;
-                av[r] = expf(hi[r]) * aw[i];
-                bv[r] = expf((hi[CHUNK - 1] - hi[r]) + (lo[CHUNK - 1] - lo[r])) * bw[i];
-            }
-        }
-        m = warp_sum(m);
-        if (tid % 32 == 0) mv[tid / 32] = m;
     }
+    // this thread's four tokens and columns
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = ti + i, v = v0 + tj;
+        float aw = 0.0f, bw = 0.0f;
+        if (t < nt && v < a.Dv) {
+            const long long r = row0 + t, rh = r * a.Hv + h;
+            const float be = a.beta[rh];
+            const float4 o = four<T>(static_cast<const T *>(a.dout) + r * a.lddo + (long long)h * a.Dv + v, vo);
+            const float4 dv = times(four<float>(a.x + rh * a.Dv + v, true), be), w = times(four<float>(a.e + rh * a.Dv + v, true), be);
+            const float o4[4] = {o.x, o.y, o.z, o.w}, d4[4] = {dv.x, dv.y, dv.z, dv.w}, w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                aw = fmaf(a.scale * qs4[i][j], o4[j], fmaf(-ks4[i][j], d4[j], aw));
+                bw = fmaf(kz4[i][j], w4[j], bw);
+            }
+        }
+#pragma unroll
+        for (int w = 1; w < 16; w <<= 1) {
+            aw += __shfl_xor_sync(0xffffffffu, aw, w);
+            bw += __shfl_xor_sync(0xffffffffu, bw, w);
+        }
+        if (tid % 16 == 0) {
+            av[t] = expf(hi[t]) * aw;
+            bv[t] = expf((hi[CHUNK - 1] - hi[t]) + (lo[CHUNK - 1] - lo[t])) * bw;
+        }
+    }
+    m = warp_sum(m);
+    if (tid % 32 == 0) mv[tid / 32] = m;
     __syncthreads();
-    if (threadIdx.x < nt) {
-        const int t = threadIdx.x;
-        float m = 0.0f, w = 0.0f, x = 0.0f, y = 0.0f;
+    if (tid < nt) {
+        float x = 0.0f, y = 0.0f;
+        m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < GT / 64; ++i) m += mv[i];
-        for (int i = t; i < CHUNK; ++i) w += M[i * MP + t], x += av[i];
-        for (int j = 0; j < t; ++j) y += bv[j];
-        a.dg[(row0 + t) * a.Hv + h] = fmaf(expf(hi[CHUNK - 1]), m, (x + y) + w);
+        for (int i = 0; i < GT / 32; ++i) m += mv[i];
+#pragma unroll 8
+        for (int i = 0; i < CHUNK; ++i) x += i >= tid ? av[i] : 0.0f, y += i < tid ? bv[i] : 0.0f;
+        out[(long long)tid * a.Hv] = fmaf(expf(hi[CHUNK - 1]), m, x + y);
     }
+}
+
+// One warp per token and value head: dv = beta X, dbeta = X . e, dg from its parts.
+template <typename T> __global__ void __launch_bounds__(256) token_grads_kernel(const Args a, int parts) {
+    griddep_wait();
+    const long long hv = (long long)blockIdx.x * 8 + threadIdx.x / 32, rows = (long long)a.B * a.L * a.Hv;
+    const int lane = threadIdx.x % 32;
+    if (hv >= rows) return;
+    const long long row = hv / a.Hv;
+    const int h = (int)(hv % a.Hv);
+    const float be = a.beta[hv], dg = warp_sum(lane < parts ? a.writes[lane * rows + hv] : 0.0f);
+    float db = 0.0f;
+    for (int c = lane; c < a.Dv; c += 32) {
+        const float x = a.x[hv * a.Dv + c];
+        db = fmaf(x, a.e[hv * a.Dv + c], db);
+        store_elem<T>(static_cast<T *>(a.dv) + row * a.lddv + (long long)h * a.Dv + c, be * x);
+    }
+    db = warp_sum(db);
+    if (lane == 0) a.dbeta[hv] = db, a.dg[hv] = dg;
 }
 
 // dq and dk of a key head: the sum over its value heads, rounded once.
@@ -808,8 +824,9 @@ template <typename T> cudaError_t backward(const Args &a, cudaStream_t st) {
     if (e != cudaSuccess || a.L == 0) return e;
     if ((e = row_sweep<T>(a, st)) != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.L * a.Hv, n = (long long)a.B * a.L * a.Hk * a.Dk;
-    if ((e = launch_after(token_grads_kernel<T>, (unsigned)((rows + 7) / 8), 256, 0, st, a)) != cudaSuccess) return e;
-    if ((e = launch_after(decay_grads_kernel<T>, dim3(chunks(a.L), a.Hv, a.B), GT, 0, st, a)) != cudaSuccess) return e;
+    const int parts = decay_parts(a.Dv);
+    if ((e = launch_after(decay_grads_kernel<T>, dim3(chunks(a.L) * parts, a.Hv, a.B), GT, 0, st, a, parts)) != cudaSuccess) return e;
+    if ((e = launch_after(token_grads_kernel<T>, (unsigned)((rows + 7) / 8), 256, 0, st, a, parts)) != cudaSuccess) return e;
     return launch_after(group_sum_kernel<T>, (unsigned)((n + 255) / 256), 256, 0, st, a);
 }
 
@@ -840,7 +857,8 @@ Sizes sizes(int B, int L, int Hv, int Dk, int Dv) {
     s.images = align256(tc_image_bytes(B, L, Hv, Dk, Dv));
     s.heads = align256(sizeof(float) * rows * Dk);
     s.inner = s.images ? align256(sizeof(float) * (size_t)B * Hv * N * inner_parts(Dk, Dv)) : 0;
-    s.writes = s.images ? align256(sizeof(float) * (size_t)B * Hv * N * CHUNK * write_parts(Dv)) : 0;
+    const size_t tc = s.images ? (size_t)B * Hv * N * CHUNK * write_parts(Dv) : 0, simt = rows * decay_parts(Dv);
+    s.writes = align256(sizeof(float) * (tc > simt ? tc : simt));
     return s;
 }
 }  // namespace

@@ -33,9 +33,9 @@ struct Args {
     // backward workspace
     float *x;                         // [B][L][Hv][Dv]   dL/du_t
     float *dqh, *dkh;                 // [B][L][Hv][Dk]   per value head
-    // tensor cores, of the decays' gradients: parts of <S, Z> and of b_j
+    // of the decays' gradients: on the tensor cores parts of <S, Z> and of b_j, else parts of dg
     float *inner;                     // [B][Hv][N][inner_parts]
-    float *writes;                    // [B][Hv][N][CHUNK][write_parts]
+    float *writes;                    // [B][Hv][N][CHUNK][write_parts], or [parts][B][L][Hv]
     void *z;                          // dL/dS at the end of chunk c: [B][Hv][N][Dk][Dv] float32, or, for the tensor
                                       // cores, [B][Hv][N][Dv / 64][2][Dk][64] bf16 (two parts)
     void *images;                     // operand images of the tensor-core path; then a state between launches
