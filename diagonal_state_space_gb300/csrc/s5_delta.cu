@@ -242,14 +242,15 @@ __global__ void __launch_bounds__(8 * C + 64) column_sweep_kernel(const Args a) 
 // known: half of a block runs forward from the chunk's kept state for dq_t and
 // a_t S_{t-1} dv_t, the other half back from its kept adjoint for Z_t u_t; their
 // difference is dk_t.  Bound by the chain of a token, 64 of them per half: 2 x 500
-// tokens of 4 heads of 64 x 64 in 25 us (38 with one half after the other).
+// tokens of 4 heads of 64 x 64 in 24 us (38 with one half after the other).  Two
+// blocks an SM up to 128 columns: 512 tokens of 16 heads of 128 in 100 us, 135 with one.
 template <int RPT> struct RowSmem {
     static constexpr int NT = RPT > 8 ? TB / 2 : TB;
     float e[2][NT][16 * RPT], x[2][NT][16 * RPT], d[2][NT][16 * RPT], q[2][NT][OWN], k[2][NT][OWN], a[2][NT];
     float dk[2][CHUNK][OWN];
 };
 template <typename T, int RPT>
-__global__ void __launch_bounds__(2 * SWT) row_sweep_kernel(const Args a) {
+__global__ void __launch_bounds__(2 * SWT, RPT > 8 ? 1 : 2) row_sweep_kernel(const Args a) {
     constexpr int NT = RowSmem<RPT>::NT;
     extern __shared__ __align__(16) unsigned char raw[];
     RowSmem<RPT> &sm = *reinterpret_cast<RowSmem<RPT> *>(raw);
