@@ -238,7 +238,11 @@ def _plain_conv(st):
     full, win = _window(st, x)
     p = (win * w.t()).sum(2) + b
     sig = 1 / (1 + torch.exp(-p))
-    out = dict(y=(p * sig if case["act"] else p).to(dt), past=full[:, full.shape[1] - (K - 1):].to(dt))
+    last = full[:, full.shape[1] - (K - 1):]
+    if st["reset"] is not None:          # the next call sees nothing of an earlier document either
+        doc = torch.cat([torch.zeros(x.shape[0], K - 1, dtype=torch.long, device=x.device), _document(st["reset"])], 1)
+        last = torch.where((doc[:, doc.shape[1] - (K - 1):] == doc[:, -1:])[..., None], last, 0.0)
+    out = dict(y=(p * sig if case["act"] else p).to(dt), past=last.to(dt))
     if case["op"] == "conv_train":
         dp = st["dy"].float()
         if case["act"]:
@@ -437,7 +441,8 @@ def _exact_conv(st):
         tap = line[:, K - 1 - back:K - 1 - back + L]
         p += w[:, K - 1 - back] * tap * (age >= back)[..., None]
     sig = torch.sigmoid(p)
-    out = dict(y=p * sig if case["act"] else p, past=line[:, L:])
+    seen = age[:, -1:] >= torch.arange(K - 2, -1, -1, device=x.device)
+    out = dict(y=p * sig if case["act"] else p, past=line[:, L:] * seen[..., None])
     if case["op"] == "conv":
         return out
     dp = st["dy"].double()
