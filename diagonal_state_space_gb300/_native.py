@@ -63,6 +63,24 @@ SIGNATURES = {
     "s5_qk_norm_rotary_backward": (_i, [_vp, _ll, _vp, _ll, _i, _vp, _vp, _i, _f, _vp, _vp, _i, _i,
                                         _f, _ll, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll,
                                         _vp, _vp, _vp, _sz, _vp]),
+    # gated linear recurrence, short convolution, layer norm of a sum
+    "s5_gated_scan_saved_size": (_sz, [_i] * 3),
+    "s5_gated_scan_workspace_size": (_sz, [_i] * 3),
+    "s5_gated_scan_forward": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _vp, _vp, _vp, _vp] + [_i] * 4
+                              + [_vp, _ll, _vp, _vp, _sz, _vp]),
+    "s5_gated_scan_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _vp, _vp, _vp] + [_i] * 4
+                               + [_vp, _ll, _vp, _vp, _sz, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp,
+                                  _sz, _vp]),
+    "s5_gated_scan_step": (_i, [_vp, _vp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp]),
+    "s5_short_conv_forward": (_i, [_vp, _ll, _i, _vp, _vp, _i, _vp, _vp, _vp] + [_i] * 4 + [_vp, _ll, _vp, _vp]),
+    "s5_short_conv_workspace_size": (_sz, [_i] * 2),
+    "s5_short_conv_backward": (_i, [_vp, _ll, _i, _vp, _vp, _i, _vp, _vp, _vp] + [_i] * 4
+                               + [_vp, _ll, _vp, _vp, _ll, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "s5_short_conv_step": (_i, [_vp, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "s5_add_layernorm": (_i, [_vp, _ll, _vp, _ll, _i, _vp, _vp, _f, _ll, _i, _vp, _ll, _vp, _ll, _vp, _vp]),
+    "s5_add_layernorm_workspace_size": (_sz, [_i]),
+    "s5_add_layernorm_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _i, _vp, _vp, _ll, _i, _vp, _ll,
+                                       _vp, _vp, _vp, _sz, _vp]),
 }
 
 _lock = threading.Lock()

@@ -556,9 +556,294 @@ def s5_qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, norm="rms"
         return out
 
 
+# ---------------------------------------------------------------------------
+# Gated linear recurrence, short causal convolution, layer norm of a sum.  Rows
+# may be views with a pitch between tokens; a token's channels are contiguous.
+# reset [B,L] (bool or uint8): the tokens that begin a new sequence.  lengths
+# [B] int32: tokens of each row; what lies behind is not read, and is zero in
+# what comes back.
+# ---------------------------------------------------------------------------
+_MARKS = (torch.bool, torch.uint8)
+_ACT = {None: 0, "none": 0, "silu": 1}
+
+
+def _tokens(t, name, dtype=None, shape=None):
+    """(address, elements between two tokens) of a [..., C] array."""
+    if isinstance(t, torch.Tensor) and t.dim() >= 1 and not t.is_contiguous():
+        return _rows(t.unsqueeze(-2), name, dtype, None if shape is None else torch.Size((*shape[:-1], 1, shape[-1])))
+    return _ptr(t, name, dtype, shape), t.shape[-1]
+
+
+def _maybe_tokens(t, name, dtype, shape):
+    return (None, 0) if t is None else _tokens(t, name, dtype, shape)
+
+
+def _marks(reset, lengths, B, L):
+    if reset is not None and reset.dtype not in _MARKS:
+        raise ValueError("reset must be bool or uint8")
+    return _ptr(reset, "reset", None, (B, L), True), _ptr(lengths, "lengths", torch.int32, (B,), True)
+
+
+def _channels(x, name, dims):
+    if not isinstance(x, torch.Tensor) or x.dim() != dims or x.dtype not in _DT:
+        raise ValueError("%s must be a float32 or bfloat16 array of %d axes" % (name, dims))
+    return x.shape
+
+
+def s5_gated_scan_saved_size(B: int, L: int, C: int) -> int:
+    return int(_native.lib().s5_gated_scan_saved_size(B, L, C))
+
+
+def s5_gated_scan_workspace_size(B: int, L: int, C: int) -> int:
+    return int(_native.lib().s5_gated_scan_workspace_size(B, L, C))
+
+
+def _need(n, what):
+    if n == 0:
+        raise S5Error(what, 2, "sizes that the call does not cover")
+    return n
+
+
+def new_gated_scan_saved(x) -> torch.Tensor:
+    """The buffer that s5_gated_scan_forward fills for s5_gated_scan_backward."""
+    B, L, C = _channels(x, "x", 3)
+    return torch.empty(_need(s5_gated_scan_saved_size(B, L, C), "new_gated_scan_saved"), dtype=torch.uint8, device=x.device)
+
+
+def s5_gated_scan_forward(x, gate_a, gate_x, rate, h0=None, h_last=None, reset=None, lengths=None, normalize=True, h=None,
+                          saved=None, stream=None):
+    """Gated linear recurrence of each channel, h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_x) x with
+    a = exp(-rate sigmoid(gate_a)): x, gate_a, gate_x (None: no input gate) [B,L,C], rate [C] float32, from the state h0
+    [B,C] float32 (None: zero).  normalize False: without the root.  Returns h, or (h, h_last) when h_last is a tensor
+    (it may be h0) or True; with `saved` (new_gated_scan_saved) also what s5_gated_scan_backward needs."""
+    if stream is None:
+        out = _native.marshal().gated_scan_forward(x, gate_a, gate_x, rate, h0, h_last, reset, lengths, bool(normalize), h, saved)
+        if _taken("s5_gated_scan_forward", out):
+            return out
+    with _Launch(stream, x=x, gate_a=gate_a, gate_x=gate_x, rate=rate, h0=h0, h_last=h_last, reset=reset, lengths=lengths, h=h,
+                 saved=saved) as on:
+        B, L, C = _channels(x, "x", 3)
+        f32, dt = torch.float32, x.dtype
+        if h is None:
+            h = on.made(_new(x))
+        if h_last is True:
+            h_last = on.made(torch.empty(B, C, dtype=f32, device=x.device))
+        code = _native.lib().s5_gated_scan_forward(
+            *_tokens(x, "x"), *_tokens(gate_a, "gate_a", dt, x.shape), *_maybe_tokens(gate_x, "gate_x", dt, x.shape), _DT[dt],
+            _ptr(rate, "rate", f32, (C,)), _ptr(h0, "h0", f32, (B, C), True), *_marks(reset, lengths, B, L), int(bool(normalize)),
+            B, L, C, *_tokens(h, "h", dt, x.shape), _ptr(h_last, "h_last", f32, (B, C), True),
+            _ptr(saved, "saved", torch.uint8, None, True), 0 if saved is None else saved.numel(), on.handle)
+        check("s5_gated_scan_forward", code)
+        return h if h_last is None else (h, h_last)
+
+
+def s5_gated_scan_backward(x, gate_a, gate_x, rate, dh, saved, h0=None, dh_last=None, reset=None, lengths=None, normalize=True,
+                           workspace=None, stream=None):
+    """Gradients of sum(dh * h) + sum(dh_last * h_last) after s5_gated_scan_forward with the same inputs and `saved`.
+    Returns a dict: dx, dgate_a, dgate_x (None without gate_x) of x's type, drate and dh0 (None without h0) float32."""
+    if stream is None:
+        out = _native.marshal().gated_scan_backward(x, gate_a, gate_x, rate, dh, saved, h0, dh_last, reset, lengths,
+                                                    bool(normalize), workspace)
+        if _taken("s5_gated_scan_backward", out):
+            return out
+    with _Launch(stream, x=x, gate_a=gate_a, gate_x=gate_x, rate=rate, dh=dh, saved=saved, h0=h0, dh_last=dh_last, reset=reset,
+                 lengths=lengths, workspace=workspace) as on:
+        B, L, C = _channels(x, "x", 3)
+        f32, dt, dev = torch.float32, x.dtype, x.device
+        _ptr(h0, "h0", f32, (B, C), True)
+        e = lambda shape, t: on.made(torch.empty(shape, dtype=t, device=dev))  # noqa: E731
+        out = dict(dx=e(x.shape, dt), dgate_a=e(x.shape, dt), dgate_x=None if gate_x is None else e(x.shape, dt),
+                   drate=e((C,), f32), dh0=None if h0 is None else e((B, C), f32))
+        if workspace is None:
+            workspace = e((_need(s5_gated_scan_workspace_size(B, L, C), "s5_gated_scan_backward"),), torch.uint8)
+        at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        code = _native.lib().s5_gated_scan_backward(
+            *_tokens(x, "x"), *_tokens(gate_a, "gate_a", dt, x.shape), *_maybe_tokens(gate_x, "gate_x", dt, x.shape), _DT[dt],
+            _ptr(rate, "rate", f32, (C,)), *_marks(reset, lengths, B, L), int(bool(normalize)), B, L, C,
+            *_tokens(dh, "dh", dt, x.shape), _ptr(dh_last, "dh_last", f32, (B, C), True), _ptr(saved, "saved", torch.uint8),
+            saved.numel(), at(out["dx"]), C, at(out["dgate_a"]), C, at(out["dgate_x"]), 0 if gate_x is None else C,
+            at(out["drate"]), at(out["dh0"]), _ptr(workspace, "workspace", torch.uint8), workspace.numel(), on.handle)
+        check("s5_gated_scan_backward", code)
+        return out
+
+
+def s5_gated_scan_step(x, gate_a, gate_x, rate, state, normalize=True, h=None, stream=None):
+    """One token per sequence: x, gate_a, gate_x (or None) [B,C], rate [C] float32; state [B,C] float32 is updated in
+    place.  Returns h [B,C] of x's type."""
+    if stream is None:
+        out = _native.marshal().gated_scan_step(x, gate_a, gate_x, rate, state, bool(normalize), h)
+        if _taken("s5_gated_scan_step", out):
+            return out
+    with _Launch(stream, x=x, gate_a=gate_a, gate_x=gate_x, rate=rate, state=state, h=h) as on:
+        B, C = _channels(x, "x", 2)
+        f32, dt = torch.float32, x.dtype
+        if h is None:
+            h = on.made(_new(x))
+        code = _native.lib().s5_gated_scan_step(
+            _ptr(x, "x"), _ptr(gate_a, "gate_a", dt, x.shape), _ptr(gate_x, "gate_x", dt, x.shape, True), _DT[dt],
+            _ptr(rate, "rate", f32, (C,)), int(bool(normalize)), B, C, _ptr(state, "state", f32, (B, C)), _ptr(h, "h", dt, x.shape),
+            on.handle)
+        check("s5_gated_scan_step", code)
+        return h
+
+
+def s5_short_conv_workspace_size(C: int, K: int) -> int:
+    return int(_native.lib().s5_short_conv_workspace_size(C, K))
+
+
+def _taps(weight, C):
+    """Taps of a [C,K] weight."""
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or weight.shape[0] != C:
+        raise ValueError("weight must have shape (%d, taps)" % C)
+    return weight.shape[1]
+
+
+def s5_short_conv_forward(x, weight, bias=None, activation=None, past=None, past_out=None, reset=None, lengths=None, y=None,
+                          stream=None):
+    """Causal convolution of each channel of x [B,L,C] along the tokens, weight [C,K] (K from 2 to 8; its last column
+    meets the token itself) and bias [C] float32, activation None or "silu".  past [B,K-1,C] of x's type: the inputs
+    before the first (None: zeros).  Returns y, or (y, past_out) when past_out is a tensor (it may be past) or True: the
+    inputs that the next call takes as its past."""
+    if stream is None:
+        out = _native.marshal().short_conv_forward(x, weight, bias, _ACT[activation], past, past_out, reset, lengths, y)
+        if _taken("s5_short_conv_forward", out):
+            return out
+    with _Launch(stream, x=x, weight=weight, bias=bias, past=past, past_out=past_out, reset=reset, lengths=lengths, y=y) as on:
+        B, L, C = _channels(x, "x", 3)
+        K, f32, dt = _taps(weight, C), torch.float32, x.dtype
+        if y is None:
+            y = on.made(_new(x))
+        if past_out is True:
+            past_out = on.made(torch.empty(B, max(K - 1, 0), C, dtype=dt, device=x.device))
+        code = _native.lib().s5_short_conv_forward(
+            *_tokens(x, "x"), _DT[dt], _ptr(weight, "weight", f32), _ptr(bias, "bias", f32, (C,), True), _ACT[activation],
+            _ptr(past, "past", dt, (B, K - 1, C), True), *_marks(reset, lengths, B, L), B, L, C, K, *_tokens(y, "y", dt, x.shape),
+            _ptr(past_out, "past_out", dt, (B, K - 1, C), True), on.handle)
+        check("s5_short_conv_forward", code)
+        return y if past_out is None else (y, past_out)
+
+
+def s5_short_conv_backward(x, weight, dy, bias=None, activation=None, past=None, dpast_out=None, reset=None, lengths=None,
+                           workspace=None, stream=None):
+    """Gradients of sum(dy * y) + sum(dpast_out * past_out) with s5_short_conv_forward's inputs.  Returns a dict: dx and
+    dpast (None without past) of x's type, dweight [C,K] and dbias [C] (None without bias) float32."""
+    if stream is None:
+        out = _native.marshal().short_conv_backward(x, weight, dy, bias, _ACT[activation], past, dpast_out, reset, lengths, workspace)
+        if _taken("s5_short_conv_backward", out):
+            return out
+    with _Launch(stream, x=x, weight=weight, dy=dy, bias=bias, past=past, dpast_out=dpast_out, reset=reset, lengths=lengths,
+                 workspace=workspace) as on:
+        B, L, C = _channels(x, "x", 3)
+        K, f32, dt, dev = _taps(weight, C), torch.float32, x.dtype, x.device
+        e = lambda shape, t: on.made(torch.empty(shape, dtype=t, device=dev))  # noqa: E731
+        out = dict(dx=e(x.shape, dt), dweight=e((C, K), f32), dbias=None if bias is None else e((C,), f32),
+                   dpast=None if past is None else e((B, max(K - 1, 0), C), dt))
+        if workspace is None:
+            workspace = e((_need(s5_short_conv_workspace_size(C, K), "s5_short_conv_backward"),), torch.uint8)
+        at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        code = _native.lib().s5_short_conv_backward(
+            *_tokens(x, "x"), _DT[dt], _ptr(weight, "weight", f32), _ptr(bias, "bias", f32, (C,), True), _ACT[activation],
+            _ptr(past, "past", dt, (B, K - 1, C), True), *_marks(reset, lengths, B, L), B, L, C, K, *_tokens(dy, "dy", dt, x.shape),
+            _ptr(dpast_out, "dpast_out", dt, (B, K - 1, C), True), at(out["dx"]), C, at(out["dweight"]), at(out["dbias"]),
+            at(out["dpast"]), _ptr(workspace, "workspace", torch.uint8), workspace.numel(), on.handle)
+        check("s5_short_conv_backward", code)
+        return out
+
+
+def s5_short_conv_step(x, weight, state, bias=None, activation=None, y=None, stream=None):
+    """One token per sequence: x [B,C]; state [B,K-1,C] of x's type, the inputs before it, is moved on in place.
+    Returns y [B,C]."""
+    if stream is None:
+        out = _native.marshal().short_conv_step(x, weight, state, bias, _ACT[activation], y)
+        if _taken("s5_short_conv_step", out):
+            return out
+    with _Launch(stream, x=x, weight=weight, state=state, bias=bias, y=y) as on:
+        B, C = _channels(x, "x", 2)
+        K, f32, dt = _taps(weight, C), torch.float32, x.dtype
+        if y is None:
+            y = on.made(_new(x))
+        code = _native.lib().s5_short_conv_step(
+            _ptr(x, "x"), _DT[dt], _ptr(weight, "weight", f32), _ptr(bias, "bias", f32, (C,), True), _ACT[activation], B, C, K,
+            _ptr(state, "state", dt, (B, K - 1, C)), _ptr(y, "y", dt, x.shape), on.handle)
+        check("s5_short_conv_step", code)
+        return y
+
+
+def s5_add_layernorm_workspace_size(H: int) -> int:
+    return int(_native.lib().s5_add_layernorm_workspace_size(H))
+
+
+def _norm_rows(x, name):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.dtype not in _DT:
+        raise ValueError("%s must be a float32 or bfloat16 array [..., H]" % name)
+    return math.prod(x.shape[:-1]), x.shape[-1]
+
+
+def new_layernorm_saved(x) -> torch.Tensor:
+    """What s5_add_layernorm fills for s5_add_layernorm_backward: mean and 1 / sqrt(var + eps) of each row."""
+    return torch.empty(_norm_rows(x, "x")[0], 2, dtype=torch.float32, device=x.device)
+
+
+def s5_add_layernorm(x, weight=None, bias=None, residual=None, eps=1e-5, y=None, total=None, saved=None, stream=None):
+    """Layer norm over the last axis of x [..., H], or of x + residual, with weight and bias [H] float32 (None: ones,
+    zeros).  Returns y, with a residual (y, total): total is the sum, rounded to x's type.  y or total may be x or
+    residual.  With `saved` (new_layernorm_saved) also what s5_add_layernorm_backward needs."""
+    if stream is None:
+        out = _native.marshal().add_layernorm(x, weight, bias, residual, eps, y, total, saved)
+        if _taken("s5_add_layernorm", out):
+            return out
+    with _Launch(stream, x=x, weight=weight, bias=bias, residual=residual, y=y, total=total, saved=saved) as on:
+        N, H = _norm_rows(x, "x")
+        f32, dt = torch.float32, x.dtype
+        if total is not None and residual is None:
+            raise ValueError("total without a residual")
+        if y is None:
+            y = on.made(_new(x))
+        if total is None and residual is not None:
+            total = on.made(_new(x))
+        code = _native.lib().s5_add_layernorm(
+            *_tokens(x, "x"), *_maybe_tokens(residual, "residual", dt, x.shape), _DT[dt], _ptr(weight, "weight", f32, (H,), True),
+            _ptr(bias, "bias", f32, (H,), True), float(eps), N, H, *_tokens(y, "y", dt, x.shape),
+            *_maybe_tokens(total, "total", dt, x.shape), _ptr(saved, "saved", f32, (N, 2), True), on.handle)
+        check("s5_add_layernorm", code)
+        return y if residual is None else (y, total)
+
+
+def s5_add_layernorm_backward(x, dy, saved, weight=None, bias=None, residual=None, dtotal=None, workspace=None, stream=None):
+    """Gradients of sum(dy * y) + sum(dtotal * total) after s5_add_layernorm with the same x, residual and `saved`.
+    Returns a dict: dx of x's type, the gradient of x and of the residual alike, dweight and dbias [H] float32 (None
+    without the weight, the bias).  The forward's total as x, without a residual, reads an array less; the gradients
+    then carry total's rounding."""
+    if stream is None:
+        out = _native.marshal().add_layernorm_backward(x, dy, saved, weight, bias, residual, dtotal, workspace)
+        if _taken("s5_add_layernorm_backward", out):
+            return out
+    with _Launch(stream, x=x, dy=dy, saved=saved, weight=weight, bias=bias, residual=residual, dtotal=dtotal,
+                 workspace=workspace) as on:
+        N, H = _norm_rows(x, "x")
+        f32, dt, dev = torch.float32, x.dtype, x.device
+        _ptr(bias, "bias", f32, (H,), True)
+        e = lambda shape, t: on.made(torch.empty(shape, dtype=t, device=dev))  # noqa: E731
+        out = dict(dx=e(x.shape, dt), dweight=None if weight is None else e((H,), f32), dbias=None if bias is None else e((H,), f32))
+        if workspace is None and not (weight is None and bias is None):
+            workspace = e((_need(s5_add_layernorm_workspace_size(H), "s5_add_layernorm_backward"),), torch.uint8)
+        at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        code = _native.lib().s5_add_layernorm_backward(
+            *_tokens(x, "x"), *_maybe_tokens(residual, "residual", dt, x.shape), *_tokens(dy, "dy", dt, x.shape),
+            *_maybe_tokens(dtotal, "dtotal", dt, x.shape), _DT[dt], _ptr(weight, "weight", f32, (H,), True),
+            _ptr(saved, "saved", f32, (N, 2)), N, H, at(out["dx"]), H, at(out["dweight"]), at(out["dbias"]),
+            _ptr(workspace, "workspace", torch.uint8, None, True), 0 if workspace is None else workspace.numel(), on.handle)
+        check("s5_add_layernorm_backward", code)
+        return out
+
+
 __all__ = ["s5_discretize", "s5_discretize_ex", "s5_forward", "s5_forward_varying_dt",
            "s5_forward_bidirectional", "s5_step", "s5_forward_noalloc", "s5_workspace_size",
            "s5_bidirectional_workspace_size", "s5_sync_status", "new_workspace",
            "s5_delta_forward", "s5_delta_backward", "s5_delta_step", "s5_delta_saved_size",
            "s5_delta_workspace_size", "s5_delta_fault", "new_delta_saved", "s5_rotary", "s5_qk_norm_rotary",
-           "s5_qk_norm_rotary_backward", "s5_rotary_fault", "S5Error", "S5_F32", "S5_BF16"]
+           "s5_qk_norm_rotary_backward", "s5_rotary_fault", "s5_gated_scan_forward", "s5_gated_scan_backward",
+           "s5_gated_scan_step", "s5_gated_scan_saved_size", "s5_gated_scan_workspace_size", "new_gated_scan_saved",
+           "s5_short_conv_forward", "s5_short_conv_backward", "s5_short_conv_step", "s5_short_conv_workspace_size",
+           "s5_add_layernorm", "s5_add_layernorm_backward", "s5_add_layernorm_workspace_size", "new_layernorm_saved",
+           "S5Error", "S5_F32", "S5_BF16"]

@@ -298,9 +298,222 @@ ENTRY(qk_norm_rotary_backward, 13) {
     return nullptr;
 }
 
+// ------------------------------------------------------------------ gated recurrence, short convolution, layer norm
+struct Marks {
+    const Tensor *reset = nullptr, *lengths = nullptr;
+    Marks(Reader &r, int at, int64_t B, int64_t L) {
+        if (!r.none(at)) {
+            reset = r.tensor(at);
+            if (r.ok && ((reset->scalar_type() != at::kBool && reset->scalar_type() != at::kByte) || reset->sizes() != at::IntArrayRef({B, L})))
+                r.ok = false;
+        }
+        lengths = r.maybe(at + 1, at::kInt, {B});
+    }
+    const unsigned char *bytes() const { return data<unsigned char>(reset); }
+    const int *ints() const { return data<int>(lengths); }
+};
+bool flag(Reader &r, int i) {
+    if (r.args[i] != Py_True && r.args[i] != Py_False) r.ok = false;
+    return r.args[i] == Py_True;
+}
+const Tensor *channels(Reader &r, int i, int dims) {
+    const Tensor *t = r.tensor(i);
+    if (r.ok && ((t->scalar_type() != F32 && t->scalar_type() != BF16) || (dims ? t->dim() != dims : t->dim() < 1))) r.ok = false;
+    return t;
+}
+Tensor given_or(const Tensor *t, const Tensor &like) { return t ? *t : make(like.sizes(), like); }
+template <typename T = float> T *at_or_null(const Tensor &t) { return t.defined() ? data<T>(&t) : nullptr; }
+
+// x, gate_a, gate_x, rate, h0, h_last, reset, lengths, normalize, h, saved
+ENTRY(gated_scan_forward, 11) {
+    const Tensor *x = channels(r, 0, 3);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t B = x->size(0), L = x->size(1), C = x->size(2);
+    const at::ScalarType type = x->scalar_type();
+    const Tensor *ga = r.like(1, type, x->sizes()), *gx = r.maybe(2, type, x->sizes()), *rate = r.like(3, F32, {C});
+    const Tensor *h0 = r.maybe(4, F32, {B, C});
+    const bool ends = r.args[5] == Py_True;
+    const Tensor *last = ends ? nullptr : r.maybe(5, F32, {B, C});
+    const Marks m(r, 6, B, L);
+    const bool normalize = flag(r, 8);
+    const Tensor *given = r.maybe(9, type, x->sizes()), *saved = r.none(10) ? nullptr : r.bytes(10);
+    if (!r.ok || !fits({B, L, C})) Py_RETURN_NONE;
+    const Tensor h = given_or(given, *x), s = ends ? make({B, C}, *x, F32) : last ? *last : Tensor();
+    const s5_status code =
+        s5_gated_scan_forward(x->data_ptr(), C, ga->data_ptr(), C, data<void>(gx), C, dtype(*x), data(rate), data(h0), m.bytes(),
+                              m.ints(), normalize, (int)B, (int)L, (int)C, h.data_ptr(), C, at_or_null(s), data<void>(saved),
+                              saved ? saved->numel() : 0, r.stream());
+    return s.defined() ? result(code, h, s) : result(code, h);
+}
+
+// x, gate_a, gate_x, rate, dh, saved, h0, dh_last, reset, lengths, normalize, workspace
+ENTRY(gated_scan_backward, 12) {
+    const Tensor *x = channels(r, 0, 3);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t B = x->size(0), L = x->size(1), C = x->size(2);
+    const at::ScalarType type = x->scalar_type();
+    const Tensor *ga = r.like(1, type, x->sizes()), *gx = r.maybe(2, type, x->sizes()), *rate = r.like(3, F32, {C});
+    const Tensor *dh = r.like(4, type, x->sizes()), *saved = r.bytes(5);
+    const Tensor *h0 = r.maybe(6, F32, {B, C}), *last = r.maybe(7, F32, {B, C});
+    const Marks m(r, 8, B, L);
+    const bool normalize = flag(r, 10);
+    const Tensor *work = r.none(11) ? nullptr : r.bytes(11);
+    if (!r.ok || !fits({B, L, C})) Py_RETURN_NONE;
+    const size_t need = work ? (size_t)work->numel() : s5_gated_scan_workspace_size((int)B, (int)L, (int)C);
+    if (need == 0) Py_RETURN_NONE;
+    const Tensor dx = make(x->sizes(), *x), dga = make(x->sizes(), *x), dgx = gx ? make(x->sizes(), *x) : Tensor();
+    const Tensor drate = make({C}, *x, F32), dh0 = h0 ? make({B, C}, *x, F32) : Tensor();
+    const Tensor w = work ? *work : make({(int64_t)need}, *x, at::kByte);
+    const s5_status code = s5_gated_scan_backward(
+        x->data_ptr(), C, ga->data_ptr(), C, data<void>(gx), C, dtype(*x), data(rate), m.bytes(), m.ints(), normalize, (int)B, (int)L,
+        (int)C, dh->data_ptr(), C, data(last), saved->data_ptr(), saved->numel(), dx.data_ptr(), C, dga.data_ptr(), C,
+        at_or_null<void>(dgx), C, data(&drate), at_or_null(dh0), w.data_ptr(), need, r.stream());
+    if (code != S5_OK) return PyLong_FromLong(code);
+    PyObject *out = PyDict_New();
+    if (out && put(out, "dx", dx) && put(out, "dgate_a", dga) && put(out, "dgate_x", dgx) && put(out, "drate", drate) &&
+        put(out, "dh0", dh0))
+        return out;
+    Py_XDECREF(out);
+    return nullptr;
+}
+
+// x, gate_a, gate_x, rate, state, normalize, h
+ENTRY(gated_scan_step, 7) {
+    const Tensor *x = channels(r, 0, 2);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t B = x->size(0), C = x->size(1);
+    const at::ScalarType type = x->scalar_type();
+    const Tensor *ga = r.like(1, type, x->sizes()), *gx = r.maybe(2, type, x->sizes()), *rate = r.like(3, F32, {C});
+    const Tensor *state = r.like(4, F32, x->sizes());
+    const bool normalize = flag(r, 5);
+    const Tensor *given = r.maybe(6, type, x->sizes());
+    if (!r.ok || !fits({B, C})) Py_RETURN_NONE;
+    const Tensor h = given_or(given, *x);
+    return result(s5_gated_scan_step(x->data_ptr(), ga->data_ptr(), data<void>(gx), dtype(*x), data(rate), normalize, (int)B, (int)C,
+                                     data(state), h.data_ptr(), r.stream()),
+                  h);
+}
+
+// The weight [C,K] of x's channels; its taps.
+int64_t taps(Reader &r, int i, int64_t C) {
+    const Tensor *w = r.tensor(i);
+    if (r.ok && (w->scalar_type() != F32 || w->dim() != 2 || w->size(0) != C || w->size(1) < 2)) r.ok = false;
+    return r.ok ? w->size(1) : 0;
+}
+
+// x, weight, bias, activation, past, past_out, reset, lengths, y
+ENTRY(short_conv_forward, 9) {
+    const Tensor *x = channels(r, 0, 3);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t B = x->size(0), L = x->size(1), C = x->size(2), K = taps(r, 1, C);
+    const at::ScalarType type = x->scalar_type();
+    const Tensor *w = r.tensor(1), *bias = r.maybe(2, F32, {C});
+    const int act = r.code(3);
+    const Tensor *past = r.maybe(4, type, {B, K - 1, C});
+    const bool ends = r.args[5] == Py_True;
+    const Tensor *last = ends ? nullptr : r.maybe(5, type, {B, K - 1, C});
+    const Marks m(r, 6, B, L);
+    const Tensor *given = r.maybe(8, type, x->sizes());
+    if (!r.ok || !fits({B, L, C, K})) Py_RETURN_NONE;
+    const Tensor y = given_or(given, *x), s = ends ? make({B, K - 1, C}, *x) : last ? *last : Tensor();
+    const s5_status code = s5_short_conv_forward(x->data_ptr(), C, dtype(*x), data(w), data(bias), (s5_activation)act, data<void>(past),
+                                                 m.bytes(), m.ints(), (int)B, (int)L, (int)C, (int)K, y.data_ptr(), C,
+                                                 at_or_null<void>(s), r.stream());
+    return s.defined() ? result(code, y, s) : result(code, y);
+}
+
+// x, weight, dy, bias, activation, past, dpast_out, reset, lengths, workspace
+ENTRY(short_conv_backward, 10) {
+    const Tensor *x = channels(r, 0, 3);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t B = x->size(0), L = x->size(1), C = x->size(2), K = taps(r, 1, C);
+    const at::ScalarType type = x->scalar_type();
+    const Tensor *w = r.tensor(1), *dy = r.like(2, type, x->sizes()), *bias = r.maybe(3, F32, {C});
+    const int act = r.code(4);
+    const Tensor *past = r.maybe(5, type, {B, K - 1, C}), *last = r.maybe(6, type, {B, K - 1, C});
+    const Marks m(r, 7, B, L);
+    const Tensor *work = r.none(9) ? nullptr : r.bytes(9);
+    if (!r.ok || !fits({B, L, C, K})) Py_RETURN_NONE;
+    const size_t need = work ? (size_t)work->numel() : s5_short_conv_workspace_size((int)C, (int)K);
+    if (need == 0) Py_RETURN_NONE;
+    const Tensor dx = make(x->sizes(), *x), dw = make({C, K}, *x, F32), db = bias ? make({C}, *x, F32) : Tensor();
+    const Tensor dpast = past ? make({B, K - 1, C}, *x) : Tensor();
+    const Tensor ws = work ? *work : make({(int64_t)need}, *x, at::kByte);
+    const s5_status code = s5_short_conv_backward(
+        x->data_ptr(), C, dtype(*x), data(w), data(bias), (s5_activation)act, data<void>(past), m.bytes(), m.ints(), (int)B, (int)L,
+        (int)C, (int)K, dy->data_ptr(), C, data<void>(last), dx.data_ptr(), C, data(&dw), at_or_null(db), at_or_null<void>(dpast),
+        ws.data_ptr(), need, r.stream());
+    if (code != S5_OK) return PyLong_FromLong(code);
+    PyObject *out = PyDict_New();
+    if (out && put(out, "dx", dx) && put(out, "dweight", dw) && put(out, "dbias", db) && put(out, "dpast", dpast)) return out;
+    Py_XDECREF(out);
+    return nullptr;
+}
+
+// x, weight, state, bias, activation, y
+ENTRY(short_conv_step, 6) {
+    const Tensor *x = channels(r, 0, 2);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t B = x->size(0), C = x->size(1), K = taps(r, 1, C);
+    const at::ScalarType type = x->scalar_type();
+    const Tensor *w = r.tensor(1), *state = r.like(2, type, {B, K - 1, C}), *bias = r.maybe(3, F32, {C});
+    const int act = r.code(4);
+    const Tensor *given = r.maybe(5, type, x->sizes());
+    if (!r.ok || !fits({B, C, K})) Py_RETURN_NONE;
+    const Tensor y = given_or(given, *x);
+    return result(s5_short_conv_step(x->data_ptr(), dtype(*x), data(w), data(bias), (s5_activation)act, (int)B, (int)C, (int)K,
+                                     state->data_ptr(), y.data_ptr(), r.stream()),
+                  y);
+}
+
+// x, weight, bias, residual, eps, y, total, saved
+ENTRY(add_layernorm, 8) {
+    const Tensor *x = channels(r, 0, 0);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t H = x->size(-1), N = x->numel() / H;
+    const at::ScalarType type = x->scalar_type();
+    const Tensor *w = r.maybe(1, F32, {H}), *bias = r.maybe(2, F32, {H}), *residual = r.maybe(3, type, x->sizes());
+    const double eps = r.number(4);
+    const Tensor *gy = r.maybe(5, type, x->sizes()), *gt = r.maybe(6, type, x->sizes()), *saved = r.maybe(7, F32, {N, 2});
+    if (!r.ok || !fits({H}) || (gt && !residual)) Py_RETURN_NONE;
+    const Tensor y = given_or(gy, *x), total = residual ? given_or(gt, *x) : Tensor();
+    const s5_status code =
+        s5_add_layernorm(x->data_ptr(), H, data<void>(residual), H, dtype(*x), data(w), data(bias), (float)eps, N, (int)H, y.data_ptr(),
+                         H, at_or_null<void>(total), H, data(saved), r.stream());
+    return residual ? result(code, y, total) : result(code, y);
+}
+
+// x, dy, saved, weight, bias, residual, dtotal, workspace
+ENTRY(add_layernorm_backward, 8) {
+    const Tensor *x = channels(r, 0, 0);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t H = x->size(-1), N = x->numel() / H;
+    const at::ScalarType type = x->scalar_type();
+    const Tensor *dy = r.like(1, type, x->sizes()), *saved = r.like(2, F32, {N, 2});
+    const Tensor *w = r.maybe(3, F32, {H}), *bias = r.maybe(4, F32, {H});
+    const Tensor *residual = r.maybe(5, type, x->sizes()), *dt = r.maybe(6, type, x->sizes());
+    const Tensor *work = r.none(7) ? nullptr : r.bytes(7);
+    if (!r.ok || !fits({H})) Py_RETURN_NONE;
+    const size_t need = work ? (size_t)work->numel() : w || bias ? s5_add_layernorm_workspace_size((int)H) : 0;
+    if ((w || bias) && need == 0) Py_RETURN_NONE;
+    const Tensor dx = make(x->sizes(), *x), dw = w ? make({H}, *x, F32) : Tensor(), db = bias ? make({H}, *x, F32) : Tensor();
+    const Tensor ws = work ? *work : need ? make({(int64_t)need}, *x, at::kByte) : Tensor();
+    const s5_status code = s5_add_layernorm_backward(x->data_ptr(), H, data<void>(residual), H, dy->data_ptr(), H, data<void>(dt), H,
+                                                     dtype(*x), data(w), data(saved), N, (int)H, dx.data_ptr(), H, at_or_null(dw),
+                                                     at_or_null(db), at_or_null<void>(ws), need, r.stream());
+    if (code != S5_OK) return PyLong_FromLong(code);
+    PyObject *out = PyDict_New();
+    if (out && put(out, "dx", dx) && put(out, "dweight", dw) && put(out, "dbias", db)) return out;
+    Py_XDECREF(out);
+    return nullptr;
+}
+
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(delta_step), METHOD(delta_forward), METHOD(delta_backward), METHOD(rotary),
-                         METHOD(qk_norm_rotary), METHOD(qk_norm_rotary_backward), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(qk_norm_rotary), METHOD(qk_norm_rotary_backward),
+                         METHOD(gated_scan_forward), METHOD(gated_scan_backward), METHOD(gated_scan_step),
+                         METHOD(short_conv_forward), METHOD(short_conv_backward), METHOD(short_conv_step),
+                         METHOD(add_layernorm), METHOD(add_layernorm_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "The common case of the binding's calls.", -1, methods};
 }  // namespace
 

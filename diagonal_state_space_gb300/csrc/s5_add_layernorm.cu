@@ -1,0 +1,395 @@
+// s5_add_layernorm.cu -- layer norm of a row, or of the sum of two, and its
+// backward pass with the weights' gradients.
+//
+//   s = x + residual,  mean = sum s / H,  inv = (sum (s - mean)^2 / H + eps)^-1/2
+//   y = n w + b,  n = (s - mean) inv
+//   g = dy w,  dx = inv (g - sum g / H - n sum(g n) / H) + dtotal
+//   dw = sum over rows of dy n,  db = sum over rows of dy.
+//
+// Bound: memory.  Forward, a row lies in the registers of one warp, or of as
+// many as it takes, between its loads and its stores: the mean first and then
+// the squares about it, so that a row far from zero keeps its digits.
+// Backward, a row is spread over more lanes, 16 columns each, because a lane
+// also keeps the weights' gradients of its columns over all the rows that it
+// sees; one block an SM adds its warps' sums up, and a second launch the
+// blocks'.  No atomics.
+#include "s5_rows.cuh"
+
+namespace s5 {
+namespace {
+using namespace rows;
+
+constexpr int MAX_H = 16384;
+constexpr int BWD_WARPS = 16;        // of a backward block; rows of more than 8192 take up to 32
+constexpr int BWD_COLS = 16;         // of a lane, backward
+
+struct NormArgs {
+    const void *x, *residual, *dy, *dtotal;
+    long long ldx, ldr, lddy, lddt;
+    const float *w, *bias;
+    float eps;
+    long long N;
+    int H, warps;                    // warps of a row
+    void *y, *total, *dx;
+    long long ldy, ldt, lddx;
+    float2 *saved;                   // [N] mean, inv
+    float *part;                     // [blocks][2][H]
+};
+
+// The sum over a row's warps, to all of them.  Every warp of the block calls it.
+__device__ __forceinline__ float row_sum(float v, int warps, float *smem) {
+#pragma unroll
+    for (int o = 16; o; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) smem[warp] = v;
+    __syncthreads();
+    v = lane < warps ? smem[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// NV vectors of V values a lane.  One warp a row: four rows a block; else a row a block.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(V * NV >= 64 ? 256 : V * NV >= 32 ? 512 : 1024) add_layernorm_fwd_kernel(const NormArgs p) {
+    __shared__ float sums[2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = p.warps == 1 ? (long long)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
+    if (row >= p.N) return;
+    const int at = ((p.warps == 1 ? 0 : warp * 32) + lane) * V, step = p.warps * 32 * V;
+    griddep_wait();
+    float s[NV][V];
+    {
+        typename Vec<T, V>::raw rx[NV], rr[NV];
+        const T *x = static_cast<const T *>(p.x) + row * p.ldx, *r = static_cast<const T *>(p.residual) + row * p.ldr;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (at + i * step < p.H) rx[i] = Vec<T, V>::get(x + at + i * step);
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (at + i * step < p.H) rr[i] = Vec<T, V>::get(r + at + i * step);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float t[V] = {};
+            if (at + i * step < p.H) {
+                Vec<T, V>::widen(rx[i], t);
+                if (p.residual) {
+                    float u[V];
+                    Vec<T, V>::widen(rr[i], u);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) t[v] += u[v];
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[i][v] = t[v];
+        }
+    }
+    if (p.total) {
+        T *t = static_cast<T *>(p.total) + row * p.ldt;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (at + i * step < p.H) Vec<T, V>::store(t + at + i * step, s[i]);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum += s[i][v];
+    const float mean = row_sum(sum, p.warps, sums[0]) / p.H;
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (at + i * step < p.H) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[i][v] -= mean, sum = fmaf(s[i][v], s[i][v], sum);
+        }
+    const float inv = 1.0f / sqrtf(row_sum(sum, p.warps, sums[1]) / p.H + p.eps);
+    if (p.saved && lane == 0 && (p.warps == 1 || warp == 0)) p.saved[row] = make_float2(mean, inv);
+    T *y = static_cast<T *>(p.y) + row * p.ldy;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = at + i * step;
+        if (c >= p.H) continue;
+        float w[V], b[V], o[V];
+        if (p.w) load_floats<V>(p.w + c, w);
+        if (p.bias) load_floats<V>(p.bias + c, b);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            o[v] = s[i][v] * inv;
+            if (p.w) o[v] *= w[v];
+            if (p.bias) o[v] += b[v];
+        }
+        Vec<T, V>::store(y + c, o);
+    }
+}
+
+// A block's warps in slots of `warps`, a row each at a time.
+template <typename T, int V, int NV, int MOST>
+__global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const NormArgs p) {
+    static_assert(V * NV == BWD_COLS, "columns of a lane");
+    __shared__ float2 sums[2][MOST];
+    extern __shared__ float shares[];    // [slots - 1][2][H]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int slots = (int)(blockDim.x >> 5) / p.warps, slot = warp / p.warps, first = slot * p.warps;
+    const int at = ((warp - first) * 32 + lane) * V, step = p.warps * 32 * V;
+    griddep_wait();
+    float w[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[i][v] = 1.0f, dw[i][v] = 0.0f, db[i][v] = 0.0f;
+        if (p.w && at + i * step < p.H) load_floats<V>(p.w + at + i * step, w[i]);
+    }
+    const long long stride = (long long)gridDim.x * slots;
+    const float per = 1.0f / p.H;
+    int turn = 0;
+    for (long long base = (long long)blockIdx.x * slots; base < p.N; base += stride, turn ^= 1) {
+        const long long row = base + slot;
+        const bool here = row < p.N;
+        typename Vec<T, V>::raw rs[NV], rr[NV], rd[NV], rt[NV];
+        float2 stat = make_float2(0.0f, 0.0f);
+        if (here) {
+            const T *s = static_cast<const T *>(p.x) + row * p.ldx, *d = static_cast<const T *>(p.dy) + row * p.lddy;
+            const T *t = static_cast<const T *>(p.dtotal) + row * p.lddt, *r = static_cast<const T *>(p.residual) + row * p.ldr;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (at + i * step < p.H) rs[i] = Vec<T, V>::get(s + at + i * step), rd[i] = Vec<T, V>::get(d + at + i * step);
+            if (p.residual) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (at + i * step < p.H) rr[i] = Vec<T, V>::get(r + at + i * step);
+            }
+            if (p.dtotal) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (at + i * step < p.H) rt[i] = Vec<T, V>::get(t + at + i * step);
+            }
+            stat = p.saved[row];
+        }
+        float n[NV][V], g[NV][V];
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float s[V] = {}, d[V] = {};
+            const bool in = here && at + i * step < p.H;
+            if (in) Vec<T, V>::widen(rs[i], s), Vec<T, V>::widen(rd[i], d);
+            if (in && p.residual) {
+                float u[V];
+                Vec<T, V>::widen(rr[i], u);
+#pragma unroll
+                for (int v = 0; v < V; ++v) s[v] += u[v];
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                n[i][v] = in ? (s[v] - stat.x) * stat.y : 0.0f;
+                g[i][v] = d[v] * w[i][v];
+                dw[i][v] = fmaf(d[v], n[i][v], dw[i][v]);
+                db[i][v] += d[v];
+                sum.x += g[i][v];
+                sum.y = fmaf(g[i][v], n[i][v], sum.y);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o /= 2) {
+            sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+            sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+        }
+        if (p.warps > 1) {
+            if (lane == 0) sums[turn][warp] = sum;
+            __syncthreads();
+            sum = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < p.warps; ++j) sum.x += sums[turn][first + j].x, sum.y += sums[turn][first + j].y;
+        }
+        sum.x *= per, sum.y *= per;
+        if (!here) continue;
+        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (at + i * step >= p.H) continue;
+            float o[V], t[V];
+            if (p.dtotal) Vec<T, V>::widen(rt[i], t);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                o[v] = stat.y * (g[i][v] - sum.x - n[i][v] * sum.y);
+                if (p.dtotal) o[v] += t[v];
+            }
+            Vec<T, V>::store(dx + at + i * step, o);
+        }
+    }
+    if (!p.part) return;
+    if (slot > 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (at + i * step < p.H) {
+                store_floats<V>(shares + (long long)(slot - 1) * 2 * p.H + at + i * step, dw[i]);
+                store_floats<V>(shares + (long long)(slot - 1) * 2 * p.H + p.H + at + i * step, db[i]);
+            }
+    }
+    __syncthreads();
+    if (slot > 0) return;
+    float *part = p.part + (long long)blockIdx.x * 2 * p.H;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = at + i * step;
+        if (c >= p.H) continue;
+        for (int q = 1; q < slots; ++q) {
+            float a[V], b[V];
+            load_floats<V>(shares + (long long)(q - 1) * 2 * p.H + c, a);
+            load_floats<V>(shares + (long long)(q - 1) * 2 * p.H + p.H + c, b);
+#pragma unroll
+            for (int v = 0; v < V; ++v) dw[i][v] += a[v], db[i][v] += b[v];
+        }
+        store_floats<V>(part + c, dw[i]);
+        store_floats<V>(part + p.H + c, db[i]);
+    }
+}
+
+// The blocks' parts in their order, 8 sums side by side and then joined.  blockIdx.y: dw, db.
+__global__ void __launch_bounds__(256) add_layernorm_weight_kernel(const float *part, int parts, int H, float *dw, float *db) {
+    __shared__ float sums[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float *out = blockIdx.y ? db : dw;
+    griddep_wait();
+    if (!out) return;
+    float s = 0.0f;
+    if (c < H)
+        for (int i = w; i < parts; i += 8) s += part[((long long)i * 2 + blockIdx.y) * H + c];
+    sums[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < H) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sums[i][lane];
+        out[c] = s;
+    }
+}
+
+// ------------------------------------------------------------------ launches
+template <typename T, int V, int NV> cudaError_t fwd_as(NormArgs &p, cudaStream_t st) {
+    const int per = 32 * V * NV;
+    p.warps = (p.H + per - 1) / per;
+    const int rows = p.warps == 1 ? 4 : 1;
+    return launch(add_layernorm_fwd_kernel<T, V, NV>, dim3((unsigned)((p.N + rows - 1) / rows)), 32 * p.warps * rows, 0, 1, st, p);
+}
+// A row in as few warps as a lane's columns allow (64 of 16 bits, 32 of 32) where the rows fill the SMs, else spread over more.
+template <typename T, int V> cudaError_t fwd_by(NormArgs &p, cudaStream_t st) {
+    constexpr int MOST = V * sizeof(T) < 16 ? 16 : sizeof(T) == 2 ? 64 : 32;
+    auto warps = [&](int cols) { return (p.H + 32 * cols - 1) / (32 * cols); };
+    int cols = MOST;
+    while (cols > V && warps(cols / 2) <= 32 && (warps(cols / 2) == 1 || p.N * warps(cols) < 8 * SMS)) cols /= 2;
+    if (cols == V) return fwd_as<T, V, 1>(p, st);
+    if (cols == 2 * V) return fwd_as<T, V, 2>(p, st);
+    if (cols == 4 * V) return fwd_as<T, V, 4>(p, st);
+    if constexpr (MOST >= 16 * V)
+        if (cols == 16 * V) return fwd_as<T, V, 16>(p, st);
+    return fwd_as<T, V, 8>(p, st);
+}
+
+int bwd_slots(int H) {
+    const int warps = (H + 32 * BWD_COLS - 1) / (32 * BWD_COLS);
+    return warps >= BWD_WARPS ? 1 : BWD_WARPS / warps;
+}
+int bwd_blocks(long long N, int H) {
+    const long long need = (N + bwd_slots(H) - 1) / bwd_slots(H);
+    return (int)(need < SMS ? need : SMS);
+}
+
+template <typename T, int V> cudaError_t bwd_by(NormArgs &p, float *dw, float *db, cudaStream_t st) {
+    p.warps = (p.H + 32 * BWD_COLS - 1) / (32 * BWD_COLS);
+    const int slots = bwd_slots(p.H), blocks = bwd_blocks(p.N, p.H);
+    const size_t smem = sizeof(float) * (size_t)(slots - 1) * 2 * p.H;
+    const int threads = 32 * p.warps * slots;
+    const cudaError_t e = p.warps <= BWD_WARPS
+                              ? launch_big(add_layernorm_bwd_kernel<T, V, BWD_COLS / V, BWD_WARPS>, dim3(blocks), threads, smem, 1, st, p)
+                              : launch_big(add_layernorm_bwd_kernel<T, V, BWD_COLS / V, 32>, dim3(blocks), threads, smem, 1, st, p);
+    if (e != cudaSuccess || !p.part) return e;
+    return launch(add_layernorm_weight_kernel, dim3((p.H + 31) / 32, 2), 256, 0, 1, st, (const float *)p.part, blocks, p.H, dw, db);
+}
+
+int width(s5_dtype dtype, int H, std::initializer_list<long long> lds) {
+    const int per = dtype == S5_BF16 ? 8 : 4;
+    int w = H % per == 0 ? per : H % 2 == 0 ? 2 : 1;
+    for (long long ld : lds) w = ld % per == 0 ? w : ld % 2 == 0 && w > 1 ? 2 : 1;
+    return w;
+}
+
+s5_status check_norm(s5_dtype dtype, long long N, int H, const float *w, const float *bias) {
+    if (!type_ok(dtype) || N < 0 || H < 1) return S5_ERR_INVALID_ARGUMENT;
+    if (H > MAX_H || N > (1ll << 31) - 4) return S5_ERR_UNSUPPORTED;
+    if (!aligned(w, 16) || !aligned(bias, 16)) return S5_ERR_INVALID_ARGUMENT;
+    return S5_OK;
+}
+
+}  // namespace
+}  // namespace s5
+
+using namespace s5;
+
+extern "C" s5_status s5_add_layernorm(const void *x, long long ldx, const void *residual, long long ldr, s5_dtype dtype,
+                                      const float *weight, const float *bias, float eps, long long N, int H, void *y,
+                                      long long ldy, void *total, long long ldt, float *saved, s5_stream_t stream) {
+    const s5_status c = check_norm(dtype, N, H, weight, bias);
+    if (c != S5_OK) return c;
+    if (!(eps >= 0.0f) || eps > 1e30f) return S5_ERR_INVALID_ARGUMENT;
+    if (N == 0) return S5_OK;
+    if (!rows_ok(x, ldx, H) || !rows_ok(y, ldy, H) || (residual && !rows_ok(residual, ldr, H)) || (total && !rows_ok(total, ldt, H)))
+        return S5_ERR_INVALID_ARGUMENT;
+    if (!aligned(saved, 16) || y == total) return S5_ERR_INVALID_ARGUMENT;
+    for (const void *in : {x, residual})
+        if (in && ((y == in && ldy != (in == x ? ldx : ldr)) || (total == in && ldt != (in == x ? ldx : ldr)))) return S5_ERR_INVALID_ARGUMENT;
+    NormArgs p = {};
+    p.x = x, p.ldx = ldx, p.residual = residual, p.ldr = residual ? ldr : 0, p.w = weight, p.bias = bias, p.eps = eps, p.N = N, p.H = H;
+    p.y = y, p.ldy = ldy, p.total = total, p.ldt = total ? ldt : 0, p.saved = reinterpret_cast<float2 *>(saved);
+    const int w = width(dtype, H, {ldx, p.ldr, ldy, p.ldt});
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    if (dtype == S5_BF16) e = w == 8 ? fwd_by<__nv_bfloat16, 8>(p, st) : w == 2 ? fwd_by<__nv_bfloat16, 2>(p, st) : fwd_by<__nv_bfloat16, 1>(p, st);
+    else e = w == 4 ? fwd_by<float, 4>(p, st) : w == 2 ? fwd_by<float, 2>(p, st) : fwd_by<float, 1>(p, st);
+    return e == cudaSuccess ? S5_OK : cuda_failure(e);
+}
+
+extern "C" size_t s5_add_layernorm_workspace_size(int H) {
+    return H < 1 || H > MAX_H ? 0 : 256 + sizeof(float) * 2 * (size_t)SMS * H;
+}
+
+extern "C" s5_status s5_add_layernorm_backward(const void *x, long long ldx, const void *residual, long long ldr, const void *dy,
+                                               long long lddy, const void *dtotal, long long lddt, s5_dtype dtype, const float *weight, const float *saved, long long N,
+                                               int H, void *dx, long long lddx, float *dweight, float *dbias, void *workspace,
+                                               size_t workspace_bytes, s5_stream_t stream) {
+    const s5_status c = check_norm(dtype, N, H, weight, dweight);
+    if (c != S5_OK) return c;
+    if (!aligned(dbias, 16)) return S5_ERR_INVALID_ARGUMENT;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (N == 0) {
+        cudaError_t e = cudaSuccess;
+        if (dweight) e = cudaMemsetAsync(dweight, 0, sizeof(float) * H, st);
+        if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, sizeof(float) * H, st);
+        return e == cudaSuccess ? S5_OK : cuda_failure(e);
+    }
+    if (!rows_ok(x, ldx, H) || !rows_ok(dy, lddy, H) || !rows_ok(dx, lddx, H) || (dtotal && !rows_ok(dtotal, lddt, H)) ||
+        (residual && !rows_ok(residual, ldr, H)))
+        return S5_ERR_INVALID_ARGUMENT;
+    if ((dx == x && lddx != ldx) || (dx == residual && lddx != ldr) || (dx == dy && lddx != lddy) || (dx == dtotal && lddx != lddt))
+        return S5_ERR_INVALID_ARGUMENT;
+    if (!saved || !aligned(saved, 16)) return S5_ERR_INVALID_ARGUMENT;
+    const bool weights = dweight || dbias;
+    if (weights && (!workspace || !aligned(workspace, 16) || workspace_bytes < s5_add_layernorm_workspace_size(H)))
+        return S5_ERR_INVALID_ARGUMENT;
+    NormArgs p = {};
+    p.x = x, p.ldx = ldx, p.residual = residual, p.ldr = residual ? ldr : 0, p.dy = dy, p.lddy = lddy, p.dtotal = dtotal, p.lddt = dtotal ? lddt : 0, p.w = weight;
+    p.saved = reinterpret_cast<float2 *>(const_cast<float *>(saved)), p.N = N, p.H = H, p.dx = dx, p.lddx = lddx;
+    p.part = weights ? static_cast<float *>(workspace) : nullptr;
+    const int w = width(dtype, H, {ldx, p.ldr, lddy, lddx, p.lddt});
+    cudaError_t e;
+    if (dtype == S5_BF16)
+        e = w == 8   ? bwd_by<__nv_bfloat16, 8>(p, dweight, dbias, st)
+            : w == 2 ? bwd_by<__nv_bfloat16, 2>(p, dweight, dbias, st)
+                     : bwd_by<__nv_bfloat16, 1>(p, dweight, dbias, st);
+    else
+        e = w == 4   ? bwd_by<float, 4>(p, dweight, dbias, st)
+            : w == 2 ? bwd_by<float, 2>(p, dweight, dbias, st)
+                     : bwd_by<float, 1>(p, dweight, dbias, st);
+    return e == cudaSuccess ? S5_OK : cuda_failure(e);
+}

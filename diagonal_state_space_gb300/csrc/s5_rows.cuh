@@ -1,0 +1,104 @@
+// s5_rows.cuh -- what the kernels on rows of channels share (s5_gated_scan.cu,
+// s5_short_conv.cu, s5_add_layernorm.cu): values in vectors, launches.
+#pragma once
+#include "s5_internal.cuh"
+
+namespace s5 {
+namespace rows {
+
+template <int BYTES> struct Raw;
+template <> struct Raw<16> { using type = uint4; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<4> { using type = unsigned; };
+template <> struct Raw<2> { using type = unsigned short; };
+
+// V values as they lie in memory, and as floats.
+template <typename T, int V> struct Vec {
+    using raw = typename Raw<sizeof(T) * V>::type;
+    __device__ static raw get(const T *p) { return *reinterpret_cast<const raw *>(p); }
+    __device__ static void put(T *p, const raw &t) { *reinterpret_cast<raw *>(p) = t; }
+    __device__ static void widen(const raw &t, float (&r)[V]) {
+        const T *e = reinterpret_cast<const T *>(&t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = (float)e[i];
+    }
+    __device__ static raw round(const float (&r)[V]) {
+        raw t;
+        T *e = reinterpret_cast<T *>(&t);
+        if constexpr (sizeof(T) == 2 && V > 1) {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) *reinterpret_cast<__nv_bfloat162 *>(e + i) = __floats2bfloat162_rn(r[i], r[i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[i] = (T)r[i];
+        }
+        return t;
+    }
+    __device__ static void load(const T *p, float (&r)[V]) { widen(get(p), r); }
+    __device__ static void store(T *p, const float (&r)[V]) { put(p, round(r)); }
+};
+
+// V floats of a parameter or a sum, by 16 bytes at most.
+template <int V> __device__ __forceinline__ void load_floats(const float *p, float (&r)[V]) {
+    constexpr int N = V < 4 ? V : 4;
+#pragma unroll
+    for (int i = 0; i < V; i += N) Vec<float, N>::load(p + i, *reinterpret_cast<float(*)[N]>(r + i));
+}
+template <int V> __device__ __forceinline__ void store_floats(float *p, const float (&r)[V]) {
+    constexpr int N = V < 4 ? V : 4;
+#pragma unroll
+    for (int i = 0; i < V; i += N) Vec<float, N>::store(p + i, *reinterpret_cast<const float(*)[N]>(r + i));
+}
+
+// 2^x, 1/x, 1/sqrt(x): the machine's own, off by 2^-22, 2^-23, 2^-22.4 relative.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rsqrt_(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid(float g) { return rcp(1.0f + ex2(-LOG2E * g)); }
+
+inline bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+inline bool type_ok(int dtype) { return dtype == S5_F32 || dtype == S5_BF16; }
+// An array that has to be there, 16-byte aligned, of rows with a pitch.
+inline bool rows_ok(const void *p, long long ld, long long width) { return p && aligned(p, 16) && ld >= width; }
+
+// A launch that may be scheduled while the kernel before it on the stream
+// ends (the kernel waits for that one itself), in clusters of `cluster` blocks.
+template <typename... Ks, typename... As>
+cudaError_t launch(void (*k)(Ks...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, As... args) {
+    cudaLaunchAttribute attr[2];
+    set_programmatic(attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+// The same for a kernel with dynamic shared memory beyond 48 KB.
+template <typename... Ks, typename... As>
+cudaError_t launch_big(void (*k)(Ks...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, As... args) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return e != cudaSuccess ? e : launch(k, grid, threads, smem, cluster, st, args...);
+}
+
+constexpr int SMS = 152;
+
+}  // namespace rows
+}  // namespace s5

@@ -58,6 +58,8 @@ typedef enum { S5_F32 = 0, S5_BF16 = 1 } s5_dtype;
 
 typedef enum { S5_ZOH = 0, S5_BILINEAR = 1 } s5_discretization;
 
+typedef enum { S5_ACT_NONE = 0, S5_ACT_SILU = 1 } s5_activation;
+
 /*
  * Zero-order-hold discretisation ("SIMPLIFIED STATE SPACE LAYERS ...",
  * section 3.2 eq. 6; review row 2):
@@ -489,6 +491,127 @@ s5_status s5_qk_norm_rotary_backward(const void *q, long long ldq, const void *k
                                      long long lddko, void *dq, long long lddq, void *dk, long long lddk,
                                      float *dq_weight, float *dk_weight, void *workspace,
                                      size_t workspace_bytes, s5_stream_t stream);
+
+/* ========================================================================
+ * The parts of a gated recurrent block beside its projections: a linear
+ * recurrence of each channel with gates from the tokens, a short causal
+ * convolution in front of it, and layer norm with the residual's sum.
+ *
+ * Rows: [B][L][C] (or [N][H]) of `dtype`, values of a token contiguous, with a
+ * pitch in elements between two tokens (ld >= C; a batch is L pitches); states
+ * float32 and contiguous.  Array bases 16-byte aligned (reset: any; lengths: 4).
+ *   reset [B][L], or NULL: a token whose byte is not 0 begins a new sequence;
+ *     nothing of the tokens before it, NaN included, reaches it.
+ *   lengths [B], or NULL: tokens of each row (taken into 0 .. L).  What lies
+ *     behind is not read, and outputs and gradients there are zeros.
+ * Outputs do not overlap inputs or each other but where a call says so.  All
+ * arithmetic in 32 bits, one rounding at the end.  No atomics: equal inputs
+ * give equal bits.  Asynchronous, launched with programmatic stream
+ * serialisation; no call waits inside a kernel for another block's memory.
+ * Errors S5_ERR_INVALID_ARGUMENT, S5_ERR_UNSUPPORTED, S5_ERR_CUDA.
+ * ======================================================================== */
+
+/*
+ * Gated linear recurrence.  Per sequence and channel, with rate [C] float32 >= 0
+ * and the state h (float32) from h0 [B][C], or zero (NULL):
+ *   r = sigmoid(gate_a),  a = exp(-rate r),  0 at a reset
+ *   n = sqrt(1 - a^2) if normalize, else 1
+ *   h_t = a_t h_{t-1} + n_t sigmoid(gate_x_t) x_t       (gate_x NULL: n_t x_t)
+ * h_last [B][C] (may be NULL, may be h0) gets the state after the row's last
+ * token.  saved NULL: nothing is kept.  B ceil(C / 16) <= 2^27, L <= 2^30.
+ * L = 0 leaves the state as it is; B = 0 is a no-op.
+ */
+size_t s5_gated_scan_saved_size(int B, int L, int C);
+s5_status s5_gated_scan_forward(const void *x, long long ldx, const void *gate_a, long long ldga, const void *gate_x,
+                                long long ldgx, s5_dtype dtype, const float *rate, const float *h0,
+                                const unsigned char *reset, const int *lengths, int normalize, int B, int L, int C,
+                                void *h, long long ldh, float *h_last, void *saved, size_t saved_bytes,
+                                s5_stream_t stream);
+
+/*
+ * Gradients of sum(dh * h) + sum(dh_last * h_last) (dh_last NULL: zero) with the
+ * forward's inputs and its `saved` buffer (the state every 64 tokens).  With
+ * u = sigmoid(gate_x) x, s = sigmoid(gate_x):
+ *   G_t = dh_t + a_{t+1} G_{t+1},  dla = G (a h_{t-1} - a^2 / n u)   (0 at a reset;
+ *     the second part 0 where rate r = 0, whose root has no slope, or not normalize)
+ *   dgate_a = -rate dla r (1 - r),  drate = -sum dla r,  dh0 = a_0 G_0,
+ *   dx = G n s,  dgate_x = G n x s (1 - s).
+ * dx, dgate_a, dgate_x (with gate_x) of `dtype`; drate [C] and dh0 [B][C] (NULL:
+ * not wanted; may be dh_last) float32.  workspace: scratch, no initialisation.
+ */
+size_t s5_gated_scan_workspace_size(int B, int L, int C);
+s5_status s5_gated_scan_backward(const void *x, long long ldx, const void *gate_a, long long ldga, const void *gate_x,
+                                 long long ldgx, s5_dtype dtype, const float *rate, const unsigned char *reset,
+                                 const int *lengths, int normalize, int B, int L, int C, const void *dh, long long lddh,
+                                 const float *dh_last, const void *saved, size_t saved_bytes, void *dx, long long lddx,
+                                 void *dgate_a, long long lddga, void *dgate_x, long long lddgx, float *drate,
+                                 float *dh0, void *workspace, size_t workspace_bytes, s5_stream_t stream);
+
+/* One token per sequence: x, gate_a, gate_x (or NULL), h [B][C] of `dtype`,
+ * contiguous; state [B][C] float32 is updated in place.  h may be x. */
+s5_status s5_gated_scan_step(const void *x, const void *gate_a, const void *gate_x, s5_dtype dtype, const float *rate,
+                             int normalize, int B, int C, float *state, void *h, s5_stream_t stream);
+
+/*
+ * Short causal convolution of each channel, weight [C][K] and bias [C] (or NULL)
+ * float32, K from 2 to 8 (S5_ERR_UNSUPPORTED otherwise):
+ *   p_t = bias + sum_{j < K} weight_j x_{t-K+1+j},   y = p, or p sigmoid(p) (S5_ACT_SILU)
+ * The tokens before the sequence are past [B][K-1][C] of `dtype`, or zeros
+ * (NULL); those before a reset are zeros.  past_out [B][K-1][C] (may be NULL, may
+ * be past) gets the row's last K - 1 inputs, the past's among them where the row
+ * has fewer, zeros for what a reset cut off: the next call's past.
+ * B ceil(L / 8) <= 2^30, and that over 4 times ceil(C / 32).
+ */
+s5_status s5_short_conv_forward(const void *x, long long ldx, s5_dtype dtype, const float *weight, const float *bias,
+                                s5_activation activation, const void *past, const unsigned char *reset,
+                                const int *lengths, int B, int L, int C, int K, void *y, long long ldy, void *past_out,
+                                s5_stream_t stream);
+
+/*
+ * Gradients of sum(dy * y) + sum(dpast_out * past_out) (dpast_out NULL: zero):
+ *   dp = dy act'(p),  dx_t = sum_j weight_j dp_{t+K-1-j},  dweight_j = sum dp_t x_{t-K+1+j},  dbias = sum dp.
+ * dx, dpast [B][K-1][C] (NULL: not wanted) of `dtype`; dweight [C][K], dbias [C]
+ * (NULL: not wanted) float32.  workspace: scratch, no initialisation.
+ */
+size_t s5_short_conv_workspace_size(int C, int K);
+s5_status s5_short_conv_backward(const void *x, long long ldx, s5_dtype dtype, const float *weight, const float *bias,
+                                 s5_activation activation, const void *past, const unsigned char *reset,
+                                 const int *lengths, int B, int L, int C, int K, const void *dy, long long lddy,
+                                 const void *dpast_out, void *dx, long long lddx, float *dweight, float *dbias,
+                                 void *dpast, void *workspace, size_t workspace_bytes, s5_stream_t stream);
+
+/* One token per sequence: x, y [B][C] of `dtype`, contiguous; state [B][K-1][C],
+ * the inputs before it, is moved on in place.  y may be x. */
+s5_status s5_short_conv_step(const void *x, s5_dtype dtype, const float *weight, const float *bias,
+                             s5_activation activation, int B, int C, int K, void *state, void *y, s5_stream_t stream);
+
+/*
+ * Layer norm of the rows of x [N][H], or of x + residual (residual not NULL):
+ *   s = x + residual,  y = (s - mean) / sqrt(var + eps) * weight + bias
+ * with the biased variance; weight, bias [H] float32 or NULL (1, 0).  total [N][H]
+ * (NULL: not wanted) gets s; the norm is that of s before its rounding.  saved
+ * [N][2] float32 (NULL: not wanted) gets the mean and 1 / sqrt(var + eps), for the
+ * backward pass.  y or total may be x or residual (same pitch).  H <= 16384
+ * (S5_ERR_UNSUPPORTED otherwise), N < 2^31 - 4, eps >= 0.  N = 0 is a no-op.
+ */
+s5_status s5_add_layernorm(const void *x, long long ldx, const void *residual, long long ldr, s5_dtype dtype,
+                           const float *weight, const float *bias, float eps, long long N, int H, void *y,
+                           long long ldy, void *total, long long ldt, float *saved, s5_stream_t stream);
+
+/*
+ * Gradients of sum(dy * y) + sum(dtotal * total) (dtotal NULL: zero) with the
+ * forward's x, residual, weight and saved.  dx is the gradient of x and of the
+ * residual alike; it may be x, residual, dy or dtotal (same pitch).  dweight,
+ * dbias [H] float32, NULL: not wanted; with either a workspace (scratch, no
+ * initialisation) is needed.  The forward's total as x, without a residual, reads
+ * an array less, and the gradients then carry total's rounding.
+ */
+size_t s5_add_layernorm_workspace_size(int H);
+s5_status s5_add_layernorm_backward(const void *x, long long ldx, const void *residual, long long ldr, const void *dy,
+                                    long long lddy, const void *dtotal, long long lddt, s5_dtype dtype,
+                                    const float *weight, const float *saved, long long N, int H, void *dx,
+                                    long long lddx, float *dweight, float *dbias, void *workspace,
+                                    size_t workspace_bytes, s5_stream_t stream);
 
 /* Waits for `stream`, returns the first device-side condition latched in
  * `workspace` since the last call (S5_OK if none) and clears it. */
