@@ -323,7 +323,7 @@ def _own(st):
         out["y"], total = y
         out["total"] = total
     if op == "norm_train":
-        out.update(there(api.s5_add_layernorm_backward(total, st["dy"], saved, dtotal=st["dtotal"], **kw)))
+        out.update(there(api.s5_add_layernorm_backward(st["x"], st["dy"], saved, residual=st["residual"], dtotal=st["dtotal"], **kw)))
     return out
 
 
