@@ -34,9 +34,9 @@ namespace {
 using namespace rows;
 using sm100::smem_addr;
 
-constexpr int THREADS = 256;
-constexpr int KEEP = 64;        // tokens between two kept states
-constexpr int MAX_CLUSTER = 8;
+constexpr int THREADS = 128;    // four blocks an SM
+constexpr int KEEP = 32;        // tokens between two kept states, and of a tile backward (twice that forward)
+constexpr int MAX_CLUSTER = 16; // beyond 8 a non-portable size
 
 struct ScanArgs {
     const void *x, *ga, *gx;            // gx null: u = x
@@ -68,29 +68,25 @@ __device__ __forceinline__ float join(float A, float a) { return A == 0.0f || a 
 __device__ __forceinline__ float apply(float A, float h, float E) { return A == 0.0f ? E : fmaf(A, h, E); }
 
 // a = exp(z) and 1 - a^2 for z <= 0.  Above -1/4 the series of exp(z) - 1 up to z^6 (the rest is below 2^-23 of it).
-__device__ __forceinline__ void decay(float z, float &a, float &n2) {
-    float q = fmaf(z, 1.0f / 720, 1.0f / 120);
-    q = fmaf(z, q, 1.0f / 24);
-    q = fmaf(z, q, 1.0f / 6);
-    q = fmaf(z, q, 0.5f);
-    const float near = fmaf(z * z, q, z), far = ex2(LOG2E * z);
-    const bool close = z > -0.25f;
-    const float m = close ? near : far - 1.0f;
-    a = close ? 1.0f + near : far;
-    n2 = -m * (2.0f + m);
+template <int V> __device__ __forceinline__ void decay(const Many<V> &z, Many<V> &a, Many<V> &n2) {
+    using M = Many<V>;
+    M q = fma(z, M::all(1.0f / 720), M::all(1.0f / 120));
+    q = fma(z, q, M::all(1.0f / 24));
+    q = fma(z, q, M::all(1.0f / 6));
+    q = fma(z, q, M::all(0.5f));
+    const M near = fma(z * z, q, z), grown = near + M::all(1.0f);
+    M far = z * M::all(LOG2E);
+#pragma unroll
+    for (int i = 0; i < V; ++i) far[i] = ex2(far[i]);
+    M m = far + M::all(-1.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool close = z[i] > -0.25f;
+        m[i] = close ? near[i] : m[i];
+        a[i] = close ? grown[i] : far[i];
+    }
+    n2 = m * fma(m, M::all(-1.0f), M::all(-2.0f));
 }
-// sqrt(n2) and 1 / sqrt(n2), both 0 at 0.
-__device__ __forceinline__ void root(float n2, float &n, float &inv) {
-    const float s = rsqrt_(fmaxf(n2, 1e-37f));
-    n = n2 * s;
-    inv = n2 > 0.0f ? s : 0.0f;
-}
-
-__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -106,91 +102,102 @@ __device__ __forceinline__ void send(float2 *p, unsigned rank, float2 v) {
 template <typename T_, int V_, int LANES_, int S_, int ARRAYS_, bool ASYNC_> struct Shape {
     using T = T_;
     static constexpr int V = V_, LANES = LANES_, S = S_, ARRAYS = ARRAYS_;
-    static constexpr bool ASYNC = ASYNC_;                     // tiles come by 16-byte copies, one ahead
+    static constexpr bool ASYNC = ASYNC_;                     // tiles come by 16-byte copies
     static constexpr int GROUPS = THREADS / LANES, WIDE = LANES * V, TILE = GROUPS * S;
     static constexpr int STAGE = ASYNC ? ARRAYS * TILE * WIDE * (int)sizeof(T) : 0;
     static constexpr int PAIRS = MAX_CLUSTER * WIDE;          // of a round
-    static constexpr int SMEM = 2 * STAGE + 2 * PAIRS * (int)sizeof(float2) + (ARRAYS == 4 ? 3 : 2) * GROUPS * WIDE * (int)sizeof(float);
-    static_assert(TILE % KEEP == 0 && KEEP % S == 0, "kept states lie at a group's start");
+    static constexpr int STAGES = ARRAYS == 4 ? 2 : 1;        // backward a tile is read twice
+    static constexpr int SMEM = STAGES * STAGE + 2 * PAIRS * (int)sizeof(float2) + (ARRAYS == 4 ? 3 : 2) * GROUPS * WIDE * (int)sizeof(float);
+    static_assert(TILE == KEEP || TILE == 2 * KEEP, "kept states lie at a group's start");
+    static_assert(LANES * 2 == 32 || LANES == 32, "a warp holds one or two groups");
 };
 
 // A block's place: its sequence, channels and rank, and the arrays in its shared memory.
 template <typename Sh> struct Block {
     using T = typename Sh::T;
-    T *stage[2];
+    using M = Many<Sh::V>;
+    static constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
+    T *stage;           // [STAGES][ARRAYS][TILE][WIDE]
     float2 *pairs;      // [2][MAX_CLUSTER][WIDE]
     float *A, *E, *Z;   // [GROUPS][WIDE] (Z: backward)
     int b, c0, rank, lane, group, c;
     int len;            // tokens of this sequence
     __device__ Block(const ScanArgs &p, unsigned char *smem) {
-        stage[0] = reinterpret_cast<T *>(smem);
-        stage[1] = reinterpret_cast<T *>(smem + Sh::STAGE);
-        pairs = reinterpret_cast<float2 *>(smem + 2 * Sh::STAGE);
+        stage = reinterpret_cast<T *>(smem);
+        pairs = reinterpret_cast<float2 *>(smem + Sh::STAGES * Sh::STAGE);
         A = reinterpret_cast<float *>(pairs + 2 * Sh::PAIRS);
-        E = A + Sh::GROUPS * Sh::WIDE;
-        Z = E + Sh::GROUPS * Sh::WIDE;
-        const int K = p.cluster, across = (p.C + Sh::WIDE - 1) / Sh::WIDE;
+        E = A + Sh::GROUPS * W;
+        Z = E + Sh::GROUPS * W;
+        const int K = p.cluster, across = (p.C + W - 1) / W;
         rank = blockIdx.x % K;
         const int chain = blockIdx.x / K;
         b = chain / across;
-        c0 = chain % across * Sh::WIDE;
+        c0 = chain % across * W;
         lane = threadIdx.x % Sh::LANES;
         group = threadIdx.x / Sh::LANES;
-        c = c0 + lane * Sh::V;
+        c = c0 + lane * V;
     }
     __device__ void read_length(const ScanArgs &p) { len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L; }
-    // Copies of tile t0 of the given arrays into a stage: rows of WIDE values one after the other, zeros where there is nothing to read.
+    // Copies of this warp's rows of the tile at t0 into a stage, zeros where there is nothing to read.
     __device__ void fetch(const ScanArgs &p, int which, int t0, const void *const *from, const long long *ld) {
-        constexpr int PER = 16 / sizeof(T), CHUNKS = Sh::WIDE / PER, ROWS = THREADS / CHUNKS;
-        const int chunk = threadIdx.x % CHUNKS, row = threadIdx.x / CHUNKS, at = c0 + chunk * PER;
+        constexpr int PER = 16 / sizeof(T), CHUNKS = W / PER, ROWS = 32 / CHUNKS, MINE = Sh::TILE / (THREADS / 32);
+        const int l = threadIdx.x & 31, chunk = l % CHUNKS, row = threadIdx.x / 32 * MINE + l / CHUNKS, at = c0 + chunk * PER;
+        const bool whole = t0 + Sh::TILE <= len && c0 + W <= p.C;
 #pragma unroll
         for (int k = 0; k < Sh::ARRAYS; ++k) {
             if (!from[k]) continue;
             const T *src = static_cast<const T *>(from[k]) + ((long long)b * p.L + t0 + row) * ld[k] + at;
-            T *dst = stage[which] + (k * Sh::TILE + row) * Sh::WIDE + chunk * PER;
+            unsigned dst = smem_addr(stage + ((which * Sh::ARRAYS + k) * Sh::TILE + row) * W + chunk * PER);
+            const long long hop = ROWS * ld[k];
+            if (whole) {
 #pragma unroll
-            for (int i = 0; i < Sh::TILE / ROWS; ++i) {
-                const bool there = t0 + row + i * ROWS < len && at < p.C;
-                cp_async16(dst + i * ROWS * Sh::WIDE, there ? src + (long long)i * ROWS * ld[k] : from[k], there);
+                for (int i = 0; i < MINE / ROWS; ++i, src += hop) cp_async16(dst + i * ROWS * W * (int)sizeof(T), src);
+            } else {
+#pragma unroll
+                for (int i = 0; i < MINE / ROWS; ++i, src += hop) {
+                    const bool there = t0 + row + i * ROWS < len && at < p.C;
+                    cp_async16(dst + i * ROWS * W * (int)sizeof(T), there ? src : from[k], there);
+                }
             }
         }
     }
     // V values of array k at this thread's token s of the tile.
-    __device__ void load(const ScanArgs &p, int which, int t0, int s, int k, const void *const *from, const long long *ld,
-                         float (&r)[Sh::V]) const {
+    __device__ M load(const ScanArgs &p, int which, int t0, int s, int k, const void *const *from, const long long *ld) const {
+        M r = M::all(0.0f);
         if constexpr (Sh::ASYNC) {
-            Vec<T, Sh::V>::load(stage[which] + (k * Sh::TILE + group * Sh::S + s) * Sh::WIDE + lane * Sh::V, r);
+            Vec<T, V>::load(stage + ((which * Sh::ARRAYS + k) * Sh::TILE + group * S + s) * W + lane * V, r.v);
         } else {
-            const int t = t0 + group * Sh::S + s;
-            if (t < len && c < p.C) {
-                Vec<T, Sh::V>::load(static_cast<const T *>(from[k]) + ((long long)b * p.L + t) * ld[k] + c, r);
-            } else {
-#pragma unroll
-                for (int v = 0; v < Sh::V; ++v) r[v] = 0.0f;
-            }
+            const int t = t0 + group * S + s;
+            if (t < len && c < p.C) Vec<T, V>::load(static_cast<const T *>(from[k]) + ((long long)b * p.L + t) * ld[k] + c, r.v);
         }
+        return r;
     }
-    // Which of this thread's tokens of the tile are resets, a bit each.
+    // Which of this thread's tokens of the tile are resets, a bit each; all lanes of the warp call it.
     __device__ unsigned marks(const ScanArgs &p, int t0) const {
-        unsigned m = 0;
-        const int t = t0 + group * Sh::S;
-        const unsigned char *at = p.reset + (long long)b * p.L + t;
-#pragma unroll
-        for (int s = 0; s < Sh::S; ++s)
-            if (t + s < len && at[s]) m |= 1u << s;
-        return m;
+        constexpr int MINE = Sh::TILE / (THREADS / 32);
+        const int l = threadIdx.x & 31, t = t0 + threadIdx.x / 32 * MINE + l;
+        const unsigned m = __ballot_sync(0xffffffffu, l < MINE && t < len && p.reset[(long long)b * p.L + t]);
+        return Sh::LANES == 32 ? m : l < 16 ? m & ((1u << S) - 1) : m >> S;
     }
-    __device__ void rates(const ScanArgs &p, float (&rate)[Sh::V]) const {
+    __device__ M rates(const ScanArgs &p) const {
+        M r = M::all(0.0f);
 #pragma unroll
-        for (int v = 0; v < Sh::V; ++v) rate[v] = c + v < p.C ? p.rate[c + v] : 0.0f;
+        for (int v = 0; v < V; ++v)
+            if (c + v < p.C) r[v] = p.rate[c + v];
+        return r;
+    }
+    __device__ void put(float *at, const M &r) const { Vec<float, V>::store(at + group * W + lane * V, r.v); }
+    __device__ M get(const float *at) const {
+        M r;
+        Vec<float, V>::load(at + group * W + lane * V, r.v);
+        return r;
     }
 };
 
-template <int V> __device__ __forceinline__ void put_smem(float *p, const float (&r)[V]) { Vec<float, V>::store(p, r); }
-
 template <typename Sh, bool GATED, bool MARKS>
-__global__ void __launch_bounds__(THREADS, 2) gated_scan_fwd_kernel(const ScanArgs p) {
+__global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanArgs p) {
     using T = typename Sh::T;
+    using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
     extern __shared__ __align__(128) unsigned char smem[];
     Block<Sh> k(p, smem);
@@ -204,8 +211,7 @@ __global__ void __launch_bounds__(THREADS, 2) gated_scan_fwd_kernel(const ScanAr
     if (Sh::ASYNC) k.fetch(p, 0, t0, from, ld);
     if (Sh::ASYNC) cp_async_commit();
     if (K > 1) cluster_arrive();
-    float rate[V];
-    k.rates(p, rate);
+    const M rate = M::all(-1.0f) * k.rates(p);
     if (MARKS) marks = k.marks(p, t0);
     // the thread that folds channel c0 + threadIdx.x over the tile's groups
     const bool folds = threadIdx.x < W && k.c0 + (int)threadIdx.x < p.C;
@@ -216,53 +222,48 @@ __global__ void __launch_bounds__(THREADS, 2) gated_scan_fwd_kernel(const ScanAr
     for (int round = 0; round < p.rounds; ++round, t0 += K * Sh::TILE) {
         const int now = round & 1;
         unsigned ahead = 0;
-        if (Sh::ASYNC) {
-            cp_async_wait();
-            __syncthreads();
-            if (round + 1 < p.rounds) k.fetch(p, 1 - now, t0 + K * Sh::TILE, from, ld);
-            cp_async_commit();
+        if (Sh::ASYNC) {                     // a warp reads the rows that it copied, no other
+            cp_async_wait<0>();
+            __syncwarp();
         }
         if (MARKS && round + 1 < p.rounds) ahead = k.marks(p, t0 + K * Sh::TILE);
         const int mine = t0 + k.group * S;   // this thread's first token
-        float a[S][V], e[S][V], A[V], E[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = 1.0f, E[v] = 0.0f;
+        const bool ragged = t0 + Sh::TILE > k.len;
+        M a[S], e[S], A = M::all(1.0f), E = M::all(0.0f);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float x[V], ga[V], gx[V];
-            k.load(p, now, t0, s, 0, from, ld, x);
-            k.load(p, now, t0, s, 1, from, ld, ga);
-            if (GATED) k.load(p, now, t0, s, 2, from, ld, gx);
-            const bool fresh = MARKS && (marks >> s & 1);
+            const M x = k.load(p, 0, t0, s, 0, from, ld);
+            M n2;
+            decay(rate * sigmoid(k.load(p, 0, t0, s, 1, from, ld)), a[s], n2);
+            e[s] = GATED ? sigmoid(k.load(p, 0, t0, s, 2, from, ld)) * x : x;
+            if (p.normalize) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float n2, n, inv;
-                decay(-rate[v] * sigmoid(ga[v]), a[s][v], n2);
-                root(n2, n, inv);
-                if (!p.normalize) n = 1.0f;
-                if (fresh) a[s][v] = 0.0f, n = 1.0f;
-                e[s][v] = n * (GATED ? sigmoid(gx[v]) * x[v] : x[v]);
+                for (int v = 0; v < V; ++v) n2[v] = sqrt_(n2[v]);
+                if (MARKS && (marks >> s & 1)) n2 = M::all(1.0f);
+                e[s] = n2 * e[s];
             }
+            if (MARKS && (marks >> s & 1)) a[s] = M::all(0.0f);
+            if (ragged && mine + s >= k.len) a[s] = M::all(1.0f), e[s] = M::all(0.0f);   // leaves the state as it is
         }
-        if (t0 + Sh::TILE > k.len) {         // tokens past the end leave the state as it is
+        if (Sh::ASYNC) {                     // the next tile is on its way while the pairs meet
+            __syncwarp();
+            if (round + 1 < p.rounds) k.fetch(p, 0, t0 + K * Sh::TILE, from, ld);
+            cp_async_commit();
+        }
+        if (MARKS && marks) {
 #pragma unroll
             for (int s = 0; s < S; ++s)
-                if (mine + s >= k.len) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) a[s][v] = 1.0f, e[s][v] = 0.0f;
+                for (int v = 0; v < V; ++v) {
+                    A[v] = join(A[v], a[s][v]);
+                    E[v] = apply(a[s][v], E[v], e[s][v]);
                 }
-        }
+        } else {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const bool fresh = MARKS && (marks >> s & 1);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                A[v] = MARKS ? join(A[v], a[s][v]) : A[v] * a[s][v];
-                E[v] = fresh ? e[s][v] : fmaf(a[s][v], E[v], e[s][v]);
-            }
+            for (int s = 0; s < S; ++s) A = A * a[s], E = fma(a[s], E, e[s]);
         }
-        put_smem(k.A + k.group * W + k.lane * V, A);
-        put_smem(k.E + k.group * W + k.lane * V, E);
+        k.put(k.A, A);
+        k.put(k.E, E);
         __syncthreads();
         float before = carry;
         if (K > 1) {
@@ -297,23 +298,15 @@ __global__ void __launch_bounds__(THREADS, 2) gated_scan_fwd_kernel(const ScanAr
             if (K == 1) carry = before;
         }
         __syncthreads();
-        float h[V];
-        Vec<float, V>::load(k.E + k.group * W + k.lane * V, h);
+        M h = k.get(k.E);
         T *out = static_cast<T *>(p.h) + ((long long)k.b * p.L + mine) * p.ldh + k.c;
-        const bool ragged = t0 + Sh::TILE > k.len;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const bool fresh = MARKS && (marks >> s & 1);
-#pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = fresh ? e[s][v] : fmaf(a[s][v], h[v], e[s][v]);
-            if (mine + s < p.L && k.c < p.C) {
-                if (ragged && mine + s >= k.len) {
-                    const float zero[V] = {};
-                    Vec<T, V>::store(out + s * p.ldh, zero);
-                } else {
-                    Vec<T, V>::store(out + s * p.ldh, h);
-                }
-            }
+        for (int s = 0; s < S; ++s, out += p.ldh) {
+            if (MARKS && (marks >> s & 1)) h = e[s];
+            else h = fma(a[s], h, e[s]);
+            M o = h;
+            if (ragged && mine + s >= k.len) o = M::all(0.0f);
+            if (mine + s < p.L && k.c < p.C) Vec<T, V>::store(out, o.v);
         }
         marks = ahead;
     }
@@ -321,8 +314,9 @@ __global__ void __launch_bounds__(THREADS, 2) gated_scan_fwd_kernel(const ScanAr
 }
 
 template <typename Sh, bool GATED, bool MARKS>
-__global__ void __launch_bounds__(THREADS, 2) gated_scan_bwd_kernel(const ScanArgs p) {
+__global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanArgs p) {
     using T = typename Sh::T;
+    using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
     extern __shared__ __align__(128) unsigned char smem[];
     Block<Sh> k(p, smem);
@@ -336,10 +330,8 @@ __global__ void __launch_bounds__(THREADS, 2) gated_scan_bwd_kernel(const ScanAr
     if (Sh::ASYNC) k.fetch(p, 0, t0, from, ld);
     if (Sh::ASYNC) cp_async_commit();
     if (K > 1) cluster_arrive();
-    float rate[V], drate[V];
-    k.rates(p, rate);
-#pragma unroll
-    for (int v = 0; v < V; ++v) drate[v] = 0.0f;
+    const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
+    M drate = none;
     if (MARKS) marks = k.marks(p, t0);
     // threads 0 .. W - 1 fold the adjoints of a channel, the next W its states
     const int col = threadIdx.x % W, ch = k.c0 + col;
@@ -351,8 +343,8 @@ __global__ void __launch_bounds__(THREADS, 2) gated_scan_bwd_kernel(const ScanAr
         const int now = round & 1;
         unsigned ahead = 0;
         if (Sh::ASYNC) {
-            cp_async_wait();
-            __syncthreads();
+            cp_async_wait<0>();
+            __syncwarp();
             if (round + 1 < p.rounds) k.fetch(p, 1 - now, t0 - K * Sh::TILE, from, ld);
             cp_async_commit();
         }
@@ -361,45 +353,45 @@ __global__ void __launch_bounds__(THREADS, 2) gated_scan_bwd_kernel(const ScanAr
         if (forward && ch < p.C && t0 < p.L) state = p.states[((long long)k.b * N + t0 / KEEP) * p.C + ch];
         const int mine = t0 + k.group * S;
         const bool ragged = t0 + Sh::TILE > k.len;
-        // per value: a, r, the sigmoid s, n s, and a h - a^2/n u once h is there
-        float a[S][V], r[S][V], g[S][V], ns[S][V], D[S][V], A[V], E[V], Z[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = 1.0f, E[v] = 0.0f, Z[v] = 0.0f;
+        // per value: a, r, the sigmoid s, n s, and a^2/n u, then a h - a^2/n u
+        M a[S], r[S], g[S], ns[S], D[S], A = one, E = none, Z = none;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float x[V], ga[V], gx[V];
-            k.load(p, now, t0, s, 0, from, ld, x);
-            k.load(p, now, t0, s, 1, from, ld, ga);
-            if (GATED) k.load(p, now, t0, s, 3, from, ld, gx);
-            const bool fresh = MARKS && (marks >> s & 1), none = ragged && mine + s >= k.len;
+            const M x = k.load(p, now, t0, s, 0, from, ld);
+            r[s] = sigmoid(k.load(p, now, t0, s, 1, from, ld));
+            if (GATED) g[s] = sigmoid(k.load(p, now, t0, s, 3, from, ld));
+            M n2, n = one, inv = none;
+            decay(rate * r[s], a[s], n2);
+            if (p.normalize) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float n2, n, inv;
-                r[s][v] = sigmoid(ga[v]);
-                decay(-rate[v] * r[s][v], a[s][v], n2);
-                root(n2, n, inv);
-                if (!p.normalize) n = 1.0f, inv = 0.0f;
-                if (fresh) a[s][v] = 0.0f, n = 1.0f;
-                if (none) a[s][v] = 1.0f, n = 0.0f, inv = 0.0f;
-                g[s][v] = GATED ? sigmoid(gx[v]) : 1.0f;
-                ns[s][v] = n * g[s][v];
-                D[s][v] = a[s][v] * a[s][v] * inv * (g[s][v] * x[v]);
-                A[v] = MARKS ? join(A[v], a[s][v]) : A[v] * a[s][v];
-                const float e = ns[s][v] * x[v];
-                E[v] = fresh ? e : fmaf(a[s][v], E[v], e);
+                for (int v = 0; v < V; ++v) {
+                    const float q = rsqrt_(fmaxf(n2[v], 1e-37f));
+                    n[v] = q;
+                    inv[v] = n2[v] > 0.0f ? q : 0.0f;    // no slope at 0
+                }
+                n = n * n2;
+            }
+            if (MARKS && (marks >> s & 1)) a[s] = none, n = one;
+            if (ragged && mine + s >= k.len) a[s] = one, n = none, inv = none;
+            ns[s] = GATED ? n * g[s] : n;
+            const M u = GATED ? g[s] * x : x, e = ns[s] * x;
+            D[s] = a[s] * a[s] * (inv * u);
+            if (MARKS && marks) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) A[v] = join(A[v], a[s][v]), E[v] = apply(a[s][v], E[v], e[v]);
+            } else {
+                A = A * a[s];
+                E = fma(a[s], E, e);
             }
         }
 #pragma unroll
         for (int s = S - 1; s >= 0; --s) {
-            float dh[V];
-            k.load(p, now, t0, s, 2, from, ld, dh);
-            const bool fresh = MARKS && (marks >> s & 1);
-#pragma unroll
-            for (int v = 0; v < V; ++v) Z[v] = fresh ? 0.0f : a[s][v] * (dh[v] + Z[v]);
+            Z = a[s] * (k.load(p, now, t0, s, 2, from, ld) + Z);
+            if (MARKS && (marks >> s & 1)) Z = none;
         }
-        put_smem(k.A + k.group * W + k.lane * V, A);
-        put_smem(k.E + k.group * W + k.lane * V, E);
-        put_smem(k.Z + k.group * W + k.lane * V, Z);
+        k.put(k.A, A);
+        k.put(k.E, E);
+        k.put(k.Z, Z);
         __syncthreads();
         float after = carry;
         if (K > 1) {
@@ -442,44 +434,33 @@ __global__ void __launch_bounds__(THREADS, 2) gated_scan_bwd_kernel(const ScanAr
             if (K == 1) carry = after;
         }
         __syncthreads();
-        float h[V], z[V];
-        Vec<float, V>::load(k.E + k.group * W + k.lane * V, h);
-        Vec<float, V>::load(k.Z + k.group * W + k.lane * V, z);
+        M h = k.get(k.E), z = k.get(k.Z);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float x[V];
-            k.load(p, now, t0, s, 0, from, ld, x);
-            const bool fresh = MARKS && (marks >> s & 1), none = ragged && mine + s >= k.len;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float e = ns[s][v] * x[v];
-                D[s][v] = fresh || none ? 0.0f : fmaf(a[s][v], h[v], -D[s][v]);
-                h[v] = fresh ? e : fmaf(a[s][v], h[v], e);
-            }
+            const M e = ns[s] * k.load(p, now, t0, s, 0, from, ld), kept = a[s] * h;
+            D[s] = fma(D[s], M::all(-1.0f), kept);
+            h = kept + e;
+            if (MARKS && (marks >> s & 1)) D[s] = none, h = e;
+            if (ragged && mine + s >= k.len) D[s] = none;
         }
-        const long long row = (long long)k.b * p.L + mine;
+        const long long row = (long long)k.b * p.L + mine + S - 1;
         T *dx = static_cast<T *>(p.dx) + row * p.lddx + k.c, *dga = static_cast<T *>(p.dga) + row * p.lddga + k.c;
         T *dgx = GATED ? static_cast<T *>(p.dgx) + row * p.lddgx + k.c : nullptr;
 #pragma unroll
-        for (int s = S - 1; s >= 0; --s) {
-            float x[V], dh[V], o1[V], o2[V], o3[V];
-            k.load(p, now, t0, s, 2, from, ld, dh);
-            if (GATED) k.load(p, now, t0, s, 0, from, ld, x);
-            const bool fresh = MARKS && (marks >> s & 1);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float G = dh[v] + z[v];
-                const float t = G * D[s][v] * r[s][v];       // dla r
-                drate[v] -= t;
-                o1[v] = G * ns[s][v];
-                o2[v] = rate[v] * t * (r[s][v] - 1.0f);
-                if (GATED) o3[v] = o1[v] * x[v] * (1.0f - g[s][v]);
-                z[v] = fresh ? 0.0f : a[s][v] * G;
-            }
+        for (int s = S - 1; s >= 0; --s, dx -= p.lddx, dga -= p.lddga, dgx -= p.lddgx) {
+            const M G = k.load(p, now, t0, s, 2, from, ld) + z;
+            const M t = G * D[s] * r[s];     // dla r
+            const M o1 = G * ns[s], o2 = rate * t * fma(r[s], M::all(-1.0f), one);
+            drate = fma(t, M::all(-1.0f), drate);
+            z = a[s] * G;
+            if (MARKS && (marks >> s & 1)) z = none;
             if (mine + s < p.L && k.c < p.C) {
-                Vec<T, V>::store(dx + s * p.lddx, o1);
-                Vec<T, V>::store(dga + s * p.lddga, o2);
-                if (GATED) Vec<T, V>::store(dgx + s * p.lddgx, o3);
+                Vec<T, V>::store(dx, o1.v);
+                Vec<T, V>::store(dga, o2.v);
+                if (GATED) {
+                    const M o3 = o1 * k.load(p, now, t0, s, 0, from, ld) * fma(g[s], M::all(-1.0f), one);
+                    Vec<T, V>::store(dgx, o3.v);
+                }
             }
         }
         marks = ahead;
@@ -487,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 2) gated_scan_bwd_kernel(const ScanAr
     if (k.rank == 0 && folds && ch < p.C && p.dh0) p.dh0[(long long)k.b * p.C + ch] = carry;
     // the rate's gradient over this block's tokens
     __syncthreads();
-    put_smem(k.A + k.group * W + k.lane * V, drate);
+    k.put(k.A, drate);
     __syncthreads();
     if (folds && ch < p.C) {
         float sum = 0.0f;
@@ -524,32 +505,29 @@ gated_scan_step_kernel(const T *x, const T *ga, const T *gx, const float *rate, 
     griddep_launch_dependents();
     if (i >= total) return;
     const int c = (int)(i % C);
-    float xv[V], av[V], gv[V], rv[V], s[V];
-    Vec<T, V>::load(x + i, xv);
-    Vec<T, V>::load(ga + i, av);
-    if (gx) Vec<T, V>::load(gx + i, gv);
-    Vec<float, V>::load(rate + c, rv);
-    Vec<float, V>::load(state + i, s);
+    Many<V> xv, av, gv, rv, s, a, n;
+    Vec<T, V>::load(x + i, xv.v);
+    Vec<T, V>::load(ga + i, av.v);
+    if (gx) Vec<T, V>::load(gx + i, gv.v);
+    Vec<float, V>::load(rate + c, rv.v);
+    Vec<float, V>::load(state + i, s.v);
+    decay(Many<V>::all(-1.0f) * rv * sigmoid(av), a, n);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float a, n2, n, inv;
-        decay(-rv[v] * sigmoid(av[v]), a, n2);
-        root(n2, n, inv);
-        if (!normalize) n = 1.0f;
-        s[v] = fmaf(a, s[v], n * (gx ? sigmoid(gv[v]) * xv[v] : xv[v]));
-    }
-    Vec<float, V>::store(state + i, s);
-    Vec<T, V>::store(h + i, s);
+    for (int v = 0; v < V; ++v) n[v] = normalize ? sqrt_(n[v]) : 1.0f;
+    s = fma(a, s, n * (gx ? sigmoid(gv) * xv : xv));
+    Vec<float, V>::store(state + i, s.v);
+    Vec<T, V>::store(h + i, s.v);
 }
 
 // ------------------------------------------------------------------ launches
-// Tiles at once: the cluster that ends first when `slots` blocks run side by
-// side and every block of a wave works through its share of the tiles.
-int choose_cluster(long long chains, int tiles, int slots) {
+// Tiles at once: the cluster that ends first when four blocks an SM run side
+// by side, a wave costs two tiles to begin, and each block of it works through
+// its share of the tiles.
+int choose_cluster(long long chains, int tiles) {
     int best = 1;
     long long cost = -1;
-    for (int K = 1; K <= MAX_CLUSTER && K <= (tiles > 1 ? tiles : 1); K *= 2) {
-        const long long t = (chains * K + slots - 1) / slots * ((tiles + K - 1) / K);
+    for (int K = 1; K <= MAX_CLUSTER && K <= tiles; ++K) {
+        const long long t = (chains * K + 4 * SMS - 1) / (4 * SMS) * ((tiles + K - 1) / K + 2);
         if (cost < 0 || t < cost) best = K, cost = t;
     }
     return best;
@@ -558,18 +536,25 @@ int choose_cluster(long long chains, int tiles, int slots) {
 template <typename Sh> cudaError_t place(ScanArgs &p, long long &blocks) {
     const int tiles = (p.L + Sh::TILE - 1) / Sh::TILE;
     const long long chains = (long long)p.B * ((p.C + Sh::WIDE - 1) / Sh::WIDE);
-    p.cluster = choose_cluster(chains, tiles, 2 * SMS);
+    p.cluster = choose_cluster(chains, tiles);
     p.rounds = (tiles + p.cluster - 1) / p.cluster;
     blocks = chains * p.cluster;
     return blocks > 0x7fffffffll ? cudaErrorInvalidValue : cudaSuccess;
+}
+
+template <typename... Ks> cudaError_t launch_scan(void (*k)(Ks...), const ScanArgs &p, long long blocks, size_t smem, cudaStream_t st) {
+    if (p.cluster > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_big(k, dim3((unsigned)blocks), THREADS, smem, p.cluster, st, p);
 }
 
 template <typename Sh> cudaError_t run_fwd(ScanArgs &p, cudaStream_t st) {
     long long blocks;
     const cudaError_t e = place<Sh>(p, blocks);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)blocks);
-#define S5_RUN(GATED, MARKS) launch_big(gated_scan_fwd_kernel<Sh, GATED, MARKS>, grid, THREADS, Sh::SMEM, p.cluster, st, p)
+#define S5_RUN(GATED, MARKS) launch_scan(gated_scan_fwd_kernel<Sh, GATED, MARKS>, p, blocks, Sh::SMEM, st)
     if (p.gx) return p.reset ? S5_RUN(true, true) : S5_RUN(true, false);
     return p.reset ? S5_RUN(false, true) : S5_RUN(false, false);
 #undef S5_RUN
@@ -579,10 +564,9 @@ template <typename Sh> cudaError_t run_bwd(ScanArgs &p, float *drate, cudaStream
     long long blocks;
     cudaError_t e = place<Sh>(p, blocks);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)blocks);
     const int parts = p.B * p.cluster;
     if (parts == 1) p.drate = drate;
-#define S5_RUN(GATED, MARKS) launch_big(gated_scan_bwd_kernel<Sh, GATED, MARKS>, grid, THREADS, Sh::SMEM, p.cluster, st, p)
+#define S5_RUN(GATED, MARKS) launch_scan(gated_scan_bwd_kernel<Sh, GATED, MARKS>, p, blocks, Sh::SMEM, st)
     if (p.gx) e = p.reset ? S5_RUN(true, true) : S5_RUN(true, false);
     else e = p.reset ? S5_RUN(false, true) : S5_RUN(false, false);
 #undef S5_RUN
@@ -661,11 +645,11 @@ extern "C" s5_status s5_gated_scan_forward(const void *x, long long ldx, const v
     if (dtype == S5_BF16)
         e = w == 8   ? run_fwd<Shape<__nv_bfloat16, 4, 16, 8, 3, true>>(p, st)
             : w == 2 ? run_fwd<Shape<__nv_bfloat16, 2, 16, 8, 3, false>>(p, st)
-                     : run_fwd<Shape<__nv_bfloat16, 1, 32, 8, 3, false>>(p, st);
+                     : run_fwd<Shape<__nv_bfloat16, 1, 32, 16, 3, false>>(p, st);
     else
         e = w == 4   ? run_fwd<Shape<float, 2, 16, 8, 3, true>>(p, st)
             : w == 2 ? run_fwd<Shape<float, 2, 16, 8, 3, false>>(p, st)
-                     : run_fwd<Shape<float, 1, 32, 8, 3, false>>(p, st);
+                     : run_fwd<Shape<float, 1, 32, 16, 3, false>>(p, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
 

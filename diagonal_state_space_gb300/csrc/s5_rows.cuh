@@ -66,8 +66,90 @@ __device__ __forceinline__ float rsqrt_(float x) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float sqrt_(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 constexpr float LOG2E = 1.4426950408889634f;
 __device__ __forceinline__ float sigmoid(float g) { return rcp(1.0f + ex2(-LOG2E * g)); }
+
+// V floats of a lane whose sums and products go two to an instruction: these
+// kernels are as short of issue slots as of bandwidth.
+template <int V> struct Many {
+    float v[V];
+    __device__ __forceinline__ float &operator[](int i) { return v[i]; }
+    __device__ __forceinline__ float operator[](int i) const { return v[i]; }
+    __device__ static __forceinline__ Many all(float x) {
+        Many r;
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.v[i] = x;
+        return r;
+    }
+};
+#define S5_TWO(op, ...)                                                                                                     \
+    asm(op : "=f"(r.v[i]), "=f"(r.v[i + 1]) : __VA_ARGS__)
+template <int V> __device__ __forceinline__ Many<V> fma(const Many<V> &a, const Many<V> &b, const Many<V> &c) {
+    Many<V> r;
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            S5_TWO("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+                   "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}",
+                   "f"(a.v[i]), "f"(a.v[i + 1]), "f"(b.v[i]), "f"(b.v[i + 1]), "f"(c.v[i]), "f"(c.v[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.v[i] = fmaf(a.v[i], b.v[i], c.v[i]);
+    }
+    return r;
+}
+template <int V> __device__ __forceinline__ Many<V> operator*(const Many<V> &a, const Many<V> &b) {
+    Many<V> r;
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            S5_TWO("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\t"
+                   "mov.b64 {%0, %1}, a;\n\t}",
+                   "f"(a.v[i]), "f"(a.v[i + 1]), "f"(b.v[i]), "f"(b.v[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.v[i] = a.v[i] * b.v[i];
+    }
+    return r;
+}
+template <int V> __device__ __forceinline__ Many<V> operator+(const Many<V> &a, const Many<V> &b) {
+    Many<V> r;
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            S5_TWO("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\t"
+                   "mov.b64 {%0, %1}, a;\n\t}",
+                   "f"(a.v[i]), "f"(a.v[i + 1]), "f"(b.v[i]), "f"(b.v[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.v[i] = a.v[i] + b.v[i];
+    }
+    return r;
+}
+#undef S5_TWO
+template <int V> __device__ __forceinline__ Many<V> sigmoid(const Many<V> &g) {
+    Many<V> e = g * Many<V>::all(-LOG2E);
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = ex2(e[i]);
+    e = e + Many<V>::all(1.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = rcp(e[i]);
+    return e;
+}
+
+__device__ __forceinline__ void cp_async16(unsigned dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16(unsigned dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 inline bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 inline bool type_ok(int dtype) { return dtype == S5_F32 || dtype == S5_BF16; }

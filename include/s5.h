@@ -530,7 +530,7 @@ s5_status s5_gated_scan_forward(const void *x, long long ldx, const void *gate_a
 
 /*
  * Gradients of sum(dh * h) + sum(dh_last * h_last) (dh_last NULL: zero) with the
- * forward's inputs and its `saved` buffer (the state every 64 tokens).  With
+ * forward's inputs and its `saved` buffer (the state every 32 tokens).  With
  * u = sigmoid(gate_x) x, s = sigmoid(gate_x):
  *   G_t = dh_t + a_{t+1} G_{t+1},  dla = G (a h_{t-1} - a^2 / n u)   (0 at a reset;
  *     the second part 0 where rate r = 0, whose root has no slope, or not normalize)
