@@ -71,6 +71,7 @@ SIGNATURES = {
     "s5_gated_scan_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _vp, _vp, _vp] + [_i] * 4
                                + [_vp, _ll, _vp, _vp, _sz, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp,
                                   _sz, _vp]),
+    "s5_gated_scan_fault": (_i, []),
     "s5_gated_scan_step": (_i, [_vp, _vp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp]),
     "s5_short_conv_forward": (_i, [_vp, _ll, _i, _vp, _vp, _i, _vp, _vp, _vp] + [_i] * 4 + [_vp, _ll, _vp, _vp]),
     "s5_short_conv_workspace_size": (_sz, [_i] * 2),

@@ -667,6 +667,12 @@ def s5_gated_scan_backward(x, gate_a, gate_x, rate, dh, saved, h0=None, dh_last=
         return out
 
 
+def s5_gated_scan_fault(device=None) -> bool:
+    """Whether a wait inside s5_gated_scan_forward or s5_gated_scan_backward has run out on the device (the current one)
+    since this was last asked: what those calls gave is then not valid.  Waits for the device."""
+    return _fault("s5_gated_scan_fault", device)
+
+
 def s5_gated_scan_step(x, gate_a, gate_x, rate, state, normalize=True, h=None, stream=None):
     """One token per sequence: x, gate_a, gate_x (or None) [B,C], rate [C] float32; state [B,C] float32 is updated in
     place.  Returns h [B,C] of x's type."""
@@ -843,7 +849,7 @@ __all__ = ["s5_discretize", "s5_discretize_ex", "s5_forward", "s5_forward_varyin
            "s5_delta_forward", "s5_delta_backward", "s5_delta_step", "s5_delta_saved_size",
            "s5_delta_workspace_size", "s5_delta_fault", "new_delta_saved", "s5_rotary", "s5_qk_norm_rotary",
            "s5_qk_norm_rotary_backward", "s5_rotary_fault", "s5_gated_scan_forward", "s5_gated_scan_backward",
-           "s5_gated_scan_step", "s5_gated_scan_saved_size", "s5_gated_scan_workspace_size", "new_gated_scan_saved",
+           "s5_gated_scan_step", "s5_gated_scan_fault", "s5_gated_scan_saved_size", "s5_gated_scan_workspace_size", "new_gated_scan_saved",
            "s5_short_conv_forward", "s5_short_conv_backward", "s5_short_conv_step", "s5_short_conv_workspace_size",
            "s5_add_layernorm", "s5_add_layernorm_backward", "s5_add_layernorm_workspace_size", "new_layernorm_saved",
            "S5Error", "S5_F32", "S5_BF16"]

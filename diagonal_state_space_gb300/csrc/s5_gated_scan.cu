@@ -13,11 +13,11 @@
 // V channels of S consecutive tokens each, fold them to one pair per lane, and
 // the tile's 8 or 16 pairs of a channel are folded by one thread.  A cluster of
 // blocks takes consecutive tiles of the same channels at once: each sends its
-// tile's pair to all the others' shared memory, and after one cluster barrier
-// each folds the pairs before it.  So a sequence is read once and written once,
-// no block waits for one that may not run, nothing is kept in global memory
-// between tiles, and the order of every sum is fixed.  The next tile is on its
-// way into shared memory meanwhile.
+// tile's pair to all the others' shared memory, and folds the pairs before it
+// once all have come.  So a sequence is read once and written once, no block
+// waits for one that may not run, nothing is kept in global memory between
+// tiles, and the order of every sum is fixed.  The next tile is on its way into
+// shared memory meanwhile.
 //
 // The backward pass walks the tiles from the last to the first with the same
 // pairs (A, Z) for G, and works the states out again inside a tile from one that
@@ -70,31 +70,43 @@ __device__ __forceinline__ float apply(float A, float h, float E) { return A == 
 // a = exp(z) and 1 - a^2 for z <= 0.  Above -1/4 the series of exp(z) - 1 up to z^6 (the rest is below 2^-23 of it).
 template <int V> __device__ __forceinline__ void decay(const Many<V> &z, Many<V> &a, Many<V> &n2) {
     using M = Many<V>;
-    M q = fma(z, M::all(1.0f / 720), M::all(1.0f / 120));
-    q = fma(z, q, M::all(1.0f / 24));
-    q = fma(z, q, M::all(1.0f / 6));
-    q = fma(z, q, M::all(0.5f));
-    const M near = fma(z * z, q, z), grown = near + M::all(1.0f);
-    M far = z * M::all(LOG2E);
+    M q, m, t;
 #pragma unroll
-    for (int i = 0; i < V; ++i) far[i] = ex2(far[i]);
-    M m = far + M::all(-1.0f);
+    for (int i = 0; i < V; ++i)
+        q[i] = fmaf(z[i], fmaf(z[i], fmaf(z[i], fmaf(z[i], 1.0f / 720, 1.0f / 120), 1.0f / 24), 1.0f / 6), 0.5f);
+    const M near = fma(z * z, q, z);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+        const float far = ex2(LOG2E * z[i]);
         const bool close = z[i] > -0.25f;
-        m[i] = close ? near[i] : m[i];
-        a[i] = close ? grown[i] : far[i];
+        m[i] = close ? near[i] : far - 1.0f;
+        a[i] = close ? 1.0f + near[i] : far;
+        t[i] = -2.0f - m[i];
     }
-    n2 = m * fma(m, M::all(-1.0f), M::all(-2.0f));
+    n2 = m * t;
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// A pair into block `rank`'s copy of this block's shared variable.
-__device__ __forceinline__ void send(float2 *p, unsigned rank, float2 v) {
-    unsigned at;
+__device__ __forceinline__ void cluster_arrive() { __syncwarp(); asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { __syncwarp(); asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// A pair into block `rank`'s copy of this block's shared variable, counted by that block's barrier.
+__device__ __forceinline__ void send(float2 *p, uint64_t *bar, unsigned rank, float2 v) {
+    unsigned at, counted;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(counted) : "r"(smem_addr(bar)), "r"(rank));
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at), "f"(v.x),
+                 "f"(v.y), "r"(counted)
+                 : "memory");
+}
+__device__ int g_scan_fault = 0;     // a wait for the cluster's pairs ran out
+constexpr unsigned long long WAIT_NS = 2000000000ull;
+// The other blocks run beside this one, so the wait ends; were it not to, the results would be wrong and said to be.
+__device__ __noinline__ void wait_long(uint64_t *bar, unsigned parity) {
+    const unsigned long long t0 = global_ns();
+    while (!sm100::mbar_try_wait_sleep(bar, parity, 100000))
+        if (global_ns() - t0 > WAIT_NS) {
+            atomicExch(&g_scan_fault, 1);
+            return;
+        }
 }
 
 // How a block's threads share a tile: LANES threads side by side hold V
@@ -103,11 +115,11 @@ template <typename T_, int V_, int LANES_, int S_, int ARRAYS_, bool ASYNC_> str
     using T = T_;
     static constexpr int V = V_, LANES = LANES_, S = S_, ARRAYS = ARRAYS_;
     static constexpr bool ASYNC = ASYNC_;                     // tiles come by 16-byte copies
-    static constexpr int GROUPS = THREADS / LANES, WIDE = LANES * V, TILE = GROUPS * S;
+    static constexpr int GROUPS = THREADS / LANES, WARPS = THREADS / 32, WIDE = LANES * V, TILE = GROUPS * S;
     static constexpr int STAGE = ASYNC ? ARRAYS * TILE * WIDE * (int)sizeof(T) : 0;
     static constexpr int PAIRS = MAX_CLUSTER * WIDE;          // of a round
     static constexpr int STAGES = ARRAYS == 4 ? 2 : 1;        // backward a tile is read twice
-    static constexpr int SMEM = STAGES * STAGE + 2 * PAIRS * (int)sizeof(float2) + (ARRAYS == 4 ? 3 : 2) * GROUPS * WIDE * (int)sizeof(float);
+    static constexpr int SMEM = STAGES * STAGE + 2 * PAIRS * (int)sizeof(float2) + (ARRAYS == 4 ? 4 : 3) * WARPS * WIDE * (int)sizeof(float);
     static_assert(TILE == KEEP || TILE == 2 * KEEP, "kept states lie at a group's start");
     static_assert(LANES * 2 == 32 || LANES == 32, "a warp holds one or two groups");
 };
@@ -119,15 +131,18 @@ template <typename Sh> struct Block {
     static constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
     T *stage;           // [STAGES][ARRAYS][TILE][WIDE]
     float2 *pairs;      // [2][MAX_CLUSTER][WIDE]
-    float *A, *E, *Z;   // [GROUPS][WIDE] (Z: backward)
+    float *A, *E, *H, *Z;   // [WARPS][WIDE]: a warp's pairs, what enters it, and backward its adjoints' pairs
+    uint64_t *bar;      // [2], one for each half of the pairs
     int b, c0, rank, lane, group, c;
+    bool upper;         // the later of a warp's two groups
     int len;            // tokens of this sequence
-    __device__ Block(const ScanArgs &p, unsigned char *smem) {
+    __device__ Block(const ScanArgs &p, unsigned char *smem, uint64_t *bars) : bar(bars) {
         stage = reinterpret_cast<T *>(smem);
         pairs = reinterpret_cast<float2 *>(smem + Sh::STAGES * Sh::STAGE);
         A = reinterpret_cast<float *>(pairs + 2 * Sh::PAIRS);
-        E = A + Sh::GROUPS * W;
-        Z = E + Sh::GROUPS * W;
+        E = A + Sh::WARPS * W;
+        H = E + Sh::WARPS * W;
+        Z = H + Sh::WARPS * W;
         const int K = p.cluster, across = (p.C + W - 1) / W;
         rank = blockIdx.x % K;
         const int chain = blockIdx.x / K;
@@ -136,6 +151,7 @@ template <typename Sh> struct Block {
         lane = threadIdx.x % Sh::LANES;
         group = threadIdx.x / Sh::LANES;
         c = c0 + lane * V;
+        upper = Sh::LANES == 32 || (threadIdx.x & 16);
     }
     __device__ void read_length(const ScanArgs &p) { len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L; }
     // Copies of this warp's rows of the tile at t0 into a stage, zeros where there is nothing to read.
@@ -186,11 +202,66 @@ template <typename Sh> struct Block {
             if (c + v < p.C) r[v] = p.rate[c + v];
         return r;
     }
-    __device__ void put(float *at, const M &r) const { Vec<float, V>::store(at + group * W + lane * V, r.v); }
+    // A warp's row of A, E or Z.
+    __device__ void put(float *at, const M &r) const { Vec<float, V>::store(at + threadIdx.x / 32 * W + lane * V, r.v); }
     __device__ M get(const float *at) const {
         M r;
-        Vec<float, V>::load(at + group * W + lane * V, r.v);
+        Vec<float, V>::load(at + threadIdx.x / 32 * W + lane * V, r.v);
         return r;
+    }
+    // The values that the lane of the warp's other group holds for the same channels.
+    __device__ static M other(const M &x) {
+        M r;
+#pragma unroll
+        for (int v = 0; v < V; ++v) r[v] = __shfl_xor_sync(0xffffffffu, x[v], 16);
+        return r;
+    }
+    __device__ static M joined(const M &a, const M &b) {
+        M r;
+#pragma unroll
+        for (int v = 0; v < V; ++v) r[v] = join(a[v], b[v]);
+        return r;
+    }
+    __device__ static M applied(const M &a, const M &h, const M &e) {
+        M r;
+#pragma unroll
+        for (int v = 0; v < V; ++v) r[v] = apply(a[v], h[v], e[v]);
+        return r;
+    }
+    // The cluster's barriers; afterwards all blocks run, and their shared memory may be written.
+    __device__ void open_cluster(const ScanArgs &p) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < 2; ++i) sm100::mbar_init(bar + i, 1);
+            sm100::fence_mbar_init();
+            for (int i = 0; i < 2 && i < p.rounds; ++i) sm100::mbar_arrive_tx(bar + i, p.cluster * W * sizeof(float2));
+        }
+        cluster_arrive();
+    }
+    // All blocks' pairs of this round to all blocks.  carry, what enters the round, becomes what leaves it; returned is
+    // what enters this block's tile.  From the tile's rows of A and `e`, folded downwards backward.  Threads below W;
+    // the others only help to send.  A block sends its pairs of round r + 2 after it has read those of round r + 1, for
+    // which this one has sent its own, after reading round r: no half is overwritten before it is read.
+    template <bool DOWN> __device__ float exchange(const ScanArgs &p, int round, const float *e, float &carry) {
+        const int K = p.cluster, col = threadIdx.x % W, now = round & 1;
+        float2 all = make_float2(1.0f, 0.0f), *slots = pairs + now * MAX_CLUSTER * W + col;
+#pragma unroll
+        for (int i = 0; i < Sh::WARPS; ++i) {
+            const int j = DOWN ? Sh::WARPS - 1 - i : i;
+            const float Aj = A[j * W + col];
+            all = make_float2(join(Aj, all.x), apply(Aj, all.y, e[j * W + col]));
+        }
+        for (int j = threadIdx.x / W; j < K; j += THREADS / W) send(slots + rank * W, bar + now, j, all);
+        if (threadIdx.x >= W) return 0.0f;
+        if (!sm100::mbar_try_wait(bar + now, round >> 1 & 1)) wait_long(bar + now, round >> 1 & 1);
+        if (threadIdx.x == 0 && round + 2 < p.rounds) sm100::mbar_arrive_tx(bar + now, K * W * sizeof(float2));
+        float before = carry;
+        for (int i = 0; i < K; ++i) {
+            const int j = DOWN ? K - 1 - i : i;
+            const float2 q = slots[j * W];
+            if (j == rank) before = carry;
+            carry = apply(q.x, carry, q.y);
+        }
+        return before;
     }
 };
 
@@ -200,7 +271,8 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
     using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
     extern __shared__ __align__(128) unsigned char smem[];
-    Block<Sh> k(p, smem);
+    __shared__ uint64_t bars[2];
+    Block<Sh> k(p, smem, bars);
     const int K = p.cluster;
     griddep_wait();
     k.read_length(p);
@@ -210,17 +282,16 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
     unsigned marks = 0;
     if (Sh::ASYNC) k.fetch(p, 0, t0, from, ld);
     if (Sh::ASYNC) cp_async_commit();
-    if (K > 1) cluster_arrive();
-    const M rate = M::all(-1.0f) * k.rates(p);
+    if (K > 1) k.open_cluster(p);
+    const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
     if (MARKS) marks = k.marks(p, t0);
-    // the thread that folds channel c0 + threadIdx.x over the tile's groups
+    // the thread that folds channel c0 + threadIdx.x over the tile's warps
     const bool folds = threadIdx.x < W && k.c0 + (int)threadIdx.x < p.C;
     const int ch = k.c0 + threadIdx.x;
     float carry = folds && p.h0 ? p.h0[(long long)k.b * p.C + ch] : 0.0f;   // the state before this round's first tile
-    if (K > 1) cluster_wait();   // all blocks run: their shared memory may be written
+    if (K > 1) cluster_wait();
 
     for (int round = 0; round < p.rounds; ++round, t0 += K * Sh::TILE) {
-        const int now = round & 1;
         unsigned ahead = 0;
         if (Sh::ASYNC) {                     // a warp reads the rows that it copied, no other
             cp_async_wait<0>();
@@ -229,87 +300,84 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
         if (MARKS && round + 1 < p.rounds) ahead = k.marks(p, t0 + K * Sh::TILE);
         const int mine = t0 + k.group * S;   // this thread's first token
         const bool ragged = t0 + Sh::TILE > k.len;
-        M a[S], e[S], A = M::all(1.0f), E = M::all(0.0f);
+        const bool slow = ragged || (MARKS && marks);
+        M a[S], e[S], A = one, E = none;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const M x = k.load(p, 0, t0, s, 0, from, ld);
-            M n2;
-            decay(rate * sigmoid(k.load(p, 0, t0, s, 1, from, ld)), a[s], n2);
+            M n;
+            decay(rate * sigmoid(k.load(p, 0, t0, s, 1, from, ld)), a[s], n);
             e[s] = GATED ? sigmoid(k.load(p, 0, t0, s, 2, from, ld)) * x : x;
             if (p.normalize) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) n2[v] = sqrt_(n2[v]);
-                if (MARKS && (marks >> s & 1)) n2 = M::all(1.0f);
-                e[s] = n2 * e[s];
+                for (int v = 0; v < V; ++v) n[v] = sqrt_(n[v]);
+                e[s] = n * e[s];
             }
-            if (MARKS && (marks >> s & 1)) a[s] = M::all(0.0f);
-            if (ragged && mine + s >= k.len) a[s] = M::all(1.0f), e[s] = M::all(0.0f);   // leaves the state as it is
+            A = A * a[s];
+            E = fma(a[s], E, e[s]);
+        }
+        if (slow) {
+            A = one, E = none;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                if (MARKS && (marks >> s & 1)) {
+                    a[s] = none, e[s] = k.load(p, 0, t0, s, 0, from, ld);
+                    if (GATED) e[s] = sigmoid(k.load(p, 0, t0, s, 2, from, ld)) * e[s];
+                }
+                if (mine + s >= k.len) a[s] = one, e[s] = none;      // leaves the state as it is
+                E = k.applied(a[s], E, e[s]);
+                A = k.joined(A, a[s]);
+            }
         }
         if (Sh::ASYNC) {                     // the next tile is on its way while the pairs meet
             __syncwarp();
             if (round + 1 < p.rounds) k.fetch(p, 0, t0 + K * Sh::TILE, from, ld);
             cp_async_commit();
         }
-        if (MARKS && marks) {
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    A[v] = join(A[v], a[s][v]);
-                    E[v] = apply(a[s][v], E[v], e[s][v]);
-                }
-        } else {
-#pragma unroll
-            for (int s = 0; s < S; ++s) A = A * a[s], E = fma(a[s], E, e[s]);
+        M pA = one, pE = none;               // of the warp's earlier group, for the later one
+        if (Sh::LANES == 16) {
+            pA = k.other(A), pE = k.other(E);
+            E = k.applied(A, pE, E);
+            A = k.joined(A, pA);
         }
-        k.put(k.A, A);
-        k.put(k.E, E);
+        if (k.upper) {
+            k.put(k.A, A);
+            k.put(k.E, E);
+        }
         __syncthreads();
-        float before = carry;
-        if (K > 1) {
-            float2 *slot = k.pairs + (now * MAX_CLUSTER + k.rank) * W + threadIdx.x;
-            if (threadIdx.x < W) {
-                float2 all = make_float2(1.0f, 0.0f);
+        float before = K > 1 ? k.template exchange<false>(p, round, k.E, carry) : carry;
+        if (K > 1 && round + 1 == p.rounds) cluster_arrive();
+        if (threadIdx.x < W) {               // the state before each warp's tokens
 #pragma unroll
-                for (int g = 0; g < Sh::GROUPS; ++g) {
-                    const float Ag = k.A[g * W + threadIdx.x];
-                    all = make_float2(join(Ag, all.x), apply(Ag, all.y, k.E[g * W + threadIdx.x]));
-                }
-                for (int j = 0; j < K; ++j) send(slot, j, all);
-            }
-            cluster_arrive();
-            cluster_wait();
-            if (threadIdx.x < W)
-                for (int j = 0; j < K; ++j) {
-                    const float2 q = k.pairs[(now * MAX_CLUSTER + j) * W + threadIdx.x];
-                    if (j == k.rank) before = carry;
-                    carry = apply(q.x, carry, q.y);
-                }
-        }
-        if (threadIdx.x < W) {               // the state before each group, in E's place
-#pragma unroll
-            for (int g = 0; g < Sh::GROUPS; ++g) {
-                const float Ag = k.A[g * W + threadIdx.x], Eg = k.E[g * W + threadIdx.x];
-                k.E[g * W + threadIdx.x] = before;
-                if (g * S % KEEP == 0 && p.states && folds && t0 + g * S < p.L)
-                    p.states[((long long)k.b * ((p.L + KEEP - 1) / KEEP) + (t0 + g * S) / KEEP) * p.C + ch] = before;
-                before = apply(Ag, before, Eg);
+            for (int j = 0; j < Sh::WARPS; ++j) {
+                k.H[j * W + threadIdx.x] = before;
+                if (j * (Sh::TILE / Sh::WARPS) % KEEP == 0 && p.states && folds && t0 + j * (Sh::TILE / Sh::WARPS) < p.L)
+                    p.states[((long long)k.b * ((p.L + KEEP - 1) / KEEP) + (t0 + j * (Sh::TILE / Sh::WARPS)) / KEEP) * p.C + ch] = before;
+                before = apply(k.A[j * W + threadIdx.x], before, k.E[j * W + threadIdx.x]);
             }
             if (K == 1) carry = before;
         }
         __syncthreads();
-        M h = k.get(k.E);
+        M h = k.get(k.H);
+        if (Sh::LANES == 16 && k.upper) h = k.applied(pA, h, pE);
         T *out = static_cast<T *>(p.h) + ((long long)k.b * p.L + mine) * p.ldh + k.c;
+        if (!slow) {
 #pragma unroll
-        for (int s = 0; s < S; ++s, out += p.ldh) {
-            if (MARKS && (marks >> s & 1)) h = e[s];
-            else h = fma(a[s], h, e[s]);
-            M o = h;
-            if (ragged && mine + s >= k.len) o = M::all(0.0f);
-            if (mine + s < p.L && k.c < p.C) Vec<T, V>::store(out, o.v);
+            for (int s = 0; s < S; ++s, out += p.ldh) {
+                h = fma(a[s], h, e[s]);
+                if (k.c < p.C) Vec<T, V>::store(out, h.v);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; ++s, out += p.ldh) {
+                h = k.applied(a[s], h, e[s]);
+                const M o = mine + s < k.len ? h : none;
+                if (mine + s < p.L && k.c < p.C) Vec<T, V>::store(out, o.v);
+            }
         }
         marks = ahead;
     }
+    if (K > 1) cluster_wait();               // no block ends while another may still write to it
     if (k.rank == 0 && folds && p.h_last) p.h_last[(long long)k.b * p.C + ch] = carry;
 }
 
@@ -319,7 +387,8 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
     using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
     extern __shared__ __align__(128) unsigned char smem[];
-    Block<Sh> k(p, smem);
+    __shared__ uint64_t bars[2];
+    Block<Sh> k(p, smem, bars);
     const int K = p.cluster, N = (p.L + KEEP - 1) / KEEP;
     griddep_wait();
     k.read_length(p);
@@ -329,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
     unsigned marks = 0;
     if (Sh::ASYNC) k.fetch(p, 0, t0, from, ld);
     if (Sh::ASYNC) cp_async_commit();
-    if (K > 1) cluster_arrive();
+    if (K > 1) k.open_cluster(p);
     const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
     M drate = none;
     if (MARKS) marks = k.marks(p, t0);
@@ -353,6 +422,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
         if (forward && ch < p.C && t0 < p.L) state = p.states[((long long)k.b * N + t0 / KEEP) * p.C + ch];
         const int mine = t0 + k.group * S;
         const bool ragged = t0 + Sh::TILE > k.len;
+        const bool slow = ragged || (MARKS && marks);
         // per value: a, r, the sigmoid s, n s, and a^2/n u, then a h - a^2/n u
         M a[S], r[S], g[S], ns[S], D[S], A = one, E = none, Z = none;
 #pragma unroll
@@ -371,109 +441,123 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
                 }
                 n = n * n2;
             }
-            if (MARKS && (marks >> s & 1)) a[s] = none, n = one;
-            if (ragged && mine + s >= k.len) a[s] = one, n = none, inv = none;
             ns[s] = GATED ? n * g[s] : n;
-            const M u = GATED ? g[s] * x : x, e = ns[s] * x;
-            D[s] = a[s] * a[s] * (inv * u);
-            if (MARKS && marks) {
+            D[s] = a[s] * a[s] * (inv * (GATED ? g[s] * x : x));
+            A = A * a[s];
+            E = fma(a[s], E, ns[s] * x);
+        }
+        if (!slow) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) A[v] = join(A[v], a[s][v]), E[v] = apply(a[s][v], E[v], e[v]);
-            } else {
-                A = A * a[s];
-                E = fma(a[s], E, e);
+            for (int s = S - 1; s >= 0; --s) Z = a[s] * (k.load(p, now, t0, s, 2, from, ld) + Z);
+        } else {
+            A = one, E = none;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                if (MARKS && (marks >> s & 1)) a[s] = none, ns[s] = GATED ? g[s] : one;
+                if (mine + s >= k.len) a[s] = one, ns[s] = none;
+                E = k.applied(a[s], E, ns[s] * k.load(p, now, t0, s, 0, from, ld));
+                A = k.joined(A, a[s]);
+            }
+#pragma unroll
+            for (int s = S - 1; s >= 0; --s) {
+                Z = a[s] * (k.load(p, now, t0, s, 2, from, ld) + Z);
+                if (MARKS && (marks >> s & 1)) Z = none;
             }
         }
-#pragma unroll
-        for (int s = S - 1; s >= 0; --s) {
-            Z = a[s] * (k.load(p, now, t0, s, 2, from, ld) + Z);
-            if (MARKS && (marks >> s & 1)) Z = none;
+        M pA = one, pE = none, pZ = none;    // of the warp's other group
+        if (Sh::LANES == 16) {
+            pA = k.other(A), pE = k.other(E), pZ = k.other(Z);
+            E = k.applied(A, pE, E);
+            Z = k.applied(A, pZ, Z);
+            A = k.joined(A, pA);
         }
-        k.put(k.A, A);
-        k.put(k.E, E);
-        k.put(k.Z, Z);
+        if (k.upper) {
+            k.put(k.A, A);
+            k.put(k.E, E);
+        }
+        if (Sh::LANES == 32 || !k.upper) k.put(k.Z, Z);
         __syncthreads();
         float after = carry;
-        if (K > 1) {
-            if (folds) {
-                float2 all = make_float2(1.0f, 0.0f);
+        if (K > 1) after = k.template exchange<true>(p, round, k.Z, carry);
+        if (K > 1 && round + 1 == p.rounds) cluster_arrive();
+        if (forward) {                       // the state before each warp's tokens, in E's place (the others read no E)
 #pragma unroll
-                for (int j = Sh::GROUPS - 1; j >= 0; --j) {
-                    const float Aj = k.A[j * W + col];
-                    all = make_float2(join(Aj, all.x), apply(Aj, all.y, k.Z[j * W + col]));
-                }
-                float2 *slot = k.pairs + (now * MAX_CLUSTER + k.rank) * W + col;
-                for (int j = 0; j < K; ++j) send(slot, j, all);
-            }
-            cluster_arrive();
-        }
-        if (forward) {                       // the state before each group, in E's place
-#pragma unroll
-            for (int j = 0; j < Sh::GROUPS; ++j) {
+            for (int j = 0; j < Sh::WARPS; ++j) {
                 const float Ej = k.E[j * W + col];
                 k.E[j * W + col] = state;
                 state = apply(k.A[j * W + col], state, Ej);
             }
         }
-        if (K > 1) {
-            cluster_wait();
-            if (folds)
-                for (int j = K - 1; j >= 0; --j) {
-                    const float2 q = k.pairs[(now * MAX_CLUSTER + j) * W + col];
-                    if (j == k.rank) after = carry;
-                    carry = apply(q.x, carry, q.y);
-                }
-        }
-        if (folds) {                         // what arrives from after each group, in Z's place
+        if (folds) {                         // what arrives from after each warp's tokens
 #pragma unroll
-            for (int j = Sh::GROUPS - 1; j >= 0; --j) {
-                const float Zj = k.Z[j * W + col];
-                k.Z[j * W + col] = after;
-                after = apply(k.A[j * W + col], after, Zj);
+            for (int j = Sh::WARPS - 1; j >= 0; --j) {
+                k.H[j * W + col] = after;
+                after = apply(k.A[j * W + col], after, k.Z[j * W + col]);
             }
             if (K == 1) carry = after;
         }
         __syncthreads();
-        M h = k.get(k.E), z = k.get(k.Z);
+        M h = k.get(k.E), z = k.get(k.H);
+        if (Sh::LANES == 16) {
+            if (k.upper) h = k.applied(pA, h, pE);
+            else z = k.applied(pA, z, pZ);
+        }
+        if (!slow) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const M e = ns[s] * k.load(p, now, t0, s, 0, from, ld), kept = a[s] * h;
-            D[s] = fma(D[s], M::all(-1.0f), kept);
-            h = kept + e;
-            if (MARKS && (marks >> s & 1)) D[s] = none, h = e;
-            if (ragged && mine + s >= k.len) D[s] = none;
+            for (int s = 0; s < S; ++s) {
+                const M kept = a[s] * h;
+#pragma unroll
+                for (int v = 0; v < V; ++v) D[s][v] = kept[v] - D[s][v];
+                h = fma(ns[s], k.load(p, now, t0, s, 0, from, ld), kept);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const M e = ns[s] * k.load(p, now, t0, s, 0, from, ld);
+                const bool dead = (MARKS && (marks >> s & 1)) || mine + s >= k.len;
+#pragma unroll
+                for (int v = 0; v < V; ++v) D[s][v] = dead ? 0.0f : fmaf(a[s][v], h[v], -D[s][v]);
+                h = k.applied(a[s], h, e);
+            }
         }
         const long long row = (long long)k.b * p.L + mine + S - 1;
         T *dx = static_cast<T *>(p.dx) + row * p.lddx + k.c, *dga = static_cast<T *>(p.dga) + row * p.lddga + k.c;
         T *dgx = GATED ? static_cast<T *>(p.dgx) + row * p.lddgx + k.c : nullptr;
 #pragma unroll
-        for (int s = S - 1; s >= 0; --s, dx -= p.lddx, dga -= p.lddga, dgx -= p.lddgx) {
+        for (int s = S - 1; s >= 0; --s) {
             const M G = k.load(p, now, t0, s, 2, from, ld) + z;
-            const M t = G * D[s] * r[s];     // dla r
-            const M o1 = G * ns[s], o2 = rate * t * fma(r[s], M::all(-1.0f), one);
-            drate = fma(t, M::all(-1.0f), drate);
+            const M t = G * D[s] * r[s], o1 = G * ns[s], w = rate * t;   // t: dla r
+            M o2, o3;
+#pragma unroll
+            for (int v = 0; v < V; ++v) drate[v] -= t[v], o2[v] = fmaf(w[v], -r[s][v], w[v]);
             z = a[s] * G;
             if (MARKS && (marks >> s & 1)) z = none;
-            if (mine + s < p.L && k.c < p.C) {
+            if (GATED) {
+                const M q = o1 * k.load(p, now, t0, s, 0, from, ld);
+#pragma unroll
+                for (int v = 0; v < V; ++v) o3[v] = fmaf(q[v], -g[s][v], q[v]);
+            }
+            if (k.c < p.C && (!slow || mine + s < p.L)) {
                 Vec<T, V>::store(dx, o1.v);
                 Vec<T, V>::store(dga, o2.v);
-                if (GATED) {
-                    const M o3 = o1 * k.load(p, now, t0, s, 0, from, ld) * fma(g[s], M::all(-1.0f), one);
-                    Vec<T, V>::store(dgx, o3.v);
-                }
+                if (GATED) Vec<T, V>::store(dgx, o3.v);
             }
+            dx -= p.lddx, dga -= p.lddga;
+            if (GATED) dgx -= p.lddgx;
         }
         marks = ahead;
     }
+    if (K > 1) cluster_wait();               // no block ends while another may still write to it
     if (k.rank == 0 && folds && ch < p.C && p.dh0) p.dh0[(long long)k.b * p.C + ch] = carry;
     // the rate's gradient over this block's tokens
+    if (Sh::LANES == 16) drate = drate + k.other(drate);
     __syncthreads();
-    k.put(k.A, drate);
+    if (k.upper) k.put(k.A, drate);
     __syncthreads();
     if (folds && ch < p.C) {
         float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < Sh::GROUPS; ++j) sum += k.A[j * W + col];
+        for (int j = 0; j < Sh::WARPS; ++j) sum += k.A[j * W + col];
         p.drate[((long long)k.b * K + k.rank) * p.C + ch] = sum;
     }
 }
@@ -695,6 +779,13 @@ extern "C" s5_status s5_gated_scan_backward(const void *x, long long ldx, const 
             : w == 2 ? run_bwd<Shape<float, 2, 16, 4, 4, false>>(p, drate, st)
                      : run_bwd<Shape<float, 1, 32, 8, 4, false>>(p, drate, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
+}
+
+extern "C" int s5_gated_scan_fault(void) {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_scan_fault, sizeof(int)) != cudaSuccess) return -1;
+    if (v && cudaMemcpyToSymbol(g_scan_fault, &zero, sizeof(int)) != cudaSuccess) return -1;
+    return v;
 }
 
 namespace {

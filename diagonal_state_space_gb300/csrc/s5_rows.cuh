@@ -75,7 +75,8 @@ constexpr float LOG2E = 1.4426950408889634f;
 __device__ __forceinline__ float sigmoid(float g) { return rcp(1.0f + ex2(-LOG2E * g)); }
 
 // V floats of a lane whose sums and products go two to an instruction: these
-// kernels are as short of issue slots as of bandwidth.
+// kernels are as short of issue slots as of bandwidth.  A constant takes a pair of
+// registers there, and one by one none, so what has one goes one by one.
 template <int V> struct Many {
     float v[V];
     __device__ __forceinline__ float &operator[](int i) { return v[i]; }
@@ -133,12 +134,9 @@ template <int V> __device__ __forceinline__ Many<V> operator+(const Many<V> &a, 
 }
 #undef S5_TWO
 template <int V> __device__ __forceinline__ Many<V> sigmoid(const Many<V> &g) {
-    Many<V> e = g * Many<V>::all(-LOG2E);
+    Many<V> e;
 #pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = ex2(e[i]);
-    e = e + Many<V>::all(1.0f);
-#pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = rcp(e[i]);
+    for (int i = 0; i < V; ++i) e[i] = sigmoid(g[i]);
     return e;
 }
 

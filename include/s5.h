@@ -507,7 +507,7 @@ s5_status s5_qk_norm_rotary_backward(const void *q, long long ldq, const void *k
  * Outputs do not overlap inputs or each other but where a call says so.  All
  * arithmetic in 32 bits, one rounding at the end.  No atomics: equal inputs
  * give equal bits.  Asynchronous, launched with programmatic stream
- * serialisation; no call waits inside a kernel for another block's memory.
+ * serialisation.
  * Errors S5_ERR_INVALID_ARGUMENT, S5_ERR_UNSUPPORTED, S5_ERR_CUDA.
  * ======================================================================== */
 
@@ -546,6 +546,11 @@ s5_status s5_gated_scan_backward(const void *x, long long ldx, const void *gate_
                                  const float *dh_last, const void *saved, size_t saved_bytes, void *dx, long long lddx,
                                  void *dgate_a, long long lddga, void *dgate_x, long long lddgx, float *drate,
                                  float *dh0, void *workspace, size_t workspace_bytes, s5_stream_t stream);
+
+/* 1 if a wait inside the kernels of the two calls above ran out since the last
+ * call (their results are then not valid), 0 if none; the flag is cleared.
+ * Synchronises the device. */
+int s5_gated_scan_fault(void);
 
 /* One token per sequence: x, gate_a, gate_x (or NULL), h [B][C] of `dtype`,
  * contiguous; state [B][C] float32 is updated in place.  h may be x. */
