@@ -60,6 +60,8 @@ struct ScanArgs {
     float *drate;                       // [parts][C]
     float *dh0;                         // or null
     int cluster, rounds;                // tiles at once, and how often
+    // by place(): in bytes, the rows of one copy of the warp (inputs), one row (outputs), a round's tiles (both)
+    long long hop[4], step[4], row[3], out_step;
 };
 
 // A run that holds a reset has A = 0 and takes nothing over, not even NaN: zeros stay zeros whatever they are joined
@@ -88,13 +90,15 @@ template <int V> __device__ __forceinline__ void decay(const Many<V> &z, Many<V>
 
 __device__ __forceinline__ void cluster_arrive() { __syncwarp(); asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { __syncwarp(); asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// A pair into block `rank`'s copy of this block's shared variable, counted by that block's barrier.
-__device__ __forceinline__ void send(float2 *p, uint64_t *bar, unsigned rank, float2 v) {
-    unsigned at, counted;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(counted) : "r"(smem_addr(bar)), "r"(rank));
+// This block's shared address as block `rank` of the cluster has it; a pair stored there, counted by a barrier there.
+__device__ __forceinline__ unsigned there(unsigned at, unsigned rank) {
+    unsigned r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void send(unsigned at, unsigned bar, float2 v) {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at), "f"(v.x),
-                 "f"(v.y), "r"(counted)
+                 "f"(v.y), "r"(bar)
                  : "memory");
 }
 __device__ int g_scan_fault = 0;     // a wait for the cluster's pairs ran out
@@ -119,7 +123,7 @@ template <typename T_, int V_, int LANES_, int S_, int ARRAYS_, bool ASYNC_> str
     static constexpr int STAGE = ASYNC ? ARRAYS * TILE * WIDE * (int)sizeof(T) : 0;
     static constexpr int PAIRS = MAX_CLUSTER * WIDE;          // of a round
     static constexpr int STAGES = ARRAYS == 4 ? 2 : 1;        // backward a tile is read twice
-    static constexpr int SMEM = STAGES * STAGE + 2 * PAIRS * (int)sizeof(float2) + (ARRAYS == 4 ? 4 : 3) * WARPS * WIDE * (int)sizeof(float);
+    static constexpr int SMEM = STAGES * STAGE + 2 * PAIRS * (int)sizeof(float2) + 16 + (ARRAYS == 4 ? 4 : 3) * WARPS * WIDE * (int)sizeof(float);
     static_assert(TILE == KEEP || TILE == 2 * KEEP, "kept states lie at a group's start");
     static_assert(LANES * 2 == 32 || LANES == 32, "a warp holds one or two groups");
 };
@@ -136,13 +140,14 @@ template <typename Sh> struct Block {
     int b, c0, rank, lane, group, c;
     bool upper;         // the later of a warp's two groups
     int len;            // tokens of this sequence
-    __device__ Block(const ScanArgs &p, unsigned char *smem, uint64_t *bars) : bar(bars) {
+    __device__ Block(const ScanArgs &p, unsigned char *smem) {
         stage = reinterpret_cast<T *>(smem);
         pairs = reinterpret_cast<float2 *>(smem + Sh::STAGES * Sh::STAGE);
         A = reinterpret_cast<float *>(pairs + 2 * Sh::PAIRS);
         E = A + Sh::WARPS * W;
         H = E + Sh::WARPS * W;
         Z = H + Sh::WARPS * W;
+        bar = reinterpret_cast<uint64_t *>(smem + Sh::SMEM - 16);
         const int K = p.cluster, across = (p.C + W - 1) / W;
         rank = blockIdx.x % K;
         const int chain = blockIdx.x / K;
@@ -154,25 +159,36 @@ template <typename Sh> struct Block {
         upper = Sh::LANES == 32 || (threadIdx.x & 16);
     }
     __device__ void read_length(const ScanArgs &p) { len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L; }
+    // Where this thread's 16 bytes of the tile at t0 begin in each input.
+    static constexpr int PER = 16 / (int)sizeof(T), CHUNKS = W / PER, ROWS = 32 / CHUNKS, MINE = Sh::TILE / Sh::WARPS;
+    __device__ int first_row() const { return threadIdx.x / 32 * MINE + (threadIdx.x & 31) / CHUNKS; }
+    __device__ int first_value() const { return (threadIdx.x & 31) % CHUNKS * PER; }
+    __device__ void aim(const ScanArgs &p, int t0, const void *const *from, const long long *ld, const char **src) const {
+#pragma unroll
+        for (int k = 0; k < Sh::ARRAYS; ++k)
+            src[k] = from[k] ? reinterpret_cast<const char *>(static_cast<const T *>(from[k]) + ((long long)b * p.L + t0 + first_row()) * ld[k] +
+                                                              c0 + first_value())
+                             : nullptr;
+    }
     // Copies of this warp's rows of the tile at t0 into a stage, zeros where there is nothing to read.
-    __device__ void fetch(const ScanArgs &p, int which, int t0, const void *const *from, const long long *ld) {
-        constexpr int PER = 16 / sizeof(T), CHUNKS = W / PER, ROWS = 32 / CHUNKS, MINE = Sh::TILE / (THREADS / 32);
-        const int l = threadIdx.x & 31, chunk = l % CHUNKS, row = threadIdx.x / 32 * MINE + l / CHUNKS, at = c0 + chunk * PER;
-        const bool whole = t0 + Sh::TILE <= len && c0 + W <= p.C;
+    __device__ void fetch(const ScanArgs &p, int which, int t0, const void *const *from, const char *const *src) const {
+        const unsigned dst = smem_addr(stage + (which * Sh::ARRAYS * Sh::TILE + first_row()) * W + first_value());
+        if (t0 + Sh::TILE <= len && c0 + W <= p.C) {
 #pragma unroll
-        for (int k = 0; k < Sh::ARRAYS; ++k) {
-            if (!from[k]) continue;
-            const T *src = static_cast<const T *>(from[k]) + ((long long)b * p.L + t0 + row) * ld[k] + at;
-            unsigned dst = smem_addr(stage + ((which * Sh::ARRAYS + k) * Sh::TILE + row) * W + chunk * PER);
-            const long long hop = ROWS * ld[k];
-            if (whole) {
+            for (int k = 0; k < Sh::ARRAYS; ++k) {
+                if (!from[k]) continue;
+                const char *at = src[k];
 #pragma unroll
-                for (int i = 0; i < MINE / ROWS; ++i, src += hop) cp_async16(dst + i * ROWS * W * (int)sizeof(T), src);
-            } else {
+                for (int i = 0; i < MINE / ROWS; ++i, at += p.hop[k]) cp_async16(dst + (k * Sh::TILE + i * ROWS) * W * (int)sizeof(T), at);
+            }
+        } else {
 #pragma unroll
-                for (int i = 0; i < MINE / ROWS; ++i, src += hop) {
-                    const bool there = t0 + row + i * ROWS < len && at < p.C;
-                    cp_async16(dst + i * ROWS * W * (int)sizeof(T), there ? src : from[k], there);
+            for (int k = 0; k < Sh::ARRAYS; ++k) {
+                if (!from[k]) continue;
+#pragma unroll
+                for (int i = 0; i < MINE / ROWS; ++i) {
+                    const bool there = t0 + first_row() + i * ROWS < len && c0 + first_value() < p.C;
+                    cp_async16(dst + (k * Sh::TILE + i * ROWS) * W * (int)sizeof(T), there ? src[k] + i * p.hop[k] : from[k], there);
                 }
             }
         }
@@ -216,6 +232,9 @@ template <typename Sh> struct Block {
         for (int v = 0; v < V; ++v) r[v] = __shfl_xor_sync(0xffffffffu, x[v], 16);
         return r;
     }
+    // Two pairs joined and one applied, in full where resets may have left zeros.
+    __device__ static M joined(bool resets, const M &a, const M &b) { return resets ? joined(a, b) : a * b; }
+    __device__ static M applied(bool resets, const M &a, const M &h, const M &e) { return resets ? applied(a, h, e) : fma(a, h, e); }
     __device__ static M joined(const M &a, const M &b) {
         M r;
 #pragma unroll
@@ -243,36 +262,53 @@ template <typename Sh> struct Block {
     // which this one has sent its own, after reading round r: no half is overwritten before it is read.
     template <bool DOWN> __device__ float exchange(const ScanArgs &p, int round, const float *e, float &carry) {
         const int K = p.cluster, col = threadIdx.x % W, now = round & 1;
-        float2 all = make_float2(1.0f, 0.0f), *slots = pairs + now * MAX_CLUSTER * W + col;
+        const bool resets = p.reset;
+        float2 all = make_float2(1.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < Sh::WARPS; ++i) {
             const int j = DOWN ? Sh::WARPS - 1 - i : i;
-            const float Aj = A[j * W + col];
-            all = make_float2(join(Aj, all.x), apply(Aj, all.y, e[j * W + col]));
+            const float Aj = A[j * W + col], Ej = e[j * W + col];
+            all = resets ? make_float2(join(Aj, all.x), apply(Aj, all.y, Ej)) : make_float2(Aj * all.x, fmaf(Aj, all.y, Ej));
         }
-        for (int j = threadIdx.x / W; j < K; j += THREADS / W) send(slots + rank * W, bar + now, j, all);
+        const float2 *slots = pairs + now * MAX_CLUSTER * W + col;
+        const unsigned base = smem_addr(pairs), at = smem_addr(slots + rank * W) - base, count = smem_addr(bar + now) - base;
+#pragma unroll 4
+        for (int j = threadIdx.x / W; j < K; j += THREADS / W) {
+            const unsigned far = there(base, j);
+            send(far + at, far + count, all);
+        }
         if (threadIdx.x >= W) return 0.0f;
         if (!sm100::mbar_try_wait(bar + now, round >> 1 & 1)) wait_long(bar + now, round >> 1 & 1);
         if (threadIdx.x == 0 && round + 2 < p.rounds) sm100::mbar_arrive_tx(bar + now, K * W * sizeof(float2));
-        float before = carry;
-        for (int i = 0; i < K; ++i) {
-            const int j = DOWN ? K - 1 - i : i;
-            const float2 q = slots[j * W];
-            if (j == rank) before = carry;
-            carry = apply(q.x, carry, q.y);
-        }
+        const int mine = DOWN ? K - 1 - rank : rank;
+        auto run = [&](int from, int to) {
+            if (resets) {
+                for (int i = from; i < to; ++i) {
+                    const float2 q = slots[(DOWN ? K - 1 - i : i) * W];
+                    carry = apply(q.x, carry, q.y);
+                }
+            } else {
+#pragma unroll 4
+                for (int i = from; i < to; ++i) {
+                    const float2 q = slots[(DOWN ? K - 1 - i : i) * W];
+                    carry = fmaf(q.x, carry, q.y);
+                }
+            }
+        };
+        run(0, mine);
+        const float before = carry;
+        run(mine, K);
         return before;
     }
 };
 
-template <typename Sh, bool GATED, bool MARKS>
+template <typename Sh, bool GATED, bool NORM>
 __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanArgs p) {
     using T = typename Sh::T;
     using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t bars[2];
-    Block<Sh> k(p, smem, bars);
+    Block<Sh> k(p, smem);
     const int K = p.cluster;
     griddep_wait();
     k.read_length(p);
@@ -280,15 +316,23 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
     const long long ld[3] = {p.ldx, p.ldga, p.ldgx};
     int t0 = k.rank * Sh::TILE;
     unsigned marks = 0;
-    if (Sh::ASYNC) k.fetch(p, 0, t0, from, ld);
-    if (Sh::ASYNC) cp_async_commit();
+    const char *src[3];
+    if (Sh::ASYNC) {
+        k.aim(p, t0, from, ld, src);
+        k.fetch(p, 0, t0, from, src);
+        cp_async_commit();
+    }
     if (K > 1) k.open_cluster(p);
     const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
-    if (MARKS) marks = k.marks(p, t0);
+    if (p.reset) marks = k.marks(p, t0);
     // the thread that folds channel c0 + threadIdx.x over the tile's warps
     const bool folds = threadIdx.x < W && k.c0 + (int)threadIdx.x < p.C;
     const int ch = k.c0 + threadIdx.x;
     float carry = folds && p.h0 ? p.h0[(long long)k.b * p.C + ch] : 0.0f;   // the state before this round's first tile
+    char *out = reinterpret_cast<char *>(static_cast<T *>(p.h) + ((long long)k.b * p.L + t0 + k.group * S) * p.ldh + k.c);
+    const int apart = KEEP / (Sh::TILE / Sh::WARPS);      // warps between two kept states
+    float *kept = p.states + ((long long)k.b * ((p.L + KEEP - 1) / KEEP) + t0 / KEEP) * p.C + ch;
+    const bool resets = p.reset;
     if (K > 1) cluster_wait();
 
     for (int round = 0; round < p.rounds; ++round, t0 += K * Sh::TILE) {
@@ -297,10 +341,10 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
             cp_async_wait<0>();
             __syncwarp();
         }
-        if (MARKS && round + 1 < p.rounds) ahead = k.marks(p, t0 + K * Sh::TILE);
+        if (p.reset && round + 1 < p.rounds) ahead = k.marks(p, t0 + K * Sh::TILE);
         const int mine = t0 + k.group * S;   // this thread's first token
         const bool ragged = t0 + Sh::TILE > k.len;
-        const bool slow = ragged || (MARKS && marks);
+        const bool slow = ragged || marks;
         M a[S], e[S], A = one, E = none;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -308,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
             M n;
             decay(rate * sigmoid(k.load(p, 0, t0, s, 1, from, ld)), a[s], n);
             e[s] = GATED ? sigmoid(k.load(p, 0, t0, s, 2, from, ld)) * x : x;
-            if (p.normalize) {
+            if (NORM) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) n[v] = sqrt_(n[v]);
                 e[s] = n * e[s];
@@ -320,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
             A = one, E = none;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                if (MARKS && (marks >> s & 1)) {
+                if (marks >> s & 1) {
                     a[s] = none, e[s] = k.load(p, 0, t0, s, 0, from, ld);
                     if (GATED) e[s] = sigmoid(k.load(p, 0, t0, s, 2, from, ld)) * e[s];
                 }
@@ -331,14 +375,18 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
         }
         if (Sh::ASYNC) {                     // the next tile is on its way while the pairs meet
             __syncwarp();
-            if (round + 1 < p.rounds) k.fetch(p, 0, t0 + K * Sh::TILE, from, ld);
+            if (round + 1 < p.rounds) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) src[i] += p.step[i];
+                k.fetch(p, 0, t0 + K * Sh::TILE, from, src);
+            }
             cp_async_commit();
         }
         M pA = one, pE = none;               // of the warp's earlier group, for the later one
         if (Sh::LANES == 16) {
             pA = k.other(A), pE = k.other(E);
-            E = k.applied(A, pE, E);
-            A = k.joined(A, pA);
+            E = k.applied(resets, A, pE, E);
+            A = k.joined(resets, A, pA);
         }
         if (k.upper) {
             k.put(k.A, A);
@@ -351,28 +399,30 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
 #pragma unroll
             for (int j = 0; j < Sh::WARPS; ++j) {
                 k.H[j * W + threadIdx.x] = before;
-                if (j * (Sh::TILE / Sh::WARPS) % KEEP == 0 && p.states && folds && t0 + j * (Sh::TILE / Sh::WARPS) < p.L)
-                    p.states[((long long)k.b * ((p.L + KEEP - 1) / KEEP) + (t0 + j * (Sh::TILE / Sh::WARPS)) / KEEP) * p.C + ch] = before;
-                before = apply(k.A[j * W + threadIdx.x], before, k.E[j * W + threadIdx.x]);
+                if (j % apart == 0 && p.states && folds && t0 + j * (Sh::TILE / Sh::WARPS) < p.L) kept[j / apart * p.C] = before;
+                const float Aj = k.A[j * W + threadIdx.x], Ej = k.E[j * W + threadIdx.x];
+                before = resets ? apply(Aj, before, Ej) : fmaf(Aj, before, Ej);
             }
             if (K == 1) carry = before;
+            kept += (long long)K * (Sh::TILE / KEEP) * p.C;
         }
         __syncthreads();
         M h = k.get(k.H);
-        if (Sh::LANES == 16 && k.upper) h = k.applied(pA, h, pE);
-        T *out = static_cast<T *>(p.h) + ((long long)k.b * p.L + mine) * p.ldh + k.c;
+        if (Sh::LANES == 16 && k.upper) h = k.applied(resets, pA, h, pE);
+        char *to = out;
+        out += p.out_step;
         if (!slow) {
 #pragma unroll
-            for (int s = 0; s < S; ++s, out += p.ldh) {
+            for (int s = 0; s < S; ++s, to += p.row[0]) {
                 h = fma(a[s], h, e[s]);
-                if (k.c < p.C) Vec<T, V>::store(out, h.v);
+                if (k.c < p.C) Vec<T, V>::store(reinterpret_cast<T *>(to), h.v);
             }
         } else {
 #pragma unroll
-            for (int s = 0; s < S; ++s, out += p.ldh) {
+            for (int s = 0; s < S; ++s, to += p.row[0]) {
                 h = k.applied(a[s], h, e[s]);
                 const M o = mine + s < k.len ? h : none;
-                if (mine + s < p.L && k.c < p.C) Vec<T, V>::store(out, o.v);
+                if (mine + s < p.L && k.c < p.C) Vec<T, V>::store(reinterpret_cast<T *>(to), o.v);
             }
         }
         marks = ahead;
@@ -381,14 +431,13 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
     if (k.rank == 0 && folds && p.h_last) p.h_last[(long long)k.b * p.C + ch] = carry;
 }
 
-template <typename Sh, bool GATED, bool MARKS>
+template <typename Sh, bool GATED, bool NORM>
 __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanArgs p) {
     using T = typename Sh::T;
     using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t bars[2];
-    Block<Sh> k(p, smem, bars);
+    Block<Sh> k(p, smem);
     const int K = p.cluster, N = (p.L + KEEP - 1) / KEEP;
     griddep_wait();
     k.read_length(p);
@@ -396,16 +445,21 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
     const long long ld[4] = {p.ldx, p.ldga, p.lddh, p.ldgx};
     int t0 = ((p.rounds - 1) * K + k.rank) * Sh::TILE;   // from the last tiles to the first
     unsigned marks = 0;
-    if (Sh::ASYNC) k.fetch(p, 0, t0, from, ld);
-    if (Sh::ASYNC) cp_async_commit();
+    if (Sh::ASYNC) {
+        const char *src[4];
+        k.aim(p, t0, from, ld, src);
+        k.fetch(p, 0, t0, from, src);
+        cp_async_commit();
+    }
     if (K > 1) k.open_cluster(p);
     const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
     M drate = none;
-    if (MARKS) marks = k.marks(p, t0);
+    if (p.reset) marks = k.marks(p, t0);
     // threads 0 .. W - 1 fold the adjoints of a channel, the next W its states
     const int col = threadIdx.x % W, ch = k.c0 + col;
     const bool folds = threadIdx.x < W, forward = threadIdx.x / W == 1;
     float carry = folds && ch < p.C && p.dh_last ? p.dh_last[(long long)k.b * p.C + ch] : 0.0f;   // a G of what follows
+    const bool resets = p.reset;
     if (K > 1) cluster_wait();
 
     for (int round = 0; round < p.rounds; ++round, t0 -= K * Sh::TILE) {
@@ -414,15 +468,19 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
         if (Sh::ASYNC) {
             cp_async_wait<0>();
             __syncwarp();
-            if (round + 1 < p.rounds) k.fetch(p, 1 - now, t0 - K * Sh::TILE, from, ld);
+            if (round + 1 < p.rounds) {
+                const char *src[4];          // worked out anew: kept, they would cost spills
+                k.aim(p, t0 - K * Sh::TILE, from, ld, src);
+                k.fetch(p, 1 - now, t0 - K * Sh::TILE, from, src);
+            }
             cp_async_commit();
         }
-        if (MARKS && round + 1 < p.rounds) ahead = k.marks(p, t0 - K * Sh::TILE);
+        if (p.reset && round + 1 < p.rounds) ahead = k.marks(p, t0 - K * Sh::TILE);
         float state = 0.0f;                  // before the tile
         if (forward && ch < p.C && t0 < p.L) state = p.states[((long long)k.b * N + t0 / KEEP) * p.C + ch];
         const int mine = t0 + k.group * S;
         const bool ragged = t0 + Sh::TILE > k.len;
-        const bool slow = ragged || (MARKS && marks);
+        const bool slow = ragged || marks;
         // per value: a, r, the sigmoid s, n s, and a^2/n u, then a h - a^2/n u
         M a[S], r[S], g[S], ns[S], D[S], A = one, E = none, Z = none;
 #pragma unroll
@@ -432,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
             if (GATED) g[s] = sigmoid(k.load(p, now, t0, s, 3, from, ld));
             M n2, n = one, inv = none;
             decay(rate * r[s], a[s], n2);
-            if (p.normalize) {
+            if (NORM) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const float q = rsqrt_(fmaxf(n2[v], 1e-37f));
@@ -453,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
             A = one, E = none;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                if (MARKS && (marks >> s & 1)) a[s] = none, ns[s] = GATED ? g[s] : one;
+                if (marks >> s & 1) a[s] = none, ns[s] = GATED ? g[s] : one;
                 if (mine + s >= k.len) a[s] = one, ns[s] = none;
                 E = k.applied(a[s], E, ns[s] * k.load(p, now, t0, s, 0, from, ld));
                 A = k.joined(A, a[s]);
@@ -461,15 +519,15 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
 #pragma unroll
             for (int s = S - 1; s >= 0; --s) {
                 Z = a[s] * (k.load(p, now, t0, s, 2, from, ld) + Z);
-                if (MARKS && (marks >> s & 1)) Z = none;
+                if (marks >> s & 1) Z = none;
             }
         }
         M pA = one, pE = none, pZ = none;    // of the warp's other group
         if (Sh::LANES == 16) {
             pA = k.other(A), pE = k.other(E), pZ = k.other(Z);
-            E = k.applied(A, pE, E);
-            Z = k.applied(A, pZ, Z);
-            A = k.joined(A, pA);
+            E = k.applied(resets, A, pE, E);
+            Z = k.applied(resets, A, pZ, Z);
+            A = k.joined(resets, A, pA);
         }
         if (k.upper) {
             k.put(k.A, A);
@@ -485,22 +543,24 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
             for (int j = 0; j < Sh::WARPS; ++j) {
                 const float Ej = k.E[j * W + col];
                 k.E[j * W + col] = state;
-                state = apply(k.A[j * W + col], state, Ej);
+                const float Aj = k.A[j * W + col];
+                state = resets ? apply(Aj, state, Ej) : fmaf(Aj, state, Ej);
             }
         }
         if (folds) {                         // what arrives from after each warp's tokens
 #pragma unroll
             for (int j = Sh::WARPS - 1; j >= 0; --j) {
                 k.H[j * W + col] = after;
-                after = apply(k.A[j * W + col], after, k.Z[j * W + col]);
+                const float Aj = k.A[j * W + col], Zj = k.Z[j * W + col];
+                after = resets ? apply(Aj, after, Zj) : fmaf(Aj, after, Zj);
             }
             if (K == 1) carry = after;
         }
         __syncthreads();
         M h = k.get(k.E), z = k.get(k.H);
         if (Sh::LANES == 16) {
-            if (k.upper) h = k.applied(pA, h, pE);
-            else z = k.applied(pA, z, pZ);
+            if (k.upper) h = k.applied(resets, pA, h, pE);
+            else z = k.applied(resets, pA, z, pZ);
         }
         if (!slow) {
 #pragma unroll
@@ -514,15 +574,16 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 const M e = ns[s] * k.load(p, now, t0, s, 0, from, ld);
-                const bool dead = (MARKS && (marks >> s & 1)) || mine + s >= k.len;
+                const bool dead = (marks >> s & 1) || mine + s >= k.len;
 #pragma unroll
                 for (int v = 0; v < V; ++v) D[s][v] = dead ? 0.0f : fmaf(a[s][v], h[v], -D[s][v]);
                 h = k.applied(a[s], h, e);
             }
         }
-        const long long row = (long long)k.b * p.L + mine + S - 1;
-        T *dx = static_cast<T *>(p.dx) + row * p.lddx + k.c, *dga = static_cast<T *>(p.dga) + row * p.lddga + k.c;
-        T *dgx = GATED ? static_cast<T *>(p.dgx) + row * p.lddgx + k.c : nullptr;
+        const long long last = (long long)k.b * p.L + mine + S - 1;
+        char *to1 = reinterpret_cast<char *>(static_cast<T *>(p.dx) + last * p.lddx + k.c);
+        char *to2 = reinterpret_cast<char *>(static_cast<T *>(p.dga) + last * p.lddga + k.c);
+        char *to3 = GATED ? reinterpret_cast<char *>(static_cast<T *>(p.dgx) + last * p.lddgx + k.c) : nullptr;
 #pragma unroll
         for (int s = S - 1; s >= 0; --s) {
             const M G = k.load(p, now, t0, s, 2, from, ld) + z;
@@ -531,19 +592,19 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
 #pragma unroll
             for (int v = 0; v < V; ++v) drate[v] -= t[v], o2[v] = fmaf(w[v], -r[s][v], w[v]);
             z = a[s] * G;
-            if (MARKS && (marks >> s & 1)) z = none;
+            if (slow && (marks >> s & 1)) z = none;
             if (GATED) {
                 const M q = o1 * k.load(p, now, t0, s, 0, from, ld);
 #pragma unroll
                 for (int v = 0; v < V; ++v) o3[v] = fmaf(q[v], -g[s][v], q[v]);
             }
             if (k.c < p.C && (!slow || mine + s < p.L)) {
-                Vec<T, V>::store(dx, o1.v);
-                Vec<T, V>::store(dga, o2.v);
-                if (GATED) Vec<T, V>::store(dgx, o3.v);
+                Vec<T, V>::store(reinterpret_cast<T *>(to1), o1.v);
+                Vec<T, V>::store(reinterpret_cast<T *>(to2), o2.v);
+                if (GATED) Vec<T, V>::store(reinterpret_cast<T *>(to3), o3.v);
             }
-            dx -= p.lddx, dga -= p.lddga;
-            if (GATED) dgx -= p.lddgx;
+            to1 -= p.row[0], to2 -= p.row[1];
+            if (GATED) to3 -= p.row[2];
         }
         marks = ahead;
     }
@@ -623,6 +684,12 @@ template <typename Sh> cudaError_t place(ScanArgs &p, long long &blocks) {
     p.cluster = choose_cluster(chains, tiles);
     p.rounds = (tiles + p.cluster - 1) / p.cluster;
     blocks = chains * p.cluster;
+    const long long bytes = sizeof(typename Sh::T), round = bytes * p.cluster * Sh::TILE;
+    const bool back = Sh::ARRAYS == 4;
+    const long long in[4] = {p.ldx, p.ldga, back ? p.lddh : p.ldgx, p.ldgx}, out[3] = {back ? p.lddx : p.ldh, p.lddga, p.lddgx};
+    for (int i = 0; i < 4; ++i) p.hop[i] = bytes * Block<Sh>::ROWS * in[i], p.step[i] = round * in[i];
+    for (int i = 0; i < 3; ++i) p.row[i] = bytes * out[i];
+    p.out_step = round * out[0];
     return blocks > 0x7fffffffll ? cudaErrorInvalidValue : cudaSuccess;
 }
 
@@ -638,9 +705,9 @@ template <typename Sh> cudaError_t run_fwd(ScanArgs &p, cudaStream_t st) {
     long long blocks;
     const cudaError_t e = place<Sh>(p, blocks);
     if (e != cudaSuccess) return e;
-#define S5_RUN(GATED, MARKS) launch_scan(gated_scan_fwd_kernel<Sh, GATED, MARKS>, p, blocks, Sh::SMEM, st)
-    if (p.gx) return p.reset ? S5_RUN(true, true) : S5_RUN(true, false);
-    return p.reset ? S5_RUN(false, true) : S5_RUN(false, false);
+#define S5_RUN(GATED, NORM) launch_scan(gated_scan_fwd_kernel<Sh, GATED, NORM>, p, blocks, Sh::SMEM, st)
+    if (p.gx) return p.normalize ? S5_RUN(true, true) : S5_RUN(true, false);
+    return p.normalize ? S5_RUN(false, true) : S5_RUN(false, false);
 #undef S5_RUN
 }
 
@@ -650,9 +717,9 @@ template <typename Sh> cudaError_t run_bwd(ScanArgs &p, float *drate, cudaStream
     if (e != cudaSuccess) return e;
     const int parts = p.B * p.cluster;
     if (parts == 1) p.drate = drate;
-#define S5_RUN(GATED, MARKS) launch_scan(gated_scan_bwd_kernel<Sh, GATED, MARKS>, p, blocks, Sh::SMEM, st)
-    if (p.gx) e = p.reset ? S5_RUN(true, true) : S5_RUN(true, false);
-    else e = p.reset ? S5_RUN(false, true) : S5_RUN(false, false);
+#define S5_RUN(GATED, NORM) launch_scan(gated_scan_bwd_kernel<Sh, GATED, NORM>, p, blocks, Sh::SMEM, st)
+    if (p.gx) e = p.normalize ? S5_RUN(true, true) : S5_RUN(true, false);
+    else e = p.normalize ? S5_RUN(false, true) : S5_RUN(false, false);
 #undef S5_RUN
     if (e != cudaSuccess || parts == 1) return e;
     return launch(gated_scan_rate_kernel, dim3((p.C + 31) / 32), 256, 0, 1, st, (const float *)p.drate, parts, p.C, drate);
@@ -729,11 +796,11 @@ extern "C" s5_status s5_gated_scan_forward(const void *x, long long ldx, const v
     if (dtype == S5_BF16)
         e = w == 8   ? run_fwd<Shape<__nv_bfloat16, 4, 16, 8, 3, true>>(p, st)
             : w == 2 ? run_fwd<Shape<__nv_bfloat16, 2, 16, 8, 3, false>>(p, st)
-                     : run_fwd<Shape<__nv_bfloat16, 1, 32, 16, 3, false>>(p, st);
+                     : run_fwd<Shape<__nv_bfloat16, 1, 32, 8, 3, false>>(p, st);
     else
         e = w == 4   ? run_fwd<Shape<float, 2, 16, 8, 3, true>>(p, st)
             : w == 2 ? run_fwd<Shape<float, 2, 16, 8, 3, false>>(p, st)
-                     : run_fwd<Shape<float, 1, 32, 16, 3, false>>(p, st);
+                     : run_fwd<Shape<float, 1, 32, 8, 3, false>>(p, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
 

@@ -18,9 +18,18 @@ template <typename T, int V> struct Vec {
     __device__ static raw get(const T *p) { return *reinterpret_cast<const raw *>(p); }
     __device__ static void put(T *p, const raw &t) { *reinterpret_cast<raw *>(p) = t; }
     __device__ static void widen(const raw &t, float (&r)[V]) {
-        const T *e = reinterpret_cast<const T *>(&t);
+        if constexpr (sizeof(T) == 2 && V > 1) {     // bf16 is the upper half of its float
+            const unsigned *w = reinterpret_cast<const unsigned *>(&t);
 #pragma unroll
-        for (int i = 0; i < V; ++i) r[i] = (float)e[i];
+            for (int i = 0; i < V; i += 2) {
+                r[i] = __uint_as_float(w[i / 2] << 16);
+                r[i + 1] = __uint_as_float(w[i / 2] & 0xffff0000u);
+            }
+        } else {
+            const T *e = reinterpret_cast<const T *>(&t);
+#pragma unroll
+            for (int i = 0; i < V; ++i) r[i] = (float)e[i];
+        }
     }
     __device__ static raw round(const float (&r)[V]) {
         raw t;
