@@ -180,10 +180,11 @@ cudaError_t launch(void (*k)(Ks...), dim3 grid, int threads, size_t smem, int cl
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
-// The same for a kernel with dynamic shared memory beyond 48 KB.
+// The same for a kernel with dynamic shared memory that may pass 48 KB.
 template <typename... Ks, typename... As>
 cudaError_t launch_big(void (*k)(Ks...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, As... args) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e =
+        smem > 48 << 10 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
     return e != cudaSuccess ? e : launch(k, grid, threads, smem, cluster, st, args...);
 }
 

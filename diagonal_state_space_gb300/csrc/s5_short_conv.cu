@@ -5,23 +5,28 @@
 // where a token before the sequence is `past` (or 0) and one before a reset 0;
 //   dp = dy act'(p),  dx_t = sum_j w_j dp_{t+K-1-j},  dw_j = sum dp_t x_{t-K+1+j}.
 //
-// Bound: memory, with little to spare: a value is 2 K + 12 instructions
-// forward and 6 K + 20 backward.  A lane walks a segment of tokens of V
+// Bound: memory, with little to spare: of K = 4 a value takes about 10
+// instructions forward and 18 backward.  A lane walks a segment of tokens of V
 // channels with the last K - 1 inputs (and, backward, the K sums of dx that are
 // not whole yet) in registers, so that an input is read once and the K - 1
-// around a segment twice, out of L2.  A warp's lanes are at one token, so what
-// a reset clears is the same for all of them: the window itself, and nothing
-// behind it is multiplied, not even by zero.
+// around a segment twice, out of L2.  Each warp has a ring of its own in shared
+// memory, that 16-byte copies fill some tokens ahead, and waits for no other.  A
+// warp's lanes are at one token, so what a reset clears is the same for all of
+// them: the window itself, and nothing behind it is multiplied, not even by
+// zero.  Tokens in the middle of a segment without resets take a path without
+// any test.
 #include "s5_rows.cuh"
+#include "s5_sm100.cuh"
 
 namespace s5 {
 namespace {
 using namespace rows;
+using sm100::smem_addr;
 
 constexpr int WARPS = 4;                 // of a block
-constexpr int UF = 8, UB = 4;            // tokens that are loaded at once, forward and backward
+constexpr int U = 8;                     // tokens of a ring's stage, and of one pass of the loop
 constexpr int MAX_TAPS = 8;
-constexpr int BWD_BLOCKS = 4 * SMS;      // of the backward pass, about: a part of the weights' gradient each
+constexpr int BLOCKS = 4 * SMS;          // that run at once; backward a part of the weights' gradient each
 
 struct ConvArgs {
     const void *x;
@@ -46,32 +51,44 @@ struct ConvArgs {
     int along;                           // blocks along the tokens
 };
 
-template <int V, int K> __device__ __forceinline__ void load_taps(const ConvArgs &p, int c, bool in, float (&w)[V * K], float (&bias)[V]) {
+template <int V, int K> __device__ __forceinline__ void load_taps(const ConvArgs &p, int c, bool in, Many<V> (&w)[K], Many<V> &bias) {
+    float flat[V * K] = {};
+    if (in) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-        float t[V] = {};
-        if (in) Vec<float, V>::load(p.w + (long long)c * K + j * V, t);
-#pragma unroll
-        for (int v = 0; v < V; ++v) w[j * V + v] = t[v];
+        for (int j = 0; j < K; ++j) Vec<float, V>::load(p.w + (long long)c * K + j * V, *reinterpret_cast<float(*)[V]>(flat + j * V));
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) bias[v] = 0.0f;
-    if (in && p.bias) Vec<float, V>::load(p.bias + c, bias);
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[j][v] = flat[v * K + j];
+    bias = Many<V>::all(0.0f);
+    if (in && p.bias) Vec<float, V>::load(p.bias + c, bias.v);
 }
 
 // Bit i: token t + i of the sequence is a reset.  All lanes of the warp call it.
-template <int U> __device__ __forceinline__ unsigned resets(const ConvArgs &p, int b, int t, int len) {
+template <int N> __device__ __forceinline__ unsigned resets(const ConvArgs &p, int b, int t, int len) {
     const int lane = threadIdx.x & 31, at = t + lane;
-    return __ballot_sync(0xffffffffu, lane < U && at >= 0 && at < len && p.reset[(long long)b * p.L + at]);
+    return __ballot_sync(0xffffffffu, lane < N && at >= 0 && at < len && p.reset[(long long)b * p.L + at]);
 }
 
 // What one segment's walk shares in both directions.
-template <typename T, int V, int K> struct Walk {
+template <typename T, int V, int K, int ARRAYS, bool ASYNC> struct Walk {
+    using M = Many<V>;
+    static constexpr int ROW = 32 * V * (int)sizeof(T);          // bytes of a warp's row
+    static constexpr int CHUNKS = ROW / 16, ROWS = ASYNC ? 32 / CHUNKS : 1;
+    static constexpr int STAGES = ARRAYS == 1 ? 4 : 3;
+    static constexpr int RING = ASYNC ? STAGES * ARRAYS * U * ROW : 0;   // bytes of a warp
     int b, t0, len, c;
     bool in;                             // this lane has channels
-    float win[K - 1][V];                 // the inputs before the token
+    M win[K - 1];                        // the inputs before the token
     int age;                             // tokens since the last reset, K where it is too long ago to matter
+    unsigned char *ring;                 // [STAGES][ARRAYS][U][ROW]
 
+    __device__ Walk(const ConvArgs &p, unsigned char *smem) {
+        c = (blockIdx.x % p.across * 32 + (threadIdx.x & 31)) * V;
+        in = c < p.C;
+        ring = smem + threadIdx.x / 32 * RING;
+    }
     __device__ const T *row(const ConvArgs &p, const void *a, long long ld, int t) const {
         return static_cast<const T *>(a) + ((long long)b * p.L + t) * ld + c;
     }
@@ -80,21 +97,41 @@ template <typename T, int V, int K> struct Walk {
         t0 = segment % p.segs * p.R;
         len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
     }
+    // Tokens t .. t + U - 1, as far as they are before `stop`, on their way into a stage.
+    __device__ void fetch(const ConvArgs &p, int stage, int t, int stop, const void *const *from, const long long *ld) {
+        if constexpr (ASYNC) {
+            const int l = threadIdx.x & 31, at = blockIdx.x % p.across * 32 * V + l % CHUNKS * (16 / (int)sizeof(T));
+#pragma unroll
+            for (int k = 0; k < ARRAYS; ++k) {
+                const char *src = reinterpret_cast<const char *>(static_cast<const T *>(from[k]) + ((long long)b * p.L + t + l / CHUNKS) * ld[k] + at);
+                const unsigned dst = smem_addr(ring + ((stage * ARRAYS + k) * U + l / CHUNKS) * ROW + l % CHUNKS * 16);
+                const long long hop = ROWS * ld[k] * (long long)sizeof(T);
+#pragma unroll
+                for (int i = 0; i < U / ROWS; ++i, src += hop)
+                    if (at < p.C && t + l / CHUNKS + i * ROWS < stop) cp_async16(dst + i * ROWS * ROW, src);
+            }
+        }
+        cp_async_commit();
+    }
+    // This lane's values of array k at token t, the i-th of the stage; whatever where there is none.
+    __device__ M load(const ConvArgs &p, int stage, int t, int i, int k, int stop, const void *const *from, const long long *ld) const {
+        M r = M::all(0.0f);
+        if constexpr (ASYNC) {
+            Vec<T, V>::load(reinterpret_cast<const T *>(ring + ((stage * ARRAYS + k) * U + i) * ROW) + (threadIdx.x & 31) * V, r.v);
+        } else {
+            if (in && t + i < stop) Vec<T, V>::load(row(p, from[k], ld[k], t + i), r.v);
+        }
+        return r;
+    }
     __device__ void fresh() {
         age = 0;
 #pragma unroll
-        for (int i = 0; i < K - 1; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[i][v] = 0.0f;
+        for (int i = 0; i < K - 1; ++i) win[i] = M::all(0.0f);
     }
-    __device__ void push(const float (&x)[V]) {
+    __device__ void push(const M &x) {
 #pragma unroll
-        for (int i = 0; i < K - 2; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[i][v] = win[i + 1][v];
-#pragma unroll
-        for (int v = 0; v < V; ++v) win[K - 2][v] = x[v];
-        if (age < K) ++age;
+        for (int i = 0; i < K - 2; ++i) win[i] = win[i + 1];
+        win[K - 2] = x;
     }
     // The K - 1 inputs before the segment.
     __device__ void open(const ConvArgs &p) {
@@ -110,16 +147,17 @@ template <typename T, int V, int K> struct Walk {
         age = K;
 #pragma unroll
         for (int i = 0; i < K - 1; ++i) {
-            float x[V];
-            Vec<T, V>::widen(raw[i], x);
+            M x;
+            Vec<T, V>::widen(raw[i], x.v);
             if (marks >> i & 1) fresh();
             push(x);
+            age = min(age + 1, K);
         }
     }
-    __device__ float tap(const float (&w)[V * K], const float (&bias)[V], const float (&x)[V], int v) const {
-        float s = fmaf(w[v * K + K - 1], x[v], bias[v]);
+    __device__ M taps(const M (&w)[K], const M &bias, const M &x) const {
+        M s = fma(w[K - 1], x, bias);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) s = fmaf(w[v * K + j], win[j][v], s);
+        for (int j = 0; j < K - 1; ++j) s = fma(w[j], win[j], s);
         return s;
     }
     // The last reset of the sequence's last K - 1 tokens, or -K.
@@ -129,25 +167,22 @@ template <typename T, int V, int K> struct Walk {
     }
 };
 
-template <typename T, int V, int K>
-__global__ void __launch_bounds__(WARPS * 32) short_conv_fwd_kernel(const ConvArgs p) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Walk<T, V, K> k;
-    k.c = (blockIdx.x % p.across * 32 + lane) * V;
-    k.in = k.c < p.C;
-    const long long segment = (long long)(blockIdx.x / p.across) * WARPS + warp;
+template <typename T, int V, int K, bool ASYNC>
+__global__ void __launch_bounds__(WARPS * 32, 4) short_conv_fwd_kernel(const ConvArgs p) {
+    using M = Many<V>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    constexpr int STAGES = Walk<T, V, K, 1, ASYNC>::STAGES;
+    Walk<T, V, K, 1, ASYNC> k(p, smem);
+    const long long segment = (long long)(blockIdx.x / p.across) * WARPS + threadIdx.x / 32;
     if (segment >= (long long)p.B * p.segs) return;
     griddep_wait();
     k.place(p, (int)segment);
-    const int end = min(k.t0 + p.R, p.L);
-    typename Vec<T, V>::raw next[UF] = {}, raw[UF];
-    auto fetch = [&](int t) {
+    const int end = min(k.t0 + p.R, p.L), stop = min(end, k.len);
+    const void *const from[1] = {p.x};
+    const long long ld[1] = {p.ldx};
 #pragma unroll
-        for (int i = 0; i < UF; ++i)
-            if (k.in && t + i < k.len && t + i < end) next[i] = Vec<T, V>::get(k.row(p, p.x, p.ldx, t + i));
-    };
-    fetch(k.t0);
-    float w[V * K], bias[V];
+    for (int i = 0; i < STAGES - 1; ++i) k.fetch(p, i, k.t0 + i * U, stop, from, ld);
+    M w[K], bias;
     load_taps<V, K>(p, k.c, k.in, w, bias);
     k.open(p);
     if (k.t0 == 0 && p.past_out) {       // all of `past` that any warp reads is read by this one, above or here
@@ -164,142 +199,167 @@ __global__ void __launch_bounds__(WARPS * 32) short_conv_fwd_kernel(const ConvAr
         for (int i = 0; i < K - 1; ++i)
             if (k.in) Vec<T, V>::put(static_cast<T *>(p.past_out) + ((long long)k.b * (K - 1) + i) * p.C + k.c, keep[i]);
     }
-    T *out = static_cast<T *>(p.y) + ((long long)k.b * p.L + k.t0) * p.ldy + k.c;
-    for (int t = k.t0; t < end; t += UF, out += UF * p.ldy) {
-#pragma unroll
-        for (int i = 0; i < UF; ++i) raw[i] = next[i];
-        fetch(t + UF);
-        const unsigned marks = p.reset ? resets<UF>(p, k.b, t, k.len) : 0;
-#pragma unroll
-        for (int i = 0; i < UF; ++i) {
-            float x[V], y[V];
-            Vec<T, V>::widen(raw[i], x);
-            if (marks >> i & 1) k.fresh();
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float s = k.tap(w, bias, x, v);
-                y[v] = p.act ? s * sigmoid(s) : s;
-                if (t + i >= k.len) y[v] = 0.0f;
-            }
-            if (k.in && t + i < end) Vec<T, V>::store(out + i * p.ldy, y);
-            k.push(x);
+    char *out = reinterpret_cast<char *>(static_cast<T *>(p.y) + ((long long)k.b * p.L + k.t0) * p.ldy + k.c);
+    const long long hop = p.ldy * (long long)sizeof(T);
+    int stage = 0;
+    for (int t = k.t0; t < end; t += U, stage = (stage + 1) % STAGES) {
+        const unsigned marks = p.reset ? resets<U>(p, k.b, t, k.len) : 0;
+        if (ASYNC) {
+            cp_async_wait<STAGES - 2>();
+            __syncwarp();                // the stage is here, and all lanes are done with the one before it
+            k.fetch(p, (stage + STAGES - 1) % STAGES, t + (STAGES - 1) * U, stop, from, ld);
         }
-    }
-}
-
-template <typename T, int V, int K>
-__global__ void __launch_bounds__(WARPS * 32) short_conv_bwd_kernel(const ConvArgs p) {
-    __shared__ float sums[WARPS - 1][(K + 1) * V][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Walk<T, V, K> k;
-    k.c = (blockIdx.x % p.across * 32 + lane) * V;
-    k.in = k.c < p.C;
-    const int block = blockIdx.x / p.across;
-    griddep_wait();
-    float w[V * K], bias[V], dw[V * K], db[V];
-    load_taps<V, K>(p, k.c, k.in, w, bias);
+        if (!marks && t + U <= stop) {
 #pragma unroll
-    for (int i = 0; i < V * K; ++i) dw[i] = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) db[v] = 0.0f;
-    const long long segments = (long long)p.B * p.segs;
-    for (long long segment = (long long)block * WARPS + warp; segment < segments; segment += (long long)p.along * WARPS) {
-        k.place(p, (int)segment);
-        const int end = min(k.t0 + p.R, p.L);            // of the gradients that this walk writes
-        const int stop = min(end + K - 1, k.len);        // of the tokens that it reads
-        typename Vec<T, V>::raw nx[UB] = {}, nd[UB] = {}, rx[UB], rd[UB];
-        auto fetch = [&](int t) {
-#pragma unroll
-            for (int i = 0; i < UB; ++i)
-                if (k.in && t + i < stop) {
-                    nx[i] = Vec<T, V>::get(k.row(p, p.x, p.ldx, t + i));
-                    nd[i] = Vec<T, V>::get(k.row(p, p.dy, p.lddy, t + i));
-                }
-        };
-        fetch(k.t0);
-        k.open(p);
-        const int last = p.dpast_out ? k.last_reset(p) : 0;
-        float acc[K][V];                                 // acc[i]: dx of the token i before
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[i][v] = 0.0f;
-        for (int t = k.t0; t < end + K - 1; t += UB) {
-#pragma unroll
-            for (int i = 0; i < UB; ++i) rx[i] = nx[i], rd[i] = nd[i];
-            fetch(t + UB);
-            const unsigned marks = p.reset ? resets<UB>(p, k.b, t, k.len) : 0;
-#pragma unroll
-            for (int i = 0; i < UB; ++i) {
-                float x[V], dp[V];
-                Vec<T, V>::widen(rx[i], x);
-                Vec<T, V>::widen(rd[i], dp);
+            for (int i = 0; i < U; ++i, out += hop) {
+                const M x = k.load(p, stage, t, i, 0, stop, from, ld);
+                M y = k.taps(w, bias, x);
+                if (p.act) y = y * sigmoid(y);
+                if (k.in) Vec<T, V>::store(reinterpret_cast<T *>(out), y.v);
+                k.push(x);
+            }
+            k.age = K;
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < U; ++i, out += hop) {
+                const M x = t + i < stop ? k.load(p, stage, t, i, 0, stop, from, ld) : M::all(0.0f);
                 if (marks >> i & 1) k.fresh();
-                if (p.act) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float s = k.tap(w, bias, x, v), g = sigmoid(s);
-                        dp[v] *= fmaf(s * g, 1.0f - g, g);
-                    }
-                }
-                if (t + i < stop) {
-                    if (t + i < end) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            db[v] += dp[v];
-                            dw[v * K + K - 1] = fmaf(dp[v], x[v], dw[v * K + K - 1]);
-#pragma unroll
-                            for (int j = 0; j < K - 1; ++j) dw[v * K + j] = fmaf(dp[v], k.win[j][v], dw[v * K + j]);
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < K; ++j)
-                        if (k.age >= j) {
-#pragma unroll
-                            for (int v = 0; v < V; ++v) acc[j][v] = fmaf(w[v * K + K - 1 - j], dp[v], acc[j][v]);
-                        }
-                }
-                // the token K - 1 before is whole
-                const int o = t + i - (K - 1), from = o - (k.len - (K - 1));
-                if (k.in && p.dpast_out && from >= 0 && from < K - 1 && last <= o && (o >= k.t0 || k.t0 == 0)) {
-                    float d[V];
-                    Vec<T, V>::load(static_cast<const T *>(p.dpast_out) + ((long long)k.b * (K - 1) + from) * p.C + k.c, d);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) acc[K - 1][v] += d[v];
-                }
-                if (k.in && o >= k.t0 && o < end) Vec<T, V>::store(const_cast<T *>(k.row(p, p.dx, p.lddx, o)), acc[K - 1]);
-                if (k.in && o < 0 && o > -K && p.dpast)
-                    Vec<T, V>::store(static_cast<T *>(p.dpast) + ((long long)k.b * (K - 1) + K - 1 + o) * p.C + k.c, acc[K - 1]);
-#pragma unroll
-                for (int j = K - 1; j > 0; --j)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) acc[j][v] = acc[j - 1][v];
-#pragma unroll
-                for (int v = 0; v < V; ++v) acc[0][v] = 0.0f;
+                M y = k.taps(w, bias, x);
+                if (p.act) y = y * sigmoid(y);
+                if (t + i >= k.len) y = M::all(0.0f);
+                if (k.in && t + i < end) Vec<T, V>::store(reinterpret_cast<T *>(out), y.v);
                 k.push(x);
             }
         }
     }
+}
+
+template <typename T, int V, int K, bool ASYNC>
+__global__ void __launch_bounds__(WARPS * 32, 4) short_conv_bwd_kernel(const ConvArgs p) {
+    using M = Many<V>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x / p.across;
+    constexpr int STAGES = Walk<T, V, K, 2, ASYNC>::STAGES;
+    Walk<T, V, K, 2, ASYNC> k(p, smem);
+    griddep_wait();
+    const void *const from[2] = {p.x, p.dy};
+    const long long ld[2] = {p.ldx, p.lddy};
+    const M none = M::all(0.0f);
+    M w[K], bias, dw[K], db = none;
+    load_taps<V, K>(p, k.c, k.in, w, bias);
+#pragma unroll
+    for (int j = 0; j < K; ++j) dw[j] = none;
+    const long long segments = (long long)p.B * p.segs, hop = p.lddx * (long long)sizeof(T);
+    for (long long segment = (long long)block * WARPS + warp; segment < segments; segment += (long long)p.along * WARPS) {
+        k.place(p, (int)segment);
+        const int end = min(k.t0 + p.R, p.L);            // of the gradients that this walk writes
+        const int stop = min(end + K - 1, k.len);        // of the tokens that it reads
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) k.fetch(p, i, k.t0 + i * U, stop, from, ld);
+        k.open(p);
+        const int last = p.dpast_out ? k.last_reset(p) : 0;
+        M acc[K];                                        // acc[j]: dx of the token j before
+#pragma unroll
+        for (int j = 0; j < K; ++j) acc[j] = none;
+        char *out = reinterpret_cast<char *>(const_cast<T *>(k.row(p, p.dx, p.lddx, k.t0 - (K - 1))));   // stored to from t0 on
+        int stage = 0;
+        for (int t = k.t0; t < end + K - 1; t += U, stage = (stage + 1) % STAGES) {
+            const unsigned marks = p.reset ? resets<U>(p, k.b, t, k.len) : 0;
+            if (ASYNC) {
+                cp_async_wait<STAGES - 2>();
+                __syncwarp();
+                k.fetch(p, (stage + STAGES - 1) % STAGES, t + (STAGES - 1) * U, stop, from, ld);
+            }
+            if (!marks && k.age >= K && t + U <= end && t + U <= k.len && (t > k.t0 || !p.dpast)) {
+#pragma unroll
+                for (int i = 0; i < U; ++i, out += hop) {
+                    const M x = k.load(p, stage, t, i, 0, stop, from, ld);
+                    M dp = k.load(p, stage, t, i, 1, stop, from, ld);
+                    if (p.act) {
+                        const M s = k.taps(w, bias, x), g = sigmoid(s), sg = s * g;
+                        M r;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) r[v] = 1.0f - g[v];
+                        dp = dp * fma(sg, r, g);
+                    }
+                    db = db + dp;
+                    dw[K - 1] = fma(dp, x, dw[K - 1]);
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) dw[j] = fma(dp, k.win[j], dw[j]);
+#pragma unroll
+                    for (int j = 0; j < K; ++j) acc[j] = fma(w[K - 1 - j], dp, acc[j]);
+                    if (k.in && (i >= K - 1 || t > k.t0)) Vec<T, V>::store(reinterpret_cast<T *>(out), acc[K - 1].v);
+#pragma unroll
+                    for (int j = K - 1; j > 0; --j) acc[j] = acc[j - 1];
+                    acc[0] = none;
+                    k.push(x);
+                }
+                continue;
+            }
+#pragma unroll 1
+            for (int i = 0; i < U; ++i, out += hop) {
+                const bool here = t + i < stop;
+                const M x = here ? k.load(p, stage, t, i, 0, stop, from, ld) : none;
+                M dp = here ? k.load(p, stage, t, i, 1, stop, from, ld) : none;
+                if (marks >> i & 1) k.fresh();
+                if (here) {
+                    if (p.act) {
+                        const M s = k.taps(w, bias, x), g = sigmoid(s), sg = s * g;
+                        M r;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) r[v] = 1.0f - g[v];
+                        dp = dp * fma(sg, r, g);
+                    }
+                    if (t + i < end) {
+                        db = db + dp;
+                        dw[K - 1] = fma(dp, x, dw[K - 1]);
+#pragma unroll
+                        for (int j = 0; j < K - 1; ++j) dw[j] = fma(dp, k.win[j], dw[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < K; ++j)
+                        if (k.age >= j) acc[j] = fma(w[K - 1 - j], dp, acc[j]);
+                }
+                // the token K - 1 before is whole
+                const int o = t + i - (K - 1), late = o - (k.len - (K - 1));
+                if (k.in && p.dpast_out && late >= 0 && late < K - 1 && last <= o && (o >= k.t0 || k.t0 == 0)) {
+                    M d;
+                    Vec<T, V>::load(static_cast<const T *>(p.dpast_out) + ((long long)k.b * (K - 1) + late) * p.C + k.c, d.v);
+                    acc[K - 1] = acc[K - 1] + d;
+                }
+                if (k.in && o >= k.t0 && o < end) Vec<T, V>::store(reinterpret_cast<T *>(out), acc[K - 1].v);
+                if (k.in && o < 0 && p.dpast)
+                    Vec<T, V>::store(static_cast<T *>(p.dpast) + ((long long)k.b * (K - 1) + K - 1 + o) * p.C + k.c, acc[K - 1].v);
+#pragma unroll
+                for (int j = K - 1; j > 0; --j) acc[j] = acc[j - 1];
+                acc[0] = none;
+                k.push(x);
+                k.age = min(k.age + 1, K);
+            }
+        }
+    }
+    // the block's sums, in the rings' place
+    float *sums = reinterpret_cast<float *>(smem);       // [WARPS - 1][K + 1][V][32]
+    cp_async_wait<0>();
+    __syncthreads();
     if (warp > 0) {
 #pragma unroll
-        for (int i = 0; i < V * K; ++i) sums[warp - 1][i][lane] = dw[i];
+        for (int j = 0; j <= K; ++j)
 #pragma unroll
-        for (int v = 0; v < V; ++v) sums[warp - 1][V * K + v][lane] = db[v];
+            for (int v = 0; v < V; ++v) sums[(((warp - 1) * (K + 1) + j) * V + v) * 32 + lane] = j < K ? dw[j < K ? j : 0][v] : db[v];
     }
     __syncthreads();
     if (warp == 0 && k.in) {
         float *part = p.part + (long long)block * (K + 1) * p.C + k.c;
 #pragma unroll
         for (int j = 0; j <= K; ++j) {
-            float s[V];
+            M s = j < K ? dw[j < K ? j : 0] : db;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int at = j < K ? v * K + j : V * K + v;
-                s[v] = j < K ? dw[v * K + (j < K ? j : 0)] : db[v];
+            for (int q = 0; q < WARPS - 1; ++q)
 #pragma unroll
-                for (int q = 0; q < WARPS - 1; ++q) s[v] += sums[q][at][lane];
-            }
-            Vec<float, V>::store(part + (long long)j * p.C, s);
+                for (int v = 0; v < V; ++v) s[v] += sums[((q * (K + 1) + j) * V + v) * 32 + lane];
+            Vec<float, V>::store(part + (long long)j * p.C, s.v);
         }
     }
 }
@@ -337,55 +397,73 @@ short_conv_step_kernel(const T *x, const float *w, const float *bias, int act, l
     for (int j = 0; j < K - 1; ++j) old[j] = Vec<T, V>::get(s + (long long)j * C);
     ConvArgs p = {};
     p.w = w, p.bias = bias;
-    float taps[V * K], out[V], r[V];
+    Many<V> taps[K], out, r;
     load_taps<V, K>(p, c, true, taps, out);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-        Vec<T, V>::widen(j < K - 1 ? old[j < K - 1 ? j : 0] : now, r);
-#pragma unroll
-        for (int v = 0; v < V; ++v) out[v] = fmaf(taps[v * K + j], r[v], out[v]);
+        Vec<T, V>::widen(j < K - 1 ? old[j < K - 1 ? j : 0] : now, r.v);
+        out = fma(taps[j], r, out);
     }
-    if (act) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) out[v] *= sigmoid(out[v]);
-    }
-    Vec<T, V>::store(y + i, out);
+    if (act) out = out * sigmoid(out);
+    Vec<T, V>::store(y + i, out.v);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) Vec<T, V>::put(s + (long long)j * C, j < K - 2 ? old[j < K - 2 ? j + 1 : 0] : now);
 }
 
 // ------------------------------------------------------------------ launches
-int vector(int C, std::initializer_list<long long> lds) {
-    int V = C % 4 == 0 ? 4 : C % 2 == 0 ? 2 : 1;
+// Channels of a lane: `most` (four; two where two rings of 32-bit rows would fill the shared memory), two where more
+// taps would fill the registers or the sizes ask for it, or one.
+int vector(int C, int K, int most, std::initializer_list<long long> lds) {
+    int V = K > 4 ? 2 : most;
+    while (C % V) V /= 2;
     for (long long ld : lds)
         while (ld % V) V /= 2;
     return V;
 }
+// Whether 16-byte copies can fetch the rows.
+template <typename T> bool copies(int V, int C, std::initializer_list<long long> lds) {
+    bool ok = V * sizeof(T) >= 4 && C * sizeof(T) % 16 == 0;
+    for (long long ld : lds) ok = ok && ld * sizeof(T) % 16 == 0;
+    return ok;
+}
 
-// Segments as long as there are enough of them for 16 warps an SM.
+// Segments as short as it takes to give every one of the warps that run at once one, from 16 tokens to 256.
 void cut(ConvArgs &p, int V) {
     p.across = (p.C + 32 * V - 1) / (32 * V);
-    for (p.R = 64; p.R > 8; p.R /= 2)
-        if ((long long)p.across * p.B * ((p.L + p.R - 1) / p.R) >= 16 * SMS) break;
+    const long long each = ((long long)p.B * p.L * p.across + BLOCKS * WARPS - 1) / (BLOCKS * WARPS);
+    p.R = each < 16 ? 16 : each > 256 ? 256 : (int)((each + U - 1) / U * U);
     p.segs = (p.L + p.R - 1) / p.R;
 }
 
+template <typename T, int V, int K, bool ASYNC> cudaError_t start_fwd(const ConvArgs &p, int blocks, cudaStream_t st) {
+    return launch_big(short_conv_fwd_kernel<T, V, K, ASYNC>, dim3(blocks), WARPS * 32, WARPS * Walk<T, V, K, 1, ASYNC>::RING, 1, st, p);
+}
 template <typename T, int V, int K> cudaError_t run_fwd(ConvArgs &p, cudaStream_t st) {
     cut(p, V);
     const long long blocks = ((long long)p.B * p.segs + WARPS - 1) / WARPS * p.across;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    return launch(short_conv_fwd_kernel<T, V, K>, dim3((unsigned)blocks), WARPS * 32, 0, 1, st, p);
+    if constexpr (V * sizeof(T) >= 4)
+        if (copies<T>(V, p.C, {p.ldx, p.ldy})) return start_fwd<T, V, K, true>(p, (int)blocks, st);
+    return start_fwd<T, V, K, false>(p, (int)blocks, st);
 }
 
 int along_blocks(long long segments, int across) {
-    const long long all = (segments + WARPS - 1) / WARPS, want = (BWD_BLOCKS + across - 1) / across;
+    const long long all = (segments + WARPS - 1) / WARPS, want = (BLOCKS + across - 1) / across;
     return (int)(all < want ? all : want);
 }
 
+template <typename T, int V, int K, bool ASYNC> cudaError_t start_bwd(const ConvArgs &p, cudaStream_t st) {
+    const size_t ring = WARPS * Walk<T, V, K, 2, ASYNC>::RING, sums = sizeof(float) * (WARPS - 1) * (K + 1) * V * 32;
+    return launch_big(short_conv_bwd_kernel<T, V, K, ASYNC>, dim3(p.along * p.across), WARPS * 32, ring > sums ? ring : sums, 1, st, p);
+}
 template <typename T, int V, int K> cudaError_t run_bwd(ConvArgs &p, float *dw, float *db, cudaStream_t st) {
     cut(p, V);
     p.along = along_blocks((long long)p.B * p.segs, p.across);
-    cudaError_t e = launch(short_conv_bwd_kernel<T, V, K>, dim3((unsigned)(p.along * p.across)), WARPS * 32, 0, 1, st, p);
+    cudaError_t e = cudaSuccess;
+    bool done = false;
+    if constexpr (V * sizeof(T) >= 4)
+        if (copies<T>(V, p.C, {p.ldx, p.lddy, p.lddx})) e = start_bwd<T, V, K, true>(p, st), done = true;
+    if (!done) e = start_bwd<T, V, K, false>(p, st);
     if (e != cudaSuccess) return e;
     return launch(short_conv_weight_kernel, dim3((p.C + 31) / 32, K + 1), 256, 0, 1, st, (const float *)p.part, p.along, K, p.C, dw, db);
 }
@@ -402,22 +480,18 @@ template <typename T, int V, int K> cudaError_t run_step(const StepArgs &a, cuda
                   a.w, a.bias, a.act, total, a.C, static_cast<T *>(a.state), static_cast<T *>(a.y));
 }
 
-// f<V, K>() for the run-time vector and tap counts.
-#define S5_BY_TAPS(f, T, V, taps, ...)                    \
-    switch (taps) {                                       \
-        case 2: return f<T, V, 2>(__VA_ARGS__);           \
-        case 3: return f<T, V, 3>(__VA_ARGS__);           \
-        case 4: return f<T, V, 4>(__VA_ARGS__);           \
-        case 5: return f<T, V, 5>(__VA_ARGS__);           \
-        case 6: return f<T, V, 6>(__VA_ARGS__);           \
-        case 7: return f<T, V, 7>(__VA_ARGS__);           \
-        default: return f<T, V, 8>(__VA_ARGS__);          \
-    }
-#define S5_BY_SIZE(f, T, V, taps, ...)                    \
-    do {                                                  \
-        if (V == 4) { S5_BY_TAPS(f, T, 4, taps, __VA_ARGS__) } \
-        if (V == 2) { S5_BY_TAPS(f, T, 2, taps, __VA_ARGS__) } \
-        S5_BY_TAPS(f, T, 1, taps, __VA_ARGS__)            \
+// f<T, V, K>() for the run-time vector and tap counts.
+#define S5_TAPS(f, T, V, K, ...) \
+    case K: return f<T, V, K>(__VA_ARGS__);
+#define S5_FEW(f, T, V, ...) S5_TAPS(f, T, V, 2, __VA_ARGS__) S5_TAPS(f, T, V, 3, __VA_ARGS__) S5_TAPS(f, T, V, 4, __VA_ARGS__)
+#define S5_MORE(f, T, V, ...) \
+    S5_TAPS(f, T, V, 5, __VA_ARGS__) S5_TAPS(f, T, V, 6, __VA_ARGS__) S5_TAPS(f, T, V, 7, __VA_ARGS__) S5_TAPS(f, T, V, 8, __VA_ARGS__)
+#define S5_BY_SIZE(f, T, V, taps, ...)                                                                        \
+    do {                                                                                                      \
+        if (V == 4) switch (taps) { S5_FEW(f, T, 4, __VA_ARGS__) }                                            \
+        if (V == 2) switch (taps) { S5_FEW(f, T, 2, __VA_ARGS__) S5_MORE(f, T, 2, __VA_ARGS__) }              \
+        switch (taps) { S5_FEW(f, T, 1, __VA_ARGS__) S5_MORE(f, T, 1, __VA_ARGS__) }                          \
+        return cudaErrorInvalidValue;                                                                         \
     } while (0)
 
 template <typename T> cudaError_t fwd(ConvArgs &p, int V, int K, cudaStream_t st) { S5_BY_SIZE(run_fwd, T, V, K, p, st); }
@@ -430,7 +504,7 @@ s5_status check_conv(s5_dtype dtype, const float *w, const float *bias, int act,
     if (!type_ok(dtype) || B < 0 || L < 0 || C < 1 || K < 1) return S5_ERR_INVALID_ARGUMENT;
     if (act != S5_ACT_NONE && act != S5_ACT_SILU) return S5_ERR_INVALID_ARGUMENT;
     if (K < 2 || K > MAX_TAPS) return S5_ERR_UNSUPPORTED;
-    // segments of 8 tokens, and blocks of 32 channels times those of four segments, within an int
+    // segments of 16 tokens or more, and blocks of 32 channels times those of four segments, within an int
     if (L > (1 << 30) || (long long)B * ((L + 7) / 8) > (1ll << 30)) return S5_ERR_UNSUPPORTED;
     if (((long long)B * ((L + 7) / 8) / 4 + 1) * ((C + 31) / 32) > (1ll << 30) || (long long)B * C > (1ll << 36)) return S5_ERR_UNSUPPORTED;
     if (B > 0 && (!w || !aligned(w, 16))) return S5_ERR_INVALID_ARGUMENT;
@@ -463,7 +537,7 @@ extern "C" s5_status s5_short_conv_forward(const void *x, long long ldx, s5_dtyp
     ConvArgs p = {};
     p.x = x, p.ldx = ldx, p.w = weight, p.bias = bias, p.act = activation, p.past = past, p.reset = reset, p.lengths = lengths;
     p.B = B, p.L = L, p.C = C, p.y = y, p.ldy = ldy, p.past_out = past_out;
-    const int V = vector(C, {ldx, ldy});
+    const int V = vector(C, K, 4, {ldx, ldy});
     const cudaError_t e = dtype == S5_BF16 ? fwd<__nv_bfloat16>(p, V, K, st) : fwd<float>(p, V, K, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
@@ -471,7 +545,7 @@ extern "C" s5_status s5_short_conv_forward(const void *x, long long ldx, s5_dtyp
 extern "C" size_t s5_short_conv_workspace_size(int C, int K) {
     if (C < 1 || K < 2 || K > MAX_TAPS) return 0;
     // along_blocks() times C is the most with the widest blocks of channels
-    return 256 + sizeof(float) * (size_t)(K + 1) * C * ((BWD_BLOCKS + (C + 127) / 128 - 1) / ((C + 127) / 128));
+    return 256 + sizeof(float) * (size_t)(K + 1) * C * ((BLOCKS + (C + 127) / 128 - 1) / ((C + 127) / 128));
 }
 
 extern "C" s5_status s5_short_conv_backward(const void *x, long long ldx, s5_dtype dtype, const float *weight, const float *bias,
@@ -498,7 +572,7 @@ extern "C" s5_status s5_short_conv_backward(const void *x, long long ldx, s5_dty
     p.x = x, p.ldx = ldx, p.w = weight, p.bias = bias, p.act = activation, p.past = past, p.reset = reset, p.lengths = lengths;
     p.B = B, p.L = L, p.C = C, p.dy = dy, p.lddy = lddy, p.dpast_out = dpast_out, p.dx = dx, p.lddx = lddx, p.dpast = dpast;
     p.part = static_cast<float *>(workspace);
-    const int V = vector(C, {ldx, lddy, lddx});
+    const int V = vector(C, K, dtype == S5_BF16 ? 4 : 2, {ldx, lddy, lddx});
     const cudaError_t e = dtype == S5_BF16 ? bwd<__nv_bfloat16>(p, V, K, dweight, dbias, st) : bwd<float>(p, V, K, dweight, dbias, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
@@ -512,7 +586,7 @@ extern "C" s5_status s5_short_conv_step(const void *x, s5_dtype dtype, const flo
         if (!q || !aligned(q, 16)) return S5_ERR_INVALID_ARGUMENT;
     const StepArgs a = {x, weight, bias, activation, B, C, state, y};
     // four channels a thread, two where that would leave SMs idle
-    const int V = vector(C, {}) == 4 && (long long)B * C < 4 * 128 * SMS ? 2 : vector(C, {});
+    const int V = vector(C, K, (long long)B * C < 4 * 128 * SMS ? 2 : 4, {});
     const cudaError_t e = dtype == S5_BF16 ? step<__nv_bfloat16>(a, V, K, (cudaStream_t)stream) : step<float>(a, V, K, (cudaStream_t)stream);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
