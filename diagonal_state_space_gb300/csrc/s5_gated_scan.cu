@@ -204,12 +204,15 @@ template <typename Sh> struct Block {
         }
         return r;
     }
-    // Which of this thread's tokens of the tile are resets, a bit each; all lanes of the warp call it.
-    __device__ unsigned marks(const ScanArgs &p, int t0) const {
-        constexpr int MINE = Sh::TILE / (THREADS / 32);
+    // Which of this thread's tokens of the tile are resets, a bit each, in two steps: the load is not waited for, and
+    // all lanes of the warp take part in both.
+    __device__ unsigned char reset_of(const ScanArgs &p, int t0) const {
         const int l = threadIdx.x & 31, t = t0 + threadIdx.x / 32 * MINE + l;
-        const unsigned m = __ballot_sync(0xffffffffu, l < MINE && t < len && p.reset[(long long)b * p.L + t]);
-        return Sh::LANES == 32 ? m : l < 16 ? m & ((1u << S) - 1) : m >> S;
+        return l < MINE && t < len ? p.reset[(long long)b * p.L + t] : 0;
+    }
+    __device__ static unsigned marks(unsigned char reset) {
+        const unsigned m = __ballot_sync(0xffffffffu, reset);
+        return Sh::LANES == 32 ? m : (threadIdx.x & 31) < 16 ? m & ((1u << S) - 1) : m >> S;
     }
     __device__ M rates(const ScanArgs &p) const {
         M r = M::all(0.0f);
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
     }
     if (K > 1) k.open_cluster(p);
     const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
-    if (p.reset) marks = k.marks(p, t0);
+    if (p.reset) marks = k.marks(k.reset_of(p, t0));
     // the thread that folds channel c0 + threadIdx.x over the tile's warps
     const bool folds = threadIdx.x < W && k.c0 + (int)threadIdx.x < p.C;
     const int ch = k.c0 + threadIdx.x;
@@ -336,12 +339,12 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
     if (K > 1) cluster_wait();
 
     for (int round = 0; round < p.rounds; ++round, t0 += K * Sh::TILE) {
-        unsigned ahead = 0;
+        unsigned char ahead = 0;
         if (Sh::ASYNC) {                     // a warp reads the rows that it copied, no other
             cp_async_wait<0>();
             __syncwarp();
         }
-        if (p.reset && round + 1 < p.rounds) ahead = k.marks(p, t0 + K * Sh::TILE);
+        if (p.reset && round + 1 < p.rounds) ahead = k.reset_of(p, t0 + K * Sh::TILE);
         const int mine = t0 + k.group * S;   // this thread's first token
         const bool ragged = t0 + Sh::TILE > k.len;
         const bool slow = ragged || marks;
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
                 if (mine + s < p.L && k.c < p.C) Vec<T, V>::store(reinterpret_cast<T *>(to), o.v);
             }
         }
-        marks = ahead;
+        if (p.reset) marks = k.marks(ahead);
     }
     if (K > 1) cluster_wait();               // no block ends while another may still write to it
     if (k.rank == 0 && folds && p.h_last) p.h_last[(long long)k.b * p.C + ch] = carry;
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
     if (K > 1) k.open_cluster(p);
     const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
     M drate = none;
-    if (p.reset) marks = k.marks(p, t0);
+    if (p.reset) marks = k.marks(k.reset_of(p, t0));
     // threads 0 .. W - 1 fold the adjoints of a channel, the next W its states
     const int col = threadIdx.x % W, ch = k.c0 + col;
     const bool folds = threadIdx.x < W, forward = threadIdx.x / W == 1;
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
 
     for (int round = 0; round < p.rounds; ++round, t0 -= K * Sh::TILE) {
         const int now = round & 1;
-        unsigned ahead = 0;
+        unsigned char ahead = 0;
         if (Sh::ASYNC) {
             cp_async_wait<0>();
             __syncwarp();
@@ -475,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
             }
             cp_async_commit();
         }
-        if (p.reset && round + 1 < p.rounds) ahead = k.marks(p, t0 - K * Sh::TILE);
+        if (p.reset && round + 1 < p.rounds) ahead = k.reset_of(p, t0 - K * Sh::TILE);
         float state = 0.0f;                  // before the tile
         if (forward && ch < p.C && t0 < p.L) state = p.states[((long long)k.b * N + t0 / KEEP) * p.C + ch];
         const int mine = t0 + k.group * S;
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
             to1 -= p.row[0], to2 -= p.row[1];
             if (GATED) to3 -= p.row[2];
         }
-        marks = ahead;
+        if (p.reset) marks = k.marks(ahead);
     }
     if (K > 1) cluster_wait();               // no block ends while another may still write to it
     if (k.rank == 0 && folds && ch < p.C && p.dh0) p.dh0[(long long)k.b * p.C + ch] = carry;

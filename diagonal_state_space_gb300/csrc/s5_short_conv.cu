@@ -26,7 +26,11 @@ using sm100::smem_addr;
 constexpr int WARPS = 4;                 // of a block
 constexpr int U = 8;                     // tokens of a ring's stage, and of one pass of the loop
 constexpr int MAX_TAPS = 8;
-constexpr int BLOCKS = 4 * SMS;          // that run at once; backward a part of the weights' gradient each
+// Blocks that the segments are cut for; backward as many as run at once, a part of the weights' gradient each.
+// Forward six fit an SM, but longer segments for four are no slower and better where resets send some chunks the
+// longer way (4 x 2048 tokens of 4096 channels with resets 25.3 us for four, 27.2 for six; 8 x 1999 of 2048 without
+// 23.4 and 22.6).
+constexpr int BLOCKS = 4 * SMS;
 
 struct ConvArgs {
     const void *x;
@@ -71,6 +75,12 @@ template <int N> __device__ __forceinline__ unsigned resets(const ConvArgs &p, i
     return __ballot_sync(0xffffffffu, lane < N && at >= 0 && at < len && p.reset[(long long)b * p.L + at]);
 }
 
+// The same for the U tokens of a stage in two steps, so that the load is not waited for.
+__device__ __forceinline__ unsigned char reset_of(const ConvArgs &p, int b, int t, int len) {
+    const int at = t + (threadIdx.x & 31);
+    return (threadIdx.x & 31) < U && at < len ? p.reset[(long long)b * p.L + at] : 0;
+}
+
 // What one segment's walk shares in both directions.
 template <typename T, int V, int K, int ARRAYS, bool ASYNC> struct Walk {
     using M = Many<V>;
@@ -101,14 +111,20 @@ template <typename T, int V, int K, int ARRAYS, bool ASYNC> struct Walk {
     __device__ void fetch(const ConvArgs &p, int stage, int t, int stop, const void *const *from, const long long *ld) {
         if constexpr (ASYNC) {
             const int l = threadIdx.x & 31, at = blockIdx.x % p.across * 32 * V + l % CHUNKS * (16 / (int)sizeof(T));
+            const bool wide = (blockIdx.x % p.across + 1) * 32 * V <= p.C;
 #pragma unroll
             for (int k = 0; k < ARRAYS; ++k) {
                 const char *src = reinterpret_cast<const char *>(static_cast<const T *>(from[k]) + ((long long)b * p.L + t + l / CHUNKS) * ld[k] + at);
                 const unsigned dst = smem_addr(ring + ((stage * ARRAYS + k) * U + l / CHUNKS) * ROW + l % CHUNKS * 16);
                 const long long hop = ROWS * ld[k] * (long long)sizeof(T);
+                if (t + U <= stop && wide) {
 #pragma unroll
-                for (int i = 0; i < U / ROWS; ++i, src += hop)
-                    if (at < p.C && t + l / CHUNKS + i * ROWS < stop) cp_async16(dst + i * ROWS * ROW, src);
+                    for (int i = 0; i < U / ROWS; ++i, src += hop) cp_async16(dst + i * ROWS * ROW, src);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < U / ROWS; ++i, src += hop)
+                        if (at < p.C && t + l / CHUNKS + i * ROWS < stop) cp_async16(dst + i * ROWS * ROW, src);
+                }
             }
         }
         cp_async_commit();
@@ -168,7 +184,7 @@ template <typename T, int V, int K, int ARRAYS, bool ASYNC> struct Walk {
 };
 
 template <typename T, int V, int K, bool ASYNC>
-__global__ void __launch_bounds__(WARPS * 32, 4) short_conv_fwd_kernel(const ConvArgs p) {
+__global__ void __launch_bounds__(WARPS * 32, 6) short_conv_fwd_kernel(const ConvArgs p) {
     using M = Many<V>;
     extern __shared__ __align__(128) unsigned char smem[];
     constexpr int STAGES = Walk<T, V, K, 1, ASYNC>::STAGES;
@@ -202,8 +218,10 @@ __global__ void __launch_bounds__(WARPS * 32, 4) short_conv_fwd_kernel(const Con
     char *out = reinterpret_cast<char *>(static_cast<T *>(p.y) + ((long long)k.b * p.L + k.t0) * p.ldy + k.c);
     const long long hop = p.ldy * (long long)sizeof(T);
     int stage = 0;
+    unsigned char ahead = p.reset ? reset_of(p, k.b, k.t0, k.len) : 0;
     for (int t = k.t0; t < end; t += U, stage = (stage + 1) % STAGES) {
-        const unsigned marks = p.reset ? resets<U>(p, k.b, t, k.len) : 0;
+        const unsigned marks = p.reset ? __ballot_sync(0xffffffffu, ahead) : 0;
+        if (p.reset) ahead = reset_of(p, k.b, t + U, k.len);
         if (ASYNC) {
             cp_async_wait<STAGES - 2>();
             __syncwarp();                // the stage is here, and all lanes are done with the one before it
@@ -242,6 +260,7 @@ __global__ void __launch_bounds__(WARPS * 32, 4) short_conv_bwd_kernel(const Con
     constexpr int STAGES = Walk<T, V, K, 2, ASYNC>::STAGES;
     Walk<T, V, K, 2, ASYNC> k(p, smem);
     griddep_wait();
+    griddep_launch_dependents();         // the kernel that sums the parts waits for this one's end
     const void *const from[2] = {p.x, p.dy};
     const long long ld[2] = {p.ldx, p.lddy};
     const M none = M::all(0.0f);
@@ -259,13 +278,15 @@ __global__ void __launch_bounds__(WARPS * 32, 4) short_conv_bwd_kernel(const Con
         for (int i = 0; i < STAGES - 1; ++i) k.fetch(p, i, k.t0 + i * U, stop, from, ld);
         k.open(p);
         const int last = p.dpast_out ? k.last_reset(p) : 0;
-        M acc[K];                                        // acc[j]: dx of the token j before
+        M acc[K];                                        // acc[j]: dx of the token j before the next one, as far as it is; [0] unused
 #pragma unroll
         for (int j = 0; j < K; ++j) acc[j] = none;
         char *out = reinterpret_cast<char *>(const_cast<T *>(k.row(p, p.dx, p.lddx, k.t0 - (K - 1))));   // stored to from t0 on
         int stage = 0;
+        unsigned char ahead = p.reset ? reset_of(p, k.b, k.t0, k.len) : 0;
         for (int t = k.t0; t < end + K - 1; t += U, stage = (stage + 1) % STAGES) {
-            const unsigned marks = p.reset ? resets<U>(p, k.b, t, k.len) : 0;
+            const unsigned marks = p.reset ? __ballot_sync(0xffffffffu, ahead) : 0;
+            if (p.reset) ahead = reset_of(p, k.b, t + U, k.len);
             if (ASYNC) {
                 cp_async_wait<STAGES - 2>();
                 __syncwarp();
@@ -287,18 +308,17 @@ __global__ void __launch_bounds__(WARPS * 32, 4) short_conv_bwd_kernel(const Con
                     dw[K - 1] = fma(dp, x, dw[K - 1]);
 #pragma unroll
                     for (int j = 0; j < K - 1; ++j) dw[j] = fma(dp, k.win[j], dw[j]);
+                    const M whole = fma(w[0], dp, acc[K - 1]);
+                    if (k.in && (i >= K - 1 || t > k.t0)) Vec<T, V>::store(reinterpret_cast<T *>(out), whole.v);
 #pragma unroll
-                    for (int j = 0; j < K; ++j) acc[j] = fma(w[K - 1 - j], dp, acc[j]);
-                    if (k.in && (i >= K - 1 || t > k.t0)) Vec<T, V>::store(reinterpret_cast<T *>(out), acc[K - 1].v);
-#pragma unroll
-                    for (int j = K - 1; j > 0; --j) acc[j] = acc[j - 1];
-                    acc[0] = none;
+                    for (int j = K - 1; j > 1; --j) acc[j] = fma(w[K - j], dp, acc[j - 1]);
+                    acc[1] = w[K - 1] * dp;
                     k.push(x);
                 }
                 continue;
             }
 #pragma unroll 1
-            for (int i = 0; i < U; ++i, out += hop) {
+            for (int i = 0; i < U && t + i < end + K - 1; ++i, out += hop) {
                 const bool here = t + i < stop;
                 const M x = here ? k.load(p, stage, t, i, 0, stop, from, ld) : none;
                 M dp = here ? k.load(p, stage, t, i, 1, stop, from, ld) : none;
@@ -317,9 +337,12 @@ __global__ void __launch_bounds__(WARPS * 32, 4) short_conv_bwd_kernel(const Con
 #pragma unroll
                         for (int j = 0; j < K - 1; ++j) dw[j] = fma(dp, k.win[j], dw[j]);
                     }
+                    acc[0] = w[K - 1] * dp;
 #pragma unroll
-                    for (int j = 0; j < K; ++j)
+                    for (int j = 1; j < K; ++j)
                         if (k.age >= j) acc[j] = fma(w[K - 1 - j], dp, acc[j]);
+                } else {
+                    acc[0] = none;
                 }
                 // the token K - 1 before is whole
                 const int o = t + i - (K - 1), late = o - (k.len - (K - 1));
@@ -333,7 +356,6 @@ __global__ void __launch_bounds__(WARPS * 32, 4) short_conv_bwd_kernel(const Con
                     Vec<T, V>::store(static_cast<T *>(p.dpast) + ((long long)k.b * (K - 1) + K - 1 + o) * p.C + k.c, acc[K - 1].v);
 #pragma unroll
                 for (int j = K - 1; j > 0; --j) acc[j] = acc[j - 1];
-                acc[0] = none;
                 k.push(x);
                 k.age = min(k.age + 1, K);
             }
