@@ -9,19 +9,21 @@
 // Bound: memory.  Forward, a row lies in the registers of one warp, or of as
 // many as it takes, between its loads and its stores: the mean first and then
 // the squares about it, so that a row far from zero keeps its digits.
-// Backward, a row is spread over more lanes, 16 columns each, because a lane
+// Backward, a row is spread over more lanes, 8 columns each, because a lane
 // also keeps the weights' gradients of its columns over all the rows that it
 // sees; one block an SM adds its warps' sums up, and a second launch the
 // blocks'.  No atomics.
 #include "s5_rows.cuh"
+#include "s5_sm100.cuh"
 
 namespace s5 {
 namespace {
 using namespace rows;
 
 constexpr int MAX_H = 16384;
-constexpr int BWD_WARPS = 16;        // of a backward block; rows of more than 8192 take up to 32
-constexpr int BWD_COLS = 16;         // of a lane, backward
+// A backward block: its warps and a lane's columns.  Eight columns leave registers for the next row (bf16 24 warps,
+// f32 16); wider rows take 16 columns a lane, 16 warps, or 32, which spill.
+template <typename T> constexpr int BWD_WARPS = sizeof(T) == 2 ? 24 : 16;
 
 struct NormArgs {
     const void *x, *residual, *dy, *dtotal;
@@ -52,7 +54,7 @@ __device__ __forceinline__ float row_sum(float v, int warps, float *smem) {
 
 // NV vectors of V values a lane.  One warp a row: four rows a block; else a row a block.
 template <typename T, int V, int NV>
-__global__ void __launch_bounds__(V * NV >= 64 ? 256 : V * NV >= 32 ? 512 : 1024) add_layernorm_fwd_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(V * NV >= 32 ? 512 : 1024) add_layernorm_fwd_kernel(const NormArgs p) {
     __shared__ float sums[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row = p.warps == 1 ? (long long)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
@@ -126,72 +128,75 @@ __global__ void __launch_bounds__(V * NV >= 64 ? 256 : V * NV >= 32 ? 512 : 1024
     }
 }
 
-// A block's warps in slots of `warps`, a row each at a time.
-template <typename T, int V, int NV, int MOST>
+// A block's warps in slots of `warps`, a row each at a time; the next row is on its way while a row's warps meet.
+template <typename T, int V, int NV, int MOST, bool AHEAD>
 __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const NormArgs p) {
-    static_assert(V * NV == BWD_COLS, "columns of a lane");
     __shared__ float2 sums[2][MOST];
-    extern __shared__ float shares[];    // [slots - 1][2][H]
+    extern __shared__ __align__(16) float smem[];    // [H] the weight; at the end [slots - 1][2][H] sums
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slots = (int)(blockDim.x >> 5) / p.warps, slot = warp / p.warps, first = slot * p.warps;
     const int at = ((warp - first) * 32 + lane) * V, step = p.warps * 32 * V;
     griddep_wait();
-    float w[NV][V], dw[NV][V], db[NV][V];
+    griddep_launch_dependents();         // the sum of the parts waits for this kernel's end
+    for (int c = threadIdx.x; c < p.H; c += blockDim.x) smem[c] = p.w ? p.w[c] : 1.0f;
+    float dw[NV][V], db[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) w[i][v] = 1.0f, dw[i][v] = 0.0f, db[i][v] = 0.0f;
-        if (p.w && at + i * step < p.H) load_floats<V>(p.w + at + i * step, w[i]);
-    }
+        for (int v = 0; v < V; ++v) dw[i][v] = 0.0f, db[i][v] = 0.0f;
     const long long stride = (long long)gridDim.x * slots;
     const float per = 1.0f / p.H;
-    int turn = 0;
-    for (long long base = (long long)blockIdx.x * slots; base < p.N; base += stride, turn ^= 1) {
-        const long long row = base + slot;
-        const bool here = row < p.N;
-        typename Vec<T, V>::raw rs[NV], rr[NV], rd[NV], rt[NV];
-        float2 stat = make_float2(0.0f, 0.0f);
-        if (here) {
-            const T *s = static_cast<const T *>(p.x) + row * p.ldx, *d = static_cast<const T *>(p.dy) + row * p.lddy;
-            const T *t = static_cast<const T *>(p.dtotal) + row * p.lddt, *r = static_cast<const T *>(p.residual) + row * p.ldr;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (at + i * step < p.H) rs[i] = Vec<T, V>::get(s + at + i * step), rd[i] = Vec<T, V>::get(d + at + i * step);
-            if (p.residual) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (at + i * step < p.H) rr[i] = Vec<T, V>::get(r + at + i * step);
-            }
-            if (p.dtotal) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (at + i * step < p.H) rt[i] = Vec<T, V>::get(t + at + i * step);
-            }
-            stat = p.saved[row];
-        }
-        float n[NV][V], g[NV][V];
-        float2 sum = make_float2(0.0f, 0.0f);
+    using raw = typename Vec<T, V>::raw;
+    raw rs[NV], rr[NV], rd[NV], rt[NV];
+    float2 stat;
+    long long row = (long long)blockIdx.x * slots + slot;
+    auto fetch = [&](long long row) {
+        if (row >= p.N) return;
+        const T *s = static_cast<const T *>(p.x) + row * p.ldx + at, *d = static_cast<const T *>(p.dy) + row * p.lddy + at;
+        const T *t = static_cast<const T *>(p.dtotal) + row * p.lddt + at, *r = static_cast<const T *>(p.residual) + row * p.ldr + at;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float s[V] = {}, d[V] = {};
-            const bool in = here && at + i * step < p.H;
-            if (in) Vec<T, V>::widen(rs[i], s), Vec<T, V>::widen(rd[i], d);
-            if (in && p.residual) {
-                float u[V];
-                Vec<T, V>::widen(rr[i], u);
+            if (at + i * step >= p.H) continue;
+            rs[i] = Vec<T, V>::get(s + i * step);
+            rd[i] = Vec<T, V>::get(d + i * step);
+            if (p.residual) rr[i] = Vec<T, V>::get(r + i * step);
+            if (p.dtotal) rt[i] = Vec<T, V>::get(t + i * step);
+        }
+        stat = p.saved[row];
+    };
+    if (AHEAD) fetch(row);
+    __syncthreads();
+    for (int turn = 0; row < p.N; row += stride, turn ^= 1) {
+        if (!AHEAD) fetch(row);
+        float n[NV][V], g[NV][V];
+        float2 sum = make_float2(0.0f, 0.0f);
+        const float inv = stat.y;
+        raw late[NV];
 #pragma unroll
-                for (int v = 0; v < V; ++v) s[v] += u[v];
+        for (int i = 0; i < NV; ++i) {
+            float s[V] = {}, d[V] = {}, w[V] = {};
+            const bool in = at + i * step < p.H;
+            if (in) {
+                Vec<T, V>::widen(rs[i], s), Vec<T, V>::widen(rd[i], d), load_floats<V>(smem + at + i * step, w);
+                if (p.residual) {
+                    float u[V];
+                    Vec<T, V>::widen(rr[i], u);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) s[v] += u[v];
+                }
             }
+            late[i] = rt[i];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                n[i][v] = in ? (s[v] - stat.x) * stat.y : 0.0f;
-                g[i][v] = d[v] * w[i][v];
+                n[i][v] = in ? (s[v] - stat.x) * inv : 0.0f;
+                g[i][v] = d[v] * w[v];
                 dw[i][v] = fmaf(d[v], n[i][v], dw[i][v]);
                 db[i][v] += d[v];
                 sum.x += g[i][v];
                 sum.y = fmaf(g[i][v], n[i][v], sum.y);
             }
         }
+        if (AHEAD) fetch(row + stride);
 #pragma unroll
         for (int o = 16; o; o /= 2) {
             sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
@@ -199,33 +204,33 @@ __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const Norm
         }
         if (p.warps > 1) {
             if (lane == 0) sums[turn][warp] = sum;
-            __syncthreads();
+            sm100::named_bar_sync(1 + slot, p.warps * 32);
             sum = make_float2(0.0f, 0.0f);
             for (int j = 0; j < p.warps; ++j) sum.x += sums[turn][first + j].x, sum.y += sums[turn][first + j].y;
         }
         sum.x *= per, sum.y *= per;
-        if (!here) continue;
-        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+        T *dx = static_cast<T *>(p.dx) + row * p.lddx + at;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (at + i * step >= p.H) continue;
             float o[V], t[V];
-            if (p.dtotal) Vec<T, V>::widen(rt[i], t);
+            if (p.dtotal) Vec<T, V>::widen(late[i], t);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                o[v] = stat.y * (g[i][v] - sum.x - n[i][v] * sum.y);
+                o[v] = inv * (g[i][v] - sum.x - n[i][v] * sum.y);
                 if (p.dtotal) o[v] += t[v];
             }
-            Vec<T, V>::store(dx + at + i * step, o);
+            Vec<T, V>::store(dx + i * step, o);
         }
     }
     if (!p.part) return;
+    __syncthreads();                     // the weight is read no more
     if (slot > 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (at + i * step < p.H) {
-                store_floats<V>(shares + (long long)(slot - 1) * 2 * p.H + at + i * step, dw[i]);
-                store_floats<V>(shares + (long long)(slot - 1) * 2 * p.H + p.H + at + i * step, db[i]);
+                store_floats<V>(smem + (long long)(slot - 1) * 2 * p.H + at + i * step, dw[i]);
+                store_floats<V>(smem + (long long)(slot - 1) * 2 * p.H + p.H + at + i * step, db[i]);
             }
     }
     __syncthreads();
@@ -237,8 +242,8 @@ __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const Norm
         if (c >= p.H) continue;
         for (int q = 1; q < slots; ++q) {
             float a[V], b[V];
-            load_floats<V>(shares + (long long)(q - 1) * 2 * p.H + c, a);
-            load_floats<V>(shares + (long long)(q - 1) * 2 * p.H + p.H + c, b);
+            load_floats<V>(smem + (long long)(q - 1) * 2 * p.H + c, a);
+            load_floats<V>(smem + (long long)(q - 1) * 2 * p.H + p.H + c, b);
 #pragma unroll
             for (int v = 0; v < V; ++v) dw[i][v] += a[v], db[i][v] += b[v];
         }
@@ -247,23 +252,12 @@ __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const Norm
     }
 }
 
-// The blocks' parts in their order, 8 sums side by side and then joined.  blockIdx.y: dw, db.
-__global__ void __launch_bounds__(256) add_layernorm_weight_kernel(const float *part, int parts, int H, float *dw, float *db) {
-    __shared__ float sums[8][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    float *out = blockIdx.y ? db : dw;
-    griddep_wait();
-    if (!out) return;
-    float s = 0.0f;
-    if (c < H)
-        for (int i = w; i < parts; i += 8) s += part[((long long)i * 2 + blockIdx.y) * H + c];
-    sums[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && c < H) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) s += sums[i][lane];
-        out[c] = s;
-    }
+// The weights' gradients from the blocks' parts [parts][2][H].
+__global__ void __launch_bounds__(SUM_THREADS) add_layernorm_weight_kernel(const float *part, int parts, int H, float *dw, float *db) {
+    sum_parts(part, parts, 2ll * H, [=](long long q, float s) {
+        if (q < H && dw) dw[q] = s;
+        if (q >= H && db) db[q - H] = s;
+    });
 }
 
 // ------------------------------------------------------------------ launches
@@ -273,39 +267,39 @@ template <typename T, int V, int NV> cudaError_t fwd_as(NormArgs &p, cudaStream_
     const int rows = p.warps == 1 ? 4 : 1;
     return launch(add_layernorm_fwd_kernel<T, V, NV>, dim3((unsigned)((p.N + rows - 1) / rows)), 32 * p.warps * rows, 0, 1, st, p);
 }
-// A row in as few warps as a lane's columns allow (64 of 16 bits, 32 of 32) where the rows fill the SMs, else spread over more.
+// A row in as few warps as a lane's columns allow (32 of 16 bits, 16 of 32) where the rows fill the SMs, else spread over more.
+// Twice the columns a lane leave too few warps an SM: 16384 rows of 2048 46.4 us for 42.9, 4099 of 8192 53.6 for 48.2.
 template <typename T, int V> cudaError_t fwd_by(NormArgs &p, cudaStream_t st) {
-    constexpr int MOST = V * sizeof(T) < 16 ? 16 : sizeof(T) == 2 ? 64 : 32;
+    constexpr int MOST = V * sizeof(T) == 16 && sizeof(T) == 2 ? 32 : 16;
     auto warps = [&](int cols) { return (p.H + 32 * cols - 1) / (32 * cols); };
     int cols = MOST;
     while (cols > V && warps(cols / 2) <= 32 && (warps(cols / 2) == 1 || p.N * warps(cols) < 8 * SMS)) cols /= 2;
     if (cols == V) return fwd_as<T, V, 1>(p, st);
     if (cols == 2 * V) return fwd_as<T, V, 2>(p, st);
     if (cols == 4 * V) return fwd_as<T, V, 4>(p, st);
+    if constexpr (MOST >= 8 * V)
+        if (cols == 8 * V) return fwd_as<T, V, 8>(p, st);
     if constexpr (MOST >= 16 * V)
         if (cols == 16 * V) return fwd_as<T, V, 16>(p, st);
-    return fwd_as<T, V, 8>(p, st);
+    return cudaErrorInvalidValue;
 }
 
-int bwd_slots(int H) {
-    const int warps = (H + 32 * BWD_COLS - 1) / (32 * BWD_COLS);
-    return warps >= BWD_WARPS ? 1 : BWD_WARPS / warps;
-}
-int bwd_blocks(long long N, int H) {
-    const long long need = (N + bwd_slots(H) - 1) / bwd_slots(H);
-    return (int)(need < SMS ? need : SMS);
-}
-
-template <typename T, int V> cudaError_t bwd_by(NormArgs &p, float *dw, float *db, cudaStream_t st) {
-    p.warps = (p.H + 32 * BWD_COLS - 1) / (32 * BWD_COLS);
-    const int slots = bwd_slots(p.H), blocks = bwd_blocks(p.N, p.H);
-    const size_t smem = sizeof(float) * (size_t)(slots - 1) * 2 * p.H;
-    const int threads = 32 * p.warps * slots;
-    const cudaError_t e = p.warps <= BWD_WARPS
-                              ? launch_big(add_layernorm_bwd_kernel<T, V, BWD_COLS / V, BWD_WARPS>, dim3(blocks), threads, smem, 1, st, p)
-                              : launch_big(add_layernorm_bwd_kernel<T, V, BWD_COLS / V, 32>, dim3(blocks), threads, smem, 1, st, p);
+template <typename T, int V, int NV, int MOST, bool AHEAD>
+cudaError_t bwd_as(NormArgs &p, float *dw, float *db, cudaStream_t st) {
+    p.warps = (p.H + 32 * V * NV - 1) / (32 * V * NV);
+    const int slots = MOST / p.warps;
+    const long long need = (p.N + slots - 1) / slots;
+    const int blocks = (int)(need < SMS ? need : SMS);
+    const size_t smem = sizeof(float) * (size_t)p.H * (slots > 1 ? (slots - 1) * 2 : 1);
+    const cudaError_t e =
+        launch_big(add_layernorm_bwd_kernel<T, V, NV, MOST, AHEAD>, dim3(blocks), 32 * p.warps * slots, smem, 1, st, p);
     if (e != cudaSuccess || !p.part) return e;
-    return launch(add_layernorm_weight_kernel, dim3((p.H + 31) / 32, 2), 256, 0, 1, st, (const float *)p.part, blocks, p.H, dw, db);
+    return launch(add_layernorm_weight_kernel, dim3((2 * p.H + 31) / 32), sum_threads(blocks), 0, 1, st, (const float *)p.part, blocks, p.H, dw, db);
+}
+template <typename T, int V> cudaError_t bwd_by(NormArgs &p, float *dw, float *db, cudaStream_t st) {
+    if (p.H <= 32 * 8 * BWD_WARPS<T>) return bwd_as<T, V, 8 / V, BWD_WARPS<T>, true>(p, dw, db, st);
+    if (p.H <= 32 * 16 * 16) return bwd_as<T, V, 16 / V, 16, false>(p, dw, db, st);
+    return bwd_as<T, V, 16 / V, 32, false>(p, dw, db, st);
 }
 
 int width(s5_dtype dtype, int H, std::initializer_list<long long> lds) {

@@ -443,6 +443,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
     Block<Sh> k(p, smem);
     const int K = p.cluster, N = (p.L + KEEP - 1) / KEEP;
     griddep_wait();
+    griddep_launch_dependents();             // the sum of the parts waits for this kernel's end
     k.read_length(p);
     const void *const from[4] = {p.x, p.ga, p.dh, GATED ? p.gx : nullptr};
     const long long ld[4] = {p.ldx, p.ldga, p.lddh, p.ldgx};
@@ -626,21 +627,9 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
     }
 }
 
-// drate: the blocks' parts in their order, 8 sums side by side and then joined.
-__global__ void __launch_bounds__(256) gated_scan_rate_kernel(const float *part, int parts, int C, float *drate) {
-    __shared__ float sums[8][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    griddep_wait();
-    float s = 0.0f;
-    if (c < C)
-        for (int i = w; i < parts; i += 8) s += part[(long long)i * C + c];
-    sums[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && c < C) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) s += sums[i][lane];
-        drate[c] = s;
-    }
+// drate from the blocks' parts.
+__global__ void __launch_bounds__(SUM_THREADS) gated_scan_rate_kernel(const float *part, int parts, int C, float *drate) {
+    sum_parts(part, parts, C, [=](long long c, float s) { drate[c] = s; });
 }
 
 // One token: a thread per V channels of a sequence.
@@ -725,7 +714,7 @@ template <typename Sh> cudaError_t run_bwd(ScanArgs &p, float *drate, cudaStream
     else e = p.normalize ? S5_RUN(false, true) : S5_RUN(false, false);
 #undef S5_RUN
     if (e != cudaSuccess || parts == 1) return e;
-    return launch(gated_scan_rate_kernel, dim3((p.C + 31) / 32), 256, 0, 1, st, (const float *)p.drate, parts, p.C, drate);
+    return launch(gated_scan_rate_kernel, dim3((p.C + 31) / 32), sum_threads(parts), 0, 1, st, (const float *)p.drate, parts, p.C, drate);
 }
 
 // 16-byte copies where all rows allow them, else pairs of channels, else single ones.

@@ -180,15 +180,44 @@ cudaError_t launch(void (*k)(Ks...), dim3 grid, int threads, size_t smem, int cl
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
-// The same for a kernel with dynamic shared memory that may pass 48 KB.
+// The same for a kernel whose dynamic shared memory, with its static one, may pass the 48 KB that need no asking.
 template <typename... Ks, typename... As>
 cudaError_t launch_big(void (*k)(Ks...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, As... args) {
     const cudaError_t e =
-        smem > 48 << 10 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
+        smem > 40 << 10 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
     return e != cudaSuccess ? e : launch(k, grid, threads, smem, cluster, st, args...);
 }
 
 constexpr int SMS = 152;
+
+// Sums of `parts` rows of n columns, in a fixed order: a warp's lanes have 32
+// columns, the block's warps (as many as sum_threads says) take turns at the
+// rows, eight loads in flight each.  store(column, sum) takes the result.
+constexpr int SUM_THREADS = 512;
+inline int sum_threads(int parts) { return parts >= 128 ? SUM_THREADS : 32 * ((parts + 7) / 8); }
+template <typename Store> __device__ __forceinline__ void sum_parts(const float *part, int parts, long long n, Store store) {
+    __shared__ float sums[SUM_THREADS / 32][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const long long c = (long long)blockIdx.x * 32 + lane;
+    griddep_wait();
+    float s = 0.0f;
+    for (int i = w; i < parts; i += 8 * warps) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int row = i + j * warps;
+            v[j] = c < n && row < parts ? part[row * n + c] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += v[j];
+    }
+    sums[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < n) {
+        for (int i = 1; i < warps; ++i) s += sums[i][lane];
+        store(c, s);
+    }
+}
 
 }  // namespace rows
 }  // namespace s5

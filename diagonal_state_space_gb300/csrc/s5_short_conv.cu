@@ -386,22 +386,13 @@ __global__ void __launch_bounds__(WARPS * 32, 4) short_conv_bwd_kernel(const Con
     }
 }
 
-// The parts in their order, 8 sums side by side and then joined.  blockIdx.y: the tap, or K for the bias.
-__global__ void __launch_bounds__(256) short_conv_weight_kernel(const float *part, int parts, int K, int C, float *dw, float *db) {
-    __shared__ float sums[8][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, j = blockIdx.y;
-    griddep_wait();
-    float s = 0.0f;
-    if (c < C)
-        for (int i = w; i < parts; i += 8) s += part[((long long)i * (K + 1) + j) * C + c];
-    sums[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && c < C) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) s += sums[i][lane];
+// The weights' gradients from the blocks' parts [parts][K + 1][C]: the taps, then the bias.
+__global__ void __launch_bounds__(SUM_THREADS) short_conv_weight_kernel(const float *part, int parts, int K, int C, float *dw, float *db) {
+    sum_parts(part, parts, (long long)(K + 1) * C, [=](long long q, float s) {
+        const int j = (int)(q / C), c = (int)(q % C);
         if (j < K) dw[(long long)c * K + j] = s;
         else if (db) db[c] = s;
-    }
+    });
 }
 
 // One token: a thread per V channels of a sequence.
@@ -487,7 +478,7 @@ template <typename T, int V, int K> cudaError_t run_bwd(ConvArgs &p, float *dw, 
         if (copies<T>(V, p.C, {p.ldx, p.lddy, p.lddx})) e = start_bwd<T, V, K, true>(p, st), done = true;
     if (!done) e = start_bwd<T, V, K, false>(p, st);
     if (e != cudaSuccess) return e;
-    return launch(short_conv_weight_kernel, dim3((p.C + 31) / 32, K + 1), 256, 0, 1, st, (const float *)p.part, p.along, K, p.C, dw, db);
+    return launch(short_conv_weight_kernel, dim3((unsigned)(((long long)(K + 1) * p.C + 31) / 32)), sum_threads(p.along), 0, 1, st, (const float *)p.part, p.along, K, p.C, dw, db);
 }
 
 struct StepArgs {
