@@ -560,7 +560,7 @@ def s5_qk_norm_rotary_backward(q, k, dq_out, dk_out, positions, freq, norm="rms"
 # Gated linear recurrence, short causal convolution, layer norm of a sum.  Rows
 # may be views with a pitch between tokens; a token's channels are contiguous.
 # reset [B,L] (bool or uint8): the tokens that begin a new sequence.  lengths
-# [B] int32: tokens of each row; what lies behind is not read, and is zero in
+# [B] int32: tokens of each row; what lies behind has no effect, and is zero in
 # what comes back.
 # ---------------------------------------------------------------------------
 _MARKS = (torch.bool, torch.uint8)

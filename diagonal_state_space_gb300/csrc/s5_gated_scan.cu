@@ -26,6 +26,9 @@
 //
 // 1 - a and 1 - a^2 come from m = exp(la) - 1, a short series where a is near
 // one: a channel that forgets over thousands of tokens keeps the digits of both.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "s5_rows.cuh"
 #include "s5_sm100.cuh"
 
@@ -37,6 +40,7 @@ using sm100::smem_addr;
 constexpr int THREADS = 128;    // four blocks an SM
 constexpr int KEEP = 32;        // tokens between two kept states, and of a tile backward (twice that forward)
 constexpr int MAX_CLUSTER = 16; // beyond 8 a non-portable size
+constexpr int FETCHER = THREADS - 32;    // the thread that starts the copies: of a warp that folds nothing
 
 struct ScanArgs {
     const void *x, *ga, *gx;            // gx null: u = x
@@ -60,8 +64,7 @@ struct ScanArgs {
     float *drate;                       // [parts][C]
     float *dh0;                         // or null
     int cluster, rounds;                // tiles at once, and how often
-    // by place(): in bytes, the rows of one copy of the warp (inputs), one row (outputs), a round's tiles (both)
-    long long hop[4], step[4], row[3], out_step;
+    long long row[3], out_step;         // bytes between two rows of the outputs, and (forward) a round's tiles
 };
 
 // A run that holds a reset has A = 0 and takes nothing over, not even NaN: zeros stay zeros whatever they are joined
@@ -113,17 +116,22 @@ __device__ __noinline__ void wait_long(uint64_t *bar, unsigned parity) {
         }
 }
 
+// The inputs as [B][L][C] in boxes of a tile: x, gate_a, then gate_x (forward) or dh and gate_x.
+struct ScanMaps {
+    CUtensorMap map[4];
+};
+
 // How a block's threads share a tile: LANES threads side by side hold V
 // channels each, and GROUPS such rows S consecutive tokens each.
 template <typename T_, int V_, int LANES_, int S_, int ARRAYS_, bool ASYNC_> struct Shape {
     using T = T_;
     static constexpr int V = V_, LANES = LANES_, S = S_, ARRAYS = ARRAYS_;
-    static constexpr bool ASYNC = ASYNC_;                     // tiles come by 16-byte copies
+    static constexpr bool ASYNC = ASYNC_;                     // tiles come by TMA
     static constexpr int GROUPS = THREADS / LANES, WARPS = THREADS / 32, WIDE = LANES * V, TILE = GROUPS * S;
     static constexpr int STAGE = ASYNC ? ARRAYS * TILE * WIDE * (int)sizeof(T) : 0;
     static constexpr int PAIRS = MAX_CLUSTER * WIDE;          // of a round
     static constexpr int STAGES = ARRAYS == 4 ? 2 : 1;        // backward a tile is read twice
-    static constexpr int SMEM = STAGES * STAGE + 2 * PAIRS * (int)sizeof(float2) + 16 + (ARRAYS == 4 ? 4 : 3) * WARPS * WIDE * (int)sizeof(float);
+    static constexpr int SMEM = STAGES * STAGE + 2 * PAIRS * (int)sizeof(float2) + 32 + (ARRAYS == 4 ? 4 : 3) * WARPS * WIDE * (int)sizeof(float);
     static_assert(TILE == KEEP || TILE == 2 * KEEP, "kept states lie at a group's start");
     static_assert(LANES * 2 == 32 || LANES == 32, "a warp holds one or two groups");
 };
@@ -137,6 +145,7 @@ template <typename Sh> struct Block {
     float2 *pairs;      // [2][MAX_CLUSTER][WIDE]
     float *A, *E, *H, *Z;   // [WARPS][WIDE]: a warp's pairs, what enters it, and backward its adjoints' pairs
     uint64_t *bar;      // [2], one for each half of the pairs
+    uint64_t *full;     // [STAGES]
     int b, c0, rank, lane, group, c;
     bool upper;         // the later of a warp's two groups
     int len;            // tokens of this sequence
@@ -147,7 +156,8 @@ template <typename Sh> struct Block {
         E = A + Sh::WARPS * W;
         H = E + Sh::WARPS * W;
         Z = H + Sh::WARPS * W;
-        bar = reinterpret_cast<uint64_t *>(smem + Sh::SMEM - 16);
+        bar = reinterpret_cast<uint64_t *>(smem + Sh::SMEM - 32);
+        full = bar + 2;
         const int K = p.cluster, across = (p.C + W - 1) / W;
         rank = blockIdx.x % K;
         const int chain = blockIdx.x / K;
@@ -159,39 +169,22 @@ template <typename Sh> struct Block {
         upper = Sh::LANES == 32 || (threadIdx.x & 16);
     }
     __device__ void read_length(const ScanArgs &p) { len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L; }
-    // Where this thread's 16 bytes of the tile at t0 begin in each input.
-    static constexpr int PER = 16 / (int)sizeof(T), CHUNKS = W / PER, ROWS = 32 / CHUNKS, MINE = Sh::TILE / Sh::WARPS;
-    __device__ int first_row() const { return threadIdx.x / 32 * MINE + (threadIdx.x & 31) / CHUNKS; }
-    __device__ int first_value() const { return (threadIdx.x & 31) % CHUNKS * PER; }
-    __device__ void aim(const ScanArgs &p, int t0, const void *const *from, const long long *ld, const char **src) const {
+    static constexpr int MINE = Sh::TILE / Sh::WARPS;      // tokens of a warp
+    // One thread: the tile at t0 of N arrays into a stage; what lies past the channels or the row's L tokens is zeros.
+    template <int N> __device__ void fetch(const ScanMaps &maps, int which, int t0) const {
+        sm100::mbar_arrive_tx(full + which, N * Sh::TILE * W * (unsigned)sizeof(T));
 #pragma unroll
-        for (int k = 0; k < Sh::ARRAYS; ++k)
-            src[k] = from[k] ? reinterpret_cast<const char *>(static_cast<const T *>(from[k]) + ((long long)b * p.L + t0 + first_row()) * ld[k] +
-                                                              c0 + first_value())
-                             : nullptr;
+        for (int k = 0; k < N; ++k) sm100::tma_load_3d(stage + (which * Sh::ARRAYS + k) * Sh::TILE * W, &maps.map[k], c0, t0, b, full + which);
     }
-    // Copies of this warp's rows of the tile at t0 into a stage, zeros where there is nothing to read.
-    __device__ void fetch(const ScanArgs &p, int which, int t0, const void *const *from, const char *const *src) const {
-        const unsigned dst = smem_addr(stage + (which * Sh::ARRAYS * Sh::TILE + first_row()) * W + first_value());
-        if (t0 + Sh::TILE <= len && c0 + W <= p.C) {
-#pragma unroll
-            for (int k = 0; k < Sh::ARRAYS; ++k) {
-                if (!from[k]) continue;
-                const char *at = src[k];
-#pragma unroll
-                for (int i = 0; i < MINE / ROWS; ++i, at += p.hop[k]) cp_async16(dst + (k * Sh::TILE + i * ROWS) * W * (int)sizeof(T), at);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < Sh::ARRAYS; ++k) {
-                if (!from[k]) continue;
-#pragma unroll
-                for (int i = 0; i < MINE / ROWS; ++i) {
-                    const bool there = t0 + first_row() + i * ROWS < len && c0 + first_value() < p.C;
-                    cp_async16(dst + (k * Sh::TILE + i * ROWS) * W * (int)sizeof(T), there ? src[k] + i * p.hop[k] : from[k], there);
-                }
-            }
+    __device__ void arrived(int which, unsigned phase) const {
+        if (!sm100::mbar_try_wait(full + which, phase)) wait_long(full + which, phase);
+    }
+    __device__ void open_copies() const {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < Sh::STAGES; ++i) sm100::mbar_init(full + i, 1);
+            sm100::fence_mbar_init();
         }
+        __syncthreads();
     }
     // V values of array k at this thread's token s of the tile.
     __device__ M load(const ScanArgs &p, int which, int t0, int s, int k, const void *const *from, const long long *ld) const {
@@ -306,25 +299,21 @@ template <typename Sh> struct Block {
 };
 
 template <typename Sh, bool GATED, bool NORM>
-__global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanArgs p) {
+__global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanArgs p, const __grid_constant__ ScanMaps maps) {
     using T = typename Sh::T;
     using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
     extern __shared__ __align__(128) unsigned char smem[];
     Block<Sh> k(p, smem);
     const int K = p.cluster;
+    if (Sh::ASYNC) k.open_copies();
     griddep_wait();
     k.read_length(p);
     const void *const from[3] = {p.x, p.ga, GATED ? p.gx : nullptr};
     const long long ld[3] = {p.ldx, p.ldga, p.ldgx};
     int t0 = k.rank * Sh::TILE;
     unsigned marks = 0;
-    const char *src[3];
-    if (Sh::ASYNC) {
-        k.aim(p, t0, from, ld, src);
-        k.fetch(p, 0, t0, from, src);
-        cp_async_commit();
-    }
+    if (Sh::ASYNC && threadIdx.x == FETCHER) k.template fetch<GATED ? 3 : 2>(maps, 0, t0);
     if (K > 1) k.open_cluster(p);
     const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
     if (p.reset) marks = k.marks(k.reset_of(p, t0));
@@ -340,10 +329,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
 
     for (int round = 0; round < p.rounds; ++round, t0 += K * Sh::TILE) {
         unsigned char ahead = 0;
-        if (Sh::ASYNC) {                     // a warp reads the rows that it copied, no other
-            cp_async_wait<0>();
-            __syncwarp();
-        }
+        if (Sh::ASYNC) k.arrived(0, round & 1);
         if (p.reset && round + 1 < p.rounds) ahead = k.reset_of(p, t0 + K * Sh::TILE);
         const int mine = t0 + k.group * S;   // this thread's first token
         const bool ragged = t0 + Sh::TILE > k.len;
@@ -376,15 +362,6 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
                 A = k.joined(A, a[s]);
             }
         }
-        if (Sh::ASYNC) {                     // the next tile is on its way while the pairs meet
-            __syncwarp();
-            if (round + 1 < p.rounds) {
-#pragma unroll
-                for (int i = 0; i < 3; ++i) src[i] += p.step[i];
-                k.fetch(p, 0, t0 + K * Sh::TILE, from, src);
-            }
-            cp_async_commit();
-        }
         M pA = one, pE = none;               // of the warp's earlier group, for the later one
         if (Sh::LANES == 16) {
             pA = k.other(A), pE = k.other(E);
@@ -396,6 +373,8 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
             k.put(k.E, E);
         }
         __syncthreads();
+        // the stage is read: the next tile is on its way while the pairs meet
+        if (Sh::ASYNC && threadIdx.x == FETCHER && round + 1 < p.rounds) k.template fetch<GATED ? 3 : 2>(maps, 0, t0 + K * Sh::TILE);
         float before = K > 1 ? k.template exchange<false>(p, round, k.E, carry) : carry;
         if (K > 1 && round + 1 == p.rounds) cluster_arrive();
         if (threadIdx.x < W) {               // the state before each warp's tokens
@@ -435,13 +414,14 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
 }
 
 template <typename Sh, bool GATED, bool NORM>
-__global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanArgs p) {
+__global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanArgs p, const __grid_constant__ ScanMaps maps) {
     using T = typename Sh::T;
     using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
     extern __shared__ __align__(128) unsigned char smem[];
     Block<Sh> k(p, smem);
     const int K = p.cluster, N = (p.L + KEEP - 1) / KEEP;
+    if (Sh::ASYNC) k.open_copies();
     griddep_wait();
     griddep_launch_dependents();             // the sum of the parts waits for this kernel's end
     k.read_length(p);
@@ -449,12 +429,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
     const long long ld[4] = {p.ldx, p.ldga, p.lddh, p.ldgx};
     int t0 = ((p.rounds - 1) * K + k.rank) * Sh::TILE;   // from the last tiles to the first
     unsigned marks = 0;
-    if (Sh::ASYNC) {
-        const char *src[4];
-        k.aim(p, t0, from, ld, src);
-        k.fetch(p, 0, t0, from, src);
-        cp_async_commit();
-    }
+    if (Sh::ASYNC && threadIdx.x == FETCHER) k.template fetch<GATED ? 4 : 3>(maps, 0, t0);
     if (K > 1) k.open_cluster(p);
     const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
     M drate = none;
@@ -469,16 +444,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
     for (int round = 0; round < p.rounds; ++round, t0 -= K * Sh::TILE) {
         const int now = round & 1;
         unsigned char ahead = 0;
-        if (Sh::ASYNC) {
-            cp_async_wait<0>();
-            __syncwarp();
-            if (round + 1 < p.rounds) {
-                const char *src[4];          // worked out anew: kept, they would cost spills
-                k.aim(p, t0 - K * Sh::TILE, from, ld, src);
-                k.fetch(p, 1 - now, t0 - K * Sh::TILE, from, src);
-            }
-            cp_async_commit();
-        }
+        if (Sh::ASYNC) k.arrived(now, round >> 1 & 1);
         if (p.reset && round + 1 < p.rounds) ahead = k.reset_of(p, t0 - K * Sh::TILE);
         float state = 0.0f;                  // before the tile
         if (forward && ch < p.C && t0 < p.L) state = p.states[((long long)k.b * N + t0 / KEEP) * p.C + ch];
@@ -516,13 +482,14 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 if (marks >> s & 1) a[s] = none, ns[s] = GATED ? g[s] : one;
-                if (mine + s >= k.len) a[s] = one, ns[s] = none;
-                E = k.applied(a[s], E, ns[s] * k.load(p, now, t0, s, 0, from, ld));
+                const bool behind = mine + s >= k.len;
+                if (behind) a[s] = one, ns[s] = none;
+                E = k.applied(a[s], E, behind ? none : ns[s] * k.load(p, now, t0, s, 0, from, ld));
                 A = k.joined(A, a[s]);
             }
 #pragma unroll
             for (int s = S - 1; s >= 0; --s) {
-                Z = a[s] * (k.load(p, now, t0, s, 2, from, ld) + Z);
+                if (mine + s < k.len) Z = a[s] * (k.load(p, now, t0, s, 2, from, ld) + Z);
                 if (marks >> s & 1) Z = none;
             }
         }
@@ -539,6 +506,8 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
         }
         if (Sh::LANES == 32 || !k.upper) k.put(k.Z, Z);
         __syncthreads();
+        // the other stage is read
+        if (Sh::ASYNC && threadIdx.x == FETCHER && round + 1 < p.rounds) k.template fetch<GATED ? 4 : 3>(maps, 1 - now, t0 - K * Sh::TILE);
         float after = carry;
         if (K > 1) after = k.template exchange<true>(p, round, k.Z, carry);
         if (K > 1 && round + 1 == p.rounds) cluster_arrive();
@@ -577,7 +546,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
         } else {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                const M e = ns[s] * k.load(p, now, t0, s, 0, from, ld);
+                const M e = mine + s < k.len ? ns[s] * k.load(p, now, t0, s, 0, from, ld) : none;
                 const bool dead = (marks >> s & 1) || mine + s >= k.len;
 #pragma unroll
                 for (int v = 0; v < V; ++v) D[s][v] = dead ? 0.0f : fmaf(a[s][v], h[v], -D[s][v]);
@@ -590,7 +559,8 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
         char *to3 = GATED ? reinterpret_cast<char *>(static_cast<T *>(p.dgx) + last * p.lddgx + k.c) : nullptr;
 #pragma unroll
         for (int s = S - 1; s >= 0; --s) {
-            const M G = k.load(p, now, t0, s, 2, from, ld) + z;
+            const bool behind = slow && mine + s >= k.len;
+            const M G = behind ? z : k.load(p, now, t0, s, 2, from, ld) + z;
             const M t = G * D[s] * r[s], o1 = G * ns[s], w = rate * t;   // t: dla r
             M o2, o3;
 #pragma unroll
@@ -598,7 +568,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
             z = a[s] * G;
             if (slow && (marks >> s & 1)) z = none;
             if (GATED) {
-                const M q = o1 * k.load(p, now, t0, s, 0, from, ld);
+                const M q = behind ? none : o1 * k.load(p, now, t0, s, 0, from, ld);
 #pragma unroll
                 for (int v = 0; v < V; ++v) o3[v] = fmaf(q[v], -g[s][v], q[v]);
             }
@@ -678,26 +648,55 @@ template <typename Sh> cudaError_t place(ScanArgs &p, long long &blocks) {
     blocks = chains * p.cluster;
     const long long bytes = sizeof(typename Sh::T), round = bytes * p.cluster * Sh::TILE;
     const bool back = Sh::ARRAYS == 4;
-    const long long in[4] = {p.ldx, p.ldga, back ? p.lddh : p.ldgx, p.ldgx}, out[3] = {back ? p.lddx : p.ldh, p.lddga, p.lddgx};
-    for (int i = 0; i < 4; ++i) p.hop[i] = bytes * Block<Sh>::ROWS * in[i], p.step[i] = round * in[i];
+    const long long out[3] = {back ? p.lddx : p.ldh, p.lddga, p.lddgx};
     for (int i = 0; i < 3; ++i) p.row[i] = bytes * out[i];
     p.out_step = round * out[0];
     return blocks > 0x7fffffffll ? cudaErrorInvalidValue : cudaSuccess;
 }
 
-template <typename... Ks> cudaError_t launch_scan(void (*k)(Ks...), const ScanArgs &p, long long blocks, size_t smem, cudaStream_t st) {
+// Rows [B][L][C] of one array in boxes of `tokens` tokens of 128 bytes.
+cudaError_t encode(CUtensorMap *m, bool f32, const void *base, long long ld, const ScanArgs &p, int tokens) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return cudaErrorNotSupported;
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }
+    const cuuint64_t e = f32 ? 4 : 2, dims[3] = {(cuuint64_t)p.C, (cuuint64_t)p.L, (cuuint64_t)p.B};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * e, (cuuint64_t)ld * e * p.L};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / e), (cuuint32_t)tokens, 1}, es[3] = {1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+template <typename Sh, typename... Ks> cudaError_t launch_scan(void (*k)(Ks...), const ScanArgs &p, long long blocks, cudaStream_t st) {
+    ScanMaps maps = {};
+    if constexpr (Sh::ASYNC) {
+        const bool f32 = sizeof(typename Sh::T) == 4;
+        cudaError_t e = encode(&maps.map[0], f32, p.x, p.ldx, p, Sh::TILE);
+        if (e == cudaSuccess) e = encode(&maps.map[1], f32, p.ga, p.ldga, p, Sh::TILE);
+        if (Sh::ARRAYS == 4 && e == cudaSuccess) e = encode(&maps.map[2], f32, p.dh, p.lddh, p, Sh::TILE);
+        if (p.gx && e == cudaSuccess) e = encode(&maps.map[Sh::ARRAYS - 1], f32, p.gx, p.ldgx, p, Sh::TILE);
+        if (e != cudaSuccess) return e;
+    }
     if (p.cluster > 8) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
-    return launch_big(k, dim3((unsigned)blocks), THREADS, smem, p.cluster, st, p);
+    return launch_big(k, dim3((unsigned)blocks), THREADS, Sh::SMEM, p.cluster, st, p, maps);
 }
 
 template <typename Sh> cudaError_t run_fwd(ScanArgs &p, cudaStream_t st) {
     long long blocks;
     const cudaError_t e = place<Sh>(p, blocks);
     if (e != cudaSuccess) return e;
-#define S5_RUN(GATED, NORM) launch_scan(gated_scan_fwd_kernel<Sh, GATED, NORM>, p, blocks, Sh::SMEM, st)
+#define S5_RUN(GATED, NORM) launch_scan<Sh>(gated_scan_fwd_kernel<Sh, GATED, NORM>, p, blocks, st)
     if (p.gx) return p.normalize ? S5_RUN(true, true) : S5_RUN(true, false);
     return p.normalize ? S5_RUN(false, true) : S5_RUN(false, false);
 #undef S5_RUN
@@ -709,7 +708,7 @@ template <typename Sh> cudaError_t run_bwd(ScanArgs &p, float *drate, cudaStream
     if (e != cudaSuccess) return e;
     const int parts = p.B * p.cluster;
     if (parts == 1) p.drate = drate;
-#define S5_RUN(GATED, NORM) launch_scan(gated_scan_bwd_kernel<Sh, GATED, NORM>, p, blocks, Sh::SMEM, st)
+#define S5_RUN(GATED, NORM) launch_scan<Sh>(gated_scan_bwd_kernel<Sh, GATED, NORM>, p, blocks, st)
     if (p.gx) e = p.normalize ? S5_RUN(true, true) : S5_RUN(true, false);
     else e = p.normalize ? S5_RUN(false, true) : S5_RUN(false, false);
 #undef S5_RUN
@@ -717,11 +716,12 @@ template <typename Sh> cudaError_t run_bwd(ScanArgs &p, float *drate, cudaStream
     return launch(gated_scan_rate_kernel, dim3((p.C + 31) / 32), sum_threads(parts), 0, 1, st, (const float *)p.drate, parts, p.C, drate);
 }
 
-// 16-byte copies where all rows allow them, else pairs of channels, else single ones.
-int width(s5_dtype dtype, int C, std::initializer_list<long long> lds) {
+// TMA where all rows allow it (starts and pitches of 16 bytes, a batch below 2^40 bytes), else pairs of channels, else
+// single ones.
+int width(s5_dtype dtype, int L, int C, std::initializer_list<long long> lds) {
     const int per = dtype == S5_BF16 ? 8 : 4;
     int w = C % per == 0 ? per : C % 2 == 0 ? 2 : 1;
-    for (long long ld : lds) w = ld % per == 0 ? w : ld % 2 == 0 && w > 1 ? 2 : 1;
+    for (long long ld : lds) w = ld % per == 0 && ld < (1ll << 37) / L ? w : ld % 2 == 0 && w > 1 ? 2 : 1;
     return w;
 }
 
@@ -783,7 +783,7 @@ extern "C" s5_status s5_gated_scan_forward(const void *x, long long ldx, const v
     if (c != S5_OK) return c;
     if (!rows_ok(h, ldh, C)) return S5_ERR_INVALID_ARGUMENT;
     p.states = static_cast<float *>(saved);
-    const int w = width(dtype, C, {ldx, ldga, p.ldgx, ldh});
+    const int w = width(dtype, L, C, {ldx, ldga, p.ldgx, ldh});
     cudaError_t e;
     if (dtype == S5_BF16)
         e = w == 8   ? run_fwd<Shape<__nv_bfloat16, 4, 16, 8, 3, true>>(p, st)
@@ -827,7 +827,7 @@ extern "C" s5_status s5_gated_scan_backward(const void *x, long long ldx, const 
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < s5_gated_scan_workspace_size(B, L, C)) return S5_ERR_INVALID_ARGUMENT;
     p.states = static_cast<float *>(const_cast<void *>(saved));
     p.drate = static_cast<float *>(workspace);
-    const int w = width(dtype, C, {ldx, ldga, p.ldgx, lddh, lddx, lddga, p.lddgx});
+    const int w = width(dtype, L, C, {ldx, ldga, p.ldgx, lddh, lddx, lddga, p.lddgx});
     cudaError_t e;
     if (dtype == S5_BF16)
         e = w == 8   ? run_bwd<Shape<__nv_bfloat16, 4, 16, 4, 4, true>>(p, drate, st)

@@ -503,7 +503,7 @@ s5_status s5_qk_norm_rotary_backward(const void *q, long long ldq, const void *k
  *   reset [B][L], or NULL: a token whose byte is not 0 begins a new sequence;
  *     nothing of the tokens before it, NaN included, reaches it.
  *   lengths [B], or NULL: tokens of each row (taken into 0 .. L).  What lies
- *     behind is not read, and outputs and gradients there are zeros.
+ *     behind has no effect, and outputs and gradients there are zeros.
  * Outputs do not overlap inputs or each other but where a call says so.  All
  * arithmetic in 32 bits, one rounding at the end.  No atomics: equal inputs
  * give equal bits.  Asynchronous, launched with programmatic stream
