@@ -606,6 +606,9 @@ def _need(n, what):
 
 def new_gated_scan_saved(x) -> torch.Tensor:
     """The buffer that s5_gated_scan_forward fills for s5_gated_scan_backward."""
+    out = _native.marshal().gated_scan_saved(x)
+    if out is not None:
+        return out
     B, L, C = _channels(x, "x", 3)
     return torch.empty(_need(s5_gated_scan_saved_size(B, L, C), "new_gated_scan_saved"), dtype=torch.uint8, device=x.device)
 
@@ -787,7 +790,8 @@ def _norm_rows(x, name):
 
 def new_layernorm_saved(x) -> torch.Tensor:
     """What s5_add_layernorm fills for s5_add_layernorm_backward: mean and 1 / sqrt(var + eps) of each row."""
-    return torch.empty(_norm_rows(x, "x")[0], 2, dtype=torch.float32, device=x.device)
+    out = _native.marshal().layernorm_saved(x)
+    return torch.empty(_norm_rows(x, "x")[0], 2, dtype=torch.float32, device=x.device) if out is None else out
 
 
 def s5_add_layernorm(x, weight=None, bias=None, residual=None, eps=1e-5, y=None, total=None, saved=None, stream=None):

@@ -12,7 +12,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -78,8 +79,12 @@ struct Reader {
 };
 
 s5_dtype dtype(const Tensor &t) { return t.scalar_type() == BF16 ? S5_BF16 : S5_F32; }
-Tensor make(at::IntArrayRef shape, const Tensor &like) { return at::empty(shape, like.options()); }
-Tensor make(at::IntArrayRef shape, const Tensor &like, at::ScalarType type) { return at::empty(shape, like.options().dtype(type)); }
+// On the current CUDA device, which is `like`'s (Reader): what at::empty does, without its way there.
+Tensor make(at::IntArrayRef shape, const Tensor &, at::ScalarType type) {
+    return Tensor(at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA), type,
+                                            std::nullopt));
+}
+Tensor make(at::IntArrayRef shape, const Tensor &like) { return make(shape, like, like.scalar_type()); }
 template <typename T = float> T *data(const Tensor *t) { return t ? static_cast<T *>(t->data_ptr()) : nullptr; }
 bool fits(std::initializer_list<int64_t> sizes) {
     for (int64_t n : sizes)
@@ -324,6 +329,20 @@ const Tensor *channels(Reader &r, int i, int dims) {
 Tensor given_or(const Tensor *t, const Tensor &like) { return t ? *t : make(like.sizes(), like); }
 template <typename T = float> T *at_or_null(const Tensor &t) { return t.defined() ? data<T>(&t) : nullptr; }
 
+// x: the buffer that the forward call fills
+ENTRY(gated_scan_saved, 1) {
+    const Tensor *x = channels(r, 0, 3);
+    if (!r.ok || !fits({x->size(0), x->size(1), x->size(2)})) Py_RETURN_NONE;
+    const size_t n = s5_gated_scan_saved_size((int)x->size(0), (int)x->size(1), (int)x->size(2));
+    if (n == 0) Py_RETURN_NONE;
+    return THPVariable_Wrap(make({(int64_t)n}, *x, at::kByte));
+}
+ENTRY(layernorm_saved, 1) {
+    const Tensor *x = channels(r, 0, 0);
+    if (!r.ok) Py_RETURN_NONE;
+    return THPVariable_Wrap(make({x->numel() / x->size(-1), 2}, *x, F32));
+}
+
 // x, gate_a, gate_x, rate, h0, h_last, reset, lengths, normalize, h, saved
 ENTRY(gated_scan_forward, 11) {
     const Tensor *x = channels(r, 0, 3);
@@ -513,7 +532,8 @@ PyMethodDef methods[] = {METHOD(delta_step), METHOD(delta_forward), METHOD(delta
                          METHOD(qk_norm_rotary), METHOD(qk_norm_rotary_backward),
                          METHOD(gated_scan_forward), METHOD(gated_scan_backward), METHOD(gated_scan_step),
                          METHOD(short_conv_forward), METHOD(short_conv_backward), METHOD(short_conv_step),
-                         METHOD(add_layernorm), METHOD(add_layernorm_backward), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(add_layernorm), METHOD(add_layernorm_backward),
+                         METHOD(gated_scan_saved), METHOD(layernorm_saved), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "The common case of the binding's calls.", -1, methods};
 }  // namespace
 

@@ -23,6 +23,7 @@ using namespace rows;
 constexpr int MAX_H = 16384;
 // A backward block: its warps and a lane's columns.  Eight columns leave registers for the next row (bf16 24 warps,
 // f32 16); wider rows take 16 columns a lane, 16 warps, or 32, which spill.
+constexpr int BWD_SMEM = 96 << 10;   // most of it: sums of two times 24 x 256 columns, or a weight of 16384
 template <typename T> constexpr int BWD_WARPS = sizeof(T) == 2 ? 24 : 16;
 
 struct NormArgs {
@@ -292,7 +293,7 @@ cudaError_t bwd_as(NormArgs &p, float *dw, float *db, cudaStream_t st) {
     const int blocks = (int)(need < SMS ? need : SMS);
     const size_t smem = sizeof(float) * (size_t)p.H * (slots > 1 ? (slots - 1) * 2 : 1);
     const cudaError_t e =
-        launch_big(add_layernorm_bwd_kernel<T, V, NV, MOST, AHEAD>, dim3(blocks), 32 * p.warps * slots, smem, 1, st, p);
+        launch_big<add_layernorm_bwd_kernel<T, V, NV, MOST, AHEAD>>(dim3(blocks), 32 * p.warps * slots, smem, BWD_SMEM, 1, st, p);
     if (e != cudaSuccess || !p.part) return e;
     return launch(add_layernorm_weight_kernel, dim3((2 * p.H + 31) / 32), sum_threads(blocks), 0, 1, st, (const float *)p.part, blocks, p.H, dw, db);
 }

@@ -29,6 +29,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "s5_rows.cuh"
 #include "s5_sm100.cuh"
 
@@ -37,10 +39,8 @@ namespace {
 using namespace rows;
 using sm100::smem_addr;
 
-constexpr int THREADS = 128;    // four blocks an SM
 constexpr int KEEP = 32;        // tokens between two kept states, and of a tile backward (twice that forward)
 constexpr int MAX_CLUSTER = 16; // beyond 8 a non-portable size
-constexpr int FETCHER = THREADS - 32;    // the thread that starts the copies: of a warp that folds nothing
 
 struct ScanArgs {
     const void *x, *ga, *gx;            // gx null: u = x
@@ -124,6 +124,8 @@ struct ScanMaps {
 // How a block's threads share a tile: LANES threads side by side hold V
 // channels each, and GROUPS such rows S consecutive tokens each.
 template <typename T_, int V_, int LANES_, int S_, int ARRAYS_, bool ASYNC_> struct Shape {
+    static constexpr int THREADS = 128, BLOCKS = 4;          // of an SM
+    static constexpr int FETCHER = THREADS - 32;             // the thread that starts the copies: of a warp that folds nothing
     using T = T_;
     static constexpr int V = V_, LANES = LANES_, S = S_, ARRAYS = ARRAYS_;
     static constexpr bool ASYNC = ASYNC_;                     // tiles come by TMA
@@ -269,7 +271,7 @@ template <typename Sh> struct Block {
         const float2 *slots = pairs + now * MAX_CLUSTER * W + col;
         const unsigned base = smem_addr(pairs), at = smem_addr(slots + rank * W) - base, count = smem_addr(bar + now) - base;
 #pragma unroll 4
-        for (int j = threadIdx.x / W; j < K; j += THREADS / W) {
+        for (int j = threadIdx.x / W; j < K; j += Sh::THREADS / W) {
             const unsigned far = there(base, j);
             send(far + at, far + count, all);
         }
@@ -299,7 +301,7 @@ template <typename Sh> struct Block {
 };
 
 template <typename Sh, bool GATED, bool NORM>
-__global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanArgs p, const __grid_constant__ ScanMaps maps) {
+__global__ void __launch_bounds__(Sh::THREADS, Sh::BLOCKS) gated_scan_fwd_kernel(const ScanArgs p, const __grid_constant__ ScanMaps maps) {
     using T = typename Sh::T;
     using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
     const long long ld[3] = {p.ldx, p.ldga, p.ldgx};
     int t0 = k.rank * Sh::TILE;
     unsigned marks = 0;
-    if (Sh::ASYNC && threadIdx.x == FETCHER) k.template fetch<GATED ? 3 : 2>(maps, 0, t0);
+    if (Sh::ASYNC && threadIdx.x == Sh::FETCHER) k.template fetch<GATED ? 3 : 2>(maps, 0, t0);
     if (K > 1) k.open_cluster(p);
     const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
     if (p.reset) marks = k.marks(k.reset_of(p, t0));
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
         }
         __syncthreads();
         // the stage is read: the next tile is on its way while the pairs meet
-        if (Sh::ASYNC && threadIdx.x == FETCHER && round + 1 < p.rounds) k.template fetch<GATED ? 3 : 2>(maps, 0, t0 + K * Sh::TILE);
+        if (Sh::ASYNC && threadIdx.x == Sh::FETCHER && round + 1 < p.rounds) k.template fetch<GATED ? 3 : 2>(maps, 0, t0 + K * Sh::TILE);
         float before = K > 1 ? k.template exchange<false>(p, round, k.E, carry) : carry;
         if (K > 1 && round + 1 == p.rounds) cluster_arrive();
         if (threadIdx.x < W) {               // the state before each warp's tokens
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_fwd_kernel(const ScanAr
 }
 
 template <typename Sh, bool GATED, bool NORM>
-__global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanArgs p, const __grid_constant__ ScanMaps maps) {
+__global__ void __launch_bounds__(Sh::THREADS, Sh::BLOCKS) gated_scan_bwd_kernel(const ScanArgs p, const __grid_constant__ ScanMaps maps) {
     using T = typename Sh::T;
     using M = Many<Sh::V>;
     constexpr int V = Sh::V, S = Sh::S, W = Sh::WIDE;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
     const long long ld[4] = {p.ldx, p.ldga, p.lddh, p.ldgx};
     int t0 = ((p.rounds - 1) * K + k.rank) * Sh::TILE;   // from the last tiles to the first
     unsigned marks = 0;
-    if (Sh::ASYNC && threadIdx.x == FETCHER) k.template fetch<GATED ? 4 : 3>(maps, 0, t0);
+    if (Sh::ASYNC && threadIdx.x == Sh::FETCHER) k.template fetch<GATED ? 4 : 3>(maps, 0, t0);
     if (K > 1) k.open_cluster(p);
     const M rate = M::all(-1.0f) * k.rates(p), none = M::all(0.0f), one = M::all(1.0f);
     M drate = none;
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(THREADS, 4) gated_scan_bwd_kernel(const ScanAr
         if (Sh::LANES == 32 || !k.upper) k.put(k.Z, Z);
         __syncthreads();
         // the other stage is read
-        if (Sh::ASYNC && threadIdx.x == FETCHER && round + 1 < p.rounds) k.template fetch<GATED ? 4 : 3>(maps, 1 - now, t0 - K * Sh::TILE);
+        if (Sh::ASYNC && threadIdx.x == Sh::FETCHER && round + 1 < p.rounds) k.template fetch<GATED ? 4 : 3>(maps, 1 - now, t0 - K * Sh::TILE);
         float after = carry;
         if (K > 1) after = k.template exchange<true>(p, round, k.Z, carry);
         if (K > 1 && round + 1 == p.rounds) cluster_arrive();
@@ -627,30 +629,56 @@ gated_scan_step_kernel(const T *x, const T *ga, const T *gx, const float *rate, 
 }
 
 // ------------------------------------------------------------------ launches
-// Tiles at once: the cluster that ends first when four blocks an SM run side
-// by side, a wave costs two tiles to begin, and each block of it works through
-// its share of the tiles.
-int choose_cluster(long long chains, int tiles) {
-    int best = 1;
-    long long cost = -1;
-    for (int K = 1; K <= MAX_CLUSTER && K <= tiles; ++K) {
-        const long long t = (chains * K + 4 * SMS - 1) / (4 * SMS) * ((tiles + K - 1) / K + 2);
-        if (cost < 0 || t < cost) best = K, cost = t;
+// Tiles at once: the cluster that ends first when as many of them run side by
+// side as the card has room for, a wave costs two tiles to begin, and each block
+// of it works through its share of the tiles.  Room: what the driver says of this
+// kernel, asked once for each size.
+template <auto kernel> cudaError_t room(int threads, int smem, int cluster, int &clusters) {
+    static std::atomic<int> known[MAX_CLUSTER + 1];
+    if ((clusters = known[cluster].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    cudaError_t e = allow<kernel>(smem, true);
+    if (e != cudaSuccess) return e;
+    if (cluster == 1) {
+        int blocks = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem);
+        clusters = blocks * SMS;
+    } else {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = cluster, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(cluster), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.attrs = &attr, cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
     }
-    return best;
+    if (e != cudaSuccess) return e;
+    known[cluster].store(clusters, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+template <auto kernel> cudaError_t choose_cluster(int threads, int smem, long long chains, int tiles, int &best) {
+    long long cost = -1;
+    best = 1;
+    for (int n = 1; n <= MAX_CLUSTER && n <= tiles; ++n) {
+        int clusters = 0;
+        const cudaError_t e = room<kernel>(threads, smem, n, clusters);
+        if (e != cudaSuccess) return e;
+        if (clusters < 1) continue;
+        const long long t = (chains + clusters - 1) / clusters * ((tiles + n - 1) / n + 2);
+        if (cost < 0 || t < cost) best = n, cost = t;
+    }
+    return cudaSuccess;
 }
 
-template <typename Sh> cudaError_t place(ScanArgs &p, long long &blocks) {
+template <typename Sh, auto kernel> cudaError_t place(ScanArgs &p, long long &blocks) {
     const int tiles = (p.L + Sh::TILE - 1) / Sh::TILE;
     const long long chains = (long long)p.B * ((p.C + Sh::WIDE - 1) / Sh::WIDE);
-    p.cluster = choose_cluster(chains, tiles);
+    const cudaError_t e = choose_cluster<kernel>(Sh::THREADS, Sh::SMEM, chains, tiles, p.cluster);
+    if (e != cudaSuccess) return e;
     p.rounds = (tiles + p.cluster - 1) / p.cluster;
     blocks = chains * p.cluster;
-    const long long bytes = sizeof(typename Sh::T), round = bytes * p.cluster * Sh::TILE;
-    const bool back = Sh::ARRAYS == 4;
-    const long long out[3] = {back ? p.lddx : p.ldh, p.lddga, p.lddgx};
+    const long long bytes = sizeof(typename Sh::T);
+    const long long out[3] = {Sh::ARRAYS == 4 ? p.lddx : p.ldh, p.lddga, p.lddgx};
     for (int i = 0; i < 3; ++i) p.row[i] = bytes * out[i];
-    p.out_step = round * out[0];
+    p.out_step = bytes * p.cluster * Sh::TILE * out[0];
     return blocks > 0x7fffffffll ? cudaErrorInvalidValue : cudaSuccess;
 }
 
@@ -675,45 +703,36 @@ cudaError_t encode(CUtensorMap *m, bool f32, const void *base, long long ld, con
                : cudaErrorInvalidValue;
 }
 
-template <typename Sh, typename... Ks> cudaError_t launch_scan(void (*k)(Ks...), const ScanArgs &p, long long blocks, cudaStream_t st) {
+template <typename Sh, auto kernel> cudaError_t launch_scan(ScanArgs &p, float *drate, cudaStream_t st) {
+    long long blocks;
+    cudaError_t e = place<Sh, kernel>(p, blocks);
     ScanMaps maps = {};
     if constexpr (Sh::ASYNC) {
         const bool f32 = sizeof(typename Sh::T) == 4;
-        cudaError_t e = encode(&maps.map[0], f32, p.x, p.ldx, p, Sh::TILE);
+        if (e == cudaSuccess) e = encode(&maps.map[0], f32, p.x, p.ldx, p, Sh::TILE);
         if (e == cudaSuccess) e = encode(&maps.map[1], f32, p.ga, p.ldga, p, Sh::TILE);
         if (Sh::ARRAYS == 4 && e == cudaSuccess) e = encode(&maps.map[2], f32, p.dh, p.lddh, p, Sh::TILE);
         if (p.gx && e == cudaSuccess) e = encode(&maps.map[Sh::ARRAYS - 1], f32, p.gx, p.ldgx, p, Sh::TILE);
-        if (e != cudaSuccess) return e;
     }
-    if (p.cluster > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_big(k, dim3((unsigned)blocks), THREADS, Sh::SMEM, p.cluster, st, p, maps);
+    if (e != cudaSuccess) return e;
+    const int parts = p.B * p.cluster;
+    if (parts == 1) p.drate = drate;     // backward: nothing to sum
+    e = launch_big<kernel>(dim3((unsigned)blocks), Sh::THREADS, Sh::SMEM, Sh::SMEM, p.cluster, st, p, maps);
+    if (e != cudaSuccess || !drate || parts == 1) return e;
+    return launch(gated_scan_rate_kernel, dim3((p.C + 31) / 32), sum_threads(parts), 0, 1, st, (const float *)p.drate, parts, p.C, drate);
 }
 
 template <typename Sh> cudaError_t run_fwd(ScanArgs &p, cudaStream_t st) {
-    long long blocks;
-    const cudaError_t e = place<Sh>(p, blocks);
-    if (e != cudaSuccess) return e;
-#define S5_RUN(GATED, NORM) launch_scan<Sh>(gated_scan_fwd_kernel<Sh, GATED, NORM>, p, blocks, st)
-    if (p.gx) return p.normalize ? S5_RUN(true, true) : S5_RUN(true, false);
-    return p.normalize ? S5_RUN(false, true) : S5_RUN(false, false);
-#undef S5_RUN
+    if (p.gx && p.normalize) return launch_scan<Sh, gated_scan_fwd_kernel<Sh, true, true>>(p, nullptr, st);
+    if (p.gx) return launch_scan<Sh, gated_scan_fwd_kernel<Sh, true, false>>(p, nullptr, st);
+    if (p.normalize) return launch_scan<Sh, gated_scan_fwd_kernel<Sh, false, true>>(p, nullptr, st);
+    return launch_scan<Sh, gated_scan_fwd_kernel<Sh, false, false>>(p, nullptr, st);
 }
-
 template <typename Sh> cudaError_t run_bwd(ScanArgs &p, float *drate, cudaStream_t st) {
-    long long blocks;
-    cudaError_t e = place<Sh>(p, blocks);
-    if (e != cudaSuccess) return e;
-    const int parts = p.B * p.cluster;
-    if (parts == 1) p.drate = drate;
-#define S5_RUN(GATED, NORM) launch_scan<Sh>(gated_scan_bwd_kernel<Sh, GATED, NORM>, p, blocks, st)
-    if (p.gx) e = p.normalize ? S5_RUN(true, true) : S5_RUN(true, false);
-    else e = p.normalize ? S5_RUN(false, true) : S5_RUN(false, false);
-#undef S5_RUN
-    if (e != cudaSuccess || parts == 1) return e;
-    return launch(gated_scan_rate_kernel, dim3((p.C + 31) / 32), sum_threads(parts), 0, 1, st, (const float *)p.drate, parts, p.C, drate);
+    if (p.gx && p.normalize) return launch_scan<Sh, gated_scan_bwd_kernel<Sh, true, true>>(p, drate, st);
+    if (p.gx) return launch_scan<Sh, gated_scan_bwd_kernel<Sh, true, false>>(p, drate, st);
+    if (p.normalize) return launch_scan<Sh, gated_scan_bwd_kernel<Sh, false, true>>(p, drate, st);
+    return launch_scan<Sh, gated_scan_bwd_kernel<Sh, false, false>>(p, drate, st);
 }
 
 // TMA where all rows allow it (starts and pitches of 16 bytes, a batch below 2^40 bytes), else pairs of channels, else

@@ -1,6 +1,8 @@
 // s5_rows.cuh -- what the kernels on rows of channels share (s5_gated_scan.cu,
 // s5_short_conv.cu, s5_add_layernorm.cu): values in vectors, launches.
 #pragma once
+#include <atomic>
+
 #include "s5_internal.cuh"
 
 namespace s5 {
@@ -180,12 +182,23 @@ cudaError_t launch(void (*k)(Ks...), dim3 grid, int threads, size_t smem, int cl
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
-// The same for a kernel whose dynamic shared memory, with its static one, may pass the 48 KB that need no asking.
-template <typename... Ks, typename... As>
-cudaError_t launch_big(void (*k)(Ks...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, As... args) {
-    const cudaError_t e =
-        smem > 40 << 10 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
-    return e != cudaSuccess ? e : launch(k, grid, threads, smem, cluster, st, args...);
+// What a kernel may ask for at a launch, set once for each device: dynamic shared memory up to `most` bytes, and
+// clusters of more than eight blocks.
+template <auto kernel> cudaError_t allow(int most, bool large_clusters) {
+    static std::atomic<unsigned long long> done{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess || (device < 64 && done.load(std::memory_order_relaxed) >> device & 1)) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess && large_clusters) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && device < 64) done.fetch_or(1ull << device, std::memory_order_relaxed);
+    return e;
+}
+// The launch of such a kernel.
+template <auto kernel, typename... As>
+cudaError_t launch_big(dim3 grid, int threads, size_t smem, int most, int cluster, cudaStream_t st, As... args) {
+    const cudaError_t e = allow<kernel>(most, cluster > 1);
+    return e != cudaSuccess ? e : launch(kernel, grid, threads, smem, cluster, st, args...);
 }
 
 constexpr int SMS = 152;

@@ -449,7 +449,8 @@ void cut(ConvArgs &p, int V) {
 }
 
 template <typename T, int V, int K, bool ASYNC> cudaError_t start_fwd(const ConvArgs &p, int blocks, cudaStream_t st) {
-    return launch_big(short_conv_fwd_kernel<T, V, K, ASYNC>, dim3(blocks), WARPS * 32, WARPS * Walk<T, V, K, 1, ASYNC>::RING, 1, st, p);
+    constexpr int SMEM = WARPS * Walk<T, V, K, 1, ASYNC>::RING;
+    return launch_big<short_conv_fwd_kernel<T, V, K, ASYNC>>(dim3(blocks), WARPS * 32, SMEM, SMEM, 1, st, p);
 }
 template <typename T, int V, int K> cudaError_t run_fwd(ConvArgs &p, cudaStream_t st) {
     cut(p, V);
@@ -466,8 +467,9 @@ int along_blocks(long long segments, int across) {
 }
 
 template <typename T, int V, int K, bool ASYNC> cudaError_t start_bwd(const ConvArgs &p, cudaStream_t st) {
-    const size_t ring = WARPS * Walk<T, V, K, 2, ASYNC>::RING, sums = sizeof(float) * (WARPS - 1) * (K + 1) * V * 32;
-    return launch_big(short_conv_bwd_kernel<T, V, K, ASYNC>, dim3(p.along * p.across), WARPS * 32, ring > sums ? ring : sums, 1, st, p);
+    constexpr int RING = WARPS * Walk<T, V, K, 2, ASYNC>::RING, SUMS = (int)sizeof(float) * (WARPS - 1) * (K + 1) * V * 32;
+    constexpr int SMEM = RING > SUMS ? RING : SUMS;
+    return launch_big<short_conv_bwd_kernel<T, V, K, ASYNC>>(dim3(p.along * p.across), WARPS * 32, SMEM, SMEM, 1, st, p);
 }
 template <typename T, int V, int K> cudaError_t run_bwd(ConvArgs &p, float *dw, float *db, cudaStream_t st) {
     cut(p, V);

@@ -25,7 +25,9 @@ def _gates(x, ga, gx, rate, reset, valid, normalize):
     ds = np.zeros_like(x) if gx is None else (np.abs(gx) + 8) * U
     dr = (np.abs(ga) + 8) * U
     far = la < -0.24
-    da = np.abs(la) * (dr + 5 * U) + np.where(far, 5, 1) * U
+    # a = 1 - m, m = 1 - exp(la): near one a rounding; further off exp2's 4 U of a and the two subtractions' U of 1 and of
+    # m, absolute, so 2 U / a relative
+    da = np.abs(la) * (dr + 5 * U) + np.where(far, 5 + 2 / np.maximum(a, 1e-30), 1) * U
     dm = np.where(far, a / np.maximum(m, 0.2) * da + U, dr + 5 * U)
     dn = dm + 7 * U if normalize else 0 * dm
     with np.errstate(divide="ignore", invalid="ignore"):
