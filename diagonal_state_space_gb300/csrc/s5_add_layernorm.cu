@@ -138,7 +138,6 @@ __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const Norm
     const int slots = (int)(blockDim.x >> 5) / p.warps, slot = warp / p.warps, first = slot * p.warps;
     const int at = ((warp - first) * 32 + lane) * V, step = p.warps * 32 * V;
     griddep_wait();
-    griddep_launch_dependents();         // the sum of the parts waits for this kernel's end
     for (int c = threadIdx.x; c < p.H; c += blockDim.x) smem[c] = p.w ? p.w[c] : 1.0f;
     float dw[NV][V], db[NV][V];
 #pragma unroll

@@ -425,7 +425,6 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::BLOCKS) gated_scan_bwd_kernel
     const int K = p.cluster, N = (p.L + KEEP - 1) / KEEP;
     if (Sh::ASYNC) k.open_copies();
     griddep_wait();
-    griddep_launch_dependents();             // the sum of the parts waits for this kernel's end
     k.read_length(p);
     const void *const from[4] = {p.x, p.ga, p.dh, GATED ? p.gx : nullptr};
     const long long ld[4] = {p.ldx, p.ldga, p.lddh, p.ldgx};

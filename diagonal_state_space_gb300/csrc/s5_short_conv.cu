@@ -260,7 +260,6 @@ __global__ void __launch_bounds__(WARPS * 32, 4) short_conv_bwd_kernel(const Con
     constexpr int STAGES = Walk<T, V, K, 2, ASYNC>::STAGES;
     Walk<T, V, K, 2, ASYNC> k(p, smem);
     griddep_wait();
-    griddep_launch_dependents();         // the kernel that sums the parts waits for this one's end
     const void *const from[2] = {p.x, p.dy};
     const long long ld[2] = {p.ldx, p.lddy};
     const M none = M::all(0.0f);
