@@ -104,13 +104,15 @@ __device__ __forceinline__ void send(unsigned at, unsigned bar, float2 v) {
                  "f"(v.y), "r"(bar)
                  : "memory");
 }
-__device__ int g_scan_fault = 0;     // a wait for the cluster's pairs ran out
-constexpr unsigned long long WAIT_NS = 2000000000ull;
-// The other blocks run beside this one, so the wait ends; were it not to, the results would be wrong and said to be.
+__device__ int g_scan_fault = 0;     // a wait ran out
+constexpr unsigned long long WAIT_NS = 2000000000ull, WAIT_AFTER_NS = 1000000ull;
+// For a tile's copies or the cluster's pairs.  The other blocks run beside this one, so the wait ends; were it not to,
+// the results would be wrong and said to be, and no later wait would take as long.
 __device__ __noinline__ void wait_long(uint64_t *bar, unsigned parity) {
     const unsigned long long t0 = global_ns();
+    const unsigned long long limit = *static_cast<volatile int *>(&g_scan_fault) ? WAIT_AFTER_NS : WAIT_NS;
     while (!sm100::mbar_try_wait_sleep(bar, parity, 100000))
-        if (global_ns() - t0 > WAIT_NS) {
+        if (global_ns() - t0 > limit) {
             atomicExch(&g_scan_fault, 1);
             return;
         }
