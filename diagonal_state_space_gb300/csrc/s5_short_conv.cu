@@ -27,7 +27,7 @@ constexpr int WARPS = 4;                 // of a block
 constexpr int U = 8;                     // tokens of a ring's stage, and of one pass of the loop
 constexpr int MAX_TAPS = 8;
 // Blocks that the segments are cut for; backward as many as run at once, a part of the weights' gradient each.
-// Forward six fit an SM, but longer segments for four are no slower and better where resets send some chunks the
+// Forward six could fit an SM, but longer segments for four are no slower and better where resets send some chunks the
 // longer way (4 x 2048 tokens of 4096 channels with resets 25.3 us for four, 27.2 for six; 8 x 1999 of 2048 without
 // 23.4 and 22.6).
 constexpr int BLOCKS = 4 * SMS;
@@ -139,6 +139,19 @@ template <typename T, int V, int K, int ARRAYS, bool ASYNC> struct Walk {
         }
         return r;
     }
+    // N tokens' values as they lie there, all loaded before any output is stored, behind which no load may move.
+    template <int N> __device__ void load_raw(const ConvArgs &p, int stage, int t, int i, int k, int stop, const void *const *from,
+                                              const long long *ld, typename Vec<T, V>::raw (&r)[N]) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if constexpr (ASYNC) {
+                r[n] = Vec<T, V>::get(reinterpret_cast<const T *>(ring + ((stage * ARRAYS + k) * U + i + n) * ROW) + (threadIdx.x & 31) * V);
+            } else {
+                r[n] = {};
+                if (in && t + i + n < stop) r[n] = Vec<T, V>::get(row(p, from[k], ld[k], t + i + n));
+            }
+        }
+    }
     __device__ void fresh() {
         age = 0;
 #pragma unroll
@@ -184,7 +197,7 @@ template <typename T, int V, int K, int ARRAYS, bool ASYNC> struct Walk {
 };
 
 template <typename T, int V, int K, bool ASYNC>
-__global__ void __launch_bounds__(WARPS * 32, 6) short_conv_fwd_kernel(const ConvArgs p) {
+__global__ void __launch_bounds__(WARPS * 32, 4) short_conv_fwd_kernel(const ConvArgs p) {
     using M = Many<V>;
     extern __shared__ __align__(128) unsigned char smem[];
     constexpr int STAGES = Walk<T, V, K, 1, ASYNC>::STAGES;
@@ -228,9 +241,12 @@ __global__ void __launch_bounds__(WARPS * 32, 6) short_conv_fwd_kernel(const Con
             k.fetch(p, (stage + STAGES - 1) % STAGES, t + (STAGES - 1) * U, stop, from, ld);
         }
         if (!marks && t + U <= stop) {
+            typename Vec<T, V>::raw raw[U];
+            k.load_raw(p, stage, t, 0, 0, stop, from, ld, raw);
 #pragma unroll
             for (int i = 0; i < U; ++i, out += hop) {
-                const M x = k.load(p, stage, t, i, 0, stop, from, ld);
+                M x;
+                Vec<T, V>::widen(raw[i], x.v);
                 M y = k.taps(w, bias, x);
                 if (p.act) y = y * sigmoid(y);
                 if (k.in) Vec<T, V>::store(reinterpret_cast<T *>(out), y.v);
@@ -292,10 +308,17 @@ __global__ void __launch_bounds__(WARPS * 32, 4) short_conv_bwd_kernel(const Con
                 k.fetch(p, (stage + STAGES - 1) % STAGES, t + (STAGES - 1) * U, stop, from, ld);
             }
             if (!marks && k.age >= K && t + U <= end && t + U <= k.len && (t > k.t0 || !p.dpast)) {
+                constexpr int N = 4;         // tokens at a time
+                typename Vec<T, V>::raw raw[N], rawd[N];
 #pragma unroll
                 for (int i = 0; i < U; ++i, out += hop) {
-                    const M x = k.load(p, stage, t, i, 0, stop, from, ld);
-                    M dp = k.load(p, stage, t, i, 1, stop, from, ld);
+                    if (i % N == 0) {
+                        k.load_raw(p, stage, t, i, 0, stop, from, ld, raw);
+                        k.load_raw(p, stage, t, i, 1, stop, from, ld, rawd);
+                    }
+                    M x, dp;
+                    Vec<T, V>::widen(raw[i % N], x.v);
+                    Vec<T, V>::widen(rawd[i % N], dp.v);
                     if (p.act) {
                         const M s = k.taps(w, bias, x), g = sigmoid(s), sg = s * g;
                         M r;
