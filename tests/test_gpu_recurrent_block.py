@@ -203,3 +203,35 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     assert all(same(list(out), want[n]) for n, out in got)
     assert not api.s5_gated_scan_fault()
+
+
+FIRST = """
+import torch
+from diagonal_state_space_gb300 import api
+gen = torch.Generator(device="cuda").manual_seed(1)
+x, a, g, dh = (torch.randn(2, 600, 72, generator=gen, device="cuda") for _ in range(4))
+rate, w, b = torch.rand(72, generator=gen, device="cuda"), torch.randn(72, 5, generator=gen, device="cuda"), torch.randn(72, generator=gen, device="cuda")
+def run():
+    stats, saved = api.new_layernorm_saved(x), api.new_gated_scan_saved(x)
+    n, total = api.s5_add_layernorm(x, b, b, residual=a, saved=stats)
+    c = api.s5_short_conv_forward(n, w, bias=b, activation="silu")
+    h = api.s5_gated_scan_forward(c, a, g, rate, saved=saved)
+    d = api.s5_gated_scan_backward(c, a, g, rate, dh, saved)
+    v = api.s5_short_conv_backward(n, w, d["dx"], bias=b, activation="silu")
+    m = api.s5_add_layernorm_backward(x, v["dx"], stats, b, b, residual=a, dtotal=dh)
+    return [n, total, c, h] + [t for u in (d, v, m) for t in u.values() if t is not None]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(out, run()))
+assert not api.s5_gated_scan_fault()
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    import subprocess
+    res = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]
