@@ -21,10 +21,12 @@ namespace {
 using namespace rows;
 
 constexpr int MAX_H = 16384;
-// A backward block: its warps and a lane's columns.  Eight columns leave registers for the next row (bf16 24 warps,
-// f32 16); wider rows take 16 columns a lane, 16 warps, or 32, which spill.
+// A backward block: its warps and a lane's columns.  Eight columns leave registers for the next row: 24 warps where a
+// lane has one vector of eight, else 16 (narrower vectors spill with 24: 8000 rows of 1799 in bf16 137 us, 69 with 16).
+// Rows of 13 to 16 warps leave no room for a second one, and go better with 16 warps' registers (8192 of 4096 74 us, 82
+// with 24).  Still wider rows take 24 warps again, only full vectors with the next row, then 16 columns a lane without
+// it, in 16 warps (single values 8 in 32: 3000 of 7001 227 us for 289) or in 32, which spill.
 constexpr int BWD_SMEM = 96 << 10;   // most of it: sums of two times 24 x 256 columns, or a weight of 16384
-template <typename T> constexpr int BWD_WARPS = sizeof(T) == 2 ? 24 : 16;
 
 struct NormArgs {
     const void *x, *residual, *dy, *dtotal;
@@ -272,7 +274,8 @@ template <typename T, int V, int NV> cudaError_t fwd_as(NormArgs &p, cudaStream_
 template <typename T, int V> cudaError_t fwd_by(NormArgs &p, cudaStream_t st) {
     constexpr int MOST = V * sizeof(T) == 16 && sizeof(T) == 2 ? 32 : 16;
     auto warps = [&](int cols) { return (p.H + 32 * cols - 1) / (32 * cols); };
-    int cols = MOST;
+    // single 32-bit values spill with 16 (8000 rows of 1799 80 us, 47 with 8)
+    int cols = sizeof(T) == 4 && V == 1 && warps(8) <= 16 ? 8 : MOST;
     while (cols > V && warps(cols / 2) <= 32 && (warps(cols / 2) == 1 || p.N * warps(cols) < 8 * SMS)) cols /= 2;
     if (cols == V) return fwd_as<T, V, 1>(p, st);
     if (cols == 2 * V) return fwd_as<T, V, 2>(p, st);
@@ -291,13 +294,19 @@ cudaError_t bwd_as(NormArgs &p, float *dw, float *db, cudaStream_t st) {
     const long long need = (p.N + slots - 1) / slots;
     const int blocks = (int)(need < SMS ? need : SMS);
     const size_t smem = sizeof(float) * (size_t)p.H * (slots > 1 ? (slots - 1) * 2 : 1);
-    const cudaError_t e =
-        launch_big<add_layernorm_bwd_kernel<T, V, NV, MOST, AHEAD>>(dim3(blocks), 32 * p.warps * slots, smem, BWD_SMEM, 1, st, p);
+    const cudaError_t e = launch_big<add_layernorm_bwd_kernel<T, V, NV, MOST, AHEAD>>(dim3(blocks), 32 * p.warps * slots, smem,
+                                                                                              BWD_SMEM, 1, st, p);
     if (e != cudaSuccess || !p.part) return e;
-    return launch(add_layernorm_weight_kernel, dim3((2 * p.H + 31) / 32), sum_threads(blocks), 0, 1, st, (const float *)p.part, blocks, p.H, dw, db);
+    return launch(add_layernorm_weight_kernel, dim3((2 * p.H + 31) / 32), sum_threads(blocks), 0, 1, st, (const float *)p.part, blocks, p.H,
+                  dw, db);
 }
 template <typename T, int V> cudaError_t bwd_by(NormArgs &p, float *dw, float *db, cudaStream_t st) {
-    if (p.H <= 32 * 8 * BWD_WARPS<T>) return bwd_as<T, V, 8 / V, BWD_WARPS<T>, true>(p, dw, db, st);
+    constexpr int MOST = V == 8 ? 24 : 16;
+    if (p.H <= 32 * 8 * MOST / 2) return bwd_as<T, V, 8 / V, MOST, true>(p, dw, db, st);
+    if (p.H <= 32 * 8 * 16) return bwd_as<T, V, 8 / V, 16, true>(p, dw, db, st);
+    if (p.H <= 32 * 8 * 24) return bwd_as<T, V, 8 / V, 24, V == 8>(p, dw, db, st);
+    if constexpr (V == 1)
+        if (p.H <= 32 * 8 * 32) return bwd_as<T, V, 8, 32, false>(p, dw, db, st);
     if (p.H <= 32 * 16 * 16) return bwd_as<T, V, 16 / V, 16, false>(p, dw, db, st);
     return bwd_as<T, V, 16 / V, 32, false>(p, dw, db, st);
 }
