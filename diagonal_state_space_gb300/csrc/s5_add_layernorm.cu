@@ -12,7 +12,10 @@
 // Backward, a row is spread over more lanes, 8 columns each, because a lane
 // also keeps the weights' gradients of its columns over all the rows that it
 // sees; one block an SM adds its warps' sums up, and a second launch the
-// blocks'.  No atomics.
+// blocks'.  No atomics.  bf16: 16384 rows of 2048 with the residual 43 us forward
+// (6.2 TB/s) and 63.5 backward (5.3), 4099 of 8192 47.5 forward (5.7).  Odd widths
+// move single values, and backward more than 8192 columns spill: 2000 of 12288
+// 259 us (0.9 TB/s).
 #include "s5_rows.cuh"
 #include "s5_sm100.cuh"
 

@@ -151,9 +151,6 @@ template <int V> __device__ __forceinline__ Many<V> sigmoid(const Many<V> &g) {
     return e;
 }
 
-__device__ __forceinline__ void cp_async16(unsigned dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void cp_async16(unsigned dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
