@@ -14,8 +14,9 @@
 // sees; one block an SM adds its warps' sums up, and a second launch the
 // blocks'.  No atomics.  bf16: 16384 rows of 2048 with the residual 43 us forward
 // (6.2 TB/s) and 63.5 backward (5.3), 4099 of 8192 47.5 forward (5.7).  Odd widths
-// move single values, and backward more than 8192 columns spill: 2000 of 12288
-// 259 us (0.9 TB/s).
+// move single values (3000 of 7001 backward 164 us, 1.3 TB/s), and backward rows of
+// more than 6144 columns are read without the next one on its way (2000 of 12288
+// 103 us, 2.4 TB/s).
 #include "s5_rows.cuh"
 #include "s5_sm100.cuh"
 
@@ -27,9 +28,13 @@ constexpr int MAX_H = 16384;
 // A backward block: its warps and a lane's columns.  Eight columns leave registers for the next row: 24 warps where a
 // lane has one vector of eight, else 16 (narrower vectors spill with 24: 8000 rows of 1799 in bf16 137 us, 69 with 16).
 // Rows of 13 to 16 warps leave no room for a second one, and go better with 16 warps' registers (8192 of 4096 74 us, 82
-// with 24).  Still wider rows take 24 warps again, only full vectors with the next row, then 16 columns a lane without
-// it, in 16 warps (single values 8 in 32: 3000 of 7001 227 us for 289) or in 32, which spill.
+// with 24).  Still wider rows take 24 warps again, only full vectors with the next row.  Above 6144 columns the sums of
+// the weights' gradients lie in shared memory, 32 warps with 8 columns a lane and above 8192 with 16 (3000 of 7001 in
+// bf16 164 us, 226 with the sums in registers; of 8192 in 32 bits 108, 124; 2000 of 12288 in bf16 103, 259), but for two
+// kinds: bf16 in vectors up to 8192, 16 columns a lane in 16 warps (3000 of 8192 70, 87), and single values above it
+// (2000 of 12289 316, 335).
 constexpr int BWD_SMEM = 96 << 10;   // most of it: sums of two times 24 x 256 columns, or a weight of 16384
+constexpr int SHARED_SMEM = 3 * MAX_H * (int)sizeof(float);
 
 struct NormArgs {
     const void *x, *residual, *dy, *dtotal;
@@ -135,20 +140,25 @@ __global__ void __launch_bounds__(V * NV >= 32 ? 512 : 1024) add_layernorm_fwd_k
 }
 
 // A block's warps in slots of `warps`, a row each at a time; the next row is on its way while a row's warps meet.
-template <typename T, int V, int NV, int MOST, bool AHEAD>
+// SHARED: one slot, the sums of the weights' gradients in shared memory, where each lane has its own columns, dy widened
+// again and dtotal read when they are needed, so that 16 columns a lane fit 64 registers.
+template <typename T, int V, int NV, int MOST, bool AHEAD, bool SHARED>
 __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const NormArgs p) {
     __shared__ float2 sums[2][MOST];
-    extern __shared__ __align__(16) float smem[];    // [H] the weight; at the end [slots - 1][2][H] sums
+    extern __shared__ __align__(16) float smem[];    // [H] the weight; at the end [slots - 1][2][H] sums; SHARED [3][H]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slots = (int)(blockDim.x >> 5) / p.warps, slot = warp / p.warps, first = slot * p.warps;
     const int at = ((warp - first) * 32 + lane) * V, step = p.warps * 32 * V;
     griddep_wait();
     for (int c = threadIdx.x; c < p.H; c += blockDim.x) smem[c] = p.w ? p.w[c] : 1.0f;
-    float dw[NV][V], db[NV][V];
+    constexpr int KEPT = SHARED ? 1 : NV;
+    float dw[KEPT][V], db[KEPT][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < KEPT; ++i)
 #pragma unroll
         for (int v = 0; v < V; ++v) dw[i][v] = 0.0f, db[i][v] = 0.0f;
+    if constexpr (SHARED)
+        for (int c = threadIdx.x; c < 2 * p.H; c += blockDim.x) smem[p.H + c] = 0.0f;
     const long long stride = (long long)gridDim.x * slots;
     const float per = 1.0f / p.H;
     using raw = typename Vec<T, V>::raw;
@@ -165,7 +175,7 @@ __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const Norm
             rs[i] = Vec<T, V>::get(s + i * step);
             rd[i] = Vec<T, V>::get(d + i * step);
             if (p.residual) rr[i] = Vec<T, V>::get(r + i * step);
-            if (p.dtotal) rt[i] = Vec<T, V>::get(t + i * step);
+            if (!SHARED && p.dtotal) rt[i] = Vec<T, V>::get(t + i * step);
         }
         stat = p.saved[row];
     };
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const Norm
     __syncthreads();
     for (int turn = 0; row < p.N; row += stride, turn ^= 1) {
         if (!AHEAD) fetch(row);
-        float n[NV][V], g[NV][V];
+        float n[NV][V], g[KEPT][V];
         float2 sum = make_float2(0.0f, 0.0f);
         const float inv = stat.y;
         raw late[NV];
@@ -190,15 +200,22 @@ __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const Norm
                     for (int v = 0; v < V; ++v) s[v] += u[v];
                 }
             }
-            late[i] = rt[i];
+            if constexpr (!SHARED) late[i] = rt[i];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 n[i][v] = in ? (s[v] - stat.x) * inv : 0.0f;
-                g[i][v] = d[v] * w[v];
-                dw[i][v] = fmaf(d[v], n[i][v], dw[i][v]);
-                db[i][v] += d[v];
-                sum.x += g[i][v];
-                sum.y = fmaf(g[i][v], n[i][v], sum.y);
+                const float e = d[v] * w[v];
+                if constexpr (!SHARED) g[i][v] = e;
+                if constexpr (!SHARED) dw[i][v] = fmaf(d[v], n[i][v], dw[i][v]), db[i][v] += d[v];
+                sum.x += e;
+                sum.y = fmaf(e, n[i][v], sum.y);
+            }
+            if (SHARED && in && p.part) {
+                float *own = smem + p.H + at + i * step, a[V], b[V];
+                load_floats<V>(own, a), load_floats<V>(own + p.H, b);
+#pragma unroll
+                for (int v = 0; v < V; ++v) a[v] = fmaf(d[v], n[i][v], a[v]), b[v] += d[v];
+                store_floats<V>(own, a), store_floats<V>(own + p.H, b);
             }
         }
         if (AHEAD) fetch(row + stride);
@@ -218,42 +235,62 @@ __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const Norm
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (at + i * step >= p.H) continue;
-            float o[V], t[V];
-            if (p.dtotal) Vec<T, V>::widen(late[i], t);
+            float o[V], t[V], e[V];
+            if constexpr (SHARED) {
+                Vec<T, V>::widen(rd[i], e), load_floats<V>(smem + at + i * step, t);
+#pragma unroll
+                for (int v = 0; v < V; ++v) e[v] *= t[v];
+                if (p.dtotal) Vec<T, V>::load(static_cast<const T *>(p.dtotal) + row * p.lddt + at + i * step, t);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) e[v] = g[i][v];
+                if (p.dtotal) Vec<T, V>::widen(late[i], t);
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                o[v] = inv * (g[i][v] - sum.x - n[i][v] * sum.y);
+                o[v] = inv * (e[v] - sum.x - n[i][v] * sum.y);
                 if (p.dtotal) o[v] += t[v];
             }
             Vec<T, V>::store(dx + i * step, o);
         }
     }
     if (!p.part) return;
-    __syncthreads();                     // the weight is read no more
-    if (slot > 0) {
+    if constexpr (SHARED) {
+        float *part = p.part + (long long)blockIdx.x * 2 * p.H;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (at + i * step < p.H) {
-                store_floats<V>(smem + (long long)(slot - 1) * 2 * p.H + at + i * step, dw[i]);
-                store_floats<V>(smem + (long long)(slot - 1) * 2 * p.H + p.H + at + i * step, db[i]);
-            }
-    }
-    __syncthreads();
-    if (slot > 0) return;
-    float *part = p.part + (long long)blockIdx.x * 2 * p.H;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = at + i * step;
-        if (c >= p.H) continue;
-        for (int q = 1; q < slots; ++q) {
-            float a[V], b[V];
-            load_floats<V>(smem + (long long)(q - 1) * 2 * p.H + c, a);
-            load_floats<V>(smem + (long long)(q - 1) * 2 * p.H + p.H + c, b);
-#pragma unroll
-            for (int v = 0; v < V; ++v) dw[i][v] += a[v], db[i][v] += b[v];
+        for (int i = 0; i < NV; ++i) {
+            const int c = at + i * step;
+            if (c >= p.H) continue;
+            load_floats<V>(smem + p.H + c, dw[0]), load_floats<V>(smem + 2 * p.H + c, db[0]);
+            store_floats<V>(part + c, dw[0]), store_floats<V>(part + p.H + c, db[0]);
         }
-        store_floats<V>(part + c, dw[i]);
-        store_floats<V>(part + p.H + c, db[i]);
+    } else {
+        __syncthreads();                     // the weight is read no more
+        if (slot > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (at + i * step < p.H) {
+                    store_floats<V>(smem + (long long)(slot - 1) * 2 * p.H + at + i * step, dw[i]);
+                    store_floats<V>(smem + (long long)(slot - 1) * 2 * p.H + p.H + at + i * step, db[i]);
+                }
+        }
+        __syncthreads();
+        if (slot > 0) return;
+        float *part = p.part + (long long)blockIdx.x * 2 * p.H;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = at + i * step;
+            if (c >= p.H) continue;
+            for (int q = 1; q < slots; ++q) {
+                float a[V], b[V];
+                load_floats<V>(smem + (long long)(q - 1) * 2 * p.H + c, a);
+                load_floats<V>(smem + (long long)(q - 1) * 2 * p.H + p.H + c, b);
+#pragma unroll
+                for (int v = 0; v < V; ++v) dw[i][v] += a[v], db[i][v] += b[v];
+            }
+            store_floats<V>(part + c, dw[i]);
+            store_floats<V>(part + p.H + c, db[i]);
+        }
     }
 }
 
@@ -290,15 +327,15 @@ template <typename T, int V> cudaError_t fwd_by(NormArgs &p, cudaStream_t st) {
     return cudaErrorInvalidValue;
 }
 
-template <typename T, int V, int NV, int MOST, bool AHEAD>
+template <typename T, int V, int NV, int MOST, bool AHEAD, bool SHARED = false>
 cudaError_t bwd_as(NormArgs &p, float *dw, float *db, cudaStream_t st) {
     p.warps = (p.H + 32 * V * NV - 1) / (32 * V * NV);
     const int slots = MOST / p.warps;
     const long long need = (p.N + slots - 1) / slots;
     const int blocks = (int)(need < SMS ? need : SMS);
-    const size_t smem = sizeof(float) * (size_t)p.H * (slots > 1 ? (slots - 1) * 2 : 1);
-    const cudaError_t e = launch_big<add_layernorm_bwd_kernel<T, V, NV, MOST, AHEAD>>(dim3(blocks), 32 * p.warps * slots, smem,
-                                                                                              BWD_SMEM, 1, st, p);
+    const size_t smem = sizeof(float) * (size_t)p.H * (SHARED ? 3 : slots > 1 ? (slots - 1) * 2 : 1);
+    const cudaError_t e = launch_big<add_layernorm_bwd_kernel<T, V, NV, MOST, AHEAD, SHARED>>(dim3(blocks), 32 * p.warps * slots, smem,
+                                                                                              SHARED ? SHARED_SMEM : BWD_SMEM, 1, st, p);
     if (e != cudaSuccess || !p.part) return e;
     return launch(add_layernorm_weight_kernel, dim3((2 * p.H + 31) / 32), sum_threads(blocks), 0, 1, st, (const float *)p.part, blocks, p.H,
                   dw, db);
@@ -308,10 +345,11 @@ template <typename T, int V> cudaError_t bwd_by(NormArgs &p, float *dw, float *d
     if (p.H <= 32 * 8 * MOST / 2) return bwd_as<T, V, 8 / V, MOST, true>(p, dw, db, st);
     if (p.H <= 32 * 8 * 16) return bwd_as<T, V, 8 / V, 16, true>(p, dw, db, st);
     if (p.H <= 32 * 8 * 24) return bwd_as<T, V, 8 / V, 24, V == 8>(p, dw, db, st);
-    if constexpr (V == 1)
-        if (p.H <= 32 * 8 * 32) return bwd_as<T, V, 8, 32, false>(p, dw, db, st);
-    if (p.H <= 32 * 16 * 16) return bwd_as<T, V, 16 / V, 16, false>(p, dw, db, st);
-    return bwd_as<T, V, 16 / V, 32, false>(p, dw, db, st);
+    if (p.H <= 32 * 8 * 32) {
+        if constexpr (V == 1 || sizeof(T) == 4) return bwd_as<T, V, 8 / V, 32, false, true>(p, dw, db, st);
+        else return bwd_as<T, V, 16 / V, 16, false>(p, dw, db, st);
+    }
+    return bwd_as<T, V, 16 / V, 32, false, (V > 1)>(p, dw, db, st);
 }
 
 int width(s5_dtype dtype, int H, std::initializer_list<long long> lds) {

@@ -179,3 +179,34 @@ def test_offsets_past_32_bits():
     x = big.as_strided((N, H), (ld, 1))
     x.copy_(t["x"])
     assert same(run(dict(t, x=x)), run(t))
+
+
+# several rows a block where the weights' gradients are summed in shared memory, and on both sides of where that begins
+WIDE = [6144, 6145, 6148, 7001, 7002, 8191, 8192, 8193, 8200, 12289, 12290, 16384]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("H", WIDE)
+def test_wide_rows_add_up(H, kind):
+    t = make(500, H, kind, residual=H % 4 != 1, seed=H + 1)
+    check(t)
+    first = run(t)
+    assert same(run(t), first)
+    only = dict(t, w=None, b=None)
+    assert run(only)["dweight"] is None
+    check(only)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("H", [7001, 12000, 12290])
+def test_wide_rows_in_place(H, kind):
+    t = make(320, H, kind, seed=H + 2)
+    want, lib, st = run(t), api._native.lib(), torch.cuda.current_stream().cuda_stream
+    work = torch.empty(api.s5_add_layernorm_workspace_size(H), dtype=torch.uint8, device="cuda")
+    for which in ("x", "r", "dy", "dt"):
+        u = {n: a.clone() for n, a in t.items()}
+        dw, db = torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+        at = [a for n in ("x", "r", "dy", "dt") for a in (u[n].data_ptr(), H)]
+        assert lib.s5_add_layernorm_backward(*at, kind == "bf16", u["w"].data_ptr(), want["saved"].data_ptr(), 320, H,
+                                             u[which].data_ptr(), H, dw.data_ptr(), db.data_ptr(), work.data_ptr(), work.numel(), st) == 0
+        assert same(u[which], want["dx"]) and same(dw, want["dweight"]) and same(db, want["dbias"])
