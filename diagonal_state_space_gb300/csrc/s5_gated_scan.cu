@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::BLOCKS) gated_scan_bwd_kernel
             A = one, E = none;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                if (marks >> s & 1) a[s] = none, ns[s] = GATED ? g[s] : one;
+                if (marks >> s & 1) a[s] = none, ns[s] = GATED ? g[s] : one, r[s] = none;
                 const bool behind = mine + s >= k.len;
                 if (behind) a[s] = one, ns[s] = none;
                 E = k.applied(a[s], E, behind ? none : ns[s] * k.load(p, now, t0, s, 0, from, ld));
@@ -569,23 +569,30 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::BLOCKS) gated_scan_bwd_kernel
         char *to3 = GATED ? reinterpret_cast<char *>(static_cast<T *>(p.dgx) + last * p.lddgx + k.c) : nullptr;
 #pragma unroll
         for (int s = S - 1; s >= 0; --s) {
-            const bool behind = slow && mine + s >= k.len;
-            const M G = behind ? z : k.load(p, now, t0, s, 2, from, ld) + z;
-            const M t = G * D[s] * r[s], o1 = G * ns[s], w = rate * t;   // t: dla r
-            M o2, o3;
+            if (slow && mine + s >= k.len) {             // zeros; the gates there, which may be NaN, meet nothing
+                if (k.c < p.C && mine + s < p.L) {
+                    Vec<T, V>::store(reinterpret_cast<T *>(to1), none.v);
+                    Vec<T, V>::store(reinterpret_cast<T *>(to2), none.v);
+                    if (GATED) Vec<T, V>::store(reinterpret_cast<T *>(to3), none.v);
+                }
+            } else {
+                const M G = k.load(p, now, t0, s, 2, from, ld) + z;
+                const M Gz = slow && (marks >> s & 1) ? none : G;        // a reset's decay has no gradient, nor what is before
+                const M t = Gz * D[s] * r[s], o1 = G * ns[s], w = rate * t;   // t: dla r
+                M o2, o3;
 #pragma unroll
-            for (int v = 0; v < V; ++v) drate[v] -= t[v], o2[v] = fmaf(w[v], -r[s][v], w[v]);
-            z = a[s] * G;
-            if (slow && (marks >> s & 1)) z = none;
-            if (GATED) {
-                const M q = behind ? none : o1 * k.load(p, now, t0, s, 0, from, ld);
+                for (int v = 0; v < V; ++v) drate[v] -= t[v], o2[v] = fmaf(w[v], -r[s][v], w[v]);
+                z = a[s] * Gz;
+                if (GATED) {
+                    const M q = o1 * k.load(p, now, t0, s, 0, from, ld);
 #pragma unroll
-                for (int v = 0; v < V; ++v) o3[v] = fmaf(q[v], -g[s][v], q[v]);
-            }
-            if (k.c < p.C && (!slow || mine + s < p.L)) {
-                Vec<T, V>::store(reinterpret_cast<T *>(to1), o1.v);
-                Vec<T, V>::store(reinterpret_cast<T *>(to2), o2.v);
-                if (GATED) Vec<T, V>::store(reinterpret_cast<T *>(to3), o3.v);
+                    for (int v = 0; v < V; ++v) o3[v] = fmaf(q[v], -g[s][v], q[v]);
+                }
+                if (k.c < p.C) {
+                    Vec<T, V>::store(reinterpret_cast<T *>(to1), o1.v);
+                    Vec<T, V>::store(reinterpret_cast<T *>(to2), o2.v);
+                    if (GATED) Vec<T, V>::store(reinterpret_cast<T *>(to3), o3.v);
+                }
             }
             to1 -= p.row[0], to2 -= p.row[1];
             if (GATED) to3 -= p.row[2];
