@@ -1,7 +1,7 @@
 // s5_gated_scan.cu -- the gated linear recurrence of each channel: whole
 // sequences, their backward pass, one token.
 //
-//   r = sigmoid(gate_a),  la = -rate r,  a = exp(la)   (0 at a reset)
+//   r = sigmoid(gate_a),  la = -rate r,  a = exp(la)   (0 and a cut at a reset)
 //   n = sqrt(1 - a^2)  (or 1),  u = sigmoid(gate_x) x  (or x)
 //   h_t = a_t h_{t-1} + n_t u_t
 // and, with G_t = dh_t + a_{t+1} G_{t+1}:
@@ -74,10 +74,11 @@ struct ScanArgs {
     long long row[3], out_step;         // bytes between two rows of the outputs, and (forward) a round's tiles
 };
 
-// A run that holds a reset has A = 0 and takes nothing over, not even NaN: zeros stay zeros whatever they are joined
-// with, and a pair applied to a state.
-__device__ __forceinline__ float join(float A, float a) { return A == 0.0f || a == 0.0f ? 0.0f : A * a; }
-__device__ __forceinline__ float apply(float A, float h, float E) { return A == 0.0f ? E : fmaf(A, h, E); }
+// A run that holds a reset takes nothing over, not even NaN: its A is negative, which no product of decays is (one that
+// vanishes is zero, and NaN stays NaN behind it), and stays so whatever it is joined with.
+constexpr float CUT = -1.0f;
+__device__ __forceinline__ float join(float A, float a) { return A < 0.0f || a < 0.0f ? CUT : A * a; }
+__device__ __forceinline__ float apply(float A, float h, float E) { return A < 0.0f ? E : fmaf(A, h, E); }
 
 // a = exp(z) and 1 - a^2 for z <= 0.  Above -1/4 the series of exp(z) - 1 up to z^6 (the rest is below 2^-23 of it).
 template <int V> __device__ __forceinline__ void decay(const Many<V> &z, Many<V> &a, Many<V> &n2) {
@@ -239,7 +240,7 @@ template <typename Sh> struct Block {
         for (int v = 0; v < V; ++v) r[v] = __shfl_xor_sync(0xffffffffu, x[v], 16);
         return r;
     }
-    // Two pairs joined and one applied, in full where resets may have left zeros.
+    // Two pairs joined and one applied, in full where resets may have left cuts.
     __device__ static M joined(bool resets, const M &a, const M &b) { return resets ? joined(a, b) : a * b; }
     __device__ static M applied(bool resets, const M &a, const M &h, const M &e) { return resets ? applied(a, h, e) : fma(a, h, e); }
     __device__ static M joined(const M &a, const M &b) {
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::BLOCKS) gated_scan_fwd_kernel
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 if (marks >> s & 1) {
-                    a[s] = none, e[s] = k.load(p, 0, t0, s, 0, from, ld);
+                    a[s] = M::all(CUT), e[s] = k.load(p, 0, t0, s, 0, from, ld);
                     if (GATED) e[s] = sigmoid(k.load(p, 0, t0, s, 2, from, ld)) * e[s];
                 }
                 if (mine + s >= k.len) a[s] = one, e[s] = none;      // leaves the state as it is
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::BLOCKS) gated_scan_bwd_kernel
             A = one, E = none;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                if (marks >> s & 1) a[s] = none, ns[s] = GATED ? g[s] : one, r[s] = none;
+                if (marks >> s & 1) a[s] = M::all(CUT), ns[s] = GATED ? g[s] : one, r[s] = none;
                 const bool behind = mine + s >= k.len;
                 if (behind) a[s] = one, ns[s] = none;
                 E = k.applied(a[s], E, behind ? none : ns[s] * k.load(p, now, t0, s, 0, from, ld));

@@ -517,6 +517,8 @@ s5_status s5_qk_norm_rotary_backward(const void *q, long long ldq, const void *k
  *   r = sigmoid(gate_a),  a = exp(-rate r),  0 at a reset
  *   n = sqrt(1 - a^2) if normalize, else 1
  *   h_t = a_t h_{t-1} + n_t sigmoid(gate_x_t) x_t       (gate_x NULL: n_t x_t)
+ * Resets alone cut: behind a state that is NaN or infinite none is finite up to
+ * the next reset, however strong the decay (infinity may turn into NaN).
  * h_last [B][C] (may be NULL, may be h0) gets the state after the row's last
  * token.  saved NULL: nothing is kept.  B ceil(C / 16) <= 2^27, L <= 2^30.
  * L = 0 leaves the state as it is; B = 0 is a no-op.
