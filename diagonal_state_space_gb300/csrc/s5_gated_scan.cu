@@ -648,12 +648,12 @@ gated_scan_step_kernel(const T *x, const T *ga, const T *gx, const float *rate, 
 // Tiles at once: the cluster that ends first when as many of them run side by
 // side as the card has room for, a wave costs two tiles to begin, and each block
 // of it works through its share of the tiles.  Room: what the driver says of this
-// kernel, asked once for each size.
-template <auto kernel> cudaError_t room(int threads, int smem, int cluster, int &clusters) {
-    static std::atomic<int> known[MAX_CLUSTER + 1];
-    if ((clusters = known[cluster].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-    cudaError_t e = allow<kernel>(smem, true);
-    if (e != cudaSuccess) return e;
+// kernel, asked once for each size and device.
+template <auto kernel> cudaError_t room(int device, int threads, int smem, int cluster, int &clusters) {
+    static std::atomic<int> known[DEVICES][MAX_CLUSTER + 1];     // 0: not asked, else one more than the clusters
+    cudaError_t e;
+    std::atomic<int> *here = device < DEVICES ? &known[device][cluster] : nullptr;
+    if (here && (clusters = here->load(std::memory_order_relaxed) - 1) >= 0) return cudaSuccess;
     if (cluster == 1) {
         int blocks = 0;
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem);
@@ -667,15 +667,18 @@ template <auto kernel> cudaError_t room(int threads, int smem, int cluster, int 
         e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
     }
     if (e != cudaSuccess) return e;
-    known[cluster].store(clusters, std::memory_order_relaxed);
+    if (here) here->store(clusters + 1, std::memory_order_relaxed);
     return cudaSuccess;
 }
 template <auto kernel> cudaError_t choose_cluster(int threads, int smem, long long chains, int tiles, int &best) {
     long long cost = -1;
+    int device = 0;
+    cudaError_t e = allow<kernel, true>(smem, device);
+    if (e != cudaSuccess) return e;
     best = 1;
     for (int n = 1; n <= MAX_CLUSTER && n <= tiles; ++n) {
         int clusters = 0;
-        const cudaError_t e = room<kernel>(threads, smem, n, clusters);
+        e = room<kernel>(device, threads, smem, n, clusters);
         if (e != cudaSuccess) return e;
         if (clusters < 1) continue;
         const long long t = (chains + clusters - 1) / clusters * ((tiles + n - 1) / n + 2);
@@ -733,7 +736,7 @@ template <typename Sh, auto kernel> cudaError_t launch_scan(ScanArgs &p, float *
     if (e != cudaSuccess) return e;
     const int parts = p.B * p.cluster;
     if (parts == 1) p.drate = drate;     // backward: nothing to sum
-    e = launch_big<kernel>(dim3((unsigned)blocks), Sh::THREADS, Sh::SMEM, Sh::SMEM, p.cluster, st, p, maps);
+    e = launch_big<kernel, true>(dim3((unsigned)blocks), Sh::THREADS, Sh::SMEM, Sh::SMEM, p.cluster, st, p, maps);
     if (e != cudaSuccess || !drate || parts == 1) return e;
     return launch(gated_scan_rate_kernel, dim3((p.C + 31) / 32), sum_threads(parts), 0, 1, st, (const float *)p.drate, parts, p.C, drate);
 }

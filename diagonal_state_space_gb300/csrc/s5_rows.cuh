@@ -179,22 +179,23 @@ cudaError_t launch(void (*k)(Ks...), dim3 grid, int threads, size_t smem, int cl
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
-// What a kernel may ask for at a launch, set once for each device: dynamic shared memory up to `most` bytes, and
-// clusters of more than eight blocks.
-template <auto kernel> cudaError_t allow(int most, bool large_clusters) {
+// What a kernel may ask for at a launch, set once for each device: dynamic shared memory up to `most` bytes, and where
+// LARGE says so clusters of more than eight blocks, whatever the first launch on a device takes.
+constexpr int DEVICES = 64;              // of which something is remembered
+template <auto kernel, bool LARGE> cudaError_t allow(int most, int &device) {
     static std::atomic<unsigned long long> done{0};
-    int device = 0;
     cudaError_t e = cudaGetDevice(&device);
-    if (e != cudaSuccess || (device < 64 && done.load(std::memory_order_relaxed) >> device & 1)) return e;
+    if (e != cudaSuccess || (device < DEVICES && done.load(std::memory_order_relaxed) >> device & 1)) return e;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e == cudaSuccess && large_clusters) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && device < 64) done.fetch_or(1ull << device, std::memory_order_relaxed);
+    if (LARGE && e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && device < DEVICES) done.fetch_or(1ull << device, std::memory_order_relaxed);
     return e;
 }
 // The launch of such a kernel.
-template <auto kernel, typename... As>
+template <auto kernel, bool LARGE = false, typename... As>
 cudaError_t launch_big(dim3 grid, int threads, size_t smem, int most, int cluster, cudaStream_t st, As... args) {
-    const cudaError_t e = allow<kernel>(most, cluster > 1);
+    int device = 0;
+    const cudaError_t e = allow<kernel, LARGE>(most, device);
     return e != cudaSuccess ? e : launch(kernel, grid, threads, smem, cluster, st, args...);
 }
 
