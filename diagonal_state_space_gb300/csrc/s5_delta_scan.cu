@@ -451,6 +451,7 @@ int scan_fault_take() { return fault_take(); }
 }  // namespace s5
 
 extern "C" int s5_delta_fault(void) {
+    if (cudaDeviceSynchronize() != cudaSuccess) return -1;       // copies alone wait for no stream that does not block
     const int f[3] = {s5::delta::prep_fault_take(), s5::delta::scan_fault_take(), s5::delta::adjoint_fault_take()};
     return f[0] < 0 || f[1] < 0 || f[2] < 0 ? -1 : f[0] | f[1] | f[2];
 }

@@ -880,6 +880,7 @@ extern "C" s5_status s5_gated_scan_backward(const void *x, long long ldx, const 
 
 extern "C" int s5_gated_scan_fault(void) {
     int v = 0, zero = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess) return -1;       // a copy alone waits for no stream that does not block
     if (cudaMemcpyFromSymbol(&v, g_scan_fault, sizeof(int)) != cudaSuccess) return -1;
     if (v && cudaMemcpyToSymbol(g_scan_fault, &zero, sizeof(int)) != cudaSuccess) return -1;
     return v;

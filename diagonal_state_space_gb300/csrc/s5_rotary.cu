@@ -1044,6 +1044,7 @@ extern "C" unsigned long long s5_rotary_wait_limit(unsigned long long ns) { retu
 
 extern "C" int s5_rotary_fault(void) {
     int v = 0, zero = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess) return -1;       // a copy alone waits for no stream that does not block
     if (cudaMemcpyFromSymbol(&v, g_rotary_fault, sizeof(int)) != cudaSuccess) return -1;
     if (v && cudaMemcpyToSymbol(g_rotary_fault, &zero, sizeof(int)) != cudaSuccess) return -1;
     return v;
