@@ -11,8 +11,12 @@
 // pitches, other devices and messages included.  An error of the call comes back as its status, an int.
 #include <Python.h>
 
-#include <ATen/core/Tensor.h>
+#include <ATen/Context.h>
 #include <ATen/EmptyTensor.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <ATen/record_function.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -34,6 +38,7 @@ struct Reader {
     PyObject *const *args;
     bool ok = true;
     c10::DeviceIndex device = -1;
+    int bare = -1;                       // whether memory is all that a new array takes; -1: not asked yet
 
     const Tensor *tensor(int i) {
         if (!ok || !THPVariable_CheckExact(args[i])) return ok = false, nullptr;
@@ -75,16 +80,22 @@ struct Reader {
         return ok = false, 0;
     }
     float scale(int i, int64_t head) { return none(i) ? (float)std::pow((double)head, -0.5) : (float)number(i); }
+    // at::empty on the current CUDA device, which is `like`'s.  Its way there takes as long as a small kernel, so it is
+    // called only where something on that way would do more than allocate: a dispatch mode, a transform or a tracer, which
+    // add a dispatch key of theirs; an observer of operators, as a profiler; filling of what is not written yet.
+    Tensor make(at::IntArrayRef shape, const Tensor &like, at::ScalarType type) {
+        if (bare < 0)
+            bare = (c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set).empty() &&
+                   !at::getStepCallbacksUnlessEmpty(at::RecordScope::FUNCTION).has_value() && !at::globalContext().deterministicAlgorithms();
+        if (!bare) return at::empty(shape, like.options().dtype(type));
+        return Tensor(at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                type, std::nullopt));
+    }
+    Tensor make(at::IntArrayRef shape, const Tensor &like) { return make(shape, like, like.scalar_type()); }
     s5_stream_t stream() const { return (s5_stream_t)c10::cuda::getCurrentCUDAStream(device).stream(); }
 };
 
 s5_dtype dtype(const Tensor &t) { return t.scalar_type() == BF16 ? S5_BF16 : S5_F32; }
-// On the current CUDA device, which is `like`'s (Reader): what at::empty does, without its way there.
-Tensor make(at::IntArrayRef shape, const Tensor &, at::ScalarType type) {
-    return Tensor(at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA), type,
-                                            std::nullopt));
-}
-Tensor make(at::IntArrayRef shape, const Tensor &like) { return make(shape, like, like.scalar_type()); }
 template <typename T = float> T *data(const Tensor *t) { return t ? static_cast<T *>(t->data_ptr()) : nullptr; }
 bool fits(std::initializer_list<int64_t> sizes) {
     for (int64_t n : sizes)
@@ -132,7 +143,7 @@ ENTRY(delta_step, 8) {
     const Tensor *state = r.like(5, F32, {B, Hv, Dk, Dv}), *given = r.maybe(7, type, v->sizes());
     const float scale = r.scale(6, Dk);
     if (!r.ok || v->scalar_type() != type || v->size(0) != B || !fits({B, Hk, Dk, Hv, Dv})) Py_RETURN_NONE;
-    const Tensor o = given ? *given : make(v->sizes(), *v);
+    const Tensor o = given ? *given : r.make(v->sizes(), *v);
     return result(s5_delta_step(q->data_ptr(), k->data_ptr(), v->data_ptr(), dtype(*q), data(g), data(beta), scale, (int)B,
                                 (int)Hk, (int)Hv, (int)Dk, (int)Dv, data(state), o.data_ptr(), r.stream()),
                   o);
@@ -169,8 +180,8 @@ ENTRY(delta_forward, 11) {
     if (!r.ok || !n.ok(*q, *v)) Py_RETURN_NONE;
     const size_t need = work ? (size_t)work->numel() : n.workspace(false);
     if (need == 0) Py_RETURN_NONE;
-    const Tensor o = given ? *given : make(v->sizes(), *v), s = ends ? make(states, *q, F32) : last ? *last : Tensor();
-    const Tensor w = work ? *work : make({(int64_t)need}, *q, at::kByte);
+    const Tensor o = given ? *given : r.make(v->sizes(), *v), s = ends ? r.make(states, *q, F32) : last ? *last : Tensor();
+    const Tensor w = work ? *work : r.make({(int64_t)need}, *q, at::kByte);
     const s5_status code = s5_delta_forward(
         q->data_ptr(), n.Hk * n.Dk, k->data_ptr(), n.Hk * n.Dk, v->data_ptr(), n.Hv * n.Dv, dtype(*q), data(g), data(beta),
         data(s0), scale, (int)n.B, (int)n.L, (int)n.Hk, (int)n.Hv, (int)n.Dk, (int)n.Dv, o.data_ptr(), n.Hv * n.Dv,
@@ -193,9 +204,9 @@ ENTRY(delta_backward, 11) {
     if (!r.ok || !n.ok(*q, *v)) Py_RETURN_NONE;
     const size_t need = work ? (size_t)work->numel() : n.workspace(true);
     if (need == 0) Py_RETURN_NONE;
-    const Tensor dq = make(q->sizes(), *q), dk = make(q->sizes(), *q), dv = make(v->sizes(), *v);
-    const Tensor dg = make(gates, *q, F32), dbeta = make(gates, *q, F32), ds0 = s0 ? make(states, *q, F32) : Tensor();
-    const Tensor w = work ? *work : make({(int64_t)need}, *q, at::kByte);
+    const Tensor dq = r.make(q->sizes(), *q), dk = r.make(q->sizes(), *q), dv = r.make(v->sizes(), *v);
+    const Tensor dg = r.make(gates, *q, F32), dbeta = r.make(gates, *q, F32), ds0 = s0 ? r.make(states, *q, F32) : Tensor();
+    const Tensor w = work ? *work : r.make({(int64_t)need}, *q, at::kByte);
     const s5_status code = s5_delta_backward(
         q->data_ptr(), n.Hk * n.Dk, k->data_ptr(), n.Hk * n.Dk, v->data_ptr(), n.Hv * n.Dv, dtype(*q), data(g), data(beta),
         data(s0), scale, (int)n.B, (int)n.L, (int)n.Hk, (int)n.Hv, (int)n.Dk, (int)n.Dv, dout->data_ptr(), n.Hv * n.Dv,
@@ -239,7 +250,7 @@ ENTRY(rotary, 7) {
     const double amplitude = r.number(4);
     const Tensor *given = r.maybe(6, x->scalar_type(), x->sizes());
     if (!r.ok) Py_RETURN_NONE;
-    const Tensor out = given ? *given : make(x->sizes(), *x);
+    const Tensor out = given ? *given : r.make(x->sizes(), *x);
     const long long ld = t.H * t.D;
     return result(s5_rotary(x->data_ptr(), ld, dtype(*x), t.pos(), data<double>(t.freq), t.rot, (s5_rotary_layout)layout,
                             (float)amplitude, inverse, t.T, (int)t.H, (int)t.D, out.data_ptr(), ld, r.stream()),
@@ -260,7 +271,7 @@ ENTRY(qk_norm_rotary, 12) {
     if (!r.ok || k->scalar_type() != type || k->size(-1) != t.D || !fits({Hk}) ||
         k->sizes().slice(0, tokens) != q->sizes().slice(0, tokens))
         Py_RETURN_NONE;
-    const Tensor qo = gq ? *gq : make(q->sizes(), *q), ko = gk ? *gk : make(k->sizes(), *k);
+    const Tensor qo = gq ? *gq : r.make(q->sizes(), *q), ko = gk ? *gk : r.make(k->sizes(), *k);
     const long long lq = t.H * t.D, lk = Hk * t.D;
     return result(s5_qk_norm_rotary(q->data_ptr(), lq, k->data_ptr(), lk, dtype(*q), data(wq), data(wk), (s5_norm)norm,
                                     (float)eps, t.pos(), data<double>(t.freq), t.rot, (s5_rotary_layout)layout,
@@ -287,9 +298,9 @@ ENTRY(qk_norm_rotary_backward, 13) {
     const bool weights = wq || wk;
     const size_t need = work ? (size_t)work->numel() : weights ? s5_qk_norm_rotary_workspace_size((int)t.D) : 0;
     if (weights && need == 0) Py_RETURN_NONE;
-    const Tensor dq = make(q->sizes(), *q), dk = make(k->sizes(), *k);
-    const Tensor dwq = wq ? make({t.D}, *q, F32) : Tensor(), dwk = wk ? make({t.D}, *q, F32) : Tensor();
-    const Tensor w = work ? *work : weights ? make({(int64_t)need}, *q, at::kByte) : Tensor();
+    const Tensor dq = r.make(q->sizes(), *q), dk = r.make(k->sizes(), *k);
+    const Tensor dwq = wq ? r.make({t.D}, *q, F32) : Tensor(), dwk = wk ? r.make({t.D}, *q, F32) : Tensor();
+    const Tensor w = work ? *work : weights ? r.make({(int64_t)need}, *q, at::kByte) : Tensor();
     const long long lq = t.H * t.D, lk = Hk * t.D;
     const s5_status code = s5_qk_norm_rotary_backward(
         q->data_ptr(), lq, k->data_ptr(), lk, dtype(*q), data(wq), data(wk), (s5_norm)norm, (float)eps, t.pos(),
@@ -326,7 +337,7 @@ const Tensor *channels(Reader &r, int i, int dims) {
     if (r.ok && ((t->scalar_type() != F32 && t->scalar_type() != BF16) || (dims ? t->dim() != dims : t->dim() < 1))) r.ok = false;
     return t;
 }
-Tensor given_or(const Tensor *t, const Tensor &like) { return t ? *t : make(like.sizes(), like); }
+Tensor given_or(Reader &r, const Tensor *t, const Tensor &like) { return t ? *t : r.make(like.sizes(), like); }
 template <typename T = float> T *at_or_null(const Tensor &t) { return t.defined() ? data<T>(&t) : nullptr; }
 
 // x: the buffer that the forward call fills
@@ -335,12 +346,12 @@ ENTRY(gated_scan_saved, 1) {
     if (!r.ok || !fits({x->size(0), x->size(1), x->size(2)})) Py_RETURN_NONE;
     const size_t n = s5_gated_scan_saved_size((int)x->size(0), (int)x->size(1), (int)x->size(2));
     if (n == 0) Py_RETURN_NONE;
-    return THPVariable_Wrap(make({(int64_t)n}, *x, at::kByte));
+    return THPVariable_Wrap(r.make({(int64_t)n}, *x, at::kByte));
 }
 ENTRY(layernorm_saved, 1) {
     const Tensor *x = channels(r, 0, 0);
     if (!r.ok) Py_RETURN_NONE;
-    return THPVariable_Wrap(make({x->numel() / x->size(-1), 2}, *x, F32));
+    return THPVariable_Wrap(r.make({x->numel() / x->size(-1), 2}, *x, F32));
 }
 
 // x, gate_a, gate_x, rate, h0, h_last, reset, lengths, normalize, h, saved
@@ -357,7 +368,7 @@ ENTRY(gated_scan_forward, 11) {
     const bool normalize = flag(r, 8);
     const Tensor *given = r.maybe(9, type, x->sizes()), *saved = r.none(10) ? nullptr : r.bytes(10);
     if (!r.ok || !fits({B, L, C})) Py_RETURN_NONE;
-    const Tensor h = given_or(given, *x), s = ends ? make({B, C}, *x, F32) : last ? *last : Tensor();
+    const Tensor h = given_or(r, given, *x), s = ends ? r.make({B, C}, *x, F32) : last ? *last : Tensor();
     const s5_status code =
         s5_gated_scan_forward(x->data_ptr(), C, ga->data_ptr(), C, data<void>(gx), C, dtype(*x), data(rate), data(h0), m.bytes(),
                               m.ints(), normalize, (int)B, (int)L, (int)C, h.data_ptr(), C, at_or_null(s), data<void>(saved),
@@ -380,9 +391,9 @@ ENTRY(gated_scan_backward, 12) {
     if (!r.ok || !fits({B, L, C})) Py_RETURN_NONE;
     const size_t need = work ? (size_t)work->numel() : s5_gated_scan_workspace_size((int)B, (int)L, (int)C);
     if (need == 0) Py_RETURN_NONE;
-    const Tensor dx = make(x->sizes(), *x), dga = make(x->sizes(), *x), dgx = gx ? make(x->sizes(), *x) : Tensor();
-    const Tensor drate = make({C}, *x, F32), dh0 = h0 ? make({B, C}, *x, F32) : Tensor();
-    const Tensor w = work ? *work : make({(int64_t)need}, *x, at::kByte);
+    const Tensor dx = r.make(x->sizes(), *x), dga = r.make(x->sizes(), *x), dgx = gx ? r.make(x->sizes(), *x) : Tensor();
+    const Tensor drate = r.make({C}, *x, F32), dh0 = h0 ? r.make({B, C}, *x, F32) : Tensor();
+    const Tensor w = work ? *work : r.make({(int64_t)need}, *x, at::kByte);
     const s5_status code = s5_gated_scan_backward(
         x->data_ptr(), C, ga->data_ptr(), C, data<void>(gx), C, dtype(*x), data(rate), m.bytes(), m.ints(), normalize, (int)B, (int)L,
         (int)C, dh->data_ptr(), C, data(last), saved->data_ptr(), saved->numel(), dx.data_ptr(), C, dga.data_ptr(), C,
@@ -407,7 +418,7 @@ ENTRY(gated_scan_step, 7) {
     const bool normalize = flag(r, 5);
     const Tensor *given = r.maybe(6, type, x->sizes());
     if (!r.ok || !fits({B, C})) Py_RETURN_NONE;
-    const Tensor h = given_or(given, *x);
+    const Tensor h = given_or(r, given, *x);
     return result(s5_gated_scan_step(x->data_ptr(), ga->data_ptr(), data<void>(gx), dtype(*x), data(rate), normalize, (int)B, (int)C,
                                      data(state), h.data_ptr(), r.stream()),
                   h);
@@ -434,7 +445,7 @@ ENTRY(short_conv_forward, 9) {
     const Marks m(r, 6, B, L);
     const Tensor *given = r.maybe(8, type, x->sizes());
     if (!r.ok || !fits({B, L, C, K})) Py_RETURN_NONE;
-    const Tensor y = given_or(given, *x), s = ends ? make({B, K - 1, C}, *x) : last ? *last : Tensor();
+    const Tensor y = given_or(r, given, *x), s = ends ? r.make({B, K - 1, C}, *x) : last ? *last : Tensor();
     const s5_status code = s5_short_conv_forward(x->data_ptr(), C, dtype(*x), data(w), data(bias), (s5_activation)act, data<void>(past),
                                                  m.bytes(), m.ints(), (int)B, (int)L, (int)C, (int)K, y.data_ptr(), C,
                                                  at_or_null<void>(s), r.stream());
@@ -455,9 +466,9 @@ ENTRY(short_conv_backward, 10) {
     if (!r.ok || !fits({B, L, C, K})) Py_RETURN_NONE;
     const size_t need = work ? (size_t)work->numel() : s5_short_conv_workspace_size((int)C, (int)K);
     if (need == 0) Py_RETURN_NONE;
-    const Tensor dx = make(x->sizes(), *x), dw = make({C, K}, *x, F32), db = bias ? make({C}, *x, F32) : Tensor();
-    const Tensor dpast = past ? make({B, K - 1, C}, *x) : Tensor();
-    const Tensor ws = work ? *work : make({(int64_t)need}, *x, at::kByte);
+    const Tensor dx = r.make(x->sizes(), *x), dw = r.make({C, K}, *x, F32), db = bias ? r.make({C}, *x, F32) : Tensor();
+    const Tensor dpast = past ? r.make({B, K - 1, C}, *x) : Tensor();
+    const Tensor ws = work ? *work : r.make({(int64_t)need}, *x, at::kByte);
     const s5_status code = s5_short_conv_backward(
         x->data_ptr(), C, dtype(*x), data(w), data(bias), (s5_activation)act, data<void>(past), m.bytes(), m.ints(), (int)B, (int)L,
         (int)C, (int)K, dy->data_ptr(), C, data<void>(last), dx.data_ptr(), C, data(&dw), at_or_null(db), at_or_null<void>(dpast),
@@ -479,7 +490,7 @@ ENTRY(short_conv_step, 6) {
     const int act = r.code(4);
     const Tensor *given = r.maybe(5, type, x->sizes());
     if (!r.ok || !fits({B, C, K})) Py_RETURN_NONE;
-    const Tensor y = given_or(given, *x);
+    const Tensor y = given_or(r, given, *x);
     return result(s5_short_conv_step(x->data_ptr(), dtype(*x), data(w), data(bias), (s5_activation)act, (int)B, (int)C, (int)K,
                                      state->data_ptr(), y.data_ptr(), r.stream()),
                   y);
@@ -495,7 +506,7 @@ ENTRY(add_layernorm, 8) {
     const double eps = r.number(4);
     const Tensor *gy = r.maybe(5, type, x->sizes()), *gt = r.maybe(6, type, x->sizes()), *saved = r.maybe(7, F32, {N, 2});
     if (!r.ok || !fits({H}) || (gt && !residual)) Py_RETURN_NONE;
-    const Tensor y = given_or(gy, *x), total = residual ? given_or(gt, *x) : Tensor();
+    const Tensor y = given_or(r, gy, *x), total = residual ? given_or(r, gt, *x) : Tensor();
     const s5_status code =
         s5_add_layernorm(x->data_ptr(), H, data<void>(residual), H, dtype(*x), data(w), data(bias), (float)eps, N, (int)H, y.data_ptr(),
                          H, at_or_null<void>(total), H, data(saved), r.stream());
@@ -515,8 +526,8 @@ ENTRY(add_layernorm_backward, 8) {
     if (!r.ok || !fits({H})) Py_RETURN_NONE;
     const size_t need = work ? (size_t)work->numel() : w || bias ? s5_add_layernorm_workspace_size((int)H) : 0;
     if ((w || bias) && need == 0) Py_RETURN_NONE;
-    const Tensor dx = make(x->sizes(), *x), dw = w ? make({H}, *x, F32) : Tensor(), db = bias ? make({H}, *x, F32) : Tensor();
-    const Tensor ws = work ? *work : need ? make({(int64_t)need}, *x, at::kByte) : Tensor();
+    const Tensor dx = r.make(x->sizes(), *x), dw = w ? r.make({H}, *x, F32) : Tensor(), db = bias ? r.make({H}, *x, F32) : Tensor();
+    const Tensor ws = work ? *work : need ? r.make({(int64_t)need}, *x, at::kByte) : Tensor();
     const s5_status code = s5_add_layernorm_backward(x->data_ptr(), H, data<void>(residual), H, dy->data_ptr(), H, data<void>(dt), H,
                                                      dtype(*x), data(w), data(saved), N, (int)H, dx.data_ptr(), H, at_or_null(dw),
                                                      at_or_null(db), at_or_null<void>(ws), need, r.stream());
