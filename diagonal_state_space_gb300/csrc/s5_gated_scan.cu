@@ -766,6 +766,7 @@ int width(s5_dtype dtype, int L, int C, std::initializer_list<long long> lds) {
 s5_status check_scan(const ScanArgs &p, s5_dtype dtype) {
     if (!type_ok(dtype) || p.B < 0 || p.L < 0 || p.C < 1) return S5_ERR_INVALID_ARGUMENT;
     // the narrowest blocks, in the largest cluster, within a grid; parts within an int
+    if (p.C > MAX_C) return S5_ERR_UNSUPPORTED;
     if ((long long)p.B * ((p.C + 15) / 16) > (1ll << 27)) return S5_ERR_UNSUPPORTED;
     if (p.L > (1 << 30)) return S5_ERR_UNSUPPORTED;
     return S5_OK;

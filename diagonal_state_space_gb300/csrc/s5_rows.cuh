@@ -200,6 +200,7 @@ cudaError_t launch_big(dim3 grid, int threads, size_t smem, int most, int cluste
 }
 
 constexpr int SMS = 152;
+constexpr int MAX_C = 0x7fffff00;        // channels: the last block of them ends up to 127 behind, still within an int
 
 // Sums of `parts` rows of n columns, in a fixed order: a warp's lanes have 32
 // columns, the block's warps (as many as sum_threads says) take turns at the

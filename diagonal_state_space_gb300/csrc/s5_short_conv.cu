@@ -542,7 +542,7 @@ template <typename T> cudaError_t step(const StepArgs &a, int V, int K, cudaStre
 s5_status check_conv(s5_dtype dtype, const float *w, const float *bias, int act, int B, int L, int C, int K) {
     if (!type_ok(dtype) || B < 0 || L < 0 || C < 1 || K < 1) return S5_ERR_INVALID_ARGUMENT;
     if (act != S5_ACT_NONE && act != S5_ACT_SILU) return S5_ERR_INVALID_ARGUMENT;
-    if (K < 2 || K > MAX_TAPS) return S5_ERR_UNSUPPORTED;
+    if (K < 2 || K > MAX_TAPS || C > MAX_C) return S5_ERR_UNSUPPORTED;
     // segments of 16 tokens or more, and blocks of 32 channels times those of four segments, within an int
     if (L > (1 << 30) || (long long)B * ((L + 7) / 8) > (1ll << 30)) return S5_ERR_UNSUPPORTED;
     if (((long long)B * ((L + 7) / 8) / 4 + 1) * ((C + 31) / 32) > (1ll << 30) || (long long)B * C > (1ll << 36)) return S5_ERR_UNSUPPORTED;
@@ -582,7 +582,7 @@ extern "C" s5_status s5_short_conv_forward(const void *x, long long ldx, s5_dtyp
 }
 
 extern "C" size_t s5_short_conv_workspace_size(int C, int K) {
-    if (C < 1 || K < 2 || K > MAX_TAPS) return 0;
+    if (C < 1 || C > MAX_C || K < 2 || K > MAX_TAPS) return 0;
     // along_blocks() times C is the most with the widest blocks of channels
     return 256 + sizeof(float) * (size_t)(K + 1) * C * ((BLOCKS + (C + 127) / 128 - 1) / ((C + 127) / 128));
 }

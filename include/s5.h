@@ -520,7 +520,8 @@ s5_status s5_qk_norm_rotary_backward(const void *q, long long ldq, const void *k
  * Resets alone cut: behind a state that is NaN or infinite none is finite up to
  * the next reset, however strong the decay (infinity may turn into NaN).
  * h_last [B][C] (may be NULL, may be h0) gets the state after the row's last
- * token.  saved NULL: nothing is kept.  B ceil(C / 16) <= 2^27, L <= 2^30.
+ * token.  saved NULL: nothing is kept.  B ceil(C / 16) <= 2^27, L <= 2^30,
+ * C <= 2^31 - 256.
  * L = 0 leaves the state as it is; B = 0 is a no-op.
  */
 size_t s5_gated_scan_saved_size(int B, int L, int C);
@@ -567,7 +568,7 @@ s5_status s5_gated_scan_step(const void *x, const void *gate_a, const void *gate
  * (NULL); those before a reset are zeros.  past_out [B][K-1][C] (may be NULL, may
  * be past) gets the row's last K - 1 inputs, the past's among them where the row
  * has fewer, zeros for what a reset cut off: the next call's past.
- * B ceil(L / 8) <= 2^30, and that over 4 times ceil(C / 32).
+ * B ceil(L / 8) <= 2^30, and that over 4 times ceil(C / 32); C <= 2^31 - 256.
  */
 s5_status s5_short_conv_forward(const void *x, long long ldx, s5_dtype dtype, const float *weight, const float *bias,
                                 s5_activation activation, const void *past, const unsigned char *reset,
