@@ -748,6 +748,7 @@ template <typename Sh> cudaError_t run_fwd(ScanArgs &p, cudaStream_t st) {
     return launch_scan<Sh, gated_scan_fwd_kernel<Sh, false, false>>(p, nullptr, st);
 }
 template <typename Sh> cudaError_t run_bwd(ScanArgs &p, float *drate, cudaStream_t st) {
+    static_assert(Sh::TILE >= KEEP, "the workspace has a part for each tile of KEEP tokens, up to a cluster's");
     if (p.gx && p.normalize) return launch_scan<Sh, gated_scan_bwd_kernel<Sh, true, true>>(p, drate, st);
     if (p.gx) return launch_scan<Sh, gated_scan_bwd_kernel<Sh, true, false>>(p, drate, st);
     if (p.normalize) return launch_scan<Sh, gated_scan_bwd_kernel<Sh, false, true>>(p, drate, st);
@@ -793,7 +794,8 @@ extern "C" size_t s5_gated_scan_workspace_size(int B, int L, int C) {
     ScanArgs p = {};
     p.B = B, p.L = L, p.C = C;
     if (check_scan(p, S5_F32) != S5_OK) return 0;
-    return 256 + sizeof(float) * (size_t)B * MAX_CLUSTER * C;
+    const int tiles = L <= KEEP ? 1 : (L + KEEP - 1) / KEEP;     // a cluster has no more blocks than a row has tiles
+    return 256 + sizeof(float) * (size_t)B * (tiles < MAX_CLUSTER ? tiles : MAX_CLUSTER) * C;
 }
 
 extern "C" s5_status s5_gated_scan_forward(const void *x, long long ldx, const void *gate_a, long long ldga, const void *gate_x,
