@@ -448,8 +448,9 @@ short_conv_step_kernel(const T *x, const float *w, const float *bias, int act, l
 }
 
 // ------------------------------------------------------------------ launches
-// Channels of a lane: `most` (four; two where two rings of 32-bit rows would fill the shared memory), two where more
+// Channels of a lane: `most` (four; backward two where two rings of 32-bit rows would fill the shared memory), two where more
 // taps would fill the registers or the sizes ask for it, or one.
+template <typename T> constexpr int BWD_MOST = sizeof(T) == 2 ? 4 : 2;
 int vector(int C, int K, int most, std::initializer_list<long long> lds) {
     int V = K > 4 ? 2 : most;
     while (C % V) V /= 2;
@@ -482,7 +483,8 @@ template <typename T, int V, int K> cudaError_t run_fwd(ConvArgs &p, cudaStream_
     if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     if constexpr (V * sizeof(T) >= 4)
         if (copies<T>(V, p.C, {p.ldx, p.ldy})) return start_fwd<T, V, K, true>(p, (int)blocks, st);
-    return start_fwd<T, V, K, false>(p, (int)blocks, st);
+    if constexpr (V * sizeof(T) < 16) return start_fwd<T, V, K, false>(p, (int)blocks, st);
+    return cudaErrorInvalidValue;        // rows of whole 16 bytes a lane can be copied
 }
 
 int along_blocks(long long segments, int across) {
@@ -519,25 +521,26 @@ template <typename T, int V, int K> cudaError_t run_step(const StepArgs &a, cuda
                   a.w, a.bias, a.act, total, a.C, static_cast<T *>(a.state), static_cast<T *>(a.y));
 }
 
-// f<T, V, K>() for the run-time vector and tap counts.
+// f<T, V, K>() for the run-time vector, of `most` channels, and tap counts.
 #define S5_TAPS(f, T, V, K, ...) \
     case K: return f<T, V, K>(__VA_ARGS__);
 #define S5_FEW(f, T, V, ...) S5_TAPS(f, T, V, 2, __VA_ARGS__) S5_TAPS(f, T, V, 3, __VA_ARGS__) S5_TAPS(f, T, V, 4, __VA_ARGS__)
 #define S5_MORE(f, T, V, ...) \
     S5_TAPS(f, T, V, 5, __VA_ARGS__) S5_TAPS(f, T, V, 6, __VA_ARGS__) S5_TAPS(f, T, V, 7, __VA_ARGS__) S5_TAPS(f, T, V, 8, __VA_ARGS__)
-#define S5_BY_SIZE(f, T, V, taps, ...)                                                                        \
+#define S5_BY_SIZE(f, T, most, V, taps, ...)                                                                  \
     do {                                                                                                      \
-        if (V == 4) switch (taps) { S5_FEW(f, T, 4, __VA_ARGS__) }                                            \
+        if constexpr (most >= 4)                                                                              \
+            if (V == 4) switch (taps) { S5_FEW(f, T, 4, __VA_ARGS__) }                                        \
         if (V == 2) switch (taps) { S5_FEW(f, T, 2, __VA_ARGS__) S5_MORE(f, T, 2, __VA_ARGS__) }              \
         switch (taps) { S5_FEW(f, T, 1, __VA_ARGS__) S5_MORE(f, T, 1, __VA_ARGS__) }                          \
         return cudaErrorInvalidValue;                                                                         \
     } while (0)
 
-template <typename T> cudaError_t fwd(ConvArgs &p, int V, int K, cudaStream_t st) { S5_BY_SIZE(run_fwd, T, V, K, p, st); }
+template <typename T> cudaError_t fwd(ConvArgs &p, int V, int K, cudaStream_t st) { S5_BY_SIZE(run_fwd, T, 4, V, K, p, st); }
 template <typename T> cudaError_t bwd(ConvArgs &p, int V, int K, float *dw, float *db, cudaStream_t st) {
-    S5_BY_SIZE(run_bwd, T, V, K, p, dw, db, st);
+    S5_BY_SIZE(run_bwd, T, BWD_MOST<T>, V, K, p, dw, db, st);
 }
-template <typename T> cudaError_t step(const StepArgs &a, int V, int K, cudaStream_t st) { S5_BY_SIZE(run_step, T, V, K, a, st); }
+template <typename T> cudaError_t step(const StepArgs &a, int V, int K, cudaStream_t st) { S5_BY_SIZE(run_step, T, 4, V, K, a, st); }
 
 s5_status check_conv(s5_dtype dtype, const float *w, const float *bias, int act, int B, int L, int C, int K) {
     if (!type_ok(dtype) || B < 0 || L < 0 || C < 1 || K < 1) return S5_ERR_INVALID_ARGUMENT;
@@ -611,7 +614,7 @@ extern "C" s5_status s5_short_conv_backward(const void *x, long long ldx, s5_dty
     p.x = x, p.ldx = ldx, p.w = weight, p.bias = bias, p.act = activation, p.past = past, p.reset = reset, p.lengths = lengths;
     p.B = B, p.L = L, p.C = C, p.dy = dy, p.lddy = lddy, p.dpast_out = dpast_out, p.dx = dx, p.lddx = lddx, p.dpast = dpast;
     p.part = static_cast<float *>(workspace);
-    const int V = vector(C, K, dtype == S5_BF16 ? 4 : 2, {ldx, lddy, lddx});
+    const int V = vector(C, K, dtype == S5_BF16 ? BWD_MOST<__nv_bfloat16> : BWD_MOST<float>, {ldx, lddy, lddx});
     const cudaError_t e = dtype == S5_BF16 ? bwd<__nv_bfloat16>(p, V, K, dweight, dbias, st) : bwd<float>(p, V, K, dweight, dbias, st);
     return e == cudaSuccess ? S5_OK : cuda_failure(e);
 }
