@@ -37,6 +37,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cfloat>
 
 #include "s5_rows.cuh"
 #include "s5_sm100.cuh"
@@ -473,12 +474,8 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::BLOCKS) gated_scan_bwd_kernel
             decay(rate * r[s], a[s], n2);
             if (NORM) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float q = rsqrt_(fmaxf(n2[v], 1e-37f));
-                    n[v] = q;
-                    inv[v] = n2[v] > 0.0f ? q : 0.0f;    // no slope at 0
-                }
-                n = n * n2;
+                for (int v = 0; v < V; ++v) inv[v] = n2[v] >= FLT_MIN ? rsqrt_(n2[v]) : 0.0f;   // below the forward root is 0: no slope
+                n = inv * n2;
             }
             ns[s] = GATED ? n * g[s] : n;
             D[s] = a[s] * a[s] * (inv * (GATED ? g[s] * x : x));

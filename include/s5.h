@@ -536,7 +536,8 @@ s5_status s5_gated_scan_forward(const void *x, long long ldx, const void *gate_a
  * forward's inputs and its `saved` buffer (the state every 32 tokens).  With
  * u = sigmoid(gate_x) x, s = sigmoid(gate_x):
  *   G_t = dh_t + a_{t+1} G_{t+1},  dla = G (a h_{t-1} - a^2 / n u)   (0 at a reset;
- *     the second part 0 where rate r = 0, whose root has no slope, or not normalize)
+ *     the second part 0 where 1 - a^2 is below 2^-126, whose root is taken as 0
+ *     without a slope, or not normalize)
  *   dgate_a = -rate dla r (1 - r),  drate = -sum dla r,  dh0 = a_0 G_0,
  *   dx = G n s,  dgate_x = G n x s (1 - s).
  * dx, dgate_a, dgate_x (with gate_x) of `dtype`; drate [C] and dh0 [B][C] (NULL:
