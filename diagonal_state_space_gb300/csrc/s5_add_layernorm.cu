@@ -13,10 +13,10 @@
 // also keeps the weights' gradients of its columns over all the rows that it
 // sees; one block an SM adds its warps' sums up, and a second launch the
 // blocks'.  No atomics.  bf16: 16384 rows of 2048 with the residual 43 us forward
-// (6.2 TB/s) and 63.5 backward (5.3), 4099 of 8192 47.5 forward (5.7).  Odd widths
+// (6.2 TB/s) and 63.6 backward (5.3), 4099 of 8192 47.0 forward (5.7).  Odd widths
 // move single values (3000 of 7001 backward 164 us, 1.3 TB/s), and backward rows of
 // more than 6144 columns are read without the next one on its way (2000 of 12288
-// 103 us, 2.4 TB/s).
+// 104 us, 2.4 TB/s; 12289, single values again, 312).
 #include "s5_rows.cuh"
 #include "s5_sm100.cuh"
 
@@ -26,13 +26,14 @@ using namespace rows;
 
 constexpr int MAX_H = 16384;
 // A backward block: its warps and a lane's columns.  Eight columns leave registers for the next row: 24 warps where a
-// lane has one vector of eight, else 16 (narrower vectors spill with 24: 8000 rows of 1799 in bf16 137 us, 69 with 16).
+// lane has one vector of eight, else 16 (narrower vectors spill with 24: 8000 rows of 1799 in bf16 137 us, 66 with 16).
 // Rows of 13 to 16 warps leave no room for a second one, and go better with 16 warps' registers (8192 of 4096 74 us, 82
 // with 24).  Still wider rows take 24 warps again, only full vectors with the next row.  Above 6144 columns the sums of
 // the weights' gradients lie in shared memory, 32 warps with 8 columns a lane and above 8192 with 16 (3000 of 7001 in
-// bf16 164 us, 226 with the sums in registers; of 8192 in 32 bits 108, 124; 2000 of 12288 in bf16 103, 259), but for two
-// kinds: bf16 in vectors up to 8192, 16 columns a lane in 16 warps (3000 of 8192 70, 87), and single values above it
-// (2000 of 12289 316, 335).
+// bf16 164 us, 226 with the sums in registers; of 8192 in 32 bits 109, 124; 2000 of 12288 in bf16 104, 259), but for two
+// kinds: bf16 in vectors up to 8192, 16 columns a lane in 16 warps (3000 of 8192 71, 87), and single values above it
+// (2000 of 12289 312, 335).  What a thread spills, in bytes stored: single values above 8192 columns 1328 to 1380, the
+// vectors there 24 to 156; below, up to 6144 with 24 warps and no next row 0 to 88, the others 20 at most.
 constexpr int BWD_SMEM = 96 << 10;   // most of it: sums of two times 24 x 256 columns, or a weight of 16384
 constexpr int SHARED_SMEM = 3 * MAX_H * (int)sizeof(float);
 
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(V * NV >= 32 ? 512 : 1024) add_layernorm_fwd_k
 
 // A block's warps in slots of `warps`, a row each at a time; the next row is on its way while a row's warps meet.
 // SHARED: one slot, the sums of the weights' gradients in shared memory, where each lane has its own columns, dy widened
-// again and dtotal read when they are needed, so that 16 columns a lane fit 64 registers.
+// again and dtotal read when they are needed, so that 16 columns a lane spill few of their 64 registers' values.
 template <typename T, int V, int NV, int MOST, bool AHEAD, bool SHARED>
 __global__ void __launch_bounds__(MOST * 32) add_layernorm_bwd_kernel(const NormArgs p) {
     __shared__ float2 sums[2][MOST];

@@ -27,9 +27,10 @@
 // 1 - a and 1 - a^2 come from m = exp(la) - 1, a short series where a is near
 // one: a channel that forgets over thousands of tokens keeps the digits of both.
 //
-// Bound: neither DRAM (34 to 44 % of its peak) nor issue slots (54 to 59 %) are
-// full; a round is a chain of load, tile and exchange, four blocks an SM beside
-// each other.  bf16: 16384 tokens of 2048 channels 67 us (4.0 TB/s), 4 x 2048 of
+// Bound: nothing is full.  DRAM is busy 34 to 44 %, issue slots 54 to 59 %, the
+// pipe of special functions (six a value with both gates and the root) 46 to
+// 52 % forward and 24 % backward; a round is a chain of load, tile and exchange, four
+// blocks an SM beside each other.  bf16: 16384 tokens of 2048 channels 67 us (4.0 TB/s), 4 x 2048 of
 // 2560 with resets 50 us forward (3.4 TB/s) and 96 backward (3.1).  Three blocks
 // an SM 74 us for the first, five 92, blocks of 256 threads 111 for 74 (before
 // TMA); tiles by 16-byte copies 71.
@@ -136,7 +137,8 @@ struct ScanMaps {
 // channels each, and GROUPS such rows S consecutive tokens each.
 template <typename T_, int V_, int LANES_, int S_, int ARRAYS_, bool ASYNC_> struct Shape {
     static constexpr int THREADS = 128, BLOCKS = 4;          // of an SM
-    static constexpr int FETCHER = THREADS - 32;             // the thread that starts the copies: of a warp that folds nothing
+    // The thread that starts the copies: of the last warp, which folds nothing but, backward where a row is 64 channels, states.
+    static constexpr int FETCHER = THREADS - 32;
     using T = T_;
     static constexpr int V = V_, LANES = LANES_, S = S_, ARRAYS = ARRAYS_;
     static constexpr bool ASYNC = ASYNC_;                     // tiles come by TMA

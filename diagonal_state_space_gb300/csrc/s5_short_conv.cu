@@ -7,7 +7,7 @@
 //
 // Bound: memory forward, with little to spare; backward no single one.  With K = 4,
 // silu and resets a value takes about 13 instructions forward and 26 backward.
-// bf16, 4 x 2048 tokens of 4096 channels with resets: 25.3 us forward (5.3 TB/s) and
+// bf16, 4 x 2048 tokens of 4096 channels with resets: 25.5 us forward (5.3 TB/s) and
 // 51 backward (3.9); 8 x 1999 of 2048 without 23.5 forward (5.6).  A lane walks a segment of tokens of V
 // channels with the last K - 1 inputs (and, backward, the K sums of dx that are
 // not whole yet) in registers, so that an input is read once and the K - 1
